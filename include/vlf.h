@@ -369,6 +369,123 @@ int vlf_attn_varlen_bwd_noalloc(const void *q, const void *k, const void *v, con
 /* Bytes of the fixed array vlf_attn_varlen_bwd_noalloc uses as its workspace. */
 size_t vlf_noalloc_scratch_bytes(void);
 
+/*
+ * Decoding on a bounded cache: rotary positions, attention behind a shared prefix, the weight each
+ * cached key received, and the cache cut down by it.  The pages have no counterpart to these entry
+ * points (they stop at "cached decode" with the end-aligned causal rule, mtlattn 0.3.0, "Use", and
+ * at a head with a "rope" part, triton-msl part 2, "Latent attention"); they are what a program
+ * that serves with the calls above runs next to them.
+ */
+
+/*
+ * Rotary positions with several axes, of packed queries and keys together.
+ *   q [total, h_q, d], k [total, h_k, d]   dtype; the heads and columns of a token are dense, tokens
+ *                are q_stride / k_stride elements apart (slices of a fused projection's output are
+ *                taken as they are); k may be NULL with h_k = 0
+ *   q_out, k_out as q, k, with strides of their own (at least h * d).  An output may be its input
+ *                (same pointer and stride); otherwise outputs overlap no input.
+ *   positions    device int32 [n_axes, total], any values
+ *   n_axes       1..4; sections: host int [n_axes], how many consecutive pairs each axis turns
+ *                (>= 0, their sum is rot / 2); NULL with n_axes = 1
+ *   inv_freq     device fp32 [rot / 2], finite: the radians pair c turns per unit of its position
+ *   rot          even, 0..d: the columns that turn; the others pass through
+ *   interleaved  0: pair c is columns (c, c + rot / 2); 1: columns (2 c, 2 c + 1)
+ *   inverse      0: y_a = x_a cos t - x_b sin t, y_b = x_b cos t + x_a sin t with
+ *                t = positions[axis(c)][token] * inv_freq[c]; 1: by -t, which is the gradient of
+ *                the rotation (and undoes it)
+ * The angle is exact to far positions (64-bit fixed point); the products are fp32, rounded once.
+ */
+int vlf_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+             const int32_t *positions, int n_axes, const int *sections, const float *inv_freq,
+             int total, int h_q, int h_k, int d, int rot, int dtype, int interleaved, int inverse,
+             void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride,
+             vlf_stream_t stream);
+
+/*
+ * Attention of a batch whose sequences all start with the same keys (a shared system prompt or
+ * document): sequence s attends over the prefix_len prefix keys followed by its own kv_len keys, and
+ * out / lse are those of vlf_attn_varlen_fwd on the concatenated keys (the causal and window rules
+ * count all prefix_len + kv_len keys; row i stands at key i + prefix_len + kv_len - q_len).  The
+ * prefix is held and read once for the batch: where it pays, rows of all sequences share its tiles.
+ *   k_prefix [prefix_len, h_kv, d_qk], v_prefix [prefix_len, h_kv, d_v]   dtype; prefix_len >= 0,
+ *                prefix_len + max_seqlen_kv < 2^31
+ *   workspace    device buffer of at least vlf_attn_varlen_fwd_prefix_workspace_size(...) bytes,
+ *                owned by the caller, clobbered (two calls that may overlap need two); may be NULL
+ *                where that is 0
+ *   flags        VLF_FLAG_FORCE_SIMT; others are ignored
+ * Other arguments as vlf_attn_varlen_fwd (no bias); dtypes and widths as there, with tensor-core
+ * kernels for F16 / BF16 and (d_qk, d_v) in {(64,64), (96,96), (128,128)}.  Keys and values of other
+ * sequences never reach a row, whatever they hold.  No backward.
+ */
+int vlf_attn_varlen_fwd_prefix(const void *q, const void *k_prefix, const void *v_prefix,
+                               int prefix_len, const void *k, const void *v,
+                               const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_kv,
+                               int num_seqs, int total_q, int total_kv, int max_seqlen_q,
+                               int max_seqlen_kv, int h_q, int h_kv, int d_qk, int d_v, int dtype,
+                               float scale, int causal, int window, void *out, float *lse,
+                               void *workspace, size_t workspace_bytes, vlf_stream_t stream,
+                               unsigned flags);
+
+/* Bytes of workspace vlf_attn_varlen_fwd_prefix needs: a rule on these sizes and the SM count
+ * (num_sms <= 0: the current device's); 0 for invalid sizes. */
+size_t vlf_attn_varlen_fwd_prefix_workspace_size(int num_seqs, int total_q, int max_seqlen_q,
+                                                 int max_seqlen_kv, int prefix_len, int h_q,
+                                                 int h_kv, int d_qk, int d_v, int dtype,
+                                                 unsigned flags, int num_sms);
+
+/*
+ * The attention weight that each key received:
+ *   weights[g, j] = prev[g, j] + sum of exp(scale * q_i,h . k_j,g - lse[h, i]) over the query rows
+ *                   i of j's sequence that see j (causal and window rules as in the forward) and
+ *                   the heads h of kv head g,
+ * the column sums of the attention matrix whose row log-sum-exps the forward returned.  With the
+ * lse of vlf_attn_varlen_fwd_prefix it gives the own keys' weights, and, called with the prefix as
+ * the one sequence's keys (cu_seqlens {0, total_q} and {0, prefix_len}, no causal rule or window),
+ * the prefix keys' over the batch.
+ *   q, k, sequences, scale, causal, window   as the forward that returned lse
+ *   lse          fp32 [h_q, total_q]; a row with -inf gives nothing
+ *   prev         NULL (zeros) or fp32 [h_kv, total_kv]; may be weights
+ *   weights      fp32 [h_kv, total_kv] (written)
+ *   workspace    at least vlf_attn_key_weights_workspace_size(...) bytes, as above
+ *   flags        VLF_FLAG_FORCE_SIMT; others are ignored
+ * Sums are fp32, each in a fixed order.  Tensor-core kernels for F16 / BF16 and d in {64, 96, 128,
+ * 192}; any d <= 256 otherwise.
+ */
+int vlf_attn_key_weights(const void *q, const void *k, const float *lse,
+                         const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_kv, int num_seqs,
+                         int total_q, int total_kv, int max_seqlen_q, int max_seqlen_kv, int h_q,
+                         int h_kv, int d, int dtype, float scale, int causal, int window,
+                         const float *prev, float *weights, void *workspace,
+                         size_t workspace_bytes, vlf_stream_t stream, unsigned flags);
+
+/* Bytes of workspace vlf_attn_key_weights needs, a rule as above. */
+size_t vlf_attn_key_weights_workspace_size(int num_seqs, int total_kv, int max_seqlen_q,
+                                           int max_seqlen_kv, int h_q, int h_kv, int d, int dtype,
+                                           unsigned flags, int num_sms);
+
+/*
+ * Cache eviction.  Of each sequence's L keys n = min(L, budget) stay: all of them, or the first
+ * `sink`, the last `recent`, and of the keys between them the budget - sink - recent with the
+ * largest weight (of equal weights the lower index; -0 equals +0, a NaN is below every number).
+ * Each kv head chooses for itself; kept keys keep their order.
+ *   k [total_kv, h_kv, d_qk], v [total_kv, h_kv, d_v]   dtype
+ *   weights      fp32 [h_kv, total_kv]
+ *   budget >= 0, sink >= 0, recent >= 0, sink + recent <= budget
+ *   total_out    rows of the outputs, at least the sum of the n (else VLF_ERR_BAD_SEQLENS on the
+ *                device, and the sequences that do not fit are not written); rows behind the last
+ *                kept one are left as they were
+ *   k_out [total_out, h_kv, d_qk], v_out [total_out, h_kv, d_v], weights_out fp32 [h_kv, total_out]
+ *   index_out    int32 [h_kv, total_out]: the sequence-local key each row came from
+ *   cu_out       int32 [num_seqs + 1]: the cu_seqlens of the outputs (-1 behind a sequence that had
+ *                an error; neither it nor the next one is copied)
+ * Outputs overlap no input.  d_qk, d_v <= 256.
+ */
+int vlf_cache_evict(const void *k, const void *v, const float *weights,
+                    const int32_t *cu_seqlens_kv, int num_seqs, int total_kv, int max_seqlen_kv,
+                    int h_kv, int d_qk, int d_v, int dtype, int budget, int sink, int recent,
+                    int total_out, void *k_out, void *v_out, float *weights_out,
+                    int32_t *index_out, int32_t *cu_out, vlf_stream_t stream);
+
 /* Library version, major * 10000 + minor * 100 + patch. */
 int vlf_version(void);
 

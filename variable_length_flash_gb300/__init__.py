@@ -10,7 +10,11 @@ The functions carry the names of the C entry points in ``include/vlf.h``:
 * ``vlf_attn_varlen_bwd(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_kv, ...)``
   -> (dq, dk, dv)
 * ``vlf_attn_varlen_bwd_workspace_size``, ``vlf_check_error``, ``vlf_status_string``,
-  ``vlf_sched_kv_band``, ``vlf_sched_q_band``, ``vlf_version``.
+  ``vlf_sched_kv_band``, ``vlf_sched_q_band``, ``vlf_version``;
+* next to them, for decoding on a bounded cache, ``vlf_rope`` (rotary positions with several axes),
+  ``vlf_attn_varlen_fwd_prefix`` (attention behind a prefix that the batch shares),
+  ``vlf_attn_key_weights`` (the attention weight each key received) and ``vlf_cache_evict`` (the
+  cache cut down to a budget by it).
 
 The operation is the varlen attention of the mtlattn 0.3.0 page (section "Use"): packed
 q/k/v [tokens, heads, head_dim] with int32 cu_seqlens, end-aligned causal, sliding window,
@@ -45,7 +49,9 @@ EXPORTS = ["vlf_attn_varlen_fwd", "vlf_attn_varlen_fwd_ex", "vlf_attn_varlen_bwd
            "vlf_noalloc_scratch_bytes", "vlf_attn_varlen_fwd_split", "vlf_fwd_num_splits",
            "vlf_attn_varlen_fwd_split_workspace_size", "vlf_attn_varlen_fwd_latent",
            "vlf_attn_varlen_bwd_latent", "vlf_attn_varlen_bwd_latent_workspace_size",
-           "vlf_bias_bands", "vlf_bias_bands_size"]
+           "vlf_bias_bands", "vlf_bias_bands_size", "vlf_rope", "vlf_attn_varlen_fwd_prefix",
+           "vlf_attn_varlen_fwd_prefix_workspace_size", "vlf_attn_key_weights",
+           "vlf_attn_key_weights_workspace_size", "vlf_cache_evict"]
 VLF_BWD_STAGES = 3
 BWD_STAGE_NAMES = ["rowdot", "dkdv", "dq"]
 
@@ -103,6 +109,20 @@ def _load():
     lib.vlf_bias_bands_size.restype = Z
     lib.vlf_bias_bands.argtypes = [P, I, P, P, I, I, I, P, Z, P]
     lib.vlf_bias_bands.restype = I
+    L = ctypes.c_int64
+    lib.vlf_rope.argtypes = [P, L, P, L, P, I, P, P, I, I, I, I, I, I, I, I, P, L, P, L, P]
+    lib.vlf_rope.restype = I
+    lib.vlf_attn_varlen_fwd_prefix.argtypes = ([P, P, P, I, P, P, P, P] + [I] * 10 + [F, I, I] +
+                                               [P, P, P, Z, P, U])
+    lib.vlf_attn_varlen_fwd_prefix.restype = I
+    lib.vlf_attn_varlen_fwd_prefix_workspace_size.argtypes = [I] * 10 + [U, I]
+    lib.vlf_attn_varlen_fwd_prefix_workspace_size.restype = Z
+    lib.vlf_attn_key_weights.argtypes = ([P] * 5 + [I] * 9 + [F, I, I, P, P, P, Z, P, U])
+    lib.vlf_attn_key_weights.restype = I
+    lib.vlf_attn_key_weights_workspace_size.argtypes = [I] * 8 + [U, I]
+    lib.vlf_attn_key_weights_workspace_size.restype = Z
+    lib.vlf_cache_evict.argtypes = [P] * 4 + [I] * 11 + [P] * 6
+    lib.vlf_cache_evict.restype = I
     lib.vlf_noalloc_scratch_bytes.argtypes = []
     lib.vlf_noalloc_scratch_bytes.restype = Z
     lib.vlf_launch_count.argtypes = []
@@ -520,16 +540,277 @@ def vlf_attn_varlen_bwd_noalloc(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlen
     return dq, dk, dv
 
 
+# ------------------------------------------------------------------ decoding on a bounded cache
+def _same_device(like, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != like.device:
+            raise VlfError(VLF_ERR_INVALID, f"{name} is on {t.device}, q on {like.device}")
+
+
+def _new(shape, dtype, like, stream):
+    """A fresh tensor that a kernel on ``stream`` (None: the current one) will use: the caching
+    allocator is told about a stream that is not the one it was allocated on."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None and t.numel():
+        t.record_stream(stream)
+    return t
+
+
+def _given(t, name, shape, dtype):
+    """A caller's output tensor."""
+    _req(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise VlfError(VLF_ERR_INVALID, f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _workspace(need, workspace, like, stream):
+    """(pointer, bytes) of a workspace of ``need`` bytes: the caller's, or a new one."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = _new(need, torch.uint8, like, stream)
+    else:
+        _req(workspace, "workspace")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _rope_rows(t, name, dtype, total=None):
+    """Checks a rope operand [tokens, heads, d] (tokens may be strided, heads and columns are
+    dense) and returns its token stride."""
+    if t is None or not t.is_cuda:
+        raise VlfError(VLF_ERR_INVALID, f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise VlfError(VLF_ERR_INVALID, f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or (total is not None and t.shape[0] != total):
+        raise VlfError(VLF_ERR_INVALID, f"{name} must be [tokens, heads, head_dim]")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
+        raise VlfError(VLF_ERR_INVALID, f"{name}: the heads and columns of a token must be dense")
+    return s0 if n > 1 else h * d
+
+
+def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=False, q_out=None,
+             k_out=None, stream=None):
+    """Rotary positions of q [T,Hq,D] and k [T,Hk,D] (k may be None) with one or several position
+    axes.  ``positions`` int32 [T] or [axes, T]; ``inv_freq`` fp32 [rot / 2], the radians a pair
+    turns per unit of its position; ``sections``: how many consecutive pairs each axis turns (None:
+    one axis).  Pair c is columns (c, c + rot / 2), or (2 c, 2 c + 1) when ``interleaved``; columns
+    from rot on pass through.  ``inverse`` turns back, which is also the gradient.  q and k may be
+    slices of a packed projection (their tokens may be strided); ``q_out`` / ``k_out`` may be q / k
+    themselves.  Returns (q_out, k_out)."""
+    dtype = q.dtype
+    if dtype not in _DTYPE:
+        raise VlfError(VLF_ERR_INVALID, f"unsupported dtype {dtype}")
+    sq = _rope_rows(q, "q", dtype)
+    total, hq, d = q.shape
+    hk, sk, sko, k_p, ko_p = 0, 0, 0, None, None
+    if k is not None:
+        sk = _rope_rows(k, "k", dtype, total)
+        hk = k.shape[1]
+        if k.shape[2] != d:
+            raise VlfError(VLF_ERR_INVALID, "q and k must have the same head_dim")
+    _req(positions, "positions", torch.int32), _req(inv_freq, "inv_freq", torch.float32)
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if positions.dim() > 2 or positions.shape[-1] != total or inv_freq.dim() != 1:
+        raise VlfError(VLF_ERR_INVALID, "positions must be [tokens] or [axes, tokens], inv_freq [rot / 2]")
+    if sections is None:
+        if axes != 1:
+            raise VlfError(VLF_ERR_INVALID, "several position axes need sections")
+        sec = None
+    else:
+        if len(sections) != axes:
+            raise VlfError(VLF_ERR_INVALID, f"{len(sections)} sections for {axes} position axes")
+        sec = (ctypes.c_int * axes)(*sections)
+    if q_out is None:
+        q_out = _new(q.shape, dtype, q, stream)
+        sqo = hq * d
+    else:
+        sqo = _rope_rows(q_out, "q_out", dtype, total)
+    if tuple(q_out.shape) != tuple(q.shape):
+        raise VlfError(VLF_ERR_INVALID, "q_out must have q's shape")
+    if k is not None:
+        if k_out is None:
+            k_out = _new(k.shape, dtype, k, stream)
+            sko = hk * d
+        else:
+            sko = _rope_rows(k_out, "k_out", dtype, total)
+        if tuple(k_out.shape) != tuple(k.shape):
+            raise VlfError(VLF_ERR_INVALID, "k_out must have k's shape")
+        k_p, ko_p = k.data_ptr(), k_out.data_ptr()
+    _same_device(q, k=k, positions=positions, inv_freq=inv_freq, q_out=q_out, k_out=k_out)
+    st = _lib.vlf_rope(q.data_ptr(), sq, k_p, sk, positions.data_ptr(), axes, sec, inv_freq.data_ptr(),
+                       total, hq, hk, d, 2 * inv_freq.shape[0], _DTYPE[dtype], 1 if interleaved else 0,
+                       1 if inverse else 0, q_out.data_ptr(), sqo, ko_p, sko, _stream(stream, q))
+    if st != VLF_OK:
+        _check(st, "vlf_rope")
+    return q_out, k_out
+
+
+_WORKSPACES = {}  # (entry point, shape, device) -> bytes of workspace
+
+
+def _workspace_size(fn, key):
+    """fn(*key[:-1], 0 SMs given), remembered: it depends on the shape and the device alone."""
+    need = _WORKSPACES.get((fn.__name__, key))
+    if need is None:
+        need = int(fn(*key[:-1], 0))
+        if len(_WORKSPACES) < 4096:
+            _WORKSPACES[(fn.__name__, key)] = need
+    return need
+
+
+def vlf_attn_varlen_fwd_prefix_workspace_size(num_seqs, total_q, max_seqlen_q, max_seqlen_kv,
+                                              prefix_len, h_q, h_kv, d_qk, d_v, dtype, flags=0,
+                                              num_sms=0) -> int:
+    dt = _DTYPE[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return int(_lib.vlf_attn_varlen_fwd_prefix_workspace_size(
+        num_seqs, total_q, max_seqlen_q, max_seqlen_kv, prefix_len, h_q, h_kv, d_qk, d_v, dt, flags,
+        num_sms))
+
+
+def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seqlens_kv,
+                               max_seqlen_q, max_seqlen_kv=None, scale=None, causal=False, window=0,
+                               out=None, lse=None, workspace=None, stream=None, flags=0):
+    """Attention of a batch whose sequences share their first keys: every sequence attends over
+    ``k_prefix`` / ``v_prefix`` [P, Hkv, D] and then its own keys.  Equals vlf_attn_varlen_fwd on
+    the concatenated keys, with the prefix read once.  Returns out [Tq, Hq, Dv] and lse fp32
+    [Hq, Tq].  ``workspace``: at least vlf_attn_varlen_fwd_prefix_workspace_size bytes, allocated
+    here when not given."""
+    _fwd_checks(q, k, v, cu_seqlens_q, cu_seqlens_kv)
+    _req(k_prefix, "k_prefix", q.dtype), _req(v_prefix, "v_prefix", q.dtype)
+    tq, hq, dqk = q.shape
+    tk, hkv, dv = v.shape
+    if k.shape != (tk, hkv, dqk):
+        raise VlfError(VLF_ERR_INVALID, "k shape")
+    n = k_prefix.shape[0]
+    if k_prefix.shape != (n, hkv, dqk) or v_prefix.shape != (n, hkv, dv):
+        raise VlfError(VLF_ERR_INVALID, "k_prefix / v_prefix must be [prefix_len, H_kv, D]")
+    if cu_seqlens_q.numel() != cu_seqlens_kv.numel() or cu_seqlens_q.numel() < 1:
+        raise VlfError(VLF_ERR_INVALID, "cu_seqlens_q and cu_seqlens_kv must have num_seqs + 1 entries")
+    if max_seqlen_kv is None:
+        max_seqlen_kv = _max_len(cu_seqlens_kv)
+    out = _new((tq, hq, dv), q.dtype, q, stream) if out is None else _given(out, "out", (tq, hq, dv), q.dtype)
+    lse = _new((hq, tq), torch.float32, q, stream) if lse is None else _given(lse, "lse", (hq, tq), torch.float32)
+    _same_device(q, k_prefix=k_prefix, v_prefix=v_prefix, k=k, v=v, cu_seqlens_q=cu_seqlens_q,
+                 cu_seqlens_kv=cu_seqlens_kv, out=out, lse=lse, workspace=workspace)
+    nseq, mq, mk, dt = cu_seqlens_q.numel() - 1, int(max_seqlen_q), int(max_seqlen_kv), _DTYPE[q.dtype]
+    need = _workspace_size(_lib.vlf_attn_varlen_fwd_prefix_workspace_size,
+                           (nseq, tq, mq, mk, n, hq, hkv, dqk, dv, dt, int(flags), q.get_device()))
+    ws_p, ws_n, workspace = _workspace(need, workspace, q, stream)
+    st = _lib.vlf_attn_varlen_fwd_prefix(
+        q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), n, k.data_ptr(), v.data_ptr(),
+        cu_seqlens_q.data_ptr(), cu_seqlens_kv.data_ptr(), nseq, tq, tk, mq, mk, hq, hkv, dqk, dv, dt,
+        float(scale) if scale else 0.0, 1 if causal else 0, int(window) if window else 0,
+        out.data_ptr(), lse.data_ptr(), ws_p, ws_n, _stream(stream, q), int(flags))
+    if st != VLF_OK:
+        _check(st, "vlf_attn_varlen_fwd_prefix")
+    return out, lse
+
+
+def vlf_attn_key_weights_workspace_size(num_seqs, total_kv, max_seqlen_q, max_seqlen_kv, h_q, h_kv, d,
+                                        dtype, flags=0, num_sms=0) -> int:
+    dt = _DTYPE[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return int(_lib.vlf_attn_key_weights_workspace_size(num_seqs, total_kv, max_seqlen_q,
+                                                        max_seqlen_kv, h_q, h_kv, d, dt, flags, num_sms))
+
+
+def vlf_attn_key_weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, max_seqlen_kv=None,
+                         scale=None, causal=False, window=0, prev=None, weights=None, workspace=None,
+                         stream=None, flags=0):
+    """The attention weight each key received, fp32 [Hkv, Tkv]: the sum over the rows that see it and
+    the heads of its group of exp(logit - lse), plus ``prev`` (fp32 [Hkv, Tkv], or None).  ``lse``
+    [Hq, Tq] comes from the forward with the same scale, causal and window.  ``weights`` (the
+    output) may be ``prev``."""
+    _fwd_checks(q, k, k, cu_seqlens_q, cu_seqlens_kv)
+    _req(lse, "lse", torch.float32)
+    tq, hq, d = q.shape
+    tk, hkv, _ = k.shape
+    if k.shape[2] != d or lse.shape != (hq, tq):
+        raise VlfError(VLF_ERR_INVALID, "k must be [Tkv, Hkv, D] and lse [Hq, Tq]")
+    if cu_seqlens_q.numel() != cu_seqlens_kv.numel() or cu_seqlens_q.numel() < 1:
+        raise VlfError(VLF_ERR_INVALID, "cu_seqlens_q and cu_seqlens_kv must have num_seqs + 1 entries")
+    if max_seqlen_kv is None:
+        max_seqlen_kv = _max_len(cu_seqlens_kv)
+    if prev is not None:
+        _given(prev, "prev", (hkv, tk), torch.float32)
+    if weights is None:
+        weights = _new((hkv, tk), torch.float32, q, stream)
+    else:
+        _given(weights, "weights", (hkv, tk), torch.float32)
+    _same_device(q, k=k, lse=lse, cu_seqlens_q=cu_seqlens_q, cu_seqlens_kv=cu_seqlens_kv, prev=prev,
+                 weights=weights, workspace=workspace)
+    nseq, mq, mk, dt = cu_seqlens_q.numel() - 1, int(max_seqlen_q), int(max_seqlen_kv), _DTYPE[q.dtype]
+    need = _workspace_size(_lib.vlf_attn_key_weights_workspace_size,
+                           (nseq, tk, mq, mk, hq, hkv, d, dt, int(flags), q.get_device()))
+    ws_p, ws_n, workspace = _workspace(need, workspace, q, stream)
+    st = _lib.vlf_attn_key_weights(
+        q.data_ptr(), k.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_kv.data_ptr(),
+        nseq, tq, tk, mq, mk, hq, hkv, d, dt, float(scale) if scale else 0.0, 1 if causal else 0,
+        int(window) if window else 0, _ptr(prev), weights.data_ptr(), ws_p, ws_n, _stream(stream, q),
+        int(flags))
+    if st != VLF_OK:
+        _check(st, "vlf_attn_key_weights")
+    return weights
+
+
+def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_seqlen_kv=None,
+                    total_out=None, k_out=None, v_out=None, weights_out=None, index_out=None,
+                    cu_out=None, stream=None):
+    """Cuts each sequence's cache to at most ``budget`` keys: the first ``sink``, the last ``recent``
+    and, between them, the ones with the largest weight (per kv head; ties keep the lower index).
+    k [Tkv,Hkv,Dk], v [Tkv,Hkv,Dv], weights fp32 [Hkv,Tkv].  Returns the compacted (k, v, weights),
+    index int32 [Hkv, total_out] (the sequence-local key each row came from) and cu int32 [n + 1].
+    ``total_out``: rows of the outputs, the sum of min(length, budget) where the caller knows the
+    lengths (None: min(Tkv, n * budget), whose last rows may stay unwritten)."""
+    _req(k, "k"), _req(v, "v", k.dtype), _req(weights, "weights", torch.float32)
+    _req(cu_seqlens_kv, "cu_seqlens_kv", torch.int32)
+    if k.dtype not in _DTYPE:
+        raise VlfError(VLF_ERR_INVALID, f"unsupported dtype {k.dtype}")
+    if k.dim() != 3 or v.dim() != 3 or k.shape[:2] != v.shape[:2] or cu_seqlens_kv.numel() < 1:
+        raise VlfError(VLF_ERR_INVALID, "k, v must be [tokens, heads, head_dim]")
+    tk, h, dk = k.shape
+    dv = v.shape[2]
+    if tuple(weights.shape) != (h, tk):
+        raise VlfError(VLF_ERR_INVALID, "weights must be [H_kv, total_kv]")
+    if max_seqlen_kv is None:
+        max_seqlen_kv = _max_len(cu_seqlens_kv)
+    n, budget = cu_seqlens_kv.numel() - 1, int(budget)
+    if total_out is None:
+        total_out = min(tk, n * max(0, budget))
+    total_out = int(total_out)
+    outs = []
+    for t, name, shape, dtype in ((k_out, "k_out", (total_out, h, dk), k.dtype),
+                                  (v_out, "v_out", (total_out, h, dv), k.dtype),
+                                  (weights_out, "weights_out", (h, total_out), torch.float32),
+                                  (index_out, "index_out", (h, total_out), torch.int32),
+                                  (cu_out, "cu_out", (n + 1,), torch.int32)):
+        outs.append(_new(shape, dtype, k, stream) if t is None else _given(t, name, shape, dtype))
+    _same_device(k, v=v, weights=weights, cu_seqlens_kv=cu_seqlens_kv, k_out=outs[0], v_out=outs[1],
+                 weights_out=outs[2], index_out=outs[3], cu_out=outs[4])
+    st = _lib.vlf_cache_evict(
+        k.data_ptr(), v.data_ptr(), weights.data_ptr(), cu_seqlens_kv.data_ptr(), n, tk,
+        int(max_seqlen_kv), h, dk, dv, _DTYPE[k.dtype], budget, int(sink), int(recent), total_out,
+        *[t.data_ptr() for t in outs], _stream(stream, k))
+    if st != VLF_OK:
+        _check(st, "vlf_cache_evict")
+    return tuple(outs)
+
+
 __all__ = ["vlf_attn_varlen_fwd", "vlf_attn_varlen_bwd", "vlf_attn_varlen_bwd_workspace_size",
            "vlf_bias_bands", "vlf_bias_bands_size",
            "vlf_check_error", "vlf_status_string", "vlf_sched_kv_band", "vlf_sched_q_band",
            "vlf_version", "vlf_launch_count", "vlf_fwd_path", "vlf_bwd_path",
            "vlf_attn_varlen_bwd_noalloc", "vlf_noalloc_scratch_bytes", "VlfError",
+           "vlf_rope", "vlf_attn_varlen_fwd_prefix", "vlf_attn_varlen_fwd_prefix_workspace_size",
+           "vlf_attn_key_weights", "vlf_attn_key_weights_workspace_size", "vlf_cache_evict",
            "LIB_PATH", "EXPORTS"]
 
 # differentiable entry points (autograd over the two calls above)
 from .functional import (flash_attn_varlen_func, flash_attn_varlen_kvpacked_func,  # noqa: E402
-                         flash_attn_varlen_qkvpacked_func, latent_attention, varlen_attention)
+                         flash_attn_varlen_qkvpacked_func, latent_attention, rotary_embedding,
+                         varlen_attention)
 
-__all__ += ["varlen_attention", "latent_attention", "flash_attn_varlen_func", "flash_attn_varlen_qkvpacked_func",
+__all__ += ["varlen_attention", "latent_attention", "rotary_embedding", "flash_attn_varlen_func", "flash_attn_varlen_qkvpacked_func",
             "flash_attn_varlen_kvpacked_func"]

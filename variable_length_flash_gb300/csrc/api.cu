@@ -544,4 +544,145 @@ int vlf_check_error(vlf_stream_t stream) {
   return word;
 }
 
+int vlf_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+             const int32_t *positions, int n_axes, const int *sections, const float *inv_freq,
+             int total, int h_q, int h_k, int d, int rot, int dtype, int interleaved, int inverse,
+             void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride,
+             vlf_stream_t stream) {
+  if (total < 0 || h_q < 1 || h_k < 0 || d < 1 || rot < 0 || rot > d || rot % 2) return VLF_ERR_INVALID;
+  if (dtype != VLF_F16 && dtype != VLF_BF16 && dtype != VLF_F32) return VLF_ERR_INVALID;
+  if (n_axes < 1 || n_axes > 4 || (!sections && n_axes != 1)) return VLF_ERR_INVALID;
+  vlf::RopeParams p{};
+  const int half = rot / 2;
+  long long sum = 0;
+  for (int a = 0; a < 4; ++a) {
+    p.first[a] = a < n_axes ? (int)sum : half;
+    if (a >= n_axes) continue;
+    const int n = sections ? sections[a] : half;
+    if (n < 0 || (sum += n) > half) return VLF_ERR_INVALID;
+  }
+  if (sum != half) return VLF_ERR_INVALID;
+  if (d > 256 || h_q > 65535 || h_k > 65535) return VLF_ERR_UNSUPPORTED;
+  if (total == 0) return VLF_OK;
+  if (!q || !q_out || (h_k > 0 && (!k || !k_out)) || (half > 0 && (!positions || !inv_freq))) return VLF_ERR_INVALID;
+  const int64_t nq = (int64_t)h_q * d, nk = (int64_t)h_k * d;
+  if (q_stride < 0 || k_stride < 0 || (total > 1 && (q_out_stride < nq || (h_k > 0 && k_out_stride < nk))))
+    return VLF_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(positions) ||
+      !aligned16(inv_freq))
+    return VLF_ERR_ALIGN;
+  // in place: the same elements, or none
+  if ((q == q_out && total > 1 && q_stride != q_out_stride) ||
+      (h_k > 0 && k == k_out && total > 1 && k_stride != k_out_stride))
+    return VLF_ERR_INVALID;
+  p.q = q; p.k = k; p.q_out = q_out; p.k_out = k_out;
+  p.q_stride = q_stride; p.k_stride = k_stride; p.q_out_stride = q_out_stride; p.k_out_stride = k_out_stride;
+  p.positions = positions; p.inv_freq = inv_freq;
+  p.total = total; p.h_q = h_q; p.h_k = h_k; p.d = d; p.rot = rot; p.dtype = dtype;
+  p.interleaved = interleaved ? 1 : 0; p.inverse = inverse ? 1 : 0;
+  p.copy_tail = rot < d && (q != q_out || (h_k > 0 && k != k_out));
+  return vlf::rope(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
+}
+
+size_t vlf_attn_varlen_fwd_prefix_workspace_size(int num_seqs, int total_q, int max_seqlen_q,
+                                                 int max_seqlen_kv, int prefix_len, int h_q,
+                                                 int h_kv, int d_qk, int d_v, int dtype,
+                                                 unsigned flags, int num_sms) {
+  (void)num_seqs; (void)total_q; (void)max_seqlen_q; (void)max_seqlen_kv; (void)prefix_len; (void)h_q;
+  (void)h_kv; (void)d_qk; (void)d_v; (void)dtype; (void)flags; (void)num_sms;
+  return 0;
+}
+
+int vlf_attn_varlen_fwd_prefix(const void *q, const void *k_prefix, const void *v_prefix,
+                               int prefix_len, const void *k, const void *v,
+                               const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_kv,
+                               int num_seqs, int total_q, int total_kv, int max_seqlen_q,
+                               int max_seqlen_kv, int h_q, int h_kv, int d_qk, int d_v, int dtype,
+                               float scale, int causal, int window, void *out, float *lse,
+                               void *workspace, size_t workspace_bytes, vlf_stream_t stream,
+                               unsigned flags) {
+  int st = check_common(q, k, v, cu_seqlens_q, cu_seqlens_kv, num_seqs, total_q, total_kv,
+                        max_seqlen_q, max_seqlen_kv, h_q, h_kv, d_qk, d_v, dtype, nullptr, 0);
+  if (st != VLF_OK) return st;
+  if (prefix_len < 0 || (prefix_len > 0 && (!k_prefix || !v_prefix))) return VLF_ERR_INVALID;
+  if (total_q > 0 && !out) return VLF_ERR_INVALID;
+  if ((long long)prefix_len + max_seqlen_kv > 0x7fffffffll) return VLF_ERR_UNSUPPORTED;
+  if (!aligned16(k_prefix) || !aligned16(v_prefix) || !aligned16(out) || !aligned16(lse) || !aligned16(workspace))
+    return VLF_ERR_ALIGN;
+  if (num_seqs == 0 || max_seqlen_q == 0) return VLF_OK;
+  vlf::PrefixParams pp{};
+  fill_common(pp.p, q, k, v, cu_seqlens_q, cu_seqlens_kv, num_seqs, total_q, total_kv, max_seqlen_q,
+              max_seqlen_kv, h_q, h_kv, d_qk, d_v, dtype, scale, causal, window, nullptr, 0, flags);
+  pp.p.out = out;
+  pp.p.lse = lse;
+  pp.p.err = error_word_ptr();
+  if (!pp.p.err) return VLF_ERR_LAUNCH;
+  pp.k_pre = k_prefix;
+  pp.v_pre = v_prefix;
+  pp.prefix_len = prefix_len;
+  (void)workspace_bytes;
+  return vlf::simt_prefix(pp, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
+}
+
+size_t vlf_attn_key_weights_workspace_size(int num_seqs, int total_kv, int max_seqlen_q,
+                                           int max_seqlen_kv, int h_q, int h_kv, int d, int dtype,
+                                           unsigned flags, int num_sms) {
+  (void)num_seqs; (void)total_kv; (void)max_seqlen_q; (void)max_seqlen_kv; (void)h_q; (void)h_kv;
+  (void)d; (void)dtype; (void)flags; (void)num_sms;
+  return 0;
+}
+
+int vlf_attn_key_weights(const void *q, const void *k, const float *lse,
+                         const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_kv, int num_seqs,
+                         int total_q, int total_kv, int max_seqlen_q, int max_seqlen_kv, int h_q,
+                         int h_kv, int d, int dtype, float scale, int causal, int window,
+                         const float *prev, float *weights, void *workspace,
+                         size_t workspace_bytes, vlf_stream_t stream, unsigned flags) {
+  int st = check_common(q, k, k, cu_seqlens_q, cu_seqlens_kv, num_seqs, total_q, total_kv,
+                        max_seqlen_q, max_seqlen_kv, h_q, h_kv, d, d, dtype, nullptr, 0);
+  if (st != VLF_OK) return st;
+  if ((total_q > 0 && !lse) || (total_kv > 0 && !weights)) return VLF_ERR_INVALID;
+  if (!aligned16(lse) || !aligned16(prev) || !aligned16(weights) || !aligned16(workspace)) return VLF_ERR_ALIGN;
+  if (num_seqs == 0 || max_seqlen_kv == 0) return VLF_OK;
+  vlf::KeyWeightParams kp{};
+  fill_common(kp.p, q, k, nullptr, cu_seqlens_q, cu_seqlens_kv, num_seqs, total_q, total_kv, max_seqlen_q,
+              max_seqlen_kv, h_q, h_kv, d, d, dtype, scale, causal, window, nullptr, 0, flags);
+  kp.p.err = error_word_ptr();
+  if (!kp.p.err) return VLF_ERR_LAUNCH;
+  kp.lse = lse;
+  kp.prev = prev;
+  kp.weights = weights;
+  (void)workspace_bytes;
+  return vlf::simt_key_weights(kp, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
+}
+
+int vlf_cache_evict(const void *k, const void *v, const float *weights,
+                    const int32_t *cu_seqlens_kv, int num_seqs, int total_kv, int max_seqlen_kv,
+                    int h_kv, int d_qk, int d_v, int dtype, int budget, int sink, int recent,
+                    int total_out, void *k_out, void *v_out, float *weights_out,
+                    int32_t *index_out, int32_t *cu_out, vlf_stream_t stream) {
+  if (num_seqs < 0 || total_kv < 0 || max_seqlen_kv < 0 || h_kv < 1 || d_qk < 1 || d_v < 1 || total_out < 0)
+    return VLF_ERR_INVALID;
+  if (dtype != VLF_F16 && dtype != VLF_BF16 && dtype != VLF_F32) return VLF_ERR_INVALID;
+  if (budget < 0 || sink < 0 || recent < 0 || (long long)sink + recent > budget) return VLF_ERR_INVALID;
+  if (num_seqs == 0 && total_kv != 0) return VLF_ERR_INVALID;
+  if (num_seqs > 0 && (!cu_seqlens_kv || !cu_out)) return VLF_ERR_INVALID;
+  if (total_kv > 0 && (!k || !v || !weights)) return VLF_ERR_INVALID;
+  if (total_out > 0 && (!k_out || !v_out || !weights_out || !index_out)) return VLF_ERR_INVALID;
+  if (d_qk > 256 || d_v > 256 || num_seqs > 65535 || h_kv > 65535) return VLF_ERR_UNSUPPORTED;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(weights) || !aligned16(cu_seqlens_kv) || !aligned16(k_out) ||
+      !aligned16(v_out) || !aligned16(weights_out) || !aligned16(index_out) || !aligned16(cu_out))
+    return VLF_ERR_ALIGN;
+  if (num_seqs == 0) return VLF_OK;
+  vlf::EvictParams p{};
+  p.k = k; p.v = v; p.weights = weights; p.cu_kv = cu_seqlens_kv;
+  p.num_seqs = num_seqs; p.total_kv = total_kv; p.max_kv = max_seqlen_kv; p.h_kv = h_kv;
+  p.d_qk = d_qk; p.d_v = d_v; p.dtype = dtype; p.budget = budget; p.sink = sink; p.recent = recent;
+  p.total_out = total_out; p.k_out = k_out; p.v_out = v_out; p.weights_out = weights_out;
+  p.index = index_out; p.cu_out = cu_out;
+  p.err = error_word_ptr();
+  if (!p.err) return VLF_ERR_LAUNCH;
+  return vlf::cache_evict(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
+}
+
 }  // extern "C"

@@ -3,9 +3,9 @@
 
 #include <cuda_runtime.h>
 
-namespace vlf {
+#include "common.cuh"
 
-struct Params;
+namespace vlf {
 
 // SIMT fp32-FMA kernels (simt.cu): every dtype and head width up to 256.
 cudaError_t simt_forward(const Params &p, cudaStream_t st);
@@ -39,6 +39,53 @@ size_t tc_backward_workspace(int total_q, int h_q, int d_qk);
 // Bias bands (bias_bands.cu): the buffer size, and the pass that fills it from p.bias.
 size_t bias_bands_bytes(int total_q, int bias_heads);
 cudaError_t bias_bands(const Params &p, void *bands, cudaStream_t st);
+
+// ---------------------------------------------------------------- decoding on a bounded cache
+// Rotary positions (rope.cu).  Strides in elements between tokens; heads and columns are dense.
+struct RopeParams {
+  const void *q, *k;
+  void *q_out, *k_out;
+  long long q_stride, k_stride, q_out_stride, k_out_stride;
+  const int32_t *positions;  // [axes][total]
+  const float *inv_freq;     // [rot / 2]
+  int first[4];              // first pair of each axis (half for the axes that are not there)
+  int total, h_q, h_k, d, rot, dtype, interleaved, inverse;
+  int copy_tail;  // the columns behind rot have to be copied (not in place)
+  int hpt, phases;  // set by the launcher: heads per thread, threads along the heads
+};
+cudaError_t rope(const RopeParams &p, cudaStream_t st);
+
+// Attention over a shared prefix and each sequence's own keys (prefix.cu): p.k / p.v / p.cu_kv /
+// p.total_kv / p.max_kv describe the own keys; the prefix is [prefix_len, h_kv, d].
+struct PrefixParams {
+  Params p;
+  const void *k_pre, *v_pre;
+  int prefix_len;
+};
+cudaError_t simt_prefix(const PrefixParams &pp, cudaStream_t st);
+
+// Attention weight received by each key (key_weights.cu).
+struct KeyWeightParams {
+  Params p;           // q, k, sequences, mask and scale
+  const float *lse;   // [h_q, total_q]
+  const float *prev;  // NULL or [h_kv, total_kv]
+  float *weights;     // [h_kv, total_kv]
+};
+cudaError_t simt_key_weights(const KeyWeightParams &kp, cudaStream_t st);
+
+// Cache eviction (cache_evict.cu).
+struct EvictParams {
+  const void *k, *v;
+  const float *weights;  // [h_kv, total_kv]
+  const int32_t *cu_kv;
+  int num_seqs, total_kv, max_kv, h_kv, d_qk, d_v, dtype, budget, sink, recent, total_out;
+  void *k_out, *v_out;
+  float *weights_out;  // [h_kv, total_out]
+  int *index;          // [h_kv, total_out]
+  int *cu_out;         // [num_seqs + 1]
+  int *err;
+};
+cudaError_t cache_evict(const EvictParams &p, cudaStream_t st);
 
 // Host-side count of successful kernel launches (api.cu).
 void count_launch(int n = 1);

@@ -20,7 +20,7 @@ import torch
 
 from . import (VLF_ERR_INVALID, VLF_ERR_UNSUPPORTED, VlfError, vlf_attn_varlen_bwd,
                vlf_attn_varlen_bwd_latent, vlf_attn_varlen_fwd, vlf_attn_varlen_fwd_latent,
-               vlf_bias_bands)
+               vlf_bias_bands, vlf_rope)
 
 
 def mask_to_bias(mask: torch.Tensor) -> torch.Tensor:
@@ -135,6 +135,42 @@ def latent_attention(q_nope, q_rope, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens
                                   k_rope.contiguous(), v.contiguous(), cu_seqlens_q,
                                   cu_seqlens_kv, int(max_seqlen_q), int(max_seqlen_kv), scale,
                                   bool(causal), int(window or 0), bias)
+
+
+def _token_dense(t):
+    """t itself where the heads and columns of a token are dense, else a contiguous copy."""
+    ok = (t.stride(2) == 1 or t.shape[2] == 1) and (t.stride(1) == t.shape[2] or t.shape[1] == 1)
+    aligned = t.data_ptr() % 16 == 0
+    return t if ok and aligned and t.stride(0) >= 0 else t.contiguous()
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, sections, interleaved):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.args = (sections, interleaved)
+        return vlf_rope(_token_dense(q), _token_dense(k), positions, inv_freq, sections, interleaved)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        positions, inv_freq = ctx.saved_tensors
+        sections, interleaved = ctx.args
+        # the rotation is orthogonal: its gradient is the rotation back
+        dq, dk = vlf_rope(_token_dense(dq), _token_dense(dk), positions, inv_freq, sections,
+                          interleaved, inverse=True)
+        return dq, dk, None, None, None, None
+
+
+def rotary_embedding(q, k, positions, inv_freq, sections=None, interleaved=False):
+    """Rotary positions of packed q [tokens, H_q, D] and k [tokens, H_k, D], differentiable in both;
+    positions int32 [tokens] or [axes, tokens], inv_freq fp32 [rot / 2], sections the pairs of each
+    axis (see ``vlf_rope``).  q and k may be slices of a packed projection."""
+    if positions.requires_grad or inv_freq.requires_grad:
+        raise VlfError(VLF_ERR_UNSUPPORTED, "positions and inv_freq are constants")
+    if q.dim() != 3 or k.dim() != 3:
+        raise VlfError(VLF_ERR_INVALID, "q and k must be [tokens, heads, head_dim]")
+    return _Rotary.apply(q, k, positions.contiguous(), inv_freq.contiguous(),
+                         None if sections is None else tuple(sections), bool(interleaved))
 
 
 def _refuse_flash_extras(dropout_p, alibi_slopes, return_attn_probs):
