@@ -67,6 +67,16 @@ int *error_word_ptr() {
   return t_ptr;
 }
 
+// The current device's SM count (looked up once per device and host thread); 0 if that fails.
+int sm_count() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  thread_local int count[kMaxDevices] = {0};
+  if (!count[dev] && cudaDeviceGetAttribute(&count[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    count[dev] = 0;
+  return count[dev];
+}
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Shared argument checks of the forward and backward.  Returns VLF_OK or a negative status.
@@ -627,9 +637,9 @@ int vlf_attn_varlen_fwd_prefix(const void *q, const void *k_prefix, const void *
 size_t vlf_attn_key_weights_workspace_size(int num_seqs, int total_kv, int max_seqlen_q,
                                            int max_seqlen_kv, int h_q, int h_kv, int d, int dtype,
                                            unsigned flags, int num_sms) {
-  (void)num_seqs; (void)total_kv; (void)max_seqlen_q; (void)max_seqlen_kv; (void)h_q; (void)h_kv;
-  (void)d; (void)dtype; (void)flags; (void)num_sms;
-  return 0;
+  if (num_sms <= 0) num_sms = sm_count();
+  return vlf::key_weights_workspace(num_seqs, total_kv, max_seqlen_q, max_seqlen_kv, h_q, h_kv, d, dtype,
+                                    flags, num_sms);
 }
 
 int vlf_attn_key_weights(const void *q, const void *k, const float *lse,
@@ -652,8 +662,12 @@ int vlf_attn_key_weights(const void *q, const void *k, const float *lse,
   kp.lse = lse;
   kp.prev = prev;
   kp.weights = weights;
-  (void)workspace_bytes;
-  return vlf::simt_key_weights(kp, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
+  const int sms = sm_count();
+  const size_t need = vlf::key_weights_workspace(num_seqs, total_kv, max_seqlen_q, max_seqlen_kv, h_q, h_kv, d,
+                                                 dtype, flags, sms);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return VLF_ERR_WORKSPACE;
+  const cudaError_t e = vlf::key_weights(kp, workspace, sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
 }
 
 int vlf_cache_evict(const void *k, const void *v, const float *weights,

@@ -71,7 +71,9 @@ struct KeyWeightParams {
   const float *prev;  // NULL or [h_kv, total_kv]
   float *weights;     // [h_kv, total_kv]
 };
-cudaError_t simt_key_weights(const KeyWeightParams &kp, cudaStream_t st);
+size_t key_weights_workspace(int num_seqs, int total_kv, int max_q, int max_kv, int h_q, int h_kv, int d,
+                             int dtype, unsigned flags, int num_sms);
+cudaError_t key_weights(const KeyWeightParams &kp, void *workspace, int num_sms, cudaStream_t st);
 
 // Cache eviction (cache_evict.cu).
 struct EvictParams {

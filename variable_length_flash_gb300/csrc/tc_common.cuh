@@ -249,6 +249,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
+// 16 consecutive columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
 // 32 columns into r[off .. off+31] of a larger array (no wait; pair with tmem_ld_wait).
 template <int N>
 __device__ __forceinline__ void tmem_ld32_at(uint32_t taddr, uint32_t (&r)[N], int off) {
@@ -450,4 +461,15 @@ __device__ __forceinline__ float4 lds_f32x4(uint32_t a) {
 }
 
 }  // namespace tc
+
+// ---------------------------------------------------------------- host side (tc_fwd.cu)
+// [rows, cols] row-major 16-bit matrix: box {64 columns, box_rows}, 128-byte swizzle.
+bool make_tmap_16bit(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols,
+                     uint64_t pitch_elems, uint32_t box_rows, int is_bf16);
+// [tokens][heads][d] 16-bit tensor: box {64 columns, box_heads, box_tokens}, 128-byte swizzle.
+bool make_tmap_q3(CUtensorMap *m, const void *base, uint64_t tokens, uint64_t heads, uint64_t d,
+                  uint32_t box_heads, uint32_t box_tokens, int is_bf16);
+// A launch that lets a small grid start as the kernel ahead of it ends (kernels wait on it first).
+cudaError_t launch_kernel(const void *kern, dim3 grid, int threads, int smem, cudaStream_t st,
+                          void **args);
 }  // namespace vlf

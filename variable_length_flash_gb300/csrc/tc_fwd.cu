@@ -797,6 +797,8 @@ cudaError_t launch_combine(const Params &p, cudaStream_t st) {
   return e;
 }
 
+}  // namespace
+
 // Launches kern with programmatic stream serialization when the grid is small (fewer CTAs than
 // SMs): its CTAs may then be made resident while the kernel ahead of them in the stream runs and
 // start the moment it finishes (the kernels wait for it before any global read), instead of
@@ -829,6 +831,7 @@ cudaError_t launch_kernel(const void *kern, dim3 grid, int threads, int smem, cu
   return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
+namespace {
 PFN_cuTensorMapEncodeTiled_v12000 driver_encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void *ptr = nullptr;
@@ -956,7 +959,6 @@ bool tc_forward_supported(const Params &p) {
   return shape;
 }
 
-namespace {
 // 3-D map over Q as [tokens][heads][D] (16-bit): box {64 columns, box_heads, box_tokens},
 // 128-byte swizzle -- 128 dense 128-byte rows (token-major, head-minor) as a 2-D box gives.
 bool make_tmap_q3(CUtensorMap *m, const void *base, uint64_t tokens, uint64_t heads, uint64_t d,
@@ -974,6 +976,7 @@ bool make_tmap_q3(CUtensorMap *m, const void *base, uint64_t tokens, uint64_t he
   return r == CUDA_SUCCESS;
 }
 
+namespace {
 // The kernel instantiation for a dtype and bias kind (0 none, 1 rows from global memory, 2 TMA
 // tiles: unpacked, unsplit, one tile per CTA only).
 // The chosen kernel and whether it takes the full map set (FwdMaps) or Q, K, V alone.
