@@ -598,9 +598,9 @@ size_t vlf_attn_varlen_fwd_prefix_workspace_size(int num_seqs, int total_q, int 
                                                  int max_seqlen_kv, int prefix_len, int h_q,
                                                  int h_kv, int d_qk, int d_v, int dtype,
                                                  unsigned flags, int num_sms) {
-  (void)num_seqs; (void)total_q; (void)max_seqlen_q; (void)max_seqlen_kv; (void)prefix_len; (void)h_q;
-  (void)h_kv; (void)d_qk; (void)d_v; (void)dtype; (void)flags; (void)num_sms;
-  return 0;
+  if (num_sms <= 0) num_sms = sm_count();
+  return vlf::prefix_workspace(num_seqs, total_q, max_seqlen_q, max_seqlen_kv, prefix_len, h_q, h_kv, d_qk,
+                               d_v, dtype, flags, num_sms);
 }
 
 int vlf_attn_varlen_fwd_prefix(const void *q, const void *k_prefix, const void *v_prefix,
@@ -630,8 +630,12 @@ int vlf_attn_varlen_fwd_prefix(const void *q, const void *k_prefix, const void *
   pp.k_pre = k_prefix;
   pp.v_pre = v_prefix;
   pp.prefix_len = prefix_len;
-  (void)workspace_bytes;
-  return vlf::simt_prefix(pp, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
+  const int sms = sm_count();
+  const size_t need = vlf::prefix_workspace(num_seqs, total_q, max_seqlen_q, max_seqlen_kv, prefix_len, h_q, h_kv,
+                                            d_qk, d_v, dtype, flags, sms);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return VLF_ERR_WORKSPACE;
+  const cudaError_t e = vlf::prefix_forward(pp, workspace, sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
 }
 
 size_t vlf_attn_key_weights_workspace_size(int num_seqs, int total_kv, int max_seqlen_q,

@@ -62,7 +62,9 @@ struct PrefixParams {
   const void *k_pre, *v_pre;
   int prefix_len;
 };
-cudaError_t simt_prefix(const PrefixParams &pp, cudaStream_t st);
+size_t prefix_workspace(int num_seqs, int total_q, int max_q, int max_kv, int prefix, int h_q, int h_kv, int d_qk,
+                        int d_v, int dtype, unsigned flags, int num_sms);
+cudaError_t prefix_forward(const PrefixParams &pp, void *workspace, int num_sms, cudaStream_t st);
 
 // Attention weight received by each key (key_weights.cu).
 struct KeyWeightParams {

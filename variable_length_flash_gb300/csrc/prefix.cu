@@ -5,8 +5,12 @@
 // i + P + kv_len - q_len).  out and lse are those of the forward on the concatenated keys.
 #include <math.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
+#include "tc_common.cuh"
 
 namespace vlf {
 namespace {
@@ -157,12 +161,636 @@ cudaError_t simt_by_width(const PrefixParams &pp, cudaStream_t st) {
   return launch_simt<T, 32>(pp, st);
 }
 
-}  // namespace
-
 cudaError_t simt_prefix(const PrefixParams &pp, cudaStream_t st) {
   if (pp.p.dtype == VLF_F32) return simt_by_width<float>(pp, st);
   if (pp.p.dtype == VLF_BF16) return simt_by_width<__nv_bfloat16>(pp, st);
   return simt_by_width<__half>(pp, st);
+}
+
+// ------------------------------------------------------------------------------ tensor-core kernel
+// 16-bit data, widths 64, 96 and 128.  The pipeline of the forward's one-tile kernel: a CTA owns a
+// 128-row tile (R query rows x Gb heads of a kv head, row r = query row r / Gb, head r mod Gb) and
+// walks key tiles of 64 through TMA rings; one warp issues S = Q K^T, another O += P V with P read
+// from TMEM, four warps run the online softmax, a thread per row.  What differs:
+//  * Key tiles come from two tensors.  Tile j < np holds prefix keys 64 j ..., tile j >= np the
+//    sequence's own keys 64 (j - np) ...; a tile never crosses the two, and keys are counted from the
+//    prefix's first one, so that one interval of visible keys per row masks both.
+//  * Two ways to cut the work.  Shared: the prefix part runs with tiles packed from the rows of ALL
+//    sequences -- the prefix is read once per 128 / Gb rows of the batch, not once per sequence --
+//    and the own keys run per sequence; a second kernel merges the parts' fp32 results by their
+//    log-sum-exps.  Per sequence: each row tile walks prefix and own keys in one go (cut into parts
+//    only where the row tiles are too few to fill the GPU).  Shared pays where a sequence's rows fill
+//    less than a tile (decode steps): make_plan below.
+//  * Values behind a sequence's last key belong to the next sequence: they are zeroed in shared memory
+//    before the product, so that an infinity or NaN there (0 x inf) cannot reach this one.
+using namespace tc;
+
+struct PfxMaps {
+  CUtensorMap q, k, v, kp, vp;
+};
+
+constexpr int kBN = 64;  // keys per tile
+constexpr float kLn2f = 0.6931471805599453f;
+constexpr float kMoveMax = 8.0f;  // the reference max moves once a row's max has grown by 2^8
+
+struct PfxPlan {
+  int shared;
+  int gb, nhb;         // heads per row tile, row tiles per kv head's group
+  int rows;            // query rows per row tile
+  int np;              // prefix key tiles
+  int heads;           // h_kv * nhb
+  int rb_pre, rb_own;  // row blocks: of the batch (shared prefix part), of a sequence
+  int parts_pre, parts_own;
+  int parts;           // results per row to merge (0: written directly)
+  unsigned n_pre, n_all;  // CTAs
+};
+
+template <int D>
+struct PfxCfg {
+  static constexpr int KB = (D + 63) / 64, NPAD = KB * 64;
+  static constexpr int QBLK = 128 * 128, KVBLK = kBN * 128;
+  static constexpr int Q_BYTES = KB * QBLK, T_BYTES = KB * KVBLK;
+  static constexpr int NK = 3, NV = D == 64 ? 3 : 2;
+  static constexpr int OFF_K = Q_BYTES, OFF_V = OFF_K + NK * T_BYTES, OFF_BAR = OFF_V + NV * T_BYTES;
+  static constexpr int B_Q = 0, B_KF = 1, B_KE = B_KF + NK, B_VF = B_KE + NK, B_VE = B_VF + NV;
+  static constexpr int B_S = B_VE + NV, B_P = B_S + 2, B_O = B_P + 2, B_DRAIN = B_O + 2, NBAR = B_DRAIN + 2;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tmem address, abort flag, band lo / hi
+  static constexpr int OFF_SEQ = OFF_MISC + 16;         // uint16 [128]: the sequence of each row
+  static constexpr int SMEM = OFF_SEQ + 256;
+  static constexpr uint32_t O_COL = 128, TMEM_COLS = 256;
+  static_assert(SMEM <= 115712, "two CTAs per SM");
+};
+
+template <int D, bool BF16, bool SPLIT>
+__global__ void __launch_bounds__(256, 2)
+tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, const PfxPlan pl, float *o_part,
+                 float *lse_part) {
+  using C = PfxCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  pdl_trigger();
+  pdl_wait();
+  const Params &p = pp.p;
+  const int P = pp.prefix_len;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int is_bf16 = BF16 ? 1 : 0;
+
+  // ---- this CTA's rows and key tiles
+  const bool pre = SPLIT && blockIdx.x < pl.n_pre;  // the shared prefix part
+  int hd, rb, part, slot;
+  Seq sq{0, 0, 0, 0};
+  if (pre) {
+    // row blocks fastest: CTAs that read the same prefix tiles run together
+    int x = blockIdx.x;
+    rb = x % pl.rb_pre;
+    x /= pl.rb_pre;
+    hd = x % pl.heads;
+    part = slot = x / pl.heads;
+  } else {
+    int x = blockIdx.x - pl.n_pre;
+    part = x % pl.parts_own;
+    x /= pl.parts_own;
+    rb = x % pl.rb_own;
+    x /= pl.rb_own;
+    hd = x % pl.heads;
+    const int s = x / pl.heads;
+    if (!load_seq(p, s, sq)) return;
+    if (s == 0 && (__ldg(p.cu_q) != 0 || __ldg(p.cu_kv) != 0)) set_error(p.err, VLF_ERR_BAD_SEQLENS);
+    if (s == p.num_seqs - 1 && (sq.q0 + sq.q_len != p.total_q || sq.k0 + sq.kv_len != p.total_kv))
+      set_error(p.err, VLF_ERR_BAD_SEQLENS);
+    if (p.causal) rb = pl.rb_own - 1 - rb;  // the rows that see most first
+    if (rb * pl.rows >= sq.q_len) return;
+    slot = pl.parts_pre + part;
+  }
+  const int hk = hd / pl.nhb, h0 = hk * p.group + hd % pl.nhb * pl.gb;
+  const int row0 = pre ? rb * pl.rows : sq.q0 + rb * pl.rows;                 // packed row of tile row 0
+  const int nrows = min(pl.rows, (pre ? p.total_q : sq.q0 + sq.q_len) - row0);  // query rows of the tile
+  const int keys = P + sq.kv_len, off = keys - sq.q_len;                      // (per-sequence CTAs)
+
+  const uint32_t base = smem_u32(smem_raw);
+  if (base & 1023u) {
+    if (threadIdx.x == 0) set_error(p.err, VLF_ERR_ALIGN);
+    return;
+  }
+  const uint32_t sQ = base, sK = base + C::OFF_K, sV = base + C::OFF_V;
+  auto bar = [&](int i) { return base + C::OFF_BAR + 8u * (uint32_t)i; };
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem_raw + C::OFF_MISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem_raw + C::OFF_MISC + 4);
+  int *band = reinterpret_cast<int *>(smem_raw + C::OFF_MISC + 8);
+  uint16_t *seq_of = reinterpret_cast<uint16_t *>(smem_raw + C::OFF_SEQ);
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(C::B_Q), 1);
+    for (int i = 0; i < C::NK; ++i) { mbar_init(bar(C::B_KF + i), 1); mbar_init(bar(C::B_KE + i), 1); }
+    for (int i = 0; i < C::NV; ++i) { mbar_init(bar(C::B_VF + i), 1); mbar_init(bar(C::B_VE + i), 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::B_S + i), 1);
+      mbar_init(bar(C::B_P + i), 128);
+      mbar_init(bar(C::B_O + i), 1);
+      mbar_init(bar(C::B_DRAIN + i), 1);
+    }
+    *abort_flag = 0;
+    band[0] = P;
+    band[1] = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  int lo, hi;  // key tiles
+  if (pre) {
+    // which sequence each row belongs to: the threads look at a sequence each (one round of loads),
+    // and at what its rows in this tile see of the prefix
+    if (threadIdx.x < 128) seq_of[threadIdx.x] = 0xffff;
+    __syncthreads();
+    for (int s = threadIdx.x; s < p.num_seqs; s += 256) {
+      const int a = __ldg(p.cu_q + s), b = __ldg(p.cu_q + s + 1);
+      const int c = __ldg(p.cu_kv + s), d = __ldg(p.cu_kv + s + 1);
+      if (a < 0 || a > b || b > p.total_q || b - a > p.max_q || c < 0 || c > d || d > p.total_kv || d - c > p.max_kv)
+        continue;  // (recorded by that sequence's own CTAs)
+      const int x = max(a, row0), y = min(b, row0 + nrows);
+      if (x >= y) continue;
+      for (int i = x; i < y; ++i) seq_of[i - row0] = (uint16_t)s;
+      int klo, khi;
+      kv_band(x - a, y - a, b - a, P + d - c, p.causal, p.window, klo, khi);
+      khi = min(khi, P);
+      if (khi > klo) { atomicMin(&band[0], klo); atomicMax(&band[1], khi); }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (pre) {
+    lo = band[1] > band[0] ? band[0] / kBN : 0;
+    hi = band[1] > band[0] ? (band[1] + kBN - 1) / kBN : 0;
+  } else {
+    int klo, khi;
+    kv_band(rb * pl.rows, rb * pl.rows + nrows, sq.q_len, keys, p.causal, p.window, klo, khi);
+    lo = klo < P ? klo / kBN : pl.np + (klo - P) / kBN;
+    hi = khi <= P ? (khi + kBN - 1) / kBN : pl.np + (khi - P + kBN - 1) / kBN;
+    if (SPLIT && pl.shared) lo = max(lo, pl.np);  // the prefix part has CTAs of its own
+    if (khi <= klo || hi < lo) hi = lo;
+  }
+  if (SPLIT) {
+    // this part's share (possibly none: it then writes O = 0 and LSE = -inf)
+    const int n = pre ? pl.parts_pre : pl.parts_own, per = (hi - lo + n - 1) / n;
+    lo = min(hi, lo + part * per);
+    hi = min(hi, lo + per);
+  }
+  const uint32_t tmem = *tmem_holder;
+  // first key of tile j, and the end of the keys that its tensor holds for this CTA
+  auto key_of = [&](int j) { return j < pl.np ? j * kBN : P + (j - pl.np) * kBN; };
+  auto end_of = [&](int j) { return j < pl.np ? P : keys; };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0 && hi > lo) {
+      mbar_expect_tx(bar(C::B_Q), C::KB * pl.gb * pl.rows * 128);
+      for (int c = 0; c < C::KB; ++c) tma_load_3d(sQ + c * C::QBLK, &maps.q, 64 * c, h0, row0, bar(C::B_Q));
+      auto load = [&](const CUtensorMap *pm, const CUtensorMap *om, int j, uint32_t dst, uint32_t b) {
+        const CUtensorMap *m = j < pl.np ? pm : om;
+        const int y = j < pl.np ? j * kBN : sq.k0 + (j - pl.np) * kBN;
+        mbar_expect_tx(b, C::T_BYTES);
+        for (int c = 0; c < C::KB; ++c) tma_load_2d(dst + c * C::KVBLK, m, hk * D + 64 * c, y, b);
+      };
+      bool ok = true;
+      int nk = 0, nv = 0;
+      for (int j = lo; j < hi + 1 && ok; ++j) {  // K leads V by one tile
+        if (j < hi) {
+          const int sl = nk % C::NK;
+          if (nk >= C::NK) ok = mbar_wait(bar(C::B_KE + sl), (nk / C::NK - 1) & 1, abort_flag, p.err);
+          if (!ok) break;
+          load(&maps.kp, &maps.k, j, sK + sl * C::T_BYTES, bar(C::B_KF + sl));
+          ++nk;
+        }
+        if (j > lo) {
+          const int sl = nv % C::NV;
+          if (nv >= C::NV) ok = mbar_wait(bar(C::B_VE + sl), (nv / C::NV - 1) & 1, abort_flag, p.err);
+          if (!ok) break;
+          load(&maps.vp, &maps.v, j - 1, sV + sl * C::T_BYTES, bar(C::B_VF + sl));
+          ++nv;
+        }
+      }
+      // no copy may still be landing when the CTA leaves
+      drain_wait(bar(C::B_Q), 0);
+      for (int i = 0; i < C::NK && i < nk; ++i) drain_wait(bar(C::B_KF + i), ((nk - 1 - i) / C::NK) & 1);
+      for (int i = 0; i < C::NV && i < nv; ++i) drain_wait(bar(C::B_VF + i), ((nv - 1 - i) / C::NV) & 1);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ S = Q K^T
+    if (hi > lo) {
+      const uint32_t id = idesc_f16(is_bf16, 128, kBN, 0, 0);
+      const uint64_t dq = sdesc_sw128(sQ, 16, 1024), dk0 = sdesc_sw128(sK, 16, 1024);
+      bool ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_Q), 0, abort_flag, p.err));
+      for (int n = 0; n < hi - lo && ok; ++n) {
+        const int b = n & 1, sl = n % C::NK;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_KF + sl), (n / C::NK) & 1, abort_flag, p.err));
+        if (!ok) break;
+        if (n >= 2) {  // S(n) overwrites the buffer that P(n - 2) was read from
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_O + b), ((n - 2) >> 1) & 1, abort_flag, p.err));
+          if (!ok) break;
+        }
+        fence_after();
+        const uint64_t dk = dk0 + (uint64_t)((sl * C::T_BYTES) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss_w(tmem + 64 * b, dq + (uint64_t)(((kk >> 2) * C::QBLK + (kk & 3) * 32) >> 4),
+                   dk + (uint64_t)(((kk >> 2) * C::KVBLK + (kk & 3) * 32) >> 4), id, kk > 0);
+        mma_commit_w(bar(C::B_S + b));
+        mma_commit_w(bar(C::B_KE + sl));
+      }
+      mma_commit_w(bar(C::B_DRAIN));
+      drain_wait(bar(C::B_DRAIN), 0);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ O += P V
+    if (hi > lo) {
+      const uint32_t id = idesc_f16(is_bf16, 128, C::NPAD, 0, 1);  // V is MN-major
+      const uint64_t dv0 = sdesc_sw128(sV, C::KVBLK, 1024);
+      bool ok = true;
+      for (int n = 0; n < hi - lo && ok; ++n) {
+        const int b = n & 1, sl = n % C::NV, j = lo + n;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_VF + sl), (n / C::NV) & 1, abort_flag, p.err));
+        if (!ok) break;
+        const int have = end_of(j) - key_of(j);
+        if (j >= pl.np && have < kBN) {
+          // the rows behind the sequence's last key: zero
+          for (int c = 0; c < C::KB; ++c) {
+            const uint32_t a = sV + sl * C::T_BYTES + c * C::KVBLK;
+            for (int x = have * 128 + lane * 16; x < kBN * 128; x += 512) sts_v4(a + x, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_P + b), (n >> 1) & 1, abort_flag, p.err));
+        if (!ok) break;
+        fence_after();
+        const uint64_t dv = dv0 + (uint64_t)((sl * C::T_BYTES) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk)
+          mma_ts_w(tmem + C::O_COL, tmem + 64 * b + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), id,
+                   (n > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_w(bar(C::B_O + b));
+        mma_commit_w(bar(C::B_VE + sl));
+      }
+      mma_commit_w(bar(C::B_DRAIN + 1));
+      drain_wait(bar(C::B_DRAIN + 1), 0);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ softmax / epilogue
+    const int r = 32 * (warp & 3) + lane, tok = r / pl.gb;
+    const int head = h0 + r % pl.gb, grow = row0 + tok;
+    bool row_ok = tok < nrows;
+    int vlo = 0, vhi = 0;  // this row's visible keys
+    if (pre) {
+      const int s = seq_of[row_ok ? tok : 0];
+      row_ok = row_ok && s != 0xffff;
+      if (row_ok) {
+        const int q0 = __ldg(p.cu_q + s), ql = __ldg(p.cu_q + s + 1) - q0;
+        const int ks = P + __ldg(p.cu_kv + s + 1) - __ldg(p.cu_kv + s);
+        visible_range(grow - q0, ks - ql, ks, p.causal, p.window, vlo, vhi);
+      }
+    } else if (row_ok) {
+      visible_range(grow - sq.q0, off, keys, p.causal, p.window, vlo, vhi);
+    }
+    const uint32_t s_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16), o_addr = s_addr + C::O_COL;
+    const float sl2 = p.scale_log2;
+    // l: sum of the rounded P that the MMA multiplies (normalises O); lf: the fp32 sum (LSE)
+    float m_ref = -INFINITY, l = 0.f, lf = 0.f;
+    const int nt = hi - lo;
+    bool ok = true;
+    for (int n = 0; n < nt; ++n) {
+      const int j = lo + n, b = n & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_S + b), (n >> 1) & 1, abort_flag, p.err));
+      if (!ok) break;
+      fence_after();
+      const uint32_t sb = s_addr + 64 * b;
+      const int kb = key_of(j), elo = vlo - kb, ehi = min(vhi, end_of(j)) - kb;
+      const bool full = elo <= 0 && ehi >= kBN;
+      uint32_t v[kBN];
+      __syncwarp();
+      tmem_ld32_at(sb + 0, v, 0);
+      tmem_ld32_at(sb + 32, v, 32);
+      tmem_ld_wait();
+      // P = 2^(logit2 - m_ref), two at a time, in 16 bits over the S buffer's first 32 columns, with
+      // the fp32 sum and the sum of the rounded P
+      float sumr = 0.f, lsum = 0.f;
+      auto exp_pass = [&](float scale, float neg_m) {
+        const uint64_t scale2 = f2pack(scale, scale), negm2 = f2pack(neg_m, neg_m);
+        uint64_t sf0 = f2pack(0.f, 0.f), sf1 = sf0;
+        float sr0 = 0.f, sr1 = 0.f;
+#pragma unroll
+        for (int ch = 0; ch < kBN / 32; ++ch) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int c = 32 * ch + 2 * e;
+            const float2 x = f2unpack(fma2(f2pack(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), scale2, negm2));
+            const float pa = ex2(x.x), pb = ex2(x.y);
+            pk[e] = pack2(pa, pb, is_bf16);
+            if (e & 1) {
+              sf1 = add2(sf1, f2pack(pa, pb));
+              sr1 = add_halves(sr1, pk[e], is_bf16);
+            } else {
+              sf0 = add2(sf0, f2pack(pa, pb));
+              sr0 = add_halves(sr0, pk[e], is_bf16);
+            }
+          }
+          __syncwarp();
+          tmem_st16(sb + ch * 16, pk);
+        }
+        const float2 f0 = f2unpack(sf0), f1 = f2unpack(sf1);
+        lsum = (f0.x + f0.y) + (f1.x + f1.y);
+        sumr = sr0 + sr1;
+      };
+      auto row_max = [&]() {
+        float m8[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float *f = reinterpret_cast<const float *>(v) + 8 * q;
+          m8[q] = fmax3(fmax3(f[0], f[1], f[2]), fmax3(f[3], f[4], f[5]), fmaxf(f[6], f[7]));
+        }
+        return fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+      };
+      // Unmasked tile and a reference max in every row of the warp: P with that reference, the row
+      // max beside it; only a max beyond the threshold goes through the general pass.
+      bool done = false;
+      if (__all_sync(0xffffffffu, full && m_ref != -INFINITY)) {
+        exp_pass(sl2, -m_ref);
+        done = !__any_sync(0xffffffffu, row_max() * sl2 > m_ref + kMoveMax);
+        if (!done) tmem_st_wait();  // (the general pass rewrites P)
+      }
+      if (!done) {
+        float mx;
+        if (full) {
+          mx = row_max() * sl2;
+        } else {
+          mx = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < kBN; ++e) {
+            const float x = e >= elo && e < ehi ? __uint_as_float(v[e]) * sl2 : -INFINITY;
+            v[e] = __float_as_uint(x);
+            mx = fmaxf(mx, x);
+          }
+        }
+        const float m_new = fmaxf(m_ref, mx);
+        float alpha = 1.f;
+        const bool move = m_new != -INFINITY && m_new > m_ref + kMoveMax;
+        if (move) alpha = ex2(m_ref - m_new);  // m_ref = -inf: 0
+        const bool need = move && n > 0 && l > 0.f;
+        if (__any_sync(0xffffffffu, need)) {
+          // O is rescaled once the product before (so every earlier one) has completed
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_O + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag, p.err));
+          if (!ok) break;
+          fence_after();
+          const float a = need ? alpha : 1.f;
+#pragma unroll 1
+          for (int ch = 0; ch < D / 32; ++ch) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + ch * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+            tmem_st32(o_addr + ch * 32, o);
+          }
+        }
+        if (move) {
+          l *= alpha;
+          lf *= alpha;
+          m_ref = m_new;
+        }
+        exp_pass(full ? sl2 : 1.f, m_ref == -INFINITY ? 0.f : -m_ref);
+      }
+      l += sumr;
+      lf += lsum;
+      __syncwarp();
+      tmem_st_wait();
+      fence_before();
+      mbar_arrive(bar(C::B_P + b));
+    }
+    if (ok && nt > 0) ok = mbar_wait(bar(C::B_O + ((nt - 1) & 1)), ((nt - 1) >> 1) & 1, abort_flag, p.err);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      fence_after();
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float lse = lf > 0.f ? (m_ref + lg2(lf)) * kLn2f : -INFINITY;
+      const size_t at = (size_t)grow * p.h_q + head;  // (row, head)
+#pragma unroll 1
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t v[32];
+        if (nt > 0) {
+          __syncwarp();
+          tmem_ld32(o_addr + ch * 32, v);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0u;
+        }
+        if (!row_ok) continue;
+        if (SPLIT) {
+          float4 *dst = reinterpret_cast<float4 *>(o_part + ((size_t)slot * p.total_q * p.h_q + at) * D) + ch * 8;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            dst[q] = make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
+                                 __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
+        } else {
+          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + at * D * 2) + ch * 4;
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            pk[e] = pack2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv, is_bf16);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) dst[q] = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+        }
+      }
+      if (row_ok) {
+        if (SPLIT) lse_part[(size_t)slot * p.total_q * p.h_q + at] = lse;
+        else if (p.lse) p.lse[(size_t)head * p.total_q + grow] = lse;
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Merges the parts: LSE = log sum_s exp(L_s), O = sum_s exp(L_s - LSE) O_s.  A warp per (row, head);
+// a lane holds four columns of a part (width 64: half a warp per part), the weights sit in the lanes.
+// Rows of no sequence are left alone.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) prefix_merge_kernel(const Params p, int parts, const float *o_part,
+                                                           const float *lse_part) {
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  pdl_trigger();
+  pdl_wait();
+  const size_t pairs = (size_t)p.total_q * p.h_q;
+  const size_t w = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (w >= pairs || w / p.h_q >= (size_t)max(0, __ldg(p.cu_q + p.num_seqs))) return;
+  constexpr int NL = D / 4;                // lanes per part
+  constexpr int PER = NL <= 16 ? 2 : 1;    // parts at a time
+  const int sub = PER == 2 ? lane >> 4 : 0, c = PER == 2 ? lane & 15 : lane;
+  float m = -INFINITY;
+  for (int s = lane; s < parts; s += 32) m = fmaxf(m, lse_part[s * pairs + w]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float mm = m == -INFINITY ? 0.f : m;
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < parts; s0 += 32) {
+    const float e = s0 + lane < parts ? expf(lse_part[(s0 + lane) * pairs + w] - mm) : 0.f;
+    sum += e;
+    const int n = min(32, parts - s0);
+#pragma unroll 4
+    for (int s = 0; s < n; s += PER) {
+      const float wgt = __shfl_sync(0xffffffffu, e, (s + sub) & 31);
+      if (s + sub < n && c < NL) {
+        const float4 x = *reinterpret_cast<const float4 *>(o_part + ((s0 + s + sub) * pairs + w) * D + 4 * c);
+        acc.x = fmaf(wgt, x.x, acc.x);
+        acc.y = fmaf(wgt, x.y, acc.y);
+        acc.z = fmaf(wgt, x.z, acc.z);
+        acc.w = fmaf(wgt, x.w, acc.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (PER == 2) {
+    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  if (c < NL && sub == 0) {
+    T y[4] = {from_f32<T>(acc.x * inv), from_f32<T>(acc.y * inv), from_f32<T>(acc.z * inv), from_f32<T>(acc.w * inv)};
+    *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + w * D + 4 * c) = *reinterpret_cast<uint2 *>(y);
+  }
+  if (lane == 0 && p.lse)
+    p.lse[(w % p.h_q) * p.total_q + w / p.h_q] = m == -INFINITY ? -INFINITY : m + logf(sum);
+}
+
+bool tc_shape(int d_qk, int d_v, int dtype, unsigned flags) {
+  return (dtype == VLF_F16 || dtype == VLF_BF16) && !(flags & VLF_FLAG_FORCE_SIMT) && d_qk == d_v &&
+         (d_qk == 64 || d_qk == 96 || d_qk == 128);
+}
+
+// How the work is cut (sizes alone; the lengths are on the device).
+//  * Shared when the batch's rows pack into at most half as many tiles as the sequences' rows do one
+//    by one.
+//  * Parts: as many as give every resident CTA slot (two per SM) about two runs of key tiles, four
+//    tiles at least each.
+PfxPlan make_plan(int num_seqs, int total_q, int max_q, int max_kv, int prefix, int h_q, int h_kv, int num_sms) {
+  PfxPlan pl{};
+  const int group = h_q / h_kv;
+  pl.gb = std::min(group, 128);
+  while (group % pl.gb) --pl.gb;
+  pl.nhb = group / pl.gb;
+  pl.rows = 128 / pl.gb;
+  pl.heads = h_kv * pl.nhb;
+  pl.np = (prefix + kBN - 1) / kBN;
+  const long long no = ((long long)max_kv + kBN - 1) / kBN;
+  pl.rb_own = (max_q + pl.rows - 1) / pl.rows;
+  pl.rb_pre = (total_q + pl.rows - 1) / pl.rows;
+  // row tiles of the sequences one by one, as far as the sizes tell
+  const long long own_tiles = std::min((long long)num_seqs * pl.rb_own, (long long)pl.rb_pre + num_seqs);
+  const long long slots = 2ll * num_sms;
+  pl.shared = pl.np > 0 && own_tiles >= 2ll * pl.rb_pre;
+  pl.parts_pre = 0;
+  pl.parts_own = 1;
+  const long long own_ctas = std::max(1ll, own_tiles * pl.heads);
+  if (pl.shared) {
+    const long long pre_ctas = (long long)pl.rb_pre * pl.heads;
+    const long long run = std::max(4ll, (pre_ctas * pl.np + own_ctas * no) / (2 * slots));
+    pl.parts_pre = (int)std::max(1ll, std::min({((long long)pl.np + run - 1) / run, 48ll}));
+    pl.parts_own = (int)std::max(1ll, std::min({(no + run - 1) / run, 16ll}));
+  } else if (own_ctas < slots) {
+    pl.parts_own = (int)std::max(1ll, std::min({slots / own_ctas, (pl.np + no) / 4, 64ll}));
+  }
+  pl.parts = pl.parts_pre + pl.parts_own;
+  if (pl.parts == 1) pl.parts = 0;
+  const long long n_pre = (long long)pl.rb_pre * pl.heads * pl.parts_pre;
+  const long long n_own = (long long)num_seqs * pl.heads * pl.rb_own * pl.parts_own;
+  pl.n_pre = (unsigned)n_pre;
+  pl.n_all = n_pre + n_own <= 0x7fffffffll ? (unsigned)(n_pre + n_own) : 0u;
+  return pl;
+}
+
+size_t parts_bytes(const PfxPlan &pl, int total_q, int h_q, int d) {
+  const size_t pairs = (size_t)pl.parts * total_q * h_q;
+  return ((pairs * d * sizeof(float) + 255) & ~(size_t)255) + ((pairs * sizeof(float) + 255) & ~(size_t)255);
+}
+
+template <int D>
+cudaError_t launch_tc(const PrefixParams &pp, PfxPlan pl, void *workspace, cudaStream_t st) {
+  const Params &p = pp.p;
+  using C = PfxCfg<D>;
+  PfxMaps maps;
+  const int bf = p.dtype == VLF_BF16;
+  const uint64_t kc = (uint64_t)p.h_kv * D;
+  const bool have_p = pp.prefix_len > 0, have_o = p.total_kv > 0;
+  if (!make_tmap_q3(&maps.q, p.q, p.total_q, p.h_q, D, pl.gb, pl.rows, bf)) return cudaErrorInvalidValue;
+  if (have_p && (!make_tmap_16bit(&maps.kp, pp.k_pre, pp.prefix_len, kc, kc, kBN, bf) ||
+                 !make_tmap_16bit(&maps.vp, pp.v_pre, pp.prefix_len, kc, kc, kBN, bf)))
+    return cudaErrorInvalidValue;
+  if (have_o && (!make_tmap_16bit(&maps.k, p.k, p.total_kv, kc, kc, kBN, bf) ||
+                 !make_tmap_16bit(&maps.v, p.v, p.total_kv, kc, kc, kBN, bf)))
+    return cudaErrorInvalidValue;
+  if (!have_p) { maps.kp = maps.k; maps.vp = maps.v; }  // (never read: no tile comes from it)
+  if (!have_o) { maps.k = maps.kp; maps.v = maps.vp; }
+  float *o_part = nullptr, *lse_part = nullptr;
+  if (pl.parts) {
+    o_part = static_cast<float *>(workspace);
+    lse_part = reinterpret_cast<float *>(
+        static_cast<uint8_t *>(workspace) +
+        (((size_t)pl.parts * p.total_q * p.h_q * D * sizeof(float) + 255) & ~(size_t)255));
+  }
+  const void *kern = pl.parts ? (bf ? (const void *)tc_prefix_kernel<D, true, true>
+                                    : (const void *)tc_prefix_kernel<D, false, true>)
+                              : (bf ? (const void *)tc_prefix_kernel<D, true, false>
+                                    : (const void *)tc_prefix_kernel<D, false, false>);
+  cudaError_t e = set_smem_once(kern, C::SMEM);
+  if (e != cudaSuccess) return e;
+  PrefixParams a = pp;
+  void *args[5] = {&maps, &a, &pl, &o_part, &lse_part};
+  e = launch_kernel(kern, dim3(pl.n_all), 256, C::SMEM, st, args);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  if (pl.parts) {
+    Params pm = p;
+    void *margs[4] = {&pm, &pl.parts, &o_part, &lse_part};
+    const size_t blocks = ((size_t)p.total_q * p.h_q + 7) / 8;
+    e = launch_dependent(bf ? (const void *)prefix_merge_kernel<D, true> : (const void *)prefix_merge_kernel<D, false>,
+                         dim3((unsigned)blocks), 256, 0, st, margs);
+    if (e == cudaSuccess) count_launch();
+  }
+  return e;
+}
+
+}  // namespace
+
+size_t prefix_workspace(int num_seqs, int total_q, int max_q, int max_kv, int prefix, int h_q, int h_kv, int d_qk,
+                        int d_v, int dtype, unsigned flags, int num_sms) {
+  if (num_seqs < 1 || total_q < 1 || max_q < 1 || max_kv < 0 || prefix < 0 || h_kv < 1 || h_q < 1 || h_q % h_kv ||
+      num_sms < 1 || !tc_shape(d_qk, d_v, dtype, flags))
+    return 0;
+  const PfxPlan pl = make_plan(num_seqs, total_q, max_q, max_kv, prefix, h_q, h_kv, num_sms);
+  return pl.parts ? parts_bytes(pl, total_q, h_q, d_v) : 0;
+}
+
+cudaError_t prefix_forward(const PrefixParams &pp, void *workspace, int num_sms, cudaStream_t st) {
+  const Params &p = pp.p;
+  // (without rows or keys there is nothing to stage)
+  if (!tc_shape(p.d_qk, p.d_v, p.dtype, p.flags) || p.total_q == 0 || (p.total_kv == 0 && pp.prefix_len == 0))
+    return simt_prefix(pp, st);
+  const PfxPlan pl = make_plan(p.num_seqs, p.total_q, p.max_q, p.max_kv, pp.prefix_len, p.h_q, p.h_kv, num_sms);
+  if (pl.n_all == 0) return cudaErrorInvalidValue;
+  if (p.d_qk == 64) return launch_tc<64>(pp, pl, workspace, st);
+  if (p.d_qk == 96) return launch_tc<96>(pp, pl, workspace, st);
+  return launch_tc<128>(pp, pl, workspace, st);
 }
 
 }  // namespace vlf

@@ -472,4 +472,7 @@ bool make_tmap_q3(CUtensorMap *m, const void *base, uint64_t tokens, uint64_t he
 // A launch that lets a small grid start as the kernel ahead of it ends (kernels wait on it first).
 cudaError_t launch_kernel(const void *kern, dim3 grid, int threads, int smem, cudaStream_t st,
                           void **args);
+// The same for any grid: for a kernel that follows one of this library's in the stream.
+cudaError_t launch_dependent(const void *kern, dim3 grid, int threads, int smem, cudaStream_t st,
+                             void **args);
 }  // namespace vlf

@@ -818,6 +818,11 @@ cudaError_t launch_kernel(const void *kern, dim3 grid, int threads, int smem, cu
     const cudaError_t e = cudaLaunchKernel(kern, grid, dim3(threads), args, (size_t)smem, st);
     return e != cudaSuccess ? e : cudaGetLastError();
   }
+  return launch_dependent(kern, grid, threads, smem, st, args);
+}
+
+cudaError_t launch_dependent(const void *kern, dim3 grid, int threads, int smem, cudaStream_t st,
+                             void **args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
