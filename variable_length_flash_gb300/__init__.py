@@ -541,19 +541,21 @@ def vlf_attn_varlen_bwd_noalloc(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlen
 
 
 # ------------------------------------------------------------------ decoding on a bounded cache
+# Host time counts in a decode step, whose kernels take microseconds: each call first tests all
+# its conditions in one expression (a tensor attribute costs ~0.1 us), and only where that fails
+# takes the checks that say which one it was.
 def _same_device(like, **tensors):
     for name, t in tensors.items():
         if t is not None and t.device != like.device:
-            raise VlfError(VLF_ERR_INVALID, f"{name} is on {t.device}, q on {like.device}")
+            raise VlfError(VLF_ERR_INVALID, f"{name} is on {t.device}, not on {like.device}")
 
 
-def _new(shape, dtype, like, stream):
-    """A fresh tensor that a kernel on ``stream`` (None: the current one) will use: the caching
-    allocator is told about a stream that is not the one it was allocated on."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None and t.numel():
-        t.record_stream(stream)
-    return t
+def _used_on(stream, *tensors):
+    """Tells the caching allocator that fresh tensors are used on a stream other than the one they
+    were allocated on."""
+    for t in tensors:
+        if t is not None and t.numel():
+            t.record_stream(stream)
 
 
 def _given(t, name, shape, dtype):
@@ -564,15 +566,17 @@ def _given(t, name, shape, dtype):
     return t
 
 
-def _workspace(need, workspace, like, stream):
-    """(pointer, bytes) of a workspace of ``need`` bytes: the caller's, or a new one."""
-    if workspace is None:
-        if need == 0:
-            return None, 0, None
-        workspace = _new(need, torch.uint8, like, stream)
-    else:
-        _req(workspace, "workspace")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+_WORKSPACES = {}  # (entry point, shape, device) -> bytes of workspace
+
+
+def _workspace_size(fn, key):
+    """fn(*key[1:-1], 0 SMs given), remembered: it depends on the shape and the device alone."""
+    need = _WORKSPACES.get(key)
+    if need is None:
+        need = int(fn(*key[1:-1], 0))
+        if len(_WORKSPACES) < 4096:
+            _WORKSPACES[key] = need
+    return need
 
 
 def _rope_rows(t, name, dtype, total=None):
@@ -591,6 +595,19 @@ def _rope_rows(t, name, dtype, total=None):
     return s0 if n > 1 else h * d
 
 
+_SECTIONS = {}  # section counts -> the C array of them
+
+
+def _sections(sections):
+    key = tuple(sections)
+    arr = _SECTIONS.get(key)
+    if arr is None:
+        arr = (ctypes.c_int * len(key))(*key)
+        if len(_SECTIONS) < 256:
+            _SECTIONS[key] = arr
+    return arr
+
+
 def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=False, q_out=None,
              k_out=None, stream=None):
     """Rotary positions of q [T,Hq,D] and k [T,Hk,D] (k may be None) with one or several position
@@ -601,20 +618,28 @@ def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, invers
     slices of a packed projection (their tokens may be strided); ``q_out`` / ``k_out`` may be q / k
     themselves.  Returns (q_out, k_out)."""
     dtype = q.dtype
-    if dtype not in _DTYPE:
+    dt = _DTYPE.get(dtype)
+    if dt is None:
         raise VlfError(VLF_ERR_INVALID, f"unsupported dtype {dtype}")
     sq = _rope_rows(q, "q", dtype)
     total, hq, d = q.shape
+    dev = q.get_device()
     hk, sk, sko, k_p, ko_p = 0, 0, 0, None, None
     if k is not None:
         sk = _rope_rows(k, "k", dtype, total)
         hk = k.shape[1]
         if k.shape[2] != d:
             raise VlfError(VLF_ERR_INVALID, "q and k must have the same head_dim")
-    _req(positions, "positions", torch.int32), _req(inv_freq, "inv_freq", torch.float32)
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if positions.dim() > 2 or positions.shape[-1] != total or inv_freq.dim() != 1:
+        k_p = k.data_ptr()
+    shape = positions.shape
+    if not (positions.dtype is torch.int32 and inv_freq.dtype is torch.float32
+            and positions.get_device() == dev and inv_freq.get_device() == dev
+            and positions.is_contiguous() and inv_freq.is_contiguous() and inv_freq.dim() == 1
+            and 1 <= len(shape) <= 2 and shape[-1] == total):
+        _req(positions, "positions", torch.int32), _req(inv_freq, "inv_freq", torch.float32)
+        _same_device(q, positions=positions, inv_freq=inv_freq)
         raise VlfError(VLF_ERR_INVALID, "positions must be [tokens] or [axes, tokens], inv_freq [rot / 2]")
+    axes = 1 if len(shape) == 1 else shape[0]
     if sections is None:
         if axes != 1:
             raise VlfError(VLF_ERR_INVALID, "several position axes need sections")
@@ -622,43 +647,35 @@ def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, invers
     else:
         if len(sections) != axes:
             raise VlfError(VLF_ERR_INVALID, f"{len(sections)} sections for {axes} position axes")
-        sec = (ctypes.c_int * axes)(*sections)
-    if q_out is None:
-        q_out = _new(q.shape, dtype, q, stream)
+        sec = _sections(sections)
+    fresh_q, fresh_k = q_out is None, k_out is None
+    if fresh_q:
+        q_out = q.new_empty((total, hq, d))
         sqo = hq * d
     else:
         sqo = _rope_rows(q_out, "q_out", dtype, total)
-    if tuple(q_out.shape) != tuple(q.shape):
-        raise VlfError(VLF_ERR_INVALID, "q_out must have q's shape")
+        if q_out.shape != q.shape:
+            raise VlfError(VLF_ERR_INVALID, "q_out must have q's shape")
+        _same_device(q, q_out=q_out)
     if k is not None:
-        if k_out is None:
-            k_out = _new(k.shape, dtype, k, stream)
+        if fresh_k:
+            k_out = k.new_empty((total, hk, d))
             sko = hk * d
         else:
             sko = _rope_rows(k_out, "k_out", dtype, total)
-        if tuple(k_out.shape) != tuple(k.shape):
-            raise VlfError(VLF_ERR_INVALID, "k_out must have k's shape")
-        k_p, ko_p = k.data_ptr(), k_out.data_ptr()
-    _same_device(q, k=k, positions=positions, inv_freq=inv_freq, q_out=q_out, k_out=k_out)
+            if k_out.shape != k.shape:
+                raise VlfError(VLF_ERR_INVALID, "k_out must have k's shape")
+        if k.get_device() != dev or k_out.get_device() != dev:
+            _same_device(q, k=k, k_out=k_out)
+        ko_p = k_out.data_ptr()
+    if stream is not None:
+        _used_on(stream, q_out if fresh_q else None, k_out if fresh_k else None)
     st = _lib.vlf_rope(q.data_ptr(), sq, k_p, sk, positions.data_ptr(), axes, sec, inv_freq.data_ptr(),
-                       total, hq, hk, d, 2 * inv_freq.shape[0], _DTYPE[dtype], 1 if interleaved else 0,
+                       total, hq, hk, d, 2 * inv_freq.shape[0], dt, 1 if interleaved else 0,
                        1 if inverse else 0, q_out.data_ptr(), sqo, ko_p, sko, _stream(stream, q))
     if st != VLF_OK:
         _check(st, "vlf_rope")
     return q_out, k_out
-
-
-_WORKSPACES = {}  # (entry point, shape, device) -> bytes of workspace
-
-
-def _workspace_size(fn, key):
-    """fn(*key[:-1], 0 SMs given), remembered: it depends on the shape and the device alone."""
-    need = _WORKSPACES.get((fn.__name__, key))
-    if need is None:
-        need = int(fn(*key[:-1], 0))
-        if len(_WORKSPACES) < 4096:
-            _WORKSPACES[(fn.__name__, key)] = need
-    return need
 
 
 def vlf_attn_varlen_fwd_prefix_workspace_size(num_seqs, total_q, max_seqlen_q, max_seqlen_kv,
@@ -670,6 +687,10 @@ def vlf_attn_varlen_fwd_prefix_workspace_size(num_seqs, total_q, max_seqlen_q, m
         num_sms))
 
 
+def _dense(t, dtype, dev):
+    return t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+
+
 def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seqlens_kv,
                                max_seqlen_q, max_seqlen_kv=None, scale=None, causal=False, window=0,
                                out=None, lse=None, workspace=None, stream=None, flags=0):
@@ -678,8 +699,16 @@ def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seq
     the concatenated keys, with the prefix read once.  Returns out [Tq, Hq, Dv] and lse fp32
     [Hq, Tq].  ``workspace``: at least vlf_attn_varlen_fwd_prefix_workspace_size bytes, allocated
     here when not given."""
-    _fwd_checks(q, k, v, cu_seqlens_q, cu_seqlens_kv)
-    _req(k_prefix, "k_prefix", q.dtype), _req(v_prefix, "v_prefix", q.dtype)
+    dtype, dev = q.dtype, q.get_device()
+    i32 = torch.int32
+    if not (dtype in _DTYPE and dev >= 0 and q.is_contiguous() and _dense(k, dtype, dev)
+            and _dense(v, dtype, dev) and _dense(k_prefix, dtype, dev) and _dense(v_prefix, dtype, dev)
+            and _dense(cu_seqlens_q, i32, dev) and _dense(cu_seqlens_kv, i32, dev)
+            and q.dim() == 3 and k.dim() == 3 and v.dim() == 3):
+        _fwd_checks(q, k, v, cu_seqlens_q, cu_seqlens_kv)
+        _req(k_prefix, "k_prefix", dtype), _req(v_prefix, "v_prefix", dtype)
+        _same_device(q, k_prefix=k_prefix, v_prefix=v_prefix, k=k, v=v, cu_seqlens_q=cu_seqlens_q,
+                     cu_seqlens_kv=cu_seqlens_kv)
     tq, hq, dqk = q.shape
     tk, hkv, dv = v.shape
     if k.shape != (tk, hkv, dqk):
@@ -687,23 +716,40 @@ def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seq
     n = k_prefix.shape[0]
     if k_prefix.shape != (n, hkv, dqk) or v_prefix.shape != (n, hkv, dv):
         raise VlfError(VLF_ERR_INVALID, "k_prefix / v_prefix must be [prefix_len, H_kv, D]")
-    if cu_seqlens_q.numel() != cu_seqlens_kv.numel() or cu_seqlens_q.numel() < 1:
+    nseq = cu_seqlens_q.numel() - 1
+    if nseq != cu_seqlens_kv.numel() - 1 or nseq < 0:
         raise VlfError(VLF_ERR_INVALID, "cu_seqlens_q and cu_seqlens_kv must have num_seqs + 1 entries")
     if max_seqlen_kv is None:
         max_seqlen_kv = _max_len(cu_seqlens_kv)
-    out = _new((tq, hq, dv), q.dtype, q, stream) if out is None else _given(out, "out", (tq, hq, dv), q.dtype)
-    lse = _new((hq, tq), torch.float32, q, stream) if lse is None else _given(lse, "lse", (hq, tq), torch.float32)
-    _same_device(q, k_prefix=k_prefix, v_prefix=v_prefix, k=k, v=v, cu_seqlens_q=cu_seqlens_q,
-                 cu_seqlens_kv=cu_seqlens_kv, out=out, lse=lse, workspace=workspace)
-    nseq, mq, mk, dt = cu_seqlens_q.numel() - 1, int(max_seqlen_q), int(max_seqlen_kv), _DTYPE[q.dtype]
+    fresh = []
+    if out is None:
+        out = q.new_empty((tq, hq, dv))
+        fresh.append(out)
+    else:
+        _given(out, "out", (tq, hq, dv), dtype), _same_device(q, out=out)
+    if lse is None:
+        lse = q.new_empty((hq, tq), dtype=torch.float32)
+        fresh.append(lse)
+    else:
+        _given(lse, "lse", (hq, tq), torch.float32), _same_device(q, lse=lse)
+    mq, mk, dt, flags = int(max_seqlen_q), int(max_seqlen_kv), _DTYPE[dtype], int(flags)
     need = _workspace_size(_lib.vlf_attn_varlen_fwd_prefix_workspace_size,
-                           (nseq, tq, mq, mk, n, hq, hkv, dqk, dv, dt, int(flags), q.get_device()))
-    ws_p, ws_n, workspace = _workspace(need, workspace, q, stream)
+                           ("prefix", nseq, tq, mq, mk, n, hq, hkv, dqk, dv, dt, flags, dev))
+    ws_p, ws_n = None, 0
+    if workspace is not None:
+        _req(workspace, "workspace"), _same_device(q, workspace=workspace)
+        ws_p, ws_n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif need:
+        workspace = q.new_empty(need, dtype=torch.uint8)
+        fresh.append(workspace)
+        ws_p, ws_n = workspace.data_ptr(), need
+    if stream is not None:
+        _used_on(stream, *fresh)
     st = _lib.vlf_attn_varlen_fwd_prefix(
         q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), n, k.data_ptr(), v.data_ptr(),
         cu_seqlens_q.data_ptr(), cu_seqlens_kv.data_ptr(), nseq, tq, tk, mq, mk, hq, hkv, dqk, dv, dt,
         float(scale) if scale else 0.0, 1 if causal else 0, int(window) if window else 0,
-        out.data_ptr(), lse.data_ptr(), ws_p, ws_n, _stream(stream, q), int(flags))
+        out.data_ptr(), lse.data_ptr(), ws_p, ws_n, _stream(stream, q), flags)
     if st != VLF_OK:
         _check(st, "vlf_attn_varlen_fwd_prefix")
     return out, lse
@@ -723,33 +769,52 @@ def vlf_attn_key_weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, m
     the heads of its group of exp(logit - lse), plus ``prev`` (fp32 [Hkv, Tkv], or None).  ``lse``
     [Hq, Tq] comes from the forward with the same scale, causal and window.  ``weights`` (the
     output) may be ``prev``."""
-    _fwd_checks(q, k, k, cu_seqlens_q, cu_seqlens_kv)
-    _req(lse, "lse", torch.float32)
+    dtype, dev = q.dtype, q.get_device()
+    i32, f32 = torch.int32, torch.float32
+    if not (dtype in _DTYPE and dev >= 0 and q.is_contiguous() and _dense(k, dtype, dev) and _dense(lse, f32, dev)
+            and _dense(cu_seqlens_q, i32, dev) and _dense(cu_seqlens_kv, i32, dev) and q.dim() == 3
+            and k.dim() == 3):
+        _fwd_checks(q, k, k, cu_seqlens_q, cu_seqlens_kv)
+        _req(lse, "lse", f32)
+        _same_device(q, k=k, lse=lse, cu_seqlens_q=cu_seqlens_q, cu_seqlens_kv=cu_seqlens_kv)
     tq, hq, d = q.shape
     tk, hkv, _ = k.shape
     if k.shape[2] != d or lse.shape != (hq, tq):
         raise VlfError(VLF_ERR_INVALID, "k must be [Tkv, Hkv, D] and lse [Hq, Tq]")
-    if cu_seqlens_q.numel() != cu_seqlens_kv.numel() or cu_seqlens_q.numel() < 1:
+    nseq = cu_seqlens_q.numel() - 1
+    if nseq != cu_seqlens_kv.numel() - 1 or nseq < 0:
         raise VlfError(VLF_ERR_INVALID, "cu_seqlens_q and cu_seqlens_kv must have num_seqs + 1 entries")
     if max_seqlen_kv is None:
         max_seqlen_kv = _max_len(cu_seqlens_kv)
+    prev_p = None
     if prev is not None:
-        _given(prev, "prev", (hkv, tk), torch.float32)
+        _given(prev, "prev", (hkv, tk), f32)
+        if prev.get_device() != dev:
+            _same_device(q, prev=prev)
+        prev_p = prev.data_ptr()
+    fresh = []
     if weights is None:
-        weights = _new((hkv, tk), torch.float32, q, stream)
+        weights = q.new_empty((hkv, tk), dtype=f32)
+        fresh.append(weights)
     else:
-        _given(weights, "weights", (hkv, tk), torch.float32)
-    _same_device(q, k=k, lse=lse, cu_seqlens_q=cu_seqlens_q, cu_seqlens_kv=cu_seqlens_kv, prev=prev,
-                 weights=weights, workspace=workspace)
-    nseq, mq, mk, dt = cu_seqlens_q.numel() - 1, int(max_seqlen_q), int(max_seqlen_kv), _DTYPE[q.dtype]
+        _given(weights, "weights", (hkv, tk), f32), _same_device(q, weights=weights)
+    mq, mk, dt, flags = int(max_seqlen_q), int(max_seqlen_kv), _DTYPE[dtype], int(flags)
     need = _workspace_size(_lib.vlf_attn_key_weights_workspace_size,
-                           (nseq, tk, mq, mk, hq, hkv, d, dt, int(flags), q.get_device()))
-    ws_p, ws_n, workspace = _workspace(need, workspace, q, stream)
+                           ("weights", nseq, tk, mq, mk, hq, hkv, d, dt, flags, dev))
+    ws_p, ws_n = None, 0
+    if workspace is not None:
+        _req(workspace, "workspace"), _same_device(q, workspace=workspace)
+        ws_p, ws_n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif need:
+        workspace = q.new_empty(need, dtype=torch.uint8)
+        fresh.append(workspace)
+        ws_p, ws_n = workspace.data_ptr(), need
+    if stream is not None:
+        _used_on(stream, *fresh)
     st = _lib.vlf_attn_key_weights(
         q.data_ptr(), k.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_kv.data_ptr(),
         nseq, tq, tk, mq, mk, hq, hkv, d, dt, float(scale) if scale else 0.0, 1 if causal else 0,
-        int(window) if window else 0, _ptr(prev), weights.data_ptr(), ws_p, ws_n, _stream(stream, q),
-        int(flags))
+        int(window) if window else 0, prev_p, weights.data_ptr(), ws_p, ws_n, _stream(stream, q), flags)
     if st != VLF_OK:
         _check(st, "vlf_attn_key_weights")
     return weights
@@ -764,15 +829,18 @@ def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_
     index int32 [Hkv, total_out] (the sequence-local key each row came from) and cu int32 [n + 1].
     ``total_out``: rows of the outputs, the sum of min(length, budget) where the caller knows the
     lengths (None: min(Tkv, n * budget), whose last rows may stay unwritten)."""
-    _req(k, "k"), _req(v, "v", k.dtype), _req(weights, "weights", torch.float32)
-    _req(cu_seqlens_kv, "cu_seqlens_kv", torch.int32)
-    if k.dtype not in _DTYPE:
-        raise VlfError(VLF_ERR_INVALID, f"unsupported dtype {k.dtype}")
+    dtype, dev = k.dtype, k.get_device()
+    if not (dtype in _DTYPE and dev >= 0 and k.is_contiguous() and _dense(v, dtype, dev)
+            and _dense(weights, torch.float32, dev) and _dense(cu_seqlens_kv, torch.int32, dev)):
+        _req(k, "k"), _req(v, "v", dtype), _req(weights, "weights", torch.float32)
+        _req(cu_seqlens_kv, "cu_seqlens_kv", torch.int32)
+        _same_device(k, v=v, weights=weights, cu_seqlens_kv=cu_seqlens_kv)
+        raise VlfError(VLF_ERR_INVALID, f"unsupported dtype {dtype}")
     if k.dim() != 3 or v.dim() != 3 or k.shape[:2] != v.shape[:2] or cu_seqlens_kv.numel() < 1:
         raise VlfError(VLF_ERR_INVALID, "k, v must be [tokens, heads, head_dim]")
     tk, h, dk = k.shape
     dv = v.shape[2]
-    if tuple(weights.shape) != (h, tk):
+    if weights.shape != (h, tk):
         raise VlfError(VLF_ERR_INVALID, "weights must be [H_kv, total_kv]")
     if max_seqlen_kv is None:
         max_seqlen_kv = _max_len(cu_seqlens_kv)
@@ -780,22 +848,31 @@ def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_
     if total_out is None:
         total_out = min(tk, n * max(0, budget))
     total_out = int(total_out)
-    outs = []
-    for t, name, shape, dtype in ((k_out, "k_out", (total_out, h, dk), k.dtype),
-                                  (v_out, "v_out", (total_out, h, dv), k.dtype),
-                                  (weights_out, "weights_out", (h, total_out), torch.float32),
-                                  (index_out, "index_out", (h, total_out), torch.int32),
-                                  (cu_out, "cu_out", (n + 1,), torch.int32)):
-        outs.append(_new(shape, dtype, k, stream) if t is None else _given(t, name, shape, dtype))
-    _same_device(k, v=v, weights=weights, cu_seqlens_kv=cu_seqlens_kv, k_out=outs[0], v_out=outs[1],
-                 weights_out=outs[2], index_out=outs[3], cu_out=outs[4])
+    fresh = []
+
+    def output(t, name, like, shape, dt):
+        if t is None:
+            t = like.new_empty(shape)
+            fresh.append(t)
+        else:
+            _given(t, name, shape, dt), _same_device(k, **{name: t})
+        return t
+
+    k_out = output(k_out, "k_out", k, (total_out, h, dk), dtype)
+    v_out = output(v_out, "v_out", v, (total_out, h, dv), dtype)
+    weights_out = output(weights_out, "weights_out", weights, (h, total_out), torch.float32)
+    index_out = output(index_out, "index_out", cu_seqlens_kv, (h, total_out), torch.int32)
+    cu_out = output(cu_out, "cu_out", cu_seqlens_kv, (n + 1,), torch.int32)
+    if stream is not None:
+        _used_on(stream, *fresh)
     st = _lib.vlf_cache_evict(
         k.data_ptr(), v.data_ptr(), weights.data_ptr(), cu_seqlens_kv.data_ptr(), n, tk,
-        int(max_seqlen_kv), h, dk, dv, _DTYPE[k.dtype], budget, int(sink), int(recent), total_out,
-        *[t.data_ptr() for t in outs], _stream(stream, k))
+        int(max_seqlen_kv), h, dk, dv, _DTYPE[dtype], budget, int(sink), int(recent), total_out,
+        k_out.data_ptr(), v_out.data_ptr(), weights_out.data_ptr(), index_out.data_ptr(),
+        cu_out.data_ptr(), _stream(stream, k))
     if st != VLF_OK:
         _check(st, "vlf_cache_evict")
-    return tuple(outs)
+    return k_out, v_out, weights_out, index_out, cu_out
 
 
 __all__ = ["vlf_attn_varlen_fwd", "vlf_attn_varlen_bwd", "vlf_attn_varlen_bwd_workspace_size",

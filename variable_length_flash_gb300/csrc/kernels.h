@@ -51,7 +51,7 @@ struct RopeParams {
   int first[4];              // first pair of each axis (half for the axes that are not there)
   int total, h_q, h_k, d, rot, dtype, interleaved, inverse;
   int copy_tail;  // the columns behind rot have to be copied (not in place)
-  int hpt, phases;  // set by the launcher: heads per thread, threads along the heads
+  int hpt;        // set by the launcher: heads per thread
 };
 cudaError_t rope(const RopeParams &p, cudaStream_t st);
 

@@ -13,121 +13,156 @@
 // position * F mod 2^64 IS the fraction of a turn, with an error of |position| inv_freq 2^-55
 // turns; its top 32 bits, a number in [-1/2, 1/2), go to sincospi.
 //
-// Bound: HBM, every element read once and written once.  A thread owns one chunk of pairs (two
-// 16-byte loads: V pairs) of one token, computes its V sines and cosines once and applies them to
-// `hpt` consecutive heads of q and k, so that the trigonometry and the 64-bit products are a small
-// share of the instructions.
+// Bound: HBM, every element read once and written once.  A thread owns V pairs of one token (two
+// 16-byte chunks, neighbouring threads on neighbouring chunks), computes their sines and cosines
+// once and applies them to `hpt` consecutive heads.  The fp64 products, which this chip is slow at,
+// run once per pair and block (a table in shared memory; per thread they took 94 us where this
+// takes TIME_VIDEO), and a block walks several runs of tokens.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 
 namespace vlf {
 namespace {
 
-template <typename T> struct alignas(16) Vec16 { T e[16 / sizeof(T)]; };
-
-// V elements at p as fp32 (V = 16 / sizeof(T): one 16-byte access; V = 1: one element).
-template <typename T, int V>
-__device__ __forceinline__ void load_v(const T *p, float (&x)[V]) {
-  if constexpr (V == 1) {
-    x[0] = to_f32<T>(*p);
-  } else {
-    const Vec16<T> v = *reinterpret_cast<const Vec16<T> *>(p);
+// V elements in one access (16 bytes; V = 1: one element).
+template <typename T, int V> struct Chunk {
+  uint4 r;
+  __device__ __forceinline__ void get(float (&x)[V]) const {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int e = 0; e < V; ++e) x[e] = to_f32<T>(v.e[e]);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        x[i] = __uint_as_float(w[i]);
+      } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    }
   }
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_v(T *p, const float (&x)[V]) {
-  if constexpr (V == 1) {
-    *p = from_f32<T>(x[0]);
-  } else {
-    Vec16<T> v;
+  __device__ __forceinline__ void set(const float (&x)[V]) {
+    uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < V; ++e) v.e[e] = from_f32<T>(x[e]);
-    *reinterpret_cast<Vec16<T> *>(p) = v;
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        w[i] = __float_as_uint(x[i]);
+      } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+      } else {
+        const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+      }
+    }
+    r = make_uint4(w[0], w[1], w[2], w[3]);
   }
-}
+};
+template <typename T> struct Chunk<T, 1> {
+  T r;
+  __device__ __forceinline__ void get(float (&x)[1]) const { x[0] = to_f32<T>(r); }
+  __device__ __forceinline__ void set(const float (&x)[1]) { r = from_f32<T>(x[0]); }
+};
 
-// cos and sin of position * f radians (see the head of this file).
-__device__ __forceinline__ void turn(int pos, float f, float &c, float &s) {
+// frac(f / 2 pi) in units of 2^-64.
+__device__ __forceinline__ unsigned long long turns_of(float f) {
   double t = (double)f * 0.15915494309189533577;  // 1 / (2 pi)
   t -= floor(t);
-  const unsigned long long F = (unsigned long long)(t * 18446744073709551616.0);
+  return (unsigned long long)(t * 18446744073709551616.0);
+}
+// cos and sin of pos * F turns.
+__device__ __forceinline__ void turn(int pos, unsigned long long F, float &c, float &s) {
   const long long ph = (long long)((unsigned long long)(long long)pos * F);
   // rounded to 32 bits (a half turn wraps to minus a half turn: the same angle)
   const int p32 = (int)((unsigned long long)(ph + 0x80000000ll) >> 32);
   sincospif((float)p32 * 4.6566128730773926e-10f, &s, &c);  // 2^-31: in half turns
 }
 
-// One thread: chunk u of token `tok`, heads [h0, h0 + hpt).  Chunks u < half / V hold V pairs;
-// the ones behind them 2 V columns that pass through.
+// Grid y: a run of hpt heads of q or k; x: runs of 256 / units tokens, walked with the grid's stride.
+// Thread: chunk u of a token.  Chunks u < nrot hold V pairs -- columns V u and rot / 2 + V u, whose
+// partners they are, or (INTER, V > 1) the V / 2 pairs of neighbours in each --, the ones behind
+// them two chunks of columns that pass through.
 template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
+  __shared__ unsigned long long F[128];
   const int half = p.rot / 2, nrot = half / V;
-  const int units = nrot + (p.copy_tail ? (p.d - p.rot + 2 * V - 1) / (2 * V) : 0);
-  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int u = (int)(id % units);
-  const long long rest = id / units;
-  const int tok = (int)(rest / p.phases), h0 = (int)(rest % p.phases) * p.hpt;
-  if (tok >= p.total) return;
-  const int h1 = min(h0 + p.hpt, p.h_q + p.h_k);
-  auto in_at = [&](int h) {
-    return h < p.h_q ? static_cast<const T *>(p.q) + (long long)tok * p.q_stride + (long long)h * p.d
-                     : static_cast<const T *>(p.k) + (long long)tok * p.k_stride + (long long)(h - p.h_q) * p.d;
-  };
-  auto out_at = [&](int h) {
-    return h < p.h_q ? static_cast<T *>(p.q_out) + (long long)tok * p.q_out_stride + (long long)h * p.d
-                     : static_cast<T *>(p.k_out) + (long long)tok * p.k_out_stride + (long long)(h - p.h_q) * p.d;
-  };
-  if (u >= nrot) {  // columns that pass through (copied as they are)
-    const int c0 = p.rot + (u - nrot) * 2 * V;
-    for (int h = h0; h < h1; ++h) {
-      const T *src = in_at(h);
-      T *dst = out_at(h);
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const int c = c0 + w * V;
-        if (c >= p.d) continue;
-        if constexpr (V == 1) dst[c] = src[c];
-        else *reinterpret_cast<Vec16<T> *>(dst + c) = *reinterpret_cast<const Vec16<T> *>(src + c);
-      }
-    }
-    return;
+  for (int c = threadIdx.x; c < half; c += 256) F[c] = turns_of(__ldg(p.inv_freq + c));
+  __syncthreads();
+  const int tail = p.copy_tail ? (p.d - p.rot + V - 1) / V : 0, ntail = (tail + 1) / 2;
+  const int units = nrot + ntail, run = 256 / units;
+  const int u = threadIdx.x % units, g = threadIdx.x / units;
+  if (g >= run) return;
+  const int phases_q = (p.h_q + p.hpt - 1) / p.hpt, ph = blockIdx.y;
+  const bool is_k = ph >= phases_q;
+  const int h0 = (is_k ? ph - phases_q : ph) * p.hpt, h1 = min(h0 + p.hpt, is_k ? p.h_k : p.h_q);
+  const bool rot = u < nrot;
+  int ca, cb;  // first columns of the thread's two chunks
+  if (rot) {
+    ca = INTER && V == 1 ? 2 * u : V * u;
+    cb = INTER && V == 1 ? ca + 1 : half + V * u;
+  } else {
+    ca = p.rot + V * (u - nrot);
+    cb = ca + V * ntail;
   }
-  float cs[V], sn[V];
+  const bool two = cb < p.d;  // (a tail of an odd number of chunks: its last unit has one)
+  if (!two) cb = ca;
+  int pair[V], axis[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const int c = u * V + e;
+    int c = V * u + e;
+    if (INTER && V > 1) c = e < V / 2 ? V / 2 * u + e : half / 2 + V / 2 * (u - 1) + e;
+    pair[e] = rot ? c : 0;
     int a = 0;
 #pragma unroll
-    for (int x = 1; x < 4; ++x) a += c >= p.first[x] ? 1 : 0;  // (first[x] = half for unused axes)
-    turn(__ldg(p.positions + (long long)a * p.total + tok), __ldg(p.inv_freq + c), cs[e], sn[e]);
-    if (p.inverse) sn[e] = -sn[e];
+    for (int x = 1; x < 4; ++x) a += pair[e] >= p.first[x] && p.first[x] < half ? 1 : 0;
+    axis[e] = a;
   }
-  const int ca = INTER ? 2 * V * u : V * u, cb = INTER ? ca + V : half + V * u;
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const T *src = in_at(h);
-    T *dst = out_at(h);
-    float a[V], b[V], ya[V], yb[V];
-    load_v<T, V>(src + ca, a);
-    load_v<T, V>(src + cb, b);
+  const long long si = is_k ? p.k_stride : p.q_stride, so = is_k ? p.k_out_stride : p.q_out_stride;
+  const T *in = static_cast<const T *>(is_k ? p.k : p.q);
+  T *out = static_cast<T *>(is_k ? p.k_out : p.q_out);
+  using C = Chunk<T, V>;
+  for (long long tok = (long long)blockIdx.x * run + g; tok < p.total; tok += (long long)gridDim.x * run) {
+    float cs[V], sn[V];
+    if (rot) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      if constexpr (INTER && V > 1) {
-        // neighbours: pair e is (2e, 2e + 1) of the chunk's 2 V columns, in a then b
-        float *y = e < V / 2 ? &ya[2 * e] : &yb[2 * e - V];
-        const float x0 = e < V / 2 ? a[(2 * e) % V] : b[(2 * e) % V];
-        const float x1 = e < V / 2 ? a[(2 * e + 1) % V] : b[(2 * e + 1) % V];
-        y[0] = fmaf(x0, cs[e], -(x1 * sn[e]));
-        y[1] = fmaf(x1, cs[e], x0 * sn[e]);
-      } else {
-        ya[e] = fmaf(a[e], cs[e], -(b[e] * sn[e]));
-        yb[e] = fmaf(b[e], cs[e], a[e] * sn[e]);
+      for (int e = 0; e < V; ++e) {
+        turn(__ldg(p.positions + (long long)axis[e] * p.total + tok), F[pair[e]], cs[e], sn[e]);
+        if (p.inverse) sn[e] = -sn[e];
       }
     }
-    store_v<T, V>(dst + ca, ya);
-    store_v<T, V>(dst + cb, yb);
+    const T *src = in + tok * si + (long long)h0 * p.d;
+    T *dst = out + tok * so + (long long)h0 * p.d;
+#pragma unroll 4
+    for (int h = h0; h < h1; ++h, src += p.d, dst += p.d) {
+      C x = *reinterpret_cast<const C *>(src + ca), y = *reinterpret_cast<const C *>(src + cb);
+      if (rot) {
+        float a[V], b[V], ya[V], yb[V];
+        x.get(a);
+        y.get(b);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          if constexpr (INTER && V > 1) {
+            // pair e < V / 2: columns 2 e, 2 e + 1 of chunk a; the others of chunk b
+            float *o = e < V / 2 ? ya : yb;
+            const float *i = e < V / 2 ? a : b;
+            const int c = 2 * (e % (V / 2));
+            o[c] = fmaf(i[c], cs[e], -(i[c + 1] * sn[e]));
+            o[c + 1] = fmaf(i[c + 1], cs[e], i[c] * sn[e]);
+          } else {
+            ya[e] = fmaf(a[e], cs[e], -(b[e] * sn[e]));
+            yb[e] = fmaf(b[e], cs[e], a[e] * sn[e]);
+          }
+        }
+        x.set(ya);
+        y.set(yb);
+      }
+      *reinterpret_cast<C *>(dst + ca) = x;
+      if (two) *reinterpret_cast<C *>(dst + cb) = y;
+    }
   }
 }
 
@@ -139,17 +174,18 @@ cudaError_t launch(RopeParams p, cudaStream_t st) {
   const bool vec = whole(p.rot / 2) && whole(p.d) && whole(p.q_stride) && whole(p.q_out_stride) &&
                    (p.h_k == 0 || (whole(p.k_stride) && whole(p.k_out_stride)));
   const int v = vec ? VW : 1;
-  const long long units = p.rot / 2 / v + (p.copy_tail ? (p.d - p.rot + 2 * v - 1) / (2 * v) : 0);
+  const int units = p.rot / 2 / v + (p.copy_tail ? ((p.d - p.rot + v - 1) / v + 1) / 2 : 0);
   if (units == 0) return cudaSuccess;  // nothing turns, and the rest is already in place
-  // Heads per thread: 8 once that leaves enough threads to fill the GPU (152 SMs x 1024), fewer
-  // for a decode step's few tokens, where the heads are the parallelism.
-  const int heads = p.h_q + p.h_k;
-  p.hpt = 8;
-  while (p.hpt > 1 && units * p.total * ((heads + p.hpt - 1) / p.hpt) < 152ll * 1024) p.hpt /= 2;
-  p.phases = (heads + p.hpt - 1) / p.hpt;
-  const long long blocks = (units * p.total * p.phases + 255) / 256;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)blocks);
+  // Heads per thread: 16 (the trigonometry is then a small share) where that still gives every SM
+  // four blocks, fewer for a decode step's few tokens, where the heads are the parallelism.
+  const long long runs = ((long long)p.total + 256 / units - 1) / (256 / units);
+  auto phases = [&](int hpt) { return (p.h_q + hpt - 1) / hpt + (p.h_k + hpt - 1) / hpt; };
+  p.hpt = 16;
+  while (p.hpt > 1 && runs * phases(p.hpt) < 152 * 4) p.hpt /= 2;
+  while (phases(p.hpt) > 65535) p.hpt *= 2;
+  // up to eight blocks per SM, each with the same number of runs
+  const long long y = phases(p.hpt), turns = (runs * y + 152 * 8 - 1) / (152 * 8);
+  const dim3 grid((unsigned)((runs + turns - 1) / turns), (unsigned)y);
   if (vec) {
     if (p.interleaved) rope_kernel<T, VW, true><<<grid, 256, 0, st>>>(p);
     else rope_kernel<T, VW, false><<<grid, 256, 0, st>>>(p);
