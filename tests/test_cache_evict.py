@@ -63,6 +63,7 @@ CASES = [
     ([20000, 9000], 1, 64, 64, BF, 3001, 4, 64),
     ([40000], 2, 64, 64, HF, 12345, 16, 512),
     ([140001, 70000], 1, 64, 64, HF, 20001, 16, 512),
+    ([420001], 1, 8, 16, HF, 5000, 4, 64),               # more keys than shared memory holds
 ]
 
 

@@ -650,7 +650,7 @@ def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, invers
         sec = _sections(sections)
     fresh_q, fresh_k = q_out is None, k_out is None
     if fresh_q:
-        q_out = q.new_empty((total, hq, d))
+        q_out = torch.empty((total, hq, d), dtype=dtype, device=q.device)
         sqo = hq * d
     else:
         sqo = _rope_rows(q_out, "q_out", dtype, total)
@@ -659,7 +659,7 @@ def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, invers
         _same_device(q, q_out=q_out)
     if k is not None:
         if fresh_k:
-            k_out = k.new_empty((total, hk, d))
+            k_out = torch.empty((total, hk, d), dtype=dtype, device=q.device)
             sko = hk * d
         else:
             sko = _rope_rows(k_out, "k_out", dtype, total)
@@ -723,12 +723,12 @@ def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seq
         max_seqlen_kv = _max_len(cu_seqlens_kv)
     fresh = []
     if out is None:
-        out = q.new_empty((tq, hq, dv))
+        out = torch.empty((tq, hq, dv), dtype=dtype, device=q.device)
         fresh.append(out)
     else:
         _given(out, "out", (tq, hq, dv), dtype), _same_device(q, out=out)
     if lse is None:
-        lse = q.new_empty((hq, tq), dtype=torch.float32)
+        lse = torch.empty((hq, tq), dtype=torch.float32, device=q.device)
         fresh.append(lse)
     else:
         _given(lse, "lse", (hq, tq), torch.float32), _same_device(q, lse=lse)
@@ -740,7 +740,7 @@ def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seq
         _req(workspace, "workspace"), _same_device(q, workspace=workspace)
         ws_p, ws_n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif need:
-        workspace = q.new_empty(need, dtype=torch.uint8)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         fresh.append(workspace)
         ws_p, ws_n = workspace.data_ptr(), need
     if stream is not None:
@@ -794,7 +794,7 @@ def vlf_attn_key_weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, m
         prev_p = prev.data_ptr()
     fresh = []
     if weights is None:
-        weights = q.new_empty((hkv, tk), dtype=f32)
+        weights = torch.empty((hkv, tk), dtype=f32, device=q.device)
         fresh.append(weights)
     else:
         _given(weights, "weights", (hkv, tk), f32), _same_device(q, weights=weights)
@@ -806,7 +806,7 @@ def vlf_attn_key_weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, m
         _req(workspace, "workspace"), _same_device(q, workspace=workspace)
         ws_p, ws_n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif need:
-        workspace = q.new_empty(need, dtype=torch.uint8)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         fresh.append(workspace)
         ws_p, ws_n = workspace.data_ptr(), need
     if stream is not None:
@@ -848,21 +848,21 @@ def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_
     if total_out is None:
         total_out = min(tk, n * max(0, budget))
     total_out = int(total_out)
-    fresh = []
+    fresh, device = [], k.device
 
-    def output(t, name, like, shape, dt):
+    def output(t, name, shape, dt):
         if t is None:
-            t = like.new_empty(shape)
+            t = torch.empty(shape, dtype=dt, device=device)
             fresh.append(t)
         else:
             _given(t, name, shape, dt), _same_device(k, **{name: t})
         return t
 
-    k_out = output(k_out, "k_out", k, (total_out, h, dk), dtype)
-    v_out = output(v_out, "v_out", v, (total_out, h, dv), dtype)
-    weights_out = output(weights_out, "weights_out", weights, (h, total_out), torch.float32)
-    index_out = output(index_out, "index_out", cu_seqlens_kv, (h, total_out), torch.int32)
-    cu_out = output(cu_out, "cu_out", cu_seqlens_kv, (n + 1,), torch.int32)
+    k_out = output(k_out, "k_out", (total_out, h, dk), dtype)
+    v_out = output(v_out, "v_out", (total_out, h, dv), dtype)
+    weights_out = output(weights_out, "weights_out", (h, total_out), torch.float32)
+    index_out = output(index_out, "index_out", (h, total_out), torch.int32)
+    cu_out = output(cu_out, "cu_out", (n + 1,), torch.int32)
     if stream is not None:
         _used_on(stream, *fresh)
     st = _lib.vlf_cache_evict(

@@ -7,11 +7,11 @@
 // keep their order.  Each kv head has a choice of its own, all heads of a sequence the same n.
 //
 // Two kernels.  The selection finds the budget-th largest weight of a (sequence, kv head) by radix:
-// weights as order-preserving 32-bit keys (the protected ones above all), a histogram of the leading
-// digit of those that still match, the digit in which the n-th falls, on to the next digit; then one
-// ordered pass writes the indices that stay.  A cluster of up to eight CTAs shares a long sequence:
+// weights as order-preserving 32-bit keys (the protected ones above all), the counts of the leading
+// digit among those that still match, the digit in which the n-th falls, on to the next digit; then
+// one ordered pass writes the indices that stay.  A cluster of up to eight CTAs shares a long sequence:
 // each keeps its share of the keys in shared memory (one read of the weights from HBM) and the
-// histograms are summed through distributed shared memory.  The gather copies the kept rows of K
+// counts are summed through distributed shared memory.  The gather copies the kept rows of K
 // and V and is the bulk of the work: bound by HBM, every kept row read once and written once.
 #include <cooperative_groups.h>
 
@@ -29,9 +29,10 @@ template <> struct Piece<16> { using type = uint4; };
 template <> struct Piece<4> { using type = uint32_t; };
 template <> struct Piece<2> { using type = uint16_t; };
 
-constexpr int kBins = 2048;          // 11-bit digits: 11 + 11 + 10 bits
+constexpr int kBins = 1024;
 constexpr int kMaxCluster = 8;
-constexpr int kKeysHeld = 49152;     // keys a CTA keeps in shared memory (192 KB); more are read again
+constexpr int kKeysHeld = 49152;     // keys a CTA keeps in shared memory (192 KB) at most
+constexpr int kBatch = 8;            // keys of a thread in flight
 constexpr uint32_t kAlways = 0xffffffffu;  // the key of a protected one (+inf's is 0xff800000)
 
 // fp32 -> unsigned with the same order; -0 and +0 are equal, NaN is below everything.
@@ -72,12 +73,16 @@ __device__ __forceinline__ int block_scan(int x, int *sums, int &total) {
   return __shfl_sync(0xffffffffu, winc - mine, warp) + inc - x;
 }
 
-// Grid x: sequence * cluster + rank, y: kv head.  Blocks of 256 or 512 threads.
-__global__ void __launch_bounds__(512) evict_select_kernel(const EvictParams p, int cluster, int held) {
+// Grid x: sequence * cluster + rank, y: kv head.  Blocks of 256 or 512 threads.  HELD: the CTA's keys
+// fit its shared memory (rounded up to whole batches, the rest filled with the lowest key, which no
+// count below sees); otherwise each pass reads the weights again.
+template <bool HELD>
+__global__ void __launch_bounds__(512) evict_select_kernel(const EvictParams p, int cluster) {
   namespace cg = cooperative_groups;
-  extern __shared__ uint32_t key_s[];  // [held]
-  __shared__ int hist[kBins];
+  extern __shared__ uint32_t key_s[];
+  __shared__ __align__(16) int hist[kBins];
   __shared__ int sums[33], found[2], counts[2];
+  __shared__ int4 warp_c[2][16], cta_c[2 * kMaxCluster];
   tc::pdl_trigger();
   tc::pdl_wait();
   const int s = blockIdx.x / cluster, rank = blockIdx.x % cluster, h = blockIdx.y, t = threadIdx.x, nt = blockDim.x;
@@ -110,73 +115,114 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const EvictParams p, 
   const int per = (len + cluster - 1) / cluster, c0 = min(len, rank * per), cn = min(per, len - c0);
   const float *w = p.weights + (size_t)h * p.total_kv + k0 + c0;
   int *index = p.index + (size_t)h * p.total_out + out0;
-  float *w_out = p.weights_out + (size_t)h * p.total_out + out0;
   if (len <= p.budget) {
-    for (int j = t; j < cn; j += nt) {
-      index[c0 + j] = c0 + j;
-      w_out[c0 + j] = w[j];
-    }
+    for (int j = t; j < cn; j += nt) index[c0 + j] = c0 + j;
     return;
   }
   const int last = len - p.recent;
+  // key j of this CTA's share from the weights (0 behind its end)
   auto make_key = [&](int j) {
+    const float x = __ldg(w + min(j, cn - 1));
     const int i = c0 + j;
-    return i < p.sink || i >= last ? kAlways : order_key(__ldg(w + j));
+    return j >= cn ? 0u : i < p.sink || i >= last ? kAlways : order_key(x);
   };
-  auto key_at = [&](int j) { return j < held ? key_s[j] : make_key(j); };
-  // Counts the digits of the keys that match the prefix found so far.  Where many lanes of a warp
-  // meet in one bin (weights of exactly nothing, protected keys) the first lane's bin is added once.
-  auto count = [&](uint32_t key, bool in, int shift, int bins) {
-    const unsigned act = __ballot_sync(0xffffffffu, in);
-    if (!act) return;
-    const int bin = (key >> shift) & (bins - 1);
-    const int lead = __ffs(act) - 1, lead_bin = __shfl_sync(0xffffffffu, bin, lead);
-    const unsigned same = __ballot_sync(0xffffffffu, in && bin == lead_bin);
-    if (lane == lead) atomicAdd(&hist[bin], __popc(same));
-    else if (in && bin != lead_bin) atomicAdd(&hist[bin], 1);
-  };
-  uint32_t prefix = 0, mask = 0;
-  int left = n;  // how many of the matching keys stay
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+  auto key_at = [&](int j) { return HELD ? key_s[j] : make_key(j); };
+  const int padded = cn > 0 ? (cn + kBatch * nt - 1) / (kBatch * nt) * (kBatch * nt) : 0;
+  if (HELD) {  // (a thread reads back its own keys until the ordered pass)
+    for (int j0 = t; j0 < padded; j0 += kBatch * nt) {
+      uint32_t k8[kBatch];
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) k8[x] = make_key(j0 + x * nt);
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) key_s[j0 + x * nt] = k8[x];
+    }
+  }
+  uint32_t prefix = 0, mask = 0;  // the leading bits of the n-th largest key, found so far
+  int left = n;                   // how many of the keys with these bits stay
+  // Twelve bits, two at a time, by counting in registers: sign, exponent and three bits of mantissa
+  // leave a few percent of the keys (with histograms in shared memory from the first bit on, the
+  // atomics of all keys took 40 of 46 us at 512 lists of 4096-8192).
+  for (int step = 0; step < 6; ++step) {
+    const int shift = 30 - 2 * step;
+    int c[4] = {0, 0, 0, 0};  // (keys with digit 0 need no count)
+    for (int j0 = t; j0 < padded; j0 += kBatch * nt) {
+      uint32_t k8[kBatch], acc = 0;  // a byte per digit
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) k8[x] = key_at(j0 + x * nt);
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x)
+        acc += ((k8[x] ^ prefix) & mask) == 0 ? 1u << (8 * ((k8[x] >> shift) & 3u)) : 0u;
+#pragma unroll
+      for (int d = 1; d < 4; ++d) c[d] += (acc >> (8 * d)) & 255u;
+    }
+#pragma unroll
+    for (int d = 1; d < 4; ++d) c[d] = __reduce_add_sync(0xffffffffu, c[d]);
+    // (two sets of slots in turn: one barrier per step)
+    if (lane == 0) warp_c[step & 1][warp] = make_int4(0, c[1], c[2], c[3]);
+    __syncthreads();
+    int4 x = lane < warps ? warp_c[step & 1][lane] : make_int4(0, 0, 0, 0);
+    if (cluster > 1) {
+      c[1] = __reduce_add_sync(0xffffffffu, x.y);
+      c[2] = __reduce_add_sync(0xffffffffu, x.z);
+      c[3] = __reduce_add_sync(0xffffffffu, x.w);
+      if (t < cluster) cg::this_cluster().map_shared_rank(cta_c, t)[(step & 1) * kMaxCluster + rank] = make_int4(0, c[1], c[2], c[3]);
+      cg::this_cluster().sync();
+      x = lane < cluster ? cta_c[(step & 1) * kMaxCluster + lane] : make_int4(0, 0, 0, 0);
+    }
+    const int c3 = __reduce_add_sync(0xffffffffu, x.w), c2 = __reduce_add_sync(0xffffffffu, x.z),
+              c1 = __reduce_add_sync(0xffffffffu, x.y);
+    uint32_t d = 3;
+    if (c3 < left) {
+      left -= c3;
+      d = 2;
+      if (c2 < left) {
+        left -= c2;
+        d = 1;
+        if (c1 < left) { left -= c1; d = 0; }
+      }
+    }
+    prefix |= d << shift;
+    mask |= 3u << shift;
+  }
+  // The other twenty, ten at a time, by histograms of the keys that are left.
+  for (int pass = 0; pass < 2; ++pass) {
+    const int shift = pass == 0 ? 10 : 0;
     for (int i = t; i < kBins; i += nt) hist[i] = 0;
     __syncthreads();
-    const int rounds = (cn + nt - 1) / nt;
-#pragma unroll 4
-    for (int x = 0; x < rounds; ++x) {
-      const int j = x * nt + t;
-      uint32_t key = 0;
-      if (j < cn) {
-        if (pass == 0) {
-          key = make_key(j);
-          if (j < held) key_s[j] = key;
-        } else {
-          key = key_at(j);
-        }
-      }
-      count(key, j < cn && (key & mask) == prefix, shift, bins);
+    // (the lowest key behind the end falls, if anywhere, into bin 0, whose count ends nothing early)
+    for (int j0 = t; j0 < padded; j0 += kBatch * nt) {
+      uint32_t k8[kBatch];
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) k8[x] = key_at(j0 + x * nt);
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x)
+        if (((k8[x] ^ prefix) & mask) == 0) atomicAdd(&hist[(k8[x] >> shift) & (kBins - 1)], 1);
     }
     if (cluster > 1) cg::this_cluster().sync();
     else __syncthreads();
-    // bins from the top, kBins / nt to a thread, summed over the cluster
-    const int own = bins / nt, top = bins - 1 - t * own;  // (own: 2, 4 or 8)
-    int c[8], sum = 0;
+    // the bins from the top, two (512 threads) or four to a thread, summed over the cluster
+    const int own = kBins / nt, top = kBins - 1 - t * own;
+    int c[4] = {0, 0, 0, 0};  // c[i]: bin top - i
+    if (cluster > 1) {  // (512 threads: a wide load per CTA, all in flight)
+      int2 x[kMaxCluster];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      c[i] = 0;
-      if (i >= own) continue;
-      if (cluster > 1) {
-        for (int r = 0; r < cluster; ++r) c[i] += cg::this_cluster().map_shared_rank(hist, r)[top - i];
-      } else {
-        c[i] = hist[top - i];
+      for (int r = 0; r < kMaxCluster; ++r) {
+        x[r] = make_int2(0, 0);
+        if (r < cluster) x[r] = *reinterpret_cast<const int2 *>(cg::this_cluster().map_shared_rank(hist, r) + top - 1);
       }
-      sum += c[i];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) { c[0] += x[r].y; c[1] += x[r].x; }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < own) c[i] = hist[top - i];
     }
+    const int sum = (c[0] + c[1]) + (c[2] + c[3]);
     int total;
     int above = block_scan(sum, sums, total);
     if (above < left && above + sum >= left) {  // (one thread)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         if (i < own && above < left && above + c[i] >= left) {
           found[0] = top - i;
           found[1] = left - above;
@@ -188,7 +234,7 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const EvictParams p, 
     if (cluster > 1) cg::this_cluster().sync();
     else __syncthreads();
     prefix |= (uint32_t)found[0] << shift;
-    mask |= (uint32_t)(bins - 1) << shift;
+    mask |= (uint32_t)(kBins - 1) << shift;
     left = found[1];
   }
   // Keys above `prefix` stay, and the first `left` of those equal to it.  A warp owns a run of the
@@ -196,12 +242,14 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const EvictParams p, 
   const int wper = (cn + warps * 32 - 1) / (warps * 32) * 32;
   const int a = min(cn, warp * wper), b = min(cn, a + wper);
   int gt = 0, eq = 0;
-  for (int j0 = a; j0 < b; j0 += 32) {
-    const int j = j0 + lane;
-    const uint32_t key = j < b ? key_at(j) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, j < b && key > prefix));
-    eq += __popc(__ballot_sync(0xffffffffu, j < b && key == prefix));
+#pragma unroll 8
+  for (int j = a + lane; j < b; j += 32) {
+    const uint32_t key = key_at(j);
+    gt += key > prefix;
+    eq += key == prefix;
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   int all_eq, all_gt;
   int eq_at = block_scan(lane == 0 ? eq : 0, sums, all_eq);  // (lane 0's is its warp's)
   eq_at = __shfl_sync(0xffffffffu, eq_at, 0);
@@ -217,17 +265,15 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const EvictParams p, 
     }
   }
   int at = gt_at + min(eq_at, left);  // this warp's first output
+  const unsigned below = (1u << lane) - 1u;
+#pragma unroll 4
   for (int j0 = a; j0 < b; j0 += 32) {
     const int j = j0 + lane;
     const uint32_t key = j < b ? key_at(j) : 0u;
-    const unsigned below = (1u << lane) - 1u;
     const unsigned eqs = __ballot_sync(0xffffffffu, j < b && key == prefix);
     const bool keep = j < b && (key > prefix || (key == prefix && eq_at + __popc(eqs & below) < left));
     const unsigned kept = __ballot_sync(0xffffffffu, keep);
-    if (keep) {
-      index[at + __popc(kept & below)] = c0 + j;
-      w_out[at + __popc(kept & below)] = __ldg(w + j);
-    }
+    if (keep) index[at + __popc(kept & below)] = c0 + j;
     at += __popc(kept);
     eq_at += __popc(eqs);
   }
@@ -235,12 +281,14 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const EvictParams p, 
   if (cluster > 1) cg::this_cluster().sync();
 }
 
-// Kept rows of K and V.  Grid y = sequence, x = runs of (output row, head) items, heads fastest, so
-// that a run's writes are one stretch.  A group of threads copies an item, a thread one B-byte piece
-// of its K or V row (or every 256th, where a row has more); kUnroll items' loads are in flight.
-constexpr int kUnroll = 8;
+// Kept rows of K, V and the weights.  Grid y = sequence, x = runs of (output row, head) items, heads
+// fastest, so that what a block writes is one stretch.  A group of threads copies an item, a thread
+// one B-byte piece of its K or V row; four items of each group are in flight (two and eight were as
+// fast, one 25% slower; rows moved by bulk copies through shared memory took 248 us where this takes
+// TIME_GATHER, at 64 x 2048 of 4096-8192 keys, 8 heads of 128).
+constexpr int kUnroll = 4;
 template <int B>
-__global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p, int rk, int rv) {
+__global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p, int rk, int rv, int rounds) {
   using P = typename Piece<B>::type;
   tc::pdl_trigger();
   tc::pdl_wait();
@@ -249,39 +297,43 @@ __global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p, 
   if (!evict_seq(p, s, k0, len)) return;
   const int out0 = p.cu_out[s], n = min(len, p.budget);
   if (out0 < 0 || (long long)out0 + n > p.total_out) return;
-  const int pieces = rk + rv, groups = max(1, 256 / pieces), g = threadIdx.x / pieces;
+  // (rows of more than 256 pieces, widths that are no whole 16-byte pieces: the threads go round)
+  const int pieces = rk + rv, groups = max(1, 256 / pieces), g = threadIdx.x / min(pieces, 256);
   if (g >= groups) return;
   const long long items = (long long)n * p.h_kv;
-  const long long i0 = (long long)blockIdx.x * groups * kUnroll + g;
-  if (i0 >= items) return;
-  const int r0 = (int)(i0 / p.h_kv), h0 = (int)(i0 % p.h_kv);  // output row and head of the first item
-  const int dr = groups / p.h_kv, dh = groups % p.h_kv;        // and from one to the next
-  for (int c0 = pieces > 256 ? (int)threadIdx.x : (int)threadIdx.x % pieces; c0 < pieces; c0 += 256) {
+  const int dr = groups / p.h_kv, dh = groups % p.h_kv;  // rows and heads from one item to the next
+  for (int c0 = (int)threadIdx.x % min(pieces, 256); c0 < pieces; c0 += 256) {
     const bool is_v = c0 >= rk;
     const int width = is_v ? rv : rk, c = is_v ? c0 - rk : c0;
-    const P *from = static_cast<const P *>(is_v ? p.v : p.k);
-    P *to = static_cast<P *>(is_v ? p.v_out : p.k_out) + ((size_t)out0 * p.h_kv + i0) * width + c;
-    P x[kUnroll];
-    int src[kUnroll];
-    int r = r0, h = h0;
+    const P *from = static_cast<const P *>(is_v ? p.v : p.k) + (size_t)k0 * p.h_kv * width + c;
+    P *to = static_cast<P *>(is_v ? p.v_out : p.k_out) + (size_t)out0 * p.h_kv * width + c;
+    long long i0 = (long long)blockIdx.x * groups * kUnroll * rounds + g;
+    int r = (int)(i0 / p.h_kv), h = (int)(i0 % p.h_kv);
+    for (int round = 0; round < rounds && i0 < items; ++round, i0 += groups * kUnroll) {
+      P x[kUnroll];
+      int src[kUnroll], hh[kUnroll], rr[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      // (a plain load: the selection wrote the indices while this kernel may already have been here)
-      src[u] = r < n ? p.index[(size_t)h * p.total_out + out0 + r] : -1;
-      r += dr;
-      h += dh;
-      if (h >= p.h_kv) { h -= p.h_kv; ++r; }
+      for (int u = 0; u < kUnroll; ++u) {
+        // (a plain load: the selection wrote the indices while this kernel may already have been here)
+        rr[u] = r;
+        hh[u] = h;
+        src[u] = r < n ? p.index[(size_t)h * p.total_out + out0 + r] : -1;
+        r += dr;
+        h += dh;
+        if (h >= p.h_kv) { h -= p.h_kv; ++r; }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if ((unsigned)src[u] < (unsigned)len) x[u] = __ldg(from + ((size_t)src[u] * p.h_kv + hh[u]) * width);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if ((unsigned)src[u] < (unsigned)len) {
+          to[((size_t)rr[u] * p.h_kv + hh[u]) * width] = x[u];
+          if (c0 == 0)
+            p.weights_out[(size_t)hh[u] * p.total_out + out0 + rr[u]] =
+                __ldg(p.weights + (size_t)hh[u] * p.total_kv + k0 + src[u]);
+        }
     }
-    h = h0;
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (src[u] >= 0 && src[u] < len) x[u] = __ldg(from + ((size_t)(k0 + src[u]) * p.h_kv + h) * width + c);
-      h += dh;
-      if (h >= p.h_kv) h -= p.h_kv;
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (src[u] >= 0 && src[u] < len) to[(size_t)u * groups * width] = x[u];
   }
 }
 
@@ -293,16 +345,19 @@ cudaError_t cache_evict(const EvictParams &p, cudaStream_t st) {
   int cluster = 1;
   while (cluster < kMaxCluster && (long long)cluster * 8192 < p.max_kv) cluster *= 2;
   const int share = (p.max_kv + cluster - 1) / cluster;
-  int threads = share > 1024 ? 512 : 256, held = std::min(share, kKeysHeld);
-  const void *sel = reinterpret_cast<const void *>(evict_select_kernel);
-  cudaError_t e = set_smem_once(sel, held * 4);
+  const int threads = share > 1024 ? 512 : 256, batch = kBatch * threads;
+  const bool held = share <= kKeysHeld;
+  const int smem = held ? (share + batch - 1) / batch * batch * 4 : 0;
+  const void *sel = held ? reinterpret_cast<const void *>(evict_select_kernel<true>)
+                         : reinterpret_cast<const void *>(evict_select_kernel<false>);
+  cudaError_t e = set_smem_once(sel, smem);
   if (e != cudaSuccess) return e;
   EvictParams a = p;
-  void *args[3] = {&a, &cluster, &held};
+  void *args[2] = {&a, &cluster};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.num_seqs * cluster, p.h_kv);
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = (size_t)held * 4;
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -319,12 +374,15 @@ cudaError_t cache_evict(const EvictParams &p, cudaStream_t st) {
   const bool whole = p.d_qk * es % 16 == 0 && p.d_v * es % 16 == 0;
   const int b = whole ? 16 : es;
   int rk = p.d_qk * es / b, rv = p.d_v * es / b;
-  const long long run = std::max(1, 256 / (rk + rv)) * kUnroll, x = (most * p.h_kv + run - 1) / run;
+  // rounds of a block: as many, up to eight, as leave eight blocks per SM
+  const long long run = std::max(1, 256 / (rk + rv)) * kUnroll, runs = (most * p.h_kv + run - 1) / run;
+  int rounds = (int)std::max(1ll, std::min(8ll, runs * p.num_seqs / (152 * 8)));
+  const long long x = (runs + rounds - 1) / rounds;
   if (x > 0x7fffffffll) return cudaErrorInvalidValue;
   const void *gather = b == 16 ? reinterpret_cast<const void *>(evict_gather_kernel<16>)
                      : b == 4 ? reinterpret_cast<const void *>(evict_gather_kernel<4>)
                               : reinterpret_cast<const void *>(evict_gather_kernel<2>);
-  void *gargs[3] = {&a, &rk, &rv};
+  void *gargs[4] = {&a, &rk, &rv, &rounds};
   e = launch_dependent(gather, dim3((unsigned)x, p.num_seqs), 256, 0, st, gargs);
   if (e == cudaSuccess) count_launch();
   return e;

@@ -235,18 +235,22 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
   constexpr int is_bf16 = BF16 ? 1 : 0;
 
   // ---- this CTA's rows and key tiles
-  const bool pre = SPLIT && blockIdx.x < pl.n_pre;  // the shared prefix part
+  // The shared prefix part's CTAs (bound by the tensor cores) and the own keys' (bound by HBM) take
+  // turns, so that an SM holds one of each, while there are both.
+  const unsigned both = 2 * min(pl.n_pre, pl.n_all - pl.n_pre), bid = blockIdx.x;
+  const bool pre = SPLIT && (bid < both ? (bid & 1) == 0 : pl.n_pre > both / 2);
+  const unsigned nth = bid < both ? bid / 2 : bid - both / 2;  // among its kind
   int hd, rb, part, slot;
   Seq sq{0, 0, 0, 0};
   if (pre) {
     // row blocks fastest: CTAs that read the same prefix tiles run together
-    int x = blockIdx.x;
+    int x = (int)nth;
     rb = x % pl.rb_pre;
     x /= pl.rb_pre;
     hd = x % pl.heads;
     part = slot = x / pl.heads;
   } else {
-    int x = blockIdx.x - pl.n_pre;
+    int x = (int)nth;
     part = x % pl.parts_own;
     x /= pl.parts_own;
     rb = x % pl.rb_own;
@@ -265,6 +269,9 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
   const int row0 = pre ? rb * pl.rows : sq.q0 + rb * pl.rows;                 // packed row of tile row 0
   const int nrows = min(pl.rows, (pre ? p.total_q : sq.q0 + sq.q_len) - row0);  // query rows of the tile
   const int keys = P + sq.kv_len, off = keys - sq.q_len;                      // (per-sequence CTAs)
+  // Softmax warps that hold a row.  The others have nothing to do: what they leave in P stands in
+  // rows of O that nobody reads (a decode step's tile is mostly such rows).
+  const int live_warps = (nrows * pl.gb + 31) / 32;
 
   const uint32_t base = smem_u32(smem_raw);
   if (base & 1023u) {
@@ -284,7 +291,7 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
     for (int i = 0; i < C::NV; ++i) { mbar_init(bar(C::B_VF + i), 1); mbar_init(bar(C::B_VE + i), 1); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::B_S + i), 1);
-      mbar_init(bar(C::B_P + i), 128);
+      mbar_init(bar(C::B_P + i), 32 * live_warps);
       mbar_init(bar(C::B_O + i), 1);
       mbar_init(bar(C::B_DRAIN + i), 1);
     }
@@ -436,7 +443,7 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
       mma_commit_w(bar(C::B_DRAIN + 1));
       drain_wait(bar(C::B_DRAIN + 1), 0);
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp - 4 < live_warps) {
     // ------------------------------------------------------------------ softmax / epilogue
     const int r = 32 * (warp & 3) + lane, tok = r / pl.gb;
     const int head = h0 + r % pl.gb, grow = row0 + tok;
@@ -644,15 +651,24 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const Params p, int p
     const float e = s0 + lane < parts ? expf(lse_part[(s0 + lane) * pairs + w] - mm) : 0.f;
     sum += e;
     const int n = min(32, parts - s0);
-#pragma unroll 4
-    for (int s = 0; s < n; s += PER) {
-      const float wgt = __shfl_sync(0xffffffffu, e, (s + sub) & 31);
-      if (s + sub < n && c < NL) {
-        const float4 x = *reinterpret_cast<const float4 *>(o_part + ((s0 + s + sub) * pairs + w) * D + 4 * c);
-        acc.x = fmaf(wgt, x.x, acc.x);
-        acc.y = fmaf(wgt, x.y, acc.y);
-        acc.z = fmaf(wgt, x.z, acc.z);
-        acc.w = fmaf(wgt, x.w, acc.w);
+    // eight parts' loads in flight
+    for (int s = 0; s < n; s += 8 * PER) {
+      float4 x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int y = s + i * PER + sub;
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (y < n && c < NL) x[i] = *reinterpret_cast<const float4 *>(o_part + ((s0 + y) * pairs + w) * D + 4 * c);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int y = s + i * PER + sub;
+        const float wgt = __shfl_sync(0xffffffffu, e, y & 31);
+        if (y >= n) continue;
+        acc.x = fmaf(wgt, x[i].x, acc.x);
+        acc.y = fmaf(wgt, x[i].y, acc.y);
+        acc.z = fmaf(wgt, x[i].z, acc.z);
+        acc.w = fmaf(wgt, x[i].w, acc.w);
       }
     }
   }

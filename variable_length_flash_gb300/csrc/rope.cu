@@ -82,6 +82,8 @@ __device__ __forceinline__ void turn(int pos, unsigned long long F, float &c, fl
   sincospif((float)p32 * 4.6566128730773926e-10f, &s, &c);  // 2^-31: in half turns
 }
 
+constexpr int kHeads = 8;
+
 // Grid y: a run of hpt heads of q or k; x: runs of 256 / units tokens, walked with the grid's stride.
 // Thread: chunk u of a token.  Chunks u < nrot hold V pairs -- columns V u and rot / 2 + V u, whose
 // partners they are, or (INTER, V > 1) the V / 2 pairs of neighbours in each --, the ones behind
@@ -136,32 +138,44 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
     }
     const T *src = in + tok * si + (long long)h0 * p.d;
     T *dst = out + tok * so + (long long)h0 * p.d;
-#pragma unroll 4
-    for (int h = h0; h < h1; ++h, src += p.d, dst += p.d) {
-      C x = *reinterpret_cast<const C *>(src + ca), y = *reinterpret_cast<const C *>(src + cb);
-      if (rot) {
-        float a[V], b[V], ya[V], yb[V];
-        x.get(a);
-        y.get(b);
+    auto apply = [&](C &x, C &y) {
+      float a[V], b[V], ya[V], yb[V];
+      x.get(a);
+      y.get(b);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          if constexpr (INTER && V > 1) {
-            // pair e < V / 2: columns 2 e, 2 e + 1 of chunk a; the others of chunk b
-            float *o = e < V / 2 ? ya : yb;
-            const float *i = e < V / 2 ? a : b;
-            const int c = 2 * (e % (V / 2));
-            o[c] = fmaf(i[c], cs[e], -(i[c + 1] * sn[e]));
-            o[c + 1] = fmaf(i[c + 1], cs[e], i[c] * sn[e]);
-          } else {
-            ya[e] = fmaf(a[e], cs[e], -(b[e] * sn[e]));
-            yb[e] = fmaf(b[e], cs[e], a[e] * sn[e]);
-          }
+      for (int e = 0; e < V; ++e) {
+        if constexpr (INTER && V > 1) {
+          // pair e < V / 2: columns 2 e, 2 e + 1 of chunk a; the others of chunk b
+          float *o = e < V / 2 ? ya : yb;
+          const float *i = e < V / 2 ? a : b;
+          const int c = 2 * (e % (V / 2));
+          o[c] = fmaf(i[c], cs[e], -(i[c + 1] * sn[e]));
+          o[c + 1] = fmaf(i[c + 1], cs[e], i[c] * sn[e]);
+        } else {
+          ya[e] = fmaf(a[e], cs[e], -(b[e] * sn[e]));
+          yb[e] = fmaf(b[e], cs[e], a[e] * sn[e]);
         }
-        x.set(ya);
-        y.set(yb);
       }
-      *reinterpret_cast<C *>(dst + ca) = x;
-      if (two) *reinterpret_cast<C *>(dst + cb) = y;
+      x.set(ya);
+      y.set(yb);
+    };
+    // kHeads heads' loads are in flight before the first store (in place the compiler could not
+    // move a load over a store by itself)
+    for (int h = h0; h < h1; h += kHeads, src += kHeads * p.d, dst += kHeads * p.d) {
+      C x[kHeads], y[kHeads];
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        if (h + i >= h1) continue;
+        x[i] = *reinterpret_cast<const C *>(src + i * p.d + ca);
+        y[i] = *reinterpret_cast<const C *>(src + i * p.d + cb);
+      }
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        if (h + i >= h1) continue;
+        if (rot) apply(x[i], y[i]);
+        *reinterpret_cast<C *>(dst + i * p.d + ca) = x[i];
+        if (two) *reinterpret_cast<C *>(dst + i * p.d + cb) = y[i];
+      }
     }
   }
 }
