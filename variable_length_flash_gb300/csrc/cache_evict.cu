@@ -10,8 +10,8 @@
 // weights as order-preserving 32-bit keys (the protected ones above all), the counts of the leading
 // digit among those that still match, the digit in which the n-th falls, on to the next digit; then
 // one ordered pass writes the indices that stay.  A cluster of up to eight CTAs shares a long sequence:
-// each keeps its share of the keys in shared memory (one read of the weights from HBM) and the
-// counts are summed through distributed shared memory.  The gather copies the kept rows of K
+// each keeps its share of the keys in registers (one read of the weights from HBM) and the counts
+// are summed through distributed shared memory.  The gather copies the kept rows of K
 // and V and is the bulk of the work: bound by HBM, every kept row read once and written once.
 #include <cooperative_groups.h>
 
@@ -31,8 +31,6 @@ template <> struct Piece<2> { using type = uint16_t; };
 
 constexpr int kBins = 1024;
 constexpr int kMaxCluster = 8;
-constexpr int kKeysHeld = 49152;     // keys a CTA keeps in shared memory (192 KB) at most
-constexpr int kBatch = 8;            // keys of a thread in flight
 constexpr uint32_t kAlways = 0xffffffffu;  // the key of a protected one (+inf's is 0xff800000)
 
 // fp32 -> unsigned with the same order; -0 and +0 are equal, NaN is below everything.
@@ -51,38 +49,26 @@ __device__ __forceinline__ bool evict_seq(const EvictParams &p, int s, int &k0, 
          (s < p.num_seqs - 1 || b == p.total_kv);
 }
 
-// Exclusive prefix sum of x over the block's threads, and its total (sums: 33 ints).
-__device__ __forceinline__ int block_scan(int x, int *sums, int &total) {
+// Exclusive prefix sum of x over the block's warps (x: the same in all lanes of a warp), and its total.
+__device__ __forceinline__ int warp_scan(int x, int *sums, int &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  int inc = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
-  }
   __syncthreads();  // (sums may still be read from the call before)
-  if (lane == 31) sums[warp] = inc;
+  if (lane == 0) sums[warp] = x;
   __syncthreads();
-  int mine = lane < warps ? sums[lane] : 0, winc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, winc, o);
-    if (lane >= o) winc += y;
-  }
-  total = __shfl_sync(0xffffffffu, winc, 31);
-  return __shfl_sync(0xffffffffu, winc - mine, warp) + inc - x;
+  const int mine = lane < warps ? sums[lane] : 0;
+  total = __reduce_add_sync(0xffffffffu, mine);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0);
 }
 
-// Grid x: sequence * cluster + rank, y: kv head.  Blocks of 256 or 512 threads.  HELD: the CTA's keys
-// fit its shared memory (rounded up to whole batches, the rest filled with the lowest key, which no
-// count below sees); otherwise each pass reads the weights again.
-template <bool HELD>
-__global__ void __launch_bounds__(512) evict_select_kernel(const EvictParams p, int cluster) {
+// Grid x: sequence * cluster + rank, y: kv head.  A warp owns a run of 32 * K keys in order, lane l
+// the keys l, 32 + l, ... of it, in registers (K = 0: more keys than that, read again on each pass).
+// What is behind the end counts as the lowest key, which no count below sees.
+template <int K>
+__global__ void __launch_bounds__(K == 0 || K >= 16 ? 1024 : 512) evict_select_kernel(const EvictParams p, int cluster) {
   namespace cg = cooperative_groups;
-  extern __shared__ uint32_t key_s[];
   __shared__ __align__(16) int hist[kBins];
-  __shared__ int sums[33], found[2], counts[2];
-  __shared__ int4 warp_c[2][16], cta_c[2 * kMaxCluster];
+  __shared__ int sums[32], found[2], counts[2];
+  __shared__ int4 warp_c[2][32], cta_c[2 * kMaxCluster];
   tc::pdl_trigger();
   tc::pdl_wait();
   const int s = blockIdx.x / cluster, rank = blockIdx.x % cluster, h = blockIdx.y, t = threadIdx.x, nt = blockDim.x;
@@ -100,182 +86,177 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const EvictParams p, 
     refuse();
     return;
   }
-  const int n = min(len, p.budget);
+  const int n = min(len, p.budget), last = len - p.recent;
+  const bool all = len <= p.budget;
+  // this CTA's keys [c0, c0 + cn), this warp's [wa, wa + 32 * ke) of them
+  const int per = (len + cluster - 1) / cluster, c0 = min(len, rank * per), cn = min(per, len - c0);
+  const int ke = K > 0 ? K : (cn + nt - 1) / nt, wa = warp * 32 * ke + lane;
+  const float *w = p.weights + (size_t)h * p.total_kv + k0 + c0;
+  auto make_key = [&](int e) {
+    const int j = wa + 32 * e, i = c0 + j;
+    const float x = __ldg(w + min(j, cn - 1));
+    return j >= cn ? 0u : i < p.sink || i >= last ? kAlways : order_key(x);
+  };
+  uint32_t key[K > 0 ? K : 1];
+  if (K > 0 && !all && cn > 0) {
+#pragma unroll
+    for (int e = 0; e < K; ++e) key[e] = make_key(e);
+  } else {
+#pragma unroll
+    for (int e = 0; e < (K > 0 ? K : 1); ++e) key[e] = 0u;
+  }
+  auto visit = [&](auto &&f) {  // f(key, e) for this lane's keys, in their order
+    if constexpr (K > 0) {
+#pragma unroll
+      for (int e = 0; e < K; ++e) f(key[e], e);
+    } else {
+#pragma unroll 4
+      for (int e = 0; e < ke; ++e) f(make_key(e), e);
+    }
+  };
   // first output row: what the sequences before this one keep (at most total_kv, an int)
   int before = 0, out0;
   for (int i = t; i < s; i += nt) before += min(max(__ldg(p.cu_kv + i + 1) - __ldg(p.cu_kv + i), 0), p.budget);
-  block_scan(before, sums, out0);
+  warp_scan(__reduce_add_sync(0xffffffffu, before), sums, out0);
   if ((long long)out0 + n > p.total_out || out0 < 0) {
     refuse();
     return;
   }
   if (first) p.cu_out[s + 1] = out0 + n;
   if (n == 0) return;
-  // this CTA's keys: [c0, c0 + cn)
-  const int per = (len + cluster - 1) / cluster, c0 = min(len, rank * per), cn = min(per, len - c0);
-  const float *w = p.weights + (size_t)h * p.total_kv + k0 + c0;
   int *index = p.index + (size_t)h * p.total_out + out0;
-  if (len <= p.budget) {
+  if (all) {
     for (int j = t; j < cn; j += nt) index[c0 + j] = c0 + j;
     return;
   }
-  const int last = len - p.recent;
-  // key j of this CTA's share from the weights (0 behind its end)
-  auto make_key = [&](int j) {
-    const float x = __ldg(w + min(j, cn - 1));
-    const int i = c0 + j;
-    return j >= cn ? 0u : i < p.sink || i >= last ? kAlways : order_key(x);
-  };
-  auto key_at = [&](int j) { return HELD ? key_s[j] : make_key(j); };
-  const int padded = cn > 0 ? (cn + kBatch * nt - 1) / (kBatch * nt) * (kBatch * nt) : 0;
-  if (HELD) {  // (a thread reads back its own keys until the ordered pass)
-    for (int j0 = t; j0 < padded; j0 += kBatch * nt) {
-      uint32_t k8[kBatch];
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x) k8[x] = make_key(j0 + x * nt);
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x) key_s[j0 + x * nt] = k8[x];
-    }
-  }
-  uint32_t prefix = 0, mask = 0;  // the leading bits of the n-th largest key, found so far
-  int left = n;                   // how many of the keys with these bits stay
-  // Twelve bits, two at a time, by counting in registers: sign, exponent and three bits of mantissa
-  // leave a few percent of the keys (with histograms in shared memory from the first bit on, the
-  // atomics of all keys took 40 of 46 us at 512 lists of 4096-8192).
-  for (int step = 0; step < 6; ++step) {
-    const int shift = 30 - 2 * step;
-    int c[4] = {0, 0, 0, 0};  // (keys with digit 0 need no count)
-    for (int j0 = t; j0 < padded; j0 += kBatch * nt) {
-      uint32_t k8[kBatch], acc = 0;  // a byte per digit
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x) k8[x] = key_at(j0 + x * nt);
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x)
-        acc += ((k8[x] ^ prefix) & mask) == 0 ? 1u << (8 * ((k8[x] >> shift) & 3u)) : 0u;
-#pragma unroll
-      for (int d = 1; d < 4; ++d) c[d] += (acc >> (8 * d)) & 255u;
-    }
-#pragma unroll
-    for (int d = 1; d < 4; ++d) c[d] = __reduce_add_sync(0xffffffffu, c[d]);
-    // (two sets of slots in turn: one barrier per step)
-    if (lane == 0) warp_c[step & 1][warp] = make_int4(0, c[1], c[2], c[3]);
+  // Twelve bits of the n-th largest key, two at a time, by counting the keys that reach each of three
+  // thresholds: sign, exponent and three bits of mantissa leave a few percent of the keys.  (With
+  // histograms from the first bit on, the shared-memory atomics of all keys took most of the time.)
+  uint32_t prefix = 0;
+  int above = 0;  // keys above every one with these bits
+  for (int shift = 30; shift >= 20; shift -= 2) {
+    const uint32_t t1 = prefix | 1u << shift, t2 = prefix | 2u << shift, t3 = prefix | 3u << shift;
+    int a1 = 0, a2 = 0, a3 = 0;
+    visit([&](uint32_t k, int) {
+      a1 += k >= t1;
+      a2 += k >= t2;
+      a3 += k >= t3;
+    });
+    a1 = __reduce_add_sync(0xffffffffu, a1);
+    a2 = __reduce_add_sync(0xffffffffu, a2);
+    a3 = __reduce_add_sync(0xffffffffu, a3);
+    const int turn = (shift >> 1) & 1;  // (two sets of slots in turn: one barrier per step)
+    if (lane == 0) warp_c[turn][warp] = make_int4(a1, a2, a3, 0);
     __syncthreads();
-    int4 x = lane < warps ? warp_c[step & 1][lane] : make_int4(0, 0, 0, 0);
+    int4 x = lane < warps ? warp_c[turn][lane] : make_int4(0, 0, 0, 0);
+    a1 = __reduce_add_sync(0xffffffffu, x.x);
+    a2 = __reduce_add_sync(0xffffffffu, x.y);
+    a3 = __reduce_add_sync(0xffffffffu, x.z);
     if (cluster > 1) {
-      c[1] = __reduce_add_sync(0xffffffffu, x.y);
-      c[2] = __reduce_add_sync(0xffffffffu, x.z);
-      c[3] = __reduce_add_sync(0xffffffffu, x.w);
-      if (t < cluster) cg::this_cluster().map_shared_rank(cta_c, t)[(step & 1) * kMaxCluster + rank] = make_int4(0, c[1], c[2], c[3]);
+      if (t < cluster) cg::this_cluster().map_shared_rank(cta_c, t)[turn * kMaxCluster + rank] = make_int4(a1, a2, a3, 0);
       cg::this_cluster().sync();
-      x = lane < cluster ? cta_c[(step & 1) * kMaxCluster + lane] : make_int4(0, 0, 0, 0);
+      x = lane < cluster ? cta_c[turn * kMaxCluster + lane] : make_int4(0, 0, 0, 0);
+      a1 = __reduce_add_sync(0xffffffffu, x.x);
+      a2 = __reduce_add_sync(0xffffffffu, x.y);
+      a3 = __reduce_add_sync(0xffffffffu, x.z);
     }
-    const int c3 = __reduce_add_sync(0xffffffffu, x.w), c2 = __reduce_add_sync(0xffffffffu, x.z),
-              c1 = __reduce_add_sync(0xffffffffu, x.y);
-    uint32_t d = 3;
-    if (c3 < left) {
-      left -= c3;
-      d = 2;
-      if (c2 < left) {
-        left -= c2;
-        d = 1;
-        if (c1 < left) { left -= c1; d = 0; }
-      }
+    if (a3 >= n) {
+      prefix = t3;
+    } else if (a2 >= n) {
+      prefix = t2;
+      above = a3;
+    } else if (a1 >= n) {
+      prefix = t1;
+      above = a2;
+    } else {
+      above = a1;
     }
-    prefix |= d << shift;
-    mask |= 3u << shift;
   }
   // The other twenty, ten at a time, by histograms of the keys that are left.
-  for (int pass = 0; pass < 2; ++pass) {
-    const int shift = pass == 0 ? 10 : 0;
+  int left = n - above;  // how many of the keys with these bits stay
+  for (int shift = 10; shift >= 0; shift -= 10) {
+    const uint32_t mask = 0xffffffffu << (shift + 10);
     for (int i = t; i < kBins; i += nt) hist[i] = 0;
     __syncthreads();
     // (the lowest key behind the end falls, if anywhere, into bin 0, whose count ends nothing early)
-    for (int j0 = t; j0 < padded; j0 += kBatch * nt) {
-      uint32_t k8[kBatch];
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x) k8[x] = key_at(j0 + x * nt);
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x)
-        if (((k8[x] ^ prefix) & mask) == 0) atomicAdd(&hist[(k8[x] >> shift) & (kBins - 1)], 1);
-    }
+    visit([&](uint32_t k, int) {
+      if (((k ^ prefix) & mask) == 0) atomicAdd(&hist[(k >> shift) & (kBins - 1)], 1);
+    });
     if (cluster > 1) cg::this_cluster().sync();
     else __syncthreads();
-    // the bins from the top, two (512 threads) or four to a thread, summed over the cluster
-    const int own = kBins / nt, top = kBins - 1 - t * own;
-    int c[4] = {0, 0, 0, 0};  // c[i]: bin top - i
-    if (cluster > 1) {  // (512 threads: a wide load per CTA, all in flight)
-      int2 x[kMaxCluster];
+    // the bins from the top, four to each of the first 256 threads, summed over the cluster
+    const int top = kBins - 1 - 4 * t;
+    int4 c = make_int4(0, 0, 0, 0);
+    if (t < kBins / 4) {
+      if (cluster > 1) {  // (a wide load per CTA, all in flight)
+        int4 x[kMaxCluster];
 #pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) {
-        x[r] = make_int2(0, 0);
-        if (r < cluster) x[r] = *reinterpret_cast<const int2 *>(cg::this_cluster().map_shared_rank(hist, r) + top - 1);
+        for (int r = 0; r < kMaxCluster; ++r) {
+          x[r] = make_int4(0, 0, 0, 0);
+          if (r < cluster) x[r] = *reinterpret_cast<const int4 *>(cg::this_cluster().map_shared_rank(hist, r) + top - 3);
+        }
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) { c.x += x[r].x; c.y += x[r].y; c.z += x[r].z; c.w += x[r].w; }
+      } else {
+        c = *reinterpret_cast<const int4 *>(hist + top - 3);
       }
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) { c[0] += x[r].y; c[1] += x[r].x; }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < own) c[i] = hist[top - i];
     }
-    const int sum = (c[0] + c[1]) + (c[2] + c[3]);
-    int total;
-    int above = block_scan(sum, sums, total);
-    if (above < left && above + sum >= left) {  // (one thread)
+    const int sum = (c.x + c.y) + (c.z + c.w);
+    int inc = sum, total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    int over = warp_scan(__shfl_sync(0xffffffffu, inc, 31), sums, total) + inc - sum;
+    if (over < left && over + sum >= left) {  // (one thread)
+      const int bins[4] = {c.w, c.z, c.y, c.x};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (i < own && above < left && above + c[i] >= left) {
+        if (over < left && over + bins[i] >= left) {
           found[0] = top - i;
-          found[1] = left - above;
+          found[1] = left - over;
         }
-        above += c[i];
+        over += bins[i];
       }
     }
     // every CTA has read the histograms before any of them starts the next one
     if (cluster > 1) cg::this_cluster().sync();
     else __syncthreads();
     prefix |= (uint32_t)found[0] << shift;
-    mask |= (uint32_t)(kBins - 1) << shift;
     left = found[1];
   }
-  // Keys above `prefix` stay, and the first `left` of those equal to it.  A warp owns a run of the
-  // CTA's keys in order: it counts, the counts are summed up (over the cluster too), it writes.
-  const int wper = (cn + warps * 32 - 1) / (warps * 32) * 32;
-  const int a = min(cn, warp * wper), b = min(cn, a + wper);
-  int gt = 0, eq = 0;
-#pragma unroll 8
-  for (int j = a + lane; j < b; j += 32) {
-    const uint32_t key = key_at(j);
-    gt += key > prefix;
-    eq += key == prefix;
-  }
+  // Keys above `prefix` stay, and the first `left` of those equal to it: the warps count, the counts
+  // are summed up (over the cluster too), each warp writes its run.
+  int gt = 0, eq = 0, all_eq, all_gt;
+  visit([&](uint32_t k, int e) {
+    gt += k > prefix;
+    eq += k == prefix && wa + 32 * e < cn;
+  });
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
-  int all_eq, all_gt;
-  int eq_at = block_scan(lane == 0 ? eq : 0, sums, all_eq);  // (lane 0's is its warp's)
-  eq_at = __shfl_sync(0xffffffffu, eq_at, 0);
-  int gt_at = block_scan(lane == 0 ? gt : 0, sums, all_gt);
-  gt_at = __shfl_sync(0xffffffffu, gt_at, 0);
+  int eq_at = warp_scan(eq, sums, all_eq), gt_at = warp_scan(gt, sums, all_gt);
   if (cluster > 1) {
     if (t == 0) { counts[0] = all_eq; counts[1] = all_gt; }
     cg::this_cluster().sync();
-    for (int r = 0; r < rank; ++r) {
-      const int *c = cg::this_cluster().map_shared_rank(counts, r);
-      eq_at += c[0];
-      gt_at += c[1];
-    }
+    // (lane r reads rank r's, of the ranks before this one)
+    const int *c = cg::this_cluster().map_shared_rank(counts, min(lane, cluster - 1));
+    eq_at += __reduce_add_sync(0xffffffffu, lane < rank ? c[0] : 0);
+    gt_at += __reduce_add_sync(0xffffffffu, lane < rank ? c[1] : 0);
   }
   int at = gt_at + min(eq_at, left);  // this warp's first output
-  const unsigned below = (1u << lane) - 1u;
-#pragma unroll 4
-  for (int j0 = a; j0 < b; j0 += 32) {
-    const int j = j0 + lane;
-    const uint32_t key = j < b ? key_at(j) : 0u;
-    const unsigned eqs = __ballot_sync(0xffffffffu, j < b && key == prefix);
-    const bool keep = j < b && (key > prefix || (key == prefix && eq_at + __popc(eqs & below) < left));
-    const unsigned kept = __ballot_sync(0xffffffffu, keep);
-    if (keep) index[at + __popc(kept & below)] = c0 + j;
-    at += __popc(kept);
-    eq_at += __popc(eqs);
+  if (gt + eq > 0) {
+    const unsigned below = (1u << lane) - 1u;
+    visit([&](uint32_t k, int e) {
+      const int j = wa + 32 * e;
+      const bool is_eq = k == prefix && j < cn;
+      const unsigned eqs = __ballot_sync(0xffffffffu, is_eq);
+      const bool keep = k > prefix || (is_eq && eq_at + __popc(eqs & below) < left);
+      const unsigned kept = __ballot_sync(0xffffffffu, keep);
+      if (keep) index[at + __popc(kept & below)] = c0 + j;
+      at += __popc(kept);
+      eq_at += __popc(eqs);
+    });
   }
   // no CTA leaves while another may still read its counts
   if (cluster > 1) cg::this_cluster().sync();
@@ -340,24 +321,31 @@ __global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p, 
 }  // namespace
 
 cudaError_t cache_evict(const EvictParams &p, cudaStream_t st) {
-  // CTAs per (sequence, kv head): one per 8192 keys of the longest sequence, eight at most; 512
-  // threads each, 256 where their share is small
+  // CTAs per (sequence, kv head): one per 8192 keys of the longest sequence, eight at most.  Threads
+  // and keys per thread by the share of a CTA: short lists in small blocks (their barriers are
+  // cheaper), 512 threads up to 8192 keys (four blocks to an SM), then 1024.
   int cluster = 1;
   while (cluster < kMaxCluster && (long long)cluster * 8192 < p.max_kv) cluster *= 2;
   const int share = (p.max_kv + cluster - 1) / cluster;
-  const int threads = share > 1024 ? 512 : 256, batch = kBatch * threads;
-  const bool held = share <= kKeysHeld;
-  const int smem = held ? (share + batch - 1) / batch * batch * 4 : 0;
-  const void *sel = held ? reinterpret_cast<const void *>(evict_select_kernel<true>)
-                         : reinterpret_cast<const void *>(evict_select_kernel<false>);
-  cudaError_t e = set_smem_once(sel, smem);
-  if (e != cudaSuccess) return e;
+  int threads = 1024;
+  const void *sel;
+  if (share <= 1024) {
+    threads = 256;
+    sel = reinterpret_cast<const void *>(evict_select_kernel<4>);
+  } else if (share <= 8192) {
+    threads = 512;
+    sel = reinterpret_cast<const void *>(evict_select_kernel<16>);
+  } else if (share <= 16384) {
+    sel = reinterpret_cast<const void *>(evict_select_kernel<16>);
+  } else {
+    sel = share <= 32768 ? reinterpret_cast<const void *>(evict_select_kernel<32>)
+                         : reinterpret_cast<const void *>(evict_select_kernel<0>);
+  }
   EvictParams a = p;
   void *args[2] = {&a, &cluster};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.num_seqs * cluster, p.h_kv);
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -365,7 +353,7 @@ cudaError_t cache_evict(const EvictParams &p, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
-  e = cudaLaunchKernelExC(&cfg, sel, args);
+  cudaError_t e = cudaLaunchKernelExC(&cfg, sel, args);
   if (e != cudaSuccess) return e;
   count_launch();
   const int es = p.dtype == VLF_F32 ? 4 : 2;
