@@ -63,16 +63,18 @@ __device__ __forceinline__ int warp_scan(int x, int *sums, int &total) {
 // Grid x: sequence * cluster + rank, y: kv head.  A warp owns a run of 32 * K keys in order, lane l
 // the keys l, 32 + l, ... of it, in registers (K = 0: more keys than that, read again on each pass).
 // What is behind the end counts as the lowest key, which no count below sees.
-template <int K>
-__global__ void __launch_bounds__(K == 0 || K >= 16 ? 1024 : 512) evict_select_kernel(const EvictParams p, int cluster) {
+// COPY: the CTA then copies its rows itself (small problems: one launch).
+template <int K, int THREADS, bool COPY>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(const EvictParams p, int cluster) {
   namespace cg = cooperative_groups;
   __shared__ __align__(16) int hist[kBins];
   __shared__ int sums[32], found[2], counts[2];
   __shared__ int4 warp_c[2][32], cta_c[2 * kMaxCluster];
   tc::pdl_trigger();
   tc::pdl_wait();
-  const int s = blockIdx.x / cluster, rank = blockIdx.x % cluster, h = blockIdx.y, t = threadIdx.x, nt = blockDim.x;
-  const int lane = t & 31, warp = t >> 5, warps = nt >> 5;
+  const int s = blockIdx.x / cluster, rank = blockIdx.x % cluster, h = blockIdx.y, t = threadIdx.x;
+  constexpr int nt = THREADS, warps = THREADS / 32;
+  const int lane = t & 31, warp = t >> 5;
   const bool first = rank == 0 && h == 0 && t == 0;
   // a sequence that cannot be kept leaves -1, and the gather skips it and the one behind it
   auto refuse = [&]() {
@@ -125,8 +127,36 @@ __global__ void __launch_bounds__(K == 0 || K >= 16 ? 1024 : 512) evict_select_k
   if (first) p.cu_out[s + 1] = out0 + n;
   if (n == 0) return;
   int *index = p.index + (size_t)h * p.total_out + out0;
+  // this (sequence, head)'s rows, a 16-byte piece of K or V per thread and turn, four in flight
+  auto copy_rows = [&]() {
+    __syncthreads();  // (the block's own writes of index)
+    const int es = p.dtype == VLF_F32 ? 4 : 2, rk = p.d_qk * es / 16, rv = p.d_v * es / 16, pieces = rk + rv;
+    for (int r = t; r < n; r += nt)
+      p.weights_out[(size_t)h * p.total_out + out0 + r] = __ldg(p.weights + (size_t)h * p.total_kv + k0 + index[r]);
+    const int all_pieces = n * pieces;
+    for (int i0 = t; i0 < all_pieces; i0 += 4 * nt) {
+      uint4 x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * nt, r = i / pieces, c = i % pieces;
+        if (i >= all_pieces) continue;
+        const size_t row = (size_t)(k0 + index[r]) * p.h_kv + h;
+        x[u] = c < rk ? __ldg(static_cast<const uint4 *>(p.k) + row * rk + c)
+                      : __ldg(static_cast<const uint4 *>(p.v) + row * rv + c - rk);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * nt, r = i / pieces, c = i % pieces;
+        if (i >= all_pieces) continue;
+        const size_t row = (size_t)(out0 + r) * p.h_kv + h;
+        if (c < rk) static_cast<uint4 *>(p.k_out)[row * rk + c] = x[u];
+        else static_cast<uint4 *>(p.v_out)[row * rv + c - rk] = x[u];
+      }
+    }
+  };
   if (all) {
     for (int j = t; j < cn; j += nt) index[c0 + j] = c0 + j;
+    if constexpr (COPY) copy_rows();
     return;
   }
   // Twelve bits of the n-th largest key, two at a time, by counting the keys that reach each of three
@@ -260,6 +290,7 @@ __global__ void __launch_bounds__(K == 0 || K >= 16 ? 1024 : 512) evict_select_k
   }
   // no CTA leaves while another may still read its counts
   if (cluster > 1) cg::this_cluster().sync();
+  if constexpr (COPY) copy_rows();
 }
 
 // Kept rows of K, V and the weights.  Grid y = sequence, x = runs of (output row, head) items, heads
@@ -321,25 +352,30 @@ __global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p, 
 }  // namespace
 
 cudaError_t cache_evict(const EvictParams &p, cudaStream_t st) {
+  const int es = p.dtype == VLF_F32 ? 4 : 2;
+  const bool whole = p.d_qk * es % 16 == 0 && p.d_v * es % 16 == 0;
+  const long long most = std::min(p.max_kv, p.budget);
   // CTAs per (sequence, kv head): one per 8192 keys of the longest sequence, eight at most.  Threads
-  // and keys per thread by the share of a CTA: short lists in small blocks (their barriers are
-  // cheaper), 512 threads up to 8192 keys (four blocks to an SM), then 1024.
+  // and keys per thread by the share of a CTA: 256 threads up to 8192 keys (four CTAs to an SM), then
+  // 1024.  Lists of at most 1024 keys whose rows are whole pieces are copied by the CTA that selected
+  // them, as long as one CTA has at most 256 KB to move: the second launch would cost more.
   int cluster = 1;
   while (cluster < kMaxCluster && (long long)cluster * 8192 < p.max_kv) cluster *= 2;
   const int share = (p.max_kv + cluster - 1) / cluster;
+  const bool copy = share <= 1024 && whole && most * (p.d_qk + p.d_v) * es <= 262144;
   int threads = 1024;
   const void *sel;
-  if (share <= 1024) {
+  if (share <= 8192) {
     threads = 256;
-    sel = reinterpret_cast<const void *>(evict_select_kernel<4>);
-  } else if (share <= 8192) {
-    threads = 512;
-    sel = reinterpret_cast<const void *>(evict_select_kernel<16>);
+    if (copy) sel = reinterpret_cast<const void *>(evict_select_kernel<4, 256, true>);
+    else if (share <= 1024) sel = reinterpret_cast<const void *>(evict_select_kernel<4, 256, false>);
+    else if (share <= 4096) sel = reinterpret_cast<const void *>(evict_select_kernel<16, 256, false>);
+    else sel = reinterpret_cast<const void *>(evict_select_kernel<32, 256, false>);
   } else if (share <= 16384) {
-    sel = reinterpret_cast<const void *>(evict_select_kernel<16>);
+    sel = reinterpret_cast<const void *>(evict_select_kernel<16, 1024, false>);
   } else {
-    sel = share <= 32768 ? reinterpret_cast<const void *>(evict_select_kernel<32>)
-                         : reinterpret_cast<const void *>(evict_select_kernel<0>);
+    sel = share <= 32768 ? reinterpret_cast<const void *>(evict_select_kernel<32, 1024, false>)
+                         : reinterpret_cast<const void *>(evict_select_kernel<0, 1024, false>);
   }
   EvictParams a = p;
   void *args[2] = {&a, &cluster};
@@ -356,10 +392,7 @@ cudaError_t cache_evict(const EvictParams &p, cudaStream_t st) {
   cudaError_t e = cudaLaunchKernelExC(&cfg, sel, args);
   if (e != cudaSuccess) return e;
   count_launch();
-  const int es = p.dtype == VLF_F32 ? 4 : 2;
-  const long long most = std::min(p.max_kv, p.budget);
-  if (most == 0 || p.total_out == 0) return cudaSuccess;
-  const bool whole = p.d_qk * es % 16 == 0 && p.d_v * es % 16 == 0;
+  if (copy || most == 0 || p.total_out == 0) return cudaSuccess;
   const int b = whole ? 16 : es;
   int rk = p.d_qk * es / b, rv = p.d_v * es / b;
   // rounds of a block: as many, up to eight, as leave eight blocks per SM

@@ -694,12 +694,16 @@ bool tc_shape(int d_qk, int d_v, int dtype, unsigned flags) {
          (d_qk == 64 || d_qk == 96 || d_qk == 128);
 }
 
-// How the work is cut (sizes alone; the lengths are on the device).
-//  * Shared when the batch's rows pack into at most half as many tiles as the sequences' rows do one
-//    by one.
-//  * Parts: as many as give every resident CTA slot (two per SM) about two runs of key tiles, four
-//    tiles at least each.
+// How the work is cut, by sizes alone (the lengths are on the device).  Costs are in key tiles of one
+// CTA (a third of a microsecond each at width 128): what the busiest of the resident CTA slots (two
+// per SM) walks, and kMerge more where results have to be merged (the second launch and its traffic:
+// 4 to 6 us).
+//  * per sequence: row tiles walk the prefix and their own keys; cut into parts, four tiles each at
+//    least, where the row tiles leave slots empty;
+//  * shared: the batch's rows packed against the prefix, and the own keys apart; parts of about half
+//    of what a slot gets.
 PfxPlan make_plan(int num_seqs, int total_q, int max_q, int max_kv, int prefix, int h_q, int h_kv, int num_sms) {
+  constexpr long long kMerge = 16;
   PfxPlan pl{};
   const int group = h_q / h_kv;
   pl.gb = std::min(group, 128);
@@ -708,28 +712,27 @@ PfxPlan make_plan(int num_seqs, int total_q, int max_q, int max_kv, int prefix, 
   pl.rows = 128 / pl.gb;
   pl.heads = h_kv * pl.nhb;
   pl.np = (prefix + kBN - 1) / kBN;
-  const long long no = ((long long)max_kv + kBN - 1) / kBN;
+  const long long no = ((long long)max_kv + kBN - 1) / kBN, slots = 2ll * num_sms;
   pl.rb_own = (max_q + pl.rows - 1) / pl.rows;
   pl.rb_pre = (total_q + pl.rows - 1) / pl.rows;
   // row tiles of the sequences one by one, as far as the sizes tell
   const long long own_tiles = std::min((long long)num_seqs * pl.rb_own, (long long)pl.rb_pre + num_seqs);
-  const long long slots = 2ll * num_sms;
-  pl.shared = pl.np > 0 && own_tiles >= 2ll * pl.rb_pre;
+  const long long own = std::max(1ll, own_tiles * pl.heads), pre = (long long)pl.rb_pre * pl.heads;
+  auto up = [](long long a, long long b) { return (a + b - 1) / b; };
+  const long long cut = std::max(1ll, std::min({slots / own, (pl.np + no) / 4, 64ll}));
+  const long long whole = up(own, slots) * (pl.np + no), in_parts = up(pl.np + no, cut) + kMerge;
+  const long long run = std::max(4ll, (pre * pl.np + own * no) / (2 * slots));
+  const long long apart = std::max(up(pre * pl.np + own * no, slots), run) + kMerge;
   pl.parts_pre = 0;
-  pl.parts_own = 1;
-  const long long own_ctas = std::max(1ll, own_tiles * pl.heads);
+  pl.parts_own = cut > 1 && in_parts < whole ? (int)cut : 1;
+  pl.shared = pl.np > 0 && apart < (pl.parts_own > 1 ? in_parts : whole);
   if (pl.shared) {
-    const long long pre_ctas = (long long)pl.rb_pre * pl.heads;
-    const long long run = std::max(4ll, (pre_ctas * pl.np + own_ctas * no) / (2 * slots));
-    pl.parts_pre = (int)std::max(1ll, std::min({((long long)pl.np + run - 1) / run, 48ll}));
-    pl.parts_own = (int)std::max(1ll, std::min({(no + run - 1) / run, 16ll}));
-  } else if (own_ctas < slots) {
-    pl.parts_own = (int)std::max(1ll, std::min({slots / own_ctas, (pl.np + no) / 4, 64ll}));
+    pl.parts_pre = (int)std::min(up(pl.np, run), 48ll);
+    pl.parts_own = (int)std::max(1ll, std::min(up(no, run), 16ll));
   }
   pl.parts = pl.parts_pre + pl.parts_own;
   if (pl.parts == 1) pl.parts = 0;
-  const long long n_pre = (long long)pl.rb_pre * pl.heads * pl.parts_pre;
-  const long long n_own = (long long)num_seqs * pl.heads * pl.rb_own * pl.parts_own;
+  const long long n_pre = pre * pl.parts_pre, n_own = (long long)num_seqs * pl.heads * pl.rb_own * pl.parts_own;
   pl.n_pre = (unsigned)n_pre;
   pl.n_all = n_pre + n_own <= 0x7fffffffll ? (unsigned)(n_pre + n_own) : 0u;
   return pl;
