@@ -181,12 +181,17 @@ cudaError_t simt_prefix(const PrefixParams &pp, cudaStream_t st) {
 //    log-sum-exps.  Per sequence: each row tile walks prefix and own keys in one go (cut into parts
 //    only where the row tiles are too few to fill the GPU).  Shared pays where a sequence's rows fill
 //    less than a tile (decode steps): make_plan below.
+//  * Quarter tiles (quad) where a sequence's rows fill at most a quarter of a row tile (decode steps).
+//    A softmax warp can only read its own 32 TMEM lanes, so with one row tile a single warp would walk
+//    all 64 columns of each key tile and set the pace.  The rows are loaded four times instead, once
+//    per quarter, and quarter w takes keys 16 w ... 16 w + 15 of each tile (its other weights are zero):
+//    four softmaxes over disjoint keys, a quarter of the work each, joined at the end in shared memory.
 //  * Values behind a sequence's last key belong to the next sequence: they are zeroed in shared memory
 //    before the product, so that an infinity or NaN there (0 x inf) cannot reach this one.
 using namespace tc;
 
 struct PfxMaps {
-  CUtensorMap q, k, v, kp, vp;
+  CUtensorMap q, q_own, k, v, kp, vp;
 };
 
 constexpr int kBN = 64;  // keys per tile
@@ -197,6 +202,7 @@ struct PfxPlan {
   int shared;
   int gb, nhb;         // heads per row tile, row tiles per kv head's group
   int rows;            // query rows per row tile
+  int quad, rows_own;  // quarter tiles for the sequences' own CTAs; query rows of their row tiles
   int np;              // prefix key tiles
   int heads;           // h_kv * nhb
   int rb_pre, rb_own;  // row blocks: of the batch (shared prefix part), of a sequence
@@ -262,16 +268,18 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
     if (s == p.num_seqs - 1 && (sq.q0 + sq.q_len != p.total_q || sq.k0 + sq.kv_len != p.total_kv))
       set_error(p.err, VLF_ERR_BAD_SEQLENS);
     if (p.causal) rb = pl.rb_own - 1 - rb;  // the rows that see most first
-    if (rb * pl.rows >= sq.q_len) return;
+    if (rb * pl.rows_own >= sq.q_len) return;
     slot = pl.parts_pre + part;
   }
   const int hk = hd / pl.nhb, h0 = hk * p.group + hd % pl.nhb * pl.gb;
-  const int row0 = pre ? rb * pl.rows : sq.q0 + rb * pl.rows;                 // packed row of tile row 0
-  const int nrows = min(pl.rows, (pre ? p.total_q : sq.q0 + sq.q_len) - row0);  // query rows of the tile
+  const bool quad = !pre && pl.quad;
+  const int rows = pre ? pl.rows : pl.rows_own;
+  const int row0 = pre ? rb * rows : sq.q0 + rb * rows;                    // packed row of tile row 0
+  const int nrows = min(rows, (pre ? p.total_q : sq.q0 + sq.q_len) - row0);  // query rows of the tile
   const int keys = P + sq.kv_len, off = keys - sq.q_len;                      // (per-sequence CTAs)
   // Softmax warps that hold a row.  The others have nothing to do: what they leave in P stands in
   // rows of O that nobody reads (a decode step's tile is mostly such rows).
-  const int live_warps = (nrows * pl.gb + 31) / 32;
+  const int live_warps = quad ? 4 : (nrows * pl.gb + 31) / 32;
 
   const uint32_t base = smem_u32(smem_raw);
   if (base & 1023u) {
@@ -332,7 +340,7 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
     hi = band[1] > band[0] ? (band[1] + kBN - 1) / kBN : 0;
   } else {
     int klo, khi;
-    kv_band(rb * pl.rows, rb * pl.rows + nrows, sq.q_len, keys, p.causal, p.window, klo, khi);
+    kv_band(rb * rows, rb * rows + nrows, sq.q_len, keys, p.causal, p.window, klo, khi);
     lo = klo < P ? klo / kBN : pl.np + (klo - P) / kBN;
     hi = khi <= P ? (khi + kBN - 1) / kBN : pl.np + (khi - P + kBN - 1) / kBN;
     if (SPLIT && pl.shared) lo = max(lo, pl.np);  // the prefix part has CTAs of its own
@@ -352,8 +360,10 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0 && hi > lo) {
-      mbar_expect_tx(bar(C::B_Q), C::KB * pl.gb * pl.rows * 128);
-      for (int c = 0; c < C::KB; ++c) tma_load_3d(sQ + c * C::QBLK, &maps.q, 64 * c, h0, row0, bar(C::B_Q));
+      mbar_expect_tx(bar(C::B_Q), (quad ? 4 : 1) * C::KB * pl.gb * rows * 128);
+      for (int c = 0; c < C::KB; ++c)
+        for (int x = 0; x < (quad ? 4 : 1); ++x)
+          tma_load_3d(sQ + c * C::QBLK + x * 32 * 128, pre ? &maps.q : &maps.q_own, 64 * c, h0, row0, bar(C::B_Q));
       auto load = [&](const CUtensorMap *pm, const CUtensorMap *om, int j, uint32_t dst, uint32_t b) {
         const CUtensorMap *m = j < pl.np ? pm : om;
         const int y = j < pl.np ? j * kBN : sq.k0 + (j - pl.np) * kBN;
@@ -445,7 +455,7 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
     }
   } else if (warp >= 4 && warp - 4 < live_warps) {
     // ------------------------------------------------------------------ softmax / epilogue
-    const int r = 32 * (warp & 3) + lane, tok = r / pl.gb;
+    const int quarter = warp & 3, r = quad ? lane : 32 * quarter + lane, tok = r / pl.gb;
     const int head = h0 + r % pl.gb, grow = row0 + tok;
     bool row_ok = tok < nrows;
     int vlo = 0, vhi = 0;  // this row's visible keys
@@ -460,13 +470,72 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
     } else if (row_ok) {
       visible_range(grow - sq.q0, off, keys, p.causal, p.window, vlo, vhi);
     }
-    const uint32_t s_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16), o_addr = s_addr + C::O_COL;
+    const uint32_t s_addr = tmem + ((uint32_t)(32 * quarter) << 16), o_addr = s_addr + C::O_COL;
     const float sl2 = p.scale_log2;
     // l: sum of the rounded P that the MMA multiplies (normalises O); lf: the fp32 sum (LSE)
     float m_ref = -INFINITY, l = 0.f, lf = 0.f;
     const int nt = hi - lo;
     bool ok = true;
-    for (int n = 0; n < nt; ++n) {
+    for (int n = 0; quad && n < nt; ++n) {
+      // quarter tiles: columns c0 ... c0 + 15
+      const int j = lo + n, b = n & 1, c0 = 16 * quarter;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_S + b), (n >> 1) & 1, abort_flag, p.err));
+      if (!ok) break;
+      fence_after();
+      const uint32_t sb = s_addr + 64 * b;
+      const int kb = key_of(j) + c0, elo = vlo - kb, ehi = min(vhi, end_of(j)) - kb;
+      uint32_t v[16];
+      __syncwarp();
+      tmem_ld16(sb + c0, v);
+      tmem_ld_wait();
+      float mx = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float x = e >= elo && e < ehi ? __uint_as_float(v[e]) * sl2 : -INFINITY;
+        v[e] = __float_as_uint(x);
+        mx = fmaxf(mx, x);
+      }
+      const float m_new = fmaxf(m_ref, mx);
+      const bool move = m_new != -INFINITY && m_new > m_ref + kMoveMax;
+      const float alpha = move ? ex2(m_ref - m_new) : 1.f;  // m_ref = -inf: 0
+      if (__any_sync(0xffffffffu, move && n > 0 && l > 0.f)) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_O + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag, p.err));
+        if (!ok) break;
+        fence_after();
+        const float a = l > 0.f ? alpha : 1.f;
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + ch * 32, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+          tmem_st32(o_addr + ch * 32, o);
+        }
+      }
+      if (move) {
+        l *= alpha;
+        lf *= alpha;
+        m_ref = m_new;
+      }
+      const float m0 = m_ref == -INFINITY ? 0.f : m_ref;
+      uint32_t pk[8], w[32];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float pa = ex2(__uint_as_float(v[2 * e]) - m0), pb = ex2(__uint_as_float(v[2 * e + 1]) - m0);
+        pk[e] = pack2(pa, pb, is_bf16);
+        lf += pa + pb;
+        l = add_halves(l, pk[e], is_bf16);
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) w[e] = (e >> 3) == quarter ? pk[e & 7] : 0u;
+      __syncwarp();
+      tmem_st32(sb, w);
+      tmem_st_wait();
+      fence_before();
+      mbar_arrive(bar(C::B_P + b));
+    }
+    for (int n = 0; !quad && n < nt; ++n) {
       const int j = lo + n, b = n & 1;
       ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_S + b), (n >> 1) & 1, abort_flag, p.err));
       if (!ok) break;
@@ -577,7 +646,75 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
     }
     if (ok && nt > 0) ok = mbar_wait(bar(C::B_O + ((nt - 1) & 1)), ((nt - 1) >> 1) & 1, abort_flag, p.err);
     ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
+    if (quad) {
+      // Join the quarters.  Weights f_w = 2^(m_w - max m); the sums by them, and O in runs of 32
+      // columns through shared memory (the K ring: every product has completed): thread t sums columns
+      // of row t / 4.  (All four warps come here, also after a wait that gave up.)
+      constexpr int LD = 36;  // floats per row: 16-byte rows, banks apart
+      float *buf = reinterpret_cast<float *>(smem_raw + C::OFF_K), *st = buf + 128 * LD;  // st [4][32][3]
+      fence_after();
+      const int tid = 32 * quarter + lane;
+      st[3 * tid] = m_ref;
+      st[3 * tid + 1] = l;
+      st[3 * tid + 2] = lf;
+      named_sync(1, 128);
+      const int jr = tid >> 2, jt = jr / pl.gb;  // row and columns that this thread writes
+      const size_t at = (size_t)(row0 + jt) * p.h_q + h0 + jr % pl.gb;
+      float m = -INFINITY, f[4], ls = 0.f, lfs = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) m = fmaxf(m, st[3 * (32 * x + jr)]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float *q = st + 3 * (32 * x + jr);
+        f[x] = m == -INFINITY ? 0.f : ex2(q[0] - m);
+        ls = fmaf(f[x], q[1], ls);
+        lfs = fmaf(f[x], q[2], lfs);
+      }
+      const float inv = ls > 0.f ? 1.f / ls : 0.f;
+      const bool wr = ok && jt < nrows;
+#pragma unroll 1
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t v[32];
+        if (nt > 0) {
+          __syncwarp();
+          tmem_ld32(o_addr + ch * 32, v);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0u;
+        }
+        // (rows of nobody hold whatever the tile held; they are not summed)
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<uint4 *>(buf + tid * LD + 4 * q) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        named_sync(1, 128);
+        float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (!(f[x] > 0.f)) continue;
+          const float *q = buf + (32 * x + jr) * LD + 8 * (tid & 3);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = fmaf(f[x], q[e], o[e]);
+        }
+        named_sync(1, 128);
+        if (!wr) continue;
+        const int c = 32 * ch + 8 * (tid & 3);
+        if (SPLIT) {
+          float4 *dst = reinterpret_cast<float4 *>(o_part + ((size_t)slot * p.total_q * p.h_q + at) * D + c);
+          dst[0] = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+          dst[1] = make_float4(o[4] * inv, o[5] * inv, o[6] * inv, o[7] * inv);
+        } else {
+          *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + (at * D + c) * 2) =
+              make_uint4(pack2(o[0] * inv, o[1] * inv, is_bf16), pack2(o[2] * inv, o[3] * inv, is_bf16),
+                         pack2(o[4] * inv, o[5] * inv, is_bf16), pack2(o[6] * inv, o[7] * inv, is_bf16));
+        }
+      }
+      if (wr && (tid & 3) == 0) {
+        const float lse = lfs > 0.f ? (m + lg2(lfs)) * kLn2f : -INFINITY;
+        if (SPLIT) lse_part[(size_t)slot * p.total_q * p.h_q + at] = lse;
+        else if (p.lse) p.lse[(size_t)(h0 + jr % pl.gb) * p.total_q + row0 + jt] = lse;
+      }
+    } else if (ok) {
       fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const float lse = lf > 0.f ? (m_ref + lg2(lf)) * kLn2f : -INFINITY;
@@ -694,42 +831,48 @@ bool tc_shape(int d_qk, int d_v, int dtype, unsigned flags) {
          (d_qk == 64 || d_qk == 96 || d_qk == 128);
 }
 
-// How the work is cut, by sizes alone (the lengths are on the device).  Costs are in key tiles of one
-// CTA (a third of a microsecond each at width 128): what the busiest of the resident CTA slots (two
-// per SM) walks, and kMerge more where results have to be merged (the second launch and its traffic:
-// 4 to 6 us).
+// How the work is cut, by sizes alone (the lengths are on the device).  Costs in tenths of a
+// microsecond: a key tile takes a CTA about 1 us whatever else runs (10; 4 with quarter tiles), the
+// busiest of the resident CTA slots (two per SM) sets the time, and merging costs a launch and the
+// traffic of the parts (70 and 1 per 0.6 MB).
 //  * per sequence: row tiles walk the prefix and their own keys; cut into parts, four tiles each at
 //    least, where the row tiles leave slots empty;
 //  * shared: the batch's rows packed against the prefix, and the own keys apart; parts of about half
-//    of what a slot gets.
-PfxPlan make_plan(int num_seqs, int total_q, int max_q, int max_kv, int prefix, int h_q, int h_kv, int num_sms) {
-  constexpr long long kMerge = 16;
+//    of what a slot gets.  Taken where it saves a fifth.
+PfxPlan make_plan(int num_seqs, int total_q, int max_q, int max_kv, int prefix, int h_q, int h_kv, int d, int num_sms) {
+  constexpr long long kTile = 10, kQuad = 4, kMerge = 70;
   PfxPlan pl{};
   const int group = h_q / h_kv;
   pl.gb = std::min(group, 128);
   while (group % pl.gb) --pl.gb;
   pl.nhb = group / pl.gb;
   pl.rows = 128 / pl.gb;
+  pl.quad = (long long)max_q * pl.gb <= 32;
+  pl.rows_own = pl.quad ? 32 / pl.gb : pl.rows;
   pl.heads = h_kv * pl.nhb;
   pl.np = (prefix + kBN - 1) / kBN;
   const long long no = ((long long)max_kv + kBN - 1) / kBN, slots = 2ll * num_sms;
-  pl.rb_own = (max_q + pl.rows - 1) / pl.rows;
+  pl.rb_own = (max_q + pl.rows_own - 1) / pl.rows_own;
   pl.rb_pre = (total_q + pl.rows - 1) / pl.rows;
   // row tiles of the sequences one by one, as far as the sizes tell
-  const long long own_tiles = std::min((long long)num_seqs * pl.rb_own, (long long)pl.rb_pre + num_seqs);
+  const long long own_tiles =
+      std::min((long long)num_seqs * pl.rb_own, (long long)(total_q + pl.rows_own - 1) / pl.rows_own + num_seqs);
   const long long own = std::max(1ll, own_tiles * pl.heads), pre = (long long)pl.rb_pre * pl.heads;
+  const long long tile = pl.quad ? kQuad : kTile;
   auto up = [](long long a, long long b) { return (a + b - 1) / b; };
-  const long long cut = std::max(1ll, std::min({slots / own, (pl.np + no) / 4, 64ll}));
-  const long long whole = up(own, slots) * (pl.np + no), in_parts = up(pl.np + no, cut) + kMerge;
-  const long long run = std::max(4ll, (pre * pl.np + own * no) / (2 * slots));
-  const long long apart = std::max(up(pre * pl.np + own * no, slots), run) + kMerge;
-  pl.parts_pre = 0;
+  auto merge = [&](long long parts) { return kMerge + parts * total_q * h_q * d * 8 / 600000; };
+  const long long all = pl.np + no;
+  const long long cut = std::max(1ll, std::min({slots / own, all / 4, 64ll}));
+  const long long whole = std::max(own * all / slots, all) * tile, in_parts = up(all, cut) * tile + merge(cut);
+  const long long work = pre * pl.np * kTile + own * no * tile;  // of the shared cut
+  const long long run = std::max(4 * kTile, work / (2 * slots));
   pl.parts_own = cut > 1 && in_parts < whole ? (int)cut : 1;
-  pl.shared = pl.np > 0 && apart < (pl.parts_own > 1 ? in_parts : whole);
-  if (pl.shared) {
-    pl.parts_pre = (int)std::min(up(pl.np, run), 48ll);
-    pl.parts_own = (int)std::max(1ll, std::min(up(no, run), 16ll));
-  }
+  const int parts_pre = (int)std::min(up(pl.np * kTile, run), 48ll);
+  const int parts_own = (int)std::max(1ll, std::min(up(no * tile, run), 16ll));
+  const long long apart = std::max(work / slots, run) + merge(parts_pre + parts_own);
+  pl.shared = pl.np > 0 && apart * 5 < (pl.parts_own > 1 ? in_parts : whole) * 4;
+  pl.parts_pre = pl.shared ? parts_pre : 0;
+  if (pl.shared) pl.parts_own = parts_own;
   pl.parts = pl.parts_pre + pl.parts_own;
   if (pl.parts == 1) pl.parts = 0;
   const long long n_pre = pre * pl.parts_pre, n_own = (long long)num_seqs * pl.heads * pl.rb_own * pl.parts_own;
@@ -751,7 +894,9 @@ cudaError_t launch_tc(const PrefixParams &pp, PfxPlan pl, void *workspace, cudaS
   const int bf = p.dtype == VLF_BF16;
   const uint64_t kc = (uint64_t)p.h_kv * D;
   const bool have_p = pp.prefix_len > 0, have_o = p.total_kv > 0;
-  if (!make_tmap_q3(&maps.q, p.q, p.total_q, p.h_q, D, pl.gb, pl.rows, bf)) return cudaErrorInvalidValue;
+  if (!make_tmap_q3(&maps.q, p.q, p.total_q, p.h_q, D, pl.gb, pl.rows, bf) ||
+      !make_tmap_q3(&maps.q_own, p.q, p.total_q, p.h_q, D, pl.gb, pl.rows_own, bf))
+    return cudaErrorInvalidValue;
   if (have_p && (!make_tmap_16bit(&maps.kp, pp.k_pre, pp.prefix_len, kc, kc, kBN, bf) ||
                  !make_tmap_16bit(&maps.vp, pp.v_pre, pp.prefix_len, kc, kc, kBN, bf)))
     return cudaErrorInvalidValue;
@@ -796,7 +941,7 @@ size_t prefix_workspace(int num_seqs, int total_q, int max_q, int max_kv, int pr
   if (num_seqs < 1 || total_q < 1 || max_q < 1 || max_kv < 0 || prefix < 0 || h_kv < 1 || h_q < 1 || h_q % h_kv ||
       num_sms < 1 || !tc_shape(d_qk, d_v, dtype, flags))
     return 0;
-  const PfxPlan pl = make_plan(num_seqs, total_q, max_q, max_kv, prefix, h_q, h_kv, num_sms);
+  const PfxPlan pl = make_plan(num_seqs, total_q, max_q, max_kv, prefix, h_q, h_kv, d_v, num_sms);
   return pl.parts ? parts_bytes(pl, total_q, h_q, d_v) : 0;
 }
 
@@ -805,7 +950,7 @@ cudaError_t prefix_forward(const PrefixParams &pp, void *workspace, int num_sms,
   // (without rows or keys there is nothing to stage)
   if (!tc_shape(p.d_qk, p.d_v, p.dtype, p.flags) || p.total_q == 0 || (p.total_kv == 0 && pp.prefix_len == 0))
     return simt_prefix(pp, st);
-  const PfxPlan pl = make_plan(p.num_seqs, p.total_q, p.max_q, p.max_kv, pp.prefix_len, p.h_q, p.h_kv, num_sms);
+  const PfxPlan pl = make_plan(p.num_seqs, p.total_q, p.max_q, p.max_kv, pp.prefix_len, p.h_q, p.h_kv, p.d_v, num_sms);
   if (pl.n_all == 0) return cudaErrorInvalidValue;
   if (p.d_qk == 64) return launch_tc<64>(pp, pl, workspace, st);
   if (p.d_qk == 96) return launch_tc<96>(pp, pl, workspace, st);
