@@ -776,37 +776,40 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const Params p, int p
   if (w >= pairs || w / p.h_q >= (size_t)max(0, __ldg(p.cu_q + p.num_seqs))) return;
   constexpr int NL = D / 4;                // lanes per part
   constexpr int PER = NL <= 16 ? 2 : 1;    // parts at a time
+  constexpr int FLY = 12;                  // their loads in flight, together with the log-sum-exps'
   const int sub = PER == 2 ? lane >> 4 : 0, c = PER == 2 ? lane & 15 : lane;
-  float m = -INFINITY;
-  for (int s = lane; s < parts; s += 32) m = fmaxf(m, lse_part[s * pairs + w]);
+  auto fetch = [&](int s0, float4 (&x)[FLY]) {
+#pragma unroll
+    for (int i = 0; i < FLY; ++i) {
+      const int s = s0 + i * PER + sub;
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < parts && c < NL) x[i] = *reinterpret_cast<const float4 *>(o_part + (s * pairs + w) * D + 4 * c);
+    }
+  };
+  float4 x[FLY];
+  fetch(0, x);
+  // (64 parts at most: two per lane)
+  const float l0 = lane < parts ? lse_part[lane * pairs + w] : -INFINITY;
+  const float l1 = 32 + lane < parts ? lse_part[(32 + lane) * pairs + w] : -INFINITY;
+  float m = fmaxf(l0, l1);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float mm = m == -INFINITY ? 0.f : m;
-  float sum = 0.f;
+  const float e0 = expf(l0 - mm), e1 = expf(l1 - mm);
+  float sum = e0 + e1;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < parts; s0 += 32) {
-    const float e = s0 + lane < parts ? expf(lse_part[(s0 + lane) * pairs + w] - mm) : 0.f;
-    sum += e;
-    const int n = min(32, parts - s0);
-    // eight parts' loads in flight
-    for (int s = 0; s < n; s += 8 * PER) {
-      float4 x[8];
+  for (int s0 = 0; s0 < parts; s0 += FLY * PER) {
+    if (s0 > 0) fetch(s0, x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int y = s + i * PER + sub;
-        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (y < n && c < NL) x[i] = *reinterpret_cast<const float4 *>(o_part + ((s0 + y) * pairs + w) * D + 4 * c);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int y = s + i * PER + sub;
-        const float wgt = __shfl_sync(0xffffffffu, e, y & 31);
-        if (y >= n) continue;
-        acc.x = fmaf(wgt, x[i].x, acc.x);
-        acc.y = fmaf(wgt, x[i].y, acc.y);
-        acc.z = fmaf(wgt, x[i].z, acc.z);
-        acc.w = fmaf(wgt, x[i].w, acc.w);
-      }
+    for (int i = 0; i < FLY; ++i) {
+      const int s = s0 + i * PER + sub;
+      const float wa = __shfl_sync(0xffffffffu, e0, s & 31), wb = __shfl_sync(0xffffffffu, e1, s & 31);
+      const float wgt = s < 32 ? wa : wb;
+      if (s >= parts || !(wgt > 0.f)) continue;
+      acc.x = fmaf(wgt, x[i].x, acc.x);
+      acc.y = fmaf(wgt, x[i].y, acc.y);
+      acc.z = fmaf(wgt, x[i].z, acc.z);
+      acc.w = fmaf(wgt, x[i].w, acc.w);
     }
   }
 #pragma unroll
@@ -837,8 +840,8 @@ bool tc_shape(int d_qk, int d_v, int dtype, unsigned flags) {
 // traffic of the parts (70 and 1 per 0.6 MB).
 //  * per sequence: row tiles walk the prefix and their own keys; cut into parts, four tiles each at
 //    least, where the row tiles leave slots empty;
-//  * shared: the batch's rows packed against the prefix, and the own keys apart; parts of about half
-//    of what a slot gets.  Taken where it saves a fifth.
+//  * shared: the batch's rows packed against the prefix, and the own keys apart; parts of what a slot
+//    gets (they start first, and the own keys' CTAs fill up behind them).  Taken where it saves a fifth.
 PfxPlan make_plan(int num_seqs, int total_q, int max_q, int max_kv, int prefix, int h_q, int h_kv, int d, int num_sms) {
   constexpr long long kTile = 10, kQuad = 4, kMerge = 70;
   PfxPlan pl{};
@@ -865,7 +868,7 @@ PfxPlan make_plan(int num_seqs, int total_q, int max_q, int max_kv, int prefix, 
   const long long cut = std::max(1ll, std::min({slots / own, all / 4, 64ll}));
   const long long whole = std::max(own * all / slots, all) * tile, in_parts = up(all, cut) * tile + merge(cut);
   const long long work = pre * pl.np * kTile + own * no * tile;  // of the shared cut
-  const long long run = std::max(4 * kTile, work / (2 * slots));
+  const long long run = std::max(4 * kTile, work / slots);
   pl.parts_own = cut > 1 && in_parts < whole ? (int)cut : 1;
   const int parts_pre = (int)std::min(up(pl.np * kTile, run), 48ll);
   const int parts_own = (int)std::max(1ll, std::min(up(no * tile, run), 16ll));
