@@ -143,7 +143,7 @@ struct KwPlan {
   int k_bytes, q_bytes, q_blk;
 };
 
-constexpr int kKwThreads = 384;
+constexpr int kKwThreads = 320;  // producer, MMA issuer, eight epilogue warps
 constexpr int kKwMisc = 1024;  // barriers, flags
 constexpr int kMaxSlots = 8;
 constexpr int kLseBytes = 8 * 2 * 128 * 4;
@@ -302,20 +302,22 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
     }
     mma_commit_w(bar(B_DRAIN));
     drain_wait(bar(B_DRAIN), 0);
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------------ sums
-    const int wg = (warp - 4) >> 2, quarter = warp & 3, tid = 32 * quarter + lane;
+    const int wg = (warp - 2) >> 2, quarter = warp & 3, tid = 32 * quarter + lane;
     const uint32_t s_addr = tmem + half * wg + ((uint32_t)(32 * quarter) << 16);
     // each warp keeps its own copy of a column tile's -lse, so that no warp waits for another
-    float *ls = lse_s + (warp - 4) * 256;
+    float *ls = lse_s + (warp - 2) * 256;
     const uint32_t ls_a = smem_u32(ls);
     const int valid = pl.rows * pl.gb;  // columns that hold a (row, head) pair
+    const bool one_hb = pl.nhb == 1;    // (saves the divisions)
     int ri[4], hi_[4];                  // row and head of this lane's four columns
 #pragma unroll
     for (int e = 0; e < 4; ++e) { ri[e] = (lane + 32 * e) / pl.gb; hi_[e] = (lane + 32 * e) % pl.gb; }
     // -lse log2(e) of this lane's columns of column tile c (-inf: takes the column out)
     auto neg_lse = [&](int c, float (&x)[4]) {
-      const int r0 = c / pl.nhb * pl.rows, h0 = hk * p.group + c % pl.nhb * pl.gb;
+      const int rb = one_hb ? c : c / pl.nhb, r0 = rb * pl.rows;
+      const int h0 = hk * p.group + (one_hb ? 0 : (c - rb * pl.nhb) * pl.gb);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         x[e] = -INFINITY;
@@ -336,6 +338,8 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
       for (int e = 0; e < 4; ++e) ls[lane + 32 * e] = next[e];
       __syncwarp();
     }
+    int lo = 0, hi = 0;  // the rows that see this thread's key
+    if (!STREAM_K) visible_rows(min(t0 * 128 + tid, sq.kv_len - 1), off, sq.q_len, p.causal, p.window, lo, hi);
     int n = 0;  // score tiles so far, both warpgroups'
     for (int t = first; t < last; ++t) {
       const bool is_live = live(t);
@@ -357,32 +361,30 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
           if (t + 2 < last) neg_lse(t + 2, next);
           __syncwarp();
         }
-        int lo, hi;
-        visible_rows(min(j, sq.kv_len - 1), off, sq.q_len, p.causal, p.window, lo, hi);
-        const int r0 = STREAM_K ? 0 : t / pl.nhb * pl.rows;
+        if (STREAM_K) visible_rows(min(j, sq.kv_len - 1), off, sq.q_len, p.causal, p.window, lo, hi);
+        const int r0 = STREAM_K ? 0 : (one_hb ? t : t / pl.nhb) * pl.rows;
         const int clo = min(max(lo - r0, 0), pl.rows) * pl.gb, chi = min(max(hi - r0, 0), pl.rows) * pl.gb;
         ok = __all_sync(0xffffffffu, mbar_wait(bar(B_SF + wg), (n >> 1) & 1, abort_flag, p.err));
         if (!ok) break;
         fence_after();
         uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
         const uint32_t la = ls_a + 512 * buf;
-        // 16 columns at a time where that is all there are, else 32
-        auto chunk = [&](auto width, int c) {
+        // W columns from c on; FULL: every one of them is visible to every key of the warp
+        auto chunk = [&](auto width, auto whole, int c) {
           constexpr int W = decltype(width)::value;
+          constexpr bool FULL = decltype(whole)::value;
           uint32_t v[W];
           __syncwarp();
           if constexpr (W == 32) tmem_ld32(s_addr + c, v);
           else tmem_ld16(s_addr + c, v);
           tmem_ld_wait();
-          const bool full = __all_sync(0xffffffffu, c >= clo && c + W <= chi);
 #pragma unroll
           for (int e = 0; e < W; e += 4) {
-            const float4 l4 = lds_f32x4(la + 4 * (c + e));
-            float2 a = f2unpack(fma2(f2pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), scale2,
-                                     f2pack(l4.x, l4.y)));
-            float2 b = f2unpack(fma2(f2pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), scale2,
-                                     f2pack(l4.z, l4.w)));
-            if (!full) {
+            uint64_t l0, l1;  // two pairs of -lse
+            lds_b64x2(la + 4 * (c + e), l0, l1);
+            float2 a = f2unpack(fma2(f2pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), scale2, l0));
+            float2 b = f2unpack(fma2(f2pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), scale2, l1));
+            if constexpr (!FULL) {
               const int x = c + e;
               a.x = x >= clo && x < chi ? a.x : -INFINITY;
               a.y = x + 1 >= clo && x + 1 < chi ? a.y : -INFINITY;
@@ -393,11 +395,19 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
             acc1 = add2(acc1, f2pack(ex2(b.x), ex2(b.y)));
           }
         };
+        constexpr std::integral_constant<int, 16> w16{};
+        constexpr std::integral_constant<int, 32> w32{};
         if (half == 16) {
-          chunk(std::integral_constant<int, 16>{}, 0);
+          chunk(w16, std::false_type{}, 0);
+        } else if (__all_sync(0xffffffffu, clo <= 0 && chi >= 128)) {
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) chunk(w32, std::true_type{}, c);
         } else {
 #pragma unroll 1
-          for (int c = 0; c < valid; c += 32) chunk(std::integral_constant<int, 32>{}, c);
+          for (int c = 0; c < valid; c += 32) {
+            // (a chunk that no key of the warp sees is passed over)
+            if (__any_sync(0xffffffffu, c < chi && c + 32 > clo)) chunk(w32, std::false_type{}, c);
+          }
         }
         // the buffer may be overwritten
         fence_before();
@@ -420,7 +430,7 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
       named_sync(1, 256);
       const int j = t0 * 128 + tid;
       if (wg == 0 && j < sq.kv_len && ok) {
-        const float w = total + lse_s[(4 + quarter) * 256 + lane];
+        const float w = total + lse_s[(4 + ((quarter + 2) & 3)) * 256 + lane];  // (warps 6 to 9: quarters 2, 3, 0, 1)
         const size_t at = (size_t)hk * p.total_kv + sq.k0 + j;
         if (parts) parts[(size_t)((int)blockIdx.z % pl.splits) * p.h_kv * p.total_kv + at] = w;
         else kp.weights[at] = kp.prev ? kp.prev[at] + w : w;

@@ -460,6 +460,10 @@ __device__ __forceinline__ float4 lds_f32x4(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ void lds_b64x2(uint32_t a, uint64_t &x, uint64_t &y) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
+}
+
 }  // namespace tc
 
 // ---------------------------------------------------------------- host side (tc_fwd.cu)
