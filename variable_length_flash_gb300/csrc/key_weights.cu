@@ -314,28 +314,31 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
     int ri[4], hi_[4];                  // row and head of this lane's four columns
 #pragma unroll
     for (int e = 0; e < 4; ++e) { ri[e] = (lane + 32 * e) / pl.gb; hi_[e] = (lane + 32 * e) % pl.gb; }
-    // -lse log2(e) of this lane's columns of column tile c (-inf: takes the column out)
-    auto neg_lse = [&](int c, float (&x)[4]) {
+    // The lse of this lane's columns of column tile c (-inf where there is no row), as loaded: nothing
+    // is computed with it before staged(), a tile later, so that the loads' latency passes under a tile
+    // (converted at once, each tile waited for them: 332 us where this takes TIME_PROMPT, 4 x 4096
+    // causal, 32 heads).
+    auto fetch_lse = [&](int c, float (&x)[4]) {
       const int rb = one_hb ? c : c / pl.nhb, r0 = rb * pl.rows;
       const int h0 = hk * p.group + (one_hb ? 0 : (c - rb * pl.nhb) * pl.gb);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         x[e] = -INFINITY;
-        if (lane + 32 * e < valid && r0 + ri[e] < sq.q_len) {
-          const float l = __ldg(kp.lse + (size_t)(h0 + hi_[e]) * p.total_q + sq.q0 + r0 + ri[e]);
-          if (l != -INFINITY) x[e] = -l * kLog2e;
-        }
+        if (lane + 32 * e < valid && r0 + ri[e] < sq.q_len)
+          x[e] = __ldg(kp.lse + (size_t)(h0 + hi_[e]) * p.total_q + sq.q0 + r0 + ri[e]);
       }
     };
+    // -lse log2(e), what the exponent adds; -inf takes the column out
+    auto staged = [](float l) { return l == -INFINITY ? -INFINITY : -l * kLog2e; };
     const float sl2 = p.scale_log2;
     const uint64_t scale2 = f2pack(sl2, sl2);
     float total = 0.f;
     bool ok = true;
     float next[4] = {0.f, 0.f, 0.f, 0.f};
-    if (STREAM_K || first + wg < last) neg_lse(STREAM_K ? 0 : first + wg, next);
+    if (STREAM_K || first + wg < last) fetch_lse(STREAM_K ? 0 : first + wg, next);
     if (STREAM_K) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) ls[lane + 32 * e] = next[e];
+      for (int e = 0; e < 4; ++e) ls[lane + 32 * e] = staged(next[e]);
       __syncwarp();
     }
     int lo = 0, hi = 0;  // the rows that see this thread's key
@@ -357,8 +360,8 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
         const int buf = STREAM_K ? 0 : (n >> 1) & 1;
         if (!STREAM_K) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) ls[128 * buf + lane + 32 * e] = next[e];
-          if (t + 2 < last) neg_lse(t + 2, next);
+          for (int e = 0; e < 4; ++e) ls[128 * buf + lane + 32 * e] = staged(next[e]);
+          if (t + 2 < last) fetch_lse(t + 2, next);
           __syncwarp();
         }
         if (STREAM_K) visible_rows(min(j, sq.kv_len - 1), off, sq.q_len, p.causal, p.window, lo, hi);
@@ -369,15 +372,10 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
         fence_after();
         uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
         const uint32_t la = ls_a + 512 * buf;
-        // W columns from c on; FULL: every one of them is visible to every key of the warp
-        auto chunk = [&](auto width, auto whole, int c) {
+        // Adds the W columns from c on, loaded into v; FULL: every key of the warp sees all of them.
+        auto add = [&](auto width, auto whole, const uint32_t *v, int c) {
           constexpr int W = decltype(width)::value;
           constexpr bool FULL = decltype(whole)::value;
-          uint32_t v[W];
-          __syncwarp();
-          if constexpr (W == 32) tmem_ld32(s_addr + c, v);
-          else tmem_ld16(s_addr + c, v);
-          tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < W; e += 4) {
             uint64_t l0, l1;  // two pairs of -lse
@@ -395,18 +393,37 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
             acc1 = add2(acc1, f2pack(ex2(b.x), ex2(b.y)));
           }
         };
-        constexpr std::integral_constant<int, 16> w16{};
         constexpr std::integral_constant<int, 32> w32{};
+        __syncwarp();
         if (half == 16) {
-          chunk(w16, std::false_type{}, 0);
+          uint32_t v[16];
+          tmem_ld16(s_addr, v);
+          tmem_ld_wait();
+          add(std::integral_constant<int, 16>{}, std::false_type{}, v, 0);
         } else if (__all_sync(0xffffffffu, clo <= 0 && chi >= 128)) {
-#pragma unroll
-          for (int c = 0; c < 128; c += 32) chunk(w32, std::true_type{}, c);
+          // 32 columns are added while the next 32 load
+          uint32_t v0[32], v1[32];
+          tmem_ld32(s_addr, v0);
+          tmem_ld_wait_for(v0);
+          tmem_ld32(s_addr + 32, v1);
+          add(w32, std::true_type{}, v0, 0);
+          tmem_ld_wait_for(v1);
+          tmem_ld32(s_addr + 64, v0);
+          add(w32, std::true_type{}, v1, 32);
+          tmem_ld_wait_for(v0);
+          tmem_ld32(s_addr + 96, v1);
+          add(w32, std::true_type{}, v0, 64);
+          tmem_ld_wait_for(v1);
+          add(w32, std::true_type{}, v1, 96);
         } else {
 #pragma unroll 1
           for (int c = 0; c < valid; c += 32) {
             // (a chunk that no key of the warp sees is passed over)
-            if (__any_sync(0xffffffffu, c < chi && c + 32 > clo)) chunk(w32, std::false_type{}, c);
+            if (!__any_sync(0xffffffffu, c < chi && c + 32 > clo)) continue;
+            uint32_t v[32];
+            tmem_ld32(s_addr + c, v);
+            tmem_ld_wait_for(v);
+            add(w32, std::false_type{}, v, c);
           }
         }
         // the buffer may be overwritten
