@@ -113,8 +113,8 @@ cudaError_t simt_key_weights(const KeyWeightParams &kp, cudaStream_t st) {
 // thread's registers -- no reduction across threads, no atomics, a fixed order.  The scores never
 // leave TMEM; per score the epilogue does half a packed FMA, one ex2 and half a packed add.
 //
-// Two shapes of the same pipeline (TMA producer warp, MMA warp, two warpgroups that take the score
-// tiles in turn, a TMEM buffer each):
+// Two shapes of the same pipeline (TMA producer warp, MMA warp, a warp that fetches the columns' lse,
+// two warpgroups that take the score tiles in turn, a TMEM buffer each):
 //  * STREAM_K, where all rows of a (sequence, kv head) make at most 128 columns (decode steps, a
 //    window of rows): Q stays in shared memory, a CTA streams a run of key tiles through a ring and
 //    each tile's 128 weights are complete at once.  Bound: HBM, K read once.
@@ -143,10 +143,10 @@ struct KwPlan {
   int k_bytes, q_bytes, q_blk;
 };
 
-constexpr int kKwThreads = 320;  // producer, MMA issuer, eight epilogue warps
+constexpr int kKwThreads = 352;  // producer, MMA issuer, lse warp, eight epilogue warps
 constexpr int kKwMisc = 1024;  // barriers, flags
 constexpr int kMaxSlots = 8;
-constexpr int kLseBytes = 8 * 2 * 128 * 4;
+constexpr int kLseBytes = 3 * 128 * 4;  // two buffers in turn, and the second warpgroup's sums
 
 template <int D, bool BF16, bool STREAM_K>
 __global__ void __launch_bounds__(kKwThreads, D <= 128 ? 2 : 1)
@@ -200,13 +200,14 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
   uint8_t *misc = smem_raw + (sM - base);
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(misc + 512);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 516);
-  float *lse_s = reinterpret_cast<float *>(misc + kKwMisc);  // [epilogue warp][2][128]
+  float *lse_s = reinterpret_cast<float *>(misc + kKwMisc);  // [score buffer][128], then [128]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(bar(B_FIX), 1);
     for (int i = 0; i < pl.slots; ++i) { mbar_init(bar(B_RF + i), 1); mbar_init(bar(B_RE + i), 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(bar(B_SF + i), 1); mbar_init(bar(B_SE + i), 4); }
+    // (a score buffer is ready with its product and its columns' lse)
+    for (int i = 0; i < 2; ++i) { mbar_init(bar(B_SF + i), 2); mbar_init(bar(B_SE + i), 4); }
     mbar_init(bar(B_DRAIN), 1);
     *abort_flag = 0;
     mbar_init_fence();
@@ -302,23 +303,15 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
     }
     mma_commit_w(bar(B_DRAIN));
     drain_wait(bar(B_DRAIN), 0);
-  } else {
-    // ------------------------------------------------------------------ sums
-    const int wg = (warp - 2) >> 2, quarter = warp & 3, tid = 32 * quarter + lane;
-    const uint32_t s_addr = tmem + half * wg + ((uint32_t)(32 * quarter) << 16);
-    // each warp keeps its own copy of a column tile's -lse, so that no warp waits for another
-    float *ls = lse_s + (warp - 2) * 256;
-    const uint32_t ls_a = smem_u32(ls);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ -lse of the columns
+    // One warp fetches it for all: the loads of the next tile pass under this one.
     const int valid = pl.rows * pl.gb;  // columns that hold a (row, head) pair
     const bool one_hb = pl.nhb == 1;    // (saves the divisions)
     int ri[4], hi_[4];                  // row and head of this lane's four columns
 #pragma unroll
     for (int e = 0; e < 4; ++e) { ri[e] = (lane + 32 * e) / pl.gb; hi_[e] = (lane + 32 * e) % pl.gb; }
-    // The lse of this lane's columns of column tile c (-inf where there is no row), as loaded: nothing
-    // is computed with it before staged(), a tile later, so that the loads' latency passes under a tile
-    // (converted at once, each tile waited for them: 332 us where this takes TIME_PROMPT, 4 x 4096
-    // causal, 32 heads).
-    auto fetch_lse = [&](int c, float (&x)[4]) {
+    auto fetch = [&](int c, float (&x)[4]) {  // (-inf where there is no row)
       const int rb = one_hb ? c : c / pl.nhb, r0 = rb * pl.rows;
       const int h0 = hk * p.group + (one_hb ? 0 : (c - rb * pl.nhb) * pl.gb);
 #pragma unroll
@@ -328,19 +321,38 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
           x[e] = __ldg(kp.lse + (size_t)(h0 + hi_[e]) * p.total_q + sq.q0 + r0 + ri[e]);
       }
     };
-    // -lse log2(e), what the exponent adds; -inf takes the column out
-    auto staged = [](float l) { return l == -INFINITY ? -INFINITY : -l * kLog2e; };
+    float next[4];
+    bool ok = true;
+    int n = 0;
+    if (first < last) fetch(STREAM_K ? 0 : first, next);
+    for (int t = first; t < last; ++t) {
+      if (!live(t)) continue;
+      const int b = n & 1;
+      if (n >= 2) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(B_SE + b), ((n >> 1) - 1) & 1, abort_flag, p.err));
+        if (!ok) break;
+      }
+      if (!STREAM_K || n < 2) {  // (STREAM_K: the same columns for every tile)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)  // what the exponent adds; -inf takes the column out
+          lse_s[128 * b + lane + 32 * e] = next[e] == -INFINITY ? -INFINITY : -next[e] * kLog2e;
+        if (!STREAM_K && t + 1 < last) fetch(t + 1, next);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_SF + b));
+      ++n;
+    }
+  } else {
+    // ------------------------------------------------------------------ sums
+    const int wg = (warp - 3) >> 2, quarter = warp & 3, tid = 32 * quarter + lane;
+    const uint32_t s_addr = tmem + half * wg + ((uint32_t)(32 * quarter) << 16);
+    const uint32_t la = smem_u32(lse_s + 128 * wg);
+    const int valid = pl.rows * pl.gb;
+    const bool one_hb = pl.nhb == 1;
     const float sl2 = p.scale_log2;
     const uint64_t scale2 = f2pack(sl2, sl2);
     float total = 0.f;
     bool ok = true;
-    float next[4] = {0.f, 0.f, 0.f, 0.f};
-    if (STREAM_K || first + wg < last) fetch_lse(STREAM_K ? 0 : first + wg, next);
-    if (STREAM_K) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) ls[lane + 32 * e] = staged(next[e]);
-      __syncwarp();
-    }
     int lo = 0, hi = 0;  // the rows that see this thread's key
     if (!STREAM_K) visible_rows(min(t0 * 128 + tid, sq.kv_len - 1), off, sq.q_len, p.causal, p.window, lo, hi);
     int n = 0;  // score tiles so far, both warpgroups'
@@ -357,13 +369,6 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
       if (STREAM_K && kp.prev && j < sq.kv_len) before = kp.prev[at];  // (kernel may write in place)
       float sum = 0.f;
       if (is_live) {
-        const int buf = STREAM_K ? 0 : (n >> 1) & 1;
-        if (!STREAM_K) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) ls[128 * buf + lane + 32 * e] = staged(next[e]);
-          if (t + 2 < last) fetch_lse(t + 2, next);
-          __syncwarp();
-        }
         if (STREAM_K) visible_rows(min(j, sq.kv_len - 1), off, sq.q_len, p.causal, p.window, lo, hi);
         const int r0 = STREAM_K ? 0 : (one_hb ? t : t / pl.nhb) * pl.rows;
         const int clo = min(max(lo - r0, 0), pl.rows) * pl.gb, chi = min(max(hi - r0, 0), pl.rows) * pl.gb;
@@ -371,7 +376,6 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
         if (!ok) break;
         fence_after();
         uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
-        const uint32_t la = ls_a + 512 * buf;
         // Adds the W columns from c on, loaded into v; FULL: every key of the warp sees all of them.
         auto add = [&](auto width, auto whole, const uint32_t *v, int c) {
           constexpr int W = decltype(width)::value;
@@ -442,12 +446,11 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
     }
     if (!STREAM_K) {
       // the two warpgroups' sums of each key
-      __syncwarp();
-      if (wg == 1) ls[lane] = total;  // (this warp's own buffer: the others may still read theirs)
+      if (wg == 1) lse_s[256 + tid] = total;
       named_sync(1, 256);
       const int j = t0 * 128 + tid;
       if (wg == 0 && j < sq.kv_len && ok) {
-        const float w = total + lse_s[(4 + ((quarter + 2) & 3)) * 256 + lane];  // (warps 6 to 9: quarters 2, 3, 0, 1)
+        const float w = total + lse_s[256 + tid];
         const size_t at = (size_t)hk * p.total_kv + sq.k0 + j;
         if (parts) parts[(size_t)((int)blockIdx.z % pl.splits) * p.h_kv * p.total_kv + at] = w;
         else kp.weights[at] = kp.prev ? kp.prev[at] + w : w;
