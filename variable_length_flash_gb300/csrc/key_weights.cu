@@ -146,7 +146,7 @@ struct KwPlan {
 constexpr int kKwThreads = 352;  // producer, MMA issuer, lse warp, eight epilogue warps
 constexpr int kKwMisc = 1024;  // barriers, flags
 constexpr int kMaxSlots = 8;
-constexpr int kLseBytes = 3 * 128 * 4;  // two buffers in turn, and the second warpgroup's sums
+constexpr int kLseBytes = 5 * 128 * 4;  // four buffers in turn, and the second warpgroup's sums
 
 template <int D, bool BF16, bool STREAM_K>
 __global__ void __launch_bounds__(kKwThreads, D <= 128 ? 2 : 1)
@@ -200,7 +200,7 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
   uint8_t *misc = smem_raw + (sM - base);
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(misc + 512);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 516);
-  float *lse_s = reinterpret_cast<float *>(misc + kKwMisc);  // [score buffer][128], then [128]
+  float *lse_s = reinterpret_cast<float *>(misc + kKwMisc);  // [score tile mod 4][128], then [128]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -332,10 +332,11 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
         ok = __all_sync(0xffffffffu, mbar_wait(bar(B_SE + b), ((n >> 1) - 1) & 1, abort_flag, p.err));
         if (!ok) break;
       }
-      if (!STREAM_K || n < 2) {  // (STREAM_K: the same columns for every tile)
+      // Four buffers: this one's last reader has since released a later score tile.
+      if (!STREAM_K || n < 4) {  // (STREAM_K: the same columns for every tile)
 #pragma unroll
         for (int e = 0; e < 4; ++e)  // what the exponent adds; -inf takes the column out
-          lse_s[128 * b + lane + 32 * e] = next[e] == -INFINITY ? -INFINITY : -next[e] * kLog2e;
+          lse_s[128 * (n & 3) + lane + 32 * e] = next[e] == -INFINITY ? -INFINITY : -next[e] * kLog2e;
         if (!STREAM_K && t + 1 < last) fetch(t + 1, next);
       }
       __syncwarp();
@@ -346,7 +347,7 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
     // ------------------------------------------------------------------ sums
     const int wg = (warp - 3) >> 2, quarter = warp & 3, tid = 32 * quarter + lane;
     const uint32_t s_addr = tmem + half * wg + ((uint32_t)(32 * quarter) << 16);
-    const uint32_t la = smem_u32(lse_s + 128 * wg);
+    const uint32_t la0 = smem_u32(lse_s);
     const int valid = pl.rows * pl.gb;
     const bool one_hb = pl.nhb == 1;
     const float sl2 = p.scale_log2;
@@ -376,6 +377,12 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
         if (!ok) break;
         fence_after();
         uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
+        const uint32_t la = la0 + 512 * (n & 3);
+        auto release = [&]() {  // the score buffer may be overwritten
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_SE + wg));
+        };
         // Adds the W columns from c on, loaded into v; FULL: every key of the warp sees all of them.
         auto add = [&](auto width, auto whole, const uint32_t *v, int c) {
           constexpr int W = decltype(width)::value;
@@ -403,6 +410,7 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
           uint32_t v[16];
           tmem_ld16(s_addr, v);
           tmem_ld_wait();
+          release();
           add(std::integral_constant<int, 16>{}, std::false_type{}, v, 0);
         } else if (__all_sync(0xffffffffu, clo <= 0 && chi >= 128)) {
           // 32 columns are added while the next 32 load
@@ -418,6 +426,7 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
           tmem_ld32(s_addr + 96, v1);
           add(w32, std::true_type{}, v0, 64);
           tmem_ld_wait_for(v1);
+          release();
           add(w32, std::true_type{}, v1, 96);
         } else {
 #pragma unroll 1
@@ -429,11 +438,8 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
             tmem_ld_wait_for(v);
             add(w32, std::false_type{}, v, c);
           }
+          release();
         }
-        // the buffer may be overwritten
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_SE + wg));
         const float2 f0 = f2unpack(acc0), f1 = f2unpack(acc1);
         sum = (f0.x + f0.y) + (f1.x + f1.y);
         ++n;
@@ -446,11 +452,11 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
     }
     if (!STREAM_K) {
       // the two warpgroups' sums of each key
-      if (wg == 1) lse_s[256 + tid] = total;
+      if (wg == 1) lse_s[512 + tid] = total;
       named_sync(1, 256);
       const int j = t0 * 128 + tid;
       if (wg == 0 && j < sq.kv_len && ok) {
-        const float w = total + lse_s[256 + tid];
+        const float w = total + lse_s[512 + tid];
         const size_t at = (size_t)hk * p.total_kv + sq.k0 + j;
         if (parts) parts[(size_t)((int)blockIdx.z % pl.splits) * p.h_kv * p.total_kv + at] = w;
         else kp.weights[at] = kp.prev ? kp.prev[at] + w : w;
