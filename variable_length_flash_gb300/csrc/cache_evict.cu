@@ -94,18 +94,18 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
   const int per = (len + cluster - 1) / cluster, c0 = min(len, rank * per), cn = min(per, len - c0);
   const int ke = K > 0 ? K : (cn + nt - 1) / nt, wa = warp * 32 * ke + lane;
   const float *w = p.weights + (size_t)h * p.total_kv + k0 + c0;
-  auto make_key = [&](int e) {
+  auto raw = [&](int e) { return __ldg(w + min(wa + 32 * e, cn - 1)); };
+  auto make_key = [&](int e, float x) {
     const int j = wa + 32 * e, i = c0 + j;
-    const float x = __ldg(w + min(j, cn - 1));
     return j >= cn ? 0u : i < p.sink || i >= last ? kAlways : order_key(x);
   };
   uint32_t key[K > 0 ? K : 1];
+#pragma unroll
+  for (int e = 0; e < (K > 0 ? K : 1); ++e) key[e] = 0u;
   if (K > 0 && !all && cn > 0) {
+    // (all loads are sent before the first is used)
 #pragma unroll
-    for (int e = 0; e < K; ++e) key[e] = make_key(e);
-  } else {
-#pragma unroll
-    for (int e = 0; e < (K > 0 ? K : 1); ++e) key[e] = 0u;
+    for (int e = 0; e < K; ++e) key[e] = __float_as_uint(raw(e));
   }
   auto visit = [&](auto &&f) {  // f(key, e) for this lane's keys, in their order
     if constexpr (K > 0) {
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
       for (int e = 0; e < K; ++e) f(key[e], e);
     } else {
 #pragma unroll 4
-      for (int e = 0; e < ke; ++e) f(make_key(e), e);
+      for (int e = 0; e < ke; ++e) f(make_key(e, raw(e)), e);
     }
   };
   // first output row: what the sequences before this one keep (at most total_kv, an int)
@@ -158,6 +158,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
     for (int j = t; j < cn; j += nt) index[c0 + j] = c0 + j;
     if constexpr (COPY) copy_rows();
     return;
+  }
+  if constexpr (K > 0) {
+#pragma unroll
+    for (int e = 0; e < K; ++e) key[e] = make_key(e, __uint_as_float(key[e]));
   }
   // Twelve bits of the n-th largest key, two at a time, by counting the keys that reach each of three
   // thresholds: sign, exponent and three bits of mantissa leave a few percent of the keys.  (With
