@@ -621,15 +621,23 @@ def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, invers
     dt = _DTYPE.get(dtype)
     if dt is None:
         raise VlfError(VLF_ERR_INVALID, f"unsupported dtype {dtype}")
-    sq = _rope_rows(q, "q", dtype)
-    total, hq, d = q.shape
-    dev = q.get_device()
+    shape, stride, dev = q.shape, q.stride(), q.get_device()
+    if dev >= 0 and len(shape) == 3 and stride[2] == 1 and stride[1] == shape[2] and shape[0] > 1:
+        sq = stride[0]
+    else:
+        sq = _rope_rows(q, "q", dtype)
+    total, hq, d = shape
     hk, sk, sko, k_p, ko_p = 0, 0, 0, None, None
     if k is not None:
-        sk = _rope_rows(k, "k", dtype, total)
-        hk = k.shape[1]
-        if k.shape[2] != d:
-            raise VlfError(VLF_ERR_INVALID, "q and k must have the same head_dim")
+        shape, stride = k.shape, k.stride()
+        if (k.get_device() == dev and k.dtype is dtype and len(shape) == 3 and stride[2] == 1
+                and stride[1] == d and shape[0] == total and shape[2] == d and total > 1):
+            sk = stride[0]
+        else:
+            sk = _rope_rows(k, "k", dtype, total)
+            if shape[2] != d:
+                raise VlfError(VLF_ERR_INVALID, "q and k must have the same head_dim")
+        hk = shape[1]
         k_p = k.data_ptr()
     shape = positions.shape
     if not (positions.dtype is torch.int32 and inv_freq.dtype is torch.float32
@@ -687,10 +695,6 @@ def vlf_attn_varlen_fwd_prefix_workspace_size(num_seqs, total_q, max_seqlen_q, m
         num_sms))
 
 
-def _dense(t, dtype, dev):
-    return t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
-
-
 def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seqlens_kv,
                                max_seqlen_q, max_seqlen_kv=None, scale=None, causal=False, window=0,
                                out=None, lse=None, workspace=None, stream=None, flags=0):
@@ -701,9 +705,13 @@ def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seq
     here when not given."""
     dtype, dev = q.dtype, q.get_device()
     i32 = torch.int32
-    if not (dtype in _DTYPE and dev >= 0 and q.is_contiguous() and _dense(k, dtype, dev)
-            and _dense(v, dtype, dev) and _dense(k_prefix, dtype, dev) and _dense(v_prefix, dtype, dev)
-            and _dense(cu_seqlens_q, i32, dev) and _dense(cu_seqlens_kv, i32, dev)
+    if not (dtype in _DTYPE and dev >= 0 and q.is_contiguous()
+            and k.dtype is dtype and k.get_device() == dev and k.is_contiguous()
+            and v.dtype is dtype and v.get_device() == dev and v.is_contiguous()
+            and k_prefix.dtype is dtype and k_prefix.get_device() == dev and k_prefix.is_contiguous()
+            and v_prefix.dtype is dtype and v_prefix.get_device() == dev and v_prefix.is_contiguous()
+            and cu_seqlens_q.dtype is i32 and cu_seqlens_q.get_device() == dev and cu_seqlens_q.is_contiguous()
+            and cu_seqlens_kv.dtype is i32 and cu_seqlens_kv.get_device() == dev and cu_seqlens_kv.is_contiguous()
             and q.dim() == 3 and k.dim() == 3 and v.dim() == 3):
         _fwd_checks(q, k, v, cu_seqlens_q, cu_seqlens_kv)
         _req(k_prefix, "k_prefix", dtype), _req(v_prefix, "v_prefix", dtype)
@@ -771,9 +779,12 @@ def vlf_attn_key_weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, m
     output) may be ``prev``."""
     dtype, dev = q.dtype, q.get_device()
     i32, f32 = torch.int32, torch.float32
-    if not (dtype in _DTYPE and dev >= 0 and q.is_contiguous() and _dense(k, dtype, dev) and _dense(lse, f32, dev)
-            and _dense(cu_seqlens_q, i32, dev) and _dense(cu_seqlens_kv, i32, dev) and q.dim() == 3
-            and k.dim() == 3):
+    if not (dtype in _DTYPE and dev >= 0 and q.is_contiguous()
+            and k.dtype is dtype and k.get_device() == dev and k.is_contiguous()
+            and lse.dtype is f32 and lse.get_device() == dev and lse.is_contiguous()
+            and cu_seqlens_q.dtype is i32 and cu_seqlens_q.get_device() == dev and cu_seqlens_q.is_contiguous()
+            and cu_seqlens_kv.dtype is i32 and cu_seqlens_kv.get_device() == dev and cu_seqlens_kv.is_contiguous()
+            and q.dim() == 3 and k.dim() == 3):
         _fwd_checks(q, k, k, cu_seqlens_q, cu_seqlens_kv)
         _req(lse, "lse", f32)
         _same_device(q, k=k, lse=lse, cu_seqlens_q=cu_seqlens_q, cu_seqlens_kv=cu_seqlens_kv)
@@ -830,16 +841,20 @@ def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_
     ``total_out``: rows of the outputs, the sum of min(length, budget) where the caller knows the
     lengths (None: min(Tkv, n * budget), whose last rows may stay unwritten)."""
     dtype, dev = k.dtype, k.get_device()
-    if not (dtype in _DTYPE and dev >= 0 and k.is_contiguous() and _dense(v, dtype, dev)
-            and _dense(weights, torch.float32, dev) and _dense(cu_seqlens_kv, torch.int32, dev)):
+    if not (dtype in _DTYPE and dev >= 0 and k.is_contiguous() and v.dtype is dtype
+            and v.get_device() == dev and v.is_contiguous() and weights.dtype is torch.float32
+            and weights.get_device() == dev and weights.is_contiguous()
+            and cu_seqlens_kv.dtype is torch.int32 and cu_seqlens_kv.get_device() == dev
+            and cu_seqlens_kv.is_contiguous()):
         _req(k, "k"), _req(v, "v", dtype), _req(weights, "weights", torch.float32)
         _req(cu_seqlens_kv, "cu_seqlens_kv", torch.int32)
         _same_device(k, v=v, weights=weights, cu_seqlens_kv=cu_seqlens_kv)
         raise VlfError(VLF_ERR_INVALID, f"unsupported dtype {dtype}")
-    if k.dim() != 3 or v.dim() != 3 or k.shape[:2] != v.shape[:2] or cu_seqlens_kv.numel() < 1:
+    ks, vs = k.shape, v.shape
+    if len(ks) != 3 or len(vs) != 3 or ks[:2] != vs[:2] or cu_seqlens_kv.numel() < 1:
         raise VlfError(VLF_ERR_INVALID, "k, v must be [tokens, heads, head_dim]")
-    tk, h, dk = k.shape
-    dv = v.shape[2]
+    tk, h, dk = ks
+    dv = vs[2]
     if weights.shape != (h, tk):
         raise VlfError(VLF_ERR_INVALID, "weights must be [H_kv, total_kv]")
     if max_seqlen_kv is None:
@@ -848,23 +863,28 @@ def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_
     if total_out is None:
         total_out = min(tk, n * max(0, budget))
     total_out = int(total_out)
-    fresh, device = [], k.device
-
-    def output(t, name, shape, dt):
-        if t is None:
-            t = torch.empty(shape, dtype=dt, device=device)
-            fresh.append(t)
-        else:
-            _given(t, name, shape, dt), _same_device(k, **{name: t})
-        return t
-
-    k_out = output(k_out, "k_out", (total_out, h, dk), dtype)
-    v_out = output(v_out, "v_out", (total_out, h, dv), dtype)
-    weights_out = output(weights_out, "weights_out", (h, total_out), torch.float32)
-    index_out = output(index_out, "index_out", (h, total_out), torch.int32)
-    cu_out = output(cu_out, "cu_out", (n + 1,), torch.int32)
+    given = (k_out, v_out, weights_out, index_out, cu_out)
+    empty, device = torch.empty, k.device
+    if k_out is None:
+        k_out = empty((total_out, h, dk), dtype=dtype, device=device)
+    if v_out is None:
+        v_out = empty((total_out, h, dv), dtype=dtype, device=device)
+    if weights_out is None:
+        weights_out = empty((h, total_out), dtype=torch.float32, device=device)
+    if index_out is None:
+        index_out = empty((h, total_out), dtype=torch.int32, device=device)
+    if cu_out is None:
+        cu_out = empty((n + 1,), dtype=torch.int32, device=device)
+    outs = (k_out, v_out, weights_out, index_out, cu_out)
+    if not all(t is None for t in given):
+        for t, name, like in zip(given, ("k_out", "v_out", "weights_out", "index_out", "cu_out"),
+                                 ((total_out, h, dk, dtype), (total_out, h, dv, dtype),
+                                  (h, total_out, torch.float32), (h, total_out, torch.int32),
+                                  (n + 1, torch.int32))):
+            if t is not None:
+                _given(t, name, like[:-1], like[-1]), _same_device(k, **{name: t})
     if stream is not None:
-        _used_on(stream, *fresh)
+        _used_on(stream, *[t for t, g in zip(outs, given) if g is None])
     st = _lib.vlf_cache_evict(
         k.data_ptr(), v.data_ptr(), weights.data_ptr(), cu_seqlens_kv.data_ptr(), n, tk,
         int(max_seqlen_kv), h, dk, dv, _DTYPE[dtype], budget, int(sink), int(recent), total_out,
@@ -872,7 +892,7 @@ def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_
         cu_out.data_ptr(), _stream(stream, k))
     if st != VLF_OK:
         _check(st, "vlf_cache_evict")
-    return k_out, v_out, weights_out, index_out, cu_out
+    return outs
 
 
 __all__ = ["vlf_attn_varlen_fwd", "vlf_attn_varlen_bwd", "vlf_attn_varlen_bwd_workspace_size",
