@@ -511,7 +511,12 @@ KwPlan make_plan(int num_seqs, int max_q, int max_kv, int h_q, int h_kv, int d, 
   pl.run = 1;
   pl.splits = 1;
   if (pl.stream_k) {
-    pl.run = (int)std::min<long long>(std::max<long long>(ctas / (4 * room), 1), 16);
+    // One wave of CTAs where that takes at most 32 tiles each (a CTA's start and end cost about three
+    // tiles), else runs of at most 16, whose many waves even out ragged lengths.  Measured: 4 x 32
+    // rows against up to 32k keys 35 us in one wave (27 tiles), 38 with 6 or 13 tiles, 43 with 3 or 16;
+    // 64 decode rows against up to 8k keys 95 us with 13 tiles, 98 with 16 or more, 109 with 64.
+    const long long wave = (ctas + room - 1) / room;
+    pl.run = (int)(wave <= 32 ? wave : std::min(16ll, std::max(1ll, ctas / (8 * room))));
   } else if (ctas < room) {
     const long long cols = (long long)((max_q + pl.rows - 1) / pl.rows) * pl.nhb;
     pl.splits = (int)std::max<long long>(1, std::min({room / ctas, cols / 4, 65535ll / num_seqs, 32ll}));

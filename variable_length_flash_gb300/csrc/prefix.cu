@@ -840,8 +840,10 @@ bool tc_shape(int d_qk, int d_v, int dtype, unsigned flags) {
 // traffic of the parts (70 and 1 per 0.6 MB).
 //  * per sequence: row tiles walk the prefix and their own keys; cut into parts, four tiles each at
 //    least, where the row tiles leave slots empty;
-//  * shared: the batch's rows packed against the prefix, and the own keys apart; parts of what a slot
-//    gets (they start first, and the own keys' CTAs fill up behind them).  Taken where it saves a fifth.
+//  * shared: the batch's rows packed against the prefix, and the own keys apart; parts of twice what
+//    a slot gets: the own keys' CTAs fill up beside and behind them, and fewer parts cost less to write
+//    and merge (64 decode rows, 16k shared keys: 50 us; 53, 54, 58 us with runs of 1.5, 1 and 0.75
+//    times a slot's share, 54 and 58 us with 2.5 and 3).  Taken where it saves a fifth.
 PfxPlan make_plan(int num_seqs, int total_q, int max_q, int max_kv, int prefix, int h_q, int h_kv, int d, int num_sms) {
   constexpr long long kTile = 10, kQuad = 4, kMerge = 70;
   PfxPlan pl{};
@@ -868,7 +870,7 @@ PfxPlan make_plan(int num_seqs, int total_q, int max_q, int max_kv, int prefix, 
   const long long cut = std::max(1ll, std::min({slots / own, all / 4, 64ll}));
   const long long whole = std::max(own * all / slots, all) * tile, in_parts = up(all, cut) * tile + merge(cut);
   const long long work = pre * pl.np * kTile + own * no * tile;  // of the shared cut
-  const long long run = std::max(4 * kTile, work / slots);
+  const long long run = std::max(4 * kTile, 2 * work / slots);
   pl.parts_own = cut > 1 && in_parts < whole ? (int)cut : 1;
   const int parts_pre = (int)std::min(up(pl.np * kTile, run), 48ll);
   const int parts_own = (int)std::max(1ll, std::min(up(no * tile, run), 16ll));
