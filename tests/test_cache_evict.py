@@ -155,6 +155,20 @@ def test_default_rows_and_errors_on_the_device():
     assert vlf.vlf_check_error() == 0
 
 
+@pytest.mark.gpu
+def test_a_budget_without_end_keeps_everything():
+    k = torch.randn(50, 2, 64, device="cuda").to(BF)
+    w = torch.rand(2, 50, device="cuda")
+    cu = cu_of([20, 30]).cuda()
+    ko, vo, wo, io, co = vlf.vlf_cache_evict(k, k, w, cu, 2 ** 40, sink=4)
+    assert torch.equal(ko, k) and torch.equal(wo, w) and co.tolist() == [0, 20, 50]
+    assert io[1].tolist() == list(range(20)) + list(range(30))
+    with pytest.raises(vlf.VlfError):
+        vlf.vlf_cache_evict(k, k, w, cu, 2 ** 40, sink=2 ** 33)
+    with pytest.raises(vlf.VlfError):
+        vlf.vlf_cache_evict(k, k, w, cu, 10, max_seqlen_kv=2 ** 32 + 30)
+
+
 def _raw(**kw):
     a = dict(k=16, v=16, w=16, cu=16, n=1, tk=8, mk=8, h=2, dk=64, dv=64, dtype=1, budget=4, sink=1, recent=1,
              to=4, ko=16, vo=16, wo=16, io=16, co=16)

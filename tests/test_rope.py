@@ -132,6 +132,19 @@ def test_gradients_match_formula_and_differences():
 
 
 @pytest.mark.gpu
+def test_gradients_of_gradients():
+    """The gradient is a rotation back, so a second derivative through it is the rotation again."""
+    q, k, pos, f, sec = make(9, 2, 1, 32, 32, torch.float32, 1, 300, seed=4)
+    q.requires_grad_()
+    g = torch.randn_like(q).requires_grad_()
+    y, _ = vlf.rotary_embedding(q, k, pos, f)
+    (dq,) = torch.autograd.grad((y * g).sum(), q, create_graph=True)
+    v = torch.randn_like(q)
+    (dg,) = torch.autograd.grad((dq * v).sum(), g)
+    check(dg, v, pos, f, sec, 32, False, False)
+
+
+@pytest.mark.gpu
 def test_gradient_through_strided_slices_and_half_types():
     qkv = torch.randn(40, 6, 64, device="cuda").to(torch.bfloat16).requires_grad_()
     pos = torch.arange(40, dtype=torch.int32, device="cuda")

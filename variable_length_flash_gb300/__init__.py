@@ -566,6 +566,14 @@ def _given(t, name, shape, dtype):
     return t
 
 
+def _c_int(x, name):
+    """x as the C int an entry point takes (ctypes would cut off what does not fit)."""
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise VlfError(VLF_ERR_INVALID, f"{name} = {x} is out of range")
+    return x
+
+
 _WORKSPACES = {}  # (entry point, shape, device) -> bytes of workspace
 
 
@@ -599,7 +607,7 @@ _SECTIONS = {}  # section counts -> the C array of them
 
 
 def _sections(sections):
-    key = tuple(sections)
+    key = tuple(map(int, sections))
     arr = _SECTIONS.get(key)
     if arr is None:
         arr = (ctypes.c_int * len(key))(*key)
@@ -740,7 +748,9 @@ def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seq
         fresh.append(lse)
     else:
         _given(lse, "lse", (hq, tq), torch.float32), _same_device(q, lse=lse)
-    mq, mk, dt, flags = int(max_seqlen_q), int(max_seqlen_kv), _DTYPE[dtype], int(flags)
+    mq, mk = _c_int(max_seqlen_q, "max_seqlen_q"), _c_int(max_seqlen_kv, "max_seqlen_kv")
+    window = _c_int(window or 0, "window")
+    dt, flags = _DTYPE[dtype], int(flags)
     need = _workspace_size(_lib.vlf_attn_varlen_fwd_prefix_workspace_size,
                            ("prefix", nseq, tq, mq, mk, n, hq, hkv, dqk, dv, dt, flags, dev))
     ws_p, ws_n = None, 0
@@ -756,7 +766,7 @@ def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seq
     st = _lib.vlf_attn_varlen_fwd_prefix(
         q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), n, k.data_ptr(), v.data_ptr(),
         cu_seqlens_q.data_ptr(), cu_seqlens_kv.data_ptr(), nseq, tq, tk, mq, mk, hq, hkv, dqk, dv, dt,
-        float(scale) if scale else 0.0, 1 if causal else 0, int(window) if window else 0,
+        float(scale) if scale else 0.0, 1 if causal else 0, window,
         out.data_ptr(), lse.data_ptr(), ws_p, ws_n, _stream(stream, q), flags)
     if st != VLF_OK:
         _check(st, "vlf_attn_varlen_fwd_prefix")
@@ -809,7 +819,9 @@ def vlf_attn_key_weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, m
         fresh.append(weights)
     else:
         _given(weights, "weights", (hkv, tk), f32), _same_device(q, weights=weights)
-    mq, mk, dt, flags = int(max_seqlen_q), int(max_seqlen_kv), _DTYPE[dtype], int(flags)
+    mq, mk = _c_int(max_seqlen_q, "max_seqlen_q"), _c_int(max_seqlen_kv, "max_seqlen_kv")
+    window = _c_int(window or 0, "window")
+    dt, flags = _DTYPE[dtype], int(flags)
     need = _workspace_size(_lib.vlf_attn_key_weights_workspace_size,
                            ("weights", nseq, tk, mq, mk, hq, hkv, d, dt, flags, dev))
     ws_p, ws_n = None, 0
@@ -825,7 +837,7 @@ def vlf_attn_key_weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, m
     st = _lib.vlf_attn_key_weights(
         q.data_ptr(), k.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_kv.data_ptr(),
         nseq, tq, tk, mq, mk, hq, hkv, d, dt, float(scale) if scale else 0.0, 1 if causal else 0,
-        int(window) if window else 0, prev_p, weights.data_ptr(), ws_p, ws_n, _stream(stream, q), flags)
+        window, prev_p, weights.data_ptr(), ws_p, ws_n, _stream(stream, q), flags)
     if st != VLF_OK:
         _check(st, "vlf_attn_key_weights")
     return weights
@@ -859,10 +871,12 @@ def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_
         raise VlfError(VLF_ERR_INVALID, "weights must be [H_kv, total_kv]")
     if max_seqlen_kv is None:
         max_seqlen_kv = _max_len(cu_seqlens_kv)
-    n, budget = cu_seqlens_kv.numel() - 1, int(budget)
-    if total_out is None:
-        total_out = min(tk, n * max(0, budget))
-    total_out = int(total_out)
+    n, budget, sink, recent = cu_seqlens_kv.numel() - 1, int(budget), int(sink), int(recent)
+    if sink < 0 or recent < 0 or sink + recent > budget:
+        raise VlfError(VLF_ERR_INVALID, "sink and recent must be at least 0, their sum at most budget")
+    budget = min(budget, 0x7fffffff)  # (more than any sequence has)
+    sink, recent = _c_int(sink, "sink"), _c_int(recent, "recent")
+    total_out = min(tk, n * budget) if total_out is None else _c_int(total_out, "total_out")
     given = (k_out, v_out, weights_out, index_out, cu_out)
     empty, device = torch.empty, k.device
     if k_out is None:
@@ -887,7 +901,7 @@ def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_
         _used_on(stream, *[t for t, g in zip(outs, given) if g is None])
     st = _lib.vlf_cache_evict(
         k.data_ptr(), v.data_ptr(), weights.data_ptr(), cu_seqlens_kv.data_ptr(), n, tk,
-        int(max_seqlen_kv), h, dk, dv, _DTYPE[dtype], budget, int(sink), int(recent), total_out,
+        _c_int(max_seqlen_kv, "max_seqlen_kv"), h, dk, dv, _DTYPE[dtype], budget, sink, recent, total_out,
         k_out.data_ptr(), v_out.data_ptr(), weights_out.data_ptr(), index_out.data_ptr(),
         cu_out.data_ptr(), _stream(stream, k))
     if st != VLF_OK:

@@ -394,7 +394,10 @@ cudaError_t cache_evict(const EvictParams &p, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
   cudaError_t e = cudaLaunchKernelExC(&cfg, sel, args);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess) {
+    cudaGetLastError();  // (reported here: not left behind for a later check)
+    return e;
+  }
   count_launch();
   if (copy || most == 0 || p.total_out == 0) return cudaSuccess;
   const int b = whole ? 16 : es;

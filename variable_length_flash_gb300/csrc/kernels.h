@@ -98,6 +98,14 @@ void count_launch(int n = 1);
 // which small problems would pay on every launch.
 cudaError_t set_smem_once(const void *kern, int bytes);
 
+// A launch that reports its own error and leaves none behind for a later check.
+inline cudaError_t launch_plain(const void *kern, dim3 grid, int threads, int smem, cudaStream_t st, void **args) {
+  const cudaError_t e = cudaLaunchKernel(kern, grid, dim3(threads), args, (size_t)smem, st);
+  if (e != cudaSuccess) cudaGetLastError();
+  else count_launch();
+  return e;
+}
+
 // Records ev[i] on st when ev is not NULL.
 inline cudaError_t mark(const cudaEvent_t *ev, int i, cudaStream_t st) {
   return ev ? cudaEventRecord(ev[i], st) : cudaSuccess;

@@ -95,10 +95,9 @@ cudaError_t launch_simt(const KeyWeightParams &kp, cudaStream_t st) {
   cudaError_t e = set_smem_once(reinterpret_cast<const void *>(simt_key_weights_kernel<T>), smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((p.max_kv + kKeys - 1) / kKeys), p.h_kv, p.num_seqs);
-  simt_key_weights_kernel<T><<<grid, kThreads, smem, st>>>(kp);
-  e = cudaGetLastError();
-  if (e == cudaSuccess) count_launch();
-  return e;
+  KeyWeightParams a = kp;
+  void *args[1] = {&a};
+  return launch_plain(reinterpret_cast<const void *>(simt_key_weights_kernel<T>), grid, kThreads, smem, st, args);
 }
 
 cudaError_t simt_key_weights(const KeyWeightParams &kp, cudaStream_t st) {
@@ -550,9 +549,12 @@ cudaError_t launch_tc(const KeyWeightParams &kp, const KwPlan &pl, float *parts,
   count_launch();
   if (pl.splits > 1) {
     const size_t n = (size_t)p.h_kv * p.total_kv;
-    key_weights_join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(parts, pl.splits, n, kp.prev, kp.weights);
-    e = cudaGetLastError();
-    if (e == cudaSuccess) count_launch();
+    if ((n + 255) / 256 > 0x7fffffffull) return cudaErrorInvalidValue;
+    const float *in = parts;
+    int splits = pl.splits;
+    size_t all = n;
+    void *jargs[5] = {&in, &splits, &all, &a.prev, &a.weights};
+    e = launch_plain((const void *)key_weights_join_kernel, dim3((unsigned)((n + 255) / 256)), 256, 0, st, jargs);
   }
   return e;
 }

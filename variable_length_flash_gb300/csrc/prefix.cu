@@ -148,10 +148,9 @@ cudaError_t launch_simt(const PrefixParams &pp, cudaStream_t st) {
   cudaError_t e = set_smem_once(reinterpret_cast<const void *>(simt_prefix_kernel<T, DVPT>), smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((p.max_q + kRows - 1) / kRows), p.h_q, p.num_seqs);
-  simt_prefix_kernel<T, DVPT><<<grid, kThreads, smem, st>>>(pp);
-  e = cudaGetLastError();
-  if (e == cudaSuccess) count_launch();
-  return e;
+  PrefixParams a = pp;
+  void *args[1] = {&a};
+  return launch_plain(reinterpret_cast<const void *>(simt_prefix_kernel<T, DVPT>), grid, kThreads, smem, st, args);
 }
 
 template <typename T>

@@ -200,17 +200,10 @@ cudaError_t launch(RopeParams p, cudaStream_t st) {
   // up to eight blocks per SM, each with the same number of runs
   const long long y = phases(p.hpt), turns = (runs * y + 152 * 8 - 1) / (152 * 8);
   const dim3 grid((unsigned)((runs + turns - 1) / turns), (unsigned)y);
-  if (vec) {
-    if (p.interleaved) rope_kernel<T, VW, true><<<grid, 256, 0, st>>>(p);
-    else rope_kernel<T, VW, false><<<grid, 256, 0, st>>>(p);
-  } else {
-    // (one pair a thread: neighbours sit at 2u and 2u + 1)
-    if (p.interleaved) rope_kernel<T, 1, true><<<grid, 256, 0, st>>>(p);
-    else rope_kernel<T, 1, false><<<grid, 256, 0, st>>>(p);
-  }
-  const cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) count_launch();
-  return e;
+  const void *kern = vec ? (p.interleaved ? (const void *)rope_kernel<T, VW, true> : (const void *)rope_kernel<T, VW, false>)
+                         : (p.interleaved ? (const void *)rope_kernel<T, 1, true> : (const void *)rope_kernel<T, 1, false>);
+  void *args[1] = {&p};
+  return launch_plain(kern, grid, 256, 0, st, args);
 }
 
 }  // namespace

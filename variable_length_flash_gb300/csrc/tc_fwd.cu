@@ -833,7 +833,9 @@ cudaError_t launch_dependent(const void *kern, dim3 grid, int threads, int smem,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelExC(&cfg, kern, args);
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, kern, args);
+  if (e != cudaSuccess) cudaGetLastError();  // (reported here: not left behind for a later check)
+  return e;
 }
 
 namespace {

@@ -146,19 +146,18 @@ def _token_dense(t):
 
 class _Rotary(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, positions, inv_freq, sections, interleaved):
+    def forward(ctx, q, k, positions, inv_freq, sections, interleaved, inverse):
         ctx.save_for_backward(positions, inv_freq)
-        ctx.args = (sections, interleaved)
-        return vlf_rope(_token_dense(q), _token_dense(k), positions, inv_freq, sections, interleaved)
+        ctx.args = (sections, interleaved, inverse)
+        return vlf_rope(_token_dense(q), _token_dense(k), positions, inv_freq, sections, interleaved, inverse)
 
     @staticmethod
     def backward(ctx, dq, dk):
         positions, inv_freq = ctx.saved_tensors
-        sections, interleaved = ctx.args
-        # the rotation is orthogonal: its gradient is the rotation back
-        dq, dk = vlf_rope(_token_dense(dq), _token_dense(dk), positions, inv_freq, sections,
-                          interleaved, inverse=True)
-        return dq, dk, None, None, None, None
+        sections, interleaved, inverse = ctx.args
+        # the rotation is orthogonal: its gradient is the rotation back (and so differentiable itself)
+        dq, dk = _Rotary.apply(dq, dk, positions, inv_freq, sections, interleaved, not inverse)
+        return dq, dk, None, None, None, None, None
 
 
 def rotary_embedding(q, k, positions, inv_freq, sections=None, interleaved=False):
@@ -170,7 +169,7 @@ def rotary_embedding(q, k, positions, inv_freq, sections=None, interleaved=False
     if q.dim() != 3 or k.dim() != 3:
         raise VlfError(VLF_ERR_INVALID, "q and k must be [tokens, heads, head_dim]")
     return _Rotary.apply(q, k, positions.contiguous(), inv_freq.contiguous(),
-                         None if sections is None else tuple(sections), bool(interleaved))
+                         None if sections is None else tuple(sections), bool(interleaved), False)
 
 
 def _refuse_flash_extras(dropout_p, alibi_slopes, return_attn_probs):
