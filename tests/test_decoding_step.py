@@ -82,6 +82,53 @@ def test_a_serving_loop(axes, d, hq, hkv):
         assert vlf.vlf_check_error() == 0
 
 
+def test_native_calls_leave_what_is_not_theirs():
+    """The native side of the calls returns None for anything but plain CUDA tensors and plain numbers,
+    and counts arguments; the Python functions then say what was wrong."""
+    x, n = torch.zeros(4, 2, 8), torch.zeros(3, dtype=torch.int32)
+    calls = vlf._calls
+    assert calls.rope(x, x, n, torch.zeros(4), None, False, False) is None
+    assert calls.rope(None, 3, "x", [], {}, 1, 2) is None and calls.rope(x) is None and calls.rope() is None
+    assert calls.prefix(x, x, x, x, x, n, n, 1, 1, None, True, 0, 0) is None
+    assert calls.weights(x, x, x, n, n, 1, 1, None, True, 0, None, 0) is None
+    assert calls.evict(x, x, x, n, 2 ** 70, 0, 0, 4, 4) is None
+    for f, args in ((vlf.vlf_rope, (x, x, n, torch.zeros(4))),
+                    (vlf.vlf_attn_varlen_fwd_prefix, (x, x, x, x, x, n, n, 1, 1)),
+                    (vlf.vlf_attn_key_weights, (x, x, x, n, n, 1, 1)), (vlf.vlf_cache_evict, (x, x, x, n, 4))):
+        with pytest.raises(vlf.VlfError, match="CUDA"):
+            f(*args)
+
+
+@pytest.mark.gpu
+def test_native_and_python_calls_agree():
+    """The same call through the native side and through Python (which a stream of the caller's takes)."""
+    g = torch.Generator().manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g).to(BF).cuda()  # noqa: E731
+    t = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    here = torch.cuda.current_stream()
+    qkv, pos, f = r(9, 12, 64), t(*range(9)), torch.rand(32, generator=g).cuda()
+    q, k, kp, vp, kc, vc = r(5, 8, 64), r(90, 2, 64), r(700, 2, 64), r(700, 2, 64), r(90, 2, 64), r(90, 2, 64)
+    cu_q, cu_kv, w = t(0, 1, 5), t(0, 40, 90), torch.rand(2, 90, generator=g).cuda()
+    lse = torch.full((8, 5), 3.0, device="cuda")
+    calls = [(vlf.vlf_rope, (qkv[:, :8], qkv[:, 8:10], pos, f), dict(sections=[32], interleaved=True)),
+             (vlf.vlf_attn_varlen_fwd_prefix, (q, kp, vp, kc, vc, cu_q, cu_kv, 4, 50), dict(causal=True, window=600, scale=0.2)),
+             (vlf.vlf_attn_key_weights, (q, k, lse, cu_q, cu_kv, 4, 50), dict(causal=True, prev=w)),
+             (vlf.vlf_cache_evict, (kc, vc, w, cu_kv, 20), dict(sink=2, recent=3, max_seqlen_kv=50, total_out=40))]
+    for fn, args, kw in calls:
+        native, python = fn(*args, **kw), fn(*args, **kw, stream=here)
+        native, python = ([x] if torch.is_tensor(x) else list(x) for x in (native, python))
+        assert len(native) == len(python)
+        for a, b in zip(native, python):
+            assert a.shape == b.shape and a.dtype == b.dtype and a.is_contiguous() and torch.equal(a, b)
+    # refused by the library: the same error either way
+    for kw in (dict(), dict(stream=here)):
+        with pytest.raises(vlf.VlfError):
+            vlf.vlf_cache_evict(kc, vc, w, cu_kv, 4, sink=3, recent=3, max_seqlen_kv=50, total_out=8, **kw)
+        with pytest.raises(vlf.VlfError):
+            vlf.vlf_rope(qkv[:, 1:8], qkv[:, 8:10], pos, torch.zeros(40, device="cuda"), **kw)
+    assert vlf.vlf_check_error() == 0
+
+
 @pytest.mark.gpu
 def test_prefix_keys_receive_the_rest():
     """Own and prefix keys' weights from the same lse: each (row, head)'s sum to 1."""

@@ -133,7 +133,21 @@ def _load():
     return lib
 
 
+def _load_calls(lib):
+    """The native side of the decoding entry points' calls (csrc/calls.cpp), bound to the library."""
+    try:
+        from . import _calls
+    except ImportError as e:
+        raise ImportError("variable_length_flash_gb300/_calls.so is not built for this torch; run "
+                          "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+    _calls.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.vlf_rope, lib.vlf_attn_varlen_fwd_prefix, lib.vlf_attn_varlen_fwd_prefix_workspace_size,
+        lib.vlf_attn_key_weights, lib.vlf_attn_key_weights_workspace_size, lib.vlf_cache_evict)])
+    return _calls
+
+
 _lib = _load()
+_calls = _load_calls(_lib)
 _fwd_ex = _lib.vlf_attn_varlen_fwd_ex  # (looked up once: the attribute lookup costs per call)
 
 
@@ -541,9 +555,11 @@ def vlf_attn_varlen_bwd_noalloc(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlen
 
 
 # ------------------------------------------------------------------ decoding on a bounded cache
-# Host time counts in a decode step, whose kernels take microseconds: each call first tests all
-# its conditions in one expression (a tensor attribute costs ~0.1 us), and only where that fails
-# takes the checks that say which one it was.
+# Host time counts in a decode step, whose kernels take microseconds: the common case (plain CUDA
+# tensors, outputs allocated here, the current stream) is one native call (csrc/calls.cpp), which
+# returns None for everything else and for what it refuses.  What follows it tests its conditions in
+# one expression (a tensor attribute costs ~0.1 us), and only where that fails takes the checks that
+# say which one it was.
 def _same_device(like, **tensors):
     for name, t in tensors.items():
         if t is not None and t.device != like.device:
@@ -625,6 +641,10 @@ def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, invers
     from rot on pass through.  ``inverse`` turns back, which is also the gradient.  q and k may be
     slices of a packed projection (their tokens may be strided); ``q_out`` / ``k_out`` may be q / k
     themselves.  Returns (q_out, k_out)."""
+    if q_out is None and k_out is None and stream is None:
+        done = _calls.rope(q, k, positions, inv_freq, sections, interleaved, inverse)
+        if done is not None:
+            return done
     dtype = q.dtype
     dt = _DTYPE.get(dtype)
     if dt is None:
@@ -711,6 +731,11 @@ def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seq
     the concatenated keys, with the prefix read once.  Returns out [Tq, Hq, Dv] and lse fp32
     [Hq, Tq].  ``workspace``: at least vlf_attn_varlen_fwd_prefix_workspace_size bytes, allocated
     here when not given."""
+    if out is None and lse is None and workspace is None and stream is None:
+        done = _calls.prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q,
+                             max_seqlen_kv, scale, causal, window, flags)
+        if done is not None:
+            return done
     dtype, dev = q.dtype, q.get_device()
     i32 = torch.int32
     if not (dtype in _DTYPE and dev >= 0 and q.is_contiguous()
@@ -787,6 +812,11 @@ def vlf_attn_key_weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, m
     the heads of its group of exp(logit - lse), plus ``prev`` (fp32 [Hkv, Tkv], or None).  ``lse``
     [Hq, Tq] comes from the forward with the same scale, causal and window.  ``weights`` (the
     output) may be ``prev``."""
+    if weights is None and workspace is None and stream is None:
+        done = _calls.weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, max_seqlen_kv,
+                              scale, causal, window, prev, flags)
+        if done is not None:
+            return done
     dtype, dev = q.dtype, q.get_device()
     i32, f32 = torch.int32, torch.float32
     if not (dtype in _DTYPE and dev >= 0 and q.is_contiguous()
@@ -852,6 +882,11 @@ def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_
     index int32 [Hkv, total_out] (the sequence-local key each row came from) and cu int32 [n + 1].
     ``total_out``: rows of the outputs, the sum of min(length, budget) where the caller knows the
     lengths (None: min(Tkv, n * budget), whose last rows may stay unwritten)."""
+    if stream is None and k_out is None and v_out is None and weights_out is None and index_out is None \
+            and cu_out is None:
+        done = _calls.evict(k, v, weights, cu_seqlens_kv, budget, sink, recent, max_seqlen_kv, total_out)
+        if done is not None:
+            return done
     dtype, dev = k.dtype, k.get_device()
     if not (dtype in _DTYPE and dev >= 0 and k.is_contiguous() and v.dtype is dtype
             and v.get_device() == dev and v.is_contiguous() and weights.dtype is torch.float32

@@ -1,4 +1,5 @@
-"""Builds libvlf.so in-tree from csrc/*.cu with nvcc for sm_103a (no cmake, parallel TUs)."""
+"""Builds, in-tree and without cmake, libvlf.so from csrc/*.cu with nvcc for sm_103a (parallel TUs) and
+_calls.so, the native side of the decoding entry points' Python calls, from csrc/calls.cpp with g++."""
 from __future__ import annotations
 
 import glob
@@ -12,6 +13,8 @@ CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libvlf.so")
+CALLS_SRC = os.path.join(CSRC, "calls.cpp")
+CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -23,11 +26,32 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _stale(sources, headers) -> bool:
-    if not os.path.exists(LIB):
+def _stale(sources, headers, target=LIB) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
+    t = os.path.getmtime(target)
     return any(os.path.getmtime(f) > t for f in sources + headers)
+
+
+def _build_calls() -> str:
+    """Compile csrc/calls.cpp against the torch that is installed."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), os.path.join(ROOT, "include"), sysconfig.get_paths()["include"]]
+    tmp = CALLS + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fno-strict-aliasing",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-isystem{i}" for i in inc],
+           CALLS_SRC, "-o", tmp, "-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -35,7 +59,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     headers = sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
                      glob.glob(os.path.join(ROOT, "include", "*.h")))
+    calls = force or _stale([CALLS_SRC], [os.path.join(ROOT, "include", "vlf.h")], CALLS)
     if not force and not _stale(sources, headers):
+        if calls:
+            _build_calls()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -50,8 +77,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(8, len(sources))) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, len(sources) + 1)) as ex:
+        pending = ex.submit(_build_calls) if calls else None
         objs = list(ex.map(compile_one, sources))
+        if pending:
+            pending.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
