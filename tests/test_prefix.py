@@ -136,6 +136,21 @@ def test_other_sequences_never_reach_a_row(q_lens, kv_lens):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("prefix,q_lens,kv_lens", [(200, [1, 1], [70, 33]), (5000, [1, 3], [40, 90]), (300, [80, 150], [90, 201])])
+def test_a_nan_key_reaches_its_rows(prefix, q_lens, kv_lens):
+    """However the keys are cut: a visible NaN makes the row and its log-sum-exp NaN, a masked one does not."""
+    x = make(prefix, q_lens, kv_lens, 8, 2, 64, 64, BF, seed=3)
+    for name, rows in (("k_prefix", slice(None)), ("k", slice(q_lens[0], None))):
+        y = dict(x, **{name: x[name].clone()})
+        y[name][17 if name == "k_prefix" else kv_lens[0] + 1] = float("nan")
+        for flags in (0, vlf.VLF_FLAG_FORCE_SIMT):
+            out, lse = vlf.vlf_attn_varlen_fwd_prefix(**y, causal=True, flags=flags)
+            assert out[rows].isnan().all() and lse[:, rows].isnan().all()
+            if name == "k":
+                assert out[:q_lens[0]].isfinite().all() and lse[:, :q_lens[0]].isfinite().all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("sigma", [0.02, 6.0])
 def test_flat_and_sharp_weights(sigma):
     x = make(900, [1, 40], [100, 90], 8, 2, 128, 128, HF, seed=8, sigma=sigma)

@@ -134,11 +134,11 @@ __global__ void __launch_bounds__(kThreads) simt_prefix_kernel(const PrefixParam
   if (!row_ok) return;
   const size_t grow = (size_t)sq.q0 + i;
   T *out = static_cast<T *>(p.out) + (grow * p.h_q + h) * dv;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int u = 0; u < DVPT; ++u)
     if (sub + 8 * u < dv) out[sub + 8 * u] = from_f32<T>(o[u] * inv);
-  if (p.lse && sub == 0) p.lse[(size_t)h * p.total_q + grow] = l > 0.f ? m + logf(l) : -INFINITY;
+  if (p.lse && sub == 0) p.lse[(size_t)h * p.total_q + grow] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 template <typename T, int DVPT>
@@ -180,7 +180,8 @@ cudaError_t simt_prefix(const PrefixParams &pp, cudaStream_t st) {
 //    log-sum-exps.  Per sequence: each row tile walks prefix and own keys in one go (cut into parts
 //    only where the row tiles are too few to fill the GPU).  Shared pays where a sequence's rows fill
 //    less than a tile (decode steps): make_plan below.
-//  * Quarter tiles (quad) where a sequence's rows fill at most a quarter of a row tile (decode steps).
+//  * Quarter tiles (quad) where the rows -- a sequence's, or all of a small batch's against the prefix --
+//    fill at most a quarter of a row tile (decode steps).
 //    A softmax warp can only read its own 32 TMEM lanes, so with one row tile a single warp would walk
 //    all 64 columns of each key tile and set the pace.  The rows are loaded four times instead, once
 //    per quarter, and quarter w takes keys 16 w ... 16 w + 15 of each tile (its other weights are zero):
@@ -200,8 +201,8 @@ constexpr float kMoveMax = 8.0f;  // the reference max moves once a row's max ha
 struct PfxPlan {
   int shared;
   int gb, nhb;         // heads per row tile, row tiles per kv head's group
-  int rows;            // query rows per row tile
-  int quad, rows_own;  // quarter tiles for the sequences' own CTAs; query rows of their row tiles
+  int quad_pre, rows;  // shared prefix part: quarter tiles, query rows per row tile
+  int quad, rows_own;  // the sequences' own CTAs: the same
   int np;              // prefix key tiles
   int heads;           // h_kv * nhb
   int rb_pre, rb_own;  // row blocks: of the batch (shared prefix part), of a sequence
@@ -271,7 +272,7 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
     slot = pl.parts_pre + part;
   }
   const int hk = hd / pl.nhb, h0 = hk * p.group + hd % pl.nhb * pl.gb;
-  const bool quad = !pre && pl.quad;
+  const bool quad = pre ? pl.quad_pre : pl.quad;
   const int rows = pre ? pl.rows : pl.rows_own;
   const int row0 = pre ? rb * rows : sq.q0 + rb * rows;                    // packed row of tile row 0
   const int nrows = min(rows, (pre ? p.total_q : sq.q0 + sq.q_len) - row0);  // query rows of the tile
@@ -669,7 +670,7 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
         ls = fmaf(f[x], q[1], ls);
         lfs = fmaf(f[x], q[2], lfs);
       }
-      const float inv = ls > 0.f ? 1.f / ls : 0.f;
+      const float inv = ls == 0.f ? 0.f : 1.f / ls;  // (a NaN logit leaves a NaN sum, and a NaN row)
       const bool wr = ok && jt < nrows;
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
@@ -709,14 +710,14 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
         }
       }
       if (wr && (tid & 3) == 0) {
-        const float lse = lfs > 0.f ? (m + lg2(lfs)) * kLn2f : -INFINITY;
+        const float lse = lfs == 0.f ? -INFINITY : (m + lg2(lfs)) * kLn2f;
         if (SPLIT) lse_part[(size_t)slot * p.total_q * p.h_q + at] = lse;
         else if (p.lse) p.lse[(size_t)(h0 + jr % pl.gb) * p.total_q + row0 + jt] = lse;
       }
     } else if (ok) {
       fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse = lf > 0.f ? (m_ref + lg2(lf)) * kLn2f : -INFINITY;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float lse = lf == 0.f ? -INFINITY : (m_ref + lg2(lf)) * kLn2f;
       const size_t at = (size_t)grow * p.h_q + head;  // (row, head)
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
@@ -804,7 +805,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const Params p, int p
       const int s = s0 + i * PER + sub;
       const float wa = __shfl_sync(0xffffffffu, e0, s & 31), wb = __shfl_sync(0xffffffffu, e1, s & 31);
       const float wgt = s < 32 ? wa : wb;
-      if (s >= parts || !(wgt > 0.f)) continue;
+      if (s >= parts || wgt == 0.f) continue;  // (a NaN weight stays)
       acc.x = fmaf(wgt, x[i].x, acc.x);
       acc.y = fmaf(wgt, x[i].y, acc.y);
       acc.z = fmaf(wgt, x[i].z, acc.z);
@@ -819,13 +820,13 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const Params p, int p
     acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
     acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   if (c < NL && sub == 0) {
     T y[4] = {from_f32<T>(acc.x * inv), from_f32<T>(acc.y * inv), from_f32<T>(acc.z * inv), from_f32<T>(acc.w * inv)};
     *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + w * D + 4 * c) = *reinterpret_cast<uint2 *>(y);
   }
   if (lane == 0 && p.lse)
-    p.lse[(w % p.h_q) * p.total_q + w / p.h_q] = m == -INFINITY ? -INFINITY : m + logf(sum);
+    p.lse[(w % p.h_q) * p.total_q + w / p.h_q] = sum == 0.f ? -INFINITY : mm + logf(sum);
 }
 
 bool tc_shape(int d_qk, int d_v, int dtype, unsigned flags) {
@@ -836,23 +837,25 @@ bool tc_shape(int d_qk, int d_v, int dtype, unsigned flags) {
 // How the work is cut, by sizes alone (the lengths are on the device).  Costs in tenths of a
 // microsecond: a key tile takes a CTA about 1 us whatever else runs (10; 4 with quarter tiles), the
 // busiest of the resident CTA slots (two per SM) sets the time, and merging costs a launch and the
-// traffic of the parts (70 and 1 per 0.6 MB).
+// traffic of the parts (30 and 1 per 0.6 MB).
 //  * per sequence: row tiles walk the prefix and their own keys; cut into parts, four tiles each at
 //    least, where the row tiles leave slots empty;
-//  * shared: the batch's rows packed against the prefix, and the own keys apart; parts of twice what
-//    a slot gets: the own keys' CTAs fill up beside and behind them, and fewer parts cost less to write
-//    and merge (64 decode rows, 16k shared keys: 50 us; 53, 54, 58 us with runs of 1.5, 1 and 0.75
-//    times a slot's share, 54 and 58 us with 2.5 and 3).  Taken where it saves a fifth.
+//  * shared: the batch's rows packed against the prefix, and the own keys apart, in parts of what a
+//    slot gets where that is one wave of CTAs, else of twice that: the own keys' CTAs fill up beside
+//    and behind them, and fewer parts cost less to write and merge (64 decode rows, 16k shared keys:
+//    50 us; 53, 54, 58 us with runs of 1.5, 1 and 0.75 times a slot's share, 54 and 58 us with 2.5 and
+//    3).  Taken where it saves a fifth.
 PfxPlan make_plan(int num_seqs, int total_q, int max_q, int max_kv, int prefix, int h_q, int h_kv, int d, int num_sms) {
-  constexpr long long kTile = 10, kQuad = 4, kMerge = 70;
+  constexpr long long kTile = 10, kQuad = 4, kMerge = 30;
   PfxPlan pl{};
   const int group = h_q / h_kv;
   pl.gb = std::min(group, 128);
   while (group % pl.gb) --pl.gb;
   pl.nhb = group / pl.gb;
-  pl.rows = 128 / pl.gb;
+  pl.quad_pre = (long long)total_q * pl.gb <= 32;
+  pl.rows = (pl.quad_pre ? 32 : 128) / pl.gb;
   pl.quad = (long long)max_q * pl.gb <= 32;
-  pl.rows_own = pl.quad ? 32 / pl.gb : pl.rows;
+  pl.rows_own = (pl.quad ? 32 : 128) / pl.gb;
   pl.heads = h_kv * pl.nhb;
   pl.np = (prefix + kBN - 1) / kBN;
   const long long no = ((long long)max_kv + kBN - 1) / kBN, slots = 2ll * num_sms;
@@ -862,17 +865,23 @@ PfxPlan make_plan(int num_seqs, int total_q, int max_q, int max_kv, int prefix, 
   const long long own_tiles =
       std::min((long long)num_seqs * pl.rb_own, (long long)(total_q + pl.rows_own - 1) / pl.rows_own + num_seqs);
   const long long own = std::max(1ll, own_tiles * pl.heads), pre = (long long)pl.rb_pre * pl.heads;
-  const long long tile = pl.quad ? kQuad : kTile;
+  const long long tile = pl.quad ? kQuad : kTile, tile_pre = pl.quad_pre ? kQuad : kTile;
   auto up = [](long long a, long long b) { return (a + b - 1) / b; };
   auto merge = [&](long long parts) { return kMerge + parts * total_q * h_q * d * 8 / 600000; };
   const long long all = pl.np + no;
   const long long cut = std::max(1ll, std::min({slots / own, all / 4, 64ll}));
   const long long whole = std::max(own * all / slots, all) * tile, in_parts = up(all, cut) * tile + merge(cut);
-  const long long work = pre * pl.np * kTile + own * no * tile;  // of the shared cut
-  const long long run = std::max(4 * kTile, 2 * work / slots);
+  const long long work = pre * pl.np * tile_pre + own * no * tile;  // of the shared cut
+  long long run;
+  int parts_pre, parts_own;
+  auto cut_shared = [&](long long share) {
+    run = std::max(4 * std::min(tile, tile_pre), share);
+    parts_pre = (int)std::min(up(pl.np * tile_pre, run), 48ll);
+    parts_own = (int)std::max(1ll, std::min(up(no * tile, run), 16ll));
+  };
+  cut_shared(work / slots);
+  if (pre * parts_pre + own * parts_own > slots) cut_shared(2 * work / slots);
   pl.parts_own = cut > 1 && in_parts < whole ? (int)cut : 1;
-  const int parts_pre = (int)std::min(up(pl.np * kTile, run), 48ll);
-  const int parts_own = (int)std::max(1ll, std::min(up(no * tile, run), 16ll));
   const long long apart = std::max(work / slots, run) + merge(parts_pre + parts_own);
   pl.shared = pl.np > 0 && apart * 5 < (pl.parts_own > 1 ? in_parts : whole) * 4;
   pl.parts_pre = pl.shared ? parts_pre : 0;
