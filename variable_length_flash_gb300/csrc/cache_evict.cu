@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
 // fastest, so that what a block writes is one stretch.  A group of threads copies an item, a thread
 // one B-byte piece of its K or V row; four items of each group are in flight (two and eight were as
 // fast, one 25% slower; rows moved by bulk copies through shared memory took 248 us where this takes
-// TIME_GATHER, at 64 x 2048 of 4096-8192 keys, 8 heads of 128).
+// 175 us = 92% of the copy rate, at 64 x 2048 of 4096-8192 keys, 8 heads of 128).
 constexpr int kUnroll = 4;
 template <int B>
 __global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p, int rk, int rv, int rounds) {
@@ -360,21 +360,28 @@ cudaError_t cache_evict(const EvictParams &p, cudaStream_t st) {
   const bool whole = p.d_qk * es % 16 == 0 && p.d_v * es % 16 == 0;
   const long long most = std::min(p.max_kv, p.budget);
   // CTAs per (sequence, kv head): one per 8192 keys of the longest sequence, eight at most.  Threads
-  // and keys per thread by the share of a CTA: 256 threads up to 8192 keys (four CTAs to an SM), then
-  // 1024.  Lists of at most 1024 keys whose rows are whole pieces are copied by the CTA that selected
-  // them, as long as one CTA has at most 256 KB to move: the second launch would cost more.
+  // and keys per thread by the share of a CTA and by how many CTAs there are: 256 threads up to 1024
+  // keys, and up to 8192 where there are many lists (four CTAs to an SM), else 1024.  Lists of at most
+  // 1024 keys whose rows are whole pieces are copied by the CTA that selected them, as long as one CTA
+  // has at most 256 KB to move: the second launch would cost more.
   int cluster = 1;
   while (cluster < kMaxCluster && (long long)cluster * 8192 < p.max_kv) cluster *= 2;
   const int share = (p.max_kv + cluster - 1) / cluster;
   const bool copy = share <= 1024 && whole && most * (p.d_qk + p.d_v) * es <= 262144;
   int threads = 1024;
   const void *sel;
-  if (share <= 8192) {
+  const bool few = (long long)p.num_seqs * p.h_kv <= 152 * 2;
+  if (share <= 1024) {
     threads = 256;
-    if (copy) sel = reinterpret_cast<const void *>(evict_select_kernel<4, 256, true>);
-    else if (share <= 1024) sel = reinterpret_cast<const void *>(evict_select_kernel<4, 256, false>);
-    else if (share <= 4096) sel = reinterpret_cast<const void *>(evict_select_kernel<16, 256, false>);
-    else sel = reinterpret_cast<const void *>(evict_select_kernel<32, 256, false>);
+    sel = copy ? reinterpret_cast<const void *>(evict_select_kernel<4, 256, true>)
+               : reinterpret_cast<const void *>(evict_select_kernel<4, 256, false>);
+  } else if (share <= 8192 && few) {
+    sel = share <= 4096 ? reinterpret_cast<const void *>(evict_select_kernel<4, 1024, false>)
+                        : reinterpret_cast<const void *>(evict_select_kernel<8, 1024, false>);
+  } else if (share <= 8192) {
+    threads = 256;
+    sel = share <= 4096 ? reinterpret_cast<const void *>(evict_select_kernel<16, 256, false>)
+                        : reinterpret_cast<const void *>(evict_select_kernel<32, 256, false>);
   } else if (share <= 16384) {
     sel = reinterpret_cast<const void *>(evict_select_kernel<16, 1024, false>);
   } else {

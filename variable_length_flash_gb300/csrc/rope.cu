@@ -17,7 +17,7 @@
 // 16-byte chunks, neighbouring threads on neighbouring chunks), computes their sines and cosines
 // once and applies them to `hpt` consecutive heads.  The fp64 products, which this chip is slow at,
 // run once per pair and block (a table in shared memory; per thread they took 94 us where this
-// takes TIME_VIDEO), and a block walks several runs of tokens.
+// takes 65, 20011 tokens of 40 heads of 128 in bf16, 93% of the copy rate), and a block walks several runs of tokens.
 #include <type_traits>
 
 #include "common.cuh"
@@ -82,13 +82,11 @@ __device__ __forceinline__ void turn(int pos, unsigned long long F, float &c, fl
   sincospif((float)p32 * 4.6566128730773926e-10f, &s, &c);  // 2^-31: in half turns
 }
 
-constexpr int kHeads = 8;
-
 // Grid y: a run of hpt heads of q or k; x: runs of 256 / units tokens, walked with the grid's stride.
 // Thread: chunk u of a token.  Chunks u < nrot hold V pairs -- columns V u and rot / 2 + V u, whose
 // partners they are, or (INTER, V > 1) the V / 2 pairs of neighbours in each --, the ones behind
-// them two chunks of columns that pass through.
-template <typename T, int V, bool INTER>
+// them two chunks of columns that pass through.  HEADS: heads whose loads are in flight.
+template <typename T, int V, bool INTER, int HEADS>
 __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
   __shared__ unsigned long long F[128];
   const int half = p.rot / 2, nrot = half / V;
@@ -159,18 +157,18 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
       x.set(ya);
       y.set(yb);
     };
-    // kHeads heads' loads are in flight before the first store (in place the compiler could not
+    // HEADS heads' loads are in flight before the first store (in place the compiler could not
     // move a load over a store by itself)
-    for (int h = h0; h < h1; h += kHeads, src += kHeads * p.d, dst += kHeads * p.d) {
-      C x[kHeads], y[kHeads];
+    for (int h = h0; h < h1; h += HEADS, src += HEADS * p.d, dst += HEADS * p.d) {
+      C x[HEADS], y[HEADS];
 #pragma unroll
-      for (int i = 0; i < kHeads; ++i) {
+      for (int i = 0; i < HEADS; ++i) {
         if (h + i >= h1) continue;
         x[i] = *reinterpret_cast<const C *>(src + i * p.d + ca);
         y[i] = *reinterpret_cast<const C *>(src + i * p.d + cb);
       }
 #pragma unroll
-      for (int i = 0; i < kHeads; ++i) {
+      for (int i = 0; i < HEADS; ++i) {
         if (h + i >= h1) continue;
         if (rot) apply(x[i], y[i]);
         *reinterpret_cast<C *>(dst + i * p.d + ca) = x[i];
@@ -190,18 +188,28 @@ cudaError_t launch(RopeParams p, cudaStream_t st) {
   const int v = vec ? VW : 1;
   const int units = p.rot / 2 / v + (p.copy_tail ? ((p.d - p.rot + v - 1) / v + 1) / 2 : 0);
   if (units == 0) return cudaSuccess;  // nothing turns, and the rest is already in place
-  // Heads per thread: 16 (the trigonometry is then a small share) where that still gives every SM
-  // four blocks, fewer for a decode step's few tokens, where the heads are the parallelism.
+  // Heads per thread: 16 (the trigonometry is then a small share) where that still gives every SM a
+  // block, fewer for a decode step's few tokens, where the heads are the parallelism (908 tokens of 40
+  // heads: 6.4 us with four heads each, 8.3 and 12.4 us when two or four blocks per SM were asked for).
   const long long runs = ((long long)p.total + 256 / units - 1) / (256 / units);
   auto phases = [&](int hpt) { return (p.h_q + hpt - 1) / hpt + (p.h_k + hpt - 1) / hpt; };
   p.hpt = 16;
-  while (p.hpt > 1 && runs * phases(p.hpt) < 152 * 4) p.hpt /= 2;
+  while (p.hpt > 1 && runs * phases(p.hpt) < 152) p.hpt /= 2;
   while (phases(p.hpt) > 65535) p.hpt *= 2;
   // up to eight blocks per SM, each with the same number of runs
   const long long y = phases(p.hpt), turns = (runs * y + 152 * 8 - 1) / (152 * 8);
   const dim3 grid((unsigned)((runs + turns - 1) / turns), (unsigned)y);
-  const void *kern = vec ? (p.interleaved ? (const void *)rope_kernel<T, VW, true> : (const void *)rope_kernel<T, VW, false>)
-                         : (p.interleaved ? (const void *)rope_kernel<T, 1, true> : (const void *)rope_kernel<T, 1, false>);
+  // (eight heads in flight take 64 registers of data: where a thread has fewer, more blocks fit instead)
+  const bool many = p.hpt >= 8;
+  auto pick = [&](auto v_, auto inter_) {
+    constexpr int V = decltype(v_)::value;
+    constexpr bool INTER = decltype(inter_)::value;
+    return many ? (const void *)rope_kernel<T, V, INTER, 8> : (const void *)rope_kernel<T, V, INTER, 2>;
+  };
+  using W = std::integral_constant<int, VW>;
+  using One = std::integral_constant<int, 1>;
+  const void *kern = vec ? (p.interleaved ? pick(W{}, std::true_type{}) : pick(W{}, std::false_type{}))
+                         : (p.interleaved ? pick(One{}, std::true_type{}) : pick(One{}, std::false_type{}));
   void *args[1] = {&p};
   return launch_plain(kern, grid, 256, 0, st, args);
 }
