@@ -159,6 +159,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
     if constexpr (COPY) copy_rows();
     return;
   }
+  // (no CTA writes another's shared memory before that one has started: awaited at the first write)
+  if (cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   if constexpr (K > 0) {
 #pragma unroll
     for (int e = 0; e < K; ++e) key[e] = make_key(e, __uint_as_float(key[e]));
@@ -187,6 +189,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
     a2 = __reduce_add_sync(0xffffffffu, x.y);
     a3 = __reduce_add_sync(0xffffffffu, x.z);
     if (cluster > 1) {
+      if (shift == 30) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
       if (t < cluster) cg::this_cluster().map_shared_rank(cta_c, t)[turn * kMaxCluster + rank] = make_int4(a1, a2, a3, 0);
       cg::this_cluster().sync();
       x = lane < cluster ? cta_c[turn * kMaxCluster + lane] : make_int4(0, 0, 0, 0);
