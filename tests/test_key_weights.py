@@ -145,6 +145,23 @@ def test_masked_rows_and_lowest_lse():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("flags", [0, vlf.VLF_FLAG_FORCE_SIMT])
+@pytest.mark.parametrize("q_lens,causal", [([1, 1], True), ([2, 9], True), ([20, 32], True), ([32, 32], False),
+                                           ([200, 40], False), ([200, 40], True)])
+def test_rows_without_an_lse_may_hold_anything(q_lens, causal, flags):
+    """(a row without an lse gives exactly nothing, so the sums are the same to the bit)"""
+    x = make(q_lens, [300, 150], 8, 2, 128, BF, causal, 0, seed=8)
+    rows = [0, sum(q_lens) // 2, sum(q_lens) - 1]
+    x["lse"][:, rows] = -float("inf")
+    x["q"][rows] = 0
+    want = vlf.vlf_attn_key_weights(**x, flags=flags)
+    assert want.isfinite().all()
+    for bad in (float("nan"), float("inf")):
+        x["q"][rows] = bad
+        assert torch.equal(vlf.vlf_attn_key_weights(**x, flags=flags), want)
+
+
+@pytest.mark.gpu
 def test_no_rows_at_all():
     q = torch.empty(0, 4, 64, device="cuda", dtype=BF)
     k = torch.randn(30, 2, 64, device="cuda").to(BF)

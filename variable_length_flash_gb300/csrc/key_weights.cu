@@ -199,6 +199,7 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
   uint8_t *misc = smem_raw + (sM - base);
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(misc + 512);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 516);
+  volatile int *dead_s = reinterpret_cast<volatile int *>(misc + 528);  // [score tile mod 4]: see below
   float *lse_s = reinterpret_cast<float *>(misc + kKwMisc);  // [score tile mod 4][128], then [128]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -336,6 +337,10 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
 #pragma unroll
         for (int e = 0; e < 4; ++e)  // what the exponent adds; -inf takes the column out
           lse_s[128 * (n & 3) + lane + 32 * e] = next[e] == -INFINITY ? -INFINITY : -next[e] * kLog2e;
+        // (a row without an lse is passed over by selection: its logits may be NaN)
+        const int dead = __any_sync(0xffffffffu, next[0] == -INFINITY || next[1] == -INFINITY ||
+                                                 next[2] == -INFINITY || next[3] == -INFINITY);
+        if (lane == 0) dead_s[n & 3] = dead;
         if (!STREAM_K && t + 1 < last) fetch(t + 1, next);
       }
       __syncwarp();
@@ -382,7 +387,8 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_SE + wg));
         };
-        // Adds the W columns from c on, loaded into v; FULL: every key of the warp sees all of them.
+        // Adds the W columns from c on, loaded into v; FULL: every key of the warp sees all of them, and
+        // all have an lse.
         auto add = [&](auto width, auto whole, const uint32_t *v, int c) {
           constexpr int W = decltype(width)::value;
           constexpr bool FULL = decltype(whole)::value;
@@ -394,10 +400,11 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
             float2 b = f2unpack(fma2(f2pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), scale2, l1));
             if constexpr (!FULL) {
               const int x = c + e;
-              a.x = x >= clo && x < chi ? a.x : -INFINITY;
-              a.y = x + 1 >= clo && x + 1 < chi ? a.y : -INFINITY;
-              b.x = x + 2 >= clo && x + 2 < chi ? b.x : -INFINITY;
-              b.y = x + 3 >= clo && x + 3 < chi ? b.y : -INFINITY;
+              const float2 la = f2unpack(l0), lb = f2unpack(l1);
+              a.x = x >= clo && x < chi && la.x != -INFINITY ? a.x : -INFINITY;
+              a.y = x + 1 >= clo && x + 1 < chi && la.y != -INFINITY ? a.y : -INFINITY;
+              b.x = x + 2 >= clo && x + 2 < chi && lb.x != -INFINITY ? b.x : -INFINITY;
+              b.y = x + 3 >= clo && x + 3 < chi && lb.y != -INFINITY ? b.y : -INFINITY;
             }
             acc0 = add2(acc0, f2pack(ex2(a.x), ex2(a.y)));
             acc1 = add2(acc1, f2pack(ex2(b.x), ex2(b.y)));
@@ -411,7 +418,7 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
           tmem_ld_wait();
           release();
           add(std::integral_constant<int, 16>{}, std::false_type{}, v, 0);
-        } else if (__all_sync(0xffffffffu, clo <= 0 && chi >= 128)) {
+        } else if (__all_sync(0xffffffffu, clo <= 0 && chi >= 128 && dead_s[n & 3] == 0)) {
           // 32 columns are added while the next 32 load
           uint32_t v0[32], v1[32];
           tmem_ld32(s_addr, v0);
