@@ -100,6 +100,35 @@ def test_native_calls_leave_what_is_not_theirs():
 
 
 @pytest.mark.gpu
+def test_calls_go_to_the_device_of_their_tensors(monkeypatch):
+    """Where another device is the current one, the tensors' own becomes it for the call."""
+    t, h, d = 6, 2, 64
+    r = lambda *s: torch.randn(*s, device="cuda").to(BF)  # noqa: E731
+    q, k, v, st = r(t, h, d), r(t, h, d), r(t, h, d), torch.cuda.current_stream()
+    cu = torch.tensor([0, 2, t], dtype=torch.int32, device="cuda")
+    w, f = torch.rand(h, t, device="cuda"), torch.rand(d // 2, device="cuda")
+    pos = torch.arange(t, dtype=torch.int32, device="cuda")
+    entered, real = [], torch.cuda.device
+
+    class Entered(real):
+        def __enter__(self):
+            entered.append(self.idx)
+            monkeypatch.setattr(torch.cuda, "current_device", lambda: self.idx)
+            return super().__enter__()
+
+    monkeypatch.setattr(torch.cuda, "device", Entered)
+    for call in (lambda: vlf.vlf_rope(q, k, pos, f, stream=st),
+                 lambda: vlf.vlf_attn_varlen_fwd_prefix(q, k, v, k, v, cu, cu, 4, 4, stream=st),
+                 lambda: vlf.vlf_attn_key_weights(q, k, w, cu, cu, 4, 4, stream=st),
+                 lambda: vlf.vlf_cache_evict(k, v, w, cu, 2, max_seqlen_kv=4, total_out=4, stream=st)):
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: q.get_device() + 1)
+        call()
+    monkeypatch.undo()
+    assert entered == 4 * [q.get_device()]
+    assert vlf.vlf_check_error() == 0
+
+
+@pytest.mark.gpu
 def test_native_and_python_calls_agree():
     """The same call through the native side and through Python (which a stream of the caller's takes)."""
     g = torch.Generator().manual_seed(1)

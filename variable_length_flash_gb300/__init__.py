@@ -574,6 +574,12 @@ def _used_on(stream, *tensors):
             t.record_stream(stream)
 
 
+def _elsewhere(t):
+    """Whether t is on another device than the current one, where a kernel would be launched whatever
+    its stream and pointers say."""
+    return t.is_cuda and t.get_device() != torch.cuda.current_device()
+
+
 def _given(t, name, shape, dtype):
     """A caller's output tensor."""
     _req(t, name, dtype)
@@ -645,6 +651,10 @@ def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, invers
         done = _calls.rope(q, k, positions, inv_freq, sections, interleaved, inverse)
         if done is not None:
             return done
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return vlf_rope(q, k, positions, inv_freq, sections, interleaved, inverse, q_out, k_out,
+                            stream)
     dtype = q.dtype
     dt = _DTYPE.get(dtype)
     if dt is None:
@@ -736,6 +746,11 @@ def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seq
                              max_seqlen_kv, scale, causal, window, flags)
         if done is not None:
             return done
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q,
+                                              cu_seqlens_kv, max_seqlen_q, max_seqlen_kv, scale,
+                                              causal, window, out, lse, workspace, stream, flags)
     dtype, dev = q.dtype, q.get_device()
     i32 = torch.int32
     if not (dtype in _DTYPE and dev >= 0 and q.is_contiguous()
@@ -817,6 +832,11 @@ def vlf_attn_key_weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, m
                               scale, causal, window, prev, flags)
         if done is not None:
             return done
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return vlf_attn_key_weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q,
+                                        max_seqlen_kv, scale, causal, window, prev, weights,
+                                        workspace, stream, flags)
     dtype, dev = q.dtype, q.get_device()
     i32, f32 = torch.int32, torch.float32
     if not (dtype in _DTYPE and dev >= 0 and q.is_contiguous()
@@ -887,6 +907,11 @@ def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_
         done = _calls.evict(k, v, weights, cu_seqlens_kv, budget, sink, recent, max_seqlen_kv, total_out)
         if done is not None:
             return done
+    if _elsewhere(k):
+        with torch.cuda.device(k.device):
+            return vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink, recent,
+                                   max_seqlen_kv, total_out, k_out, v_out, weights_out, index_out,
+                                   cu_out, stream)
     dtype, dev = k.dtype, k.get_device()
     if not (dtype in _DTYPE and dev >= 0 and k.is_contiguous() and v.dtype is dtype
             and v.get_device() == dev and v.is_contiguous() and weights.dtype is torch.float32

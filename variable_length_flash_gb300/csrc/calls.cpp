@@ -3,7 +3,8 @@
 // A decode step's kernels take microseconds, and so does the host: a Python function that looks at
 // ten tensors, allocates its outputs and goes through ctypes costs 13 to 24 us, three to four times
 // the kernel.  The functions here do the same for plain CUDA tensors and library-allocated outputs:
-// test the arguments, allocate with torch's allocator, call the C entry point on the current stream.
+// test the arguments, allocate with torch's allocator, call the C entry point on the current stream
+// of the tensors' device, whichever device is the current one.
 // They return None, having done nothing that counts, for whatever is not such a call or is refused;
 // the Python function behind them then takes its own way, which says what was wrong.
 #define PY_SSIZE_T_CLEAN
@@ -11,6 +12,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -125,6 +127,7 @@ PyObject *rope(PyObject *const *a) {
     for (int i = 0; i < axes; ++i)
       if (!whole(PySequence_Fast_GET_ITEM(a[4], i), sections[i])) return nullptr;
   }
+  const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
   at::Tensor qo = fresh(q->sizes(), q->scalar_type(), *q), ko = fresh(k->sizes(), k->scalar_type(), *k);
   if (p_rope(q->const_data_ptr(), sq, k->const_data_ptr(), sk, static_cast<const int32_t *>(pos->const_data_ptr()),
              (int)axes, sections, static_cast<const float *>(f->const_data_ptr()), (int)total, (int)q->size(1),
@@ -155,6 +158,7 @@ PyObject *prefix(PyObject *const *a) {
       vp->size(0) != n || vp->size(1) != hkv || vp->size(2) != dv || seqs < 0 || ck->numel() - 1 != seqs)
     return nullptr;
   if (!fits(tq) || !fits(hq) || !fits(dqk) || !fits(tk) || !fits(hkv) || !fits(dv) || !fits(n) || !fits(seqs)) return nullptr;
+  const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
   const size_t need = p_prefix_ws((int)seqs, (int)tq, mq, mk, (int)n, (int)hq, (int)hkv, (int)dqk, (int)dv, dt,
                                   (unsigned)flags, 0);
   at::Tensor out = fresh({tq, hq, dv}, ty, *q), lse = fresh({hq, tq}, at::kFloat, *q), ws;
@@ -189,6 +193,7 @@ PyObject *weights(PyObject *const *a) {
       (prev && (prev->size(0) != hkv || prev->size(1) != tk)))
     return nullptr;
   if (!fits(tq) || !fits(hq) || !fits(d) || !fits(tk) || !fits(hkv) || !fits(seqs)) return nullptr;
+  const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
   const size_t need = p_weights_ws((int)seqs, (int)tk, mq, mk, (int)hq, (int)hkv, (int)d, dt, (unsigned)flags, 0);
   at::Tensor out = fresh({hkv, tk}, at::kFloat, *q), ws;
   if (need) ws = fresh({(int64_t)need}, at::kByte, *q);
@@ -217,6 +222,7 @@ PyObject *evict(PyObject *const *a) {
   const int64_t tk = k->size(0), h = k->size(1), dk = k->size(2), dv = v->size(2), n = cu->numel() - 1;
   if (v->size(0) != tk || v->size(1) != h || w->size(0) != h || w->size(1) != tk) return nullptr;
   if (!fits(tk) || !fits(h) || !fits(dk) || !fits(dv) || !fits(n)) return nullptr;
+  const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
   at::Tensor ko = fresh({total, h, dk}, ty, *k), vo = fresh({total, h, dv}, ty, *k);
   at::Tensor wo = fresh({h, total}, at::kFloat, *k), io = fresh({h, total}, at::kInt, *k), co = fresh({n + 1}, at::kInt, *k);
   if (p_evict(k->const_data_ptr(), v->const_data_ptr(), static_cast<const float *>(w->const_data_ptr()),
