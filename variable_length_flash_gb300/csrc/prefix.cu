@@ -186,6 +186,12 @@ cudaError_t simt_prefix(const PrefixParams &pp, cudaStream_t st) {
 //    all 64 columns of each key tile and set the pace.  The rows are loaded four times instead, once
 //    per quarter, and quarter w takes keys 16 w ... 16 w + 15 of each tile (its other weights are zero):
 //    four softmaxes over disjoint keys, a quarter of the work each, joined at the end in shared memory.
+//  * Measured, width 128, 32 heads on 8: 64 decode rows behind 16384 shared keys and 100-1024 own ones
+//    50 us (floor 32 us of HBM; a CTA's start and end and about 1 us per key tile); 16 x 64-436 rows
+//    behind 8192 and 436-2048, 530 us (floor 322 us of products; tensor pipe 63%): a key tile's S reads
+//    48 KB of shared memory and its PV 16 KB while TMA writes 32 KB, 768 of the 1000 cycles it takes at
+//    128 bytes a cycle.  3 decode rows behind 1000 keys 9 us, two launches.  Tried and slower: two
+//    warps per quarter of the rows, 32 columns each (609 and 58 us).
 //  * Values behind a sequence's last key belong to the next sequence: they are zeroed in shared memory
 //    before the product, so that an infinity or NaN there (0 x inf) cannot reach this one.
 using namespace tc;

@@ -16,8 +16,11 @@
 // Bound: HBM, every element read once and written once.  A thread owns V pairs of one token (two
 // 16-byte chunks, neighbouring threads on neighbouring chunks), computes their sines and cosines
 // once and applies them to `hpt` consecutive heads.  The fp64 products, which this chip is slow at,
-// run once per pair and block (a table in shared memory; per thread they took 94 us where this
-// takes 65, 20011 tokens of 40 heads of 128 in bf16, 93% of the copy rate), and a block walks several runs of tokens.
+// run once per pair and block (a table in shared memory; done by each thread they took 94 us where
+// this takes 65), and a block walks several runs of tokens.  Measured: 20011 tokens of 40 heads of
+// 128 in bf16, sliced from a fused projection, 65 us = 93% of the copy rate; 16384 tokens of 32 heads
+// of 96 in fp16, 64 columns of which turn, 35 us = 84% (short rows: fewer bytes in flight per
+// thread); 64 tokens 3 us, which is a launch.
 #include <type_traits>
 
 #include "common.cuh"
@@ -188,8 +191,8 @@ cudaError_t launch(RopeParams p, cudaStream_t st) {
   const int v = vec ? VW : 1;
   const int units = p.rot / 2 / v + (p.copy_tail ? ((p.d - p.rot + v - 1) / v + 1) / 2 : 0);
   if (units == 0) return cudaSuccess;  // nothing turns, and the rest is already in place
-  // Heads per thread: 16 (the trigonometry is then a small share) where that still gives every SM a
-  // block, fewer for a decode step's few tokens, where the heads are the parallelism (908 tokens of 40
+  // Heads per thread: 16 (the trigonometry is then a small share) where that still gives every one of
+  // the 152 SMs a block, fewer for a decode step's few tokens, where the heads are the parallelism (908 tokens of 40
   // heads: 6.4 us with four heads each, 8.3 and 12.4 us when two or four blocks per SM were asked for).
   const long long runs = ((long long)p.total + 256 / units - 1) / (256 / units);
   auto phases = [&](int hpt) { return (p.h_q + hpt - 1) / hpt + (p.h_k + hpt - 1) / hpt; };
