@@ -100,6 +100,53 @@ def test_native_calls_leave_what_is_not_theirs():
 
 
 @pytest.mark.gpu
+def test_captured_steps_replay_like_eager_ones():
+    """A whole step in a graph, two such graphs of different batches replayed in turn on two streams, with
+    eager calls between: every replay gives the eager step's results to the bit."""
+    hq, hkv, d, P = 8, 2, 64, 700
+
+    def batch(lens, seed):
+        g = torch.Generator().manual_seed(seed)
+        r = lambda *s: torch.randn(*s, generator=g).to(BF).cuda()  # noqa: E731
+        n, f = len(lens), (10000.0 ** (-torch.arange(d // 2) / (d // 2))).float().cuda()
+        cu_q = torch.arange(n + 1, dtype=torch.int32).cuda()
+        cu_kv = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32).cuda()
+        qkv, pos = r(n, hq + 2 * hkv, d), torch.randint(0, 10 ** 6, (n,), generator=g, dtype=torch.int32).cuda()
+        kp, vp, k, v, w = r(P, hkv, d), r(P, hkv, d), r(sum(lens), hkv, d), r(sum(lens), hkv, d), \
+            torch.rand(hkv, sum(lens), generator=g).cuda()
+        top, rows = max(lens), sum(min(x, 100) for x in lens)
+
+        def step():
+            q, _ = vlf.vlf_rope(qkv[:, :hq], qkv[:, hq:hq + hkv], pos, f)
+            out, lse = vlf.vlf_attn_varlen_fwd_prefix(q, kp, vp, k, v, cu_q, cu_kv, 1, top, causal=True)
+            got = vlf.vlf_attn_key_weights(q, k, lse, cu_q, cu_kv, 1, top, causal=True, prev=w)
+            return (out, lse, got) + tuple(vlf.vlf_cache_evict(k, v, got, cu_kv, 100, 4, 16, top, rows))
+        return step
+
+    steps = [batch([300, 90, 1200], 1), batch([9000], 2)]
+    want = [s() for s in steps]
+    graphs, held = [], []
+    for s in steps:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held.append(s())
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, stream, outs in zip(graphs, streams, held):
+            with torch.cuda.stream(stream):
+                for t in outs:
+                    t.zero_()
+                graph.replay()
+        again = [s() for s in steps]
+        torch.cuda.synchronize()
+        for a, b, c in zip(want, again, held):
+            assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(a, b, c))
+    assert vlf.vlf_check_error() == 0
+
+
+@pytest.mark.gpu
 def test_calls_go_to_the_device_of_their_tensors(monkeypatch):
     """Where another device is the current one, the tensors' own becomes it for the call."""
     t, h, d = 6, 2, 64
