@@ -1,0 +1,76 @@
+"""How the decoding entry points are called: streams, batches without sequences, alignment, sizes and
+bounds far from the usual ones, and what the package does without the native side of its calls."""
+import numpy as np
+import pytest
+import torch
+
+import variable_length_flash_gb300 as vlf
+
+BF = torch.bfloat16
+
+
+def cu_of(lens, device="cuda"):
+    return torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device=device)
+
+
+def some_calls(max_kv=50):
+    """A call of each entry point, as a function of further arguments; the inputs are ready when it returns."""
+    g = torch.Generator().manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g).to(BF).cuda()  # noqa: E731
+    qkv, pos = r(9, 12, 64), torch.arange(9, dtype=torch.int32, device="cuda")
+    f = torch.rand(32, generator=g).cuda()
+    q, k, kp, vp, kc, vc = r(5, 8, 64), r(90, 2, 64), r(3000, 2, 64), r(3000, 2, 64), r(90, 2, 64), r(90, 2, 64)
+    cu_q, cu_kv, w = cu_of([1, 4]), cu_of([40, 50]), torch.rand(2, 90, generator=g).cuda()
+    lse = torch.full((8, 5), 3.0, device="cuda")
+    long_q, long_k, long_lse = r(700, 8, 64), r(700, 1, 64), torch.full((8, 700), 6.0, device="cuda")
+    one = cu_of([700])
+    torch.cuda.synchronize()
+    return dict(
+        rope=lambda **kw: vlf.vlf_rope(qkv[:, :8], qkv[:, 8:10], pos, f, **kw),
+        prefix=lambda cu=cu_kv, mk=max_kv, **kw: vlf.vlf_attn_varlen_fwd_prefix(q, kp, vp, kc, vc, cu_q, cu, 4, mk, causal=True, **kw),
+        weights=lambda cu=cu_kv, mk=max_kv, **kw: vlf.vlf_attn_key_weights(q, k, lse, cu_q, cu, 4, mk, causal=True, prev=w, **kw),
+        # (in parts: a workspace)
+        prompt=lambda **kw: vlf.vlf_attn_key_weights(long_q, long_k, long_lse, one, one, 700, 700, causal=True, **kw),
+        evict=lambda cu=cu_kv, mk=max_kv, **kw: vlf.vlf_cache_evict(kc, vc, w, cu, 20, 2, 3, max_seqlen_kv=mk, total_out=40, **kw))
+
+
+def as_list(x):
+    return [x] if torch.is_tensor(x) else list(x)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["rope", "prefix", "weights", "prompt", "evict"])
+def test_outputs_on_another_stream_are_allocated_in_its_order(name):
+    """Blocks that are free on the current stream, but still to be written by what is queued there, are
+    not what a call on another stream writes to."""
+    call = some_calls()[name]
+    want = as_list(call())
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        sizes = [t.numel() * t.element_size() for t in want] + [1 << 20, 1 << 18]
+        held = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+        torch.cuda._sleep(40_000_000)
+        for t in held:
+            t.fill_(1)
+        del held, t
+        got = as_list(call(stream=side))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert vlf.vlf_check_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["prefix", "weights", "evict"])
+def test_lengths_left_to_the_call_are_read_in_its_stream(name):
+    call = some_calls()[name]
+    want = as_list(call())
+    cu, late = cu_of([40, 50]), cu_of([0, 0])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)
+        late.copy_(cu)
+    got = as_list(call(cu=late, mk=None, stream=side))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and vlf.vlf_check_error() == 0

@@ -566,12 +566,27 @@ def _same_device(like, **tensors):
             raise VlfError(VLF_ERR_INVALID, f"{name} is on {t.device}, not on {like.device}")
 
 
-def _used_on(stream, *tensors):
-    """Tells the caching allocator that fresh tensors are used on a stream other than the one they
-    were allocated on."""
-    for t in tensors:
-        if t is not None and t.numel():
-            t.record_stream(stream)
+def _another(stream, like):
+    """Whether the caller's stream is another than the current one of like's device."""
+    if stream is None or not like.is_cuda:
+        return False
+    if stream.device != like.device:
+        raise VlfError(VLF_ERR_INVALID, f"stream is on {stream.device}, the tensors on {like.device}")
+    return stream.cuda_stream != _stream(None, like)
+
+
+def _under(stream, given, call):
+    """call() with the caller's stream as the current one: what it allocates or reads on the host is in
+    that stream's order.  (A block allocated on the current stream may still be read or written by
+    what is queued there, which the caller's stream does not wait for.)  The outputs that the caller
+    did not give are told of the stream they are returned to, so that they outlive its work on them."""
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        got = call()
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None and t.numel() and not any(t is g for g in given):
+            t.record_stream(here)
+    return got
 
 
 def _elsewhere(t):
@@ -655,6 +670,9 @@ def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, invers
         with torch.cuda.device(q.device):
             return vlf_rope(q, k, positions, inv_freq, sections, interleaved, inverse, q_out, k_out,
                             stream)
+    if _another(stream, q):
+        return _under(stream, (q_out, k_out), lambda: vlf_rope(
+            q, k, positions, inv_freq, sections, interleaved, inverse, q_out, k_out))
     dtype = q.dtype
     dt = _DTYPE.get(dtype)
     if dt is None:
@@ -694,8 +712,7 @@ def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, invers
         if len(sections) != axes:
             raise VlfError(VLF_ERR_INVALID, f"{len(sections)} sections for {axes} position axes")
         sec = _sections(sections)
-    fresh_q, fresh_k = q_out is None, k_out is None
-    if fresh_q:
+    if q_out is None:
         q_out = torch.empty((total, hq, d), dtype=dtype, device=q.device)
         sqo = hq * d
     else:
@@ -704,7 +721,7 @@ def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, invers
             raise VlfError(VLF_ERR_INVALID, "q_out must have q's shape")
         _same_device(q, q_out=q_out)
     if k is not None:
-        if fresh_k:
+        if k_out is None:
             k_out = torch.empty((total, hk, d), dtype=dtype, device=q.device)
             sko = hk * d
         else:
@@ -714,8 +731,6 @@ def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, invers
         if k.get_device() != dev or k_out.get_device() != dev:
             _same_device(q, k=k, k_out=k_out)
         ko_p = k_out.data_ptr()
-    if stream is not None:
-        _used_on(stream, q_out if fresh_q else None, k_out if fresh_k else None)
     st = _lib.vlf_rope(q.data_ptr(), sq, k_p, sk, positions.data_ptr(), axes, sec, inv_freq.data_ptr(),
                        total, hq, hk, d, 2 * inv_freq.shape[0], dt, 1 if interleaved else 0,
                        1 if inverse else 0, q_out.data_ptr(), sqo, ko_p, sko, _stream(stream, q))
@@ -751,6 +766,10 @@ def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seq
             return vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q,
                                               cu_seqlens_kv, max_seqlen_q, max_seqlen_kv, scale,
                                               causal, window, out, lse, workspace, stream, flags)
+    if _another(stream, q):
+        return _under(stream, (out, lse), lambda: vlf_attn_varlen_fwd_prefix(
+            q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, max_seqlen_kv, scale,
+            causal, window, out, lse, workspace, flags=flags))
     dtype, dev = q.dtype, q.get_device()
     i32 = torch.int32
     if not (dtype in _DTYPE and dev >= 0 and q.is_contiguous()
@@ -777,15 +796,12 @@ def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seq
         raise VlfError(VLF_ERR_INVALID, "cu_seqlens_q and cu_seqlens_kv must have num_seqs + 1 entries")
     if max_seqlen_kv is None:
         max_seqlen_kv = _max_len(cu_seqlens_kv)
-    fresh = []
     if out is None:
         out = torch.empty((tq, hq, dv), dtype=dtype, device=q.device)
-        fresh.append(out)
     else:
         _given(out, "out", (tq, hq, dv), dtype), _same_device(q, out=out)
     if lse is None:
         lse = torch.empty((hq, tq), dtype=torch.float32, device=q.device)
-        fresh.append(lse)
     else:
         _given(lse, "lse", (hq, tq), torch.float32), _same_device(q, lse=lse)
     mq, mk = _c_int(max_seqlen_q, "max_seqlen_q"), _c_int(max_seqlen_kv, "max_seqlen_kv")
@@ -799,10 +815,7 @@ def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seq
         ws_p, ws_n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        fresh.append(workspace)
         ws_p, ws_n = workspace.data_ptr(), need
-    if stream is not None:
-        _used_on(stream, *fresh)
     st = _lib.vlf_attn_varlen_fwd_prefix(
         q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), n, k.data_ptr(), v.data_ptr(),
         cu_seqlens_q.data_ptr(), cu_seqlens_kv.data_ptr(), nseq, tq, tk, mq, mk, hq, hkv, dqk, dv, dt,
@@ -837,6 +850,10 @@ def vlf_attn_key_weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, m
             return vlf_attn_key_weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q,
                                         max_seqlen_kv, scale, causal, window, prev, weights,
                                         workspace, stream, flags)
+    if _another(stream, q):
+        return _under(stream, (weights,), lambda: vlf_attn_key_weights(
+            q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, max_seqlen_kv, scale, causal, window,
+            prev, weights, workspace, flags=flags))
     dtype, dev = q.dtype, q.get_device()
     i32, f32 = torch.int32, torch.float32
     if not (dtype in _DTYPE and dev >= 0 and q.is_contiguous()
@@ -863,10 +880,8 @@ def vlf_attn_key_weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, m
         if prev.get_device() != dev:
             _same_device(q, prev=prev)
         prev_p = prev.data_ptr()
-    fresh = []
     if weights is None:
         weights = torch.empty((hkv, tk), dtype=f32, device=q.device)
-        fresh.append(weights)
     else:
         _given(weights, "weights", (hkv, tk), f32), _same_device(q, weights=weights)
     mq, mk = _c_int(max_seqlen_q, "max_seqlen_q"), _c_int(max_seqlen_kv, "max_seqlen_kv")
@@ -880,10 +895,7 @@ def vlf_attn_key_weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, m
         ws_p, ws_n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        fresh.append(workspace)
         ws_p, ws_n = workspace.data_ptr(), need
-    if stream is not None:
-        _used_on(stream, *fresh)
     st = _lib.vlf_attn_key_weights(
         q.data_ptr(), k.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_kv.data_ptr(),
         nseq, tq, tk, mq, mk, hq, hkv, d, dt, float(scale) if scale else 0.0, 1 if causal else 0,
@@ -912,6 +924,10 @@ def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_
             return vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink, recent,
                                    max_seqlen_kv, total_out, k_out, v_out, weights_out, index_out,
                                    cu_out, stream)
+    if _another(stream, k):
+        return _under(stream, (k_out, v_out, weights_out, index_out, cu_out), lambda: vlf_cache_evict(
+            k, v, weights, cu_seqlens_kv, budget, sink, recent, max_seqlen_kv, total_out, k_out, v_out,
+            weights_out, index_out, cu_out))
     dtype, dev = k.dtype, k.get_device()
     if not (dtype in _DTYPE and dev >= 0 and k.is_contiguous() and v.dtype is dtype
             and v.get_device() == dev and v.is_contiguous() and weights.dtype is torch.float32
@@ -957,8 +973,6 @@ def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_
                                   (n + 1, torch.int32))):
             if t is not None:
                 _given(t, name, like[:-1], like[-1]), _same_device(k, **{name: t})
-    if stream is not None:
-        _used_on(stream, *[t for t, g in zip(outs, given) if g is None])
     st = _lib.vlf_cache_evict(
         k.data_ptr(), v.data_ptr(), weights.data_ptr(), cu_seqlens_kv.data_ptr(), n, tk,
         _c_int(max_seqlen_kv, "max_seqlen_kv"), h, dk, dv, _DTYPE[dtype], budget, sink, recent, total_out,
