@@ -479,7 +479,8 @@ size_t vlf_attn_key_weights_workspace_size(int num_seqs, int total_kv, int max_s
  *   k_out [total_out, h_kv, d_qk], v_out [total_out, h_kv, d_v], weights_out fp32 [h_kv, total_out]
  *   index_out    int32 [h_kv, total_out]: the sequence-local key each row came from
  *   cu_out       int32 [num_seqs + 1]: the cu_seqlens of the outputs (-1 behind a sequence that had
- *                an error; neither it nor the next one is copied)
+ *                an error; neither it nor the next one is copied).  With num_seqs = 0 nothing is
+ *                enqueued, and the one entry is the caller's to set to 0
  * Outputs overlap no input.  d_qk, d_v <= 256.
  */
 int vlf_cache_evict(const void *k, const void *v, const float *weights,

@@ -74,3 +74,19 @@ def test_lengths_left_to_the_call_are_read_in_its_stream(name):
     got = as_list(call(cu=late, mk=None, stream=side))
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got)) and vlf.vlf_check_error() == 0
+
+
+@pytest.mark.gpu
+def test_eviction_of_an_empty_batch():
+    """No sequences: cu_seqlens [0] out, whichever way the call goes and whoever holds the output."""
+    k, w, cu = torch.empty(0, 2, 64, device="cuda", dtype=BF), torch.empty(2, 0, device="cuda"), cu_of([])
+    for kw in (dict(total_out=0, max_seqlen_kv=0), dict(), dict(stream=torch.cuda.current_stream()),
+               dict(stream=torch.cuda.Stream()), dict(cu_out=torch.full((1,), 9, dtype=torch.int32, device="cuda"))):
+        # (what a fresh output of this size would hold)
+        junk = torch.full((1,), 77, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        del junk
+        ko, vo, wo, io, co = vlf.vlf_cache_evict(k, k, w, cu, 4, **kw)
+        torch.cuda.synchronize()
+        assert co.tolist() == [0] and ko.shape == (0, 2, 64) and wo.shape == io.shape == (2, 0)
+    assert vlf.vlf_check_error() == 0

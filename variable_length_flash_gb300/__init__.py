@@ -980,6 +980,8 @@ def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_
         cu_out.data_ptr(), _stream(stream, k))
     if st != VLF_OK:
         _check(st, "vlf_cache_evict")
+    if n == 0:  # (for an empty batch the library enqueues nothing)
+        cu_out.zero_()
     return outs
 
 

@@ -216,8 +216,8 @@ PyObject *evict(PyObject *const *a) {
   const int dev = k->get_device(), dt = dtype_of(*k);
   const at::ScalarType ty = k->scalar_type();
   if (dt < 0 || !dense(k, ty, dev) || !dense(v, ty, dev) || !dense(w, at::kFloat, dev) || !dense(cu, at::kInt, dev) ||
-      k->dim() != 3 || v->dim() != 3 || w->dim() != 2 || cu->numel() < 1)
-    return nullptr;
+      k->dim() != 3 || v->dim() != 3 || w->dim() != 2 || cu->numel() < 2)
+    return nullptr;  // (no sequences: cu_out is then the caller's to write)
   const int64_t tk = k->size(0), h = k->size(1), dk = k->size(2), dv = v->size(2), n = cu->numel() - 1;
   if (v->size(0) != tk || v->size(1) != h || w->size(0) != h || w->size(1) != tk) return nullptr;
   if (!fits(tk) || !fits(h) || !fits(dk) || !fits(dv) || !fits(n)) return nullptr;
