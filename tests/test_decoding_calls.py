@@ -90,3 +90,32 @@ def test_eviction_of_an_empty_batch():
         torch.cuda.synchronize()
         assert co.tolist() == [0] and ko.shape == (0, 2, 64) and wo.shape == io.shape == (2, 0)
     assert vlf.vlf_check_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,why", [(60, "lengths"), (1500, "lengths"), (60, "rows"), (1500, "rows")])
+def test_no_rows_are_copied_behind_a_refused_sequence(n, why):
+    """In one launch (60 keys) and in two: of four sequences the second is refused; its rows and the next
+    one's stay as they were, the others are copied."""
+    h, budget = 2, 20
+    lens = [n, n + 40 if why == "lengths" else n, n, n]
+    k = torch.randn(sum(lens), h, 64, device="cuda").to(BF)
+    w, cu = torch.rand(h, sum(lens), device="cuda"), cu_of(lens)
+    rows = 4 * budget if why == "lengths" else budget + 5  # (the second one and those behind it do not fit)
+    out = torch.full((rows, h, 64), 7.0, device="cuda", dtype=BF)
+    got = torch.full((h, rows), 7.0, device="cuda")
+    ko, _, wo, io, co = vlf.vlf_cache_evict(k, k, w, cu, budget, max_seqlen_kv=n, total_out=rows, k_out=out, weights_out=got)
+    assert vlf.vlf_check_error() == vlf.VLF_ERR_BAD_SEQLENS
+    if why == "lengths":
+        assert co.tolist() == [0, budget, -1, 3 * budget, 4 * budget]
+        copied = [0, 3]
+        assert (ko[budget:3 * budget] == 7).all() and (wo[:, budget:3 * budget] == 7).all()
+    else:
+        assert co.tolist() == [0, budget, -1, -1, -1]
+        copied = [0]
+        assert (ko[budget:] == 7).all() and (wo[:, budget:] == 7).all()
+    for s in copied:
+        for g in range(h):
+            at = int(cu[s]) + io[g, s * budget:(s + 1) * budget].long()
+            assert torch.equal(ko[s * budget:(s + 1) * budget, g], k[at, g])
+            assert torch.equal(wo[g, s * budget:(s + 1) * budget], w[g, at])

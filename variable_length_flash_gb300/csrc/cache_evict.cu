@@ -88,6 +88,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
   };
   if (s == 0 && first) p.cu_out[0] = 0;
   int k0, len;
+  // (no rows for a sequence behind a refused one, as in the gather: one that does not fit leaves none
+  // that fits behind it, so its lengths say all)
+  bool copy = COPY;
+  if (COPY && s > 0) copy = evict_seq(p, s - 1, k0, len);
   if (!evict_seq(p, s, k0, len)) {  // (the same for the whole cluster)
     refuse();
     return;
@@ -160,7 +164,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
   };
   if (all) {
     for (int j = t; j < cn; j += nt) index[c0 + j] = c0 + j;
-    if constexpr (COPY) copy_rows();
+    if (COPY && copy) copy_rows();
     return;
   }
   // (no CTA writes another's shared memory before that one has started: awaited at the first write)
@@ -301,7 +305,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
   }
   // no CTA leaves while another may still read its counts
   if (cluster > 1) cg::this_cluster().sync();
-  if constexpr (COPY) copy_rows();
+  if (COPY && copy) copy_rows();
 }
 
 // Kept rows of K, V and the weights.  Grid y = sequence, x = runs of (output row, head) items, heads
