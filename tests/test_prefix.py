@@ -250,3 +250,30 @@ def test_python_refusals():
                dict(lse=torch.empty(4, 3, device="cuda")), dict(k_prefix=x["k_prefix"].cpu())):
         with pytest.raises(vlf.VlfError):
             vlf.vlf_attn_varlen_fwd_prefix(**dict(x, **kw))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,dtype,flags", [(64, FP, 0), (128, FP, 0), (40, HF, 0), (128, BF, vlf.VLF_FLAG_FORCE_SIMT),
+                                           (128, BF, 0), (64, HF, 0)])
+def test_nan_logits_alone_in_their_tiles_reach_their_rows(d, dtype, flags):
+    """A row of q that is NaN, a prefix of one NaN key, a window whose first key is NaN: the row and its
+    log-sum-exp are NaN; rows that do not see it are what they were."""
+    q_lens, kv_lens = [1, 3], [70, 33]
+    for prefix in (1, 200):
+        x = make(prefix, q_lens, kv_lens, 4, 2, d, d, dtype, seed=prefix)
+        x["q"][2] = float("nan")
+        out, lse = vlf.vlf_attn_varlen_fwd_prefix(**x, causal=True, flags=flags)
+        assert out[2].isnan().all() and lse[:, 2].isnan().all()
+        assert out[[0, 1, 3]].isfinite().all() and lse[:, [0, 1, 3]].isfinite().all()
+    x = make(1, q_lens, kv_lens, 4, 2, d, d, dtype, seed=1)
+    x["k_prefix"][0] = float("nan")
+    out, lse = vlf.vlf_attn_varlen_fwd_prefix(**x, causal=True, flags=flags)
+    assert out.isnan().all() and lse.isnan().all()
+    # (the window's first key at many places of its tile, the last ones among them)
+    for window in range(2, 70):
+        x = make(26, [1], [70], 4, 2, d, d, dtype, seed=window)
+        x["k"][70 - window] = float("nan")
+        out, lse = vlf.vlf_attn_varlen_fwd_prefix(**x, causal=True, window=window, flags=flags)
+        assert out.isnan().all() and lse.isnan().all(), window
+        out, lse = vlf.vlf_attn_varlen_fwd_prefix(**x, causal=True, window=window - 1, flags=flags)
+        assert out.isfinite().all() and lse.isfinite().all(), window

@@ -102,17 +102,15 @@ __global__ void __launch_bounds__(kThreads) simt_prefix_kernel(const PrefixParam
         tmax = fmaxf(tmax, y);
       }
       const float m_new = fmaxf(m, lanes8_max(tmax));
-      float alpha = 1.f, psum = 0.f;
-      if (m_new != -INFINITY) {
-        alpha = expf(m - m_new);  // m = -inf: 0
+      // (no maximum yet: masked keys, whose weight is 0 from any reference, or NaN logits, which fmaxf
+      // passes over and which have to reach the sums)
+      const float ref = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = expf(m - ref);  // m = -inf: 0 (and a NaN sum stays NaN)
+      float psum = 0.f;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          sc[x] = expf(sc[x] - m_new);  // masked: 0
-          psum += sc[x];
-        }
-      } else {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) sc[x] = 0.f;
+      for (int x = 0; x < 4; ++x) {
+        sc[x] = expf(sc[x] - ref);  // masked: 0
+        psum += sc[x];
       }
       l = l * alpha + lanes8_sum(psum);
       m = m_new;
