@@ -417,7 +417,7 @@ int vlf_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
  * kernels for F16 / BF16 and (d_qk, d_v) in {(64,64), (96,96), (128,128)}.  Keys and values of other
  * sequences never reach a row, whatever they hold; a value of its own sequence or of the prefix that
  * is not finite may also reach rows that do not see its key (a weight of 0 times it), as in
- * vlf_attn_varlen_fwd.  No backward.
+ * vlf_attn_varlen_fwd.  A row that sees a NaN logit is NaN, and so is its lse.  No backward.
  */
 int vlf_attn_varlen_fwd_prefix(const void *q, const void *k_prefix, const void *v_prefix,
                                int prefix_len, const void *k, const void *v,
