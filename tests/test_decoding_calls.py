@@ -119,3 +119,24 @@ def test_no_rows_are_copied_behind_a_refused_sequence(n, why):
             at = int(cu[s]) + io[g, s * budget:(s + 1) * budget].long()
             assert torch.equal(ko[s * budget:(s + 1) * budget, g], k[at, g])
             assert torch.equal(wo[g, s * budget:(s + 1) * budget], w[g, at])
+
+
+@pytest.mark.gpu
+def test_positions_and_frequencies_may_be_slices():
+    """A chunk of a prompt's positions, a run of the frequencies: from any element on, on any route."""
+    g = torch.Generator().manual_seed(2)
+    pos = torch.randint(0, 10 ** 6, (40,), generator=g, dtype=torch.int32).cuda()
+    freq = torch.rand(70, generator=g).cuda()
+    q, k = (torch.randn(9, h, 64, generator=g).to(BF).cuda() for h in (4, 2))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for a in range(5):
+        for b in range(5):
+            p, f = pos[a:a + 9], freq[b:b + 32]
+            want = vlf.vlf_rope(q, k, p.clone(), f.clone())
+            got = [vlf.vlf_rope(q, k, p, f), vlf.rotary_embedding(q, k, p, f), vlf.vlf_rope(q, k, p, f, stream=side)]
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for pair in got for x, y in zip(want, pair))
+    two = pos[1:19].view(2, 9)
+    want = vlf.vlf_rope(q, k, two.clone(), freq[:32], [20, 12])
+    assert all(torch.equal(x, y) for x, y in zip(want, vlf.vlf_rope(q, k, two, freq[:32], [20, 12])))

@@ -703,6 +703,11 @@ def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, invers
         _req(positions, "positions", torch.int32), _req(inv_freq, "inv_freq", torch.float32)
         _same_device(q, positions=positions, inv_freq=inv_freq)
         raise VlfError(VLF_ERR_INVALID, "positions must be [tokens] or [axes, tokens], inv_freq [rot / 2]")
+    # (slices of them start anywhere; the library takes 16-byte aligned pointers)
+    if positions.data_ptr() % 16:
+        positions = positions.clone()
+    if inv_freq.data_ptr() % 16:
+        inv_freq = inv_freq.clone()
     axes = 1 if len(shape) == 1 else shape[0]
     if sections is None:
         if axes != 1:
