@@ -393,7 +393,8 @@ size_t vlf_noalloc_scratch_bytes(void);
  *   inverse      0: y_a = x_a cos t - x_b sin t, y_b = x_b cos t + x_a sin t with
  *                t = positions[axis(c)][token] * inv_freq[c]; 1: by -t, which is the gradient of
  *                the rotation (and undoes it)
- * The angle is exact to far positions (64-bit fixed point); the products are fp32, rounded once.
+ * The angle is taken in 64-bit fixed point, off by at most |position| (|inv_freq| 2^-55 + 2^-64) turns
+ * whatever the position; sines, cosines and products are fp32, the result is rounded once.
  */
 int vlf_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
              const int32_t *positions, int n_axes, const int *sections, const float *inv_freq,

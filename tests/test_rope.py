@@ -230,3 +230,21 @@ def test_python_refusals():
             vlf.vlf_rope(**a)
     with pytest.raises(vlf.VlfError):
         vlf.rotary_embedding(q, k, pos, f.clone().requires_grad_(), sec)
+
+
+@pytest.mark.gpu
+def test_far_turns_of_small_and_negative_frequencies():
+    """The turn itself: (1, 0) in fp32 becomes (cos t, sin t) without a rounding of products.  Errors of the
+    angle: |position| (|inv_freq| 2^-55 + 2^-64) turns, pi (2^-25 + 2^-32) radians for the fraction in
+    32 bits and in fp32; two ulp (2^-23) for a sine or cosine: together less than 2^-22 and the first."""
+    f = np.float32([1.0, 0.5, -0.5, 2.74e-4, 2.46e-6, 1e-7, 1e-10, -1e-10, -3e-7, -2.46e-6, -1e-3, -0.7, 3.0, 0.0,
+                    -4.4e-5, -6.1e-6])
+    pos = np.int64([2 ** 31 - 1, -2 ** 31, 1999999999, -1234567891, 2 ** 20, 1, 0])
+    x = torch.zeros(len(pos), 1, 2 * len(f), device="cuda")
+    x[..., :len(f)] = 1
+    y, _ = vlf.vlf_rope(x, None, torch.tensor(pos, dtype=torch.int32, device="cuda"), torch.tensor(f, device="cuda"))
+    want = ref.rope(np64(x), pos[None], f, [len(f)], 2 * len(f), False)
+    turns = np.abs(pos[:, None].astype(np.float64)) * (np.abs(f.astype(np.float64)) * 2.0 ** -55 + 2.0 ** -64)
+    tol = 2.0 ** -22 + 2 * np.pi * np.concatenate([turns, turns], 1)[:, None]
+    err = np.abs(np64(y) - want)
+    assert (err <= tol).all(), (err - tol).max()

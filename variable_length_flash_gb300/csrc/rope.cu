@@ -9,9 +9,10 @@
 //
 // The angle.  t grows to position * frequency, a million radians and more, where an fp32 product
 // is off by whole percents of a turn.  Positions are integers, so the turn fraction is formed in
-// 64-bit fixed point instead: F = frac(inv_freq / 2 pi) 2^64 (one double product per pair), and
-// position * F mod 2^64 IS the fraction of a turn, with an error of |position| inv_freq 2^-55
-// turns; its top 32 bits, a number in [-1/2, 1/2), go to sincospi.
+// 64-bit fixed point instead: F = inv_freq / 2 pi mod 1 in units of 2^-64 (one double product per
+// pair), and position * F mod 2^64 IS the fraction of a turn, with an error of at most
+// |position| (|inv_freq| 2^-55 + 2^-64) turns: the product's rounding and F's own.  Its top 32 bits, a
+// number in [-1/2, 1/2), go to sincospi.
 //
 // Bound: HBM, every element read once and written once.  A thread owns V pairs of one token (two
 // 16-byte chunks, neighbouring threads on neighbouring chunks), computes their sines and cosines
@@ -71,11 +72,12 @@ template <typename T> struct Chunk<T, 1> {
   __device__ __forceinline__ void set(const float (&x)[1]) { r = from_f32<T>(x[0]); }
 };
 
-// frac(f / 2 pi) in units of 2^-64.
+// f / 2 pi less the nearest whole number, in units of 2^-64 (as an unsigned number: mod 2^64).  Counted
+// from the nearest whole number, not from the one below, a small negative turn keeps its bits.
 __device__ __forceinline__ unsigned long long turns_of(float f) {
   double t = (double)f * 0.15915494309189533577;  // 1 / (2 pi)
-  t -= floor(t);
-  return (unsigned long long)(t * 18446744073709551616.0);
+  t -= rint(t);
+  return (unsigned long long)__double2ll_rn(t * 18446744073709551616.0);
 }
 // cos and sin of pos * F turns.
 __device__ __forceinline__ void turn(int pos, unsigned long long F, float &c, float &s) {
