@@ -140,3 +140,68 @@ def test_positions_and_frequencies_may_be_slices():
     two = pos[1:19].view(2, 9)
     want = vlf.vlf_rope(q, k, two.clone(), freq[:32], [20, 12])
     assert all(torch.equal(x, y) for x, y in zip(want, vlf.vlf_rope(q, k, two, freq[:32], [20, 12])))
+
+
+def test_the_package_works_without_its_native_calls(tmp_path):
+    """libvlf.so is enough: the import warns, and every call goes through the Python functions."""
+    import os
+    import subprocess
+    import sys
+    src = os.path.dirname(vlf.LIB_PATH)
+    dst = tmp_path / os.path.basename(src)
+    dst.mkdir()
+    for name in ("__init__.py", "functional.py", "flops.py", "libvlf.so"):
+        os.symlink(os.path.join(src, name), dst / name)
+    code = """
+import warnings
+with warnings.catch_warnings(record=True) as w:
+    warnings.simplefilter("always")
+    import variable_length_flash_gb300 as vlf
+assert any("native calls" in str(x.message) for x in w), w
+assert vlf.__file__.startswith(%r), vlf.__file__
+assert vlf._calls.rope(1, 2) is None
+import torch
+try:
+    vlf.vlf_rope(torch.zeros(4, 2, 8), None, torch.zeros(4, dtype=torch.int32), torch.zeros(4))
+except vlf.VlfError as e:
+    assert "CUDA" in str(e)
+else:
+    raise AssertionError
+""" % str(tmp_path)
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, env={**os.environ, "PYTHONPATH": str(tmp_path)},
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_native_calls_of_another_torch_are_not_bound(monkeypatch):
+    import types
+    bound = []
+    for other in (types.SimpleNamespace(TORCH="1.2.3+other", bind=lambda *a: bound.append(a)),
+                  types.SimpleNamespace(bind=lambda *a: bound.append(a))):
+        monkeypatch.setattr(vlf, "_calls", other)
+        with pytest.warns(UserWarning, match="native calls"):
+            got = vlf._load_calls(vlf._lib)
+        assert not bound and got.evict(1, 2, 3) is None
+
+
+def test_native_calls_of_another_torch_are_built_anew(monkeypatch, tmp_path):
+    from variable_length_flash_gb300 import _build
+    stamp, lib = tmp_path / "calls.for", tmp_path / "_calls.so"
+    monkeypatch.setattr(_build, "CALLS_FOR", str(stamp))
+    monkeypatch.setattr(_build, "CALLS", str(lib))
+    assert _build._calls_stale()
+    lib.write_text("")
+    assert _build._calls_stale()
+    stamp.write_text(_build._calls_for())
+    assert not _build._calls_stale()
+    stamp.write_text("1.2.3 .so")
+    assert _build._calls_stale()
+
+
+@pytest.mark.gpu
+def test_results_do_not_depend_on_the_native_calls(monkeypatch):
+    calls = some_calls()
+    want = {n: as_list(c()) for n, c in calls.items()}
+    monkeypatch.setattr(vlf, "_calls", vlf._NoCalls())
+    for n, c in calls.items():
+        assert all(torch.equal(a, b) for a, b in zip(want[n], as_list(c()))), n

@@ -25,6 +25,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -133,13 +134,24 @@ def _load():
     return lib
 
 
+class _NoCalls:
+    """In place of the native calls: every call is left to the Python functions."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _load_calls(lib):
-    """The native side of the decoding entry points' calls (csrc/calls.cpp), bound to the library."""
+    """The native side of the decoding entry points' calls (csrc/calls.cpp), bound to the library.  It
+    saves host time only: where it is not built, or for another torch, the Python functions do all."""
     try:
         from . import _calls
-    except ImportError as e:
-        raise ImportError("variable_length_flash_gb300/_calls.so is not built for this torch; run "
-                          "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        if _calls.TORCH != str(torch.__version__):
+            raise ImportError(f"it was built for torch {_calls.TORCH}")
+    except (ImportError, AttributeError) as e:
+        warnings.warn(f"variable_length_flash_gb300: the native calls are not used ({e}); run `python -c "
+                      "'import __graft_entry__ as g; g.build()'`", stacklevel=3)
+        return _NoCalls()
     _calls.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.vlf_rope, lib.vlf_attn_varlen_fwd_prefix, lib.vlf_attn_varlen_fwd_prefix_workspace_size,
         lib.vlf_attn_key_weights, lib.vlf_attn_key_weights_workspace_size, lib.vlf_cache_evict)])

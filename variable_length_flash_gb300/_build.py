@@ -15,6 +15,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libvlf.so")
 CALLS_SRC = os.path.join(CSRC, "calls.cpp")
 CALLS = os.path.join(PKG, "_calls.so")
+CALLS_FOR = os.path.join(BUILD, "calls.for")  # what _calls.so was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -33,6 +34,24 @@ def _stale(sources, headers, target=LIB) -> bool:
     return any(os.path.getmtime(f) > t for f in sources + headers)
 
 
+def _calls_for() -> str:
+    """The torch and the Python that are installed."""
+    import sysconfig
+
+    import torch
+    return f"{torch.__version__} {sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
+def _calls_stale() -> bool:
+    """Whether _calls.so is older than its sources or was built for another torch or Python."""
+    try:
+        with open(CALLS_FOR) as f:
+            built_for = f.read()
+    except OSError:
+        return True
+    return built_for != _calls_for() or _stale([CALLS_SRC], [os.path.join(ROOT, "include", "vlf.h")], CALLS)
+
+
 def _build_calls() -> str:
     """Compile csrc/calls.cpp against the torch that is installed."""
     import sysconfig
@@ -44,13 +63,16 @@ def _build_calls() -> str:
            os.path.join(cuda, "include"), os.path.join(ROOT, "include"), sysconfig.get_paths()["include"]]
     tmp = CALLS + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fno-strict-aliasing",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-isystem{i}" for i in inc],
-           CALLS_SRC, "-o", tmp, "-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
-           "-ltorch", "-ltorch_python"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DVLF_TORCH="{torch.__version__}"', *[f"-isystem{i}" for i in inc], CALLS_SRC, "-o", tmp,
+           "-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(CALLS_FOR, "w") as f:
+        f.write(_calls_for())
     return CALLS
 
 
@@ -59,7 +81,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     headers = sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
                      glob.glob(os.path.join(ROOT, "include", "*.h")))
-    calls = force or _stale([CALLS_SRC], [os.path.join(ROOT, "include", "vlf.h")], CALLS)
+    calls = force or _calls_stale()
     if not force and not _stale(sources, headers):
         if calls:
             _build_calls()
