@@ -277,3 +277,24 @@ def test_nan_logits_alone_in_their_tiles_reach_their_rows(d, dtype, flags):
         assert out.isnan().all() and lse.isnan().all(), window
         out, lse = vlf.vlf_attn_varlen_fwd_prefix(**x, causal=True, window=window - 1, flags=flags)
         assert out.isfinite().all() and lse.isfinite().all(), window
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,flags", [(BF, 0), (HF, 0), (BF, vlf.VLF_FLAG_FORCE_SIMT)])
+@pytest.mark.parametrize("prefix,q_lens,kv_lens", [(200, [1, 1], [70, 33]), (5000, [1, 3], [40, 90]), (300, [80, 150], [190, 201]),
+                                                   (0, [1, 2, 1], [70, 33, 500])])
+def test_an_infinite_value_that_is_seen_gives_infinity(prefix, q_lens, kv_lens, dtype, flags):
+    """Rows that all see the key: its column is infinite with the value's sign, the others what they were."""
+    x = make(prefix, q_lens, kv_lens, 8, 2, 64, 64, dtype, seed=3)
+    clean, clean_lse = vlf.vlf_attn_varlen_fwd_prefix(**x, causal=True, flags=flags)
+    assert clean.isfinite().all()
+    for name, key, rows in (("v_prefix", 17, slice(None)), ("v", sum(kv_lens[:-1]) + 3, slice(sum(q_lens[:-1]), None))):
+        if name == "v_prefix" and not prefix:
+            continue
+        y = dict(x, **{name: x[name].clone()})
+        y[name][key, 0, 5], y[name][key, 1, 63] = float("inf"), -float("inf")
+        out, lse = vlf.vlf_attn_varlen_fwd_prefix(**y, causal=True, flags=flags)
+        assert vlf.vlf_check_error() == 0
+        want = clean.clone()
+        want[rows, :4, 5], want[rows, 4:, 63] = float("inf"), -float("inf")
+        assert torch.equal(out, want) and torch.equal(lse, clean_lse)

@@ -182,8 +182,10 @@ cudaError_t simt_prefix(const PrefixParams &pp, cudaStream_t st) {
 //    fill at most a quarter of a row tile (decode steps).
 //    A softmax warp can only read its own 32 TMEM lanes, so with one row tile a single warp would walk
 //    all 64 columns of each key tile and set the pace.  The rows are loaded four times instead, once
-//    per quarter, and quarter w takes keys 16 w ... 16 w + 15 of each tile (its other weights are zero):
-//    four softmaxes over disjoint keys, a quarter of the work each, joined at the end in shared memory.
+//    per quarter, and quarter w takes keys 16 w ... 16 w + 15 of each tile: four softmaxes over disjoint
+//    keys, a quarter of the work each, joined at the end in shared memory.  The product for 16 keys
+//    writes the lanes of their quarter alone: weights of zero in the others would make NaN of an
+//    infinite value that a row sees.
 //  * Measured, width 128, 32 heads on 8: 64 decode rows behind 16384 shared keys and 100-1024 own ones
 //    50 us (floor 32 us of HBM; a CTA's start and end and about 1 us per key tile); 16 x 64-436 rows
 //    behind 8192 and 436-2048, 530 us (floor 322 us of products; tensor pipe 63%): a key tile's S reads
@@ -447,10 +449,19 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
         if (!ok) break;
         fence_after();
         const uint64_t dv = dv0 + (uint64_t)((sl * C::T_BYTES) >> 4);
+        // (two loops: with a choice in each step the common one's operands left the uniform registers,
+        // 545 us where prefix extensions take 530)
+        if (quad) {
 #pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk)
-          mma_ts_w(tmem + C::O_COL, tmem + 64 * b + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), id,
-                   (n > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            mma_ts_quarter_w(tmem + C::O_COL, tmem + 64 * b + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), id,
+                             n > 0 ? 1u : 0u, kk);
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            mma_ts_w(tmem + C::O_COL, tmem + 64 * b + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), id,
+                     (n > 0 || kk > 0) ? 1u : 0u);
+        }
         mma_commit_w(bar(C::B_O + b));
         mma_commit_w(bar(C::B_VE + sl));
       }
@@ -523,7 +534,7 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
         m_ref = m_new;
       }
       const float m0 = m_ref == -INFINITY ? 0.f : m_ref;
-      uint32_t pk[8], w[32];
+      uint32_t pk[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float pa = ex2(__uint_as_float(v[2 * e]) - m0), pb = ex2(__uint_as_float(v[2 * e + 1]) - m0);
@@ -531,10 +542,8 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
         lf += pa + pb;
         l = add_halves(l, pk[e], is_bf16);
       }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) w[e] = (e >> 3) == quarter ? pk[e & 7] : 0u;
       __syncwarp();
-      tmem_st32(sb, w);
+      tmem_st8(sb + 8 * quarter, pk);  // (this quarter's product reads these columns alone)
       tmem_st_wait();
       fence_before();
       mbar_arrive(bar(C::B_P + b));
