@@ -375,6 +375,10 @@ size_t vlf_noalloc_scratch_bytes(void);
  * points (they stop at "cached decode" with the end-aligned causal rule, mtlattn 0.3.0, "Use", and
  * at a head with a "rope" part, triton-msl part 2, "Latent attention"); they are what a program
  * that serves with the calls above runs next to them.
+ *
+ * total_q and total_kv are below 2^31 - 2^16 in them (VLF_ERR_UNSUPPORTED).  max_seqlen_q and max_seqlen_kv
+ * may be any upper bounds, but how the work is cut goes by them: pass them tight where time counts
+ * (a bound of the longest cache for a batch of short ones costs shared-prefix attention its split).
  */
 
 /*
@@ -409,7 +413,7 @@ int vlf_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
  * count all prefix_len + kv_len keys; row i stands at key i + prefix_len + kv_len - q_len).  The
  * prefix is held and read once for the batch: where it pays, rows of all sequences share its tiles.
  *   k_prefix [prefix_len, h_kv, d_qk], v_prefix [prefix_len, h_kv, d_v]   dtype; prefix_len >= 0,
- *                prefix_len + max_seqlen_kv < 2^31
+ *                prefix_len + max_seqlen_kv < 2^31 - 2^16
  *   workspace    device buffer of at least vlf_attn_varlen_fwd_prefix_workspace_size(...) bytes,
  *                owned by the caller, clobbered (two calls that may overlap need two); may be NULL
  *                where that is 0

@@ -200,3 +200,15 @@ def test_python_refusals():
         a.update(kw)
         with pytest.raises(vlf.VlfError):
             vlf.vlf_cache_evict(**a)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[20000, 9000], [100, 300, 7], [140001]])
+def test_loose_bounds_on_the_lengths(lens):
+    """A longest length that is an upper bound alone, up to the largest int."""
+    for most in (sum(lens), 10 ** 6, 2 ** 31 - 8, 2 ** 31 - 1):
+        run(lens, 2, 64, 64, BF, 64, 4, 16, seed=3, max_kv=most)
+
+
+def test_sizes_next_to_the_largest_int_are_refused():
+    assert _raw(tk=2 ** 31 - 1) == vlf.VLF_ERR_UNSUPPORTED

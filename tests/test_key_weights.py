@@ -239,3 +239,19 @@ def test_python_refusals():
                dict(cu_seqlens_q=cu_of([2, 2]).cuda()), dict(q=x["q"].transpose(0, 1))):
         with pytest.raises(vlf.VlfError):
             vlf.vlf_attn_key_weights(**dict(x, **kw))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("flags", [0, vlf.VLF_FLAG_FORCE_SIMT])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1, 1], [17, 136, 255]), ([90, 150], [190, 201]), ([700], [700])])
+def test_loose_bounds_on_the_lengths(q_lens, kv_lens, flags):
+    """Longest lengths that are upper bounds alone, up to the largest int."""
+    x = make(q_lens, kv_lens, 8, 2, 128, BF, True, 0, seed=1)
+    for mq, mk in ((max(q_lens), 16384), (1000, 100000), (2 ** 31 - 1, 2 ** 31 - 1)):
+        verify(x, vlf.vlf_attn_key_weights(**dict(x, max_seqlen_q=mq, max_seqlen_kv=mk), flags=flags))
+        assert vlf.vlf_check_error() == 0
+
+
+@pytest.mark.parametrize("kw", [dict(tq=2 ** 31 - 1), dict(tk=2 ** 31 - 1)])
+def test_sizes_next_to_the_largest_int_are_refused(kw):
+    assert _raw(**kw) == vlf.VLF_ERR_UNSUPPORTED

@@ -77,6 +77,10 @@ int sm_count() {
   return count[dev];
 }
 
+// The decoding entry points' kernels step over rows and keys with ints, a few tiles past the end at
+// most: they take fewer than 2^31 - 2^16 of them.
+constexpr long long kMostTokens = 0x7fff0000ll;
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Shared argument checks of the forward and backward.  Returns VLF_OK or a negative status.
@@ -599,6 +603,7 @@ size_t vlf_attn_varlen_fwd_prefix_workspace_size(int num_seqs, int total_q, int 
                                                  int h_kv, int d_qk, int d_v, int dtype,
                                                  unsigned flags, int num_sms) {
   if (num_sms <= 0) num_sms = sm_count();
+  if (max_seqlen_q > total_q) max_seqlen_q = total_q;  // (as in the call)
   return vlf::prefix_workspace(num_seqs, total_q, max_seqlen_q, max_seqlen_kv, prefix_len, h_q, h_kv, d_qk,
                                d_v, dtype, flags, num_sms);
 }
@@ -616,10 +621,12 @@ int vlf_attn_varlen_fwd_prefix(const void *q, const void *k_prefix, const void *
   if (st != VLF_OK) return st;
   if (prefix_len < 0 || (prefix_len > 0 && (!k_prefix || !v_prefix))) return VLF_ERR_INVALID;
   if (total_q > 0 && !out) return VLF_ERR_INVALID;
-  if ((long long)prefix_len + max_seqlen_kv > 0x7fffffffll) return VLF_ERR_UNSUPPORTED;
+  if (total_q >= kMostTokens || total_kv >= kMostTokens || (long long)prefix_len + max_seqlen_kv >= kMostTokens)
+    return VLF_ERR_UNSUPPORTED;
   if (!aligned16(k_prefix) || !aligned16(v_prefix) || !aligned16(out) || !aligned16(lse) || !aligned16(workspace))
     return VLF_ERR_ALIGN;
   if (num_seqs == 0 || max_seqlen_q == 0) return VLF_OK;
+  if (total_q > 0 && max_seqlen_q > total_q) max_seqlen_q = total_q;  // (no sequence has more)
   vlf::PrefixParams pp{};
   fill_common(pp.p, q, k, v, cu_seqlens_q, cu_seqlens_kv, num_seqs, total_q, total_kv, max_seqlen_q,
               max_seqlen_kv, h_q, h_kv, d_qk, d_v, dtype, scale, causal, window, nullptr, 0, flags);
@@ -642,6 +649,7 @@ size_t vlf_attn_key_weights_workspace_size(int num_seqs, int total_kv, int max_s
                                            int max_seqlen_kv, int h_q, int h_kv, int d, int dtype,
                                            unsigned flags, int num_sms) {
   if (num_sms <= 0) num_sms = sm_count();
+  if (max_seqlen_kv > total_kv) max_seqlen_kv = total_kv;  // (as in the call)
   return vlf::key_weights_workspace(num_seqs, total_kv, max_seqlen_q, max_seqlen_kv, h_q, h_kv, d, dtype,
                                     flags, num_sms);
 }
@@ -656,8 +664,10 @@ int vlf_attn_key_weights(const void *q, const void *k, const float *lse,
                         max_seqlen_q, max_seqlen_kv, h_q, h_kv, d, d, dtype, nullptr, 0);
   if (st != VLF_OK) return st;
   if ((total_q > 0 && !lse) || (total_kv > 0 && !weights)) return VLF_ERR_INVALID;
+  if (total_q >= kMostTokens || total_kv >= kMostTokens) return VLF_ERR_UNSUPPORTED;
   if (!aligned16(lse) || !aligned16(prev) || !aligned16(weights) || !aligned16(workspace)) return VLF_ERR_ALIGN;
   if (num_seqs == 0 || max_seqlen_kv == 0) return VLF_OK;
+  if (total_kv > 0 && max_seqlen_kv > total_kv) max_seqlen_kv = total_kv;  // (no sequence has more)
   vlf::KeyWeightParams kp{};
   fill_common(kp.p, q, k, nullptr, cu_seqlens_q, cu_seqlens_kv, num_seqs, total_q, total_kv, max_seqlen_q,
               max_seqlen_kv, h_q, h_kv, d, d, dtype, scale, causal, window, nullptr, 0, flags);
@@ -687,14 +697,15 @@ int vlf_cache_evict(const void *k, const void *v, const float *weights,
   if (num_seqs > 0 && (!cu_seqlens_kv || !cu_out)) return VLF_ERR_INVALID;
   if (total_kv > 0 && (!k || !v || !weights)) return VLF_ERR_INVALID;
   if (total_out > 0 && (!k_out || !v_out || !weights_out || !index_out)) return VLF_ERR_INVALID;
-  if (d_qk > 256 || d_v > 256 || num_seqs > 65535 || h_kv > 65535) return VLF_ERR_UNSUPPORTED;
+  if (d_qk > 256 || d_v > 256 || num_seqs > 65535 || h_kv > 65535 || total_kv >= kMostTokens) return VLF_ERR_UNSUPPORTED;
   if (!aligned16(k) || !aligned16(v) || !aligned16(weights) || !aligned16(cu_seqlens_kv) || !aligned16(k_out) ||
       !aligned16(v_out) || !aligned16(weights_out) || !aligned16(index_out) || !aligned16(cu_out))
     return VLF_ERR_ALIGN;
   if (num_seqs == 0) return VLF_OK;
   vlf::EvictParams p{};
   p.k = k; p.v = v; p.weights = weights; p.cu_kv = cu_seqlens_kv;
-  p.num_seqs = num_seqs; p.total_kv = total_kv; p.max_kv = max_seqlen_kv; p.h_kv = h_kv;
+  p.num_seqs = num_seqs; p.total_kv = total_kv; p.h_kv = h_kv;
+  p.max_kv = max_seqlen_kv < total_kv ? max_seqlen_kv : total_kv;  // (no sequence has more)
   p.d_qk = d_qk; p.d_v = d_v; p.dtype = dtype; p.budget = budget; p.sink = sink; p.recent = recent;
   p.total_out = total_out; p.k_out = k_out; p.v_out = v_out; p.weights_out = weights_out;
   p.index = index_out; p.cu_out = cu_out;

@@ -531,7 +531,7 @@ KwPlan make_plan(int num_seqs, int max_q, int max_kv, int h_q, int h_kv, int d, 
     const long long wave = (ctas + room - 1) / room;
     pl.run = (int)(wave <= 32 ? wave : std::min(16ll, std::max(1ll, ctas / (8 * room))));
   } else if (ctas < room) {
-    const long long cols = (long long)((max_q + pl.rows - 1) / pl.rows) * pl.nhb;
+    const long long cols = ((long long)max_q + pl.rows - 1) / pl.rows * pl.nhb;
     pl.splits = (int)std::max<long long>(1, std::min({room / ctas, cols / 4, 65535ll / num_seqs, 32ll}));
   }
   return pl;
