@@ -205,3 +205,49 @@ def test_results_do_not_depend_on_the_native_calls(monkeypatch):
     monkeypatch.setattr(vlf, "_calls", vlf._NoCalls())
     for n, c in calls.items():
         assert all(torch.equal(a, b) for a, b in zip(want[n], as_list(c()))), n
+
+
+class _Huge:
+    """What the Python functions ask of a CUDA tensor, without its memory."""
+    is_cuda, requires_grad = True, False
+
+    def __init__(self, *shape, dtype=BF):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device("cuda", 0)
+
+    def stride(self):
+        return tuple(int(np.prod(self.shape[i + 1:], dtype=np.int64)) for i in range(len(self.shape)))
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return int(np.prod(self.shape, dtype=np.int64))
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 16
+
+
+@pytest.mark.parametrize("n", [2 ** 31, 2 ** 32 + 5])
+def test_sizes_that_no_c_int_holds_are_refused(monkeypatch, n):
+    """2^32 + 5 tokens are not 5."""
+    monkeypatch.setattr(vlf, "_elsewhere", lambda t: False)
+    i32, f32, cu = torch.int32, torch.float32, _Huge(3, dtype=torch.int32)
+    t, few, w = _Huge(n, 2, 8), _Huge(4, 2, 8), _Huge(2, n, dtype=f32)
+    calls = [lambda: vlf.vlf_rope(t, None, _Huge(n, dtype=i32), _Huge(4, dtype=f32)),
+             lambda: vlf.vlf_rope(t, t, _Huge(n, dtype=i32), _Huge(4, dtype=f32)),
+             lambda: vlf.vlf_rope(_Huge(4, n, 8), None, _Huge(4, dtype=i32), _Huge(4, dtype=f32)),
+             lambda: vlf.vlf_attn_varlen_fwd_prefix(t, few, few, few, few, cu, cu, 1, 4),
+             lambda: vlf.vlf_attn_varlen_fwd_prefix(few, t, t, few, few, cu, cu, 1, 4),
+             lambda: vlf.vlf_attn_varlen_fwd_prefix(few, few, few, t, t, cu, cu, 1, 4),
+             lambda: vlf.vlf_attn_key_weights(t, few, w, cu, cu, 1, 4),
+             lambda: vlf.vlf_attn_key_weights(few, t, _Huge(2, 4, dtype=f32), cu, cu, 1, 4),
+             lambda: vlf.vlf_cache_evict(t, t, w, cu, 4, max_seqlen_kv=4, total_out=4)]
+    for call in calls:
+        with pytest.raises(vlf.VlfError, match="out of range"):
+            call()

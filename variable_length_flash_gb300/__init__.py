@@ -623,6 +623,12 @@ def _c_int(x, name):
     return x
 
 
+def _fits(*sizes):
+    """Refuses shapes that no C int holds (ctypes would cut them off)."""
+    if max(sizes) > 0x7fffffff:
+        raise VlfError(VLF_ERR_UNSUPPORTED, f"a size of {max(sizes)} is out of range")
+
+
 _WORKSPACES = {}  # (entry point, shape, device) -> bytes of workspace
 
 
@@ -715,6 +721,7 @@ def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, invers
         _req(positions, "positions", torch.int32), _req(inv_freq, "inv_freq", torch.float32)
         _same_device(q, positions=positions, inv_freq=inv_freq)
         raise VlfError(VLF_ERR_INVALID, "positions must be [tokens] or [axes, tokens], inv_freq [rot / 2]")
+    _fits(total, hq, hk, d, 2 * inv_freq.shape[0])
     # (slices of them start anywhere; the library takes 16-byte aligned pointers)
     if positions.data_ptr() % 16:
         positions = positions.clone()
@@ -811,6 +818,7 @@ def vlf_attn_varlen_fwd_prefix(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seq
     nseq = cu_seqlens_q.numel() - 1
     if nseq != cu_seqlens_kv.numel() - 1 or nseq < 0:
         raise VlfError(VLF_ERR_INVALID, "cu_seqlens_q and cu_seqlens_kv must have num_seqs + 1 entries")
+    _fits(tq, tk, n, nseq, hq, hkv, dqk, dv)
     if max_seqlen_kv is None:
         max_seqlen_kv = _max_len(cu_seqlens_kv)
     if out is None:
@@ -889,6 +897,7 @@ def vlf_attn_key_weights(q, k, lse, cu_seqlens_q, cu_seqlens_kv, max_seqlen_q, m
     nseq = cu_seqlens_q.numel() - 1
     if nseq != cu_seqlens_kv.numel() - 1 or nseq < 0:
         raise VlfError(VLF_ERR_INVALID, "cu_seqlens_q and cu_seqlens_kv must have num_seqs + 1 entries")
+    _fits(tq, tk, nseq, hq, hkv, d)
     if max_seqlen_kv is None:
         max_seqlen_kv = _max_len(cu_seqlens_kv)
     prev_p = None
@@ -962,6 +971,7 @@ def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_
     dv = vs[2]
     if weights.shape != (h, tk):
         raise VlfError(VLF_ERR_INVALID, "weights must be [H_kv, total_kv]")
+    _fits(tk, h, dk, dv, cu_seqlens_kv.numel())
     if max_seqlen_kv is None:
         max_seqlen_kv = _max_len(cu_seqlens_kv)
     n, budget, sink, recent = cu_seqlens_kv.numel() - 1, int(budget), int(sink), int(recent)
