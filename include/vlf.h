@@ -486,7 +486,7 @@ size_t vlf_attn_key_weights_workspace_size(int num_seqs, int total_kv, int max_s
  *   cu_out       int32 [num_seqs + 1]: the cu_seqlens of the outputs (-1 behind a sequence that had
  *                an error; neither it nor the next one is copied).  With num_seqs = 0 nothing is
  *                enqueued, and the one entry is the caller's to set to 0
- * Outputs overlap no input.  d_qk, d_v <= 256.
+ * Outputs overlap neither an input nor one another (VLF_ERR_INVALID).  d_qk, d_v <= 256.
  */
 int vlf_cache_evict(const void *k, const void *v, const float *weights,
                     const int32_t *cu_seqlens_kv, int num_seqs, int total_kv, int max_seqlen_kv,

@@ -212,3 +212,20 @@ def test_loose_bounds_on_the_lengths(lens):
 
 def test_sizes_next_to_the_largest_int_are_refused():
     assert _raw(tk=2 ** 31 - 1) == vlf.VLF_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw", [dict(ko=1 << 20), dict(vo=(1 << 20) + 2032), dict(vo=1 << 20), dict(wo=2 << 20), dict(io=3 << 20),
+                                dict(co=(4 << 20) + 16), dict(ko=5 << 20), dict(wo=(5 << 20) + 1008)])
+def test_outputs_that_overlap_are_refused(kw):
+    """In place, on another input, on another output: k is 8 rows x 2 heads x 64 x 2 bytes at 1 MB."""
+    a = dict(k=1 << 20, v=2 << 20, w=3 << 20, cu=4 << 20, n=4, ko=16, vo=5 << 20, wo=6 << 20, io=7 << 20, co=8 << 20)
+    assert _raw(**dict(a, **kw)) == vlf.VLF_ERR_INVALID
+
+
+@pytest.mark.gpu
+def test_a_cache_is_not_cut_in_place():
+    k, w, cu = torch.randn(300, 2, 64, device="cuda").to(BF), torch.rand(2, 300, device="cuda"), cu_of([100, 200]).cuda()
+    for kw in (dict(k_out=k), dict(v_out=k[:200]), dict(k_out=k[100:]), dict(cu_out=cu), dict(weights_out=w)):
+        rows = kw["k_out"].shape[0] if "k_out" in kw else 300 if "weights_out" in kw else 200
+        with pytest.raises(vlf.VlfError):
+            vlf.vlf_cache_evict(k, k.clone(), w, cu, 100, max_seqlen_kv=200, total_out=rows, **kw)

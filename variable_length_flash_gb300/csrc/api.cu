@@ -702,6 +702,17 @@ int vlf_cache_evict(const void *k, const void *v, const float *weights,
       !aligned16(v_out) || !aligned16(weights_out) || !aligned16(index_out) || !aligned16(cu_out))
     return VLF_ERR_ALIGN;
   if (num_seqs == 0) return VLF_OK;
+  // kept rows are read while others are written: an output shares no byte with an input or another output
+  const size_t es = dtype == VLF_F32 ? 4 : 2, in = (size_t)total_kv * h_kv, to = (size_t)total_out * h_kv;
+  const size_t cu = ((size_t)num_seqs + 1) * 4;
+  const struct { const void *p; size_t n; } all[9] = {
+      {k_out, to * d_qk * es}, {v_out, to * d_v * es}, {weights_out, to * 4}, {index_out, to * 4}, {cu_out, cu},
+      {k, in * d_qk * es}, {v, in * d_v * es}, {weights, in * 4}, {cu_seqlens_kv, cu}};
+  for (int a = 0; a < 5; ++a)
+    for (int b = a + 1; b < 9; ++b) {
+      const uintptr_t x = (uintptr_t)all[a].p, y = (uintptr_t)all[b].p;
+      if (all[a].n && all[b].n && x < y + all[b].n && y < x + all[a].n) return VLF_ERR_INVALID;
+    }
   vlf::EvictParams p{};
   p.k = k; p.v = v; p.weights = weights; p.cu_kv = cu_seqlens_kv;
   p.num_seqs = num_seqs; p.total_kv = total_kv; p.h_kv = h_kv;
