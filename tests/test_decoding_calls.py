@@ -251,3 +251,10 @@ def test_sizes_that_no_c_int_holds_are_refused(monkeypatch, n):
     for call in calls:
         with pytest.raises(vlf.VlfError, match="out of range"):
             call()
+
+
+def test_an_output_without_its_input_is_refused(monkeypatch):
+    monkeypatch.setattr(vlf, "_elsewhere", lambda t: False)
+    q, out = _Huge(4, 2, 8), _Huge(4, 2, 8)
+    with pytest.raises(vlf.VlfError, match="k_out without k"):
+        vlf.vlf_rope(q, None, _Huge(4, dtype=torch.int32), _Huge(4, dtype=torch.float32), q_out=out, k_out=_Huge(4, 1, 8))

@@ -755,6 +755,8 @@ def vlf_rope(q, k, positions, inv_freq, sections=None, interleaved=False, invers
         if k.get_device() != dev or k_out.get_device() != dev:
             _same_device(q, k=k, k_out=k_out)
         ko_p = k_out.data_ptr()
+    elif k_out is not None:
+        raise VlfError(VLF_ERR_INVALID, "k_out without k")
     st = _lib.vlf_rope(q.data_ptr(), sq, k_p, sk, positions.data_ptr(), axes, sec, inv_freq.data_ptr(),
                        total, hq, hk, d, 2 * inv_freq.shape[0], dt, 1 if interleaved else 0,
                        1 if inverse else 0, q_out.data_ptr(), sqo, ko_p, sko, _stream(stream, q))
