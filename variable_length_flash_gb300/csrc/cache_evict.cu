@@ -10,8 +10,9 @@
 // weights as order-preserving 32-bit keys (the protected ones above all), the counts of the leading
 // digit among those that still match, the digit in which the n-th falls, on to the next digit; then
 // one ordered pass writes the indices that stay.  A cluster of up to eight CTAs shares a long sequence:
-// each keeps its share of the keys in registers (one read of the weights from HBM) and the counts
-// are summed through distributed shared memory.  The gather copies the kept rows of K
+// each keeps its share of the keys on chip (one read of the weights from HBM): in registers up to 8 keys
+// per thread, beyond that some of them in local memory (64 registers a thread; 36 and 56 bytes of
+// spills at 16 keys, 172 and 220 at 32).  The counts are summed through distributed shared memory.  The gather copies the kept rows of K
 // and V and is the bulk of the work: bound by HBM, every kept row read once and written once.
 // Measured: 64 x 4096-8192 keys of 8 heads of 128 in bf16 cut to 2048, 206 us (gather 175, selection
 // 30: the latency of its 6 + 2 counting steps, a read of 12 MB); one list of 131071 keys cut to
@@ -424,7 +425,8 @@ cudaError_t cache_evict(const EvictParams &p, cudaStream_t st) {
   if (copy || most == 0 || p.total_out == 0) return cudaSuccess;
   const int b = whole ? 16 : es;
   int rk = p.d_qk * es / b, rv = p.d_v * es / b;
-  // rounds of a block: as many, up to eight, as leave eight blocks per SM
+  // rounds of a block: as many, up to eight, as leave a grid of eight blocks per SM (four are resident,
+  // by their 64 registers a thread)
   const long long run = std::max(1, 256 / (rk + rv)) * kUnroll, runs = (most * p.h_kv + run - 1) / run;
   int rounds = (int)std::max(1ll, std::min(8ll, runs * p.num_seqs / (152 * 8)));
   const long long x = (runs + rounds - 1) / rounds;

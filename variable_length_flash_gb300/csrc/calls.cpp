@@ -4,8 +4,10 @@
 // ten tensors, allocates its outputs and goes through ctypes costs 13 to 24 us, three to four times
 // the kernel; these calls take 5 to 11.  The functions here do the same for plain CUDA tensors and
 // library-allocated outputs: test the arguments, allocate with torch's allocator, call the C entry
-// point on the current stream of the tensors' device, whichever device is the current one.  They return None, having done nothing that counts, for whatever is not such a call or is refused;
-// the Python function behind them then takes its own way, which says what was wrong.
+// point on the current stream of the tensors' device, whichever device is the current one.  They return
+// None, having done nothing that counts, for whatever is not such a call or is refused; the Python
+// function behind them then takes its own way, which says what was wrong.  What a call has to meet is
+// tested on both ways and has to stay alike on both.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

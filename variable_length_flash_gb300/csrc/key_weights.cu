@@ -121,7 +121,7 @@ cudaError_t simt_key_weights(const KeyWeightParams &kp, cudaStream_t st) {
 //    registers until the last.  Where the key tiles alone leave SMs idle, the column tiles are cut
 //    into parts whose sums a second kernel adds in order.
 // Measured, bf16 / fp16, width 128: 64 decode rows of 32 heads against 1-8k keys of 8 kv heads 95 us
-// (97% of the copy rate); 4 x 32 rows against 12-32k keys 37 us (76%: the rest is the CTAs' start and
+// (97% of the copy rate); 4 x 32 rows against 12-32k keys 37 us (77%: the rest is the CTAs' start and
 // end, one wave of them); 4 x 4096 causal rows, 32 heads, 271 us against 145 us of products: tensor
 // pipe 47% of its cycles, exponentials 47%, issue slots 56%, and per score tile two CTAs of an SM
 // wait for one another's products, TMEM loads and exponentials in turn.  Tried and slower: score
@@ -395,7 +395,8 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
           if (lane == 0) mbar_arrive(bar(B_SE + wg));
         };
         // Adds the W columns from c on, loaded into v; FULL: every key of the warp sees all of them, and
-        // all have an lse.
+        // all have an lse.  (All 128: groups of 3, 5, 6 and 7 heads, whose tiles hold 125 or 126 rows, go
+        // through the selects on every tile.)
         auto add = [&](auto width, auto whole, const uint32_t *v, int c) {
           constexpr int W = decltype(width)::value;
           constexpr bool FULL = decltype(whole)::value;
@@ -527,7 +528,10 @@ KwPlan make_plan(int num_seqs, int max_q, int max_kv, int h_q, int h_kv, int d, 
     // One wave of CTAs where that takes at most 32 tiles each (a CTA's start and end cost about three
     // tiles), else runs of at most 16, whose many waves even out ragged lengths.  Measured: 4 x 32
     // rows against up to 32k keys 35 us in one wave (27 tiles), 38 with 6 or 13 tiles, 43 with 3 or 16;
-    // 64 decode rows against up to 8k keys 95 us with 13 tiles, 98 with 16 or more, 109 with 64.
+    // 64 decode rows against up to 8k keys 95 us with 13 tiles, 98 with 16 or more, 109 with 64.  The rule
+    // has a step where one wave ends, which costs: 64 decode rows, 8 kv heads, against 2432 keys each 53 us
+    // with 32 tiles, against 2500 keys 61 us with 4 (6230 and 5530 GB/s); from 3500 keys on (5 tiles,
+    // 76 us) the rate is back, at 4096 keys (6 tiles) 86 us, at 8192 (13 tiles) 165 us.
     const long long wave = (ctas + room - 1) / room;
     pl.run = (int)(wave <= 32 ? wave : std::min(16ll, std::max(1ll, ctas / (8 * room))));
   } else if (ctas < room) {

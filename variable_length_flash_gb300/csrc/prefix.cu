@@ -602,7 +602,9 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
         return fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
       };
       // Unmasked tile and a reference max in every row of the warp: P with that reference, the row
-      // max beside it; only a max beyond the threshold goes through the general pass.
+      // max beside it; only a max beyond the threshold goes through the general pass.  (Lanes that hold
+      // no row, the last two or three with groups of 3, 5, 6 or 7 heads, have neither: their warp takes
+      // the general pass on every tile.)
       bool done = false;
       if (__all_sync(0xffffffffu, full && m_ref != -INFINITY)) {
         exp_pass(sl2, -m_ref);
@@ -847,7 +849,10 @@ bool tc_shape(int d_qk, int d_v, int dtype, unsigned flags) {
          (d_qk == 64 || d_qk == 96 || d_qk == 128);
 }
 
-// How the work is cut, by sizes alone (the lengths are on the device).  Costs in tenths of a
+// How the work is cut, by sizes alone (the lengths are on the device: every sequence counts with the
+// longest length, so that a loose bound or one long sequence makes fewer prefix parts, or none: the 64
+// decode rows below get 6 of them with a bound of 1024 own keys, 3 with 4096, no shared part with 16384).
+// Costs in tenths of a
 // microsecond: a key tile takes a CTA about 1 us whatever else runs (10; 4 with quarter tiles), the
 // busiest of the resident CTA slots (two per SM) sets the time, and merging costs a launch and the
 // traffic of the parts (30 and 1 per 0.6 MB).

@@ -19,9 +19,9 @@
 // once and applies them to `hpt` consecutive heads.  The fp64 products, which this chip is slow at,
 // run once per pair and block (a table in shared memory; done by each thread they took 94 us where
 // this takes 65), and a block walks several runs of tokens.  Measured: 20011 tokens of 40 heads of
-// 128 in bf16, sliced from a fused projection, 65 us = 93% of the copy rate; 16384 tokens of 32 heads
-// of 96 in fp16, 64 columns of which turn, 35 us = 84% (short rows: fewer bytes in flight per
-// thread); 64 tokens 3 us, which is a launch.
+// 128 in bf16, sliced from a fused projection, 65 us = 94% of the copy rate; 16384 tokens of 32 heads
+// of 96 in fp16, 64 columns of which turn, 35 us = 85% (segments of 64 bytes, and 782 blocks where 304 are
+// resident: the third wave is half full); 64 tokens 3 us, which is a launch.
 #include <type_traits>
 
 #include "common.cuh"
@@ -194,14 +194,16 @@ cudaError_t launch(RopeParams p, cudaStream_t st) {
   const int units = p.rot / 2 / v + (p.copy_tail ? ((p.d - p.rot + v - 1) / v + 1) / 2 : 0);
   if (units == 0) return cudaSuccess;  // nothing turns, and the rest is already in place
   // Heads per thread: 16 (the trigonometry is then a small share) where that still gives every one of
-  // the 152 SMs a block, fewer for a decode step's few tokens, where the heads are the parallelism (908 tokens of 40
-  // heads: 6.4 us with four heads each, 8.3 and 12.4 us when two or four blocks per SM were asked for).
+  // the 152 SMs a block, fewer for a decode step's few tokens, where the heads are the parallelism (908
+  // tokens of 40 heads: 6.4 us with four heads each, 8.3 and 12.4 us when two or four blocks per SM were
+  // asked for).
   const long long runs = ((long long)p.total + 256 / units - 1) / (256 / units);
   auto phases = [&](int hpt) { return (p.h_q + hpt - 1) / hpt + (p.h_k + hpt - 1) / hpt; };
   p.hpt = 16;
   while (p.hpt > 1 && runs * phases(p.hpt) < 152) p.hpt /= 2;
   while (phases(p.hpt) > 65535) p.hpt *= 2;
-  // up to eight blocks per SM, each with the same number of runs
+  // a grid of up to eight blocks per SM, each with the same number of runs (resident are two of the
+  // kernel with eight heads in flight, 128 registers, and three with two, 74-80)
   const long long y = phases(p.hpt), turns = (runs * y + 152 * 8 - 1) / (152 * 8);
   const dim3 grid((unsigned)((runs + turns - 1) / turns), (unsigned)y);
   // (eight heads in flight take 64 registers of data: where a thread has fewer, more blocks fit instead)
