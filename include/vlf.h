@@ -413,7 +413,7 @@ int vlf_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
  * count all prefix_len + kv_len keys; row i stands at key i + prefix_len + kv_len - q_len).  The
  * prefix is held and read once for the batch: where it pays, rows of all sequences share its tiles.
  *   k_prefix [prefix_len, h_kv, d_qk], v_prefix [prefix_len, h_kv, d_v]   dtype; prefix_len >= 0,
- *                prefix_len + max_seqlen_kv < 2^31 - 2^16
+ *                with the longest own length, min(max_seqlen_kv, total_kv), below 2^31 - 2^16
  *   workspace    device buffer of at least vlf_attn_varlen_fwd_prefix_workspace_size(...) bytes,
  *                owned by the caller, clobbered (two calls that may overlap need two); may be NULL
  *                where that is 0

@@ -621,8 +621,8 @@ int vlf_attn_varlen_fwd_prefix(const void *q, const void *k_prefix, const void *
   if (st != VLF_OK) return st;
   if (prefix_len < 0 || (prefix_len > 0 && (!k_prefix || !v_prefix))) return VLF_ERR_INVALID;
   if (total_q > 0 && !out) return VLF_ERR_INVALID;
-  if (total_q >= kMostTokens || total_kv >= kMostTokens || (long long)prefix_len + max_seqlen_kv >= kMostTokens)
-    return VLF_ERR_UNSUPPORTED;
+  const long long own = max_seqlen_kv < total_kv ? max_seqlen_kv : total_kv;  // (no sequence has more keys)
+  if (total_q >= kMostTokens || total_kv >= kMostTokens || prefix_len + own >= kMostTokens) return VLF_ERR_UNSUPPORTED;
   if (!aligned16(k_prefix) || !aligned16(v_prefix) || !aligned16(out) || !aligned16(lse) || !aligned16(workspace))
     return VLF_ERR_ALIGN;
   if (num_seqs == 0 || max_seqlen_q == 0) return VLF_OK;
