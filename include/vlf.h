@@ -57,7 +57,8 @@ typedef enum {
   VLF_ERR_LAUNCH = -4,      /* the CUDA runtime refused a launch or a query */
   VLF_ERR_TIMEOUT = -5,     /* device: a pipeline wait exceeded its time limit (kernel bailed out) */
   VLF_ERR_BAD_SEQLENS = -6, /* device: cu_seqlens not in [0, total], decreasing, or longer than max_seqlen */
-  VLF_ERR_WORKSPACE = -7    /* a workspace missing or smaller than its size query returns */
+  VLF_ERR_WORKSPACE = -7,   /* a workspace missing or smaller than its size query returns */
+  VLF_ERR_BAD_PAGES = -8    /* device: a page outside the pool, or tables and counts that disagree */
 } vlf_status;
 
 /* Extended-call flags (vlf_attn_varlen_fwd_ex / _bwd_ex). */
@@ -493,6 +494,165 @@ int vlf_cache_evict(const void *k, const void *v, const float *weights,
                     int h_kv, int d_qk, int d_v, int dtype, int budget, int sink, int recent,
                     int total_out, void *k_out, void *v_out, float *weights_out,
                     int32_t *index_out, int32_t *cu_out, vlf_stream_t stream);
+
+/*
+ * Serving from a cache of pages in 8 bits: the norm of queries and keys with their positions, the pages
+ * that hold keys and values, attention over them, and the tables that say which sequence has which
+ * pages.  The pages have no counterpart to these entry points either.
+ *
+ * The cache of a layer:
+ *   k_pages      e4m3 (one byte: sign, 4 exponent and 3 mantissa bits, no infinities, 0x7f and 0xff are
+ *                NaN) [num_pages, h_kv, page, d_qk]; v_pages the same with d_v
+ *   k_scale, v_scale   fp32 [num_pages, h_kv]: a value is its byte's times its page's and head's scale.
+ *                Scales are powers of two from 2^-64 on (those that vlf_pages_write leaves)
+ *   page         16, 32, 64, 128 or 256 tokens (VLF_ERR_UNSUPPORTED otherwise)
+ *   page_table   int32 [num_seqs, max_pages]: key j of sequence s is slot j % page of page
+ *                page_table[s][j / page]; entries behind a sequence's last page are not looked at
+ *   seqlens_kv   int32 [num_seqs], at most max_pages * page
+ * max_pages * page and the numbers of tokens are below 2^31 - 2^16; d_qk, d_v <= 256.  A page that is needed
+ * and lies outside 0..num_pages - 1 records VLF_ERR_BAD_PAGES and is passed over, a sequence whose lengths
+ * are out of range VLF_ERR_BAD_SEQLENS.
+ */
+
+/*
+ * Root-mean-square norm of each head of q and k, and the rotary positions of vlf_rope, in one pass:
+ *   y = R(t) (w o x / sqrt(mean(x^2) + eps)),
+ * the mean over the head's d columns.
+ *   q_weight, k_weight   [d] of type weight_dtype (`dtype` or VLF_F32), for every head; NULL: ones
+ *   eps          >= 0, finite
+ *   others       as in vlf_rope (rot = 0, positions and inv_freq NULL: the norm alone)
+ * The arithmetic is fp32, the result is rounded once.
+ */
+int vlf_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                  const void *q_weight, const void *k_weight, int weight_dtype, float eps,
+                  const int32_t *positions, int n_axes, const int *sections, const float *inv_freq,
+                  int total, int h_q, int h_k, int d, int rot, int dtype, int interleaved,
+                  void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride,
+                  vlf_stream_t stream);
+
+/*
+ * Its gradients: of sum(q_out o dq_out) + sum(k_out o dk_out) with respect to q, k and the weights.
+ *   dq_out, dk_out   gradients of the outputs, dtype, with strides of their own
+ *   dq, dk       as q, k (written); may be dq_out / dk_out or q / k (same pointer and stride)
+ *   dq_weight, dk_weight   [d] of type weight_dtype (written), or NULL: not wanted.  The sums over tokens
+ *                and heads are fp32, in a fixed order, rounded once
+ *   workspace    at least vlf_norm_rope_bwd_workspace_size(d) bytes where a weight's gradient is
+ *                wanted; owned by the caller, clobbered (two calls that may overlap need two)
+ */
+int vlf_norm_rope_bwd(const void *dq_out, int64_t dq_out_stride, const void *dk_out,
+                      int64_t dk_out_stride, const void *q, int64_t q_stride, const void *k,
+                      int64_t k_stride, const void *q_weight, const void *k_weight, int weight_dtype,
+                      float eps, const int32_t *positions, int n_axes, const int *sections,
+                      const float *inv_freq, int total, int h_q, int h_k, int d, int rot, int dtype,
+                      int interleaved, void *dq, int64_t dq_stride, void *dk, int64_t dk_stride,
+                      void *dq_weight, void *dk_weight, void *workspace, size_t workspace_bytes,
+                      vlf_stream_t stream);
+size_t vlf_norm_rope_bwd_workspace_size(int d);
+
+/*
+ * New tokens into their pages.  Token i of sequence s becomes key seqlens_kv[s] - n + i of it, n =
+ * cu_seqlens[s + 1] - cu_seqlens[s]: seqlens_kv counts the new tokens, and the same two tensors describe
+ * the queries of these tokens to vlf_attn_varlen_fwd_pages.
+ *   k [total, h_kv, d_qk], v [total, h_kv, d_v]   dtype; heads and columns of a token are dense, tokens
+ *                k_stride / v_stride elements apart
+ * A page's scale (each head's for itself) is the smallest power of two, 2^-64 at least, times which 448
+ * holds the largest new value of the page, or the scale that the page has where that is larger: then the
+ * bytes of the page that are not written anew are multiplied by old / new and rounded again, which costs
+ * them nothing but what falls below e4m3's least step.  A call that writes slot 0 of a page begins
+ * it: the scale that it had does not count, and its other bytes stay as they are.  Values are rounded to
+ * nearest, ties to even.  A value that is not finite is held as a NaN and does not count for the scale.
+ * Each page that is written belongs to one sequence (vlf_pages_fork sees to it); where two tokens of a
+ * call reach the same slot, either may be left.
+ */
+int vlf_pages_write(const void *k, int64_t k_stride, const void *v, int64_t v_stride, void *k_pages,
+                    void *v_pages, float *k_scale, float *v_scale, const int32_t *page_table,
+                    const int32_t *cu_seqlens, const int32_t *seqlens_kv, int num_seqs, int total,
+                    int max_pages, int num_pages, int page, int h_kv, int d_qk, int d_v, int dtype,
+                    vlf_stream_t stream);
+
+/*
+ * Attention over the pages: out and lse are those of vlf_attn_varlen_fwd on the keys and values that the
+ * bytes stand for, without a bias.
+ *   q, cu_seqlens_q, total_q, max_seqlen_q, heads, dtype, scale, causal, window, out, lse   as there
+ *   workspace    at least vlf_attn_varlen_fwd_pages_workspace_size(...) bytes, owned by the caller,
+ *                clobbered (two calls that may overlap need two); may be NULL where that is 0
+ *   flags        VLF_FLAG_FORCE_SIMT; others are ignored
+ * Pages of which no row of a sequence sees a key (in front of the window) are not looked at and may be
+ * outside the pool.  What other bytes of a page hold never reaches a row, but a value of its own sequence
+ * that is NaN may also reach rows that do not see its key.  A row that sees a NaN logit is NaN, and so is
+ * its lse.  Tensor-core kernels for F16 / BF16 and d_qk = d_v in {64, 128}; fp32 FMA otherwise.  No
+ * backward.
+ */
+int vlf_attn_varlen_fwd_pages(const void *q, const void *k_pages, const void *v_pages,
+                              const float *k_scale, const float *v_scale, const int32_t *page_table,
+                              const int32_t *cu_seqlens_q, const int32_t *seqlens_kv, int num_seqs,
+                              int total_q, int max_seqlen_q, int max_pages, int num_pages, int page,
+                              int h_q, int h_kv, int d_qk, int d_v, int dtype, float scale, int causal,
+                              int window, void *out, float *lse, void *workspace,
+                              size_t workspace_bytes, vlf_stream_t stream, unsigned flags);
+
+/* Bytes of workspace vlf_attn_varlen_fwd_pages needs: a rule on these sizes and the SM count
+ * (num_sms <= 0: the current device's); 0 for invalid sizes. */
+size_t vlf_attn_varlen_fwd_pages_workspace_size(int num_seqs, int total_q, int max_seqlen_q, int h_q,
+                                                int h_kv, int d_qk, int d_v, int dtype, unsigned flags,
+                                                int num_sms);
+
+/*
+ * Pages copied: page src[i] (keys, values and scales of every head) over page dst[i], for each i with
+ * src[i] >= 0.  A page is in dst at most once and not in src as well (what it then holds is not
+ * defined).  src and dst are int32 [n], on the device: the lists of the two calls below.
+ */
+int vlf_pages_copy(void *k_pages, void *v_pages, float *k_scale, float *v_scale, const int32_t *src,
+                   const int32_t *dst, int n, int num_pages, int page, int h_kv, int d_qk, int d_v,
+                   vlf_stream_t stream);
+
+/*
+ * The page tables of the next step.  New row s follows the old row parents[s] (the same row: it goes on;
+ * several with one parent: it forks; a row that is no one's parent: its pages are released), or none
+ * (parents[s] < 0: it begins empty), and gets room for grow[s] more tokens.
+ *   page_table [num_in, max_pages], seqlens [num_in]   the old rows
+ *   refs         int32 [num_pages]: how many hold each page: old rows, and others (a prompt kept for
+ *                later); 0: the page is free
+ *   parents, grow   int32 [num_out], grow >= 0
+ *   table_out    [num_out, max_pages] (-1 behind a row's last page); seqlens_out [num_out], the parent's
+ *                plus grow; refs_out [num_pages], in which new rows stand for the old ones
+ *   src, dst     int32 [num_out]: the copies to make before anything is written, for vlf_pages_copy of
+ *                each layer (-1: none)
+ *   left         int32 [1]: free pages left
+ * Whole pages are shared.  A page that is not full has one holder: the first new row that goes on in it
+ * keeps it, if no one else holds it, and every other gets a copy.  New pages are the free ones in
+ * ascending order, for the rows in order, a row's copy first.
+ * Where more pages are needed than are free, left is negative (their number) and nothing else happens:
+ * table_out is -1 throughout, seqlens_out 0, refs_out is refs, src and dst are -1.  So it is, with left =
+ * INT32_MIN, after an error: VLF_ERR_BAD_SEQLENS (a length or grow negative or beyond max_pages * page),
+ * VLF_ERR_BAD_PAGES (a parent or page out of range, refs below the old rows' holds).
+ *   workspace    at least vlf_pages_fork_workspace_size(num_pages, num_out) bytes, owned by the caller,
+ *                clobbered (two calls that may overlap need two)
+ * Outputs overlap no input and not one another (VLF_ERR_INVALID).
+ */
+int vlf_pages_fork(const int32_t *page_table, const int32_t *seqlens, const int32_t *refs,
+                   const int32_t *parents, const int32_t *grow, int num_in, int num_out, int max_pages,
+                   int num_pages, int page, int32_t *table_out, int32_t *seqlens_out, int32_t *refs_out,
+                   int32_t *src, int32_t *dst, int32_t *left, void *workspace, size_t workspace_bytes,
+                   vlf_stream_t stream);
+size_t vlf_pages_fork_workspace_size(int num_pages, int num_out);
+
+/*
+ * The U pages in use (refs > 0) moved into the first U of the pool: those behind move into the free ones
+ * among the first U, in order.
+ *   page_table [num_seqs, max_pages], refs [num_pages]   as above
+ *   table_out    the tables afterwards: entries that name a page in use follow it, others become -1
+ *   refs_out [num_pages]; to int32 [num_pages]: where each page in use is afterwards (-1: it was free)
+ *   src, dst     int32 [num_pages / 2]: the copies to make, for vlf_pages_copy of each layer; -1 behind them
+ *   used         int32 [1]: U
+ *   workspace    at least vlf_pages_compact_workspace_size(num_pages) bytes, as above
+ * Outputs overlap no input and not one another (VLF_ERR_INVALID).
+ */
+int vlf_pages_compact(const int32_t *page_table, const int32_t *refs, int num_seqs, int max_pages,
+                      int num_pages, int32_t *table_out, int32_t *refs_out, int32_t *to, int32_t *src,
+                      int32_t *dst, int32_t *used, void *workspace, size_t workspace_bytes,
+                      vlf_stream_t stream);
+size_t vlf_pages_compact_workspace_size(int num_pages);
 
 /* Library version, major * 10000 + minor * 100 + patch. */
 int vlf_version(void);

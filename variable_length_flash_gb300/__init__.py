@@ -14,7 +14,12 @@ The functions carry the names of the C entry points in ``include/vlf.h``:
 * next to them, for decoding on a bounded cache, ``vlf_rope`` (rotary positions with several axes),
   ``vlf_attn_varlen_fwd_prefix`` (attention behind a prefix that the batch shares),
   ``vlf_attn_key_weights`` (the attention weight each key received) and ``vlf_cache_evict`` (the
-  cache cut down to a budget by it).
+  cache cut down to a budget by it);
+* for serving from a cache of pages in 8 bits, ``vlf_norm_rope`` / ``vlf_norm_rope_bwd`` (the norm of
+  each head with its rotary positions, and its gradients), ``vlf_pages_write`` (new tokens into their
+  pages), ``vlf_attn_varlen_fwd_pages`` (attention over them), ``vlf_pages_fork`` and
+  ``vlf_pages_compact`` (the sequences' page tables: going on, forking, ending, moving together) and
+  ``vlf_pages_copy`` (the copies that those ask for).
 
 The operation is the varlen attention of the mtlattn 0.3.0 page (section "Use"): packed
 q/k/v [tokens, heads, head_dim] with int32 cu_seqlens, end-aligned causal, sliding window,
@@ -35,7 +40,7 @@ LIB_PATH = os.path.join(_HERE, "libvlf.so")
 VLF_F16, VLF_BF16, VLF_F32 = 0, 1, 2
 VLF_OK = 0
 VLF_ERR_INVALID, VLF_ERR_UNSUPPORTED, VLF_ERR_ALIGN, VLF_ERR_LAUNCH = -1, -2, -3, -4
-VLF_ERR_TIMEOUT, VLF_ERR_BAD_SEQLENS, VLF_ERR_WORKSPACE = -5, -6, -7
+VLF_ERR_TIMEOUT, VLF_ERR_BAD_SEQLENS, VLF_ERR_WORKSPACE, VLF_ERR_BAD_PAGES = -5, -6, -7, -8
 VLF_FLAG_NO_SKIP = 1
 VLF_FLAG_FORCE_SIMT = 2
 VLF_FLAG_NO_PACK = 4
@@ -52,7 +57,10 @@ EXPORTS = ["vlf_attn_varlen_fwd", "vlf_attn_varlen_fwd_ex", "vlf_attn_varlen_bwd
            "vlf_attn_varlen_bwd_latent", "vlf_attn_varlen_bwd_latent_workspace_size",
            "vlf_bias_bands", "vlf_bias_bands_size", "vlf_rope", "vlf_attn_varlen_fwd_prefix",
            "vlf_attn_varlen_fwd_prefix_workspace_size", "vlf_attn_key_weights",
-           "vlf_attn_key_weights_workspace_size", "vlf_cache_evict"]
+           "vlf_attn_key_weights_workspace_size", "vlf_cache_evict", "vlf_norm_rope", "vlf_norm_rope_bwd",
+           "vlf_norm_rope_bwd_workspace_size", "vlf_pages_write", "vlf_attn_varlen_fwd_pages",
+           "vlf_attn_varlen_fwd_pages_workspace_size", "vlf_pages_copy", "vlf_pages_fork",
+           "vlf_pages_fork_workspace_size", "vlf_pages_compact", "vlf_pages_compact_workspace_size"]
 VLF_BWD_STAGES = 3
 BWD_STAGE_NAMES = ["rowdot", "dkdv", "dq"]
 
@@ -124,6 +132,30 @@ def _load():
     lib.vlf_attn_key_weights_workspace_size.restype = Z
     lib.vlf_cache_evict.argtypes = [P] * 4 + [I] * 11 + [P] * 6
     lib.vlf_cache_evict.restype = I
+    where = [P, I, P, P]  # positions, axes, sections, inv_freq
+    lib.vlf_norm_rope.argtypes = [P, L, P, L, P, P, I, F] + where + [I] * 7 + [P, L, P, L, P]
+    lib.vlf_norm_rope.restype = I
+    lib.vlf_norm_rope_bwd.argtypes = ([P, L] * 4 + [P, P, I, F] + where + [I] * 7 + [P, L, P, L] +
+                                      [P, P, P, Z, P])
+    lib.vlf_norm_rope_bwd.restype = I
+    lib.vlf_norm_rope_bwd_workspace_size.argtypes = [I]
+    lib.vlf_norm_rope_bwd_workspace_size.restype = Z
+    lib.vlf_pages_write.argtypes = [P, L, P, L] + [P] * 7 + [I] * 9 + [P]
+    lib.vlf_pages_write.restype = I
+    lib.vlf_attn_varlen_fwd_pages.argtypes = [P] * 8 + [I] * 11 + [F, I, I, P, P, P, Z, P, U]
+    lib.vlf_attn_varlen_fwd_pages.restype = I
+    lib.vlf_attn_varlen_fwd_pages_workspace_size.argtypes = [I] * 8 + [U, I]
+    lib.vlf_attn_varlen_fwd_pages_workspace_size.restype = Z
+    lib.vlf_pages_copy.argtypes = [P] * 6 + [I] * 6 + [P]
+    lib.vlf_pages_copy.restype = I
+    lib.vlf_pages_fork.argtypes = [P] * 5 + [I] * 5 + [P] * 7 + [Z, P]
+    lib.vlf_pages_fork.restype = I
+    lib.vlf_pages_fork_workspace_size.argtypes = [I, I]
+    lib.vlf_pages_fork_workspace_size.restype = Z
+    lib.vlf_pages_compact.argtypes = [P, P, I, I, I] + [P] * 7 + [Z, P]
+    lib.vlf_pages_compact.restype = I
+    lib.vlf_pages_compact_workspace_size.argtypes = [I]
+    lib.vlf_pages_compact_workspace_size.restype = Z
     lib.vlf_noalloc_scratch_bytes.argtypes = []
     lib.vlf_noalloc_scratch_bytes.restype = Z
     lib.vlf_launch_count.argtypes = []
@@ -154,7 +186,11 @@ def _load_calls(lib):
         return _NoCalls()
     _calls.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.vlf_rope, lib.vlf_attn_varlen_fwd_prefix, lib.vlf_attn_varlen_fwd_prefix_workspace_size,
-        lib.vlf_attn_key_weights, lib.vlf_attn_key_weights_workspace_size, lib.vlf_cache_evict)])
+        lib.vlf_attn_key_weights, lib.vlf_attn_key_weights_workspace_size, lib.vlf_cache_evict,
+        lib.vlf_norm_rope, lib.vlf_norm_rope_bwd, lib.vlf_norm_rope_bwd_workspace_size, lib.vlf_pages_write,
+        lib.vlf_attn_varlen_fwd_pages, lib.vlf_attn_varlen_fwd_pages_workspace_size, lib.vlf_pages_copy,
+        lib.vlf_pages_fork, lib.vlf_pages_fork_workspace_size, lib.vlf_pages_compact,
+        lib.vlf_pages_compact_workspace_size)])
     return _calls
 
 
@@ -1014,6 +1050,421 @@ def vlf_cache_evict(k, v, weights, cu_seqlens_kv, budget, sink=0, recent=0, max_
     return outs
 
 
+# ------------------------------------------------------------------ serving from a cache of pages in 8 bits
+_I32, _F32, _E4M3 = torch.int32, torch.float32, getattr(torch, "float8_e4m3fn", None)
+
+
+def _at16(t):
+    """t, or a copy of a slice that starts anywhere: the library takes 16-byte aligned pointers."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _room(workspace, need, like):
+    """(pointer, bytes) of the caller's workspace, or of one allocated here, and the tensor to keep."""
+    if workspace is None:
+        if need <= 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    else:
+        _req(workspace, "workspace"), _same_device(like, workspace=workspace)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _turns(like, total, positions, inv_freq, sections):
+    """The arguments of the rotary positions, checked: (positions, axes, sections, inv_freq, rot); positions
+    and inv_freq may be None, for none."""
+    if positions is None or inv_freq is None:
+        if positions is not None or inv_freq is not None or sections is not None:
+            raise VlfError(VLF_ERR_INVALID, "positions and inv_freq go together")
+        return None, 1, None, None, 0
+    _req(positions, "positions", _I32), _req(inv_freq, "inv_freq", _F32)
+    _same_device(like, positions=positions, inv_freq=inv_freq)
+    if not 1 <= positions.dim() <= 2 or positions.shape[-1] != total or inv_freq.dim() != 1:
+        raise VlfError(VLF_ERR_INVALID, "positions must be [tokens] or [axes, tokens], inv_freq [rot / 2]")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if sections is None:
+        if axes != 1:
+            raise VlfError(VLF_ERR_INVALID, "several position axes need sections")
+    elif len(sections) != axes:
+        raise VlfError(VLF_ERR_INVALID, f"{len(sections)} sections for {axes} position axes")
+    _fits(axes, 2 * inv_freq.shape[0])
+    return positions, axes, None if sections is None else _sections(sections), inv_freq, 2 * inv_freq.shape[0]
+
+
+def _norm_weights(like, q_weight, k_weight, d):
+    """Checks the weights and returns their type (the same for both)."""
+    dtype = None
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is None:
+            continue
+        _given(w, name, (d,), dtype)
+        if w.dtype not in (like.dtype, _F32):
+            raise VlfError(VLF_ERR_INVALID, f"{name} must be {like.dtype} or {_F32}, got {w.dtype}")
+        _same_device(like, **{name: w})
+        dtype = w.dtype
+    return like.dtype if dtype is None else dtype
+
+
+def _eps(eps):
+    eps = float(eps)
+    if not 0.0 <= eps < 3.4e38:
+        raise VlfError(VLF_ERR_INVALID, f"eps = {eps} is out of range")
+    return eps
+
+
+def _rows_like(out, name, like, strides):
+    """The caller's output of ``like``'s shape and type, or a dense one; its token stride is appended."""
+    if out is None:
+        out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    stride = _rope_rows(out, name, like.dtype, like.shape[0])
+    if out.shape != like.shape:
+        raise VlfError(VLF_ERR_INVALID, f"{name} must have the shape {tuple(like.shape)}")
+    _same_device(like, **{name: out})
+    strides.append(stride)
+    return out
+
+
+def _norm_rows(q, k):
+    """Checks q and k [tokens, heads, d] of one type; (token strides, total, h_q, h_k, d)."""
+    if q.dtype not in _DTYPE:
+        raise VlfError(VLF_ERR_INVALID, f"unsupported dtype {q.dtype}")
+    strides = [_rope_rows(q, "q", q.dtype)]
+    total, hq, d = q.shape
+    hk = 0
+    if k is not None:
+        strides.append(_rope_rows(k, "k", q.dtype, total))
+        if k.shape[2] != d:
+            raise VlfError(VLF_ERR_INVALID, "q and k must have the same head_dim")
+        _same_device(q, k=k)
+        hk = k.shape[1]
+    else:
+        strides.append(0)
+    _fits(total, hq, hk, d)
+    return strides, total, hq, hk, d
+
+
+def vlf_norm_rope(q, k, q_weight, k_weight, positions=None, inv_freq=None, sections=None,
+                  interleaved=False, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """Root-mean-square norm of each head of q [T,Hq,D] and k [T,Hk,D] (k may be None), times the weights
+    ``q_weight`` / ``k_weight`` [D] (None: ones; q's type or fp32), and the rotary positions of ``vlf_rope``
+    in the same pass (``positions`` and ``inv_freq`` None: the norm alone).  q and k may be slices of a
+    packed projection, the outputs q / k themselves.  Returns (q_out, k_out)."""
+    if q_out is None and k_out is None and stream is None:
+        done = _calls.norm_rope(q, k, q_weight, k_weight, positions, inv_freq, sections, interleaved, eps)
+        if done is not None:
+            return done
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return vlf_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, sections, interleaved, eps,
+                                 q_out, k_out, stream)
+    if _another(stream, q):
+        return _under(stream, (q_out, k_out), lambda: vlf_norm_rope(
+            q, k, q_weight, k_weight, positions, inv_freq, sections, interleaved, eps, q_out, k_out))
+    (sq, sk), total, hq, hk, d = _norm_rows(q, k)
+    if k is None and (k_out is not None or k_weight is not None):
+        raise VlfError(VLF_ERR_INVALID, "k_out or k_weight without k")
+    w_dtype = _norm_weights(q, q_weight, k_weight, d)
+    positions, axes, sec, inv_freq, rot = _turns(q, total, positions, inv_freq, sections)
+    q_weight, k_weight, positions, inv_freq = map(_at16, (q_weight, k_weight, positions, inv_freq))
+    so = []
+    q_out = _rows_like(q_out, "q_out", q, so)
+    k_out = _rows_like(k_out, "k_out", k, so) if k is not None else so.append(0)
+    _check(_lib.vlf_norm_rope(
+        _ptr(q), sq, _ptr(k), sk, _ptr(q_weight), _ptr(k_weight), _DTYPE[w_dtype], _eps(eps), _ptr(positions),
+        axes, sec, _ptr(inv_freq), total, hq, hk, d, rot, _DTYPE[q.dtype], int(bool(interleaved)),
+        _ptr(q_out), so[0], _ptr(k_out), so[1], _stream(stream, q)), "vlf_norm_rope")
+    return q_out, k_out
+
+
+def vlf_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions=None, inv_freq=None,
+                      sections=None, interleaved=False, eps=1e-6, dq=None, dk=None, dq_weight=None,
+                      dk_weight=None, workspace=None, stream=None):
+    """Gradients of vlf_norm_rope: ``dq_out`` / ``dk_out`` are those of its outputs, the other arguments its
+    own.  Returns (dq, dk, dq_weight, dk_weight), None where the input is None.  ``workspace``: at least
+    vlf_norm_rope_bwd_workspace_size bytes, allocated here when not given."""
+    if dq is None and dk is None and dq_weight is None and dk_weight is None and workspace is None and stream is None:
+        done = _calls.norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, sections,
+                                    interleaved, eps)
+        if done is not None:
+            return done
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return vlf_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, sections,
+                                     interleaved, eps, dq, dk, dq_weight, dk_weight, workspace, stream)
+    if _another(stream, q):
+        return _under(stream, (dq, dk, dq_weight, dk_weight), lambda: vlf_norm_rope_bwd(
+            dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, sections, interleaved, eps, dq, dk,
+            dq_weight, dk_weight, workspace))
+    (sq, sk), total, hq, hk, d = _norm_rows(q, k)
+    if k is None and any(t is not None for t in (dk_out, dk, k_weight, dk_weight)):
+        raise VlfError(VLF_ERR_INVALID, "dk_out, dk, k_weight or dk_weight without k")
+    w_dtype = _norm_weights(q, q_weight, k_weight, d)
+    positions, axes, sec, inv_freq, rot = _turns(q, total, positions, inv_freq, sections)
+    q_weight, k_weight, positions, inv_freq = map(_at16, (q_weight, k_weight, positions, inv_freq))
+    sg, so = [], []
+    for t, name, x in ((dq_out, "dq_out", q), (dk_out, "dk_out", k)):
+        if x is not None:
+            if t is None:
+                raise VlfError(VLF_ERR_INVALID, f"{name} is None")
+            _rows_like(t, name, x, sg)
+    dq = _rows_like(dq, "dq", q, so)
+    dk = _rows_like(dk, "dk", k, so) if k is not None else so.append(0)
+    grads = []
+    for w, dw, name in ((q_weight, dq_weight, "dq_weight"), (k_weight, dk_weight, "dk_weight")):
+        if w is None and dw is not None:
+            raise VlfError(VLF_ERR_INVALID, f"{name} without its weight")
+        if w is not None and dw is None:
+            dw = torch.empty_like(w)
+        if w is not None:
+            _given(dw, name, (d,), w_dtype), _same_device(q, **{name: dw})
+        grads.append(dw)
+    need = vlf_norm_rope_bwd_workspace_size(d) if q_weight is not None or k_weight is not None else 0
+    ws_p, ws_n, workspace = _room(workspace, need, q)
+    _check(_lib.vlf_norm_rope_bwd(
+        _ptr(dq_out), sg[0], _ptr(dk_out), sg[1] if k is not None else 0, _ptr(q), sq, _ptr(k), sk, _ptr(q_weight),
+        _ptr(k_weight), _DTYPE[w_dtype], _eps(eps), _ptr(positions), axes, sec, _ptr(inv_freq), total, hq, hk, d,
+        rot, _DTYPE[q.dtype], int(bool(interleaved)), _ptr(dq), so[0], _ptr(dk), so[1], _ptr(grads[0]),
+        _ptr(grads[1]), ws_p, ws_n, _stream(stream, q)), "vlf_norm_rope_bwd")
+    return dq, dk, grads[0], grads[1]
+
+
+def vlf_norm_rope_bwd_workspace_size(d) -> int:
+    return int(_lib.vlf_norm_rope_bwd_workspace_size(_c_int(d, "d")))
+
+
+def _pool(k_pages, v_pages, k_scale, v_scale):
+    """Checks a layer's pages and scales; (num_pages, h_kv, page, d_qk, d_v)."""
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        _req(t, name)
+        if t.dtype not in (torch.uint8, _E4M3):
+            raise VlfError(VLF_ERR_INVALID, f"{name} must be {_E4M3} or {torch.uint8}, got {t.dtype}")
+        if t.dim() != 4:
+            raise VlfError(VLF_ERR_INVALID, f"{name} must be [num_pages, H_kv, page, head_dim]")
+    n, h, page, dk = k_pages.shape
+    dv = v_pages.shape[3]
+    if v_pages.shape[:3] != k_pages.shape[:3]:
+        raise VlfError(VLF_ERR_INVALID, "k_pages and v_pages must have the same pages, heads and page size")
+    _given(k_scale, "k_scale", (n, h), _F32), _given(v_scale, "v_scale", (n, h), _F32)
+    _same_device(k_pages, v_pages=v_pages, k_scale=k_scale, v_scale=v_scale)
+    _fits(n, h, page, dk, dv)
+    return n, h, page, dk, dv
+
+
+def _table(like, page_table, lens, names=("page_table", "seqlens_kv")):
+    """Checks a page table [num_seqs, max_pages] and its sequences' lengths; (num_seqs, max_pages)."""
+    _req(page_table, names[0], _I32), _req(lens, names[1], _I32)
+    _same_device(like, **{names[0]: page_table, names[1]: lens})
+    if page_table.dim() != 2 or lens.shape != page_table.shape[:1]:
+        raise VlfError(VLF_ERR_INVALID, f"{names[0]} must be [num_seqs, max_pages] and {names[1]} [num_seqs]")
+    _fits(*page_table.shape)
+    return page_table.shape
+
+
+def vlf_pages_write(k, v, k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens, seqlens_kv, stream=None):
+    """New keys and values into their pages.  k [T,Hkv,Dk], v [T,Hkv,Dv] (tokens may be strided) packed by
+    ``cu_seqlens`` int32 [n + 1]; ``seqlens_kv`` int32 [n] are the sequences' lengths with them;
+    ``page_table`` int32 [n, max_pages].  The cache (``k_pages`` [pages,Hkv,page,Dk] and ``v_pages`` in e4m3 or
+    uint8, ``k_scale`` / ``v_scale`` fp32 [pages,Hkv]) is written in place: each page has, for each head, one
+    power of two as its scale, which grows where a new value needs it (include/vlf.h)."""
+    if stream is None and _calls.pages_write(k, v, k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens,
+                                             seqlens_kv):
+        return
+    if _elsewhere(k):
+        with torch.cuda.device(k.device):
+            return vlf_pages_write(k, v, k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens, seqlens_kv,
+                                   stream)
+    if _another(stream, k):
+        return _under(stream, (), lambda: vlf_pages_write(
+            k, v, k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens, seqlens_kv))
+    if k.dtype not in _DTYPE:
+        raise VlfError(VLF_ERR_INVALID, f"unsupported dtype {k.dtype}")
+    sk, sv = _rope_rows(k, "k", k.dtype), _rope_rows(v, "v", k.dtype, k.shape[0])
+    pages, h, page, dk, dv = _pool(k_pages, v_pages, k_scale, v_scale)
+    total = k.shape[0]
+    if k.shape[1:] != (h, dk) or v.shape[1:] != (h, dv):
+        raise VlfError(VLF_ERR_INVALID, "k, v must be [tokens, H_kv, head_dim] of the pages' heads and widths")
+    _same_device(k, v=v, k_pages=k_pages)
+    n, most = _table(k, page_table, seqlens_kv)
+    _given(cu_seqlens, "cu_seqlens", (n + 1,), _I32), _same_device(k, cu_seqlens=cu_seqlens)
+    _fits(total)
+    page_table, cu_seqlens, seqlens_kv = map(_at16, (page_table, cu_seqlens, seqlens_kv))
+    _check(_lib.vlf_pages_write(
+        _ptr(k), sk, _ptr(v), sv, _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
+        _ptr(cu_seqlens), _ptr(seqlens_kv), n, total, most, pages, page, h, dk, dv, _DTYPE[k.dtype],
+        _stream(stream, k)), "vlf_pages_write")
+
+
+def vlf_attn_varlen_fwd_pages_workspace_size(num_seqs, total_q, max_seqlen_q, h_q, h_kv, d_qk, d_v, dtype, flags=0,
+                                             num_sms=0) -> int:
+    dt = _DTYPE[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return int(_lib.vlf_attn_varlen_fwd_pages_workspace_size(num_seqs, total_q, max_seqlen_q, h_q, h_kv, d_qk, d_v,
+                                                             dt, flags, num_sms))
+
+
+def vlf_attn_varlen_fwd_pages(q, k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens_q, seqlens_kv,
+                              max_seqlen_q, scale=None, causal=False, window=0, out=None, lse=None,
+                              workspace=None, stream=None, flags=0):
+    """Attention of q [Tq,Hq,Dk] over a cache of pages in e4m3 (see vlf_pages_write for its tensors): sequence
+    s has the first ``seqlens_kv[s]`` keys of its row of ``page_table``.  Equals vlf_attn_varlen_fwd on the
+    values that the bytes stand for.  Returns out [Tq,Hq,Dv] and lse fp32 [Hq,Tq].  ``workspace``: at least
+    vlf_attn_varlen_fwd_pages_workspace_size bytes, allocated here when not given."""
+    if out is None and lse is None and workspace is None and stream is None:
+        done = _calls.pages_attn(q, k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens_q, seqlens_kv,
+                                 max_seqlen_q, scale, causal, window, flags)
+        if done is not None:
+            return done
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return vlf_attn_varlen_fwd_pages(q, k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens_q,
+                                             seqlens_kv, max_seqlen_q, scale, causal, window, out, lse, workspace,
+                                             stream, flags)
+    if _another(stream, q):
+        return _under(stream, (out, lse), lambda: vlf_attn_varlen_fwd_pages(
+            q, k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens_q, seqlens_kv, max_seqlen_q, scale, causal,
+            window, out, lse, workspace, flags=flags))
+    _req(q, "q")
+    if q.dtype not in _DTYPE or q.dim() != 3:
+        raise VlfError(VLF_ERR_INVALID, f"q must be [tokens, heads, head_dim] in fp16, bf16 or fp32, got {q.dtype}")
+    pages, hkv, page, dqk, dv = _pool(k_pages, v_pages, k_scale, v_scale)
+    tq, hq, d = q.shape
+    if d != dqk:
+        raise VlfError(VLF_ERR_INVALID, "q and k_pages must have the same head_dim")
+    _same_device(q, k_pages=k_pages)
+    n, most = _table(q, page_table, seqlens_kv)
+    _given(cu_seqlens_q, "cu_seqlens_q", (n + 1,), _I32), _same_device(q, cu_seqlens_q=cu_seqlens_q)
+    _fits(tq, hq)
+    if out is None:
+        out = torch.empty((tq, hq, dv), dtype=q.dtype, device=q.device)
+    else:
+        _given(out, "out", (tq, hq, dv), q.dtype), _same_device(q, out=out)
+    if lse is None:
+        lse = torch.empty((hq, tq), dtype=_F32, device=q.device)
+    else:
+        _given(lse, "lse", (hq, tq), _F32), _same_device(q, lse=lse)
+    mq, window, dt, flags = _c_int(max_seqlen_q, "max_seqlen_q"), _c_int(window or 0, "window"), _DTYPE[q.dtype], int(flags)
+    page_table, cu_seqlens_q, seqlens_kv = map(_at16, (page_table, cu_seqlens_q, seqlens_kv))
+    need = _workspace_size(_lib.vlf_attn_varlen_fwd_pages_workspace_size,
+                           ("pages", n, tq, mq, hq, hkv, dqk, dv, dt, flags, q.get_device()))
+    ws_p, ws_n, workspace = _room(workspace, need, q)
+    _check(_lib.vlf_attn_varlen_fwd_pages(
+        _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(cu_seqlens_q),
+        _ptr(seqlens_kv), n, tq, mq, most, pages, page, hq, hkv, dqk, dv, dt, float(scale) if scale else 0.0,
+        int(bool(causal)), window, _ptr(out), _ptr(lse), ws_p, ws_n, _stream(stream, q), flags),
+        "vlf_attn_varlen_fwd_pages")
+    return out, lse
+
+
+def vlf_pages_copy(k_pages, v_pages, k_scale, v_scale, src, dst, stream=None):
+    """Copies page src[i] (keys, values and scales) over page dst[i] for each i with src[i] >= 0; ``src`` and
+    ``dst`` int32 [n], as vlf_pages_fork and vlf_pages_compact return them (a page is in dst once at most,
+    and not in src as well).  In place; called for each layer's cache."""
+    if stream is None and _calls.pages_copy(k_pages, v_pages, k_scale, v_scale, src, dst):
+        return
+    if _elsewhere(k_pages):
+        with torch.cuda.device(k_pages.device):
+            return vlf_pages_copy(k_pages, v_pages, k_scale, v_scale, src, dst, stream)
+    if _another(stream, k_pages):
+        return _under(stream, (), lambda: vlf_pages_copy(k_pages, v_pages, k_scale, v_scale, src, dst))
+    pages, h, page, dk, dv = _pool(k_pages, v_pages, k_scale, v_scale)
+    _req(src, "src", _I32), _req(dst, "dst", _I32), _same_device(k_pages, src=src, dst=dst)
+    if src.dim() != 1 or dst.shape != src.shape:
+        raise VlfError(VLF_ERR_INVALID, "src and dst must be [n]")
+    _fits(src.shape[0])
+    src, dst = _at16(src), _at16(dst)
+    _check(_lib.vlf_pages_copy(
+        _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(src), _ptr(dst), src.shape[0], pages, page, h,
+        dk, dv, _stream(stream, k_pages)), "vlf_pages_copy")
+
+
+def vlf_pages_fork_workspace_size(num_pages, num_out) -> int:
+    return int(_lib.vlf_pages_fork_workspace_size(_c_int(num_pages, "num_pages"), _c_int(num_out, "num_out")))
+
+
+def vlf_pages_fork(page_table, seqlens, refs, parents, grow, page_size, table_out=None, seqlens_out=None,
+                   refs_out=None, src=None, dst=None, left=None, workspace=None, stream=None):
+    """The page tables of the next step: new row s follows old row ``parents[s]`` (-1: it begins empty) and has
+    room for ``grow[s]`` more tokens.  ``page_table`` int32 [n, max_pages], ``seqlens`` [n], ``refs`` [pages]
+    (how many hold each page), ``parents`` and ``grow`` [m].  A row that is no one's parent gives its pages
+    back, whole pages are shared, and a page that is not full has one holder: the other rows get
+    copies.  Returns (table [m, max_pages], seqlens [m] with the growth, refs [pages], src [m], dst [m],
+    left [1]); src and dst are for vlf_pages_copy of every layer, before anything is written; left, the free
+    pages that are left, is negative where there were too few: nothing has changed then, and the tables
+    returned are empty (include/vlf.h).  Nothing is read on the host."""
+    if all(t is None for t in (table_out, seqlens_out, refs_out, src, dst, left, workspace, stream)):
+        done = _calls.pages_fork(page_table, seqlens, refs, parents, grow, page_size)
+        if done is not None:
+            return done
+    if _elsewhere(refs):
+        with torch.cuda.device(refs.device):
+            return vlf_pages_fork(page_table, seqlens, refs, parents, grow, page_size, table_out, seqlens_out,
+                                  refs_out, src, dst, left, workspace, stream)
+    if _another(stream, refs):
+        return _under(stream, (table_out, seqlens_out, refs_out, src, dst, left), lambda: vlf_pages_fork(
+            page_table, seqlens, refs, parents, grow, page_size, table_out, seqlens_out, refs_out, src, dst, left,
+            workspace))
+    _req(refs, "refs", _I32), _req(parents, "parents", _I32), _req(grow, "grow", _I32)
+    n, most = _table(refs, page_table, seqlens, ("page_table", "seqlens"))
+    _same_device(refs, parents=parents, grow=grow)
+    if refs.dim() != 1 or parents.dim() != 1 or grow.shape != parents.shape:
+        raise VlfError(VLF_ERR_INVALID, "refs must be [num_pages], parents and grow [m]")
+    m, pages = parents.shape[0], refs.shape[0]
+    _fits(m, pages)
+    outs = []
+    for t, name, shape in ((table_out, "table_out", (m, most)), (seqlens_out, "seqlens_out", (m,)),
+                           (refs_out, "refs_out", (pages,)), (src, "src", (m,)), (dst, "dst", (m,)),
+                           (left, "left", (1,))):
+        if t is None:
+            t = torch.empty(shape, dtype=_I32, device=refs.device)
+        _given(t, name, shape, _I32), _same_device(refs, **{name: t})
+        outs.append(t)
+    page_table, seqlens, refs, parents, grow = map(_at16, (page_table, seqlens, refs, parents, grow))
+    ws_p, ws_n, workspace = _room(workspace, vlf_pages_fork_workspace_size(pages, m), refs)
+    _check(_lib.vlf_pages_fork(
+        _ptr(page_table), _ptr(seqlens), _ptr(refs), _ptr(parents), _ptr(grow), n, m, most, pages,
+        _c_int(page_size, "page_size"), *map(_ptr, outs), ws_p, ws_n, _stream(stream, refs)), "vlf_pages_fork")
+    return tuple(outs)
+
+
+def vlf_pages_compact_workspace_size(num_pages) -> int:
+    return int(_lib.vlf_pages_compact_workspace_size(_c_int(num_pages, "num_pages")))
+
+
+def vlf_pages_compact(page_table, refs, table_out=None, refs_out=None, to=None, src=None, dst=None, used=None,
+                      workspace=None, stream=None):
+    """The pages in use (``refs`` [pages] above 0) moved to the front of the pool.  Returns (table, refs, to, src,
+    dst, used): the tables and counts afterwards, where each page in use then is (-1: it was free), the
+    copies to make (int32 [pages // 2], -1 behind them) with vlf_pages_copy of every layer, and int32 [1]
+    how many pages are in use.  Nothing is read on the host."""
+    if all(t is None for t in (table_out, refs_out, to, src, dst, used, workspace, stream)):
+        done = _calls.pages_compact(page_table, refs)
+        if done is not None:
+            return done
+    if _elsewhere(refs):
+        with torch.cuda.device(refs.device):
+            return vlf_pages_compact(page_table, refs, table_out, refs_out, to, src, dst, used, workspace, stream)
+    if _another(stream, refs):
+        return _under(stream, (table_out, refs_out, to, src, dst, used), lambda: vlf_pages_compact(
+            page_table, refs, table_out, refs_out, to, src, dst, used, workspace))
+    _req(page_table, "page_table", _I32), _req(refs, "refs", _I32), _same_device(refs, page_table=page_table)
+    if page_table.dim() != 2 or refs.dim() != 1:
+        raise VlfError(VLF_ERR_INVALID, "page_table must be [num_seqs, max_pages], refs [num_pages]")
+    n, most = page_table.shape
+    pages = refs.shape[0]
+    _fits(n, most, pages)
+    outs = []
+    for t, name, shape in ((table_out, "table_out", (n, most)), (refs_out, "refs_out", (pages,)), (to, "to", (pages,)),
+                           (src, "src", (pages // 2,)), (dst, "dst", (pages // 2,)), (used, "used", (1,))):
+        if t is None:
+            t = torch.empty(shape, dtype=_I32, device=refs.device)
+        _given(t, name, shape, _I32), _same_device(refs, **{name: t})
+        outs.append(t)
+    page_table, refs = _at16(page_table), _at16(refs)
+    ws_p, ws_n, workspace = _room(workspace, vlf_pages_compact_workspace_size(pages), refs)
+    _check(_lib.vlf_pages_compact(_ptr(page_table), _ptr(refs), n, most, pages, *map(_ptr, outs), ws_p, ws_n,
+                                  _stream(stream, refs)), "vlf_pages_compact")
+    return tuple(outs)
+
+
 __all__ = ["vlf_attn_varlen_fwd", "vlf_attn_varlen_bwd", "vlf_attn_varlen_bwd_workspace_size",
            "vlf_bias_bands", "vlf_bias_bands_size",
            "vlf_check_error", "vlf_status_string", "vlf_sched_kv_band", "vlf_sched_q_band",
@@ -1021,12 +1472,16 @@ __all__ = ["vlf_attn_varlen_fwd", "vlf_attn_varlen_bwd", "vlf_attn_varlen_bwd_wo
            "vlf_attn_varlen_bwd_noalloc", "vlf_noalloc_scratch_bytes", "VlfError",
            "vlf_rope", "vlf_attn_varlen_fwd_prefix", "vlf_attn_varlen_fwd_prefix_workspace_size",
            "vlf_attn_key_weights", "vlf_attn_key_weights_workspace_size", "vlf_cache_evict",
+           "vlf_norm_rope", "vlf_norm_rope_bwd", "vlf_norm_rope_bwd_workspace_size", "vlf_pages_write",
+           "vlf_attn_varlen_fwd_pages", "vlf_attn_varlen_fwd_pages_workspace_size", "vlf_pages_copy",
+           "vlf_pages_fork", "vlf_pages_fork_workspace_size", "vlf_pages_compact",
+           "vlf_pages_compact_workspace_size",
            "LIB_PATH", "EXPORTS"]
 
 # differentiable entry points (autograd over the two calls above)
 from .functional import (flash_attn_varlen_func, flash_attn_varlen_kvpacked_func,  # noqa: E402
-                         flash_attn_varlen_qkvpacked_func, latent_attention, rotary_embedding,
-                         varlen_attention)
+                         flash_attn_varlen_qkvpacked_func, latent_attention,
+                         norm_rotary_embedding, rotary_embedding, varlen_attention)
 
-__all__ += ["varlen_attention", "latent_attention", "rotary_embedding", "flash_attn_varlen_func", "flash_attn_varlen_qkvpacked_func",
+__all__ += ["varlen_attention", "latent_attention", "rotary_embedding", "norm_rotary_embedding", "flash_attn_varlen_func", "flash_attn_varlen_qkvpacked_func",
             "flash_attn_varlen_kvpacked_func"]

@@ -81,7 +81,34 @@ int sm_count() {
 // most: they take fewer than 2^31 - 2^16 of them.
 constexpr long long kMostTokens = 0x7fff0000ll;
 
+// The first pair of each position axis (half for the axes that are not there); false where the sections
+// are not `half` pairs in all.
+bool first_pairs(int (&first)[4], int n_axes, const int *sections, int half) {
+  long long sum = 0;
+  for (int a = 0; a < 4; ++a) {
+    first[a] = a < n_axes ? (int)sum : half;
+    if (a >= n_axes) continue;
+    const int n = sections ? sections[a] : half;
+    if (n < 0 || (sum += n) > half) return false;
+  }
+  return sum == half;
+}
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Whether one of the first `outs` of n spans shares a byte with any other.
+struct Span {
+  const void *p;
+  size_t n;
+};
+bool overlap(const Span *all, int outs, int n) {
+  for (int a = 0; a < outs; ++a)
+    for (int b = a + 1; b < n; ++b) {
+      const uintptr_t x = (uintptr_t)all[a].p, y = (uintptr_t)all[b].p;
+      if (all[a].n && all[b].n && x < y + all[b].n && y < x + all[a].n) return true;
+    }
+  return false;
+}
 
 // Shared argument checks of the forward and backward.  Returns VLF_OK or a negative status.
 int check_common(const void *q, const void *k, const void *v, const int32_t *cu_q,
@@ -220,6 +247,7 @@ const char *vlf_status_string(int status) {
     case VLF_ERR_TIMEOUT: return "device pipeline wait timed out";
     case VLF_ERR_BAD_SEQLENS: return "bad cu_seqlens (out of range, decreasing, or longer than max_seqlen)";
     case VLF_ERR_WORKSPACE: return "backward workspace missing or too small";
+    case VLF_ERR_BAD_PAGES: return "bad pages (outside the pool, or tables and counts that disagree)";
     default: return "unknown status";
   }
 }
@@ -568,14 +596,7 @@ int vlf_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
   if (n_axes < 1 || n_axes > 4 || (!sections && n_axes != 1)) return VLF_ERR_INVALID;
   vlf::RopeParams p{};
   const int half = rot / 2;
-  long long sum = 0;
-  for (int a = 0; a < 4; ++a) {
-    p.first[a] = a < n_axes ? (int)sum : half;
-    if (a >= n_axes) continue;
-    const int n = sections ? sections[a] : half;
-    if (n < 0 || (sum += n) > half) return VLF_ERR_INVALID;
-  }
-  if (sum != half) return VLF_ERR_INVALID;
+  if (!first_pairs(p.first, n_axes, sections, half)) return VLF_ERR_INVALID;
   if (d > 256 || h_q > 65535 || h_k > 65535) return VLF_ERR_UNSUPPORTED;
   if (total == 0) return VLF_OK;
   if (!q || !q_out || (h_k > 0 && (!k || !k_out)) || (half > 0 && (!positions || !inv_freq))) return VLF_ERR_INVALID;
@@ -705,14 +726,10 @@ int vlf_cache_evict(const void *k, const void *v, const float *weights,
   // kept rows are read while others are written: an output shares no byte with an input or another output
   const size_t es = dtype == VLF_F32 ? 4 : 2, in = (size_t)total_kv * h_kv, to = (size_t)total_out * h_kv;
   const size_t cu = ((size_t)num_seqs + 1) * 4;
-  const struct { const void *p; size_t n; } all[9] = {
+  const Span all[9] = {
       {k_out, to * d_qk * es}, {v_out, to * d_v * es}, {weights_out, to * 4}, {index_out, to * 4}, {cu_out, cu},
       {k, in * d_qk * es}, {v, in * d_v * es}, {weights, in * 4}, {cu_seqlens_kv, cu}};
-  for (int a = 0; a < 5; ++a)
-    for (int b = a + 1; b < 9; ++b) {
-      const uintptr_t x = (uintptr_t)all[a].p, y = (uintptr_t)all[b].p;
-      if (all[a].n && all[b].n && x < y + all[b].n && y < x + all[a].n) return VLF_ERR_INVALID;
-    }
+  if (overlap(all, 5, 9)) return VLF_ERR_INVALID;
   vlf::EvictParams p{};
   p.k = k; p.v = v; p.weights = weights; p.cu_kv = cu_seqlens_kv;
   p.num_seqs = num_seqs; p.total_kv = total_kv; p.h_kv = h_kv;
@@ -723,6 +740,264 @@ int vlf_cache_evict(const void *k, const void *v, const float *weights,
   p.err = error_word_ptr();
   if (!p.err) return VLF_ERR_LAUNCH;
   return vlf::cache_evict(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
+}
+
+namespace {
+// The arguments that vlf_norm_rope and its backward share, into p (strides, weights and positions among
+// them; the outputs are the caller's).  VLF_OK with total = 0 as well.
+int norm_rope_args(vlf::NormRopeParams &p, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                   const void *q_weight, const void *k_weight, int weight_dtype, float eps,
+                   const int32_t *positions, int n_axes, const int *sections, const float *inv_freq, int total,
+                   int h_q, int h_k, int d, int rot, int dtype, int interleaved) {
+  if (total < 0 || h_q < 1 || h_k < 0 || d < 1 || rot < 0 || rot > d || rot % 2) return VLF_ERR_INVALID;
+  if (dtype != VLF_F16 && dtype != VLF_BF16 && dtype != VLF_F32) return VLF_ERR_INVALID;
+  if ((q_weight || k_weight) && weight_dtype != dtype && weight_dtype != VLF_F32) return VLF_ERR_INVALID;
+  if (!(eps >= 0.f) || isinf(eps)) return VLF_ERR_INVALID;
+  if (n_axes < 1 || n_axes > 4 || (!sections && n_axes != 1)) return VLF_ERR_INVALID;
+  if (!first_pairs(p.first, n_axes, sections, rot / 2)) return VLF_ERR_INVALID;
+  if (d > 256 || h_q > 65535 || h_k > 65535) return VLF_ERR_UNSUPPORTED;
+  if (total > 0 && (!q || (h_k > 0 && !k) || (rot > 0 && (!positions || !inv_freq)))) return VLF_ERR_INVALID;
+  if (q_stride < 0 || k_stride < 0) return VLF_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(positions) ||
+      !aligned16(inv_freq))
+    return VLF_ERR_ALIGN;
+  p.q.x = q; p.q.x_stride = q_stride; p.q.w = q_weight;
+  p.k.x = k; p.k.x_stride = k_stride; p.k.w = k_weight;
+  p.positions = positions; p.inv_freq = inv_freq;
+  p.total = total; p.h_q = h_q; p.h_k = h_k; p.d = d; p.rot = rot; p.dtype = dtype; p.w_dtype = weight_dtype;
+  p.interleaved = interleaved ? 1 : 0;
+  p.eps = eps;
+  return VLF_OK;
+}
+// Whether an output is written in place of an input with another stride.
+bool other_stride(const void *in, int64_t in_stride, const void *out, int64_t out_stride, int total) {
+  return in == out && total > 1 && in_stride != out_stride;
+}
+}  // namespace
+
+int vlf_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *q_weight,
+                  const void *k_weight, int weight_dtype, float eps, const int32_t *positions, int n_axes,
+                  const int *sections, const float *inv_freq, int total, int h_q, int h_k, int d, int rot,
+                  int dtype, int interleaved, void *q_out, int64_t q_out_stride, void *k_out,
+                  int64_t k_out_stride, vlf_stream_t stream) {
+  vlf::NormRopeParams p{};
+  const int st = norm_rope_args(p, q, q_stride, k, k_stride, q_weight, k_weight, weight_dtype, eps, positions, n_axes,
+                                sections, inv_freq, total, h_q, h_k, d, rot, dtype, interleaved);
+  if (st != VLF_OK) return st;
+  if (total == 0) return VLF_OK;
+  if (!q_out || (h_k > 0 && !k_out)) return VLF_ERR_INVALID;
+  if (total > 1 && (q_out_stride < (int64_t)h_q * d || (h_k > 0 && k_out_stride < (int64_t)h_k * d))) return VLF_ERR_INVALID;
+  if (!aligned16(q_out) || !aligned16(k_out)) return VLF_ERR_ALIGN;
+  if (other_stride(q, q_stride, q_out, q_out_stride, total) ||
+      (h_k > 0 && other_stride(k, k_stride, k_out, k_out_stride, total)))
+    return VLF_ERR_INVALID;
+  p.q.out = q_out; p.q.out_stride = q_out_stride;
+  p.k.out = k_out; p.k.out_stride = k_out_stride;
+  return vlf::norm_rope(p, false, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
+}
+
+size_t vlf_norm_rope_bwd_workspace_size(int d) { return d < 1 || d > 256 ? 0 : vlf::norm_rope_workspace(d); }
+
+int vlf_norm_rope_bwd(const void *dq_out, int64_t dq_out_stride, const void *dk_out, int64_t dk_out_stride,
+                      const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *q_weight,
+                      const void *k_weight, int weight_dtype, float eps, const int32_t *positions, int n_axes,
+                      const int *sections, const float *inv_freq, int total, int h_q, int h_k, int d, int rot,
+                      int dtype, int interleaved, void *dq, int64_t dq_stride, void *dk, int64_t dk_stride,
+                      void *dq_weight, void *dk_weight, void *workspace, size_t workspace_bytes,
+                      vlf_stream_t stream) {
+  vlf::NormRopeParams p{};
+  const int st = norm_rope_args(p, q, q_stride, k, k_stride, q_weight, k_weight, weight_dtype, eps, positions, n_axes,
+                                sections, inv_freq, total, h_q, h_k, d, rot, dtype, interleaved);
+  if (st != VLF_OK) return st;
+  if ((dq_weight && !q_weight) || (dk_weight && (!k_weight || h_k == 0))) return VLF_ERR_INVALID;
+  if (total > 0 && (!dq_out || !dq || (h_k > 0 && (!dk_out || !dk)))) return VLF_ERR_INVALID;
+  if (dq_out_stride < 0 || dk_out_stride < 0 ||
+      (total > 1 && (dq_stride < (int64_t)h_q * d || (h_k > 0 && dk_stride < (int64_t)h_k * d))))
+    return VLF_ERR_INVALID;
+  if (!aligned16(dq_out) || !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk) || !aligned16(dq_weight) ||
+      !aligned16(dk_weight) || !aligned16(workspace))
+    return VLF_ERR_ALIGN;
+  if (total > 0 && (other_stride(q, q_stride, dq, dq_stride, total) || other_stride(dq_out, dq_out_stride, dq, dq_stride, total) ||
+                    (h_k > 0 && (other_stride(k, k_stride, dk, dk_stride, total) ||
+                                 other_stride(dk_out, dk_out_stride, dk, dk_stride, total)))))
+    return VLF_ERR_INVALID;
+  if (dq_weight || dk_weight) {
+    if (!workspace || workspace_bytes < vlf::norm_rope_workspace(d)) return VLF_ERR_WORKSPACE;
+    p.part = static_cast<float *>(workspace);
+  }
+  p.q.dy = dq_out; p.q.dy_stride = dq_out_stride; p.q.out = dq; p.q.out_stride = dq_stride; p.q.dw = dq_weight;
+  p.k.dy = dk_out; p.k.dy_stride = dk_out_stride; p.k.out = dk; p.k.out_stride = dk_stride; p.k.dw = dk_weight;
+  return vlf::norm_rope(p, true, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
+}
+
+namespace {
+// log2 of a page's tokens; -1 where a page of that size is not supported.
+int log2_of_page(int page) {
+  for (int l = 4; l <= 8; ++l)
+    if (page == 1 << l) return l;
+  return -1;
+}
+// Sizes that every call on pages shares.
+int check_pool(const void *k_pages, const void *v_pages, const void *k_scale, const void *v_scale, int num_pages,
+               int page, int h_kv, int d_qk, int d_v) {
+  if (num_pages < 0 || h_kv < 1 || d_qk < 1 || d_v < 1) return VLF_ERR_INVALID;
+  if (num_pages > 0 && (!k_pages || !v_pages || !k_scale || !v_scale)) return VLF_ERR_INVALID;
+  if (log2_of_page(page) < 0 || d_qk > 256 || d_v > 256 || h_kv > 32767) return VLF_ERR_UNSUPPORTED;
+  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_scale) || !aligned16(v_scale)) return VLF_ERR_ALIGN;
+  return VLF_OK;
+}
+int check_table(const int32_t *table, const int32_t *lens, int num_seqs, int max_pages, int page) {
+  if (num_seqs < 0 || max_pages < 0 || page < 1) return VLF_ERR_INVALID;
+  if (num_seqs > 0 && ((max_pages > 0 && !table) || !lens)) return VLF_ERR_INVALID;
+  if (num_seqs > 65535 || (long long)max_pages * page >= kMostTokens) return VLF_ERR_UNSUPPORTED;
+  if (!aligned16(table) || !aligned16(lens)) return VLF_ERR_ALIGN;
+  return VLF_OK;
+}
+}  // namespace
+
+int vlf_pages_write(const void *k, int64_t k_stride, const void *v, int64_t v_stride, void *k_pages, void *v_pages,
+                    float *k_scale, float *v_scale, const int32_t *page_table, const int32_t *cu_seqlens,
+                    const int32_t *seqlens_kv, int num_seqs, int total, int max_pages, int num_pages, int page,
+                    int h_kv, int d_qk, int d_v, int dtype, vlf_stream_t stream) {
+  int st = check_pool(k_pages, v_pages, k_scale, v_scale, num_pages, page, h_kv, d_qk, d_v);
+  if (st == VLF_OK) st = check_table(page_table, seqlens_kv, num_seqs, max_pages, page);
+  if (st != VLF_OK) return st;
+  if (total < 0 || (num_seqs == 0 && total != 0) || (num_seqs > 0 && !cu_seqlens)) return VLF_ERR_INVALID;
+  if (dtype != VLF_F16 && dtype != VLF_BF16 && dtype != VLF_F32) return VLF_ERR_INVALID;
+  if (total >= kMostTokens) return VLF_ERR_UNSUPPORTED;
+  if (total > 0 && (!k || !v)) return VLF_ERR_INVALID;
+  if (total > 1 && (k_stride < 0 || v_stride < 0)) return VLF_ERR_INVALID;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(cu_seqlens)) return VLF_ERR_ALIGN;
+  if (total == 0) return VLF_OK;
+  vlf::PagesWriteParams p{};
+  p.k = k; p.v = v; p.k_stride = k_stride; p.v_stride = v_stride;
+  p.k_pages = k_pages; p.v_pages = v_pages; p.k_scale = k_scale; p.v_scale = v_scale;
+  p.table = page_table; p.cu = cu_seqlens; p.kv_lens = seqlens_kv;
+  p.num_seqs = num_seqs; p.total = total; p.max_pages = max_pages; p.num_pages = num_pages;
+  p.page = page; p.log2_page = log2_of_page(page);
+  p.h_kv = h_kv; p.d_qk = d_qk; p.d_v = d_v; p.dtype = dtype;
+  p.err = error_word_ptr();
+  if (!p.err) return VLF_ERR_LAUNCH;
+  return vlf::pages_write(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
+}
+
+size_t vlf_attn_varlen_fwd_pages_workspace_size(int num_seqs, int total_q, int max_seqlen_q, int h_q, int h_kv,
+                                                int d_qk, int d_v, int dtype, unsigned flags, int num_sms) {
+  if (num_seqs < 1 || total_q < 1 || max_seqlen_q < 1 || h_kv < 1 || h_q < h_kv || h_q % h_kv) return 0;
+  if (num_sms <= 0) num_sms = sm_count();
+  if (max_seqlen_q > total_q) max_seqlen_q = total_q;  // (as in the call)
+  return vlf::pages_attn_workspace(num_seqs, max_seqlen_q, h_q, h_kv, d_qk, d_v, dtype, flags, num_sms);
+}
+
+int vlf_attn_varlen_fwd_pages(const void *q, const void *k_pages, const void *v_pages, const float *k_scale,
+                              const float *v_scale, const int32_t *page_table, const int32_t *cu_seqlens_q,
+                              const int32_t *seqlens_kv, int num_seqs, int total_q, int max_seqlen_q,
+                              int max_pages, int num_pages, int page, int h_q, int h_kv, int d_qk, int d_v,
+                              int dtype, float scale, int causal, int window, void *out, float *lse,
+                              void *workspace, size_t workspace_bytes, vlf_stream_t stream, unsigned flags) {
+  int st = check_pool(k_pages, v_pages, k_scale, v_scale, num_pages, page, h_kv, d_qk, d_v);
+  if (st == VLF_OK) st = check_table(page_table, seqlens_kv, num_seqs, max_pages, page);
+  if (st == VLF_OK)
+    st = check_common(q, k_pages, v_pages, cu_seqlens_q, seqlens_kv, num_seqs, total_q, 0, max_seqlen_q, 0, h_q, h_kv,
+                      d_qk, d_v, dtype, nullptr, 0);
+  if (st != VLF_OK) return st;
+  if (total_q > 0 && !out) return VLF_ERR_INVALID;
+  if (total_q >= kMostTokens) return VLF_ERR_UNSUPPORTED;
+  if (!aligned16(out) || !aligned16(lse) || !aligned16(workspace)) return VLF_ERR_ALIGN;
+  if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return VLF_OK;
+  if (max_seqlen_q > total_q) max_seqlen_q = total_q;  // (no sequence has more)
+  vlf::PagesAttnParams a{};
+  fill_common(a.p, q, k_pages, v_pages, cu_seqlens_q, nullptr, num_seqs, total_q, 0, max_seqlen_q, max_pages * page, h_q,
+              h_kv, d_qk, d_v, dtype, scale, causal, window, nullptr, 0, flags);
+  a.p.out = out;
+  a.p.lse = lse;
+  a.p.err = error_word_ptr();
+  if (!a.p.err) return VLF_ERR_LAUNCH;
+  a.k_pages = static_cast<const uint8_t *>(k_pages);
+  a.v_pages = static_cast<const uint8_t *>(v_pages);
+  a.k_scale = k_scale; a.v_scale = v_scale;
+  a.table = page_table; a.kv_lens = seqlens_kv;
+  a.max_pages = max_pages; a.num_pages = num_pages; a.page = page; a.log2_page = log2_of_page(page);
+  const int sms = sm_count();
+  const size_t need = vlf::pages_attn_workspace(num_seqs, max_seqlen_q, h_q, h_kv, d_qk, d_v, dtype, flags, sms);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return VLF_ERR_WORKSPACE;
+  const cudaError_t e = vlf::pages_forward(a, workspace, sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
+}
+
+int vlf_pages_copy(void *k_pages, void *v_pages, float *k_scale, float *v_scale, const int32_t *src,
+                   const int32_t *dst, int n, int num_pages, int page, int h_kv, int d_qk, int d_v,
+                   vlf_stream_t stream) {
+  const int st = check_pool(k_pages, v_pages, k_scale, v_scale, num_pages, page, h_kv, d_qk, d_v);
+  if (st != VLF_OK) return st;
+  if (n < 0 || (n > 0 && (!src || !dst))) return VLF_ERR_INVALID;
+  if (!aligned16(src) || !aligned16(dst)) return VLF_ERR_ALIGN;
+  if (n == 0) return VLF_OK;
+  vlf::PagesCopyParams p{};
+  p.k_pages = k_pages; p.v_pages = v_pages; p.k_scale = k_scale; p.v_scale = v_scale;
+  p.src = src; p.dst = dst; p.n = n; p.num_pages = num_pages; p.page = page;
+  p.h_kv = h_kv; p.d_qk = d_qk; p.d_v = d_v;
+  p.err = error_word_ptr();
+  if (!p.err) return VLF_ERR_LAUNCH;
+  return vlf::pages_copy(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
+}
+
+size_t vlf_pages_fork_workspace_size(int num_pages, int num_out) {
+  return num_pages < 0 || num_out < 0 ? 0 : vlf::pages_fork_workspace(num_pages, num_out);
+}
+
+int vlf_pages_fork(const int32_t *page_table, const int32_t *seqlens, const int32_t *refs, const int32_t *parents,
+                   const int32_t *grow, int num_in, int num_out, int max_pages, int num_pages, int page,
+                   int32_t *table_out, int32_t *seqlens_out, int32_t *refs_out, int32_t *src, int32_t *dst,
+                   int32_t *left, void *workspace, size_t workspace_bytes, vlf_stream_t stream) {
+  if (num_pages < 0 || num_out < 0 || !left || (num_pages > 0 && (!refs || !refs_out))) return VLF_ERR_INVALID;
+  if (log2_of_page(page) < 0) return VLF_ERR_UNSUPPORTED;
+  const int st = check_table(page_table, seqlens, num_in, max_pages, page);
+  if (st != VLF_OK) return st;
+  if (num_out > 0 && (!parents || !grow || (max_pages > 0 && !table_out) || !seqlens_out || !src || !dst)) return VLF_ERR_INVALID;
+  if (num_out > 65535 || num_pages >= kMostTokens) return VLF_ERR_UNSUPPORTED;
+  const void *all16[] = {refs, parents, grow, table_out, seqlens_out, refs_out, src, dst, left, workspace};
+  for (const void *x : all16)
+    if (!aligned16(x)) return VLF_ERR_ALIGN;
+  if (!workspace || workspace_bytes < vlf::pages_fork_workspace(num_pages, num_out)) return VLF_ERR_WORKSPACE;
+  const size_t row = (size_t)max_pages * 4, in = num_in, out = num_out, pool = (size_t)num_pages * 4;
+  const Span all[12] = {{table_out, out * row}, {seqlens_out, out * 4}, {refs_out, pool}, {src, out * 4}, {dst, out * 4},
+                        {left, 4}, {workspace, workspace_bytes}, {page_table, in * row}, {seqlens, in * 4}, {refs, pool},
+                        {parents, out * 4}, {grow, out * 4}};
+  if (overlap(all, 7, 12)) return VLF_ERR_INVALID;
+  vlf::PagesForkParams p{};
+  p.table = page_table; p.lens = seqlens; p.refs = refs; p.parents = parents; p.grow = grow;
+  p.num_in = num_in; p.num_out = num_out; p.max_pages = max_pages; p.num_pages = num_pages;
+  p.log2_page = log2_of_page(page);
+  p.table_out = table_out; p.lens_out = seqlens_out; p.refs_out = refs_out; p.src = src; p.dst = dst; p.left = left;
+  p.err = error_word_ptr();
+  if (!p.err) return VLF_ERR_LAUNCH;
+  return vlf::pages_fork(p, workspace, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
+}
+
+size_t vlf_pages_compact_workspace_size(int num_pages) {
+  return num_pages < 0 ? 0 : vlf::pages_compact_workspace(num_pages);
+}
+
+int vlf_pages_compact(const int32_t *page_table, const int32_t *refs, int num_seqs, int max_pages, int num_pages,
+                      int32_t *table_out, int32_t *refs_out, int32_t *to, int32_t *src, int32_t *dst, int32_t *used,
+                      void *workspace, size_t workspace_bytes, vlf_stream_t stream) {
+  if (num_seqs < 0 || max_pages < 0 || num_pages < 1 || !used || !refs || !refs_out || !to) return VLF_ERR_INVALID;
+  const long long entries = (long long)num_seqs * max_pages;
+  if ((entries > 0 && (!page_table || !table_out)) || (num_pages > 1 && (!src || !dst))) return VLF_ERR_INVALID;
+  if (num_seqs > 65535 || num_pages >= kMostTokens) return VLF_ERR_UNSUPPORTED;
+  const void *all16[] = {page_table, refs, table_out, refs_out, to, src, dst, used, workspace};
+  for (const void *x : all16)
+    if (!aligned16(x)) return VLF_ERR_ALIGN;
+  if (!workspace || workspace_bytes < vlf::pages_compact_workspace(num_pages)) return VLF_ERR_WORKSPACE;
+  const size_t table = (size_t)entries * 4, pool = (size_t)num_pages * 4, half = (size_t)(num_pages / 2) * 4;
+  const Span all[9] = {{table_out, table}, {refs_out, pool}, {to, pool}, {src, half}, {dst, half}, {used, 4},
+                       {workspace, workspace_bytes}, {page_table, table}, {refs, pool}};
+  if (overlap(all, 7, 9)) return VLF_ERR_INVALID;
+  vlf::PagesCompactParams p{};
+  p.table = page_table; p.refs = refs; p.entries = entries; p.num_pages = num_pages;
+  p.table_out = table_out; p.refs_out = refs_out; p.to = to; p.src = src; p.dst = dst; p.used = used;
+  return vlf::pages_compact(p, workspace, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? VLF_OK : VLF_ERR_LAUNCH;
 }
 
 }  // extern "C"

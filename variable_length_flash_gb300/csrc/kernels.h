@@ -55,6 +55,25 @@ struct RopeParams {
 };
 cudaError_t rope(const RopeParams &p, cudaStream_t st);
 
+// Norm of each head with the rotary positions in the same pass, and its gradients (norm_rope.cu).
+struct Rows {  // of q or k; strides as above
+  const void *x, *dy, *w;  // dy: backward; w: NULL (ones) or [d] of type w_dtype
+  void *out, *dw;          // y, or dx; dw: backward, NULL or [d]
+  long long x_stride, dy_stride, out_stride;
+};
+struct NormRopeParams {
+  Rows q, k;
+  const int32_t *positions;
+  const float *inv_freq;
+  float *part;  // backward: norm_rope_workspace(d) bytes where a dw is wanted, else NULL
+  int first[4];
+  int total, h_q, h_k, d, rot, dtype, w_dtype, interleaved;
+  float eps;
+  int lanes, hpt;  // set by the launcher: lanes of a token, heads of a lane
+};
+size_t norm_rope_workspace(int d);
+cudaError_t norm_rope(const NormRopeParams &p, bool backward, cudaStream_t st);
+
 // Attention over a shared prefix and each sequence's own keys (prefix.cu): p.k / p.v / p.cu_kv /
 // p.total_kv / p.max_kv describe the own keys; the prefix is [prefix_len, h_kv, d].
 struct PrefixParams {
@@ -90,6 +109,63 @@ struct EvictParams {
   int *err;
 };
 cudaError_t cache_evict(const EvictParams &p, cudaStream_t st);
+
+// A cache of pages in e4m3 (pages.cu): k_pages [num_pages][h_kv][page][d_qk], scales [num_pages][h_kv].
+struct PagesWriteParams {
+  const void *k, *v;              // [total][h_kv][d]
+  long long k_stride, v_stride;   // elements between tokens
+  void *k_pages, *v_pages;
+  float *k_scale, *v_scale;
+  const int32_t *table;           // [num_seqs][max_pages]
+  const int32_t *cu, *kv_lens;    // new tokens [num_seqs + 1], lengths with them [num_seqs]
+  int num_seqs, total, max_pages, num_pages, page, log2_page, h_kv, d_qk, d_v, dtype;
+  int *err;
+};
+cudaError_t pages_write(const PagesWriteParams &p, cudaStream_t st);
+
+struct PagesCopyParams {
+  void *k_pages, *v_pages;
+  float *k_scale, *v_scale;
+  const int32_t *src, *dst;  // [n]; src < 0: no copy
+  int n, num_pages, page, h_kv, d_qk, d_v;
+  int *err;
+  int chunk;  // set by the launcher: pairs per block
+};
+cudaError_t pages_copy(PagesCopyParams p, cudaStream_t st);
+
+struct PagesForkParams {
+  const int32_t *table, *lens, *refs, *parents, *grow;
+  int num_in, num_out, max_pages, num_pages, log2_page;
+  int *table_out, *lens_out, *refs_out, *src, *dst, *left;
+  int *err;
+  // workspace
+  int *outside, *whole, *owner, *list, *counts, *begin, *state, chunks;
+};
+size_t pages_fork_workspace(int num_pages, int num_out);
+cudaError_t pages_fork(PagesForkParams p, void *workspace, cudaStream_t st);
+
+struct PagesCompactParams {
+  const int32_t *table, *refs;
+  long long entries;  // of the table
+  int num_pages;
+  int *table_out, *refs_out, *to, *src, *dst, *used;
+  // workspace
+  int *counts, *order, chunks;
+};
+size_t pages_compact_workspace(int num_pages);
+cudaError_t pages_compact(PagesCompactParams p, void *workspace, cudaStream_t st);
+
+// Attention over it (pages_attn.cu): p.q, p.cu_q, sizes, mask, scale, out and lse as in the forward.
+struct PagesAttnParams {
+  Params p;
+  const uint8_t *k_pages, *v_pages;
+  const float *k_scale, *v_scale;
+  const int32_t *table, *kv_lens;
+  int max_pages, num_pages, page, log2_page;
+};
+size_t pages_attn_workspace(int num_seqs, int max_q, int h_q, int h_kv, int d_qk, int d_v, int dtype, unsigned flags,
+                            int num_sms);
+cudaError_t pages_forward(const PagesAttnParams &a, void *workspace, int num_sms, cudaStream_t st);
 
 // Host-side count of successful kernel launches (api.cu).
 void count_launch(int n = 1);

@@ -1,0 +1,564 @@
+// A cache of pages: keys and values of a layer held in e4m3 as [num_pages][h_kv][page][d], with one fp32
+// scale for each page and head ([num_pages][h_kv]), reached through the sequences' page tables.  Here are
+// the kernels that write tokens into pages, copy pages, and keep the tables: which pages the sequences of
+// the next step have (fork), and the pages in use moved to the front (compact).
+#include "e4m3.cuh"
+#include "kernels.h"
+#include "tc_common.cuh"
+
+namespace vlf {
+namespace {
+
+// ------------------------------------------------------------------------------ writing
+// A value rounds to nearest e4m3 of x / scale.  The scale is a power of two, so a page whose scale grows
+// loses nothing but what falls below e4m3's least step: bytes already there are multiplied by
+// old / new and rounded again.  (A scale that is not a power of two, 448 / amax say, would round the whole
+// page anew with each token that raises it.)
+//
+// Bound: HBM, each token read once, a byte written for it.  A block has one page of one head, of K or of
+// V: it keeps the rows in registers between the maximum and the rounding.
+constexpr int kKeep = 8;  // chunks a thread keeps; what is behind them is read again
+
+template <typename T, int V> struct Values {
+  float x[V];
+  __device__ __forceinline__ void load(const T *p) {
+    if constexpr (V == 1) {
+      x[0] = to_f32<T>(*p);
+    } else if constexpr (sizeof(T) == 4) {
+      const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+      const uint4 r = *reinterpret_cast<const uint4 *>(p);
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = tc::unpack2(w[i], std::is_same<T, __nv_bfloat16>::value);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    }
+  }
+};
+
+// The unit blockIdx.x of a call: sequence s has the units from cu[s] / page + 2 s on, at least as many as
+// its tokens touch pages.
+template <typename T, int V, int NT>
+__global__ void __launch_bounds__(NT) pages_write_kernel(const PagesWriteParams p) {
+  __shared__ float top[NT / 32];
+  const int unit = blockIdx.x, head = blockIdx.y >> 1, is_v = blockIdx.y & 1;
+  int s = 0, hi = p.num_seqs;
+  while (hi - s > 1) {
+    const int mid = (s + hi) / 2;
+    if ((__ldg(p.cu + mid) >> p.log2_page) + 2 * mid <= unit) s = mid;
+    else hi = mid;
+  }
+  const int t0 = __ldg(p.cu + s), t1 = __ldg(p.cu + s + 1), len = __ldg(p.kv_lens + s);
+  if (t0 < 0 || t0 > t1 || t1 > p.total || len < t1 - t0 || (len > 0 && (len - 1) >> p.log2_page >= p.max_pages)) {
+    if (threadIdx.x == 0) set_error(p.err, VLF_ERR_BAD_SEQLENS);
+    return;
+  }
+  if (t0 == t1) return;
+  const int first = len - (t1 - t0), nth = unit - ((t0 >> p.log2_page) + 2 * s);
+  const int index = (first >> p.log2_page) + nth;
+  if (nth < 0 || index > (len - 1) >> p.log2_page) return;
+  const int page = __ldg(p.table + (long long)s * p.max_pages + index);
+  if (page < 0 || page >= p.num_pages) {
+    if (threadIdx.x == 0) set_error(p.err, VLF_ERR_BAD_PAGES);
+    return;
+  }
+  // slots [a, b) of the page take tokens t .. t + b - a
+  const int base = index << p.log2_page, a = max(first - base, 0), b = min(len - base, p.page);
+  const long long t = (long long)t0 + (base + a - first);
+  const int d = is_v ? p.d_v : p.d_qk;
+  const long long stride = is_v ? p.v_stride : p.k_stride;
+  const T *x = static_cast<const T *>(is_v ? p.v : p.k) + t * stride + (long long)head * d;
+  const long long slot = (long long)page * p.h_kv + head;
+  uint8_t *bytes = static_cast<uint8_t *>(is_v ? p.v_pages : p.k_pages) + slot * p.page * d;
+  float *scale = (is_v ? p.v_scale : p.k_scale) + slot;
+  const float was = *scale;
+
+  const int chunks = d / V, n = (b - a) * chunks;
+  Values<T, V> kept[kKeep];
+  float m = 0.f;
+  auto biggest = [&](const Values<T, V> &v) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float y = fabsf(v.x[e]);
+      if (y <= 3.402823466e38f) m = fmaxf(m, y);  // (what is not finite does not count)
+    }
+  };
+  auto at = [&](int i) { return x + (long long)(i / chunks) * stride + (i % chunks) * V; };
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    const int i = threadIdx.x + k * NT;
+    if (i < n) kept[k].load(at(i));
+  }
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if (threadIdx.x + k * NT < n) biggest(kept[k]);
+  for (int i = threadIdx.x + kKeep * NT; i < n; i += NT) {
+    Values<T, V> v;
+    v.load(at(i));
+    biggest(v);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if constexpr (NT > 32) {
+    if (threadIdx.x % 32 == 0) top[threadIdx.x / 32] = m;
+    __syncthreads();
+    m = top[threadIdx.x % (NT / 32)];
+#pragma unroll
+    for (int o = NT / 64; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
+  float now = page_scale(m);
+  if (a > 0 && was >= now) now = was;  // (slot 0 begins a page: what its scale was does not count)
+  const float inv = 1.f / now;
+  if (a > 0 && now != was) {
+    const float ratio = was / now;
+    for (int i = threadIdx.x; i < p.page * d / 2; i += NT) {
+      const int c0 = 2 * i / d;
+      // (pairs of bytes: d may be odd, but a page has an even number of rows)
+      uint16_t *at2 = reinterpret_cast<uint16_t *>(bytes) + i;
+      if (c0 >= a && (2 * i + 1) / d < b) continue;
+      const float2 f = e4m3_pair(*at2);
+      *at2 = (uint16_t)e4m3x2(f.x * ratio, f.y * ratio);
+    }
+    if constexpr (NT > 32) __syncthreads();
+    else __syncwarp();
+  }
+  auto store = [&](int i, const Values<T, V> &v) {
+    uint8_t *to = bytes + (long long)(a + i / chunks) * d + (i % chunks) * V;
+    if constexpr (V == 1) {
+      *to = (uint8_t)e4m3_byte(v.x[0], inv);
+    } else {
+      float most = 0.f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) most = fmaxf(most, fabsf(v.x[e]));
+      uint32_t w[2];
+      bool odd = !(most <= 3.402823466e38f);
+#pragma unroll
+      for (int e = 0; e < V; ++e) odd |= v.x[e] != v.x[e];
+      if (odd) {
+        w[0] = w[1] = 0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) w[e / 4] |= e4m3_byte(v.x[e], inv) << 8 * (e % 4);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          w[e] = e4m3x2(v.x[4 * e] * inv, v.x[4 * e + 1] * inv) | e4m3x2(v.x[4 * e + 2] * inv, v.x[4 * e + 3] * inv) << 16;
+      }
+      *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if (threadIdx.x + k * NT < n) store(threadIdx.x + k * NT, kept[k]);
+  for (int i = threadIdx.x + kKeep * NT; i < n; i += NT) {
+    Values<T, V> v;
+    v.load(at(i));
+    store(i, v);
+  }
+  if (threadIdx.x == 0 && now != was) *scale = now;
+}
+
+template <typename T>
+cudaError_t write(PagesWriteParams p, cudaStream_t st) {
+  constexpr int A = 16 / sizeof(T);
+  const bool vec = p.d_qk % 8 == 0 && p.d_v % 8 == 0 && p.k_stride % A == 0 && p.v_stride % A == 0;
+  // one warp where a sequence has a few tokens (a decode step), else enough threads to keep a page
+  const bool few = (long long)p.total <= 4ll * p.num_seqs;
+  const void *kern = vec ? (few ? (const void *)pages_write_kernel<T, 8, 32> : (const void *)pages_write_kernel<T, 8, 256>)
+                         : (few ? (const void *)pages_write_kernel<T, 1, 32> : (const void *)pages_write_kernel<T, 1, 256>);
+  const dim3 grid((unsigned)((p.total >> p.log2_page) + 2 * p.num_seqs), (unsigned)(2 * p.h_kv));
+  void *args[1] = {&p};
+  return launch_plain(kern, grid, few ? 32 : 256, 0, st, args);
+}
+
+// ------------------------------------------------------------------------------ copying
+// Bound: HBM.  Pair i is page src[i] over page dst[i], all heads; a block has `chunk` pairs' segments of
+// 16 KB.
+constexpr int kSegment = 16384;
+
+__global__ void __launch_bounds__(256) pages_copy_kernel(const PagesCopyParams p) {
+  const long long kb = (long long)p.h_kv * p.page * p.d_qk, vb = (long long)p.h_kv * p.page * p.d_v;
+  const int ks = (int)((kb + kSegment - 1) / kSegment);
+  const bool is_v = (int)blockIdx.y >= ks;
+  const long long at = (long long)(is_v ? blockIdx.y - ks : blockIdx.y) * kSegment;
+  const long long size = is_v ? vb : kb;
+  const int n = (int)((min(size, at + kSegment) - at) / 16);  // (a page has 16 rows or more)
+  uint8_t *pages = static_cast<uint8_t *>(is_v ? p.v_pages : p.k_pages);
+  float *scale = is_v ? p.v_scale : p.k_scale;
+  const int i0 = blockIdx.x * p.chunk, i1 = min(i0 + p.chunk, p.n);
+  for (int i = i0; i < i1; ++i) {
+    const int src = __ldg(p.src + i), dst = __ldg(p.dst + i);
+    if (src < 0) continue;
+    if (src >= p.num_pages || dst < 0 || dst >= p.num_pages) {
+      if (threadIdx.x == 0) set_error(p.err, VLF_ERR_BAD_PAGES);
+      continue;
+    }
+    const uint4 *from = reinterpret_cast<const uint4 *>(pages + (long long)src * size + at);
+    uint4 *to = reinterpret_cast<uint4 *>(pages + (long long)dst * size + at);
+    uint4 r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (threadIdx.x + 256 * k < n) r[k] = from[threadIdx.x + 256 * k];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (threadIdx.x + 256 * k < n) to[threadIdx.x + 256 * k] = r[k];
+    if (at == 0)
+      for (int h = threadIdx.x; h < p.h_kv; h += 256)
+        scale[(long long)dst * p.h_kv + h] = scale[(long long)src * p.h_kv + h];
+  }
+}
+
+// ------------------------------------------------------------------------------ tables
+constexpr int kChunk = 1024;  // pages of a block that counts
+
+__device__ __forceinline__ int pages_of(int len, int log2_page) { return (int)(((long long)len + (1 << log2_page) - 1) >> log2_page); }
+
+// Sum over a block of 256 threads; every thread gets it.
+__device__ __forceinline__ long long block_sum(long long x) {
+  __shared__ long long red[8];
+  for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = x;
+  __syncthreads();
+  x = 0;
+  for (int i = 0; i < 8; ++i) x += red[i];
+  return x;
+}
+// The sum before this thread, over a block of 256 threads; `all` is the whole sum.
+__device__ __forceinline__ int block_before(int x, int &all) {
+  __shared__ int red[8];
+  const int lane = threadIdx.x % 32;
+  int y = x;
+  for (int o = 1; o < 32; o *= 2) {
+    const int z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
+  }
+  __syncthreads();
+  if (lane == 31) red[threadIdx.x / 32] = y;
+  __syncthreads();
+  int before = 0;
+  all = 0;
+  for (int i = 0; i < 8; ++i) {
+    if (i < (int)threadIdx.x / 32) before += red[i];
+    all += red[i];
+  }
+  return before + y - x;
+}
+
+// Fork.  outside[p]: holders of p that are no row of the old table; whole[p]: new rows that have it whole;
+// owner[p]: the first new row that goes on inside it.
+__global__ void __launch_bounds__(256) fork_begin_kernel(const PagesForkParams p) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i < p.num_pages) {
+    p.outside[i] = p.refs[i];
+    p.whole[i] = 0;
+    p.owner[i] = 0x7fffffff;
+  }
+  if (i < 4) p.state[i] = 0;  // bad, free pages, pages needed
+}
+
+// A new row's parent, its length and the whole pages in it; false where it has no pages.
+struct Row {
+  int parent, len, whole;
+  bool part;
+};
+__device__ __forceinline__ Row row_of(const PagesForkParams &p, int s) {
+  Row r{__ldg(p.parents + s), 0, 0, false};
+  if (r.parent >= 0 && r.parent < p.num_in) r.len = max(0, __ldg(p.lens + r.parent));
+  r.whole = r.len >> p.log2_page;
+  r.part = (r.len & ((1 << p.log2_page) - 1)) != 0;
+  return r;
+}
+
+// Grid y: the old rows, then the new ones; x: runs of 256 entries.
+__global__ void __launch_bounds__(256) fork_count_kernel(const PagesForkParams p) {
+  tc::pdl_wait();
+  const int j = blockIdx.x * 256 + threadIdx.x;
+  for (int y = blockIdx.y; y < p.num_in + p.num_out; y += gridDim.y) {
+    const bool old = y < p.num_in;
+    Row r{y, 0, 0, false};
+    if (old) {
+      r.len = __ldg(p.lens + y);
+      if (r.len < 0 || pages_of(r.len, p.log2_page) > p.max_pages) {
+        if (j == 0) p.state[0] = VLF_ERR_BAD_SEQLENS;
+        continue;
+      }
+    } else {
+      r = row_of(p, y - p.num_in);
+      const int grow = __ldg(p.grow + y - p.num_in);
+      if (j == 0 && r.parent >= p.num_in) p.state[0] = VLF_ERR_BAD_PAGES;
+      if (grow < 0 || (long long)r.len + grow > (long long)p.max_pages << p.log2_page) {
+        if (j == 0) p.state[0] = VLF_ERR_BAD_SEQLENS;
+        continue;
+      }
+    }
+    if (j >= min(pages_of(r.len, p.log2_page), p.max_pages)) continue;
+    const int page = __ldg(p.table + (long long)r.parent * p.max_pages + j);
+    if (page < 0 || page >= p.num_pages) {
+      p.state[0] = VLF_ERR_BAD_PAGES;
+    } else if (old) {
+      atomicSub(p.outside + page, 1);
+    } else if (j < r.whole) {
+      atomicAdd(p.whole + page, 1);
+    } else {
+      atomicMin(p.owner + page, y - p.num_in);
+    }
+  }
+}
+// Holders of page i once the new rows have what they share or keep.
+__device__ __forceinline__ int held(const PagesForkParams &p, int i) {
+  const int n = p.outside[i] + p.whole[i];
+  return n == 0 && p.owner[i] != 0x7fffffff ? 1 : n;
+}
+// The page that a new row goes on in, and whether it keeps it (else it takes a copy).
+__device__ __forceinline__ int part_of(const PagesForkParams &p, const Row &r, int s, bool &keeps) {
+  keeps = false;
+  if (!r.part || r.whole >= p.max_pages) return -1;
+  const int page = __ldg(p.table + (long long)r.parent * p.max_pages + r.whole);
+  if (page < 0 || page >= p.num_pages) return -1;
+  keeps = p.outside[page] + p.whole[page] == 0 && p.owner[page] == s;
+  return page;
+}
+
+// Free pages of each chunk.
+__global__ void __launch_bounds__(256) fork_free_kernel(const PagesForkParams p) {
+  tc::pdl_wait();
+  int n = 0;
+  for (int k = 0; k < kChunk / 256; ++k) {
+    const long long i = (long long)blockIdx.x * kChunk + k * 256 + threadIdx.x;
+    if (i >= p.num_pages) continue;
+    if (p.outside[i] < 0 || p.refs[i] < 0) p.state[0] = VLF_ERR_BAD_PAGES;
+    n += held(p, (int)i) == 0;
+  }
+  n = (int)block_sum(n);
+  if (threadIdx.x == 0) p.counts[blockIdx.x] = n;
+}
+
+// The free pages in order (a block for each chunk); the last block: where each new row's new pages begin.
+__global__ void __launch_bounds__(256) fork_list_kernel(const PagesForkParams p) {
+  tc::pdl_wait();
+  if ((int)blockIdx.x < p.chunks) {
+    long long before = 0, total = 0;
+    for (int c = threadIdx.x; c < p.chunks; c += 256) {
+      const int n = p.counts[c];
+      before += c < (int)blockIdx.x ? n : 0;
+      total += n;
+    }
+    int at = (int)block_sum(before);
+    total = block_sum(total);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.state[1] = (int)total;
+    for (int k = 0; k < kChunk / 256; ++k) {
+      const long long i = (long long)blockIdx.x * kChunk + k * 256 + threadIdx.x;
+      const int n = i < p.num_pages && held(p, (int)i) == 0;
+      int all;
+      const int mine = block_before(n, all);
+      if (n) p.list[at + mine] = (int)i;
+      at += all;
+    }
+    return;
+  }
+  long long at = 0;
+  for (int s0 = 0; s0 < p.num_out; s0 += 256) {
+    const int s = s0 + threadIdx.x;
+    int need = 0;
+    if (s < p.num_out) {
+      const Row r = row_of(p, s);
+      bool keeps;
+      const int page = part_of(p, r, s, keeps);
+      const long long to = min((long long)r.len + max(0, __ldg(p.grow + s)), (long long)p.max_pages << p.log2_page);
+      need = pages_of((int)to, p.log2_page) - pages_of(r.len, p.log2_page) + (page >= 0 && !keeps);
+    }
+    int all;
+    const int before = block_before(need, all);
+    if (s < p.num_out) p.begin[s] = (int)min(at + before, (long long)0x7fffffff);
+    at += all;
+  }
+  if (threadIdx.x == 0) p.state[2] = (int)min(at, (long long)0x7fffffff);
+}
+
+// The new tables (grid y: the new rows, x: runs of 256 entries) and, in the same grid, the new counts.
+__global__ void __launch_bounds__(256) fork_end_kernel(const PagesForkParams p) {
+  tc::pdl_wait();
+  const int bad = p.state[0], free = p.state[1], need = p.state[2];
+  const bool ok = bad == 0 && need <= free;
+  const long long flat = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+  if (flat == 0) {
+    if (bad) set_error(p.err, bad);
+    *p.left = bad ? (int)0x80000000 : free - need;
+  }
+  // pages that the call gives out are its `need` first free ones: each new row has its run of them
+  for (long long i = flat; i < p.num_pages; i += (long long)gridDim.x * gridDim.y * 256)
+    if (!ok) p.refs_out[i] = p.refs[i];
+    else if (const int n = held(p, (int)i)) p.refs_out[i] = n;
+  if (ok)
+    for (long long i = flat; i < free; i += (long long)gridDim.x * gridDim.y * 256) p.refs_out[p.list[i]] = i < need;
+  const int j = blockIdx.x * 256 + threadIdx.x;
+  for (int s = blockIdx.y; s < p.num_out; s += gridDim.y) {
+    const Row r = row_of(p, s);
+    bool keeps;
+    const int part = part_of(p, r, s, keeps);
+    const int len = ok ? r.len + __ldg(p.grow + s) : 0;
+    if (j == 0) {
+      const bool copy = ok && part >= 0 && !keeps;
+      p.lens_out[s] = len;
+      p.src[s] = copy ? part : -1;
+      p.dst[s] = copy ? p.list[p.begin[s]] : -1;
+    }
+    if (j >= p.max_pages) continue;
+    int page = -1;
+    if (j < pages_of(len, p.log2_page)) {
+      if (j < r.whole) page = __ldg(p.table + (long long)r.parent * p.max_pages + j);
+      else if (keeps && j == r.whole) page = part;
+      else page = p.list[p.begin[s] + j - r.whole - (keeps ? 1 : 0)];
+    }
+    p.table_out[(long long)s * p.max_pages + j] = page;
+  }
+}
+
+// Compact.  Of the U pages in use the ones behind the first U pages move into the free ones among them, the
+// first into the first.
+__global__ void __launch_bounds__(256) compact_count_kernel(const PagesCompactParams p) {
+  int n = 0;
+  for (int k = 0; k < kChunk / 256; ++k) {
+    const long long i = (long long)blockIdx.x * kChunk + k * 256 + threadIdx.x;
+    if (i >= p.num_pages) continue;
+    n += p.refs[i] > 0;
+    if (i < p.num_pages / 2) p.src[i] = p.dst[i] = -1;
+  }
+  n = (int)block_sum(n);
+  if (threadIdx.x == 0) p.counts[blockIdx.x] = n;
+}
+// order[p]: which of the moving pages p is (-1: none).
+__global__ void __launch_bounds__(256) compact_list_kernel(const PagesCompactParams p) {
+  tc::pdl_wait();
+  long long before = 0, total = 0;
+  for (int c = threadIdx.x; c < p.chunks; c += 256) {
+    const int n = p.counts[c];
+    before += c < (int)blockIdx.x ? n : 0;
+    total += n;
+  }
+  int at = (int)block_sum(before);
+  const int used = (int)block_sum(total);
+  // pages in use among the first `used`
+  long long front = 0;
+  for (int c = threadIdx.x; c < used / kChunk; c += 256) front += p.counts[c];
+  for (int i = used / kChunk * kChunk + threadIdx.x; i < used; i += 256) front += p.refs[i] > 0;
+  front = block_sum(front);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.used = used;
+  for (int k = 0; k < kChunk / 256; ++k) {
+    const int i = (int)(blockIdx.x * kChunk + k * 256 + threadIdx.x);
+    const int n = i < p.num_pages && p.refs[i] > 0;
+    int all;
+    const int rank = at + block_before(n, all);  // pages in use before this one
+    at += all;
+    if (i >= p.num_pages) continue;
+    p.order[i] = -1;
+    if (n && i >= used) {
+      p.order[i] = rank - (int)front;
+      p.src[rank - (int)front] = i;
+    } else if (!n && i < used) {
+      p.dst[i - rank] = i;
+    }
+  }
+}
+// Where the page i in use is afterwards.
+__device__ __forceinline__ int moved(const PagesCompactParams &p, int i) {
+  const int o = p.order[i];
+  return o < 0 ? i : p.dst[o];
+}
+__global__ void __launch_bounds__(256) compact_end_kernel(const PagesCompactParams p) {
+  tc::pdl_wait();
+  const long long step = (long long)gridDim.x * 256;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < p.num_pages; i += step) {
+    const int n = p.refs[i];
+    p.to[i] = n > 0 ? moved(p, (int)i) : -1;
+    const int used = *p.used;
+    if (n > 0) p.refs_out[moved(p, (int)i)] = n;
+    if (i >= used) p.refs_out[i] = 0;
+  }
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < p.entries; i += step) {
+    const int page = p.table[i];
+    p.table_out[i] = page >= 0 && page < p.num_pages && p.refs[page] > 0 ? moved(p, page) : -1;
+  }
+}
+
+size_t ints(long long n) { return ((size_t)n * 4 + 255) & ~(size_t)255; }
+int chunks_of(int num_pages) { return (int)(((long long)num_pages + kChunk - 1) / kChunk); }
+
+}  // namespace
+
+cudaError_t pages_write(const PagesWriteParams &p, cudaStream_t st) {
+  if (p.dtype == VLF_F32) return write<float>(p, st);
+  if (p.dtype == VLF_BF16) return write<__nv_bfloat16>(p, st);
+  return write<__half>(p, st);
+}
+
+cudaError_t pages_copy(PagesCopyParams p, cudaStream_t st) {
+  auto segments = [&](int d) { return ((long long)p.h_kv * p.page * d + kSegment - 1) / kSegment; };
+  const long long segs = segments(p.d_qk) + segments(p.d_v);
+  // pairs per block: what leaves about eight blocks per SM (as many are resident)
+  p.chunk = (int)max(1ll, min(32ll, (long long)p.n * segs / (152 * 8)));
+  void *args[1] = {&p};
+  return launch_plain((const void *)pages_copy_kernel, dim3((unsigned)((p.n + p.chunk - 1) / p.chunk), (unsigned)segs),
+                      256, 0, st, args);
+}
+
+size_t pages_fork_workspace(int num_pages, int num_out) {
+  return 4 * ints(num_pages) + ints(chunks_of(num_pages)) + ints(num_out) + ints(4);
+}
+cudaError_t pages_fork(PagesForkParams p, void *workspace, cudaStream_t st) {
+  char *w = static_cast<char *>(workspace);
+  auto take = [&](long long n) {
+    int *r = reinterpret_cast<int *>(w);
+    w += ints(n);
+    return r;
+  };
+  p.chunks = chunks_of(p.num_pages);
+  p.outside = take(p.num_pages);
+  p.whole = take(p.num_pages);
+  p.owner = take(p.num_pages);
+  p.list = take(p.num_pages);
+  p.counts = take(p.chunks);
+  p.begin = take(p.num_out);
+  p.state = take(4);
+  void *args[1] = {&p};
+  const unsigned pages = (unsigned)(((long long)max(p.num_pages, 4) + 255) / 256);
+  const unsigned wide = (unsigned)max(1, (p.max_pages + 255) / 256);
+  auto then = [&](const void *kern, dim3 grid) {
+    const cudaError_t r = launch_dependent(kern, grid, 256, 0, st, args);
+    if (r == cudaSuccess) count_launch();
+    return r;
+  };
+  cudaError_t e = launch_plain((const void *)fork_begin_kernel, dim3(pages), 256, 0, st, args);
+  if (e == cudaSuccess && p.num_in + p.num_out > 0)
+    e = then((const void *)fork_count_kernel, dim3(wide, (unsigned)min(p.num_in + p.num_out, 65535)));
+  if (e == cudaSuccess && p.chunks > 0)
+    e = then((const void *)fork_free_kernel, dim3((unsigned)p.chunks));
+  if (e == cudaSuccess) e = then((const void *)fork_list_kernel, dim3((unsigned)p.chunks + 1));
+  if (e == cudaSuccess) e = then((const void *)fork_end_kernel, dim3(wide, (unsigned)max(1, min(p.num_out, 65535))));
+  return e;
+}
+
+size_t pages_compact_workspace(int num_pages) { return ints(chunks_of(num_pages)) + ints(num_pages); }
+cudaError_t pages_compact(PagesCompactParams p, void *workspace, cudaStream_t st) {
+  p.chunks = chunks_of(p.num_pages);
+  p.counts = static_cast<int *>(workspace);
+  p.order = reinterpret_cast<int *>(static_cast<char *>(workspace) + ints(p.chunks));
+  void *args[1] = {&p};
+  cudaError_t e = launch_plain((const void *)compact_count_kernel, dim3((unsigned)p.chunks), 256, 0, st, args);
+  auto then = [&](const void *kern, unsigned blocks) {
+    const cudaError_t r = launch_dependent(kern, dim3(blocks), 256, 0, st, args);
+    if (r == cudaSuccess) count_launch();
+    return r;
+  };
+  if (e == cudaSuccess) e = then((const void *)compact_list_kernel, (unsigned)p.chunks);
+  const long long most = max(p.entries, (long long)p.num_pages);
+  if (e == cudaSuccess)
+    e = then((const void *)compact_end_kernel, (unsigned)min((most + 255) / 256, 152ll * 8));
+  return e;
+}
+
+}  // namespace vlf

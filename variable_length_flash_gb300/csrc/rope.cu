@@ -22,75 +22,16 @@
 // 128 in bf16, sliced from a fused projection, 65 us = 94% of the copy rate; 16384 tokens of 32 heads
 // of 96 in fp16, 64 columns of which turn, 35 us = 85% (segments of 64 bytes, and 782 blocks where 304 are
 // resident: the third wave is half full); 64 tokens 3 us, which is a launch.
-#include <type_traits>
-
-#include "common.cuh"
 #include "kernels.h"
+#include "rope.cuh"
 
 namespace vlf {
 namespace {
 
-// V elements in one access (16 bytes; V = 1: one element).
-template <typename T, int V> struct Chunk {
-  uint4 r;
-  __device__ __forceinline__ void get(float (&x)[V]) const {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(T) == 4) {
-        x[i] = __uint_as_float(w[i]);
-      } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-      }
-    }
-  }
-  __device__ __forceinline__ void set(const float (&x)[V]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(T) == 4) {
-        w[i] = __float_as_uint(x[i]);
-      } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
-      } else {
-        const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
-      }
-    }
-    r = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <typename T> struct Chunk<T, 1> {
-  T r;
-  __device__ __forceinline__ void get(float (&x)[1]) const { x[0] = to_f32<T>(r); }
-  __device__ __forceinline__ void set(const float (&x)[1]) { r = from_f32<T>(x[0]); }
-};
-
-// f / 2 pi less the nearest whole number, in units of 2^-64 (as an unsigned number: mod 2^64).  Counted
-// from the nearest whole number, not from the one below, a small negative turn keeps its bits.
-__device__ __forceinline__ unsigned long long turns_of(float f) {
-  double t = (double)f * 0.15915494309189533577;  // 1 / (2 pi)
-  t -= rint(t);
-  return (unsigned long long)__double2ll_rn(t * 18446744073709551616.0);
-}
-// cos and sin of pos * F turns.
-__device__ __forceinline__ void turn(int pos, unsigned long long F, float &c, float &s) {
-  const long long ph = (long long)((unsigned long long)(long long)pos * F);
-  // rounded to 32 bits (a half turn wraps to minus a half turn: the same angle)
-  const int p32 = (int)((unsigned long long)(ph + 0x80000000ll) >> 32);
-  sincospif((float)p32 * 4.6566128730773926e-10f, &s, &c);  // 2^-31: in half turns
-}
+using namespace turning;
 
 // Grid y: a run of hpt heads of q or k; x: runs of 256 / units tokens, walked with the grid's stride.
-// Thread: chunk u of a token.  Chunks u < nrot hold V pairs -- columns V u and rot / 2 + V u, whose
-// partners they are, or (INTER, V > 1) the V / 2 pairs of neighbours in each --, the ones behind
-// them two chunks of columns that pass through.  HEADS: heads whose loads are in flight.
+// Thread: unit u of a token.  HEADS: heads whose loads are in flight.
 template <typename T, int V, bool INTER, int HEADS>
 __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
   __shared__ unsigned long long F[128];
@@ -104,28 +45,9 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
   const int phases_q = (p.h_q + p.hpt - 1) / p.hpt, ph = blockIdx.y;
   const bool is_k = ph >= phases_q;
   const int h0 = (is_k ? ph - phases_q : ph) * p.hpt, h1 = min(h0 + p.hpt, is_k ? p.h_k : p.h_q);
-  const bool rot = u < nrot;
-  int ca, cb;  // first columns of the thread's two chunks
-  if (rot) {
-    ca = INTER && V == 1 ? 2 * u : V * u;
-    cb = INTER && V == 1 ? ca + 1 : half + V * u;
-  } else {
-    ca = p.rot + V * (u - nrot);
-    cb = ca + V * ntail;
-  }
-  const bool two = cb < p.d;  // (a tail of an odd number of chunks: its last unit has one)
-  if (!two) cb = ca;
-  int pair[V], axis[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    int c = V * u + e;
-    if (INTER && V > 1) c = e < V / 2 ? V / 2 * u + e : half / 2 + V / 2 * (u - 1) + e;
-    pair[e] = rot ? c : 0;
-    int a = 0;
-#pragma unroll
-    for (int x = 1; x < 4; ++x) a += pair[e] >= p.first[x] && p.first[x] < half ? 1 : 0;
-    axis[e] = a;
-  }
+  const Unit<V, INTER> at(u, nrot, ntail, half, p.d, p.first);
+  const bool rot = at.rot, two = at.two;
+  const int ca = at.ca, cb = at.cb;
   const long long si = is_k ? p.k_stride : p.q_stride, so = is_k ? p.k_out_stride : p.q_out_stride;
   const T *in = static_cast<const T *>(is_k ? p.k : p.q);
   T *out = static_cast<T *>(is_k ? p.k_out : p.q_out);
@@ -135,7 +57,7 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
     if (rot) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        turn(__ldg(p.positions + (long long)axis[e] * p.total + tok), F[pair[e]], cs[e], sn[e]);
+        turn(__ldg(p.positions + (long long)at.axis[e] * p.total + tok), F[at.pair[e]], cs[e], sn[e]);
         if (p.inverse) sn[e] = -sn[e];
       }
     }
@@ -145,20 +67,7 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
       float a[V], b[V], ya[V], yb[V];
       x.get(a);
       y.get(b);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if constexpr (INTER && V > 1) {
-          // pair e < V / 2: columns 2 e, 2 e + 1 of chunk a; the others of chunk b
-          float *o = e < V / 2 ? ya : yb;
-          const float *i = e < V / 2 ? a : b;
-          const int c = 2 * (e % (V / 2));
-          o[c] = fmaf(i[c], cs[e], -(i[c + 1] * sn[e]));
-          o[c + 1] = fmaf(i[c + 1], cs[e], i[c] * sn[e]);
-        } else {
-          ya[e] = fmaf(a[e], cs[e], -(b[e] * sn[e]));
-          yb[e] = fmaf(b[e], cs[e], a[e] * sn[e]);
-        }
-      }
+      rotate<V, INTER>(a, b, cs, sn, ya, yb);
       x.set(ya);
       y.set(yb);
     };

@@ -20,7 +20,7 @@ import torch
 
 from . import (VLF_ERR_INVALID, VLF_ERR_UNSUPPORTED, VlfError, vlf_attn_varlen_bwd,
                vlf_attn_varlen_bwd_latent, vlf_attn_varlen_fwd, vlf_attn_varlen_fwd_latent,
-               vlf_bias_bands, vlf_rope)
+               vlf_bias_bands, vlf_norm_rope, vlf_norm_rope_bwd, vlf_rope)
 
 
 def mask_to_bias(mask: torch.Tensor) -> torch.Tensor:
@@ -170,6 +170,38 @@ def rotary_embedding(q, k, positions, inv_freq, sections=None, interleaved=False
         raise VlfError(VLF_ERR_INVALID, "q and k must be [tokens, heads, head_dim]")
     return _Rotary.apply(q, k, positions.contiguous(), inv_freq.contiguous(),
                          None if sections is None else tuple(sections), bool(interleaved), False)
+
+
+class _NormRotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, sections, interleaved, eps):
+        q, k = _token_dense(q), _token_dense(k)
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
+        ctx.args = (sections, interleaved, eps)
+        return vlf_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, sections, interleaved, eps)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq, dk):
+        q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
+        grads = vlf_norm_rope_bwd(_token_dense(dq), _token_dense(dk), q, k, q_weight, k_weight, positions, inv_freq,
+                                  *ctx.args)
+        return (*grads, None, None, None, None, None)
+
+
+def norm_rotary_embedding(q, k, q_weight, k_weight, positions=None, inv_freq=None, sections=None,
+                          interleaved=False, eps=1e-6):
+    """Root-mean-square norm of each head of packed q [tokens, H_q, D] and k [tokens, H_k, D] with its weight
+    [D] (or None), and rotary positions in the same pass (see ``vlf_norm_rope``), differentiable in q, k
+    and the weights.  q and k may be slices of a packed projection."""
+    for t in (positions, inv_freq):
+        if t is not None and t.requires_grad:
+            raise VlfError(VLF_ERR_UNSUPPORTED, "positions and inv_freq are constants")
+    if q.dim() != 3 or k.dim() != 3:
+        raise VlfError(VLF_ERR_INVALID, "q and k must be [tokens, heads, head_dim]")
+    c = lambda t: None if t is None else t.contiguous()  # noqa: E731
+    return _NormRotary.apply(q, k, c(q_weight), c(k_weight), c(positions), c(inv_freq),
+                             None if sections is None else tuple(sections), bool(interleaved), float(eps))
 
 
 def _refuse_flash_extras(dropout_p, alibi_slopes, return_attn_probs):
