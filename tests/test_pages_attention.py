@@ -116,9 +116,10 @@ def test_matches_the_definition(q_lens, kv_lens, page, hq, hkv, d, causal, windo
     c = problem(q_lens, kv_lens, page, hq, hkv, d, d, dtype, seed=len(q_lens) + page)
     got = call(c, causal=causal, window=window, flags=flags)
     check(got, c, causal=causal, window=window)
-    # (the same bits again; and a loose bound is any bound)
-    again = call(c, causal=causal, window=window, flags=flags, max_q=c["max_q"] + 5000)
-    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    again = call(c, causal=causal, window=window, flags=flags)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])  # the same bits
+    # (a loose bound is any bound; it may cut the work otherwise)
+    check(call(c, causal=causal, window=window, flags=flags, max_q=c["max_q"] + 5000), c, causal=causal, window=window)
 
 
 @pytest.mark.gpu

@@ -166,6 +166,10 @@ struct PagesAttnParams {
 size_t pages_attn_workspace(int num_seqs, int max_q, int h_q, int h_kv, int d_qk, int d_v, int dtype, unsigned flags,
                             int num_sms);
 cudaError_t pages_forward(const PagesAttnParams &a, void *workspace, int num_sms, cudaStream_t st);
+// Its tensor-core kernels (pages_tc.cu).
+bool pages_tc_supported(int d_qk, int d_v, int dtype, unsigned flags);
+size_t pages_tc_workspace(int max_q, int group, int d, int num_sms);
+cudaError_t pages_tc_forward(const PagesAttnParams &a, void *workspace, int num_sms, cudaStream_t st);
 
 // Host-side count of successful kernel launches (api.cu).
 void count_launch(int n = 1);

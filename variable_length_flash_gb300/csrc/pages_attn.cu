@@ -116,15 +116,24 @@ __global__ void __launch_bounds__(32 * kFmaWarps) pages_fma_kernel(const PagesAt
 
 }  // namespace
 
-size_t pages_attn_workspace(int, int, int, int, int, int, int, unsigned, int) { return 0; }
+size_t pages_attn_workspace(int num_seqs, int max_q, int h_q, int h_kv, int d_qk, int d_v, int dtype, unsigned flags,
+                            int num_sms) {
+  if (num_seqs < 1 || !pages_tc_supported(d_qk, d_v, dtype, flags)) return 0;
+  return pages_tc_workspace(max_q, h_q / h_kv, d_qk, num_sms);
+}
 
-cudaError_t pages_forward(const PagesAttnParams &a, void *, int, cudaStream_t st) {
-  const dim3 grid((unsigned)a.p.max_q, (unsigned)a.p.h_q, (unsigned)a.p.num_seqs);
+cudaError_t pages_forward(const PagesAttnParams &a, void *workspace, int num_sms, cudaStream_t st) {
+  const Params &p = a.p;
+  // (a tensor map needs a page, and its coordinates are ints)
+  const long long heads = (long long)a.num_pages * p.h_kv;
+  if (pages_tc_supported(p.d_qk, p.d_v, p.dtype, p.flags) && heads > 0 && heads < 0x7fffffff)
+    return pages_tc_forward(a, workspace, num_sms, st);
+  const dim3 grid((unsigned)p.max_q, (unsigned)p.h_q, (unsigned)p.num_seqs);
   PagesAttnParams copy = a;
   void *args[1] = {&copy};
-  const void *kern = a.p.dtype == VLF_F32    ? (const void *)pages_fma_kernel<float>
-                     : a.p.dtype == VLF_BF16 ? (const void *)pages_fma_kernel<__nv_bfloat16>
-                                             : (const void *)pages_fma_kernel<__half>;
+  const void *kern = p.dtype == VLF_F32    ? (const void *)pages_fma_kernel<float>
+                     : p.dtype == VLF_BF16 ? (const void *)pages_fma_kernel<__nv_bfloat16>
+                                           : (const void *)pages_fma_kernel<__half>;
   return launch_plain(kern, grid, 32 * kFmaWarps, 0, st, args);
 }
 

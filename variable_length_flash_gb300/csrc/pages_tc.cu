@@ -1,0 +1,889 @@
+// Attention over pages in e4m3 on the tensor cores (16-bit queries, widths 64 and 128).
+//
+// The bytes are multiplied as they are: both products are tcgen05 kind::f8f6f4, with the page as operand A
+// from shared memory, where TMA puts it, and nothing is converted.  Keys are the rows of a tile:
+//     S^T[key, column] = sum_c K[key, c] Q[column, c],       O^T[c, column] += sum_key V[key, c] P[key, column],
+// 128 keys a tile; a column is one query row of one head of the kv head's group.  So each of the 128
+// softmax threads has a key, whose scale (its page's) is one number of its, and a step with few
+// columns, a decode step's four or eight, still has 128 threads to share its exponentials.
+//
+// Eight bits are not enough for Q and P; each is a sum of several numbers of eight bits, exact enough:
+//  * Q, brought to [128, 256) by a power of two for each column, as two e4m3 terms (bf16) or three (fp16):
+//    x = t0 + t1 + t2, each the rest's nearest e4m3.  A term holds 4 bits and a sign, so bf16's 8 and fp16's
+//    11 bits are exact down to where the last term meets e4m3's least step, 2^-18 of the column's largest.
+//  * P, as three e5m2 terms: 3 bits each and two signs are 11 bits, half a step of fp16; the first term is
+//    the high byte of P in fp16.  e5m2 reaches from 2^-16 to 57344: with the column's largest P between 2^7 and
+//    2^15, what a key loses is below 2^-24 of the largest weight.  (Two e4m3 terms hold 9 bits, but reach
+//    down to 2^-18 only: a long tail of small weights behind one large one would vanish.)
+// The terms of Q are added by the accumulator; those of P are columns of their own, added at the end: the
+// matrix pipe reads each byte of V once for all of them.
+//
+// A key's scale multiplies its logits.  A value's scale goes into the exponent, P = 2^(logit + log2 scale -
+// reference), so that the reference follows the weights as they meet the values; the sum of the weights
+// takes P / scale.  The reference of a column moves when a P would pass 2^15 (a vote of the 128 threads on
+// each tile), and O is rescaled then.
+//
+// Work is cut evenly, whatever the lengths: the (sequence, kv head, query tile) items' key tiles, laid end to
+// end, are shared out to the resident CTAs in equal runs.  A run that holds a whole item writes it; one that
+// starts or ends inside an item leaves its part (two at most), which a second launch joins.  Loads run on
+// across items, so nothing starts or drains but at the two ends.  Nothing about the lengths is needed on the
+// host, and a loose bound costs nothing.
+//
+// Roles of a CTA: warps 0-3 softmax (thread = key) and the output (thread = column of V), warp 4 page loads,
+// warp 5 both products.
+#include <type_traits>
+
+#include "e4m3.cuh"
+#include "kernels.h"
+#include "tc_common.cuh"
+
+namespace vlf {
+namespace {
+
+using namespace tc;
+
+constexpr int kKeys = 128;         // keys of a tile
+constexpr float kNoRef = -1e30f;   // reference of a column that has met no key
+constexpr float kTop = 15.f;       // log2 of the largest P
+constexpr float kSet = 7.f;        // log2 of the largest P when the reference is set
+constexpr int kScales = 8;         // tiles whose scales are held (more than the rings let loads run ahead)
+constexpr float kLn2 = 0.69314718055994531f;
+
+struct TcParams {
+  PagesAttnParams a;
+  float *part;  // [2 grid][NC (D + 2)]
+  int4 *rec;    // [grid] {sequence, kv head, query tile, last CTA} of the item that a CTA begins and leaves open; -1: none
+  int rows;     // query rows of a query tile
+  int splits;   // query tiles of a row (a group with more heads than columns), else 1
+};
+
+// NC: columns of a tile.
+template <int D, int NC> struct Cfg {
+  static constexpr int NS = NC < 16 ? 16 : NC;              // columns of S (the least N of the product)
+  static constexpr int NP = (3 * NC + 15) / 16 * 16;        // columns of P and O: three terms
+  static constexpr int T_BYTES = kKeys * D;
+  static constexpr int KST = 3, VST = D == 128 && NC >= 32 ? 2 : 3;
+  static constexpr int PB = NC >= 16 ? 1 : 2;               // buffers of P
+  static constexpr int Q_TERM = NS * D, P_BYTES = NP * kKeys;
+  static constexpr int OFF_K = 0, OFF_V = OFF_K + KST * T_BYTES, OFF_Q = OFF_V + VST * T_BYTES, OFF_P = OFF_Q + 3 * Q_TERM;
+  static constexpr int OFF_COL = OFF_P + PB * P_BYTES;      // float2 (scale, -reference)[2][NC]
+  static constexpr int OFF_LIM = OFF_COL + 2 * NC * 8;      // int2 (first, end)[2][NC]
+  static constexpr int OFF_WM = OFF_LIM + 2 * NC * 8;       // float[4][NC]
+  static constexpr int OFF_FAC = OFF_WM + 4 * NC * 4;       // float[NC]
+  static constexpr int OFF_SC = OFF_FAC + NC * 4;           // float2 (k, v scale)[kScales][8]
+  static constexpr int OFF_RED = OFF_SC + kScales * 8 * 8;  // long long[8]
+  static constexpr int OFF_BAR = OFF_RED + 64;
+  static constexpr int B_KF = 0, B_KE = B_KF + KST, B_VF = B_KE + KST, B_VE = B_VF + VST, B_SF = B_VE + VST, B_SE = B_SF + 2,
+                       B_PF = B_SE + 2, B_PE = B_PF + PB, B_Q = B_PE + PB, B_OF = B_Q + 1, B_OE = B_OF + 1, B_SC = B_OE + 1,
+                       B_DRAIN = B_SC + kScales, BARS = B_DRAIN + 1;
+  static constexpr int OFF_END = OFF_BAR + BARS * 8 + 16;   // then the TMEM address and the abort flag
+  static constexpr int SMEM = OFF_END + 1024;               // (to start on 1024 bytes)
+  static constexpr int O_COL = 2 * NS;
+  static constexpr int TMEM = O_COL + NP <= 64 ? 64 : O_COL + NP <= 128 ? 128 : 256;
+  // resident CTAs per SM: by shared memory (227 KB) and TMEM (512 columns)
+  static constexpr int CTAS = (227 * 1024) / (SMEM + 1024) < 512 / TMEM ? (227 * 1024) / (SMEM + 1024) : 512 / TMEM;
+  static constexpr int PART = NC * (D + 2);                 // floats of a part
+};
+
+__device__ __forceinline__ uint32_t idesc_f8(uint32_t b_type, uint32_t n, uint32_t mn) {
+  // D fp32; A e4m3 (0), B e4m3 (0) or e5m2 (1); both K-major or both MN-major; M = 128
+  return (1u << 4) | (b_type << 10) | (mn << 15) | (mn << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+// Shared-memory descriptor with a swizzle code (0 none, 2 128 bytes, 4 64 bytes).
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 | (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)swizzle << 61;
+}
+__device__ __forceinline__ void mma_f8_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Barrier of the 128 softmax threads; whether any of them says x.
+__device__ __forceinline__ bool any_of_128(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+template <int N> __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t *r) {
+  static_assert(N == 4 || N == 8 || N == 16, "columns");
+  if constexpr (N == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr) : "memory");
+  } else if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr) : "memory");
+  } else {
+    tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(r));
+  }
+}
+// NC columns.
+template <int NC> __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[NC]) {
+  if constexpr (NC <= 16) {
+    tmem_ld<NC>(taddr, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NC; i += 16) tmem_ld<16>(taddr + i, r + i);
+  }
+}
+
+// The key tiles of the items from one on, in order.
+struct Walk {
+  const TcParams &p;
+  int s, head, qt;                // sequence, kv head, query tile
+  int q0, q_len, len, tiles_q;    // of the sequence; tiles_q = 0: nothing to do
+  int r0, r1, lo, hi, t0, nt;     // of the item: its rows, the keys they see, its key tiles (none: nt = 0)
+
+  __device__ __forceinline__ explicit Walk(const TcParams &x) : p(x) {}
+  __device__ __forceinline__ bool load(int seq) {  // false: bad lengths
+    s = seq;
+    const Params &b = p.a.p;
+    const int x = __ldg(b.cu_q + s), y = __ldg(b.cu_q + s + 1);
+    len = __ldg(p.a.kv_lens + s);
+    q0 = x;
+    q_len = y - x;
+    tiles_q = 0;
+    if (x < 0 || x > y || y > b.total_q || q_len > b.max_q || len < 0 ||
+        (len > 0 && (len - 1) >> p.a.log2_page >= p.a.max_pages))
+      return false;
+    tiles_q = p.splits > 1 ? q_len * p.splits : (q_len + p.rows - 1) / p.rows;
+    return true;
+  }
+  __device__ __forceinline__ void item() {
+    r0 = p.splits > 1 ? qt / p.splits : qt * p.rows;
+    r1 = min(r0 + p.rows, q_len);
+    kv_band(r0, r1, q_len, len, p.a.p.causal, p.a.p.window, lo, hi);
+    t0 = lo / kKeys;
+    nt = hi > lo ? (hi + kKeys - 1) / kKeys - t0 : 0;
+  }
+  __device__ __forceinline__ int units() const { return max(nt, 1); }
+  // units of one head of the sequence
+  __device__ __forceinline__ long long head_units() {
+    long long n = 0;
+    for (qt = 0; qt < tiles_q; ++qt) {
+      item();
+      n += units();
+    }
+    return n;
+  }
+  // to unit `at` of sequence seq; returns the unit within the item
+  __device__ __forceinline__ int seek(int seq, long long at) {
+    load(seq);
+    const long long per = head_units();
+    head = (int)(at / per);
+    at -= head * per;
+    for (qt = 0;; ++qt) {
+      item();
+      if (at < units()) return (int)at;
+      at -= units();
+    }
+  }
+  __device__ __forceinline__ void next() {
+    if (++qt >= tiles_q) {
+      qt = 0;
+      if (++head >= p.a.p.h_kv) {
+        head = 0;
+        do {  // (there is another one: the caller has units left)
+          if (s + 1 >= p.a.p.num_seqs) return;
+          load(s + 1);
+        } while (tiles_q == 0);
+      }
+    }
+    item();
+  }
+};
+// Values that a wait has made good: what uses them is not scheduled ahead of it.
+template <int N> __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+// The query row and head of column c; false where there is none.
+__device__ __forceinline__ bool column_of(const TcParams &p, int nc, const Walk &w, int c, int &row, int &head) {
+  const int group = p.a.p.group;
+  if (p.splits > 1) {
+    const int h = w.qt % p.splits * nc + c;
+    row = w.r0;
+    head = w.head * group + h;
+    return h < group;
+  }
+  row = w.r0 + c / group;
+  head = w.head * group + c % group;
+  return row < w.r1;
+}
+
+template <int D, int NC, bool BF16>
+__global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
+    pages_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                    const __grid_constant__ TcParams p) {
+  using C = Cfg<D, NC>;
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  constexpr int QT = BF16 ? 2 : 3;  // terms of Q
+  extern __shared__ uint8_t smem_dyn[];
+  const uint32_t base = (smem_u32(smem_dyn) + 1023u) & ~1023u;
+  uint8_t *const smem = smem_dyn + (base - smem_u32(smem_dyn));
+  const uint32_t sK = base + C::OFF_K, sV = base + C::OFF_V, sQ = base + C::OFF_Q, sP = base + C::OFF_P;
+  float2 *const col = reinterpret_cast<float2 *>(smem + C::OFF_COL);
+  int2 *const lim = reinterpret_cast<int2 *>(smem + C::OFF_LIM);
+  float *const wm = reinterpret_cast<float *>(smem + C::OFF_WM), *const fac = reinterpret_cast<float *>(smem + C::OFF_FAC);
+  float2 *const scales = reinterpret_cast<float2 *>(smem + C::OFF_SC);
+  long long *const red = reinterpret_cast<long long *>(smem + C::OFF_RED);
+  auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
+  uint32_t *const tmem_holder = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + C::BARS * 8);
+  volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const Params &b = p.a.p;
+  int *const err = b.err;
+
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::KST; ++i) { mbar_init(bar(C::B_KF + i), 1); mbar_init(bar(C::B_KE + i), 1); }
+    for (int i = 0; i < C::VST; ++i) { mbar_init(bar(C::B_VF + i), 1); mbar_init(bar(C::B_VE + i), 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(bar(C::B_SF + i), 1); mbar_init(bar(C::B_SE + i), 128); }
+    for (int i = 0; i < C::PB; ++i) { mbar_init(bar(C::B_PF + i), 128); mbar_init(bar(C::B_PE + i), 1); }
+    mbar_init(bar(C::B_Q), 128);
+    mbar_init(bar(C::B_OF), 1);
+    mbar_init(bar(C::B_OE), 128);
+    for (int i = 0; i < kScales; ++i) mbar_init(bar(C::B_SC + i), 1);
+    mbar_init(bar(C::B_DRAIN), 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(tmem_holder), C::TMEM);
+    tmem_relinquish();
+  }
+  if (warp == 4 && lane == 0) {
+    tma_prefetch_desc(&k_map);
+    tma_prefetch_desc(&v_map);
+  }
+  pdl_wait();
+
+  // Units of all sequences, then this CTA's run of them and where it begins: the threads take a sequence each.
+  Walk w(p);
+  auto units_of = [&](int s, bool tell) -> long long {
+    if (s >= b.num_seqs) return 0;
+    if (!w.load(s)) {
+      if (tell && blockIdx.x == 0) set_error(err, VLF_ERR_BAD_SEQLENS);
+      return 0;
+    }
+    return w.head_units() * b.h_kv;
+  };
+  auto block_sum = [&](long long x) {  // (six warps)
+    for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+    __syncthreads();
+    if (lane == 0) red[warp] = x;
+    __syncthreads();
+    x = 0;
+    for (int i = 0; i < 6; ++i) x += red[i];
+    return x;
+  };
+  long long total = 0, mine = 0;
+  for (int s0 = 0; s0 < b.num_seqs; s0 += 192) {
+    mine = units_of(s0 + threadIdx.x, true);
+    total += block_sum(mine);
+  }
+  // (CTAs with a run: two tiles each at least)
+  const long long grid = max(1ll, min((long long)gridDim.x, total / 2));
+  const bool run = total > 0 && blockIdx.x < grid;
+  const long long f0 = run ? total * blockIdx.x / grid : 0, f1 = run ? total * (blockIdx.x + 1) / grid : 0;
+  long long *const start = red + 6;  // {sequence, unit within it}
+  if (run) {
+    long long before = 0;
+    for (int s0 = 0; s0 < b.num_seqs; s0 += 192) {
+      const long long x = b.num_seqs <= 192 ? mine : units_of(s0 + threadIdx.x, false);
+      long long y = x;
+      for (int o = 1; o < 32; o *= 2) {
+        const long long z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+      }
+      __syncthreads();
+      if (lane == 31) red[warp] = y;
+      __syncthreads();
+      y += before;
+      for (int i = 0; i < 6; ++i) {
+        if (i < warp) y += red[i];
+        before += red[i];
+      }
+      if (x > 0 && y - x <= f0 && f0 < y) {
+        start[0] = s0 + threadIdx.x;
+        start[1] = f0 - (y - x);
+      }
+      if (before > f0) break;
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  if (!run) {
+    if (threadIdx.x == 0) p.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  } else if (warp == 4) {
+    // ------------------------------------------------------------------ pages
+    int off = w.seek((int)start[0], start[1]);
+    const int page = min(p.a.page, kKeys), npt = kKeys / page;  // slots and pages of a tile
+    const int log2_page = p.a.log2_page, none = p.a.num_pages * b.h_kv;
+    bool ok = true;
+    long long left = f1 - f0;
+    int nk = 0, nv = 0;
+    while (left > 0 && ok) {
+      const int n = (int)min((long long)(w.units() - off), left);
+      if (w.nt > 0) {
+        const int j0 = (w.t0 + off) * kKeys, first = j0 >> log2_page;  // the first page of the run's tiles
+        const int last = (min(w.hi, j0 + n * kKeys) - 1) >> log2_page;
+        const int32_t *row = p.a.table + (long long)w.s * p.a.max_pages;
+        // a lane has a page of the next 32, and one of the 32 behind them
+        auto id_of = [&](int i) {
+          if (i > last || i < w.lo >> log2_page) return -2;  // no key of the run's in it
+          return max(__ldg(row + i), -1);
+        };
+        auto real = [&](int id) { return id >= 0 && id < p.a.num_pages; };
+        int id = id_of(first + lane), id_next = id_of(first + 32 + lane);
+        auto scale_of = [&](int i) {
+          if (!real(i)) return make_float2(0.f, 0.f);
+          const long long at = (long long)i * b.h_kv + w.head;
+          return make_float2(__ldg(p.a.k_scale + at), __ldg(p.a.v_scale + at));
+        };
+        float2 sc = scale_of(id), sc_next = make_float2(0.f, 0.f);
+        for (int m = 0; m < n && ok; ++m) {
+          // page index of the tile's first page among the run's (a page of 256 has two tiles)
+          const int at = ((j0 + m * kKeys) >> log2_page) - first, in = at % 32;
+          if (in == 0 && m > 0 && ((j0 + m * kKeys) & (p.a.page - 1)) == 0) {
+            id = id_next;
+            sc = sc_next;
+            id_next = id_of(first + at + 32 + lane);
+          }
+          if (in == 16) sc_next = scale_of(id_next);  // (every run of 32 pages has a tile that begins there)
+          const int mine_id = __shfl_sync(0xffffffffu, id, in + lane % npt);
+          const bool have = lane < npt && mine_id != -2;
+          if (have && !real(mine_id)) set_error(err, VLF_ERR_BAD_PAGES);
+          const int z = real(mine_id) ? mine_id * b.h_kv + w.head : none;  // (outside: zeros)
+          const int bytes = __popc(__ballot_sync(0xffffffffu, have)) * page * D;
+          const int y = p.a.page > kKeys ? (j0 + m * kKeys) & (p.a.page - 1) : 0;
+          const int ks = nk % C::KST, vs = nv % C::VST;
+          if (nk >= C::KST) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_KE + ks), (nk / C::KST - 1) & 1, abort_flag, err));
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(bar(C::B_KF + ks), bytes);
+          __syncwarp();
+          if (have) tma_load_3d(sK + ks * C::T_BYTES + lane * page * D, &k_map, 0, y, z, bar(C::B_KF + ks));
+          const float2 mine_sc = make_float2(__shfl_sync(0xffffffffu, sc.x, in + lane % npt),
+                                             __shfl_sync(0xffffffffu, sc.y, in + lane % npt));
+          if (lane < npt) scales[nk % kScales * 8 + lane] = mine_sc;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::B_SC + nk % kScales));
+          ++nk;
+          if (nv >= C::VST) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_VE + vs), (nv / C::VST - 1) & 1, abort_flag, err));
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(bar(C::B_VF + vs), bytes);
+          __syncwarp();
+          if (have) tma_load_3d(sV + vs * C::T_BYTES + lane * page * D, &v_map, 0, y, z, bar(C::B_VF + vs));
+          ++nv;
+        }
+      }
+      left -= n;
+      off = 0;
+      if (left > 0) w.next();
+    }
+    // no copy may still be landing when the CTA leaves
+    if (lane == 0) {
+      for (int i = 0; i < C::KST && i < nk; ++i) drain_wait(bar(C::B_KF + i), ((nk - 1 - i) / C::KST) & 1);
+      for (int i = 0; i < C::VST && i < nv; ++i) drain_wait(bar(C::B_VF + i), ((nv - 1 - i) / C::VST) & 1);
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------------ products
+    int off = w.seek((int)start[0], start[1]);
+    const uint32_t id_s = idesc_f8(0, C::NS, 0), id_o = idesc_f8(1, C::NP, 1);
+    constexpr uint32_t SW = D == 128 ? 2 : 4;
+    // K and Q: rows of D bytes, eight to a swizzle atom.  V: 128 (64: twice the same 64) columns of a key in a
+    // row, eight keys to an atom.  P: 16 columns of a key in 16 bytes, 128 keys, then the next 16 columns.
+    const uint64_t dk0 = sdesc(sK, 16, 8 * D, SW), dq0 = sdesc(sQ, 16, 8 * D, SW), dv0 = sdesc(sV, 0, 8 * D, SW);
+    const uint64_t dp0 = sdesc(sP, 128, 16 * kKeys, 0);
+    bool ok = true;
+    int ns = 0, np = 0, seg = 0;  // tiles of S and of O issued, items begun
+    auto wait = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_wait(bar(i), parity & 1, abort_flag, err)); };
+    auto issue_s = [&]() {
+      const int ks = ns % C::KST, sb = ns & 1;
+      ok = wait(C::B_KF + ks, ns / C::KST);
+      if (ok && ns >= 2) ok = wait(C::B_SE + sb, ns / 2 - 1);
+      if (!ok) return;
+      fence_after();
+      const uint64_t dk = dk0 + (uint64_t)((ks * C::T_BYTES) >> 4);
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk)
+          mma_f8_w(tmem + C::NS * sb, dk + 2 * kk, dq0 + (uint64_t)((t * C::Q_TERM + 32 * kk) >> 4), id_s, t > 0 || kk > 0);
+      mma_commit_w(bar(C::B_SF + sb));
+      mma_commit_w(bar(C::B_KE + ks));
+      ++ns;
+    };
+    long long left = f1 - f0;
+    while (left > 0 && ok) {
+      const int n = (int)min((long long)(w.units() - off), left);
+      if (w.nt > 0) {
+        ok = wait(C::B_Q, seg);
+        if (ok) issue_s();
+        for (int m = 0; m < n && ok; ++m) {
+          if (m + 1 < n) issue_s();
+          if (!ok) break;
+          const int vs = np % C::VST, pb = np % C::PB;
+          ok = wait(C::B_VF + vs, np / C::VST) && wait(C::B_PF + pb, np / C::PB);
+          if (ok && m == 0 && seg > 0) ok = wait(C::B_OE, seg - 1);
+          if (!ok) break;
+          fence_after();
+          const uint64_t dv = dv0 + (uint64_t)((vs * C::T_BYTES) >> 4), dp = dp0 + (uint64_t)((pb * C::P_BYTES) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 32; ++kk)
+            mma_f8_w(tmem + C::O_COL, dv + (uint64_t)((kk * 32 * D) >> 4), dp + (uint64_t)((kk * 512) >> 4), id_o, m > 0 || kk > 0);
+          mma_commit_w(bar(C::B_VE + vs));
+          mma_commit_w(bar(C::B_PE + pb));
+          if (m + 1 == n) mma_commit_w(bar(C::B_OF));
+          ++np;
+        }
+        ++seg;
+      }
+      left -= n;
+      off = 0;
+      if (left > 0) w.next();
+    }
+    mma_commit_w(bar(C::B_DRAIN));
+    drain_wait(bar(C::B_DRAIN), 0);
+  } else if (warp < 4) {
+    // ------------------------------------------------------------------ softmax / output
+    const int tid = threadIdx.x;  // the key of a tile, or the column of V
+    const uint32_t t_addr = tmem + ((uint32_t)(32 * warp) << 16);
+    int off = w.seek((int)start[0], start[1]);
+    int seg = 0, ns = 0;  // items with tiles begun, tiles
+    bool bad = false;     // a wait gave up (all four warps leave together)
+    auto wait = [&](int i, int parity) {
+      if (!bad) bad = !__all_sync(0xffffffffu, mbar_wait(bar(i), parity & 1, abort_flag, err));
+    };
+    // The item's queries in terms, its columns' scales, references and limits.  A warp has every fourth column,
+    // its lanes D / 32 elements each.
+    auto prepare = [&](int par) {
+      named_sync(1, 128);
+      constexpr int E = D / 32, PER = C::NS / 4;
+      uint32_t raw[PER][E / 2];  // (all loads in flight at once)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        int row = 0, head = 0;
+        const int c = warp + 4 * i;
+        const bool have = c < NC && column_of(p, NC, w, c, row, head);
+        const T *q = static_cast<const T *>(b.q) + ((long long)(w.q0 + row) * b.h_q + head) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) raw[i][e] = have ? __ldg(reinterpret_cast<const uint32_t *>(q) + e) : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        int row = 0, head = 0;
+        const int c = warp + 4 * i;
+        const bool have = c < NC && column_of(p, NC, w, c, row, head);
+        float x[E];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 f = unpack2(raw[i][e / 2], BF16);
+          x[e] = f.x;
+          x[e + 1] = f.y;
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+        top = __reduce_max_sync(0xffffffffu, top);
+        const bool odd = top >= 0x7f800000u;  // a query that is not finite: every logit of the row is NaN
+        const int ex = min(max((int)(top >> 23) - 127, -100), 127);
+        const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23), down = __uint_as_float((uint32_t)(127 - 7 + ex) << 23);
+        uint32_t word[3];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = odd ? 0.f : x[e] * up;
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+          word[t] = 0;
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const uint32_t two = e4m3x2(x[e], x[e + 1]);
+            const float2 f = e4m3_pair(two);
+            x[e] -= f.x;
+            x[e + 1] -= f.y;
+            word[t] |= two << 8 * e;
+          }
+          // row c: D bytes, 16-byte chunks swizzled by the row
+          const int chunk = lane * E / 16, in = lane * E % 16;
+          const uint32_t to = sQ + t * C::Q_TERM + c * D + ((D == 128 ? chunk ^ (c & 7) : chunk ^ (c >> 1 & 3)) << 4) + in;
+          if constexpr (E == 4) asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(word[t]) : "memory");
+          else asm volatile("st.shared.b16 [%0], %1;" ::"r"(to), "h"((uint16_t)word[t]) : "memory");
+        }
+        if (lane == 0 && c < NC) {
+          const float nan = __uint_as_float(0x7fffffffu);
+          // (a column of nobody: P = 0)
+          col[par * NC + c] = make_float2(odd ? nan : down * b.scale_log2, have ? -kNoRef : kNoRef);
+          int a = 0, e = 0;
+          if (have) visible_range(row, w.len - w.q_len, w.len, b.causal, b.window, a, e);
+          lim[par * NC + c] = make_int2(a, e);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(C::B_Q));
+      named_sync(1, 128);
+    };
+    long long left = f1 - f0;
+    while (left > 0 && !bad) {
+      const int n = (int)min((long long)(w.units() - off), left), units = w.units();
+      const bool whole = off == 0 && n == units;
+      if (w.nt == 0) {
+        // rows that see no key
+        for (int c = 0; c < NC; ++c) {
+          int row, head;
+          if (!column_of(p, NC, w, c, row, head)) continue;
+          const long long at = (long long)(w.q0 + row) * b.h_q + head;
+          if (tid < D) static_cast<T *>(b.out)[at * D + tid] = from_f32<T>(0.f);
+          if (tid == 0 && b.lse) b.lse[(long long)head * b.total_q + w.q0 + row] = -INFINITY;
+        }
+      } else {
+        const int par = seg & 1;
+        prepare(par);
+        float l[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) l[c] = 0.f;
+        // keys that every column sees
+        int all_lo, all_hi, x;
+        visible_range(w.r1 - 1, w.len - w.q_len, w.len, b.causal, b.window, all_lo, x);
+        visible_range(w.r0, w.len - w.q_len, w.len, b.causal, b.window, x, all_hi);
+        for (int m = 0; m < n; ++m, ++ns) {
+          const int j0 = (w.t0 + off + m) * kKeys, j = j0 + tid;
+          const int sb = ns & 1, pb = ns % C::PB, sc = ns % kScales;
+          wait(C::B_SF + sb, ns / 2);
+          wait(C::B_SC + sc, ns / kScales);
+          uint32_t acc[NC];
+#pragma unroll
+          for (int c = 0; c < NC; ++c) acc[c] = 0;
+          if (!bad) {
+            fence_after();
+            __syncwarp();
+            tmem_ld_cols<NC>(t_addr + C::NS * sb, acc);
+            tmem_ld_wait();
+            pin(acc);
+            fence_before();
+            mbar_arrive(bar(C::B_SE + sb));
+          }
+          const float2 s2 = scales[sc * 8 + (tid >> min(p.a.log2_page, 7))];
+          const float vs = fminf(fmaxf(s2.y, 0x1p-100f), 0x1p120f);  // (a scale of zero or no number: of no weight)
+          const float lv = lg2(vs), over = 1.f / vs;
+          const bool in = j >= w.lo && j < w.hi;
+          const bool full = j0 >= all_lo && j0 + kKeys <= all_hi;
+          if (j0 < w.lo || j0 + kKeys > w.hi) {
+            // slots that hold no key of the item: zero times them would be NaN if they held one
+            wait(C::B_VF + ns % C::VST, ns / C::VST);
+            if (!in && !bad) {
+              const uint32_t to = sV + ns % C::VST * C::T_BYTES + tid * D;
+#pragma unroll
+              for (int i = 0; i < D; i += 16) sts_v4(to + i, 0, 0, 0, 0);
+            }
+          }
+          if (ns >= C::PB) wait(C::B_PE + pb, ns / C::PB - 1);
+          // y = log2 of P, with the references as they are; -inf where the key is not seen
+          float y[NC], most = -INFINITY;
+          auto logits = [&]() {
+            most = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < NC; c += 2) {
+              const float4 f = *reinterpret_cast<const float4 *>(col + par * NC + c);
+              y[c] = fmaf(__uint_as_float(acc[c]) * s2.x, f.x, lv + f.y);
+              y[c + 1] = fmaf(__uint_as_float(acc[c + 1]) * s2.x, f.z, lv + f.w);
+            }
+            if (!full) {
+#pragma unroll
+              for (int c = 0; c < NC; ++c) {
+                const int2 r = lim[par * NC + c];
+                if (j < r.x || j >= r.y) y[c] = -INFINITY;
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c) most = fmaxf(most, y[c]);
+          };
+          logits();
+          if (any_of_128(most > kTop || bad)) {
+            if (any_of_128(bad)) {
+              bad = true;
+              break;
+            }
+            // the columns' largest logits, and a new reference where one is passed
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              float t = y[c];
+#pragma unroll
+              for (int o = 16; o > 0; o /= 2) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+              if (lane == 0) wm[warp * NC + c] = t;
+            }
+            named_sync(1, 128);
+            if (tid < NC) {
+              const float t = fmaxf(fmaxf(wm[tid], wm[NC + tid]), fmaxf(wm[2 * NC + tid], wm[3 * NC + tid]));
+              // (t is less the reference, and tells nothing where there was none)
+              const float2 now = col[par * NC + tid];
+              float f = 1.f;
+              if (t > kTop) {
+                const bool none = now.y == -kNoRef;
+                col[par * NC + tid].y = none ? 0.f : now.y - (t - kSet);
+                f = none ? 0.f : ex2(kSet - t);
+              }
+              fac[tid] = f;
+            }
+            named_sync(1, 128);
+            bool first = false;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) first |= fac[c] == 0.f;
+            if (first) {
+              // columns that had no reference: their logits as they are, then the reference from them
+              logits();
+#pragma unroll
+              for (int c = 0; c < NC; ++c) {
+                float t = y[c];
+#pragma unroll
+                for (int o = 16; o > 0; o /= 2) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+                if (lane == 0) wm[warp * NC + c] = t;
+              }
+              named_sync(1, 128);
+              if (tid < NC && fac[tid] == 0.f) {
+                const float t = fmaxf(fmaxf(wm[tid], wm[NC + tid]), fmaxf(wm[2 * NC + tid], wm[3 * NC + tid]));
+                col[par * NC + tid].y += kSet - t;
+              }
+              named_sync(1, 128);
+            }
+            if (m > 0) {
+              // O is rescaled once the product before has completed
+              wait(C::B_PE + (ns - 1) % C::PB, (ns - 1) / C::PB);
+              if (any_of_128(bad)) {
+                bad = true;
+                break;
+              }
+              fence_after();
+#pragma unroll 1
+              for (int i = 0; i < C::NP; i += 16) {
+                uint32_t o[16];
+                __syncwarp();
+                tmem_ld16(t_addr + C::O_COL + i, o);
+                tmem_ld_wait();
+                pin(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (i + e < 3 * NC) o[e] = __float_as_uint(__uint_as_float(o[e]) * fac[(i + e) % NC]);
+                tmem_st16(t_addr + C::O_COL + i, o);
+              }
+              tmem_st_wait();
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c) l[c] *= fac[c];
+            logits();
+          }
+          // P in three terms: each the rest's nearest with the high byte of an fp16 alone
+          uint32_t w4[C::NP / 4];
+#pragma unroll
+          for (int i = 3 * NC / 4; i < C::NP / 4; ++i) w4[i] = 0;
+#pragma unroll
+          for (int c = 0; c < NC; c += 4) {
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              e[i] = ex2(y[c + i]);
+              l[c + i] = fmaf(e[i], over, l[c + i]);
+            }
+            __half2 a = __floats2half2_rn(e[0], e[1]), d = __floats2half2_rn(e[2], e[3]);
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+              const uint32_t ra = *reinterpret_cast<uint32_t *>(&a) + 0x00800080u, rd = *reinterpret_cast<uint32_t *>(&d) + 0x00800080u;
+              w4[t * NC / 4 + c / 4] = __byte_perm(ra, rd, 0x7531);
+              if (t < 2) {
+                const uint32_t ka = ra & 0xff00ff00u, kd = rd & 0xff00ff00u;
+                a = __hsub2(a, *reinterpret_cast<const __half2 *>(&ka));
+                d = __hsub2(d, *reinterpret_cast<const __half2 *>(&kd));
+              }
+            }
+          }
+          const uint32_t to = sP + pb * C::P_BYTES + tid * 16;
+#pragma unroll
+          for (int i = 0; i < C::NP / 16; ++i) sts_v4(to + i * 16 * kKeys, w4[4 * i], w4[4 * i + 1], w4[4 * i + 2], w4[4 * i + 3]);
+          fence_proxy_async_smem();
+          fence_before();  // (a rescaled O)
+          mbar_arrive(bar(C::B_PF + pb));
+        }
+        if (bad) break;
+        // sums over the keys
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+#pragma unroll
+          for (int o = 16; o > 0; o /= 2) l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
+          if (lane == 0) wm[warp * NC + c] = l[c];
+        }
+        wait(C::B_OF, seg);
+        if (any_of_128(bad)) {
+          bad = true;
+          break;
+        }
+        fence_after();
+        float o[NC];
+        {
+          uint32_t r[C::NP];
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < C::NP; i += 16) tmem_ld<16>(t_addr + C::O_COL + i, r + i);
+          tmem_ld_wait();
+          pin(r);
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            o[c] = __uint_as_float(r[c]) + (__uint_as_float(r[NC + c]) + __uint_as_float(r[2 * NC + c]));
+        }
+        fence_before();
+        mbar_arrive(bar(C::B_OE));
+        float *part = p.part + (2ll * blockIdx.x + (off == 0 ? 1 : 0)) * C::PART;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          int row, head;
+          if (!column_of(p, NC, w, c, row, head)) continue;
+          const float sum = wm[c] + wm[NC + c] + wm[2 * NC + c] + wm[3 * NC + c], ref = -col[par * NC + c].y;
+          if (whole) {
+            const long long at = (long long)(w.q0 + row) * b.h_q + head;
+            if (tid < D) static_cast<T *>(b.out)[at * D + tid] = from_f32<T>(sum == 0.f ? 0.f : o[c] / sum);
+            if (tid == 0 && b.lse)
+              b.lse[(long long)head * b.total_q + w.q0 + row] = sum == 0.f ? -INFINITY : (ref + lg2(sum)) * kLn2;
+          } else {
+            if (tid < D) part[c * D + tid] = o[c];
+            if (tid == 0) {
+              part[NC * D + c] = ref;
+              part[NC * D + NC + c] = sum;
+            }
+          }
+        }
+        ++seg;
+      }
+      left -= n;
+      if (left == 0 && tid == 0) {
+        // an item that this CTA begins and others end
+        const bool open = w.nt > 0 && off == 0 && n < units;
+        const long long end = f1 + units - n;
+        p.rec[blockIdx.x] = open ? make_int4(w.s, w.head, w.qt, (int)((end * grid - 1) / total)) : make_int4(-1, 0, 0, 0);
+      }
+      off = 0;
+      if (left > 0) w.next();
+    }
+    if (bad && tid == 0) p.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    fence_after();
+    tmem_dealloc(tmem, C::TMEM);
+  }
+}
+
+// Joins the parts of the item that CTA blockIdx.x of the launch before began and others ended: out = sum_i f_i O_i /
+// sum_i f_i l_i with f_i = 2^(reference_i - the largest).  Grid y: four columns of the item.
+template <int D, int NC, bool BF16>
+__global__ void __launch_bounds__(D) pages_join_kernel(const TcParams p) {
+  using C = Cfg<D, NC>;
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  pdl_wait();
+  const int4 rec = p.rec[blockIdx.x];
+  if (rec.x < 0) return;
+  Walk w(p);
+  w.load(rec.x);
+  w.head = rec.y;
+  w.qt = rec.z;
+  w.item();
+  const int n = rec.w - blockIdx.x + 1;
+  auto part = [&](int i) { return p.part + (2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * C::PART; };
+#pragma unroll 1
+  for (int c = 4 * blockIdx.y; c < min(NC, 4 * (int)blockIdx.y + 4); ++c) {
+    int row, head;
+    if (!column_of(p, NC, w, c, row, head)) continue;
+    float top = kNoRef;
+    for (int i = 0; i < n; ++i) {
+      const float *x = part(i) + NC * D + c;
+      if (x[NC] != 0.f) top = fmaxf(top, x[0]);
+    }
+    float o = 0.f, sum = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float *x = part(i) + NC * D + c;
+      const float l = x[NC], f = l == 0.f ? 0.f : ex2(x[0] - top);
+      if (l == 0.f) continue;
+      sum = fmaf(f, l, sum);
+      o = fmaf(f, part(i)[c * D + threadIdx.x], o);
+    }
+    const long long at = (long long)(w.q0 + row) * p.a.p.h_q + head;
+    static_cast<T *>(p.a.p.out)[at * D + threadIdx.x] = from_f32<T>(sum == 0.f ? 0.f : o / sum);
+    if (threadIdx.x == 0 && p.a.p.lse)
+      p.a.p.lse[(long long)head * p.a.p.total_q + w.q0 + row] = sum == 0.f ? -INFINITY : (top + lg2(sum)) * kLn2;
+  }
+}
+
+// Columns of a tile: the fewest that hold a sequence's rows of a kv head's group, 32 at most.
+int columns(int max_q, int group) {
+  const long long n = (long long)max_q * group;
+  return n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : 32;
+}
+template <typename F> void with(int d, int nc, F f) {
+  auto at = [&](auto dd) {
+    if (nc == 4) f(dd, std::integral_constant<int, 4>{});
+    else if (nc == 8) f(dd, std::integral_constant<int, 8>{});
+    else if (nc == 16) f(dd, std::integral_constant<int, 16>{});
+    else f(dd, std::integral_constant<int, 32>{});
+  };
+  if (d == 64) at(std::integral_constant<int, 64>{});
+  else at(std::integral_constant<int, 128>{});
+}
+
+}  // namespace
+
+bool pages_tc_supported(int d_qk, int d_v, int dtype, unsigned flags) {
+  return (dtype == VLF_F16 || dtype == VLF_BF16) && !(flags & VLF_FLAG_FORCE_SIMT) && d_qk == d_v && (d_qk == 64 || d_qk == 128);
+}
+
+size_t pages_tc_workspace(int max_q, int group, int d, int num_sms) {
+  if (num_sms < 1) return 0;
+  size_t n = 0;
+  with(d, columns(max_q, group), [&](auto dd, auto nc) {
+    using C = Cfg<decltype(dd)::value, decltype(nc)::value>;
+    const size_t grid = (size_t)C::CTAS * num_sms;
+    n = ((grid * sizeof(int4) + 255) & ~(size_t)255) + 2 * grid * C::PART * sizeof(float);
+  });
+  return n;
+}
+
+cudaError_t pages_tc_forward(const PagesAttnParams &a, void *workspace, int num_sms, cudaStream_t st) {
+  cudaError_t e = cudaErrorInvalidValue;
+  const int group = a.p.group, nc = columns(a.p.max_q, group);
+  CUtensorMap k_map, v_map;
+  const uint64_t heads = (uint64_t)a.num_pages * a.p.h_kv;
+  if (!make_tmap_pages(&k_map, a.k_pages, heads, a.page, a.p.d_qk) || !make_tmap_pages(&v_map, a.v_pages, heads, a.page, a.p.d_v))
+    return e;
+  with(a.p.d_qk, nc, [&](auto dd, auto cc) {
+    constexpr int D = decltype(dd)::value, NC = decltype(cc)::value;
+    using C = Cfg<D, NC>;
+    TcParams p{};
+    p.a = a;
+    p.splits = group > NC ? (group + NC - 1) / NC : 1;
+    p.rows = group > NC ? 1 : NC / group;
+    const size_t grid = (size_t)C::CTAS * num_sms;
+    p.rec = static_cast<int4 *>(workspace);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + ((grid * sizeof(int4) + 255) & ~(size_t)255));
+    const bool bf = a.p.dtype == VLF_BF16;
+    const void *kern = bf ? (const void *)pages_tc_kernel<D, NC, true> : (const void *)pages_tc_kernel<D, NC, false>;
+    const void *join = bf ? (const void *)pages_join_kernel<D, NC, true> : (const void *)pages_join_kernel<D, NC, false>;
+    if ((e = set_smem_once(kern, C::SMEM)) != cudaSuccess) return;
+    void *args[3] = {&k_map, &v_map, &p};
+    e = launch_plain(kern, dim3((unsigned)grid), 192, C::SMEM, st, args);
+    void *jargs[1] = {&p};
+    if (e == cudaSuccess) e = launch_dependent(join, dim3((unsigned)grid, (NC + 3) / 4), D, 0, st, jargs);
+    if (e == cudaSuccess) count_launch();
+  });
+  return e;
+}
+
+}  // namespace vlf
