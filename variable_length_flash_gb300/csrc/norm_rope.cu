@@ -10,6 +10,13 @@
 // cosines and weights are made once for them; a head's sums go over its G lanes by shuffles.  A lane's
 // columns are the same for every row, so dw is summed in registers over all its rows, then over
 // the block's tokens, and a second launch adds the blocks' parts: every sum in a fixed order.
+//
+// Measured: 20011 tokens of 40 heads of 128 in bf16, sliced from a fused projection, 78 us (78% of the copy
+// rate; the weights times sine and cosine are made once for a token, which took it from 92); the gradients of
+// 16384 tokens of 32 heads of 96 in fp16, 64 columns of which turn in pairs of neighbours, 87 us (51%): it
+// issues 30 instructions for an element, a quarter of them for lanes that have no columns (12 chunks of a row
+// over 8 lanes), and the sums, weights and turns that a lane keeps leave one block an SM its registers (two
+// with half the heads in flight: 105 us).  64 tokens 4.2 us, which is a launch.
 #include "kernels.h"
 #include "rope.cuh"
 
@@ -18,7 +25,7 @@ namespace {
 
 using namespace turning;
 
-constexpr int kMostBlocks = 152 * 8;  // of the backward: the parts of dw that the workspace has room for
+constexpr int kMostBlocks = 152 * 2;  // of the backward: the parts of dw that the workspace has room for
 
 __device__ __forceinline__ float weight_at(const void *w, int dtype, int c) {
   if (!w) return 1.f;
@@ -30,27 +37,29 @@ __device__ __forceinline__ float weight_at(const void *w, int dtype, int c) {
 // Grid y: a run of hpt heads of q or k; x: runs of 256 / G tokens, walked with the grid's stride.  Lane
 // u of a token's G has its units u, u + G, ... (NU of them; one where they hold 16 bytes).  HEADS:
 // heads whose loads are in flight.
-template <typename T, int V, bool INTER, int NU, int HEADS, bool BWD>
-__global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeParams p) {
+template <typename T, int V, bool INTER, int NU, int HEADS, bool BWD, bool ODD>
+__global__ void __launch_bounds__(256, BWD || V == 1 ? 1 : 2) norm_rope_kernel(const NormRopeParams p) {
   __shared__ unsigned long long F[128];
   __shared__ float red[BWD ? 512 * V : 1][BWD && NU > 1 ? NU : 1];
   const int half = p.rot / 2, nrot = half / V;
+  __shared__ float w[256 + 8];  // (a unit's columns may pass the end, as its weights may)
+  const int phases_q = (p.h_q + p.hpt - 1) / p.hpt, ph = blockIdx.y;
+  const bool is_k = ph >= phases_q;
+  const Rows &rows = is_k ? p.k : p.q;
   for (int c = threadIdx.x; c < half; c += 256) F[c] = turns_of(__ldg(p.inv_freq + c));
+  for (int c = threadIdx.x; c < 256 + 8; c += 256) w[c] = c < p.d ? weight_at(rows.w, p.w_dtype, c) : 0.f;
   __syncthreads();
   const int ntail = ((p.d - p.rot + V - 1) / V + 1) / 2, units = nrot + ntail;
   const int G = p.lanes, run = 256 / G, u = threadIdx.x % G, g = threadIdx.x / G;
   const uint32_t mask = (G == 32 ? 0xffffffffu : (1u << G) - 1) << (threadIdx.x % 32 & ~(G - 1));
-  const int phases_q = (p.h_q + p.hpt - 1) / p.hpt, ph = blockIdx.y;
-  const bool is_k = ph >= phases_q;
   const int h0 = (is_k ? ph - phases_q : ph) * p.hpt, h1 = min(h0 + p.hpt, is_k ? p.h_k : p.h_q);
-  const Rows &rows = is_k ? p.k : p.q;
   const float over_d = 1.f / (float)p.d;
   using C = Chunk<T, V>;
 
   // what this lane has of a row: per unit its columns, its weights
   bool have[NU], two[NU], rot[NU];
-  int ca[NU], cb[NU], pair[NU][V], axis[NU][V];
-  float wa[NU][V], wb[NU][V], sa[NU][V], sb[NU][V];
+  int ca[NU], cb[NU];
+  float wa[BWD ? NU : 1][V], wb[BWD ? NU : 1][V], sa[BWD ? NU : 1][V], sb[BWD ? NU : 1][V];
 #pragma unroll
   for (int n = 0; n < NU; ++n) {
     const int un = u + n * G;
@@ -60,36 +69,47 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeParams p) 
     rot[n] = have[n] && at.rot;
     ca[n] = at.ca;
     cb[n] = at.cb;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      pair[n][e] = at.pair[e];
-      axis[n][e] = at.axis[e];
-      wa[n][e] = have[n] ? weight_at(rows.w, p.w_dtype, ca[n] + e) : 0.f;
-      wb[n][e] = two[n] ? weight_at(rows.w, p.w_dtype, cb[n] + e) : 0.f;
-      sa[n][e] = sb[n][e] = 0.f;
-    }
-  }
-  auto sum = [&](float x) {
-    for (int o = G / 2; o > 0; o /= 2) x += __shfl_xor_sync(mask, x, o);
-    return x;
-  };
-  for (long long tok = (long long)blockIdx.x * run + g; tok < p.total; tok += (long long)gridDim.x * run) {
-    float cs[NU][V], sn[NU][V];
-#pragma unroll
-    for (int n = 0; n < NU; ++n)
+    if constexpr (BWD) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        cs[n][e] = 1.f;
-        sn[n][e] = 0.f;
-        if (!rot[n]) continue;
-        turn(__ldg(p.positions + (long long)axis[n][e] * p.total + tok), F[pair[n][e]], cs[n][e], sn[n][e]);
-        if (BWD) sn[n][e] = -sn[n][e];
+        wa[n][e] = have[n] ? w[ca[n] + e] : 0.f;
+        wb[n][e] = two[n] ? w[cb[n] + e] : 0.f;
+        sa[n][e] = sb[n][e] = 0.f;
       }
+    }
+  }
+  // HEADS heads of a token at a time
+  C x[HEADS][NU], y[HEADS][NU], dx[BWD ? HEADS : 1][NU], dy[BWD ? HEADS : 1][NU];
+  const long long step = (long long)gridDim.x * run;
+  for (long long tok = (long long)blockIdx.x * run + g; tok < p.total; tok += step) {
+    // The weights and the rotation of a pair (l, h) in one: forward y_l = x_l A - x_h B, y_h = x_h C + x_l D with
+    // A = w_l cos, B = w_h sin, C = w_h cos, D = w_l sin; backward with g = R(-t) dy alone: A = C = cos, B = D = -sin.
+    float A[NU][V], B[NU][V], Cc[NU][V], Dd[NU][V];
+#pragma unroll
+    for (int n = 0; n < NU; ++n) {
+      const Unit<V, INTER> at(have[n] ? u + n * G : 0, nrot, ntail, half, p.d, p.first);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        float cs = 1.f, sn = 0.f;
+        if (rot[n]) turn(__ldg(p.positions + (long long)at.axis[e] * p.total + tok), F[at.pair[e]], cs, sn);
+        if (BWD) sn = -sn;
+        A[n][e] = cs;
+        B[n][e] = sn;
+        if constexpr (!BWD) {
+          int l, hi;
+          at.columns(e, l, hi);
+          const float wl = w[l], wh = w[hi];
+          A[n][e] = wl * cs;
+          B[n][e] = wh * sn;
+          Cc[n][e] = wh * cs;
+          Dd[n][e] = wl * sn;
+        }
+      }
+    }
+    T *out0 = static_cast<T *>(rows.out) + tok * rows.out_stride + (long long)h0 * p.d;
     const T *x0 = static_cast<const T *>(rows.x) + tok * rows.x_stride + (long long)h0 * p.d;
     const T *dy0 = BWD ? static_cast<const T *>(rows.dy) + tok * rows.dy_stride + (long long)h0 * p.d : nullptr;
-    T *out0 = static_cast<T *>(rows.out) + tok * rows.out_stride + (long long)h0 * p.d;
     for (int h = h0; h < h1; h += HEADS, x0 += HEADS * p.d, dy0 += BWD ? HEADS * p.d : 0, out0 += HEADS * p.d) {
-      C x[HEADS][NU], y[HEADS][NU], dx[BWD ? HEADS : 1][NU], dy[BWD ? HEADS : 1][NU];
 #pragma unroll
       for (int i = 0; i < HEADS; ++i) {
         if (h + i >= h1) continue;
@@ -104,56 +124,80 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeParams p) 
           }
         }
       }
+      // a head's values in fp32 (what a lane does not have is zero), and its gradients turned back
+      auto values = [&](int i, int n, float (&a)[V], float (&b)[V]) {
+        x[i][n].get(a);
+        y[i][n].get(b);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (ODD && !two[n]) b[e] = 0.f;
+      };
+      auto turned = [&](int i, int n, float (&ga)[V], float (&gb)[V]) {
+        float da[V], db[V];
+        dx[i][n].get(da);
+        dy[i][n].get(db);
+        rotate<V, INTER>(da, db, A[n], B[n], ga, gb);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (ODD && !two[n]) gb[e] = 0.f;
+      };
+      // the sums of all heads in flight go over the lanes together: one after the other they wait for
+      // a shuffle at each step (20011 tokens of 40 heads: 109 us where this took 92)
+      float ss[HEADS], xs[HEADS], ga[BWD ? HEADS : 1][NU][V], gb[BWD ? HEADS : 1][NU][V];
 #pragma unroll
       for (int i = 0; i < HEADS; ++i) {
+        ss[i] = xs[i] = 0.f;
         if (h + i >= h1) continue;
-        float a[NU][V], b[NU][V], ga[NU][V], gb[NU][V], ss = 0.f, xs = 0.f;
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
           if (!have[n]) continue;
-          x[i][n].get(a[n]);
-          y[i][n].get(b[n]);
+          float a[V], b[V];
+          values(i, n, a, b);
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            if (!two[n]) b[n][e] = 0.f;
-            ss = fmaf(a[n][e], a[n][e], ss);
-            ss = fmaf(b[n][e], b[n][e], ss);
-          }
+          for (int e = 0; e < V; ++e) ss[i] = fmaf(a[e], a[e], fmaf(b[e], b[e], ss[i]));
           if constexpr (BWD) {
-            float da[V], db[V];
-            dx[i][n].get(da);
-            dy[i][n].get(db);
-            rotate<V, INTER>(da, db, cs[n], sn[n], ga[n], gb[n]);
+            turned(i, n, ga[i][n], gb[i][n]);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-              if (!two[n]) gb[n][e] = 0.f;
-              xs = fmaf(ga[n][e] * wa[n][e], a[n][e], xs);
-              xs = fmaf(gb[n][e] * wb[n][e], b[n][e], xs);
+              xs[i] = fmaf(ga[i][n][e] * wa[n][e], a[e], xs[i]);
+              xs[i] = fmaf(gb[i][n][e] * wb[n][e], b[e], xs[i]);
             }
           }
         }
-        const float r = rsqrtf(fmaf(sum(ss), over_d, p.eps));
-        const float pull = BWD ? sum(xs) * over_d * r * r : 0.f;
+      }
+      for (int o = G / 2; o > 0; o /= 2) {
+#pragma unroll
+        for (int i = 0; i < HEADS; ++i) {
+          ss[i] += __shfl_xor_sync(mask, ss[i], o);
+          if (BWD) xs[i] += __shfl_xor_sync(mask, xs[i], o);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < HEADS; ++i) {
+        if (h + i >= h1) continue;
+        const float r = rsqrtf(fmaf(ss[i], over_d, p.eps));
+        const float pull = BWD ? xs[i] * over_d * r * r * r : 0.f;
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
           if (!have[n]) continue;
-          float oa[V], ob[V];
+          float a[V], b[V], oa[V], ob[V];
+          values(i, n, a, b);
           if constexpr (BWD) {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-              const float ua = a[n][e] * r, ub = b[n][e] * r;
-              sa[n][e] = fmaf(ga[n][e], ua, sa[n][e]);
-              sb[n][e] = fmaf(gb[n][e], ub, sb[n][e]);
-              oa[e] = r * fmaf(-a[n][e], pull, ga[n][e] * wa[n][e]);
-              ob[e] = r * fmaf(-b[n][e], pull, gb[n][e] * wb[n][e]);
+              const float va = ga[i][n][e] * r, vb = gb[i][n][e] * r;
+              sa[n][e] = fmaf(va, a[e], sa[n][e]);
+              sb[n][e] = fmaf(vb, b[e], sb[n][e]);
+              oa[e] = fmaf(-a[e], pull, va * wa[n][e]);
+              ob[e] = fmaf(-b[e], pull, vb * wb[n][e]);
             }
           } else {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-              a[n][e] *= r * wa[n][e];
-              b[n][e] *= r * wb[n][e];
+              a[e] *= r;
+              b[e] *= r;
             }
-            rotate<V, INTER>(a[n], b[n], cs[n], sn[n], oa, ob);
+            rotate<V, INTER>(a, b, A[n], B[n], Cc[n], Dd[n], oa, ob);
           }
           C ra, rb;
           ra.set(oa);
@@ -223,21 +267,24 @@ cudaError_t launch(NormRopeParams p, cudaStream_t st) {
   auto phases = [&](int hpt) { return (long long)(p.h_q + hpt - 1) / hpt + (p.h_k + hpt - 1) / hpt; };
   // heads per lane: as in rope.cu, 16 where that gives every SM a block, fewer for few tokens
   p.hpt = 16;
+  // (q's runs and k's the same size where that is to be had: blocks then end together)
+  if (p.h_q % 8 == 0 && p.h_k % 8 == 0 && (p.h_q % 16 || p.h_k % 16)) p.hpt = 8;
   while (p.hpt > 1 && runs * phases(p.hpt) < 152) p.hpt /= 2;
   while (phases(p.hpt) > 256) p.hpt *= 2;
-  const long long y = phases(p.hpt), most = BWD ? 152 * 3 : kMostBlocks;
+  const long long y = phases(p.hpt), most = BWD ? 152 : 152 * 2;  // (as many as are resident: they end together)
   long long turns = (runs * y + most - 1) / most;
   long long x = turns ? (runs + turns - 1) / turns : 0;
   if (BWD && x * y > kMostBlocks) x = kMostBlocks / y;
   if (x > 0) {
-    const bool many = p.hpt >= 8;
+    const bool many = p.hpt >= 8, odd = (p.d - p.rot) / v % 2 != 0;
     auto pick = [&](auto v_, auto inter_) {
       constexpr int V = decltype(v_)::value;
       constexpr bool INTER = decltype(inter_)::value;
       constexpr int NU = V == 1 ? 4 : 1;
       constexpr int MANY = V == 1 ? 1 : BWD ? 4 : 8, FEW = V == 1 ? 1 : 2;
-      return many ? (const void *)norm_rope_kernel<T, V, INTER, NU, MANY, BWD>
-                  : (const void *)norm_rope_kernel<T, V, INTER, NU, FEW, BWD>;
+      if (odd || V == 1) return (const void *)norm_rope_kernel<T, V, INTER, NU, V == 1 ? 1 : 2, BWD, true>;
+      return many ? (const void *)norm_rope_kernel<T, V, INTER, NU, MANY, BWD, V == 1>
+                  : (const void *)norm_rope_kernel<T, V, INTER, NU, FEW, BWD, V == 1>;
     };
     using W = std::integral_constant<int, VW>;
     using One = std::integral_constant<int, 1>;

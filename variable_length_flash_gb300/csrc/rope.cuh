@@ -96,7 +96,35 @@ template <int V, bool INTER> struct Unit {
       axis[e] = a;
     }
   }
+  // The two columns of pair e of the unit.
+  __device__ __forceinline__ void columns(int e, int &l, int &h) const {
+    if constexpr (INTER && V > 1) {
+      l = (e < V / 2 ? ca : cb) + 2 * (e % (V / 2));
+      h = l + 1;
+    } else {
+      l = ca + e;
+      h = cb + e;
+    }
+  }
 };
+// The two chunks' values turned, each pair by factors of its own: y_l = x_l A - x_h B, y_h = x_h C + x_l D.
+template <int V, bool INTER>
+__device__ __forceinline__ void rotate(const float (&a)[V], const float (&b)[V], const float (&A)[V], const float (&B)[V],
+                                       const float (&C)[V], const float (&D)[V], float (&ya)[V], float (&yb)[V]) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    if constexpr (INTER && V > 1) {
+      float *o = e < V / 2 ? ya : yb;
+      const float *i = e < V / 2 ? a : b;
+      const int c = 2 * (e % (V / 2));
+      o[c] = fmaf(i[c], A[e], -(i[c + 1] * B[e]));
+      o[c + 1] = fmaf(i[c + 1], C[e], i[c] * D[e]);
+    } else {
+      ya[e] = fmaf(a[e], A[e], -(b[e] * B[e]));
+      yb[e] = fmaf(b[e], C[e], a[e] * D[e]);
+    }
+  }
+}
 // The two chunks' values turned.
 template <int V, bool INTER>
 __device__ __forceinline__ void rotate(const float (&a)[V], const float (&b)[V], const float (&cs)[V],
