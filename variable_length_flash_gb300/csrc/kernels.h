@@ -170,6 +170,9 @@ cudaError_t pages_forward(const PagesAttnParams &a, void *workspace, int num_sms
 bool pages_tc_supported(int d_qk, int d_v, int dtype, unsigned flags);
 size_t pages_tc_workspace(int max_q, int group, int d, int num_sms);
 cudaError_t pages_tc_forward(const PagesAttnParams &a, void *workspace, int num_sms, cudaStream_t st);
+// The ones for many rows (pages_rows.cu).
+size_t pages_rows_workspace(int d, int num_sms);
+cudaError_t pages_rows_forward(const PagesAttnParams &a, void *workspace, int num_sms, cudaStream_t st);
 
 // Host-side count of successful kernel launches (api.cu).
 void count_launch(int n = 1);

@@ -114,12 +114,16 @@ __global__ void __launch_bounds__(32 * kFmaWarps) pages_fma_kernel(const PagesAt
         sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
 }
 
+// Whether a sequence's rows of a kv head's group are enough for the kernel that has them as rows of its products.
+bool many_rows(int max_q, int group) { return (long long)max_q * group > 32; }
+
 }  // namespace
 
 size_t pages_attn_workspace(int num_seqs, int max_q, int h_q, int h_kv, int d_qk, int d_v, int dtype, unsigned flags,
                             int num_sms) {
   if (num_seqs < 1 || !pages_tc_supported(d_qk, d_v, dtype, flags)) return 0;
-  return pages_tc_workspace(max_q, h_q / h_kv, d_qk, num_sms);
+  if (num_sms < 1) return 0;
+  return many_rows(max_q, h_q / h_kv) ? pages_rows_workspace(d_qk, num_sms) : pages_tc_workspace(max_q, h_q / h_kv, d_qk, num_sms);
 }
 
 cudaError_t pages_forward(const PagesAttnParams &a, void *workspace, int num_sms, cudaStream_t st) {
@@ -127,7 +131,7 @@ cudaError_t pages_forward(const PagesAttnParams &a, void *workspace, int num_sms
   // (a tensor map needs a page, and its coordinates are ints)
   const long long heads = (long long)a.num_pages * p.h_kv;
   if (pages_tc_supported(p.d_qk, p.d_v, p.dtype, p.flags) && heads > 0 && heads < 0x7fffffff)
-    return pages_tc_forward(a, workspace, num_sms, st);
+    return many_rows(p.max_q, p.group) ? pages_rows_forward(a, workspace, num_sms, st) : pages_tc_forward(a, workspace, num_sms, st);
   const dim3 grid((unsigned)p.max_q, (unsigned)p.h_q, (unsigned)p.num_seqs);
   PagesAttnParams copy = a;
   void *args[1] = {&copy};

@@ -31,31 +31,19 @@
 //
 // Roles of a CTA: warps 0-3 softmax (thread = key) and the output (thread = column of V), warp 4 page loads,
 // warp 5 both products.
-#include <type_traits>
-
 #include "e4m3.cuh"
-#include "kernels.h"
-#include "tc_common.cuh"
+#include "pages_tc.cuh"
 
 namespace vlf {
 namespace {
 
-using namespace tc;
+using namespace pages;
 
 constexpr int kKeys = 128;         // keys of a tile
 constexpr float kNoRef = -1e30f;   // reference of a column that has met no key
 constexpr float kTop = 15.f;       // log2 of the largest P
 constexpr float kSet = 7.f;        // log2 of the largest P when the reference is set
 constexpr int kScales = 8;         // tiles whose scales are held (more than the rings let loads run ahead)
-constexpr float kLn2 = 0.69314718055994531f;
-
-struct TcParams {
-  PagesAttnParams a;
-  float *part;  // [2 grid][NC (D + 2)]
-  int4 *rec;    // [grid] {sequence, kv head, query tile, last CTA} of the item that a CTA begins and leaves open; -1: none
-  int rows;     // query rows of a query tile
-  int splits;   // query tiles of a row (a group with more heads than columns), else 1
-};
 
 // NC: columns of a tile.
 template <int D, int NC> struct Cfg {
@@ -135,90 +123,6 @@ template <int NC> __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, u
   }
 }
 
-// The key tiles of the items from one on, in order.
-struct Walk {
-  const TcParams &p;
-  int s, head, qt;                // sequence, kv head, query tile
-  int q0, q_len, len, tiles_q;    // of the sequence; tiles_q = 0: nothing to do
-  int r0, r1, lo, hi, t0, nt;     // of the item: its rows, the keys they see, its key tiles (none: nt = 0)
-
-  __device__ __forceinline__ explicit Walk(const TcParams &x) : p(x) {}
-  __device__ __forceinline__ bool load(int seq) {  // false: bad lengths
-    s = seq;
-    const Params &b = p.a.p;
-    const int x = __ldg(b.cu_q + s), y = __ldg(b.cu_q + s + 1);
-    len = __ldg(p.a.kv_lens + s);
-    q0 = x;
-    q_len = y - x;
-    tiles_q = 0;
-    if (x < 0 || x > y || y > b.total_q || q_len > b.max_q || len < 0 ||
-        (len > 0 && (len - 1) >> p.a.log2_page >= p.a.max_pages))
-      return false;
-    tiles_q = p.splits > 1 ? q_len * p.splits : (q_len + p.rows - 1) / p.rows;
-    return true;
-  }
-  __device__ __forceinline__ void item() {
-    r0 = p.splits > 1 ? qt / p.splits : qt * p.rows;
-    r1 = min(r0 + p.rows, q_len);
-    kv_band(r0, r1, q_len, len, p.a.p.causal, p.a.p.window, lo, hi);
-    t0 = lo / kKeys;
-    nt = hi > lo ? (hi + kKeys - 1) / kKeys - t0 : 0;
-  }
-  __device__ __forceinline__ int units() const { return max(nt, 1); }
-  // units of one head of the sequence
-  __device__ __forceinline__ long long head_units() {
-    long long n = 0;
-    for (qt = 0; qt < tiles_q; ++qt) {
-      item();
-      n += units();
-    }
-    return n;
-  }
-  // to unit `at` of sequence seq; returns the unit within the item
-  __device__ __forceinline__ int seek(int seq, long long at) {
-    load(seq);
-    const long long per = head_units();
-    head = (int)(at / per);
-    at -= head * per;
-    for (qt = 0;; ++qt) {
-      item();
-      if (at < units()) return (int)at;
-      at -= units();
-    }
-  }
-  __device__ __forceinline__ void next() {
-    if (++qt >= tiles_q) {
-      qt = 0;
-      if (++head >= p.a.p.h_kv) {
-        head = 0;
-        do {  // (there is another one: the caller has units left)
-          if (s + 1 >= p.a.p.num_seqs) return;
-          load(s + 1);
-        } while (tiles_q == 0);
-      }
-    }
-    item();
-  }
-};
-// Values that a wait has made good: what uses them is not scheduled ahead of it.
-template <int N> __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
-// The query row and head of column c; false where there is none.
-__device__ __forceinline__ bool column_of(const TcParams &p, int nc, const Walk &w, int c, int &row, int &head) {
-  const int group = p.a.p.group;
-  if (p.splits > 1) {
-    const int h = w.qt % p.splits * nc + c;
-    row = w.r0;
-    head = w.head * group + h;
-    return h < group;
-  }
-  row = w.r0 + c / group;
-  head = w.head * group + c % group;
-  return row < w.r1;
-}
-
 template <int D, int NC, bool BF16>
 __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
     pages_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
@@ -266,73 +170,22 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
   }
   pdl_wait();
 
-  // Units of all sequences, then this CTA's run of them and where it begins: the threads take a sequence each.
-  Walk w(p);
-  auto units_of = [&](int s, bool tell) -> long long {
-    if (s >= b.num_seqs) return 0;
-    if (!w.load(s)) {
-      if (tell && blockIdx.x == 0) set_error(err, VLF_ERR_BAD_SEQLENS);
-      return 0;
-    }
-    return w.head_units() * b.h_kv;
-  };
-  auto block_sum = [&](long long x) {  // (six warps)
-    for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
-    __syncthreads();
-    if (lane == 0) red[warp] = x;
-    __syncthreads();
-    x = 0;
-    for (int i = 0; i < 6; ++i) x += red[i];
-    return x;
-  };
-  long long total = 0, mine = 0;
-  for (int s0 = 0; s0 < b.num_seqs; s0 += 192) {
-    mine = units_of(s0 + threadIdx.x, true);
-    total += block_sum(mine);
-  }
-  // (CTAs with a run: two tiles each at least)
-  const long long grid = max(1ll, min((long long)gridDim.x, total / 2));
-  const bool run = total > 0 && blockIdx.x < grid;
-  const long long f0 = run ? total * blockIdx.x / grid : 0, f1 = run ? total * (blockIdx.x + 1) / grid : 0;
-  long long *const start = red + 6;  // {sequence, unit within it}
-  if (run) {
-    long long before = 0;
-    for (int s0 = 0; s0 < b.num_seqs; s0 += 192) {
-      const long long x = b.num_seqs <= 192 ? mine : units_of(s0 + threadIdx.x, false);
-      long long y = x;
-      for (int o = 1; o < 32; o *= 2) {
-        const long long z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) y += z;
-      }
-      __syncthreads();
-      if (lane == 31) red[warp] = y;
-      __syncthreads();
-      y += before;
-      for (int i = 0; i < 6; ++i) {
-        if (i < warp) y += red[i];
-        before += red[i];
-      }
-      if (x > 0 && y - x <= f0 && f0 < y) {
-        start[0] = s0 + threadIdx.x;
-        start[1] = f0 - (y - x);
-      }
-      if (before > f0) break;
-    }
-  }
+  const Run run = run_of<kKeys, 192>(p, red);
+  Walk<kKeys> w(p);
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  if (!run) {
+  if (!run.any) {
     if (threadIdx.x == 0) p.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
   } else if (warp == 4) {
     // ------------------------------------------------------------------ pages
-    int off = w.seek((int)start[0], start[1]);
+    int off = w.seek(run.seq, run.unit);
     const int page = min(p.a.page, kKeys), npt = kKeys / page;  // slots and pages of a tile
     const int log2_page = p.a.log2_page, none = p.a.num_pages * b.h_kv;
     bool ok = true;
-    long long left = f1 - f0;
+    long long left = run.f1 - run.f0;
     int nk = 0, nv = 0;
     while (left > 0 && ok) {
       const int n = (int)min((long long)(w.units() - off), left);
@@ -399,7 +252,7 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
     }
   } else if (warp == 5) {
     // ------------------------------------------------------------------ products
-    int off = w.seek((int)start[0], start[1]);
+    int off = w.seek(run.seq, run.unit);
     const uint32_t id_s = idesc_f8(0, C::NS, 0), id_o = idesc_f8(1, C::NP, 1);
     constexpr uint32_t SW = D == 128 ? 2 : 4;
     // K and Q: rows of D bytes, eight to a swizzle atom.  V: 128 (64: twice the same 64) columns of a key in a
@@ -425,7 +278,7 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
       mma_commit_w(bar(C::B_KE + ks));
       ++ns;
     };
-    long long left = f1 - f0;
+    long long left = run.f1 - run.f0;
     while (left > 0 && ok) {
       const int n = (int)min((long long)(w.units() - off), left);
       if (w.nt > 0) {
@@ -460,7 +313,7 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
     // ------------------------------------------------------------------ softmax / output
     const int tid = threadIdx.x;  // the key of a tile, or the column of V
     const uint32_t t_addr = tmem + ((uint32_t)(32 * warp) << 16);
-    int off = w.seek((int)start[0], start[1]);
+    int off = w.seek(run.seq, run.unit);
     int seg = 0, ns = 0;  // items with tiles begun, tiles
     bool bad = false;     // a wait gave up (all four warps leave together)
     auto wait = [&](int i, int parity) {
@@ -533,7 +386,7 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
       mbar_arrive(bar(C::B_Q));
       named_sync(1, 128);
     };
-    long long left = f1 - f0;
+    long long left = run.f1 - run.f0;
     while (left > 0 && !bad) {
       const int n = (int)min((long long)(w.units() - off), left), units = w.units();
       const bool whole = off == 0 && n == units;
@@ -766,8 +619,7 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
       if (left == 0 && tid == 0) {
         // an item that this CTA begins and others end
         const bool open = w.nt > 0 && off == 0 && n < units;
-        const long long end = f1 + units - n;
-        p.rec[blockIdx.x] = open ? make_int4(w.s, w.head, w.qt, (int)((end * grid - 1) / total)) : make_int4(-1, 0, 0, 0);
+        p.rec[blockIdx.x] = open ? open_item(run, w, units - n) : make_int4(-1, 0, 0, 0);
       }
       off = 0;
       if (left > 0) w.next();
@@ -779,47 +631,6 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
   if (warp == 5) {
     fence_after();
     tmem_dealloc(tmem, C::TMEM);
-  }
-}
-
-// Joins the parts of the item that CTA blockIdx.x of the launch before began and others ended: out = sum_i f_i O_i /
-// sum_i f_i l_i with f_i = 2^(reference_i - the largest).  Grid y: four columns of the item.
-template <int D, int NC, bool BF16>
-__global__ void __launch_bounds__(D) pages_join_kernel(const TcParams p) {
-  using C = Cfg<D, NC>;
-  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  pdl_wait();
-  const int4 rec = p.rec[blockIdx.x];
-  if (rec.x < 0) return;
-  Walk w(p);
-  w.load(rec.x);
-  w.head = rec.y;
-  w.qt = rec.z;
-  w.item();
-  const int n = rec.w - blockIdx.x + 1;
-  auto part = [&](int i) { return p.part + (2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * C::PART; };
-#pragma unroll 1
-  for (int c = 4 * blockIdx.y; c < min(NC, 4 * (int)blockIdx.y + 4); ++c) {
-    int row, head;
-    if (!column_of(p, NC, w, c, row, head)) continue;
-    float top = kNoRef;
-    for (int i = 0; i < n; ++i) {
-      const float *x = part(i) + NC * D + c;
-      if (x[NC] != 0.f) top = fmaxf(top, x[0]);
-    }
-    float o = 0.f, sum = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float *x = part(i) + NC * D + c;
-      const float l = x[NC], f = l == 0.f ? 0.f : ex2(x[0] - top);
-      if (l == 0.f) continue;
-      sum = fmaf(f, l, sum);
-      o = fmaf(f, part(i)[c * D + threadIdx.x], o);
-    }
-    const long long at = (long long)(w.q0 + row) * p.a.p.h_q + head;
-    static_cast<T *>(p.a.p.out)[at * D + threadIdx.x] = from_f32<T>(sum == 0.f ? 0.f : o / sum);
-    if (threadIdx.x == 0 && p.a.p.lse)
-      p.a.p.lse[(long long)head * p.a.p.total_q + w.q0 + row] = sum == 0.f ? -INFINITY : (top + lg2(sum)) * kLn2;
   }
 }
 
@@ -861,7 +672,7 @@ cudaError_t pages_tc_forward(const PagesAttnParams &a, void *workspace, int num_
   const int group = a.p.group, nc = columns(a.p.max_q, group);
   CUtensorMap k_map, v_map;
   const uint64_t heads = (uint64_t)a.num_pages * a.p.h_kv;
-  if (!make_tmap_pages(&k_map, a.k_pages, heads, a.page, a.p.d_qk) || !make_tmap_pages(&v_map, a.v_pages, heads, a.page, a.p.d_v))
+  if (!make_tmap_pages(&k_map, a.k_pages, heads, a.page, a.p.d_qk, kKeys) || !make_tmap_pages(&v_map, a.v_pages, heads, a.page, a.p.d_v, kKeys))
     return e;
   with(a.p.d_qk, nc, [&](auto dd, auto cc) {
     constexpr int D = decltype(dd)::value, NC = decltype(cc)::value;
@@ -875,7 +686,7 @@ cudaError_t pages_tc_forward(const PagesAttnParams &a, void *workspace, int num_
     p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + ((grid * sizeof(int4) + 255) & ~(size_t)255));
     const bool bf = a.p.dtype == VLF_BF16;
     const void *kern = bf ? (const void *)pages_tc_kernel<D, NC, true> : (const void *)pages_tc_kernel<D, NC, false>;
-    const void *join = bf ? (const void *)pages_join_kernel<D, NC, true> : (const void *)pages_join_kernel<D, NC, false>;
+    const void *join = bf ? (const void *)pages_join_kernel<D, NC, kKeys, true> : (const void *)pages_join_kernel<D, NC, kKeys, false>;
     if ((e = set_smem_once(kern, C::SMEM)) != cudaSuccess) return;
     void *args[3] = {&k_map, &v_map, &p};
     e = launch_plain(kern, dim3((unsigned)grid), 192, C::SMEM, st, args);

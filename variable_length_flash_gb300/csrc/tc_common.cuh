@@ -500,8 +500,8 @@ bool make_tmap_16bit(CUtensorMap *m, const void *base, uint64_t rows, uint64_t c
 // [tokens][heads][d] 16-bit tensor: box {64 columns, box_heads, box_tokens}, 128-byte swizzle.
 bool make_tmap_q3(CUtensorMap *m, const void *base, uint64_t tokens, uint64_t heads, uint64_t d,
                   uint32_t box_heads, uint32_t box_tokens, int is_bf16);
-// [heads][page][d] bytes: box {d, page up to 128, 1}, swizzle of the row's 64 or 128 bytes.
-bool make_tmap_pages(CUtensorMap *m, const void *base, uint64_t heads, uint64_t page, uint64_t d);
+// [heads][page][d] bytes: box {d, page up to `most`, 1}, swizzle of the row's 64 or 128 bytes.
+bool make_tmap_pages(CUtensorMap *m, const void *base, uint64_t heads, uint64_t page, uint64_t d, uint32_t most);
 // A launch that lets a small grid start as the kernel ahead of it ends (kernels wait on it first).
 cudaError_t launch_kernel(const void *kern, dim3 grid, int threads, int smem, cudaStream_t st,
                           void **args);

@@ -924,12 +924,12 @@ bool make_tmap_16bit(CUtensorMap *m, const void *base, uint64_t rows, uint64_t c
   return r == CUDA_SUCCESS;
 }
 
-bool make_tmap_pages(CUtensorMap *m, const void *base, uint64_t heads, uint64_t page, uint64_t d) {
+bool make_tmap_pages(CUtensorMap *m, const void *base, uint64_t heads, uint64_t page, uint64_t d, uint32_t most) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc || heads == 0 || (d != 64 && d != 128)) return false;
   cuuint64_t dims[3] = {d, page, heads};
   cuuint64_t strides[2] = {d, page * d};
-  cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)(page < 128 ? page : 128), 1};
+  cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)(page < most ? page : most), 1};
   cuuint32_t es[3] = {1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, es,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
