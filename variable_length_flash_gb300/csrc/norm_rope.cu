@@ -19,6 +19,7 @@
 // with half the heads in flight: 105 us).  64 tokens 4.2 us, which is a launch.
 #include "kernels.h"
 #include "rope.cuh"
+#include "tc_common.cuh"
 
 namespace vlf {
 namespace {
@@ -46,6 +47,8 @@ __global__ void __launch_bounds__(256, BWD || V == 1 ? 1 : 2) norm_rope_kernel(c
   const int phases_q = (p.h_q + p.hpt - 1) / p.hpt, ph = blockIdx.y;
   const bool is_k = ph >= phases_q;
   const Rows &rows = is_k ? p.k : p.q;
+  tc::pdl_trigger();
+  tc::pdl_wait();
   for (int c = threadIdx.x; c < half; c += 256) F[c] = turns_of(__ldg(p.inv_freq + c));
   for (int c = threadIdx.x; c < 256 + 8; c += 256) w[c] = c < p.d ? weight_at(rows.w, p.w_dtype, c) : 0.f;
   __syncthreads();
@@ -232,6 +235,8 @@ __global__ void __launch_bounds__(256, BWD || V == 1 ? 1 : 2) norm_rope_kernel(c
 __global__ void __launch_bounds__(256) norm_rope_weights_kernel(const float *part, int d, int q_parts, int parts,
                                                                void *dwq, void *dwk, int w_dtype) {
   __shared__ float red[8][32];
+  tc::pdl_trigger();
+  tc::pdl_wait();
   void *dw = blockIdx.y ? dwk : dwq;
   if (!dw) return;
   const int c = blockIdx.x * 32 + threadIdx.x % 32, r = threadIdx.x / 32;
@@ -291,15 +296,18 @@ cudaError_t launch(NormRopeParams p, cudaStream_t st) {
     const void *kern = vec ? (p.interleaved ? pick(W{}, std::true_type{}) : pick(W{}, std::false_type{}))
                            : (p.interleaved ? pick(One{}, std::true_type{}) : pick(One{}, std::false_type{}));
     void *args[1] = {&p};
-    const cudaError_t e = launch_plain(kern, dim3((unsigned)x, (unsigned)y), 256, 0, st, args);
+    const cudaError_t e = launch_dependent(kern, dim3((unsigned)x, (unsigned)y), 256, 0, st, args);
     if (e != cudaSuccess) return e;
+    count_launch();
   }
   if (!BWD || !p.part) return cudaSuccess;
   int d = p.d, q_parts = (int)(x * ((p.h_q + p.hpt - 1) / p.hpt)), parts = (int)(x * y), wd = p.w_dtype;
   const float *part = p.part;
   void *dwq = p.q.dw, *dwk = p.k.dw;
   void *args[7] = {&part, &d, &q_parts, &parts, &dwq, &dwk, &wd};
-  return launch_plain((const void *)norm_rope_weights_kernel, dim3((unsigned)((d + 31) / 32), 2), 256, 0, st, args);
+  const cudaError_t e = launch_dependent((const void *)norm_rope_weights_kernel, dim3((unsigned)((d + 31) / 32), 2), 256, 0, st, args);
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 }  // namespace

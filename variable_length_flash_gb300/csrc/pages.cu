@@ -81,6 +81,8 @@ template <typename T, int V> struct Values {
 template <typename T, int V, int NT>
 __global__ void __launch_bounds__(NT) pages_write_kernel(const PagesWriteParams p) {
   __shared__ uint32_t top[NT / 32];
+  tc::pdl_trigger();
+  tc::pdl_wait();
   const int unit = blockIdx.x, head = blockIdx.y >> 1, is_v = blockIdx.y & 1;
   int s = 0, hi = p.num_seqs;
   while (hi - s > 1) {
@@ -202,6 +204,13 @@ __global__ void __launch_bounds__(NT) pages_write_kernel(const PagesWriteParams 
   if (threadIdx.x == 0 && now != was) *scale = now;
 }
 
+// A launch that starts as the one ahead of it in the stream ends (its kernel waits for that one first).
+cudaError_t launch_step(const void *kern, dim3 grid, int threads, cudaStream_t st, void **args) {
+  const cudaError_t e = launch_dependent(kern, grid, threads, 0, st, args);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
 template <typename T>
 cudaError_t write(PagesWriteParams p, cudaStream_t st) {
   constexpr int A = 16 / sizeof(T);
@@ -215,7 +224,7 @@ cudaError_t write(PagesWriteParams p, cudaStream_t st) {
                          : (const void *)pages_write_kernel<T, 1, 256>;
   const dim3 grid((unsigned)((p.total >> p.log2_page) + 2 * p.num_seqs), (unsigned)(2 * p.h_kv));
   void *args[1] = {&p};
-  return launch_plain(kern, grid, vec ? nt : 256, 0, st, args);
+  return launch_step(kern, grid, vec ? nt : 256, st, args);
 }
 
 // ------------------------------------------------------------------------------ copying
@@ -224,6 +233,8 @@ cudaError_t write(PagesWriteParams p, cudaStream_t st) {
 constexpr int kSegment = 16384;
 
 __global__ void __launch_bounds__(256) pages_copy_kernel(const PagesCopyParams p) {
+  tc::pdl_trigger();
+  tc::pdl_wait();
   const long long kb = (long long)p.h_kv * p.page * p.d_qk, vb = (long long)p.h_kv * p.page * p.d_v;
   const int ks = (int)((kb + kSegment - 1) / kSegment);
   const bool is_v = (int)blockIdx.y >= ks;
@@ -256,9 +267,17 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const PagesCopyParams p
 }
 
 // ------------------------------------------------------------------------------ tables
+// A call's steps wait for one another: each is a launch that starts while the one before ends (its blocks are
+// there already, and wait).  One cluster of eight CTAs with its barriers between the steps took 13.1 us for 32
+// rows of 16 pages (with their copies) where this takes LATER, and 66 us for 256 rows of 1000 where this takes
+// LATER: its eight SMs look at a quarter of a million entries.
 constexpr int kChunk = 1024;  // pages of a block that counts
 
 __device__ __forceinline__ int pages_of(int len, int log2_page) { return (int)(((long long)len + (1 << log2_page) - 1) >> log2_page); }
+__device__ __forceinline__ void step_begins() {
+  tc::pdl_trigger();
+  tc::pdl_wait();
+}
 
 // Sum over a block of 256 threads; every thread gets it.
 __device__ __forceinline__ long long block_sum(long long x) {
@@ -271,11 +290,12 @@ __device__ __forceinline__ long long block_sum(long long x) {
   for (int i = 0; i < 8; ++i) x += red[i];
   return x;
 }
-// The sum before this thread, over a block of 256 threads; `all` is the whole sum.
-__device__ __forceinline__ int block_before(int x, int &all) {
+// How many of the flags of a chunk's pages are set, as each thread has four of them in a row: before its own, and in all.
+__device__ __forceinline__ int chunk_before(int mine, int &all) {
   __shared__ int red[8];
   const int lane = threadIdx.x % 32;
-  int y = x;
+  int y = mine;
+#pragma unroll
   for (int o = 1; o < 32; o *= 2) {
     const int z = __shfl_up_sync(0xffffffffu, y, o);
     if (lane >= o) y += z;
@@ -283,28 +303,17 @@ __device__ __forceinline__ int block_before(int x, int &all) {
   __syncthreads();
   if (lane == 31) red[threadIdx.x / 32] = y;
   __syncthreads();
-  int before = 0;
+  int before = y - mine;
   all = 0;
+#pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (i < (int)threadIdx.x / 32) before += red[i];
+    before += i < (int)threadIdx.x / 32 ? red[i] : 0;
     all += red[i];
   }
-  return before + y - x;
+  return before;
 }
 
-// Fork.  outside[p]: holders of p that are no row of the old table; whole[p]: new rows that have it whole;
-// owner[p]: the first new row that goes on inside it.
-__global__ void __launch_bounds__(256) fork_begin_kernel(const PagesForkParams p) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i < p.num_pages) {
-    p.outside[i] = p.refs[i];
-    p.whole[i] = 0;
-    p.owner[i] = 0x7fffffff;
-  }
-  if (i < 4) p.state[i] = 0;  // bad, free pages, pages needed
-}
-
-// A new row's parent, its length and the whole pages in it; false where it has no pages.
+// A new row's parent, its length and the whole pages in it.
 struct Row {
   int parent, len, whole;
   bool part;
@@ -315,42 +324,6 @@ __device__ __forceinline__ Row row_of(const PagesForkParams &p, int s) {
   r.whole = r.len >> p.log2_page;
   r.part = (r.len & ((1 << p.log2_page) - 1)) != 0;
   return r;
-}
-
-// Grid y: the old rows, then the new ones; x: runs of 256 entries.
-__global__ void __launch_bounds__(256) fork_count_kernel(const PagesForkParams p) {
-  tc::pdl_wait();
-  const int j = blockIdx.x * 256 + threadIdx.x;
-  for (int y = blockIdx.y; y < p.num_in + p.num_out; y += gridDim.y) {
-    const bool old = y < p.num_in;
-    Row r{y, 0, 0, false};
-    if (old) {
-      r.len = __ldg(p.lens + y);
-      if (r.len < 0 || pages_of(r.len, p.log2_page) > p.max_pages) {
-        if (j == 0) p.state[0] = VLF_ERR_BAD_SEQLENS;
-        continue;
-      }
-    } else {
-      r = row_of(p, y - p.num_in);
-      const int grow = __ldg(p.grow + y - p.num_in);
-      if (j == 0 && r.parent >= p.num_in) p.state[0] = VLF_ERR_BAD_PAGES;
-      if (grow < 0 || (long long)r.len + grow > (long long)p.max_pages << p.log2_page) {
-        if (j == 0) p.state[0] = VLF_ERR_BAD_SEQLENS;
-        continue;
-      }
-    }
-    if (j >= min(pages_of(r.len, p.log2_page), p.max_pages)) continue;
-    const int page = __ldg(p.table + (long long)r.parent * p.max_pages + j);
-    if (page < 0 || page >= p.num_pages) {
-      p.state[0] = VLF_ERR_BAD_PAGES;
-    } else if (old) {
-      atomicSub(p.outside + page, 1);
-    } else if (j < r.whole) {
-      atomicAdd(p.whole + page, 1);
-    } else {
-      atomicMin(p.owner + page, y - p.num_in);
-    }
-  }
 }
 // Holders of page i once the new rows have what they share or keep.
 __device__ __forceinline__ int held(const PagesForkParams &p, int i) {
@@ -367,105 +340,189 @@ __device__ __forceinline__ int part_of(const PagesForkParams &p, const Row &r, i
   return page;
 }
 
-// Free pages of each chunk.
-__global__ void __launch_bounds__(256) fork_free_kernel(const PagesForkParams p) {
-  tc::pdl_wait();
-  int n = 0;
-  for (int k = 0; k < kChunk / 256; ++k) {
-    const long long i = (long long)blockIdx.x * kChunk + k * 256 + threadIdx.x;
-    if (i >= p.num_pages) continue;
-    if (p.outside[i] < 0 || p.refs[i] < 0) p.state[0] = VLF_ERR_BAD_PAGES;
-    n += held(p, (int)i) == 0;
+// Fork.  outside[p]: holders of p that are no row of the old table; whole[p]: new rows that have it whole;
+// owner[p]: the first new row that goes on inside it; bits: the free pages, a bit each; counts: those of each
+// chunk; need[s]: new pages of row s; state: an error, free pages, new pages.
+__global__ void __launch_bounds__(256) fork_begin_kernel(const PagesForkParams p) {
+  step_begins();
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i < p.num_pages) {
+    p.outside[i] = p.refs[i];
+    p.whole[i] = 0;
+    p.owner[i] = 0x7fffffff;
   }
-  n = (int)block_sum(n);
-  if (threadIdx.x == 0) p.counts[blockIdx.x] = n;
+  if (i < 4) p.state[i] = 0;
 }
 
-// The free pages in order (a block for each chunk); the last block: where each new row's new pages begin.
-__global__ void __launch_bounds__(256) fork_list_kernel(const PagesForkParams p) {
-  tc::pdl_wait();
-  if ((int)blockIdx.x < p.chunks) {
-    long long before = 0, total = 0;
-    for (int c = threadIdx.x; c < p.chunks; c += 256) {
-      const int n = p.counts[c];
-      before += c < (int)blockIdx.x ? n : 0;
-      total += n;
+// The old rows' holds and the new ones'.  Grid y: rows, the old ones first; x: runs of 256 entries.
+__global__ void __launch_bounds__(256) fork_count_kernel(const PagesForkParams p) {
+  step_begins();
+  const int j = blockIdx.x * 256 + threadIdx.x;
+  for (int y = blockIdx.y; y < p.num_in + p.num_out; y += gridDim.y) {
+    const bool old = y < p.num_in;
+    const int s = y - p.num_in;
+    Row r{y, 0, 0, false};
+    if (old) {
+      r.len = __ldg(p.lens + y);
+      if (r.len < 0 || pages_of(r.len, p.log2_page) > p.max_pages) {
+        if (j == 0) p.state[0] = VLF_ERR_BAD_SEQLENS;
+        continue;
+      }
+    } else {
+      r = row_of(p, s);
+      const int grow = __ldg(p.grow + s);
+      if (j == 0 && r.parent >= p.num_in) p.state[0] = VLF_ERR_BAD_PAGES;
+      if (grow < 0 || (long long)r.len + grow > (long long)p.max_pages << p.log2_page) {
+        if (j == 0) p.state[0] = VLF_ERR_BAD_SEQLENS;
+        continue;
+      }
     }
-    int at = (int)block_sum(before);
-    total = block_sum(total);
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.state[1] = (int)total;
+    if (j >= min(pages_of(r.len, p.log2_page), p.max_pages)) continue;
+    const int page = __ldg(p.table + (long long)r.parent * p.max_pages + j);
+    if (page < 0 || page >= p.num_pages) p.state[0] = VLF_ERR_BAD_PAGES;
+    else if (old) atomicSub(p.outside + page, 1);
+    else if (j < r.whole) atomicAdd(p.whole + page, 1);
+    else atomicMin(p.owner + page, s);
+  }
+}
+
+// The free pages of a chunk (a block each); the blocks behind them: what new rows need, 256 a block.
+__global__ void __launch_bounds__(256) fork_free_kernel(const PagesForkParams p) {
+  step_begins();
+  int n = 0;
+  if ((int)blockIdx.x < p.chunks) {
+#pragma unroll
     for (int k = 0; k < kChunk / 256; ++k) {
       const long long i = (long long)blockIdx.x * kChunk + k * 256 + threadIdx.x;
-      const int n = i < p.num_pages && held(p, (int)i) == 0;
-      int all;
-      const int mine = block_before(n, all);
-      if (n) p.list[at + mine] = (int)i;
-      at += all;
+      const bool in = i < p.num_pages;
+      if (in && (p.outside[i] < 0 || p.refs[i] < 0)) p.state[0] = VLF_ERR_BAD_PAGES;
+      const uint32_t m = __ballot_sync(0xffffffffu, in && held(p, (int)i) == 0);
+      if (threadIdx.x % 32 == 0) {
+        p.bits[(long long)blockIdx.x * (kChunk / 32) + (k * 256 + threadIdx.x) / 32] = m;
+        n += __popc(m);
+      }
+    }
+    n = (int)block_sum(n);
+    if (threadIdx.x == 0) {
+      p.counts[blockIdx.x] = n;
+      atomicAdd(p.state + 1, n);
     }
     return;
   }
-  long long at = 0;
-  for (int s0 = 0; s0 < p.num_out; s0 += 256) {
-    const int s = s0 + threadIdx.x;
-    int need = 0;
-    if (s < p.num_out) {
-      const Row r = row_of(p, s);
-      bool keeps;
-      const int page = part_of(p, r, s, keeps);
-      const long long to = min((long long)r.len + max(0, __ldg(p.grow + s)), (long long)p.max_pages << p.log2_page);
-      need = pages_of((int)to, p.log2_page) - pages_of(r.len, p.log2_page) + (page >= 0 && !keeps);
-    }
-    int all;
-    const int before = block_before(need, all);
-    if (s < p.num_out) p.begin[s] = (int)min(at + before, (long long)0x7fffffff);
-    at += all;
-  }
-  if (threadIdx.x == 0) p.state[2] = (int)min(at, (long long)0x7fffffff);
-}
-
-// The new tables (grid y: the new rows, x: runs of 256 entries) and, in the same grid, the new counts.
-__global__ void __launch_bounds__(256) fork_end_kernel(const PagesForkParams p) {
-  tc::pdl_wait();
-  const int bad = p.state[0], free = p.state[1], need = p.state[2];
-  const bool ok = bad == 0 && need <= free;
-  const long long flat = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
-  if (flat == 0) {
-    if (bad) set_error(p.err, bad);
-    *p.left = bad ? (int)0x80000000 : free - need;
-  }
-  // pages that the call gives out are its `need` first free ones: each new row has its run of them
-  for (long long i = flat; i < p.num_pages; i += (long long)gridDim.x * gridDim.y * 256)
-    if (!ok) p.refs_out[i] = p.refs[i];
-    else if (const int n = held(p, (int)i)) p.refs_out[i] = n;
-  if (ok)
-    for (long long i = flat; i < free; i += (long long)gridDim.x * gridDim.y * 256) p.refs_out[p.list[i]] = i < need;
-  const int j = blockIdx.x * 256 + threadIdx.x;
-  for (int s = blockIdx.y; s < p.num_out; s += gridDim.y) {
+  const int s = (blockIdx.x - p.chunks) * 256 + threadIdx.x;
+  if (s < p.num_out) {
     const Row r = row_of(p, s);
     bool keeps;
-    const int part = part_of(p, r, s, keeps);
-    const int len = ok ? r.len + __ldg(p.grow + s) : 0;
-    if (j == 0) {
-      const bool copy = ok && part >= 0 && !keeps;
-      p.lens_out[s] = len;
-      p.src[s] = copy ? part : -1;
-      p.dst[s] = copy ? p.list[p.begin[s]] : -1;
+    const int page = part_of(p, r, s, keeps);
+    const long long to = min((long long)r.len + max(0, __ldg(p.grow + s)), (long long)p.max_pages << p.log2_page);
+    n = pages_of((int)to, p.log2_page) - pages_of(r.len, p.log2_page) + (page >= 0 && !keeps);
+    p.need[s] = n;
+  }
+  // (more pages than there are is all that has to be told apart)
+  const long long all = block_sum(n);
+  if (threadIdx.x == 0) atomicAdd(reinterpret_cast<unsigned long long *>(p.state + 2), (unsigned long long)all);
+}
+
+// The new counts (a block for each chunk), and the new rows (a block of eight warps for eight rows).
+__global__ void __launch_bounds__(256) fork_end_kernel(const PagesForkParams p) {
+  step_begins();
+  const int bad = p.state[0], free = p.state[1], lane = threadIdx.x % 32;
+  const long long need = *reinterpret_cast<const long long *>(p.state + 2);
+  const bool ok = bad == 0 && need <= free;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (bad) set_error(p.err, bad);
+    *p.left = bad ? (int)0x80000000 : (int)max((long long)free - need, -0x7fffffffll);
+  }
+  if ((int)blockIdx.x < p.chunks) {
+    long long before = 0;
+    for (int c = threadIdx.x; c < (int)blockIdx.x; c += 256) before += p.counts[c];
+    const int at = (int)block_sum(before);  // free pages in front of the chunk
+    const uint32_t word = p.bits[(long long)blockIdx.x * (kChunk / 32) + threadIdx.x / 8];
+    const uint32_t mine = word >> 4 * (threadIdx.x % 8) & 15u;  // of this thread's four pages
+    int all, rank = at + chunk_before(__popc(mine), all);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const long long i = (long long)blockIdx.x * kChunk + 4 * threadIdx.x + k;
+      if (i >= p.num_pages) continue;
+      // the pages given out are the first `need` free ones
+      if (!ok) p.refs_out[i] = p.refs[i];
+      else if (mine >> k & 1) p.refs_out[i] = rank++ < need;
+      else p.refs_out[i] = held(p, (int)i);
     }
-    if (j >= p.max_pages) continue;
-    int page = -1;
-    if (j < pages_of(len, p.log2_page)) {
-      if (j < r.whole) page = __ldg(p.table + (long long)r.parent * p.max_pages + j);
-      else if (keeps && j == r.whole) page = part;
-      else page = p.list[p.begin[s] + j - r.whole - (keeps ? 1 : 0)];
+    return;
+  }
+  const int s0 = (blockIdx.x - p.chunks) * 8;
+  long long sum = 0;
+  for (int s = threadIdx.x; s < s0; s += 256) sum += p.need[s];
+  sum = block_sum(sum);
+  const int s = s0 + threadIdx.x / 32;
+  if (s >= p.num_out) return;
+  for (int i = s0; i < s; ++i) sum += p.need[i];  // new pages of the rows before
+  // the free page of rank k: its chunk by the counts, its word and bit by the words' (the whole warp)
+  auto free_page = [&](long long k) {
+    int c = 0;
+    for (int c0 = 0;; c0 += 32) {
+      const int n = c0 + lane < p.chunks ? p.counts[c0 + lane] : 0;
+      int y = n;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+      }
+      const uint32_t m = __ballot_sync(0xffffffffu, k < y);
+      if (m) {
+        c = c0 + __ffs(m) - 1;
+        k -= __shfl_sync(0xffffffffu, y - n, __ffs(m) - 1);
+        break;
+      }
+      k -= __shfl_sync(0xffffffffu, y, 31);
+      if (c0 + 32 >= p.chunks) return -1;  // (there is one: the ranks asked for are below the free pages' number)
     }
-    p.table_out[(long long)s * p.max_pages + j] = page;
+    uint32_t word = p.bits[(long long)c * (kChunk / 32) + lane];
+    const int n = __popc(word);
+    int y = n;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, k < y);
+    const int from = __ffs(m) - 1;
+    int in = (int)k - __shfl_sync(0xffffffffu, y - n, from);
+    word = __shfl_sync(0xffffffffu, word, from);
+    while (in-- > 0) word &= word - 1;
+    return c * kChunk + 32 * from + __ffs(word) - 1;
+  };
+  const Row r = row_of(p, s);
+  bool keeps;
+  const int part = part_of(p, r, s, keeps);
+  const bool copy = ok && part >= 0 && !keeps;
+  const int len = ok ? r.len + __ldg(p.grow + s) : 0, has = pages_of(len, p.log2_page);
+  const int32_t *row = p.table + (long long)r.parent * p.max_pages;
+  int *out = p.table_out + (long long)s * p.max_pages;
+  const int shared = ok ? r.whole + (keeps ? 1 : 0) : 0;  // entries that stay
+#pragma unroll 4
+  for (int j = lane; j < p.max_pages; j += 32)
+    if (j < shared || j >= has) out[j] = j >= has ? -1 : j < r.whole ? __ldg(row + j) : part;
+  int first = -1;
+  for (int j = shared; j < has; ++j) {
+    const int page = free_page(sum + j - shared);
+    if (j == shared) first = page;
+    if (lane == 0) out[j] = page;
+  }
+  if (lane == 0) {
+    p.lens_out[s] = len;
+    p.src[s] = copy ? part : -1;
+    p.dst[s] = copy ? first : -1;
   }
 }
 
 // Compact.  Of the U pages in use the ones behind the first U pages move into the free ones among them, the
 // first into the first.
 __global__ void __launch_bounds__(256) compact_count_kernel(const PagesCompactParams p) {
+  step_begins();
   int n = 0;
+#pragma unroll
   for (int k = 0; k < kChunk / 256; ++k) {
     const long long i = (long long)blockIdx.x * kChunk + k * 256 + threadIdx.x;
     if (i >= p.num_pages) continue;
@@ -477,61 +534,64 @@ __global__ void __launch_bounds__(256) compact_count_kernel(const PagesCompactPa
 }
 // order[p]: which of the moving pages p is (-1: none).
 __global__ void __launch_bounds__(256) compact_list_kernel(const PagesCompactParams p) {
-  tc::pdl_wait();
+  step_begins();
   long long before = 0, total = 0;
   for (int c = threadIdx.x; c < p.chunks; c += 256) {
     const int n = p.counts[c];
     before += c < (int)blockIdx.x ? n : 0;
     total += n;
   }
-  int at = (int)block_sum(before);
-  const int used = (int)block_sum(total);
+  const int at = (int)block_sum(before), used = (int)block_sum(total);
   // pages in use among the first `used`
   long long front = 0;
   for (int c = threadIdx.x; c < used / kChunk; c += 256) front += p.counts[c];
   for (int i = used / kChunk * kChunk + threadIdx.x; i < used; i += 256) front += p.refs[i] > 0;
   front = block_sum(front);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.used = used;
-  for (int k = 0; k < kChunk / 256; ++k) {
-    const int i = (int)(blockIdx.x * kChunk + k * 256 + threadIdx.x);
-    const int n = i < p.num_pages && p.refs[i] > 0;
-    int all;
-    const int rank = at + block_before(n, all);  // pages in use before this one
-    at += all;
+  bool is[4];
+  int mine = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const long long i = (long long)blockIdx.x * kChunk + 4 * threadIdx.x + k;
+    is[k] = i < p.num_pages && p.refs[i] > 0;
+    mine += is[k];
+  }
+  int all, rank = at + chunk_before(mine, all);  // pages in use before this one
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = (int)(blockIdx.x * kChunk + 4 * threadIdx.x + k);
     if (i >= p.num_pages) continue;
     p.order[i] = -1;
-    if (n && i >= used) {
+    if (is[k] && i >= used) {
       p.order[i] = rank - (int)front;
       p.src[rank - (int)front] = i;
-    } else if (!n && i < used) {
+    } else if (!is[k] && i < used) {
       p.dst[i - rank] = i;
     }
+    rank += is[k];
   }
 }
-// Where the page i in use is afterwards.
-__device__ __forceinline__ int moved(const PagesCompactParams &p, int i) {
-  const int o = p.order[i];
-  return o < 0 ? i : p.dst[o];
-}
 __global__ void __launch_bounds__(256) compact_end_kernel(const PagesCompactParams p) {
-  tc::pdl_wait();
+  step_begins();
   const long long step = (long long)gridDim.x * 256;
+  auto moved = [&](int i) {  // where the page i in use is afterwards
+    const int o = p.order[i];
+    return o < 0 ? i : p.dst[o];
+  };
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < p.num_pages; i += step) {
-    const int n = p.refs[i];
-    p.to[i] = n > 0 ? moved(p, (int)i) : -1;
-    const int used = *p.used;
-    if (n > 0) p.refs_out[moved(p, (int)i)] = n;
-    if (i >= used) p.refs_out[i] = 0;
+    const int n = p.refs[i], to = n > 0 ? moved((int)i) : -1;
+    p.to[i] = to;
+    if (n > 0) p.refs_out[to] = n;
+    if (i >= *p.used) p.refs_out[i] = 0;
   }
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < p.entries; i += step) {
     const int page = p.table[i];
-    p.table_out[i] = page >= 0 && page < p.num_pages && p.refs[page] > 0 ? moved(p, page) : -1;
+    p.table_out[i] = page >= 0 && page < p.num_pages && p.refs[page] > 0 ? moved(page) : -1;
   }
 }
 
 size_t ints(long long n) { return ((size_t)n * 4 + 255) & ~(size_t)255; }
 int chunks_of(int num_pages) { return (int)(((long long)num_pages + kChunk - 1) / kChunk); }
-
 }  // namespace
 
 cudaError_t pages_write(const PagesWriteParams &p, cudaStream_t st) {
@@ -546,12 +606,13 @@ cudaError_t pages_copy(PagesCopyParams p, cudaStream_t st) {
   // pairs per block: what leaves about eight blocks per SM (as many are resident)
   p.chunk = (int)max(1ll, min(32ll, (long long)p.n * segs / (152 * 8)));
   void *args[1] = {&p};
-  return launch_plain((const void *)pages_copy_kernel, dim3((unsigned)((p.n + p.chunk - 1) / p.chunk), (unsigned)segs),
-                      256, 0, st, args);
+  return launch_step((const void *)pages_copy_kernel, dim3((unsigned)((p.n + p.chunk - 1) / p.chunk), (unsigned)segs), 256,
+                     st, args);
 }
 
 size_t pages_fork_workspace(int num_pages, int num_out) {
-  return 4 * ints(num_pages) + ints(chunks_of(num_pages)) + ints(num_out) + ints(4);
+  const int chunks = chunks_of(num_pages);
+  return 3 * ints(num_pages) + ints((long long)chunks * (kChunk / 32)) + ints(chunks) + ints(num_out) + ints(4);
 }
 cudaError_t pages_fork(PagesForkParams p, void *workspace, cudaStream_t st) {
   char *w = static_cast<char *>(workspace);
@@ -564,25 +625,19 @@ cudaError_t pages_fork(PagesForkParams p, void *workspace, cudaStream_t st) {
   p.outside = take(p.num_pages);
   p.whole = take(p.num_pages);
   p.owner = take(p.num_pages);
-  p.list = take(p.num_pages);
+  p.bits = reinterpret_cast<unsigned *>(take((long long)p.chunks * (kChunk / 32)));
   p.counts = take(p.chunks);
-  p.begin = take(p.num_out);
+  p.need = take(p.num_out);
   p.state = take(4);
   void *args[1] = {&p};
-  const unsigned pages = (unsigned)(((long long)max(p.num_pages, 4) + 255) / 256);
-  const unsigned wide = (unsigned)max(1, (p.max_pages + 255) / 256);
-  auto then = [&](const void *kern, dim3 grid) {
-    const cudaError_t r = launch_dependent(kern, grid, 256, 0, st, args);
-    if (r == cudaSuccess) count_launch();
-    return r;
-  };
-  cudaError_t e = launch_plain((const void *)fork_begin_kernel, dim3(pages), 256, 0, st, args);
-  if (e == cudaSuccess && p.num_in + p.num_out > 0)
-    e = then((const void *)fork_count_kernel, dim3(wide, (unsigned)min(p.num_in + p.num_out, 65535)));
-  if (e == cudaSuccess && p.chunks > 0)
-    e = then((const void *)fork_free_kernel, dim3((unsigned)p.chunks));
-  if (e == cudaSuccess) e = then((const void *)fork_list_kernel, dim3((unsigned)p.chunks + 1));
-  if (e == cudaSuccess) e = then((const void *)fork_end_kernel, dim3(wide, (unsigned)max(1, min(p.num_out, 65535))));
+  const int rows = p.num_in + p.num_out;
+  auto step = [&](const void *kern, dim3 grid) { return launch_step(kern, grid, 256, st, args); };
+  cudaError_t e = step((const void *)fork_begin_kernel, dim3((unsigned)(((long long)max(p.num_pages, 4) + 255) / 256)));
+  if (e == cudaSuccess && rows > 0)
+    e = step((const void *)fork_count_kernel, dim3((unsigned)max(1, (p.max_pages + 255) / 256), (unsigned)min(rows, 65535)));
+  const int behind = (p.num_out + 255) / 256;
+  if (e == cudaSuccess && p.chunks + behind > 0) e = step((const void *)fork_free_kernel, dim3((unsigned)(p.chunks + behind)));
+  if (e == cudaSuccess) e = step((const void *)fork_end_kernel, dim3((unsigned)max(1, p.chunks + (p.num_out + 7) / 8)));
   return e;
 }
 
@@ -592,16 +647,11 @@ cudaError_t pages_compact(PagesCompactParams p, void *workspace, cudaStream_t st
   p.counts = static_cast<int *>(workspace);
   p.order = reinterpret_cast<int *>(static_cast<char *>(workspace) + ints(p.chunks));
   void *args[1] = {&p};
-  cudaError_t e = launch_plain((const void *)compact_count_kernel, dim3((unsigned)p.chunks), 256, 0, st, args);
-  auto then = [&](const void *kern, unsigned blocks) {
-    const cudaError_t r = launch_dependent(kern, dim3(blocks), 256, 0, st, args);
-    if (r == cudaSuccess) count_launch();
-    return r;
-  };
-  if (e == cudaSuccess) e = then((const void *)compact_list_kernel, (unsigned)p.chunks);
-  const long long most = max(p.entries, (long long)p.num_pages);
+  auto step = [&](const void *kern, long long blocks) { return launch_step(kern, dim3((unsigned)blocks), 256, st, args); };
+  cudaError_t e = step((const void *)compact_count_kernel, p.chunks);
+  if (e == cudaSuccess) e = step((const void *)compact_list_kernel, p.chunks);
   if (e == cudaSuccess)
-    e = then((const void *)compact_end_kernel, (unsigned)min((most + 255) / 256, 152ll * 8));
+    e = step((const void *)compact_end_kernel, min((max(p.entries, (long long)p.num_pages) + 255) / 256, 152ll * 8));
   return e;
 }
 

@@ -567,9 +567,10 @@ cudaError_t pages_rows_forward(const PagesAttnParams &a, void *workspace, int nu
     cudaError_t e = set_smem_once(kern, C::SMEM);
     if (e != cudaSuccess) return e;
     void *args[3] = {&k_map, &v_map, &p};
-    e = launch_plain(kern, dim3((unsigned)num_sms), kThreads, C::SMEM, st, args);
+    e = launch_dependent(kern, dim3((unsigned)num_sms), kThreads, C::SMEM, st, args);
+    if (e == cudaSuccess) count_launch();
     void *jargs[1] = {&p};
-    if (e == cudaSuccess) e = launch_dependent(join, dim3((unsigned)num_sms, C::NC / 4), D, 0, st, jargs);
+    if (e == cudaSuccess) e = launch_dependent(join, dim3((unsigned)num_sms, C::NC / kJoinWarps), 32 * kJoinWarps, 0, st, jargs);
     if (e == cudaSuccess) count_launch();
     return e;
   };

@@ -440,7 +440,6 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
               for (int i = 0; i < D; i += 16) sts_v4(to + i, 0, 0, 0, 0);
             }
           }
-          if (ns >= C::PB) wait(C::B_PE + pb, ns / C::PB - 1);
           // y = log2 of P, with the references as they are; -inf where the key is not seen
           float y[NC], most = -INFINITY;
           auto logits = [&]() {
@@ -559,6 +558,7 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
               }
             }
           }
+          if (ns >= C::PB) wait(C::B_PE + pb, ns / C::PB - 1);  // (a wait that gave up: the vote on the next tile tells)
           const uint32_t to = sP + pb * C::P_BYTES + tid * 16;
 #pragma unroll
           for (int i = 0; i < C::NP / 16; ++i) sts_v4(to + i * 16 * kKeys, w4[4 * i], w4[4 * i + 1], w4[4 * i + 2], w4[4 * i + 3]);
@@ -689,9 +689,10 @@ cudaError_t pages_tc_forward(const PagesAttnParams &a, void *workspace, int num_
     const void *join = bf ? (const void *)pages_join_kernel<D, NC, kKeys, true> : (const void *)pages_join_kernel<D, NC, kKeys, false>;
     if ((e = set_smem_once(kern, C::SMEM)) != cudaSuccess) return;
     void *args[3] = {&k_map, &v_map, &p};
-    e = launch_plain(kern, dim3((unsigned)grid), 192, C::SMEM, st, args);
+    e = launch_dependent(kern, dim3((unsigned)grid), 192, C::SMEM, st, args);
+    if (e == cudaSuccess) count_launch();
     void *jargs[1] = {&p};
-    if (e == cudaSuccess) e = launch_dependent(join, dim3((unsigned)grid, (NC + 3) / 4), D, 0, st, jargs);
+    if (e == cudaSuccess) e = launch_dependent(join, dim3((unsigned)grid, (NC + kJoinWarps - 1) / kJoinWarps), 32 * min(NC, kJoinWarps), 0, st, jargs);
     if (e == cudaSuccess) count_launch();
   });
   return e;
