@@ -10,8 +10,10 @@
 // exponent, as in pages_tc.cu, whose runs of key tiles, parts and join these are as well.  P is rounded to
 // fp16 with the row's largest between 2^7 and 2^15: half a step of 2^-11, nothing above 2^-31 of the largest lost.
 //
-// Roles of a CTA (one per SM): warp 0 page loads, warp 1 S = Q K^T, warp 2 O += P V, warps 4-7 bytes to fp16,
-// warps 8-15 softmax and output, a thread for each row of the two query tiles.  TMEM: O of both tiles, two S of
+// Roles of a CTA (one per SM): warp 0 page loads, warp 1 S = Q K^T, warp 2 O += P V, warp 3 the items of the CTA's
+// run, which it lays out in shared memory for the others (their registers are full without it), warps 4-11 bytes
+// to fp16, warps 12-19 softmax and output, a thread for each row of the two query tiles: these have the registers that
+// the others give up.  TMEM: O of both tiles, two S of
 // 64 keys each, over which P is written.
 #include "e4m3.cuh"
 #include "pages_tc.cuh"
@@ -25,21 +27,34 @@ constexpr int kN = 64;             // keys of a tile
 constexpr float kMove = 8.f;       // log2 of what a row's largest may grow by before O is rescaled
 constexpr float kLift = 7.f;       // log2 of a row's largest P when its reference is set
 constexpr int kScales = 16;        // tiles whose scales are held (more than the rings let loads run ahead)
-constexpr int kThreads = 512;
+constexpr int kThreads = 640, kTurners = 256;  // of a CTA; that turn bytes to fp16
+
+// A run's part of an item, as the CTA's warps read it.
+struct Item {
+  int s, head, q0, q_len, len, r0, r1, split;  // sequence, kv head, first row, lengths, rows, first head of the group (splits)
+  int tile, n, lo, hi;                         // key tiles [tile, tile + n), the keys that its rows see
+  int flags, pad[3];
+};
+constexpr int kEnd = 1, kTiles = 2, kWhole = 4, kFirst = 8, kTwo = 16;  // behind the last; has key tiles; is all of the item;
+                                                                       // begins it; has rows for the second query tile
+constexpr int kItems = 4, kReaders = 19;  // items laid out at a time; warps that read them
 
 template <int D> struct RowCfg {
   static constexpr int KB = D / 64;                          // blocks of 64 columns
   static constexpr int QBLK = 128 * 128, Q_TILE = KB * QBLK;
   static constexpr int BLK = kN * 128, T_BYTES = KB * BLK;   // an fp16 tile
   static constexpr int B_BYTES = kN * D;                     // a tile as bytes
-  static constexpr int NK = 3, NV = 3, NB = 2;
+  static constexpr int NK = 3, NV = NK, NB = 2;              // (barriers and slots of values lie behind those of keys)
   static constexpr int OFF_Q = 0, OFF_K = OFF_Q + 2 * Q_TILE, OFF_V = OFF_K + NK * T_BYTES, OFF_BK = OFF_V + NV * T_BYTES,
                        OFF_BV = OFF_BK + NB * B_BYTES, OFF_SC = OFF_BV + NB * B_BYTES;  // float2[kScales][4]
-  static constexpr int OFF_RED = OFF_SC + kScales * 4 * 8;   // long long[18]
-  static constexpr int OFF_BAR = OFF_RED + 18 * 8;
+  static constexpr int OFF_DOWN = OFF_SC + kScales * 4 * 8;  // float[256]
+  static constexpr int OFF_STAGE = OFF_DOWN + 256 * 4;       // [8 warps][32 rows of 64 bytes]
+  static constexpr int OFF_ITEM = OFF_STAGE + 8 * 2048;
+  static constexpr int OFF_RED = OFF_ITEM + kItems * (int)sizeof(Item);  // long long[22]
+  static constexpr int OFF_BAR = OFF_RED + 22 * 8;
   static constexpr int B_BKF = 0, B_BKE = B_BKF + NB, B_BVF = B_BKE + NB, B_BVE = B_BVF + NB, B_KF = B_BVE + NB,
                        B_KE = B_KF + NK, B_VF = B_KE + NK, B_VE = B_VF + NV, B_Q = B_VE + NV, B_S = B_Q + 2, B_P = B_S + 4,
-                       B_O = B_P + 4, B_OE = B_O + 4, B_SC = B_OE + 2, B_DRAIN = B_SC + kScales, BARS = B_DRAIN + 2;
+                       B_O = B_P + 4, B_OE = B_O + 4, B_SC = B_OE + 2, B_IF = B_SC + kScales, B_IE = B_IF + kItems, B_DRAIN = B_IE + kItems, BARS = B_DRAIN + 2;
   static constexpr int SMEM = OFF_BAR + BARS * 8 + 16 + 1024;
   static constexpr int S_COL = 2 * D, TMEM = 512;            // S[tile][buffer] behind the two O
   static constexpr int NC = 256, PART = NC * (D + 2);
@@ -58,8 +73,14 @@ __device__ __forceinline__ uint32_t scaled(uint32_t h, uint32_t by) {
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1) 
     pages_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                       const __grid_constant__ TcParams p) {
   using C = RowCfg<D>;
@@ -69,6 +90,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *const smem = smem_dyn + (base - smem_u32(smem_dyn));
   const uint32_t sQ = base + C::OFF_Q, sK = base + C::OFF_K, sV = base + C::OFF_V, sBK = base + C::OFF_BK, sBV = base + C::OFF_BV;
   float2 *const scales = reinterpret_cast<float2 *>(smem + C::OFF_SC);
+  float *const downs = reinterpret_cast<float *>(smem + C::OFF_DOWN);
+  volatile Item *const items = reinterpret_cast<volatile Item *>(smem + C::OFF_ITEM);
   auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
   uint32_t *const tmem_holder = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + C::BARS * 8);
   volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
@@ -79,14 +102,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NB; ++i) {
-      mbar_init(bar(C::B_BKF + i), 1); mbar_init(bar(C::B_BKE + i), 128);
-      mbar_init(bar(C::B_BVF + i), 1); mbar_init(bar(C::B_BVE + i), 128);
+      mbar_init(bar(C::B_BKF + i), 1); mbar_init(bar(C::B_BKE + i), kTurners);
+      mbar_init(bar(C::B_BVF + i), 1); mbar_init(bar(C::B_BVE + i), kTurners);
     }
-    for (int i = 0; i < C::NK; ++i) { mbar_init(bar(C::B_KF + i), 128); mbar_init(bar(C::B_KE + i), 1); }
-    for (int i = 0; i < C::NV; ++i) { mbar_init(bar(C::B_VF + i), 128); mbar_init(bar(C::B_VE + i), 1); }
+    for (int i = 0; i < C::NK; ++i) { mbar_init(bar(C::B_KF + i), kTurners); mbar_init(bar(C::B_KE + i), 1); }
+    for (int i = 0; i < C::NV; ++i) { mbar_init(bar(C::B_VF + i), kTurners); mbar_init(bar(C::B_VE + i), 1); }
     for (int i = 0; i < 4; ++i) { mbar_init(bar(C::B_S + i), 1); mbar_init(bar(C::B_P + i), 128); mbar_init(bar(C::B_O + i), 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(bar(C::B_Q + i), 128); mbar_init(bar(C::B_OE + i), 128); mbar_init(bar(C::B_DRAIN + i), 1); }
     for (int i = 0; i < kScales; ++i) mbar_init(bar(C::B_SC + i), 1);
+    for (int i = 0; i < kItems; ++i) { mbar_init(bar(C::B_IF + i), 1); mbar_init(bar(C::B_IE + i), kReaders); }
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -100,42 +124,70 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   const Run run = run_of<kN, kThreads>(p, reinterpret_cast<long long *>(smem + C::OFF_RED));
+  // (here, ahead of the roles: a 64-bit division is a call, which code that changes its registers cannot make)
   Walk<kN> w(p);
+  const int run_off = warp == 3 && run.any ? w.seek(run.seq, run.unit) : 0;
   const int L = lanes_of(b.group);
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_holder;
-  auto wait = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_wait(bar(i), parity & 1, abort_flag, err)); };
-  // whether an item has rows for the second query tile
-  auto tiles_of = [&](const Walk<kN> &x) {
-    return p.splits > 1 ? (b.group - x.qt % p.splits * C::NC > L ? 2 : 1) : ((x.r1 - x.r0) * b.group > L ? 2 : 1);
+  auto wait = [&](int i, int parity) {
+    // (mbar_wait in line, for the same reason)
+    bool done = mbar_try_wait(bar(i), parity & 1);
+    if (__builtin_expect(!done, 0)) {
+      const uint64_t t0 = globaltimer();
+      for (uint32_t n = 1; !done; ++n) {
+        done = mbar_try_wait(bar(i), parity & 1);
+        if ((n & 31u) || done) continue;
+        if (*abort_flag) break;
+        if (globaltimer() - t0 > kTimeoutNs) {
+          *abort_flag = 1;
+          set_error(err, VLF_ERR_TIMEOUT);
+          break;
+        }
+      }
+    }
+    return __all_sync(0xffffffffu, done);
+  };
+  // the next item (nullptr behind the last, or where a wait gave up), and a warp's word that it is done with it
+  int it = 0;
+  auto next_item = [&]() -> volatile Item * {
+    if (!wait(C::B_IF + it % kItems, it / kItems)) return nullptr;
+    volatile Item *x = items + it % kItems;
+    return x->flags & kEnd ? nullptr : x;
+  };
+  auto done_item = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::B_IE + it % kItems));
+    ++it;
   };
 
   if (!run.any) {
-    if (threadIdx.x == 0) p.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  } else if (warp == 0) {
+    if (threadIdx.x == 0) no_item(p);
+  } else if (warp < 12) {
+  // registers: launched with 96 a thread, 61440 in all; then 64 for 384 threads and 144 for the 256 of the softmax, which is as many
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+  if (warp == 0) {
     // ------------------------------------------------------------------ pages
-    int off = w.seek(run.seq, run.unit);
     const int page = min(p.a.page, kN), npt = kN / page;  // slots and pages of a tile
     const int log2_page = p.a.log2_page, none = p.a.num_pages * b.h_kv;
     bool ok = true;
-    long long left = run.f1 - run.f0;
     int nt = 0;
-    while (left > 0 && ok) {
-      const int n = (int)min((long long)(w.units() - off), left);
-      if (w.nt > 0) {
-        const int32_t *row = p.a.table + (long long)w.s * p.a.max_pages;
+    while (volatile Item *const x = ok ? next_item() : nullptr) {
+      if (x->flags & kTiles) {
+        const int n = x->n, tile = x->tile, lo = x->lo, hi = x->hi, kv_head = x->head;
+        const int32_t *row = p.a.table + (long long)x->s * p.a.max_pages;
         // a lane has a page of a tile, and that of the next one
         auto id_of = [&](int m) {
-          const int i = ((w.t0 + off + m) * kN >> log2_page) + lane;
-          if (m >= n || lane >= npt || i > (w.hi - 1) >> log2_page || i < w.lo >> log2_page) return -2;  // no key in it
+          const int i = ((tile + m) * kN >> log2_page) + lane;
+          if (m >= n || lane >= npt || i > (hi - 1) >> log2_page || i < lo >> log2_page) return -2;  // no key in it
           return max(__ldg(row + i), -1);
         };
         auto real = [&](int id) { return id >= 0 && id < p.a.num_pages; };
         auto scale_of = [&](int id) {
           if (!real(id)) return make_float2(0.f, 0.f);
-          const long long at = (long long)id * b.h_kv + w.head;
+          const long long at = (long long)id * b.h_kv + kv_head;
           return make_float2(__ldg(p.a.k_scale + at), __ldg(p.a.v_scale + at));
         };
         int id = id_of(0), next = id_of(1);
@@ -145,9 +197,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 sc_next = scale_of(next);
           const bool have = id != -2;
           if (have && !real(id)) set_error(err, VLF_ERR_BAD_PAGES);
-          const int z = real(id) ? id * b.h_kv + w.head : none;  // (outside: zeros)
+          const int z = real(id) ? id * b.h_kv + kv_head : none;  // (outside: zeros)
           const int bytes = __popc(__ballot_sync(0xffffffffu, have)) * page * D;
-          const int y = p.a.page > kN ? (w.t0 + off + m) * kN & (p.a.page - 1) : 0;
+          const int y = p.a.page > kN ? (tile + m) * kN & (p.a.page - 1) : 0;
           const int sb = nt % C::NB;
           if (nt >= C::NB) ok = wait(C::B_BKE + sb, nt / C::NB - 1);
           if (!ok) break;
@@ -168,9 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           sc = sc_next;
         }
       }
-      left -= n;
-      off = 0;
-      if (left > 0) w.next();
+      done_item();
     }
     // no copy may still be landing when the CTA leaves
     if (lane == 0)
@@ -180,228 +230,270 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ S = Q K^T
-    int off = w.seek(run.seq, run.unit);
     const uint32_t id = idesc_f16(0, 128, kN, 0, 0);
     const uint64_t dq0 = sdesc_sw128(sQ, 16, 1024), dk0 = sdesc_sw128(sK, 16, 1024);
     bool ok = true;
-    long long left = run.f1 - run.f0;
-    int nt = 0, ns[2] = {0, 0}, seg[2] = {0, 0};  // tiles; of each query tile the S issued and items begun
-    while (left > 0 && ok) {
-      const int n = (int)min((long long)(w.units() - off), left);
-      if (w.nt > 0) {
-        const int tiles = tiles_of(w);
-        for (int t = 0; t < tiles && ok; ++t) ok = wait(C::B_Q + t, seg[t]++);
+    int nt = 0, ns0 = 0, ns1 = 0, seg0 = 0, seg1 = 0;  // tiles; of each query tile the S issued and items begun
+    while (volatile Item *const x = ok ? next_item() : nullptr) {
+      const int flags = x->flags, n = x->n, tiles = flags & kTwo ? 2 : 1;
+      done_item();
+      if (flags & kTiles) {
+        ok = wait(C::B_Q, seg0++);
+        if (ok && tiles > 1) ok = wait(C::B_Q + 1, seg1++);
         for (int m = 0; m < n && ok; ++m, ++nt) {
           const int sl = nt % C::NK;
           ok = wait(C::B_KF + sl, nt / C::NK);
           const uint64_t dk = dk0 + (uint64_t)((sl * C::T_BYTES) >> 4);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (t >= tiles || !ok) continue;
-            const int sb = ns[t] & 1;
-            if (ns[t] >= 2) ok = wait(C::B_O + 2 * t + sb, ns[t] / 2 - 1);  // (the P there has been multiplied)
-            if (!ok) continue;
+#pragma unroll 1
+          for (int t = 0; t < tiles && ok; ++t) {
+            const int ns = t ? ns1 : ns0, sb = ns & 1;
+            if (ns >= 2) ok = wait(C::B_O + 2 * t + sb, ns / 2 - 1);  // (the P there has been multiplied)
+            if (!ok) break;
             fence_after();
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               mma_ss_w(tmem + C::S_COL + (2 * t + sb) * kN, dq0 + (uint64_t)((t * C::Q_TILE + (kk >> 2) * C::QBLK + (kk & 3) * 32) >> 4),
                        dk + (uint64_t)(((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4), id, kk > 0);
             mma_commit_w(bar(C::B_S + 2 * t + sb));
-            ++ns[t];
+            if (t) ++ns1;
+            else ++ns0;
           }
           if (ok) mma_commit_w(bar(C::B_KE + sl));
         }
       }
-      left -= n;
-      off = 0;
-      if (left > 0) w.next();
     }
     mma_commit_w(bar(C::B_DRAIN));
     drain_wait(bar(C::B_DRAIN), 0);
   } else if (warp == 2) {
     // ------------------------------------------------------------------ O += P V
-    int off = w.seek(run.seq, run.unit);
     const uint32_t id = idesc_f16(0, 128, D, 0, 1);  // V is MN-major
     const uint64_t dv0 = sdesc_sw128(sV, C::BLK, 1024);
     bool ok = true;
-    long long left = run.f1 - run.f0;
-    int nt = 0, ns[2] = {0, 0}, seg[2] = {0, 0};
-    while (left > 0 && ok) {
-      const int n = (int)min((long long)(w.units() - off), left);
-      if (w.nt > 0) {
-        const int tiles = tiles_of(w);
+    int nt = 0, ns0 = 0, ns1 = 0, seg0 = 0, seg1 = 0;
+    while (volatile Item *const x = ok ? next_item() : nullptr) {
+      const int flags = x->flags, n = x->n, tiles = flags & kTwo ? 2 : 1;
+      done_item();
+      if (flags & kTiles) {
         for (int m = 0; m < n && ok; ++m, ++nt) {
           const int sl = nt % C::NV;
           ok = wait(C::B_VF + sl, nt / C::NV);
           const uint64_t dv = dv0 + (uint64_t)((sl * C::T_BYTES) >> 4);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (t >= tiles || !ok) continue;
-            const int sb = ns[t] & 1;
-            ok = wait(C::B_P + 2 * t + sb, ns[t] / 2);
-            if (ok && m == 0 && seg[t] > 0) ok = wait(C::B_OE + t, seg[t] - 1);
-            if (!ok) continue;
+#pragma unroll 1
+          for (int t = 0; t < tiles && ok; ++t) {
+            const int ns = t ? ns1 : ns0, sb = ns & 1;
+            ok = wait(C::B_P + 2 * t + sb, ns / 2);
+            if (ok && m == 0 && (t ? seg1 : seg0) > 0) ok = wait(C::B_OE + t, (t ? seg1 : seg0) - 1);
+            if (!ok) break;
             fence_after();
 #pragma unroll
             for (int kk = 0; kk < kN / 16; ++kk)
               mma_ts_w(tmem + t * D, tmem + C::S_COL + (2 * t + sb) * kN + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), id,
                        (m > 0 || kk > 0) ? 1u : 0u);
             mma_commit_w(bar(C::B_O + 2 * t + sb));
-            ++ns[t];
+            if (t) ++ns1;
+            else ++ns0;
           }
           if (ok) mma_commit_w(bar(C::B_VE + sl));
         }
-        for (int t = 0; t < tiles; ++t) ++seg[t];
+        ++seg0;
+        if (tiles > 1) ++seg1;
       }
-      left -= n;
-      off = 0;
-      if (left > 0) w.next();
     }
     mma_commit_w(bar(C::B_DRAIN + 1));
     drain_wait(bar(C::B_DRAIN + 1), 0);
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp == 3) {
+    // ------------------------------------------------------------------ items
+    int off = run_off;
+    long long left = run.f1 - run.f0;
+    for (bool ok = true; ok; ++it) {
+      ok = it < kItems || wait(C::B_IE + it % kItems, it / kItems - 1);
+      if (!ok) break;
+      volatile Item *const x = items + it % kItems;
+      const int units = w.units(), n = (int)min((long long)(units - off), left);
+      if (lane == 0) {
+        if (left > 0) {
+          x->s = w.s; x->head = w.head; x->q0 = w.q0; x->q_len = w.q_len; x->len = w.len; x->r0 = w.r0; x->r1 = w.r1;
+          x->split = p.splits > 1 ? w.qt % p.splits * C::NC : 0;
+          x->tile = w.t0 + off; x->n = n; x->lo = w.lo; x->hi = w.hi;
+          const int columns = p.splits > 1 ? b.group - w.qt % p.splits * C::NC : (w.r1 - w.r0) * b.group;
+          x->flags = (w.nt > 0 ? kTiles : 0) | (off == 0 && n == units ? kWhole : 0) | (off == 0 ? kFirst : 0) | (columns > L ? kTwo : 0);
+        } else {
+          x->flags = kEnd;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::B_IF + it % kItems));
+      if (left <= 0) break;
+      left -= n;
+      if (left == 0 && lane == 0) {
+        // an item that this CTA begins and others end
+        if (w.nt > 0 && off == 0 && n < units) open_item(p, run, w, units - n);
+        else no_item(p);
+      }
+      off = 0;
+      if (left > 0) w.next();
+    }
+    if (left > 0 && lane == 0) no_item(p);  // (a wait gave up)
+  } else {
     // ------------------------------------------------------------------ bytes to fp16
-    int off = w.seek(run.seq, run.unit);
     const int tid = threadIdx.x - 128;
-    constexpr int PER = D / 16, UNITS = kN * PER / 128;  // 16-byte pieces of a row; of a thread
+    constexpr int PER = D / 16, UNITS = kN * PER / kTurners;  // 16-byte pieces of a row; of a thread
     const int log2_page = min(p.a.log2_page, 6), npt = kN >> log2_page;
     bool ok = true;
-    long long left = run.f1 - run.f0;
     int nt = 0;
-    while (left > 0 && ok) {
-      const int n = (int)min((long long)(w.units() - off), left);
-      if (w.nt > 0) {
+    while (volatile Item *const x = ok ? next_item() : nullptr) {
+      const int flags = x->flags, n = x->n, tile = x->tile, lo = x->lo, hi = x->hi;
+      done_item();
+      if (flags & kTiles) {
         for (int m = 0; m < n && ok; ++m, ++nt) {
-          const int j0 = (w.t0 + off + m) * kN, sb = nt % C::NB, sc = nt % kScales;
-          const bool inside = j0 >= w.lo && j0 + kN <= w.hi;
-          ok = wait(C::B_SC + sc, nt / kScales);
-          float kref = 0.f, vref = 0.f;
-          for (int i = 0; ok && i < npt; ++i) {
-            kref = fmaxf(kref, scales[sc * 4 + i].x);
-            vref = fmaxf(vref, scales[sc * 4 + i].y);
-          }
-          // one operand: its bytes, the slot of the fp16 tile, the scale of a page against the tile's
-          auto turn = [&](uint32_t from, uint32_t to, bool values) {
+          const int j0 = (tile + m) * kN, sb = nt % C::NB, sc = nt % kScales;
+          const bool inside = j0 >= lo && j0 + kN <= hi;
+          if (npt > 1) ok = wait(C::B_SC + sc, nt / kScales);
+          // keys, then values (one body: the loops of all roles share the SM's instruction cache, which holds no more)
+#pragma unroll 1
+          for (int v = 0; v < 2 && ok; ++v) {
+            const int to_slot = nt % C::NK, full = C::B_BKF + 2 * C::NB * v + sb, turned = C::B_KF + 2 * C::NK * v + to_slot;
+            ok = wait(full, nt / C::NB);
+            if (ok && nt >= C::NK) ok = wait(turned + C::NK, nt / C::NK - 1);
+            if (!ok) break;
+            const uint32_t from = sBK + (C::NB * v + sb) * C::B_BYTES, to = sK + (C::NK * v + to_slot) * C::T_BYTES;
+            // (rows of D bytes, 16-byte pieces swizzled by the row; eight lanes have four pieces of each of two
+            // rows, at width 128 the other half of the second one: no two of them then share a bank, neither
+            // here nor where they write)
+            const int r = 2 * (tid >> 3) + (tid >> 2 & 1);
+            auto piece = [&](int i) { return (tid & 3) + (D == 128 ? ((tid >> 2 & 1) ^ (i & 1)) * 4 : 0); };
+            uint32_t q[UNITS][4];
+#pragma unroll
+            for (int i = 0; i < UNITS; ++i)
+              lds_v4(from + r * D + ((D == 128 ? piece(i) ^ (r & 7) : piece(i) ^ (r >> 1 & 3)) << 4), q[i][0], q[i][1], q[i][2], q[i][3]);
+            const bool in = inside || (j0 + r >= lo && j0 + r < hi);
+            uint32_t by = 0x3c003c00u;  // the page's scale against the tile's, the largest of its pages'
+            if (npt > 1) {
+              const float *x = reinterpret_cast<const float *>(scales + sc * 4) + v;
+              float top = 0.f;
+              for (int i = 0; i < npt; ++i) top = fmaxf(top, x[2 * i]);
+              const __half2 f = __float2half2_rn(x[2 * (r >> log2_page)] * rcp(top));
+              by = *reinterpret_cast<const uint32_t *>(&f);
+            }
 #pragma unroll
             for (int i = 0; i < UNITS; ++i) {
-              const int x = tid + 128 * i, r = x / PER, u = x % PER;
-              uint32_t q[4];
-              // (rows of D bytes, 16-byte pieces swizzled by the row)
-              lds_v4(from + r * D + ((D == 128 ? u ^ (r & 7) : u ^ (r >> 1 & 3)) << 4), q[0], q[1], q[2], q[3]);
-              const bool in = inside || (j0 + r >= w.lo && j0 + r < w.hi);
               uint32_t h[8];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                h[2 * e] = fp16_of(q[e]);
-                h[2 * e + 1] = fp16_of(q[e] >> 16);
+                h[2 * e] = fp16_of(q[i][e]);
+                h[2 * e + 1] = fp16_of(q[i][e] >> 16);
               }
               if (npt > 1) {
-                const float2 s = scales[sc * 4 + (r >> log2_page)];
-                const float f = values ? s.y / vref : s.x / kref;
-                const __half2 by = __float2half2_rn(f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[e] = scaled(h[e], *reinterpret_cast<const uint32_t *>(&by));
+                for (int e = 0; e < 8; ++e) h[e] = scaled(h[e], by);
               }
               if (!in) {  // (slots that hold no key of the item)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) h[e] = 0;
               }
-              const uint32_t at = to + (u >> 2) * C::BLK + r * 128;
-              const int c = 2 * (u & 3);
+              const uint32_t at = to + (piece(i) >> 2) * C::BLK + r * 128;
+              const int c = 2 * (piece(i) & 3);
               sts_v4(at + (((c) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
               sts_v4(at + (((c + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
             }
-          };
-          const int ks = nt % C::NK, vs = nt % C::NV;
-          if (ok) ok = wait(C::B_BKF + sb, nt / C::NB);
-          if (ok && nt >= C::NK) ok = wait(C::B_KE + ks, nt / C::NK - 1);
-          if (!ok) break;
-          turn(sBK + sb * C::B_BYTES, sK + ks * C::T_BYTES, false);
-          fence_proxy_async_smem();
-          mbar_arrive(bar(C::B_BKE + sb));
-          mbar_arrive(bar(C::B_KF + ks));
-          ok = wait(C::B_BVF + sb, nt / C::NB);
-          if (ok && nt >= C::NV) ok = wait(C::B_VE + vs, nt / C::NV - 1);
-          if (!ok) break;
-          turn(sBV + sb * C::B_BYTES, sV + vs * C::T_BYTES, true);
-          fence_proxy_async_smem();
-          mbar_arrive(bar(C::B_BVE + sb));
-          mbar_arrive(bar(C::B_VF + vs));
+            fence_proxy_async_smem();
+            mbar_arrive(bar(full + C::NB));
+            mbar_arrive(bar(turned));
+          }
         }
       }
-      left -= n;
-      off = 0;
-      if (left > 0) w.next();
     }
-  } else if (warp >= 8) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     // ------------------------------------------------------------------ softmax / output
-    const int t = (warp - 8) / 4, r = (threadIdx.x - 256) % 128;  // query tile and row of it
+    const int t = (warp - 12) / 4, r = (threadIdx.x - 384) % 128;  // query tile and row of it
     const uint32_t t_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t o_addr = t_addr + t * D, s_addr = t_addr + C::S_COL + 2 * t * kN;
     const int log2_page = min(p.a.log2_page, 6), npt = kN >> log2_page;
-    int off = w.seek(run.seq, run.unit);
     int nt = 0, ns = 0;  // tiles; the ones of this query tile
     bool ok = true;
-    long long left = run.f1 - run.f0;
-    while (left > 0 && ok) {
-      const int n = (int)min((long long)(w.units() - off), left), units = w.units();
-      const bool whole = off == 0 && n == units, live = t < tiles_of(w);
-      int row = 0, head = 0;
-      const int c = t * L + r;
-      const bool have = live && r < L && column_of(p, C::NC, w, c, row, head);
-      const long long at = (long long)(w.q0 + row) * b.h_q + head;
-      if (w.nt == 0) {
-        if (have) {  // a row that sees no key
-          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(b.out) + at * D);
+    const int wr = 32 * (warp & 3);  // first row of the warp
+    // the query row and head of column c of an item; false where there is none
+    auto place = [&](volatile Item *x, int c, int &row, int &head) {
+      if (p.splits > 1) {
+        const int h = x->split + c;
+        row = x->r0;
+        head = x->head * b.group + h;
+        return h < b.group;
+      }
+      const int i = c * p.magic >> 16;
+      row = x->r0 + i;
+      head = x->head * b.group + c - i * b.group;
+      return row < x->r1;
+    };
+    while (volatile Item *const x = next_item()) {
+      const bool live = t == 0 || (x->flags & kTwo) != 0;
+      const int c = t * L + r, n = x->n;
+      if (!(x->flags & kTiles)) {
+        int row, head;
+        if (live && r < L && place(x, c, row, head)) {  // a row that sees no key
+          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(b.out) + ((long long)(x->q0 + row) * b.h_q + head) * D);
           for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
-          if (b.lse) b.lse[(long long)head * b.total_q + w.q0 + row] = -INFINITY;
+          if (b.lse) b.lse[(long long)head * b.total_q + x->q0 + row] = -INFINITY;
         }
       } else if (!live) {
         nt += n;
       } else {
-        // the row's query, in fp16 over a power of two, where the product finds it
-        float down = 1.f;
+        // The queries of this warp's rows, in fp16 over a power of two, where the product finds them: PL lanes
+        // have a row, so that a load takes whole rows.
         {
-          const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const T *>(b.q) + at * D);
-          float up = 1.f;
-          if constexpr (BF16) {
-            uint32_t top = 0;
-            if (have) {
-#pragma unroll
-              for (int i = 0; i < D / 8; ++i) {
-                const uint4 x = __ldg(q + i);
-                top = __vmaxu2(__vmaxu2(top, x.x & 0x7fff7fffu), __vmaxu2(x.y & 0x7fff7fffu, __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-              }
+          constexpr int PL = D / 8, AT_ONCE = 32 / PL, STEPS = 32 / AT_ONCE, FLY = 4;
+          const int sub = lane / PL, piece = lane % PL;
+    #pragma unroll 1
+          for (int i0 = 0; i0 < STEPS; i0 += FLY) {
+            uint4 y4[FLY];
+    #pragma unroll
+            for (int k = 0; k < FLY; ++k) {
+              const int r2 = wr + (i0 + k) * AT_ONCE + sub;
+              int row2 = 0, head2 = 0;
+              y4[k] = make_uint4(0, 0, 0, 0);
+              if (r2 < L && place(x, t * L + r2, row2, head2))
+                y4[k] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(b.q) + ((long long)(x->q0 + row2) * b.h_q + head2) * D) + piece);
             }
-            top = max(top & 0xffffu, top >> 16);
-            const int ex = min(max((int)(top >> 7) - 127, -100), 127);
-            up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
-            down = __uint_as_float((uint32_t)(127 - 7 + ex) << 23);
-          }
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (have) x = __ldg(q + i);
-            if constexpr (BF16) {
-              uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 f = unpack2(y[e], 1);
-                y[e] = pack2(f.x * up, f.y * up, 0);
+    #pragma unroll
+            for (int k = 0; k < FLY; ++k) {
+              const int r2 = wr + (i0 + k) * AT_ONCE + sub;
+              if constexpr (BF16) {
+                uint32_t y[4] = {y4[k].x, y4[k].y, y4[k].z, y4[k].w};
+                uint32_t top = __vmaxu2(__vmaxu2(y[0] & 0x7fff7fffu, y[1] & 0x7fff7fffu), __vmaxu2(y[2] & 0x7fff7fffu, y[3] & 0x7fff7fffu));
+    #pragma unroll
+                for (int o = PL / 2; o > 0; o /= 2) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+                top = max(top & 0xffffu, top >> 16);
+                const int ex = min(max((int)(top >> 7) - 127, -100), 127);
+                const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
+                if (piece == 0) downs[t * 128 + r2] = __uint_as_float((uint32_t)(127 - 7 + ex) << 23);
+    #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float2 f = unpack2(y[e], 1);
+                  y[e] = pack2(f.x * up, f.y * up, 0);
+                }
+                y4[k] = make_uint4(y[0], y[1], y[2], y[3]);
               }
-              x = make_uint4(y[0], y[1], y[2], y[3]);
+              sts_v4(sQ + t * C::Q_TILE + (piece >> 3) * C::QBLK + r2 * 128 + (((piece & 7) ^ (r2 & 7)) << 4), y4[k].x, y4[k].y, y4[k].z, y4[k].w);
             }
-            sts_v4(sQ + t * C::Q_TILE + (i >> 3) * C::QBLK + r * 128 + (((i & 7) ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
           }
           fence_proxy_async_smem();
           mbar_arrive(bar(C::B_Q + t));
+          __syncwarp();
         }
+        const float down = BF16 ? downs[t * 128 + r] : 1.f;
         int vlo = 0, vhi = 0x7fffffff;  // the row's keys (of a lane without a row, which nobody reads: all)
-        if (have) visible_range(row, w.len - w.q_len, w.len, b.causal, b.window, vlo, vhi);
+        {
+          int row, head;
+          if (r < L && place(x, c, row, head))
+            visible_range(row, x->len - x->q_len, x->len, b.causal, b.window, vlo, vhi);
+        }
+        const int tile = x->tile;
         const float sl2 = b.scale_log2 * down;
         float m_ref = -INFINITY, l = 0.f;
         for (int m = 0; m < n; ++m, ++nt, ++ns) {
-          const int kb = (w.t0 + off + m) * kN, sb = ns & 1, sc = nt % kScales;
+          const int kb = (tile + m) * kN, sb = ns & 1, sc = nt % kScales;
           ok = wait(C::B_S + 2 * t + sb, ns / 2) && wait(C::B_SC + sc, nt / kScales);
           if (!ok) break;
           fence_after();
@@ -417,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             vref = fmaxf(vref, scales[sc * 4 + i].y);
           }
           vref = fminf(fmaxf(vref, 0x1p-100f), 0x1p120f);  // (a scale of zero or no number: of no weight)
-          const float c1 = fmaxf(kref * sl2, 1e-37f), lv = lg2(vref), over = 1.f / vref;
+          const float c1 = fmaxf(kref * sl2, 1e-37f), lv = lg2(vref), over = rcp(vref);
           tmem_ld_wait();
           pin(v);
           if (!__all_sync(0xffffffffu, elo <= 0 && ehi >= kN)) {
@@ -485,51 +577,67 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ok = wait(C::B_O + 2 * t + ((ns - 1) & 1), (ns - 1) / 2);
         if (!ok) break;
         fence_after();
+        // O through shared memory, 64 bytes of a row at a time, so that stores take whole rows: a lane writes its
+        // row's in 16-byte pieces, swizzled by the row, and reads pieces of neighbouring lanes' rows
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        float *part = p.part + (2ll * blockIdx.x + (off == 0 ? 1 : 0)) * C::PART;
+        float *part = p.part + (2ll * blockIdx.x + (x->flags & kFirst ? 1 : 0)) * C::PART;
+        const uint32_t stage = base + C::OFF_STAGE + (warp - 12) * 2048;
+        auto spread = [&](uint8_t *to, long long pitch, int at_col, bool by_row) {
+          // four lanes have a row's 64 bytes, eight rows at a time
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r2 = 8 * k + lane / 4, piece = lane % 4, c2 = t * L + wr + r2;
+            int row2, head2;
+            if (wr + r2 >= L || !place(x, c2, row2, head2)) continue;
+            uint32_t y[4];
+            lds_v4(stage + r2 * 64 + ((piece ^ (r2 >> 1 & 3)) << 4), y[0], y[1], y[2], y[3]);
+            const long long i2 = by_row ? (long long)(x->q0 + row2) * b.h_q + head2 : c2;
+            *reinterpret_cast<uint4 *>(to + i2 * pitch + at_col + 16 * piece) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+          __syncwarp();
+        };
+        auto put = [&](int e, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
+          sts_v4(stage + lane * 64 + ((e ^ (lane >> 1 & 3)) << 4), x0, x1, x2, x3);
+        };
 #pragma unroll 1
         for (int i = 0; i < D; i += 32) {
           uint32_t o[32];
           __syncwarp();
           tmem_ld32(o_addr + i, o);
           tmem_ld_wait_for(o);
-          if (!have) continue;
-          if (whole) {
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(b.out) + at * D + i);
+          if (x->flags & kWhole) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               pk[e] = pack2(l == 0.f ? 0.f : __uint_as_float(o[2 * e]) * inv, l == 0.f ? 0.f : __uint_as_float(o[2 * e + 1]) * inv, BF16);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) put(e, pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+            spread(static_cast<uint8_t *>(b.out), 2 * D, 2 * i, true);
           } else {
-            float2 *dst = reinterpret_cast<float2 *>(part + (long long)c * D + i);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) dst[e] = make_float2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) put(e, o[16 * x + 4 * e], o[16 * x + 4 * e + 1], o[16 * x + 4 * e + 2], o[16 * x + 4 * e + 3]);
+              spread(reinterpret_cast<uint8_t *>(part), 4 * D, 4 * (i + 16 * x), false);
+            }
           }
         }
         fence_before();
         mbar_arrive(bar(C::B_OE + t));
-        if (have) {
+        int row, head;
+        if (r < L && place(x, c, row, head)) {
           const float ref = m_ref - kLift;  // (minus infinity where no key was seen: l is 0 then)
-          if (!whole) {
+          if (!(x->flags & kWhole)) {
             part[C::NC * D + c] = ref;
             part[C::NC * D + C::NC + c] = l;
           } else if (b.lse) {
-            b.lse[(long long)head * b.total_q + w.q0 + row] = l == 0.f ? -INFINITY : (ref + lg2(l)) * kLn2;
+            b.lse[(long long)head * b.total_q + x->q0 + row] = l == 0.f ? -INFINITY : (ref + lg2(l)) * kLn2;
           }
         }
       }
-      left -= n;
-      if (left == 0 && threadIdx.x == 256) {
-        // an item that this CTA begins and others end
-        const bool open = w.nt > 0 && off == 0 && n < units;
-        p.rec[blockIdx.x] = open ? open_item(run, w, units - n) : make_int4(-1, 0, 0, 0);
-      }
-      off = 0;
-      if (left > 0) w.next();
+      done_item();
     }
-    if (!ok && threadIdx.x == 256) p.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
   fence_before();
   __syncthreads();
@@ -543,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 size_t pages_rows_workspace(int d, int num_sms) {
   const size_t part = d == 64 ? RowCfg<64>::PART : RowCfg<128>::PART;
-  return (((size_t)num_sms * sizeof(int4) + 255) & ~(size_t)255) + 2 * (size_t)num_sms * part * sizeof(float);
+  return (((size_t)num_sms * 2 * sizeof(int4) + 255) & ~(size_t)255) + 2 * (size_t)num_sms * part * sizeof(float);
 }
 
 cudaError_t pages_rows_forward(const PagesAttnParams &a, void *workspace, int num_sms, cudaStream_t st) {
@@ -559,8 +667,9 @@ cudaError_t pages_rows_forward(const PagesAttnParams &a, void *workspace, int nu
     p.a = a;
     p.splits = group > 128 ? (group + C::NC - 1) / C::NC : 1;
     p.rows = group > 128 ? 1 : 2 * L / group;
+    p.magic = magic_of(group);
     p.rec = static_cast<int4 *>(workspace);
-    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + (((size_t)num_sms * sizeof(int4) + 255) & ~(size_t)255));
+    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + (((size_t)num_sms * 2 * sizeof(int4) + 255) & ~(size_t)255));
     const bool bf = a.p.dtype == VLF_BF16;
     const void *kern = bf ? (const void *)pages_rows_kernel<D, true> : (const void *)pages_rows_kernel<D, false>;
     const void *join = bf ? (const void *)pages_join_kernel<D, C::NC, kN, true> : (const void *)pages_join_kernel<D, C::NC, kN, false>;

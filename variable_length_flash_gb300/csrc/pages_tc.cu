@@ -100,19 +100,6 @@ __device__ __forceinline__ bool any_of_128(bool x) {
       : "memory");
   return r != 0;
 }
-template <int N> __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t *r) {
-  static_assert(N == 4 || N == 8 || N == 16, "columns");
-  if constexpr (N == 4) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr) : "memory");
-  } else if constexpr (N == 8) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr) : "memory");
-  } else {
-    tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(r));
-  }
-}
 // NC columns.
 template <int NC> __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[NC]) {
   if constexpr (NC <= 16) {
@@ -178,7 +165,7 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
   const uint32_t tmem = *tmem_holder;
 
   if (!run.any) {
-    if (threadIdx.x == 0) p.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (threadIdx.x == 0) no_item(p);
   } else if (warp == 4) {
     // ------------------------------------------------------------------ pages
     int off = w.seek(run.seq, run.unit);
@@ -618,13 +605,13 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
       left -= n;
       if (left == 0 && tid == 0) {
         // an item that this CTA begins and others end
-        const bool open = w.nt > 0 && off == 0 && n < units;
-        p.rec[blockIdx.x] = open ? open_item(run, w, units - n) : make_int4(-1, 0, 0, 0);
+        if (w.nt > 0 && off == 0 && n < units) open_item(p, run, w, units - n);
+        else no_item(p);
       }
       off = 0;
       if (left > 0) w.next();
     }
-    if (bad && tid == 0) p.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (bad && tid == 0) no_item(p);
   }
   fence_before();
   __syncthreads();
@@ -662,7 +649,7 @@ size_t pages_tc_workspace(int max_q, int group, int d, int num_sms) {
   with(d, columns(max_q, group), [&](auto dd, auto nc) {
     using C = Cfg<decltype(dd)::value, decltype(nc)::value>;
     const size_t grid = (size_t)C::CTAS * num_sms;
-    n = ((grid * sizeof(int4) + 255) & ~(size_t)255) + 2 * grid * C::PART * sizeof(float);
+    n = ((grid * 2 * sizeof(int4) + 255) & ~(size_t)255) + 2 * grid * C::PART * sizeof(float);
   });
   return n;
 }
@@ -681,9 +668,10 @@ cudaError_t pages_tc_forward(const PagesAttnParams &a, void *workspace, int num_
     p.a = a;
     p.splits = group > NC ? (group + NC - 1) / NC : 1;
     p.rows = group > NC ? 1 : NC / group;
+    p.magic = magic_of(group);
     const size_t grid = (size_t)C::CTAS * num_sms;
     p.rec = static_cast<int4 *>(workspace);
-    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + ((grid * sizeof(int4) + 255) & ~(size_t)255));
+    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + ((grid * 2 * sizeof(int4) + 255) & ~(size_t)255));
     const bool bf = a.p.dtype == VLF_BF16;
     const void *kern = bf ? (const void *)pages_tc_kernel<D, NC, true> : (const void *)pages_tc_kernel<D, NC, false>;
     const void *join = bf ? (const void *)pages_join_kernel<D, NC, kKeys, true> : (const void *)pages_join_kernel<D, NC, kKeys, false>;

@@ -17,10 +17,14 @@ constexpr float kLn2 = 0.69314718055994531f;
 struct TcParams {
   PagesAttnParams a;
   float *part;  // [2 grid][columns (D + 2)]
-  int4 *rec;    // [grid] {sequence, kv head, query tile, last CTA} of the item that a CTA begins and leaves open; -1: none
+  int4 *rec;    // [grid][2] {sequence, kv head, query tile, units behind the run's end} of the item that a CTA begins and
+                // leaves open (-1: none); then {units of the call (64 bits), CTAs with a run}
   int rows;     // query rows of a query tile
   int splits;   // query tiles of a row (a group with more heads than columns), else 1
+  int magic;    // magic_of(group)
 };
+// c / group is c * this >> 16 for c < 256 (c * group < 2^16); where there are more heads it is not asked for.
+inline int magic_of(int group) { return 65536 / group + 1; }
 
 // The key tiles (of KEYS keys) of the items from one on, in order.
 template <int KEYS> struct Walk {
@@ -99,8 +103,9 @@ __device__ __forceinline__ bool column_of(const TcParams &p, int nc, const W &w,
     head = w.head * group + h;
     return h < group;
   }
-  row = w.r0 + c / group;
-  head = w.head * group + c % group;
+  const int r = c * p.magic >> 16;
+  row = w.r0 + r;
+  head = w.head * group + c - r * group;
   return row < w.r1;
 }
 
@@ -108,6 +113,20 @@ __device__ __forceinline__ bool column_of(const TcParams &p, int nc, const W &w,
 template <int N> __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+// N consecutive columns (no wait).
+template <int N> __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t *r) {
+  static_assert(N == 4 || N == 8 || N == 16, "columns");
+  if constexpr (N == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr) : "memory");
+  } else if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr) : "memory");
+  } else {
+    tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(r));
+  }
 }
 // A CTA's run of units.
 struct Run {
@@ -177,10 +196,12 @@ __device__ __forceinline__ Run run_of(const TcParams &p, long long *red) {
   r.unit = start[1];
   return r;
 }
-// The record of an item with `rest` units behind a run's end, which the run begins.
-template <typename W> __device__ __forceinline__ int4 open_item(const Run &r, const W &w, int rest) {
-  return make_int4(w.s, w.head, w.qt, (int)(((r.f1 + rest) * r.grid - 1) / r.total));
+// The record of an item that has `rest` units behind the end of a run that begins it; none.
+template <typename W> __device__ __forceinline__ void open_item(const TcParams &p, const Run &r, const W &w, int rest) {
+  p.rec[2 * blockIdx.x] = make_int4(w.s, w.head, w.qt, rest);
+  p.rec[2 * blockIdx.x + 1] = make_int4((int)(uint32_t)r.total, (int)(r.total >> 32), (int)r.grid, 0);
 }
+__device__ __forceinline__ void no_item(const TcParams &p) { p.rec[2 * blockIdx.x] = make_int4(-1, 0, 0, 0); }
 
 // Joins the parts of the item that CTA blockIdx.x of the launch before began and others ended: out = sum_i f_i O_i /
 // sum_i f_i l_i with f_i = 2^(reference_i - the largest).  A warp has a column of the item (grid y: runs of them),
@@ -194,7 +215,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) pages_join_kernel(const TcPar
   constexpr int PART = NC * (D + 2), FLY = 8;
   pdl_wait();
   pdl_trigger();
-  const int4 rec = p.rec[blockIdx.x];
+  const int4 rec = p.rec[2 * blockIdx.x];
   const int c = blockIdx.y * kJoinWarps + threadIdx.x / 32, lane = threadIdx.x % 32;
   if (rec.x < 0 || c >= NC) return;
   Walk<KEYS> w(p);
@@ -204,7 +225,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) pages_join_kernel(const TcPar
   w.item();
   int row, head;
   if (!column_of(p, NC, w, c, row, head)) return;
-  const int n = rec.w - blockIdx.x + 1;
+  // the last CTA with a part: the one that has the item's last unit
+  const int4 of = p.rec[2 * blockIdx.x + 1];
+  const long long total = (long long)(uint32_t)of.x | (long long)of.y << 32, grid = of.z;
+  const long long end = total * (blockIdx.x + 1) / grid + rec.w;
+  const int n = (int)((end * grid - 1) / total) - (int)blockIdx.x + 1;
   auto part = [&](int i) { return p.part + (2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * PART; };
   float top = -INFINITY;
   for (int i = lane; i < n; i += 32) {
