@@ -494,7 +494,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m_ref = -INFINITY, l = 0.f;
         for (int m = 0; m < n; ++m, ++nt, ++ns) {
           const int kb = (tile + m) * kN, sb = ns & 1, sc = nt % kScales;
-          ok = wait(C::B_S + 2 * t + sb, ns / 2) && wait(C::B_SC + sc, nt / kScales);
+          // (the scales are there long before S.  Not so for an item's first tile, behind others without rows for this
+          // query tile: S tells then that the barrier is in this tile's phase)
+          ok = m > 0 || wait(C::B_S + 2 * t + sb, ns / 2);
+          ok = ok && wait(C::B_SC + sc, nt / kScales);
+          float kref = 0.f, vref = 0.f;
+          for (int i = 0; i < npt; ++i) {
+            kref = fmaxf(kref, scales[sc * 4 + i].x);
+            vref = fmaxf(vref, scales[sc * 4 + i].y);
+          }
+          vref = fminf(fmaxf(vref, 0x1p-100f), 0x1p120f);  // (a scale of zero or no number: of no weight)
+          const float c1 = fmaxf(kref * sl2, 1e-37f), lv = lg2(vref), over = rcp(vref);
+          ok = ok && wait(C::B_S + 2 * t + sb, ns / 2);
           if (!ok) break;
           fence_after();
           const uint32_t s_at = s_addr + sb * kN;
@@ -503,19 +514,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           tmem_ld32_at(s_at, v, 0);
           tmem_ld32_at(s_at + 32, v, 32);
-          float kref = 0.f, vref = 0.f;
-          for (int i = 0; i < npt; ++i) {
-            kref = fmaxf(kref, scales[sc * 4 + i].x);
-            vref = fmaxf(vref, scales[sc * 4 + i].y);
-          }
-          vref = fminf(fmaxf(vref, 0x1p-100f), 0x1p120f);  // (a scale of zero or no number: of no weight)
-          const float c1 = fmaxf(kref * sl2, 1e-37f), lv = lg2(vref), over = rcp(vref);
           tmem_ld_wait();
           pin(v);
           if (!__all_sync(0xffffffffu, elo <= 0 && ehi >= kN)) {
+            // (a bit for each key that is seen)
+            const int first = max(0, min(elo, kN)), end = max(first, min(ehi, kN));
+            const uint64_t upto = end >= 64 ? ~0ull : (1ull << end) - 1, from = first >= 64 ? ~0ull : (1ull << first) - 1;
+            const uint32_t see0 = (uint32_t)(upto & ~from), see1 = (uint32_t)((upto & ~from) >> 32);
 #pragma unroll
             for (int e = 0; e < kN; ++e)
-              if (e < elo || e >= ehi) v[e] = 0xff800000u;
+              if (!((e < 32 ? see0 : see1) >> (e & 31) & 1)) v[e] = 0xff800000u;
           }
           float m8[8];
 #pragma unroll
@@ -582,18 +590,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         float *part = p.part + (2ll * blockIdx.x + (x->flags & kFirst ? 1 : 0)) * C::PART;
         const uint32_t stage = base + C::OFF_STAGE + (warp - 12) * 2048;
-        auto spread = [&](uint8_t *to, long long pitch, int at_col, bool by_row) {
-          // four lanes have a row's 64 bytes, eight rows at a time
+        const bool all = (x->flags & kWhole) != 0;
+        // four lanes have a row's 64 bytes, eight rows at a time: where this lane's four rows go (-1: nowhere)
+        long long to[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r2 = 8 * k + lane / 4, c2 = t * L + wr + r2;
+          int row2, head2;
+          to[k] = -1;
+          if (wr + r2 < L && place(x, c2, row2, head2))
+            to[k] = (all ? ((long long)(x->q0 + row2) * b.h_q + head2) * (2 * D) : (long long)c2 * (4 * D)) + 16 * (lane % 4);
+        }
+        uint8_t *const out = all ? static_cast<uint8_t *>(b.out) : reinterpret_cast<uint8_t *>(part);
+        auto spread = [&](int at_col) {
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int r2 = 8 * k + lane / 4, piece = lane % 4, c2 = t * L + wr + r2;
-            int row2, head2;
-            if (wr + r2 >= L || !place(x, c2, row2, head2)) continue;
+            const int r2 = 8 * k + lane / 4;
             uint32_t y[4];
-            lds_v4(stage + r2 * 64 + ((piece ^ (r2 >> 1 & 3)) << 4), y[0], y[1], y[2], y[3]);
-            const long long i2 = by_row ? (long long)(x->q0 + row2) * b.h_q + head2 : c2;
-            *reinterpret_cast<uint4 *>(to + i2 * pitch + at_col + 16 * piece) = make_uint4(y[0], y[1], y[2], y[3]);
+            lds_v4(stage + r2 * 64 + ((lane % 4 ^ (r2 >> 1 & 3)) << 4), y[0], y[1], y[2], y[3]);
+            if (to[k] >= 0) *reinterpret_cast<uint4 *>(out + to[k] + at_col) = make_uint4(y[0], y[1], y[2], y[3]);
           }
           __syncwarp();
         };
@@ -606,20 +622,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           tmem_ld32(o_addr + i, o);
           tmem_ld_wait_for(o);
-          if (x->flags & kWhole) {
+          if (all) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               pk[e] = pack2(l == 0.f ? 0.f : __uint_as_float(o[2 * e]) * inv, l == 0.f ? 0.f : __uint_as_float(o[2 * e + 1]) * inv, BF16);
 #pragma unroll
             for (int e = 0; e < 4; ++e) put(e, pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
-            spread(static_cast<uint8_t *>(b.out), 2 * D, 2 * i, true);
+            spread(2 * i);
           } else {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int x2 = 0; x2 < 2; ++x2) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) put(e, o[16 * x + 4 * e], o[16 * x + 4 * e + 1], o[16 * x + 4 * e + 2], o[16 * x + 4 * e + 3]);
-              spread(reinterpret_cast<uint8_t *>(part), 4 * D, 4 * (i + 16 * x), false);
+              for (int e = 0; e < 4; ++e) put(e, o[16 * x2 + 4 * e], o[16 * x2 + 4 * e + 1], o[16 * x2 + 4 * e + 2], o[16 * x2 + 4 * e + 3]);
+              spread(4 * (i + 16 * x2));
             }
           }
         }
@@ -628,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int row, head;
         if (r < L && place(x, c, row, head)) {
           const float ref = m_ref - kLift;  // (minus infinity where no key was seen: l is 0 then)
-          if (!(x->flags & kWhole)) {
+          if (!all) {
             part[C::NC * D + c] = ref;
             part[C::NC * D + C::NC + c] = l;
           } else if (b.lse) {
