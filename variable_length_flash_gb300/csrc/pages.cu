@@ -517,6 +517,125 @@ __global__ void __launch_bounds__(256) fork_end_kernel(const PagesForkParams p) 
   }
 }
 
+// Small calls as one block of 1024 threads, counters and free pages in shared memory: five launches are what the
+// host spends its time on there.
+constexpr int kSmallPages = 4096, kSmallRows = 1024, kSmallEntries = 32768;
+
+// The sum of x over the threads before this one, and over all (1024 threads).
+__device__ __forceinline__ int before_1024(int x, int &all) {
+  __shared__ int red[32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int y = x;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
+  }
+  __syncthreads();
+  if (lane == 31) red[warp] = y;
+  __syncthreads();
+  const int r = red[lane];
+  all = __reduce_add_sync(0xffffffffu, r);
+  return y - x + __reduce_add_sync(0xffffffffu, lane < warp ? r : 0);
+}
+
+__global__ void __launch_bounds__(1024) fork_small_kernel(PagesForkParams p) {
+  extern __shared__ int dyn[];
+  __shared__ int begin[kSmallRows], bad;
+  step_begins();
+  const int t = threadIdx.x, warp = t / 32, lane = t % 32;
+  int *const list = dyn + 3 * p.num_pages;
+  p.outside = dyn;
+  p.whole = dyn + p.num_pages;
+  p.owner = dyn + 2 * p.num_pages;
+  for (int i = t; i < p.num_pages; i += 1024) {
+    p.outside[i] = p.refs[i];
+    p.whole[i] = 0;
+    p.owner[i] = 0x7fffffff;
+  }
+  if (t == 0) bad = 0;
+  __syncthreads();
+  for (int y = warp; y < p.num_in + p.num_out; y += 32) {
+    const int s = y - p.num_in;
+    Row r{y, 0, 0, false};
+    if (s < 0) {
+      r.len = __ldg(p.lens + y);
+      if (r.len < 0 || pages_of(r.len, p.log2_page) > p.max_pages) {
+        if (lane == 0) bad = VLF_ERR_BAD_SEQLENS;
+        continue;
+      }
+    } else {
+      r = row_of(p, s);
+      const int grow = __ldg(p.grow + s);
+      if (lane == 0 && r.parent >= p.num_in) bad = VLF_ERR_BAD_PAGES;
+      if (grow < 0 || (long long)r.len + grow > (long long)p.max_pages << p.log2_page) {
+        if (lane == 0) bad = VLF_ERR_BAD_SEQLENS;
+        continue;
+      }
+    }
+    const int n = min(pages_of(r.len, p.log2_page), p.max_pages);
+    const int32_t *row = p.table + (long long)r.parent * p.max_pages;
+    for (int j = lane; j < n; j += 32) {
+      const int page = __ldg(row + j);
+      if (page < 0 || page >= p.num_pages) bad = VLF_ERR_BAD_PAGES;
+      else if (s < 0) atomicSub(p.outside + page, 1);
+      else if (j < r.whole) atomicAdd(p.whole + page, 1);
+      else atomicMin(p.owner + page, s);
+    }
+  }
+  __syncthreads();
+  // the free pages in order, and where each new row's new pages begin among them
+  int free = 0, need = 0;
+  for (int i0 = 0; i0 < p.num_pages; i0 += 1024) {
+    const int i = i0 + t;
+    const bool in = i < p.num_pages, is = in && held(p, i) == 0;
+    if (in && (p.outside[i] < 0 || p.refs[i] < 0)) bad = VLF_ERR_BAD_PAGES;
+    int all;
+    const int at = free + before_1024(is, all);
+    if (is) list[at] = i;
+    free += all;
+  }
+  bool keeps = false;
+  Row mine{-1, 0, 0, false};
+  int part = -1, more = 0;
+  if (t < p.num_out) {
+    mine = row_of(p, t);
+    part = part_of(p, mine, t, keeps);
+    const long long to = min((long long)mine.len + max(0, __ldg(p.grow + t)), (long long)p.max_pages << p.log2_page);
+    more = pages_of((int)to, p.log2_page) - pages_of(mine.len, p.log2_page) + (part >= 0 && !keeps);
+  }
+  const int at = before_1024(more, need);  // (at most kSmallEntries pages)
+  if (t < p.num_out) begin[t] = at;
+  __syncthreads();
+  const bool ok = bad == 0 && need <= free;
+  if (t == 0) {
+    if (bad) set_error(p.err, bad);
+    *p.left = bad ? (int)0x80000000 : free - need;
+  }
+  if (t < p.num_out) {
+    const bool copy = ok && part >= 0 && !keeps;
+    p.lens_out[t] = ok ? mine.len + __ldg(p.grow + t) : 0;
+    p.src[t] = copy ? part : -1;
+    p.dst[t] = copy ? list[at] : -1;
+  }
+  for (int i = t; i < p.num_pages; i += 1024) {
+    if (!ok) p.refs_out[i] = p.refs[i];
+    else if (const int n = held(p, i)) p.refs_out[i] = n;
+  }
+  if (ok)
+    for (int i = t; i < free; i += 1024) p.refs_out[list[i]] = i < need;
+  for (int s = warp; s < p.num_out; s += 32) {
+    const Row r = row_of(p, s);
+    bool keep;
+    const int page = part_of(p, r, s, keep);
+    const int has = ok ? pages_of(r.len + __ldg(p.grow + s), p.log2_page) : 0, stay = r.whole + (keep ? 1 : 0);
+    const int32_t *row = p.table + (long long)r.parent * p.max_pages;
+    int *out = p.table_out + (long long)s * p.max_pages;
+    for (int j = lane; j < p.max_pages; j += 32)
+      out[j] = j >= has ? -1 : j < r.whole ? __ldg(row + j) : j < stay ? page : list[begin[s] + j - stay];
+  }
+}
+
 // Compact.  Of the U pages in use the ones behind the first U pages move into the free ones among them, the
 // first into the first.
 __global__ void __launch_bounds__(256) compact_count_kernel(const PagesCompactParams p) {
@@ -590,6 +709,48 @@ __global__ void __launch_bounds__(256) compact_end_kernel(const PagesCompactPara
   }
 }
 
+// The same for few pages and entries, as one block: src, dst and order in shared memory.
+__global__ void __launch_bounds__(1024) compact_small_kernel(const PagesCompactParams p) {
+  __shared__ short order[kSmallPages], dst[kSmallPages / 2];
+  step_begins();
+  const int t = threadIdx.x;
+  int used = 0;
+  for (int i0 = 0; i0 < p.num_pages; i0 += 1024) used += __syncthreads_count(i0 + t < p.num_pages && p.refs[i0 + t] > 0);
+  int rank0 = 0, front = 0;
+  for (int i0 = 0; i0 < p.num_pages; i0 += 1024) front += __syncthreads_count(i0 + t < used && p.refs[i0 + t] > 0);
+  for (int i = t; i < p.num_pages / 2; i += 1024) p.src[i] = p.dst[i] = -1;
+  __syncthreads();
+  for (int i0 = 0; i0 < p.num_pages; i0 += 1024) {
+    const int i = i0 + t;
+    const bool in = i < p.num_pages, is = in && p.refs[i] > 0;
+    int all;
+    const int rank = rank0 + before_1024(is, all);  // pages in use before this one
+    rank0 += all;
+    if (!in) continue;
+    order[i] = -1;
+    if (is && i >= used) {
+      order[i] = (short)(rank - front);
+      p.src[rank - front] = i;
+    } else if (!is && i < used) {
+      dst[i - rank] = (short)i;
+      p.dst[i - rank] = i;
+    }
+  }
+  __syncthreads();
+  auto moved = [&](int i) { return order[i] < 0 ? i : (int)dst[order[i]]; };
+  for (int i = t; i < p.num_pages; i += 1024) {
+    const int n = p.refs[i], to = n > 0 ? moved(i) : -1;
+    p.to[i] = to;
+    if (n > 0) p.refs_out[to] = n;
+    if (i >= used) p.refs_out[i] = 0;
+  }
+  for (int i = t; i < (int)p.entries; i += 1024) {
+    const int page = __ldg(p.table + i);
+    p.table_out[i] = page >= 0 && page < p.num_pages && __ldg(p.refs + page) > 0 ? moved(page) : -1;
+  }
+  if (t == 0) *p.used = used;
+}
+
 size_t ints(long long n) { return ((size_t)n * 4 + 255) & ~(size_t)255; }
 int chunks_of(int num_pages) { return (int)(((long long)num_pages + kChunk - 1) / kChunk); }
 }  // namespace
@@ -631,6 +792,13 @@ cudaError_t pages_fork(PagesForkParams p, void *workspace, cudaStream_t st) {
   p.state = take(4);
   void *args[1] = {&p};
   const int rows = p.num_in + p.num_out;
+  if (p.num_pages <= kSmallPages && p.num_out <= kSmallRows && (long long)rows * p.max_pages <= kSmallEntries) {
+    const int bytes = 4 * p.num_pages * (int)sizeof(int);
+    cudaError_t e = set_smem_once((const void *)fork_small_kernel, bytes);
+    if (e == cudaSuccess) e = launch_dependent((const void *)fork_small_kernel, dim3(1), 1024, bytes, st, args);
+    if (e == cudaSuccess) count_launch();
+    return e;
+  }
   auto step = [&](const void *kern, dim3 grid) { return launch_step(kern, grid, 256, st, args); };
   cudaError_t e = step((const void *)fork_begin_kernel, dim3((unsigned)(((long long)max(p.num_pages, 4) + 255) / 256)));
   if (e == cudaSuccess && rows > 0)
@@ -647,6 +815,8 @@ cudaError_t pages_compact(PagesCompactParams p, void *workspace, cudaStream_t st
   p.counts = static_cast<int *>(workspace);
   p.order = reinterpret_cast<int *>(static_cast<char *>(workspace) + ints(p.chunks));
   void *args[1] = {&p};
+  if (p.num_pages <= kSmallPages && p.entries <= kSmallEntries)
+    return launch_step((const void *)compact_small_kernel, dim3(1), 1024, st, args);
   auto step = [&](const void *kern, long long blocks) { return launch_step(kern, dim3((unsigned)blocks), 256, st, args); };
   cudaError_t e = step((const void *)compact_count_kernel, p.chunks);
   if (e == cudaSuccess) e = step((const void *)compact_list_kernel, p.chunks);
