@@ -400,6 +400,34 @@ PyObject *pages_copy(PyObject *const *a) {
   Py_RETURN_TRUE;
 }
 
+// Several int32 outputs of a call from one allocation, each on 256 bytes, in the order they are taken (an allocation
+// costs the host 1.1 us, a fork has six outputs and a workspace): plain tensors that share its memory.  `behind`
+// bytes of workspace come after them where that is little; memory that is much is an allocation of its own, so
+// that an output that is kept does not keep it.
+struct Pieces {
+  static constexpr int64_t kLittle = 1 << 18;
+  at::Tensor all, apart;
+  int64_t at = 0, behind;
+  static int64_t room(int64_t n) { return (n + 63) / 64 * 64; }
+  Pieces(std::initializer_list<int64_t> counts, size_t workspace, const at::Tensor &like) : behind((int64_t)workspace) {
+    int64_t n = 0;
+    for (const int64_t c : counts) n += room(c);
+    if (behind > kLittle) apart = fresh({behind}, at::kByte, like);
+    else n += (behind + 3) / 4;
+    all = fresh({n}, at::kInt, like);
+  }
+  at::Tensor take(at::IntArrayRef shape) {
+    int64_t n = 1;
+    for (const int64_t x : shape) n *= x;
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    t.unsafeGetTensorImpl()->set_storage_offset(at);
+    at += room(n);
+    return t;
+  }
+  void *workspace() { return behind > kLittle ? apart.mutable_data_ptr() : static_cast<int32_t *>(all.mutable_data_ptr()) + at; }
+};
+
 // pages_fork(page_table, seqlens, refs, parents, grow, page) -> (table, seqlens, refs, src, dst, left)
 PyObject *pages_fork(PyObject *const *a) {
   const at::Tensor *t = tensor(a[0]), *len = tensor(a[1]), *refs = tensor(a[2]), *par = tensor(a[3]), *grow = tensor(a[4]);
@@ -412,11 +440,11 @@ PyObject *pages_fork(PyObject *const *a) {
     return nullptr;
   const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
   const size_t need = p_fork_ws((int)pool, (int)m);
-  at::Tensor to = fresh({m, t->size(1)}, at::kInt, *t), lo = fresh({m}, at::kInt, *t), ro = fresh({pool}, at::kInt, *t);
-  at::Tensor src = fresh({m}, at::kInt, *t), dst = fresh({m}, at::kInt, *t), left = fresh({1}, at::kInt, *t);
-  at::Tensor ws = fresh({(int64_t)need}, at::kByte, *t);
+  Pieces all({m * t->size(1), m, pool, m, m, 1}, need, *t);
+  at::Tensor to = all.take({m, t->size(1)}), lo = all.take({m}), ro = all.take({pool}), src = all.take({m}), dst = all.take({m});
+  at::Tensor left = all.take({1});
   if (p_fork(ints(t), ints(len), ints(refs), ints(par), ints(grow), (int)t->size(0), (int)m, (int)t->size(1), (int)pool, page,
-             ints(&to), ints(&lo), ints(&ro), ints(&src), ints(&dst), ints(&left), ws.mutable_data_ptr(), need,
+             ints(&to), ints(&lo), ints(&ro), ints(&src), ints(&dst), ints(&left), all.workspace(), need,
              stream_of(dev)) != VLF_OK)
     return nullptr;
   return tuple(to, lo, ro, src, dst, left);
@@ -431,11 +459,11 @@ PyObject *pages_compact(PyObject *const *a) {
   if (!table(t, dev) || !list(refs, dev, pool) || !fits(pool)) return nullptr;
   const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
   const size_t need = p_compact_ws((int)pool);
-  at::Tensor table_out = fresh(t->sizes(), at::kInt, *t), ro = fresh({pool}, at::kInt, *t), to = fresh({pool}, at::kInt, *t);
-  at::Tensor src = fresh({pool / 2}, at::kInt, *t), dst = fresh({pool / 2}, at::kInt, *t), used = fresh({1}, at::kInt, *t);
-  at::Tensor ws = fresh({(int64_t)need}, at::kByte, *t);
+  Pieces all({t->numel(), pool, pool, pool / 2, pool / 2, 1}, need, *t);
+  at::Tensor table_out = all.take(t->sizes()), ro = all.take({pool}), to = all.take({pool}), src = all.take({pool / 2});
+  at::Tensor dst = all.take({pool / 2}), used = all.take({1});
   if (p_compact(ints(t), ints(refs), (int)t->size(0), (int)t->size(1), (int)pool, ints(&table_out), ints(&ro), ints(&to),
-                ints(&src), ints(&dst), ints(&used), ws.mutable_data_ptr(), need, stream_of(dev)) != VLF_OK)
+                ints(&src), ints(&dst), ints(&used), all.workspace(), need, stream_of(dev)) != VLF_OK)
     return nullptr;
   return tuple(table_out, ro, to, src, dst, used);
 }
