@@ -317,3 +317,48 @@ def test_refusals_with_tensors():
     if need:
         with pytest.raises(vlf.VlfError):
             vlf.vlf_attn_varlen_fwd_pages(*a, 3, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("q_len,d,dtype,window", [(1, 128, BF, 0), (2, 64, FP, 7000), (20, 128, FP, 0)])
+def test_long_caches_in_pages_of_every_size(page, q_len, d, dtype, window):
+    """More pages than are looked up at a time, and ends inside pages and tiles."""
+    c = problem([q_len, q_len], [20011, 9001], page, 4, 2, d, d, dtype, seed=page)
+    check(call(c, causal=True, window=window), c, causal=True, window=window)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("flags", [0, SIMT])
+def test_many_sequences_with_and_without_rows(flags):
+    """More sequences than a block has threads; most have no rows, or no keys."""
+    n = 1500
+    q = [1 if s % 7 == 0 else 0 for s in range(n)]
+    kv = [0 if s % 11 == 0 else s % 90 for s in range(n)]
+    kv[700], q[700] = 3000, 1
+    c = problem(q, kv, 16, 4, 2, 64, 64, BF, seed=3)
+    check(call(c, causal=True, flags=flags), c, causal=True)
+    q[350] = 40
+    c = problem(q, kv, 16, 4, 2, 64, 64, BF, seed=3)
+    check(call(c, causal=True, flags=flags), c, causal=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,rows", [(3, 1, 30), (5, 1, 60), (7, 1, 9), (130, 1, 2), (300, 1, 3), (20, 1, 7)])
+def test_groups_that_do_not_divide_a_tile(hq, hkv, rows):
+    c = problem([rows, 1], [rows + 100, 333], 32, hq, hkv, 64, 64, FP, seed=hq)
+    check(call(c, causal=True), c, causal=True)
+
+
+@pytest.mark.gpu
+def test_queries_of_every_size():
+    """Rows of zeros, of fp16's largest numbers, of bf16's smallest and largest: the powers of two that they are held over."""
+    for dtype, sizes in ((FP, (0.0, 6e-8, 1.0, 6e4)), (BF, (0.0, 1e-38, 1e-20, 1e4))):
+        for rows in (1, 40):
+            c = problem([rows] * 4, [200, 90, 64, 300], 64, 4, 2, 128, 128, dtype, seed=5)
+            scale = 2.0 ** -10
+            for s, size in enumerate(sizes):
+                x = c["q"][c["cu"][s]:c["cu"][s + 1]]
+                x.copy_((x.float().clamp(-1, 1) * size).to(dtype))
+            c["k_scale"].clamp_(max=2.0 ** -7)
+            check(call(c, scale=scale), c, scale=scale)

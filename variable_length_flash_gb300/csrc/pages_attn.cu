@@ -19,14 +19,21 @@ __global__ void __launch_bounds__(32 * kFmaWarps) pages_fma_kernel(const PagesAt
   __shared__ float q[256];
   __shared__ float o_part[kFmaWarps][256], m_part[kFmaWarps], l_part[kFmaWarps];
   const Params &p = a.p;
-  const int s = blockIdx.z, head = blockIdx.y, kv_head = head / p.group, i = blockIdx.x;
+  const int head = blockIdx.y, kv_head = head / p.group;
+  int s = 0;  // the sequence of row blockIdx.x: the last that begins at it or before
+  for (int end = p.num_seqs; end - s > 1;) {
+    const int mid = (s + end) / 2;
+    if (__ldg(p.cu_q + mid) <= (int)blockIdx.x) s = mid;
+    else end = mid;
+  }
   const int q0 = __ldg(p.cu_q + s), q1 = __ldg(p.cu_q + s + 1), len = __ldg(a.kv_lens + s);
   if (q0 < 0 || q0 > q1 || q1 > p.total_q || q1 - q0 > p.max_q || len < 0 ||
       (len > 0 && (len - 1) >> a.log2_page >= a.max_pages)) {
     if (threadIdx.x == 0) set_error(p.err, VLF_ERR_BAD_SEQLENS);
     return;
   }
-  if (i >= q1 - q0) return;
+  const int i = (int)blockIdx.x - q0;
+  if (i < 0 || i >= q1 - q0) return;
   const long long row = (long long)(q0 + i) * p.h_q + head;
   for (int c = threadIdx.x; c < p.d_qk; c += 32 * kFmaWarps) q[c] = to_f32<T>(static_cast<const T *>(p.q)[row * p.d_qk + c]);
   __syncthreads();
@@ -132,7 +139,7 @@ cudaError_t pages_forward(const PagesAttnParams &a, void *workspace, int num_sms
   const long long heads = (long long)a.num_pages * p.h_kv;
   if (pages_tc_supported(p.d_qk, p.d_v, p.dtype, p.flags) && heads > 0 && heads < 0x7fffffff)
     return many_rows(p.max_q, p.group) ? pages_rows_forward(a, workspace, num_sms, st) : pages_tc_forward(a, workspace, num_sms, st);
-  const dim3 grid((unsigned)p.max_q, (unsigned)p.h_q, (unsigned)p.num_seqs);
+  const dim3 grid((unsigned)p.total_q, (unsigned)p.h_q);
   PagesAttnParams copy = a;
   void *args[1] = {&copy};
   const void *kern = p.dtype == VLF_F32    ? (const void *)pages_fma_kernel<float>

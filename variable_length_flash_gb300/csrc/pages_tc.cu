@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
   }
 }
 
-// Columns of a tile: the fewest that hold a sequence's rows of a kv head's group, 32 at most.
+// Columns of a tile: the fewest that hold a sequence's rows of a kv head's group (32 at most: many_rows).
 int columns(int max_q, int group) {
   const long long n = (long long)max_q * group;
   return n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : 32;
@@ -666,8 +666,8 @@ cudaError_t pages_tc_forward(const PagesAttnParams &a, void *workspace, int num_
     using C = Cfg<D, NC>;
     TcParams p{};
     p.a = a;
-    p.splits = group > NC ? (group + NC - 1) / NC : 1;
-    p.rows = group > NC ? 1 : NC / group;
+    p.splits = 1;  // (the columns hold a whole group)
+    p.rows = NC / group;
     p.magic = magic_of(group);
     const size_t grid = (size_t)C::CTAS * num_sms;
     p.rec = static_cast<int4 *>(workspace);
