@@ -341,8 +341,8 @@ __device__ __forceinline__ int part_of(const PagesForkParams &p, const Row &r, i
 }
 
 // Fork.  outside[p]: holders of p that are no row of the old table; whole[p]: new rows that have it whole;
-// owner[p]: the first new row that goes on inside it; bits: the free pages, a bit each; counts: those of each
-// chunk; need[s]: new pages of row s; state: an error, free pages, new pages.
+// owner[p]: the first new row that goes on inside it; list: each chunk's free pages in order; counts: how many;
+// need[s]: new pages of row s; state: an error, free pages, new pages.
 __global__ void __launch_bounds__(256) fork_begin_kernel(const PagesForkParams p) {
   step_begins();
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -391,18 +391,18 @@ __global__ void __launch_bounds__(256) fork_free_kernel(const PagesForkParams p)
   step_begins();
   int n = 0;
   if ((int)blockIdx.x < p.chunks) {
+    const long long i0 = (long long)blockIdx.x * kChunk + 4 * threadIdx.x;
+    uint32_t mine = 0;
 #pragma unroll
-    for (int k = 0; k < kChunk / 256; ++k) {
-      const long long i = (long long)blockIdx.x * kChunk + k * 256 + threadIdx.x;
-      const bool in = i < p.num_pages;
-      if (in && (p.outside[i] < 0 || p.refs[i] < 0)) p.state[0] = VLF_ERR_BAD_PAGES;
-      const uint32_t m = __ballot_sync(0xffffffffu, in && held(p, (int)i) == 0);
-      if (threadIdx.x % 32 == 0) {
-        p.bits[(long long)blockIdx.x * (kChunk / 32) + (k * 256 + threadIdx.x) / 32] = m;
-        n += __popc(m);
-      }
+    for (int k = 0; k < 4; ++k) {
+      const bool in = i0 + k < p.num_pages;
+      if (in && (p.outside[i0 + k] < 0 || p.refs[i0 + k] < 0)) p.state[0] = VLF_ERR_BAD_PAGES;
+      mine |= (uint32_t)(in && held(p, (int)i0 + k) == 0) << k;
     }
-    n = (int)block_sum(n);
+    int *at = p.list + (long long)blockIdx.x * kChunk + chunk_before(__popc(mine), n);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (mine >> k & 1) *at++ = (int)i0 + k;
     if (threadIdx.x == 0) {
       p.counts[blockIdx.x] = n;
       atomicAdd(p.state + 1, n);
@@ -437,17 +437,22 @@ __global__ void __launch_bounds__(256) fork_end_kernel(const PagesForkParams p) 
     long long before = 0;
     for (int c = threadIdx.x; c < (int)blockIdx.x; c += 256) before += p.counts[c];
     const int at = (int)block_sum(before);  // free pages in front of the chunk
-    const uint32_t word = p.bits[(long long)blockIdx.x * (kChunk / 32) + threadIdx.x / 8];
-    const uint32_t mine = word >> 4 * (threadIdx.x % 8) & 15u;  // of this thread's four pages
-    int all, rank = at + chunk_before(__popc(mine), all);
+    const long long i0 = (long long)blockIdx.x * kChunk + 4 * threadIdx.x;
+    int holds[4], mine = 0;  // of this thread's four pages
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const long long i = (long long)blockIdx.x * kChunk + 4 * threadIdx.x + k;
+      holds[k] = i0 + k < p.num_pages ? held(p, (int)i0 + k) : 1;
+      mine += holds[k] == 0;
+    }
+    int all, rank = at + chunk_before(mine, all);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const long long i = i0 + k;
       if (i >= p.num_pages) continue;
       // the pages given out are the first `need` free ones
       if (!ok) p.refs_out[i] = p.refs[i];
-      else if (mine >> k & 1) p.refs_out[i] = rank++ < need;
-      else p.refs_out[i] = held(p, (int)i);
+      else if (holds[k] == 0) p.refs_out[i] = rank++ < need;
+      else p.refs_out[i] = holds[k];
     }
     return;
   }
@@ -458,41 +463,6 @@ __global__ void __launch_bounds__(256) fork_end_kernel(const PagesForkParams p) 
   const int s = s0 + threadIdx.x / 32;
   if (s >= p.num_out) return;
   for (int i = s0; i < s; ++i) sum += p.need[i];  // new pages of the rows before
-  // the free page of rank k: its chunk by the counts, its word and bit by the words' (the whole warp)
-  auto free_page = [&](long long k) {
-    int c = 0;
-    for (int c0 = 0;; c0 += 32) {
-      const int n = c0 + lane < p.chunks ? p.counts[c0 + lane] : 0;
-      int y = n;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) y += z;
-      }
-      const uint32_t m = __ballot_sync(0xffffffffu, k < y);
-      if (m) {
-        c = c0 + __ffs(m) - 1;
-        k -= __shfl_sync(0xffffffffu, y - n, __ffs(m) - 1);
-        break;
-      }
-      k -= __shfl_sync(0xffffffffu, y, 31);
-      if (c0 + 32 >= p.chunks) return -1;  // (there is one: the ranks asked for are below the free pages' number)
-    }
-    uint32_t word = p.bits[(long long)c * (kChunk / 32) + lane];
-    const int n = __popc(word);
-    int y = n;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int z = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) y += z;
-    }
-    const uint32_t m = __ballot_sync(0xffffffffu, k < y);
-    const int from = __ffs(m) - 1;
-    int in = (int)k - __shfl_sync(0xffffffffu, y - n, from);
-    word = __shfl_sync(0xffffffffu, word, from);
-    while (in-- > 0) word &= word - 1;
-    return c * kChunk + 32 * from + __ffs(word) - 1;
-  };
   const Row r = row_of(p, s);
   bool keeps;
   const int part = part_of(p, r, s, keeps);
@@ -504,12 +474,43 @@ __global__ void __launch_bounds__(256) fork_end_kernel(const PagesForkParams p) 
 #pragma unroll 4
   for (int j = lane; j < p.max_pages; j += 32)
     if (j < shared || j >= has) out[j] = j >= has ? -1 : j < r.whole ? __ldg(row + j) : part;
+  // the new pages are the free ones of ranks sum, sum + 1, ...; a lane looks at eight chunks
+  const long long end = sum + has - shared;
   int first = -1;
-  for (int j = shared; j < has; ++j) {
-    const int page = free_page(sum + j - shared);
-    if (j == shared) first = page;
-    if (lane == 0) out[j] = page;
+  long long base = 0;
+  for (int c0 = 0; c0 < p.chunks && base < end && has > shared; c0 += 256) {
+    const int c = c0 + 8 * lane;
+    int n[8], y = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      n[i] = c + i < p.chunks ? p.counts[c + i] : 0;
+      y += n[i];
+    }
+    const int own = y;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    const long long at = base + y - own;
+    for (uint32_t m = __ballot_sync(0xffffffffu, at < end && at + own > sum); m; m &= m - 1) {
+      const int from = __ffs(m) - 1;
+      long long lo = __shfl_sync(0xffffffffu, at, from);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = __shfl_sync(0xffffffffu, n[i], from);
+        const int *list = p.list + (long long)(c0 + 8 * from + i) * kChunk - lo;
+        for (long long g = max(lo, sum) + lane; g < min(lo + k, end); g += 32) {
+          const int page = list[g];
+          out[shared + (int)(g - sum)] = page;
+          if (g == sum) first = page;
+        }
+        lo += k;
+      }
+    }
+    base += __shfl_sync(0xffffffffu, y, 31);
   }
+  first = __reduce_max_sync(0xffffffffu, first);  // (one lane met it)
   if (lane == 0) {
     p.lens_out[s] = len;
     p.src[s] = copy ? part : -1;
@@ -773,7 +774,7 @@ cudaError_t pages_copy(PagesCopyParams p, cudaStream_t st) {
 
 size_t pages_fork_workspace(int num_pages, int num_out) {
   const int chunks = chunks_of(num_pages);
-  return 3 * ints(num_pages) + ints((long long)chunks * (kChunk / 32)) + ints(chunks) + ints(num_out) + ints(4);
+  return 3 * ints(num_pages) + ints((long long)chunks * kChunk) + ints(chunks) + ints(num_out) + ints(4);
 }
 cudaError_t pages_fork(PagesForkParams p, void *workspace, cudaStream_t st) {
   char *w = static_cast<char *>(workspace);
@@ -786,7 +787,7 @@ cudaError_t pages_fork(PagesForkParams p, void *workspace, cudaStream_t st) {
   p.outside = take(p.num_pages);
   p.whole = take(p.num_pages);
   p.owner = take(p.num_pages);
-  p.bits = reinterpret_cast<unsigned *>(take((long long)p.chunks * (kChunk / 32)));
+  p.list = take((long long)p.chunks * kChunk);
   p.counts = take(p.chunks);
   p.need = take(p.num_out);
   p.state = take(4);
