@@ -139,7 +139,7 @@ struct PagesForkParams {
   int *table_out, *lens_out, *refs_out, *src, *dst, *left;
   int *err;
   // workspace
-  int *outside, *whole, *owner, *list, *counts, *need, *state, chunks;
+  int *outside, *whole, *owner, *list, *counts, *need, *group, *state, chunks;
 };
 size_t pages_fork_workspace(int num_pages, int num_out);
 cudaError_t pages_fork(PagesForkParams p, void *workspace, cudaStream_t st);

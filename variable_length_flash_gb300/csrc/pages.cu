@@ -267,10 +267,12 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const PagesCopyParams p
 }
 
 // ------------------------------------------------------------------------------ tables
-// A call's steps wait for one another: each is a launch that starts while the one before ends (its blocks are
-// there already, and wait).  One cluster of eight CTAs with its barriers between the steps took 13.1 us for 32
-// rows of 16 pages (with their copies) where this takes LATER, and 66 us for 256 rows of 1000 where this takes
-// LATER: its eight SMs look at a quarter of a million entries.
+// Bound: latency; a call is three or four dependent steps, each a launch that starts while the one before ends
+// (its blocks are there already, and wait).  256 rows of up to 1041 pages on 256 others, with their copies: 16.0 us,
+// of which the entries and counts are 1 us at the memory's rate; 21.1 with a warp for each row in the last step
+// instead of a block (a row's entries are 33 loads one behind another then), 66 as one cluster of eight CTAs with its
+// barriers between the steps (eight SMs look at a quarter of a million entries).  Tables of few entries
+// take one block (below).
 constexpr int kChunk = 1024;  // pages of a block that counts
 
 __device__ __forceinline__ int pages_of(int len, int log2_page) { return (int)(((long long)len + (1 << log2_page) - 1) >> log2_page); }
@@ -342,7 +344,8 @@ __device__ __forceinline__ int part_of(const PagesForkParams &p, const Row &r, i
 
 // Fork.  outside[p]: holders of p that are no row of the old table; whole[p]: new rows that have it whole;
 // owner[p]: the first new row that goes on inside it; list: each chunk's free pages in order; counts: how many;
-// need[s]: new pages of row s; state: an error, free pages, new pages.
+// need[s]: new pages of the rows before row s in its 256; group: those of each 256 rows; state: an
+// error, free pages, new pages.
 __global__ void __launch_bounds__(256) fork_begin_kernel(const PagesForkParams p) {
   step_begins();
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -416,14 +419,16 @@ __global__ void __launch_bounds__(256) fork_free_kernel(const PagesForkParams p)
     const int page = part_of(p, r, s, keeps);
     const long long to = min((long long)r.len + max(0, __ldg(p.grow + s)), (long long)p.max_pages << p.log2_page);
     n = pages_of((int)to, p.log2_page) - pages_of(r.len, p.log2_page) + (page >= 0 && !keeps);
-    p.need[s] = n;
   }
-  // (more pages than there are is all that has to be told apart)
+  int sum;
+  const int before = chunk_before(n, sum);  // (may wrap only where the call asks for more pages than there are)
+  if (s < p.num_out) p.need[s] = before;
   const long long all = block_sum(n);
+  if (threadIdx.x == 0) p.group[blockIdx.x - p.chunks] = sum;
   if (threadIdx.x == 0) atomicAdd(reinterpret_cast<unsigned long long *>(p.state + 2), (unsigned long long)all);
 }
 
-// The new counts (a block for each chunk), and the new rows (a block of eight warps for eight rows).
+// The new counts (a block for each chunk), and the new rows (a block each; its first warp finds the new pages).
 __global__ void __launch_bounds__(256) fork_end_kernel(const PagesForkParams p) {
   step_begins();
   const int bad = p.state[0], free = p.state[1], lane = threadIdx.x % 32;
@@ -456,13 +461,11 @@ __global__ void __launch_bounds__(256) fork_end_kernel(const PagesForkParams p) 
     }
     return;
   }
-  const int s0 = (blockIdx.x - p.chunks) * 8;
+  const int s = blockIdx.x - p.chunks;
+  if (s >= p.num_out) return;  // (a call without rows)
   long long sum = 0;
-  for (int s = threadIdx.x; s < s0; s += 256) sum += p.need[s];
-  sum = block_sum(sum);
-  const int s = s0 + threadIdx.x / 32;
-  if (s >= p.num_out) return;
-  for (int i = s0; i < s; ++i) sum += p.need[i];  // new pages of the rows before
+  for (int g = threadIdx.x; g < s / 256; g += 256) sum += p.group[g];
+  sum = block_sum(sum) + p.need[s];  // new pages of the rows before
   const Row r = row_of(p, s);
   bool keeps;
   const int part = part_of(p, r, s, keeps);
@@ -472,8 +475,9 @@ __global__ void __launch_bounds__(256) fork_end_kernel(const PagesForkParams p) 
   int *out = p.table_out + (long long)s * p.max_pages;
   const int shared = ok ? r.whole + (keeps ? 1 : 0) : 0;  // entries that stay
 #pragma unroll 4
-  for (int j = lane; j < p.max_pages; j += 32)
+  for (int j = threadIdx.x; j < p.max_pages; j += 256)
     if (j < shared || j >= has) out[j] = j >= has ? -1 : j < r.whole ? __ldg(row + j) : part;
+  if (threadIdx.x >= 32) return;
   // the new pages are the free ones of ranks sum, sum + 1, ...; a lane looks at eight chunks
   const long long end = sum + has - shared;
   int first = -1;
@@ -518,8 +522,9 @@ __global__ void __launch_bounds__(256) fork_end_kernel(const PagesForkParams p) 
   }
 }
 
-// Small calls as one block of 1024 threads, counters and free pages in shared memory: five launches are what the
-// host spends its time on there.
+// Small calls as one block of 1024 threads, counters and free pages in shared memory: 32 rows of 16 pages on 8 others
+// take 6.8 us with their copies, the steps above 10.7 and a cluster of eight CTAs 13.1; the host spends 5.7 us on
+// the call instead of 11.9.
 constexpr int kSmallPages = 4096, kSmallRows = 1024, kSmallEntries = 32768;
 
 // The sum of x over the threads before this one, and over all (1024 threads).
@@ -774,7 +779,7 @@ cudaError_t pages_copy(PagesCopyParams p, cudaStream_t st) {
 
 size_t pages_fork_workspace(int num_pages, int num_out) {
   const int chunks = chunks_of(num_pages);
-  return 3 * ints(num_pages) + ints((long long)chunks * kChunk) + ints(chunks) + ints(num_out) + ints(4);
+  return 3 * ints(num_pages) + ints((long long)chunks * kChunk) + ints(chunks) + ints(num_out) + ints((num_out + 255ll) / 256) + ints(4);
 }
 cudaError_t pages_fork(PagesForkParams p, void *workspace, cudaStream_t st) {
   char *w = static_cast<char *>(workspace);
@@ -790,6 +795,7 @@ cudaError_t pages_fork(PagesForkParams p, void *workspace, cudaStream_t st) {
   p.list = take((long long)p.chunks * kChunk);
   p.counts = take(p.chunks);
   p.need = take(p.num_out);
+  p.group = take((p.num_out + 255ll) / 256);
   p.state = take(4);
   void *args[1] = {&p};
   const int rows = p.num_in + p.num_out;
@@ -804,9 +810,9 @@ cudaError_t pages_fork(PagesForkParams p, void *workspace, cudaStream_t st) {
   cudaError_t e = step((const void *)fork_begin_kernel, dim3((unsigned)(((long long)max(p.num_pages, 4) + 255) / 256)));
   if (e == cudaSuccess && rows > 0)
     e = step((const void *)fork_count_kernel, dim3((unsigned)max(1, (p.max_pages + 255) / 256), (unsigned)min(rows, 65535)));
-  const int behind = (p.num_out + 255) / 256;
+  const int behind = (int)((p.num_out + 255ll) / 256);
   if (e == cudaSuccess && p.chunks + behind > 0) e = step((const void *)fork_free_kernel, dim3((unsigned)(p.chunks + behind)));
-  if (e == cudaSuccess) e = step((const void *)fork_end_kernel, dim3((unsigned)max(1, p.chunks + (p.num_out + 7) / 8)));
+  if (e == cudaSuccess) e = step((const void *)fork_end_kernel, dim3((unsigned)max(1ll, (long long)p.chunks + p.num_out)));
   return e;
 }
 
