@@ -229,7 +229,8 @@ cudaError_t write(PagesWriteParams p, cudaStream_t st) {
 
 // ------------------------------------------------------------------------------ copying
 // Bound: HBM.  Pair i is page src[i] over page dst[i], all heads; a block has `chunk` pairs' segments of
-// 16 KB.
+// 16 KB, four wide loads a thread in flight.  Measured: 4368 of 8723 pairs, pages of 128 KB, 173 us (97% of the copy
+// rate; with chunks of 32 189, of 2 177, of 1 194).
 constexpr int kSegment = 16384;
 
 __global__ void __launch_bounds__(256) pages_copy_kernel(const PagesCopyParams p) {
@@ -770,8 +771,9 @@ cudaError_t pages_write(const PagesWriteParams &p, cudaStream_t st) {
 cudaError_t pages_copy(PagesCopyParams p, cudaStream_t st) {
   auto segments = [&](int d) { return ((long long)p.h_kv * p.page * d + kSegment - 1) / kSegment; };
   const long long segs = segments(p.d_qk) + segments(p.d_v);
-  // pairs per block: what leaves about eight blocks per SM (as many are resident)
-  p.chunk = (int)max(1ll, min(32ll, (long long)p.n * segs / (152 * 8)));
+  // pairs per block: one where the call is small, eight where blocks of one are more than are resident (pairs
+  // that are not to be copied cost a block each then; 32 leave the SMs unequal work)
+  p.chunk = (int)max(1ll, min(8ll, (long long)p.n * segs / (152 * 8)));
   void *args[1] = {&p};
   return launch_step((const void *)pages_copy_kernel, dim3((unsigned)((p.n + p.chunk - 1) / p.chunk), (unsigned)segs), 256,
                      st, args);
