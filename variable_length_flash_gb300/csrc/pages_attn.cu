@@ -15,11 +15,17 @@ namespace {
 // keys in turn, so a byte is read and made a number once for the H heads.  A lane has a key's whole dot products, then
 // four columns of the output in 128.  Each warp keeps a running maximum and sum; they are joined at
 // the end, over the cluster's blocks as well where the launch has few rows and gives a row's keys to several.
+//
+// Bound: latency of a warp's dependent steps (loads, sums, exponentials), then issue.  A decode step of 64 caches of
+// 1000 to 16384 keys, 32 heads over 8 of 128 in fp32: 810 us, 21% of the copy rate (3451 with a block for each head
+// and bytes of values read singly; 907 with four keys in flight); width 96 in bf16 700 us; one cache of 131071 keys
+// 491 us.  Four blocks an SM, by bounding the registers, were 10% faster on the 64 caches and 65% slower
+// on the one.  Rows of one sequence share nothing here: 16 chats with 64 to 436 new rows take 22 ms.
 constexpr int kFmaWarps = 8, kFmaSplit = 8;  // warps of a block; blocks of a row, if it is shared out
 
 template <typename T, int H>
 __global__ void __launch_bounds__(32 * kFmaWarps) pages_fma_kernel(const PagesAttnParams a, const int splits) {
-  constexpr int NT = 32 * kFmaWarps;
+  constexpr int NT = 32 * kFmaWarps, KV = 8;  // keys whose values are in flight
   __shared__ __align__(16) float q[256][H];   // then the block's sums
   __shared__ float o_part[kFmaWarps][H][256], m_part[kFmaWarps][H], l_part[kFmaWarps][H], m_all[H], l_all[H];
   __shared__ __align__(16) float weight[kFmaWarps][32][H];
@@ -81,7 +87,7 @@ __global__ void __launch_bounds__(32 * kFmaWarps) pages_fma_kernel(const PagesAt
       const uint8_t *k = a.k_pages + at * p.d_qk;
       int c = 0;
       if (p.d_qk % 16 == 0) {
-#pragma unroll 2
+#pragma unroll 4
         for (; c < p.d_qk; c += 16) {
           const uint4 r = *reinterpret_cast<const uint4 *>(k + c);
           const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -121,13 +127,13 @@ __global__ void __launch_bounds__(32 * kFmaWarps) pages_fma_kernel(const PagesAt
     place[warp][lane] = at;
     const uint32_t seen = __ballot_sync(0xffffffffu, see);
     __syncwarp();
-    // four keys' values at a time (a key that is not seen is not read: its slot may hold anything)
+    // KV keys' values at a time (a key that is not seen is not read: its slot may hold anything)
 #pragma unroll 1
-    for (int k0 = 0; k0 < 32; k0 += 4) {
-      if (!(seen >> k0 & 15u)) continue;
-      uint32_t v[4][2];
+    for (int k0 = 0; k0 < 32; k0 += KV) {
+      if (!(seen >> k0 & ((1u << KV) - 1))) continue;
+      uint32_t v[KV][2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < KV; ++k)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const int c = 4 * lane + 128 * b;
@@ -144,7 +150,7 @@ __global__ void __launch_bounds__(32 * kFmaWarps) pages_fma_kernel(const PagesAt
           }
         }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < KV; ++k) {
         float w[H];
 #pragma unroll
         for (int h = 0; h < H; ++h) w[h] = weight[warp][k0 + k][h];
@@ -241,7 +247,9 @@ template <typename T> cudaError_t fma_forward(const PagesAttnParams &a, int num_
   return e;
 }
 
-// Whether a sequence's rows of a kv head's group are enough for the kernel that has them as rows of its products.
+// Whether a sequence's rows of a kv head's group are enough for the kernel that has them as rows of its products.  64
+// caches of 1000 to 16384 keys, groups of 4 heads of 128: 4 rows (16 with the heads) take 226 us as columns, 489 as
+// rows; 8 rows 355 and 504; 9 rows 614 and 503 (two tiles of columns then, each reading the cache); 16 rows 659 and 507.
 bool many_rows(int max_q, int group) { return (long long)max_q * group > 32; }
 
 }  // namespace

@@ -13,8 +13,16 @@
 // Roles of a CTA (one per SM): warp 0 page loads, warp 1 S = Q K^T, warp 2 O += P V, warp 3 the items of the CTA's
 // run, which it lays out in shared memory for the others (their registers are full without it), warps 4-11 bytes
 // to fp16, warps 12-19 softmax and output, a thread for each row of the two query tiles: these have the registers that
-// the others give up.  TMEM: O of both tiles, two S of
-// 64 keys each, over which P is written.
+// the others give up (64 and 144 of the 96 that the launch has; a wait or a walk that is not inlined
+// takes more than 64).  TMEM: O of both tiles, two S of 64 keys each, over which P is written.
+//
+// Bound: the softmax warps' exponentials and roundings beside the conversions, and the fetching of the roles'
+// instructions, which do not all fit the instruction cache.  16 chats of 436 to 8192 keys with 64 to 436 new
+// rows, 32 heads over 8 of 128: 479 us (717 TFLOP/s, 38% of the rate of a large product); prompts of 4 x 4096 tokens
+// 782 us (703 TFLOP/s); width 64 386 us.  Steps: 2607 us on the decode kernel's columns; 598 as rows; 557 with a
+// warp that lays the items out; 506 with bodies short enough for the instruction cache; 479 with masks as bits,
+// output places found once and scales ahead of S.  Slower: exponentials before the vote (829, registers spilled),
+// rolled loops that read S again (525 to 566), masks kept in TMEM (534), queries brought in by the converting warps (494).
 #include "e4m3.cuh"
 #include "pages_tc.cuh"
 
@@ -80,7 +88,7 @@ __device__ __forceinline__ float rcp(float x) {
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1) 
+__global__ void __launch_bounds__(kThreads, 1)
     pages_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                       const __grid_constant__ TcParams p) {
   using C = RowCfg<D>;
