@@ -580,8 +580,11 @@ int vlf_pages_write(const void *k, int64_t k_stride, const void *v, int64_t v_st
  * Pages of which no row of a sequence sees a key (in front of the window) are not looked at and may be
  * outside the pool.  What other bytes of a page hold never reaches a row, but a value of its own sequence
  * that is NaN may also reach rows that do not see its key.  A row that sees a NaN logit is NaN, and so is
- * its lse.  Tensor-core kernels for F16 / BF16 and d_qk = d_v in {64, 128}; fp32 FMA otherwise.  No
- * backward.
+ * its lse.  Tensor-core kernels for F16 / BF16 and d_qk = d_v in {64, 128}; fp32 FMA otherwise.  On the
+ * tensor cores the value scales of a sequence's pages lie within a factor of 2^100 of one another (a key
+ * whose page's scale is further below the others' may lose its weight).  max_seqlen_q decides which kernel
+ * runs: more than 32 rows of a kv head's group (max_seqlen_q * h_q / h_kv) take the one for many rows, so a
+ * loose bound makes single rows slower (2.7 times, in large batches), never wrong.  No backward.
  */
 int vlf_attn_varlen_fwd_pages(const void *q, const void *k_pages, const void *v_pages,
                               const float *k_scale, const float *v_scale, const int32_t *page_table,
