@@ -308,6 +308,29 @@ def test_fork_refuses_tables_that_disagree(change, status):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("pages,rows,most,every", [(300001, 9, 7000, 3), (300001, 700, 40, 50), (5000, 300, 17, 1), (4097, 1, 4097, 1)])
+def test_fork_takes_free_pages_from_all_over_the_pool(pages, rows, most, every):
+    """Rows whose new pages lie in many of the pool's chunks, more chunks and rows than are looked at at a time, and a pool
+    that is used up to its last page."""
+    r = random.Random(pages + rows)
+    refs = [0 if p % every == 0 else r.randint(1, 3) for p in range(pages)]
+    left = refs.count(0)
+    grow = []
+    for _ in range(rows):
+        n = min(r.randint(0, most), left)
+        grow.append(16 * n - (r.randint(0, 15) if n else 0))
+        left -= n
+    if left and left <= most - -(-grow[-1] // 16):
+        grow[-1] += 16 * left
+    none = torch.empty(0, most, dtype=I32, device="cuda")
+    got = vlf.vlf_pages_fork(none, ints([]), ints(refs), ints([-1] * rows), ints(grow), 16)
+    want = ref.fork([], [], refs, [-1] * rows, grow, 16)
+    full = [x + [-1] * (most - len(x)) for x in want[0]]
+    assert [x.tolist() for x in got] == [full, want[1], want[2], want[3], want[4], [want[5]]]
+    assert want[5] >= 0 and vlf.vlf_check_error() == 0
+
+
+@pytest.mark.gpu
 def test_fork_of_nothing():
     none = torch.empty(0, 4, dtype=I32, device="cuda")
     got = vlf.vlf_pages_fork(none, ints([]), ints([0, 1]), ints([-1]), ints([5]), 16)

@@ -362,3 +362,13 @@ def test_queries_of_every_size():
                 x.copy_((x.float().clamp(-1, 1) * size).to(dtype))
             c["k_scale"].clamp_(max=2.0 ** -7)
             check(call(c, scale=scale), c, scale=scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 2], [999, 40]), ([1, 1], [3, 5000]), ([300, 1, 400], [700, 31, 400])])
+@pytest.mark.parametrize("hq,hkv,dk,dv", [(4, 4, 40, 40), (2, 1, 100, 100), (3, 1, 96, 96), (10, 2, 250, 129), (9, 3, 64, 6), (5, 1, 17, 256)])
+def test_heads_and_rows_of_the_fma_kernel(q_lens, kv_lens, hq, hkv, dk, dv):
+    """Groups that its blocks of four heads do not divide; a row's keys in one block, and shared out to eight."""
+    c = problem(q_lens, kv_lens, 32, hq, hkv, dk, dv, BF, seed=dk)
+    check(call(c, causal=True), c, causal=True)
+    check(call(c, causal=True, window=37), c, causal=True, window=37)

@@ -64,11 +64,10 @@ __global__ void __launch_bounds__(32 * kFmaWarps) pages_fma_kernel(const PagesAt
 #pragma unroll
     for (int c = 0; c < 8; ++c) o[h][c] = 0.f;
   }
-  // (in 64 bits: the end of a run of keys may lie behind the largest int)
-  for (long long j0 = (lo & ~31) + 32 * (split * kFmaWarps + warp); j0 < hi; j0 += 32 * kFmaWarps * splits) {
+  for (int j0 = (lo & ~31) + 32 * (split * kFmaWarps + warp); j0 < hi; j0 += 32 * kFmaWarps * splits) {
     // (32 keys lie in one or two pages)
-    const int j = (int)j0 + lane;
-    bool see = j >= lo && j < hi && j0 + lane < hi;
+    const int j = j0 + lane;  // (lengths stay 2^16 below the largest int)
+    bool see = j >= lo && j < hi;
     int page = see ? __ldg(a.table + (long long)s * a.max_pages + (j >> a.log2_page)) : 0;
     if (page < 0 || page >= a.num_pages) {
       if (see) set_error(p.err, VLF_ERR_BAD_PAGES);
