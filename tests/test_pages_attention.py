@@ -372,3 +372,20 @@ def test_heads_and_rows_of_the_fma_kernel(q_lens, kv_lens, hq, hkv, dk, dv):
     c = problem(q_lens, kv_lens, 32, hq, hkv, dk, dv, BF, seed=dk)
     check(call(c, causal=True), c, causal=True)
     check(call(c, causal=True, window=37), c, causal=True, window=37)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q_lens,flags", [([1, 3], 0), ([60, 30], 0), ([1, 3], SIMT)])
+def test_pages_past_32_bits(q_lens, flags):
+    """The same pages at the end of a pool of more than 4 GB: the same bits."""
+    c = problem(q_lens, [700, 130], 64, 8, 2, 128, 128, BF, seed=9)
+    want = call(c, causal=True, flags=flags)
+    n = c["k_pages"].shape[0]
+    first = (1 << 32) // c["k_pages"][0].numel() + 3
+    far = dict(c, table=torch.where(c["table"] >= 0, c["table"] + first, c["table"]))
+    for x in ("k_pages", "v_pages", "k_scale", "v_scale"):
+        far[x] = torch.empty(first + n, *c[x].shape[1:], dtype=c[x].dtype, device="cuda")
+        far[x][first:] = c[x]
+    got = call(far, causal=True, flags=flags)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert vlf.vlf_check_error() == 0
