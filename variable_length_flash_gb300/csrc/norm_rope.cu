@@ -13,10 +13,12 @@
 //
 // Measured: 20011 tokens of 40 heads of 128 in bf16, sliced from a fused projection, 78 us (78% of the copy
 // rate; the weights times sine and cosine are made once for a token, which took it from 92); the gradients of
-// 16384 tokens of 32 heads of 96 in fp16, 64 columns of which turn in pairs of neighbours, 87 us (51%): it
+// 16384 tokens of 32 heads of 96 in fp16, 64 columns of which turn in pairs of neighbours, 74 us (60%): it
 // issues 30 instructions for an element, a quarter of them for lanes that have no columns (12 chunks of a row
-// over 8 lanes), and the sums, weights and turns that a lane keeps leave one block an SM its registers (two
-// with half the heads in flight: 105 us).  64 tokens 4.2 us, which is a launch.
+// over 8 lanes), and the sums, weights and turns that a lane keeps leave one block an SM its registers.  So what the
+// next heads need is on its way to shared memory meanwhile, each thread's to places of its own (85 us with the
+// loads in registers, four heads at a time; two heads at a time 78, two such blocks an SM 116).  64 tokens 4.2 us,
+// which is a launch.
 #include "kernels.h"
 #include "rope.cuh"
 #include "tc_common.cuh"
@@ -35,11 +37,19 @@ __device__ __forceinline__ float weight_at(const void *w, int dtype, int c) {
   return __half2float(static_cast<const __half *>(w)[c]);
 }
 
+constexpr int kSlots = 3;  // of the backward: heads' values on their way or in use
+
+__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
 // Grid y: a run of hpt heads of q or k; x: runs of 256 / G tokens, walked with the grid's stride.  Lane
 // u of a token's G has its units u, u + G, ... (NU of them; one where they hold 16 bytes).  HEADS:
 // heads whose loads are in flight.
 template <typename T, int V, bool INTER, int NU, int HEADS, bool BWD, bool ODD>
 __global__ void __launch_bounds__(256, BWD || V == 1 ? 1 : 2) norm_rope_kernel(const NormRopeParams p) {
+  constexpr bool AHEAD = BWD && V > 1;
+  extern __shared__ __align__(16) uint4 slots[];  // [kSlots][HEADS][4][256]
   __shared__ unsigned long long F[128];
   __shared__ float red[BWD ? 512 * V : 1][BWD && NU > 1 ? NU : 1];
   const int half = p.rot / 2, nrot = half / V;
@@ -84,6 +94,33 @@ __global__ void __launch_bounds__(256, BWD || V == 1 ? 1 : 2) norm_rope_kernel(c
   // HEADS heads of a token at a time
   C x[HEADS][NU], y[HEADS][NU], dx[BWD ? HEADS : 1][NU], dy[BWD ? HEADS : 1][NU];
   const long long step = (long long)gridDim.x * run;
+  // AHEAD: what a thread reads of the heads after the next ones goes to its own places in shared memory meanwhile
+  int slot = 0, to_slot = 0, next_h = h0;
+  long long next_tok = (long long)blockIdx.x * run + g;
+  auto fetch = [&]() {
+    if (next_tok < p.total && have[0]) {
+      const T *x0 = static_cast<const T *>(rows.x) + next_tok * rows.x_stride + (long long)next_h * p.d;
+      const T *dy0 = static_cast<const T *>(rows.dy) + next_tok * rows.dy_stride + (long long)next_h * p.d;
+      const uint32_t to = tc::smem_u32(slots) + ((uint32_t)to_slot * HEADS * 4 * 256 + threadIdx.x) * 16;
+#pragma unroll
+      for (int i = 0; i < HEADS; ++i) {
+        if (next_h + i >= h1) continue;
+        copy16(to + (4 * i) * 4096, x0 + i * p.d + ca[0]);
+        copy16(to + (4 * i + 1) * 4096, x0 + i * p.d + cb[0]);
+        copy16(to + (4 * i + 2) * 4096, dy0 + i * p.d + ca[0]);
+        copy16(to + (4 * i + 3) * 4096, dy0 + i * p.d + cb[0]);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    to_slot = to_slot == kSlots - 1 ? 0 : to_slot + 1;
+    if ((next_h += HEADS) >= h1) {
+      next_h = h0;
+      next_tok += step;
+    }
+  };
+  if constexpr (AHEAD)
+#pragma unroll 1
+    for (int i = 0; i < kSlots - 1; ++i) fetch();
   for (long long tok = (long long)blockIdx.x * run + g; tok < p.total; tok += step) {
     // The weights and the rotation of a pair (l, h) in one: forward y_l = x_l A - x_h B, y_h = x_h C + x_l D with
     // A = w_l cos, B = w_h sin, C = w_h cos, D = w_l sin; backward with g = R(-t) dy alone: A = C = cos, B = D = -sin.
@@ -113,6 +150,19 @@ __global__ void __launch_bounds__(256, BWD || V == 1 ? 1 : 2) norm_rope_kernel(c
     const T *x0 = static_cast<const T *>(rows.x) + tok * rows.x_stride + (long long)h0 * p.d;
     const T *dy0 = BWD ? static_cast<const T *>(rows.dy) + tok * rows.dy_stride + (long long)h0 * p.d : nullptr;
     for (int h = h0; h < h1; h += HEADS, x0 += HEADS * p.d, dy0 += BWD ? HEADS * p.d : 0, out0 += HEADS * p.d) {
+      if constexpr (AHEAD) {
+        fetch();
+        asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
+        const uint4 *at = slots + (slot * HEADS * 4 * 256 + threadIdx.x);
+        slot = slot == kSlots - 1 ? 0 : slot + 1;
+#pragma unroll
+        for (int i = 0; i < HEADS; ++i) {
+          x[i][0] = *reinterpret_cast<const C *>(at + 4 * i * 256);
+          y[i][0] = *reinterpret_cast<const C *>(at + (4 * i + 1) * 256);
+          dx[i][0] = *reinterpret_cast<const C *>(at + (4 * i + 2) * 256);
+          dy[i][0] = *reinterpret_cast<const C *>(at + (4 * i + 3) * 256);
+        }
+      } else
 #pragma unroll
       for (int i = 0; i < HEADS; ++i) {
         if (h + i >= h1) continue;
@@ -282,11 +332,13 @@ cudaError_t launch(NormRopeParams p, cudaStream_t st) {
   if (BWD && x * y > kMostBlocks) x = kMostBlocks / y;
   if (x > 0) {
     const bool many = p.hpt >= 8, odd = (p.d - p.rot) / v % 2 != 0;
+    int heads = 1;
     auto pick = [&](auto v_, auto inter_) {
       constexpr int V = decltype(v_)::value;
       constexpr bool INTER = decltype(inter_)::value;
       constexpr int NU = V == 1 ? 4 : 1;
       constexpr int MANY = V == 1 ? 1 : BWD ? 4 : 8, FEW = V == 1 ? 1 : 2;
+      heads = odd || !many ? FEW : MANY;
       if (odd || V == 1) return (const void *)norm_rope_kernel<T, V, INTER, NU, V == 1 ? 1 : 2, BWD, true>;
       return many ? (const void *)norm_rope_kernel<T, V, INTER, NU, MANY, BWD, V == 1>
                   : (const void *)norm_rope_kernel<T, V, INTER, NU, FEW, BWD, V == 1>;
@@ -296,7 +348,9 @@ cudaError_t launch(NormRopeParams p, cudaStream_t st) {
     const void *kern = vec ? (p.interleaved ? pick(W{}, std::true_type{}) : pick(W{}, std::false_type{}))
                            : (p.interleaved ? pick(One{}, std::true_type{}) : pick(One{}, std::false_type{}));
     void *args[1] = {&p};
-    const cudaError_t e = launch_dependent(kern, dim3((unsigned)x, (unsigned)y), 256, 0, st, args);
+    const int smem = BWD && vec ? kSlots * heads * 4 * 256 * 16 : 0;
+    cudaError_t e = smem ? set_smem_once(kern, smem) : cudaSuccess;
+    if (e == cudaSuccess) e = launch_dependent(kern, dim3((unsigned)x, (unsigned)y), 256, smem, st, args);
     if (e != cudaSuccess) return e;
     count_launch();
   }
