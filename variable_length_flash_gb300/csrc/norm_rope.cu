@@ -13,12 +13,12 @@
 //
 // Measured: 20011 tokens of 40 heads of 128 in bf16, sliced from a fused projection, 78 us (78% of the copy
 // rate; the weights times sine and cosine are made once for a token, which took it from 92); the gradients of
-// 16384 tokens of 32 heads of 96 in fp16, 64 columns of which turn in pairs of neighbours, 74 us (60%): it
-// issues 30 instructions for an element, a quarter of them for lanes that have no columns (12 chunks of a row
-// over 8 lanes), and the sums, weights and turns that a lane keeps leave one block an SM its registers.  So what the
-// next heads need is on its way to shared memory meanwhile, each thread's to places of its own (85 us with the
-// loads in registers, four heads at a time; two heads at a time 78, two such blocks an SM 116).  64 tokens 4.2 us,
-// which is a launch.
+// 16384 tokens of 32 heads of 96 in fp16, 64 columns of which turn in pairs of neighbours, 70.5 us (63%): a
+// quarter of what it issues is for lanes that have no columns (12 chunks of a row over 8 lanes), and the sums,
+// weights and turns that a lane keeps leave one block an SM its registers, eight warps.  So what the next heads need
+// is on its way to shared memory meanwhile, each thread's to places of its own (85 us with the loads in
+// registers, four heads at a time), and two numbers go through an instruction where there is one for two (74
+// without).  Two heads at a time 73, two such blocks an SM 116.  64 tokens 4.2 us, which is a launch.
 #include "kernels.h"
 #include "rope.cuh"
 #include "tc_common.cuh"
@@ -91,6 +91,24 @@ __global__ void __launch_bounds__(256, BWD || V == 1 ? 1 : 2) norm_rope_kernel(c
       }
     }
   }
+  // AHEAD: the l's and h's of a unit's pairs (Unit::columns), two pairs in a register pair for the fp32 instructions that
+  // have two of each operand: they are most of what the kernel issues
+  constexpr int P = V / 2 > 0 ? V / 2 : 1;
+  uint64_t wl[P], wh[P], sl[P], sh[P];
+  auto low = [&](const float (&a)[V], const float (&b)[V], int e) { return INTER && V > 1 ? (e < V / 2 ? a : b)[2 * e % V] : a[e]; };
+  auto high = [&](const float (&a)[V], const float (&b)[V], int e) { return INTER && V > 1 ? (e < V / 2 ? a : b)[2 * e % V + 1] : b[e]; };
+  auto pairs = [&](const float (&a)[V], const float (&b)[V], uint64_t (&l)[P], uint64_t (&h)[P]) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      l[k] = tc::f2pack(low(a, b, 2 * k), low(a, b, 2 * k + 1));
+      h[k] = tc::f2pack(high(a, b, 2 * k), high(a, b, 2 * k + 1));
+    }
+  };
+  if constexpr (AHEAD) {
+    pairs(wa[0], wb[0], wl, wh);
+#pragma unroll
+    for (int k = 0; k < P; ++k) sl[k] = sh[k] = 0;
+  }
   // HEADS heads of a token at a time
   C x[HEADS][NU], y[HEADS][NU], dx[BWD ? HEADS : 1][NU], dy[BWD ? HEADS : 1][NU];
   const long long step = (long long)gridDim.x * run;
@@ -146,6 +164,15 @@ __global__ void __launch_bounds__(256, BWD || V == 1 ? 1 : 2) norm_rope_kernel(c
         }
       }
     }
+    uint64_t A2[P], B2[P], N2[P];
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        A2[k] = tc::f2pack(A[0][2 * k], A[0][2 * k + 1]);
+        B2[k] = tc::f2pack(B[0][2 * k], B[0][2 * k + 1]);
+        N2[k] = tc::f2pack(-B[0][2 * k], -B[0][2 * k + 1]);
+      }
+    }
     T *out0 = static_cast<T *>(rows.out) + tok * rows.out_stride + (long long)h0 * p.d;
     const T *x0 = static_cast<const T *>(rows.x) + tok * rows.x_stride + (long long)h0 * p.d;
     const T *dy0 = BWD ? static_cast<const T *>(rows.dy) + tok * rows.dy_stride + (long long)h0 * p.d : nullptr;
@@ -176,6 +203,81 @@ __global__ void __launch_bounds__(256, BWD || V == 1 ? 1 : 2) norm_rope_kernel(c
             dy[i][n] = *reinterpret_cast<const C *>(dy0 + i * p.d + cb[n]);
           }
         }
+      }
+      if constexpr (AHEAD) {
+        uint64_t gl[HEADS][P], gh[HEADS][P];
+        float ss[HEADS], xs[HEADS];
+        auto values2 = [&](const C &c0, const C &c1, uint64_t (&l)[P], uint64_t (&h)[P]) {
+          float a[V], b[V];
+          c0.get(a);
+          c1.get(b);
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            if (ODD && !two[0]) b[e] = 0.f;
+          pairs(a, b, l, h);
+        };
+#pragma unroll
+        for (int i = 0; i < HEADS; ++i) {
+          ss[i] = xs[i] = 0.f;
+          if (h + i >= h1 || !have[0]) continue;
+          uint64_t xl[P], xh[P], dl[P], dh[P], s2 = 0, t2 = 0;
+          values2(x[i][0], y[i][0], xl, xh);
+          values2(dx[i][0], dy[i][0], dl, dh);
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            gl[i][k] = tc::fma2(dh[k], N2[k], tc::mul2(dl[k], A2[k]));
+            gh[i][k] = tc::fma2(dl[k], B2[k], tc::mul2(dh[k], A2[k]));
+            s2 = tc::fma2(xl[k], xl[k], tc::fma2(xh[k], xh[k], s2));
+            t2 = tc::fma2(tc::mul2(gl[i][k], wl[k]), xl[k], t2);
+            t2 = tc::fma2(tc::mul2(gh[i][k], wh[k]), xh[k], t2);
+          }
+          const float2 s = tc::f2unpack(s2), t = tc::f2unpack(t2);
+          ss[i] = s.x + s.y;
+          xs[i] = t.x + t.y;
+        }
+        for (int o = G / 2; o > 0; o /= 2) {
+#pragma unroll
+          for (int i = 0; i < HEADS; ++i) {
+            ss[i] += __shfl_xor_sync(mask, ss[i], o);
+            xs[i] += __shfl_xor_sync(mask, xs[i], o);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < HEADS; ++i) {
+          if (h + i >= h1 || !have[0]) continue;
+          const float r = rsqrtf(fmaf(ss[i], over_d, p.eps)), pull = -xs[i] * over_d * r * r * r;
+          const uint64_t r2 = tc::f2pack(r, r), p2 = tc::f2pack(pull, pull);
+          uint64_t xl[P], xh[P];
+          values2(x[i][0], y[i][0], xl, xh);
+          float oa[V], ob[V];
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            const uint64_t vl = tc::mul2(gl[i][k], r2), vh = tc::mul2(gh[i][k], r2);
+            sl[k] = tc::fma2(vl, xl[k], sl[k]);
+            sh[k] = tc::fma2(vh, xh[k], sh[k]);
+            const float2 ol = tc::f2unpack(tc::fma2(xl[k], p2, tc::mul2(vl, wl[k])));
+            const float2 oh = tc::f2unpack(tc::fma2(xh[k], p2, tc::mul2(vh, wh[k])));
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int e = 2 * k + q;
+              const float l1 = q ? ol.y : ol.x, h1_ = q ? oh.y : oh.x;
+              if constexpr (INTER) {
+                float *o = e < V / 2 ? oa : ob;
+                o[2 * e % V] = l1;
+                o[2 * e % V + 1] = h1_;
+              } else {
+                oa[e] = l1;
+                ob[e] = h1_;
+              }
+            }
+          }
+          C ra, rb;
+          ra.set(oa);
+          rb.set(ob);
+          *reinterpret_cast<C *>(out0 + i * p.d + ca[0]) = ra;
+          if (two[0]) *reinterpret_cast<C *>(out0 + i * p.d + cb[0]) = rb;
+        }
+        continue;
       }
       // a head's values in fp32 (what a lane does not have is zero), and its gradients turned back
       auto values = [&](int i, int n, float (&a)[V], float (&b)[V]) {
@@ -264,6 +366,20 @@ __global__ void __launch_bounds__(256, BWD || V == 1 ? 1 : 2) norm_rope_kernel(c
   if constexpr (BWD) {
     if (!p.part) return;
     float *sums = &red[0][0];  // [run][d]
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float2 l = tc::f2unpack(sl[e / 2]), h = tc::f2unpack(sh[e / 2]);
+        const float l1 = e % 2 ? l.y : l.x, h1_ = e % 2 ? h.y : h.x;
+        if constexpr (INTER) {
+          (e < V / 2 ? sa : sb)[0][2 * e % V] = l1;
+          (e < V / 2 ? sa : sb)[0][2 * e % V + 1] = h1_;
+        } else {
+          sa[0][e] = l1;
+          sb[0][e] = h1_;
+        }
+      }
+    }
 #pragma unroll
     for (int n = 0; n < NU; ++n)
 #pragma unroll
