@@ -122,15 +122,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     mbar_init_fence();
   }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_holder), C::TMEM);
-    tmem_relinquish();
-  }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&k_map);
     tma_prefetch_desc(&v_map);
   }
   pdl_wait();
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), C::TMEM);
+    tmem_relinquish();
+  }
   const Run run = run_of<kN, kThreads>(p, reinterpret_cast<long long *>(smem + C::OFF_RED));
   // (here, ahead of the roles: a 64-bit division is a call, which code that changes its registers cannot make)
   Walk<kN> w(p);

@@ -153,15 +153,15 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
     *abort_flag = 0;
     mbar_init_fence();
   }
-  if (warp == 5) {
-    tmem_alloc(smem_u32(tmem_holder), C::TMEM);
-    tmem_relinquish();
-  }
   if (warp == 4 && lane == 0) {
     tma_prefetch_desc(&k_map);
     tma_prefetch_desc(&v_map);
   }
   pdl_wait();
+  if (warp == 5) {
+    tmem_alloc(smem_u32(tmem_holder), C::TMEM);
+    tmem_relinquish();
+  }
 
   const Run run = run_of<kKeys, 192>(p, red);
   Walk<kKeys> w(p);

@@ -1191,6 +1191,7 @@ template <int MODE, int DQK, int DV, int IR, int NBUF, int NSTAGE, int NSTAGE1, 
           int PST1 = 0>
 cudaError_t launch_bwd(const Params &p, cudaStream_t st) {
   using C = BwdCfg<MODE, DQK, DV, IR, NBUF, NSTAGE, NSTAGE1, NBS>;
+  static_assert(2 * C::SMEM > 227 * 1024, "two CTAs of an SM would wait for each other's TMEM (tc_common.cuh, pdl_wait)");
   const int bf = p.dtype == VLF_BF16;
   BwdMaps m;
   const uint64_t tq = p.total_q, tk = p.total_kv;

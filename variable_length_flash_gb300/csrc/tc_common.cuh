@@ -33,6 +33,10 @@ __device__ __forceinline__ uint64_t globaltimer() {
 // it in the stream has finished: it must wait (griddepcontrol.wait) for that kernel's completion
 // and memory before reading anything global.  pdl_trigger lets the kernel after this one be
 // launched as soon as every CTA of this one has issued it.  (No-ops for a normal launch.)
+// A kernel that triggers at its start may allocate its TMEM after the next kernel's CTAs are resident, so
+// none of these may hold TMEM ahead of its own wait: the kernel before would wait for columns that only its own
+// end sets free.  (The backward's later kernels wait at their end; a CTA of theirs and one of the kernel before
+// do not fit an SM's shared memory together.)
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
