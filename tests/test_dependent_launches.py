@@ -49,3 +49,12 @@ def test_no_tensor_memory_is_held_ahead_of_the_wait(name):
     for kernel, body in kernels(source(name)):
         if "pdl_wait()" in body and "tmem_alloc(" in body:
             assert body.index("pdl_wait()") < body.index("tmem_alloc("), kernel
+
+
+SERVING = ["norm_rope.cu", "pages.cu", "pages_tc.cu", "pages_tc.cuh", "pages_rows.cu", "rope.cuh", "e4m3.cuh"]
+
+
+@pytest.mark.parametrize("name", SERVING)
+def test_what_the_kernel_ahead_writes_is_not_read_as_constant(name):
+    """__ldg asks that nobody writes the memory from the kernel's start on; these start before the one ahead ends."""
+    assert not re.search(r"__ldg\b|ld\.global\.nc|__restrict__", source(name))

@@ -10,6 +10,11 @@
 
 namespace vlf {
 
+// A load of what the kernel ahead in the stream may have written, where this one may start before that one ends
+// (tc_common.cuh, pdl_wait): a plain one.  __ldg is for memory that nobody writes from the kernel's start on, and the
+// compiler may move it ahead of the wait.
+template <typename T> __device__ __forceinline__ T ld(const T *p) { return *p; }
+
 // Everything a kernel needs, passed by value (kernel parameter space).
 struct Params {
   const void *q, *k, *v;

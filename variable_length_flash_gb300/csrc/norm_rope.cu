@@ -32,7 +32,7 @@ constexpr int kMostBlocks = 152 * 2;  // of the backward: the parts of dw that t
 
 __device__ __forceinline__ float weight_at(const void *w, int dtype, int c) {
   if (!w) return 1.f;
-  if (dtype == VLF_F32) return __ldg(static_cast<const float *>(w) + c);
+  if (dtype == VLF_F32) return ld(static_cast<const float *>(w) + c);
   if (dtype == VLF_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[c]);
   return __half2float(static_cast<const __half *>(w)[c]);
 }
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(256, BWD || V == 1 ? 1 : 2) norm_rope_kernel(c
   const Rows &rows = is_k ? p.k : p.q;
   tc::pdl_trigger();
   tc::pdl_wait();
-  for (int c = threadIdx.x; c < half; c += 256) F[c] = turns_of(__ldg(p.inv_freq + c));
+  for (int c = threadIdx.x; c < half; c += 256) F[c] = turns_of(ld(p.inv_freq + c));
   for (int c = threadIdx.x; c < 256 + 8; c += 256) w[c] = c < p.d ? weight_at(rows.w, p.w_dtype, c) : 0.f;
   __syncthreads();
   const int ntail = ((p.d - p.rot + V - 1) / V + 1) / 2, units = nrot + ntail;
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(256, BWD || V == 1 ? 1 : 2) norm_rope_kernel(c
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         float cs = 1.f, sn = 0.f;
-        if (rot[n]) turn(__ldg(p.positions + (long long)at.axis[e] * p.total + tok), F[at.pair[e]], cs, sn);
+        if (rot[n]) turn(ld(p.positions + (long long)at.axis[e] * p.total + tok), F[at.pair[e]], cs, sn);
         if (BWD) sn = -sn;
         A[n][e] = cs;
         B[n][e] = sn;

@@ -87,10 +87,10 @@ __global__ void __launch_bounds__(NT) pages_write_kernel(const PagesWriteParams 
   int s = 0, hi = p.num_seqs;
   while (hi - s > 1) {
     const int mid = (s + hi) / 2;
-    if ((__ldg(p.cu + mid) >> p.log2_page) + 2 * mid <= unit) s = mid;
+    if ((ld(p.cu + mid) >> p.log2_page) + 2 * mid <= unit) s = mid;
     else hi = mid;
   }
-  const int t0 = __ldg(p.cu + s), t1 = __ldg(p.cu + s + 1), len = __ldg(p.kv_lens + s);
+  const int t0 = ld(p.cu + s), t1 = ld(p.cu + s + 1), len = ld(p.kv_lens + s);
   if (t0 < 0 || t0 > t1 || t1 > p.total || len < t1 - t0 || (len > 0 && (len - 1) >> p.log2_page >= p.max_pages)) {
     if (threadIdx.x == 0) set_error(p.err, VLF_ERR_BAD_SEQLENS);
     return;
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(NT) pages_write_kernel(const PagesWriteParams 
   const int first = len - (t1 - t0), nth = unit - ((t0 >> p.log2_page) + 2 * s);
   const int index = (first >> p.log2_page) + nth;
   if (nth < 0 || index > (len - 1) >> p.log2_page) return;
-  const int page = __ldg(p.table + (long long)s * p.max_pages + index);
+  const int page = ld(p.table + (long long)s * p.max_pages + index);
   if (page < 0 || page >= p.num_pages) {
     if (threadIdx.x == 0) set_error(p.err, VLF_ERR_BAD_PAGES);
     return;
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const PagesCopyParams p
   float *scale = is_v ? p.v_scale : p.k_scale;
   const int i0 = blockIdx.x * p.chunk, i1 = min(i0 + p.chunk, p.n);
   for (int i = i0; i < i1; ++i) {
-    const int src = __ldg(p.src + i), dst = __ldg(p.dst + i);
+    const int src = ld(p.src + i), dst = ld(p.dst + i);
     if (src < 0) continue;
     if (src >= p.num_pages || dst < 0 || dst >= p.num_pages) {
       if (threadIdx.x == 0) set_error(p.err, VLF_ERR_BAD_PAGES);
@@ -322,8 +322,8 @@ struct Row {
   bool part;
 };
 __device__ __forceinline__ Row row_of(const PagesForkParams &p, int s) {
-  Row r{__ldg(p.parents + s), 0, 0, false};
-  if (r.parent >= 0 && r.parent < p.num_in) r.len = max(0, __ldg(p.lens + r.parent));
+  Row r{ld(p.parents + s), 0, 0, false};
+  if (r.parent >= 0 && r.parent < p.num_in) r.len = max(0, ld(p.lens + r.parent));
   r.whole = r.len >> p.log2_page;
   r.part = (r.len & ((1 << p.log2_page) - 1)) != 0;
   return r;
@@ -337,7 +337,7 @@ __device__ __forceinline__ int held(const PagesForkParams &p, int i) {
 __device__ __forceinline__ int part_of(const PagesForkParams &p, const Row &r, int s, bool &keeps) {
   keeps = false;
   if (!r.part || r.whole >= p.max_pages) return -1;
-  const int page = __ldg(p.table + (long long)r.parent * p.max_pages + r.whole);
+  const int page = ld(p.table + (long long)r.parent * p.max_pages + r.whole);
   if (page < 0 || page >= p.num_pages) return -1;
   keeps = p.outside[page] + p.whole[page] == 0 && p.owner[page] == s;
   return page;
@@ -367,14 +367,14 @@ __global__ void __launch_bounds__(256) fork_count_kernel(const PagesForkParams p
     const int s = y - p.num_in;
     Row r{y, 0, 0, false};
     if (old) {
-      r.len = __ldg(p.lens + y);
+      r.len = ld(p.lens + y);
       if (r.len < 0 || pages_of(r.len, p.log2_page) > p.max_pages) {
         if (j == 0) p.state[0] = VLF_ERR_BAD_SEQLENS;
         continue;
       }
     } else {
       r = row_of(p, s);
-      const int grow = __ldg(p.grow + s);
+      const int grow = ld(p.grow + s);
       if (j == 0 && r.parent >= p.num_in) p.state[0] = VLF_ERR_BAD_PAGES;
       if (grow < 0 || (long long)r.len + grow > (long long)p.max_pages << p.log2_page) {
         if (j == 0) p.state[0] = VLF_ERR_BAD_SEQLENS;
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(256) fork_count_kernel(const PagesForkParams p
       }
     }
     if (j >= min(pages_of(r.len, p.log2_page), p.max_pages)) continue;
-    const int page = __ldg(p.table + (long long)r.parent * p.max_pages + j);
+    const int page = ld(p.table + (long long)r.parent * p.max_pages + j);
     if (page < 0 || page >= p.num_pages) p.state[0] = VLF_ERR_BAD_PAGES;
     else if (old) atomicSub(p.outside + page, 1);
     else if (j < r.whole) atomicAdd(p.whole + page, 1);
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(256) fork_free_kernel(const PagesForkParams p)
     const Row r = row_of(p, s);
     bool keeps;
     const int page = part_of(p, r, s, keeps);
-    const long long to = min((long long)r.len + max(0, __ldg(p.grow + s)), (long long)p.max_pages << p.log2_page);
+    const long long to = min((long long)r.len + max(0, ld(p.grow + s)), (long long)p.max_pages << p.log2_page);
     n = pages_of((int)to, p.log2_page) - pages_of(r.len, p.log2_page) + (page >= 0 && !keeps);
   }
   int sum;
@@ -471,13 +471,20 @@ __global__ void __launch_bounds__(256) fork_end_kernel(const PagesForkParams p) 
   bool keeps;
   const int part = part_of(p, r, s, keeps);
   const bool copy = ok && part >= 0 && !keeps;
-  const int len = ok ? r.len + __ldg(p.grow + s) : 0, has = pages_of(len, p.log2_page);
+  const int len = ok ? r.len + ld(p.grow + s) : 0, has = pages_of(len, p.log2_page);
   const int32_t *row = p.table + (long long)r.parent * p.max_pages;
   int *out = p.table_out + (long long)s * p.max_pages;
   const int shared = ok ? r.whole + (keeps ? 1 : 0) : 0;  // entries that stay
-#pragma unroll 4
-  for (int j = threadIdx.x; j < p.max_pages; j += 256)
-    if (j < shared || j >= has) out[j] = j >= has ? -1 : j < r.whole ? __ldg(row + j) : part;
+  for (int j0 = threadIdx.x; j0 < p.max_pages; j0 += 4 * 256) {
+    int x[4];  // (loads in flight together: a store between them would hold the next one up)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = j0 + 256 * k < min(r.whole, has) ? ld(row + j0 + 256 * k) : part;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = j0 + 256 * k;
+      if (j < p.max_pages && (j < shared || j >= has)) out[j] = j >= has ? -1 : x[k];
+    }
+  }
   if (threadIdx.x >= 32) return;
   // the new pages are the free ones of ranks sum, sum + 1, ...; a lane looks at eight chunks
   const long long end = sum + has - shared;
@@ -566,14 +573,14 @@ __global__ void __launch_bounds__(1024) fork_small_kernel(PagesForkParams p) {
     const int s = y - p.num_in;
     Row r{y, 0, 0, false};
     if (s < 0) {
-      r.len = __ldg(p.lens + y);
+      r.len = ld(p.lens + y);
       if (r.len < 0 || pages_of(r.len, p.log2_page) > p.max_pages) {
         if (lane == 0) bad = VLF_ERR_BAD_SEQLENS;
         continue;
       }
     } else {
       r = row_of(p, s);
-      const int grow = __ldg(p.grow + s);
+      const int grow = ld(p.grow + s);
       if (lane == 0 && r.parent >= p.num_in) bad = VLF_ERR_BAD_PAGES;
       if (grow < 0 || (long long)r.len + grow > (long long)p.max_pages << p.log2_page) {
         if (lane == 0) bad = VLF_ERR_BAD_SEQLENS;
@@ -583,7 +590,7 @@ __global__ void __launch_bounds__(1024) fork_small_kernel(PagesForkParams p) {
     const int n = min(pages_of(r.len, p.log2_page), p.max_pages);
     const int32_t *row = p.table + (long long)r.parent * p.max_pages;
     for (int j = lane; j < n; j += 32) {
-      const int page = __ldg(row + j);
+      const int page = ld(row + j);
       if (page < 0 || page >= p.num_pages) bad = VLF_ERR_BAD_PAGES;
       else if (s < 0) atomicSub(p.outside + page, 1);
       else if (j < r.whole) atomicAdd(p.whole + page, 1);
@@ -608,7 +615,7 @@ __global__ void __launch_bounds__(1024) fork_small_kernel(PagesForkParams p) {
   if (t < p.num_out) {
     mine = row_of(p, t);
     part = part_of(p, mine, t, keeps);
-    const long long to = min((long long)mine.len + max(0, __ldg(p.grow + t)), (long long)p.max_pages << p.log2_page);
+    const long long to = min((long long)mine.len + max(0, ld(p.grow + t)), (long long)p.max_pages << p.log2_page);
     more = pages_of((int)to, p.log2_page) - pages_of(mine.len, p.log2_page) + (part >= 0 && !keeps);
   }
   const int at = before_1024(more, need);  // (at most kSmallEntries pages)
@@ -621,7 +628,7 @@ __global__ void __launch_bounds__(1024) fork_small_kernel(PagesForkParams p) {
   }
   if (t < p.num_out) {
     const bool copy = ok && part >= 0 && !keeps;
-    p.lens_out[t] = ok ? mine.len + __ldg(p.grow + t) : 0;
+    p.lens_out[t] = ok ? mine.len + ld(p.grow + t) : 0;
     p.src[t] = copy ? part : -1;
     p.dst[t] = copy ? list[at] : -1;
   }
@@ -635,11 +642,11 @@ __global__ void __launch_bounds__(1024) fork_small_kernel(PagesForkParams p) {
     const Row r = row_of(p, s);
     bool keep;
     const int page = part_of(p, r, s, keep);
-    const int has = ok ? pages_of(r.len + __ldg(p.grow + s), p.log2_page) : 0, stay = r.whole + (keep ? 1 : 0);
+    const int has = ok ? pages_of(r.len + ld(p.grow + s), p.log2_page) : 0, stay = r.whole + (keep ? 1 : 0);
     const int32_t *row = p.table + (long long)r.parent * p.max_pages;
     int *out = p.table_out + (long long)s * p.max_pages;
     for (int j = lane; j < p.max_pages; j += 32)
-      out[j] = j >= has ? -1 : j < r.whole ? __ldg(row + j) : j < stay ? page : list[begin[s] + j - stay];
+      out[j] = j >= has ? -1 : j < r.whole ? ld(row + j) : j < stay ? page : list[begin[s] + j - stay];
   }
 }
 
@@ -751,9 +758,15 @@ __global__ void __launch_bounds__(1024) compact_small_kernel(const PagesCompactP
     if (n > 0) p.refs_out[to] = n;
     if (i >= used) p.refs_out[i] = 0;
   }
-  for (int i = t; i < (int)p.entries; i += 1024) {
-    const int page = __ldg(p.table + i);
-    p.table_out[i] = page >= 0 && page < p.num_pages && __ldg(p.refs + page) > 0 ? moved(page) : -1;
+  for (int i0 = t; i0 < (int)p.entries; i0 += 4 * 1024) {
+    int page[4];  // (loads in flight together: a store between them would hold the next one up)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) page[k] = i0 + 1024 * k < (int)p.entries ? ld(p.table + i0 + 1024 * k) : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) page[k] = page[k] >= 0 && page[k] < p.num_pages && ld(p.refs + page[k]) > 0 ? moved(page[k]) : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i0 + 1024 * k < (int)p.entries) p.table_out[i0 + 1024 * k] = page[k];
   }
   if (t == 0) *p.used = used;
 }

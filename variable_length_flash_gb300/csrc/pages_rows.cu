@@ -190,13 +190,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto id_of = [&](int m) {
           const int i = ((tile + m) * kN >> log2_page) + lane;
           if (m >= n || lane >= npt || i > (hi - 1) >> log2_page || i < lo >> log2_page) return -2;  // no key in it
-          return max(__ldg(row + i), -1);
+          return max(ld(row + i), -1);
         };
         auto real = [&](int id) { return id >= 0 && id < p.a.num_pages; };
         auto scale_of = [&](int id) {
           if (!real(id)) return make_float2(0.f, 0.f);
           const long long at = (long long)id * b.h_kv + kv_head;
-          return make_float2(__ldg(p.a.k_scale + at), __ldg(p.a.v_scale + at));
+          return make_float2(ld(p.a.k_scale + at), ld(p.a.v_scale + at));
         };
         int id = id_of(0), next = id_of(1);
         float2 sc = scale_of(id);
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               int row2 = 0, head2 = 0;
               y4[k] = make_uint4(0, 0, 0, 0);
               if (r2 < L && place(x, t * L + r2, row2, head2))
-                y4[k] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(b.q) + ((long long)(x->q0 + row2) * b.h_q + head2) * D) + piece);
+                y4[k] = ld(reinterpret_cast<const uint4 *>(static_cast<const T *>(b.q) + ((long long)(x->q0 + row2) * b.h_q + head2) * D) + piece);
             }
     #pragma unroll
             for (int k = 0; k < FLY; ++k) {

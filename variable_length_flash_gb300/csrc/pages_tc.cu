@@ -189,14 +189,14 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
         // a lane has a page of the next 32, and one of the 32 behind them
         auto id_of = [&](int i) {
           if (i > last || i < w.lo >> log2_page) return -2;  // no key of the run's in it
-          return max(__ldg(row + i), -1);
+          return max(ld(row + i), -1);
         };
         auto real = [&](int id) { return id >= 0 && id < p.a.num_pages; };
         int id = id_of(first + lane), id_next = id_of(first + 32 + lane);
         auto scale_of = [&](int i) {
           if (!real(i)) return make_float2(0.f, 0.f);
           const long long at = (long long)i * b.h_kv + w.head;
-          return make_float2(__ldg(p.a.k_scale + at), __ldg(p.a.v_scale + at));
+          return make_float2(ld(p.a.k_scale + at), ld(p.a.v_scale + at));
         };
         float2 sc = scale_of(id), sc_next = make_float2(0.f, 0.f);
         for (int m = 0; m < n && ok; ++m) {
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
         const bool have = c < NC && column_of(p, NC, w, c, row, head);
         const T *q = static_cast<const T *>(b.q) + ((long long)(w.q0 + row) * b.h_q + head) * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) raw[i][e] = have ? __ldg(reinterpret_cast<const uint32_t *>(q) + e) : 0;
+        for (int e = 0; e < E / 2; ++e) raw[i][e] = have ? ld(reinterpret_cast<const uint32_t *>(q) + e) : 0;
       }
 #pragma unroll
       for (int i = 0; i < PER; ++i) {

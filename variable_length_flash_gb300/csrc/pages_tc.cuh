@@ -38,8 +38,8 @@ template <int KEYS> struct Walk {
     s = seq;
     const TcParams &p = *at;
     const Params &b = p.a.p;
-    const int x = __ldg(b.cu_q + s), y = __ldg(b.cu_q + s + 1);
-    len = __ldg(p.a.kv_lens + s);
+    const int x = ld(b.cu_q + s), y = ld(b.cu_q + s + 1);
+    len = ld(p.a.kv_lens + s);
     q0 = x;
     q_len = y - x;
     tiles_q = 0;
