@@ -58,3 +58,10 @@ SERVING = ["norm_rope.cu", "pages.cu", "pages_tc.cu", "pages_tc.cuh", "pages_row
 def test_what_the_kernel_ahead_writes_is_not_read_as_constant(name):
     """__ldg asks that nobody writes the memory from the kernel's start on; these start before the one ahead ends."""
     assert not re.search(r"__ldg\b|ld\.global\.nc|__restrict__", source(name))
+
+
+@pytest.mark.parametrize("name", ["tc_fwd.cu", "prefix.cu", "key_weights.cu", "common.cuh", "tc_common.cuh"])
+def test_nor_by_the_forward_and_the_decoding_kernels(name):
+    """The forward, shared-prefix attention and key weights start so where their grids are small.  (The others' __ldg is
+    right: their first kernel is launched plainly, and reads inputs.)"""
+    assert not re.search(r"__ldg\b|ld\.global\.nc|__restrict__", source(name))

@@ -107,8 +107,8 @@ __device__ __forceinline__ bool seq_from(const Params &p, int a, int b, int c, i
 }
 
 __device__ __forceinline__ bool load_seq(const Params &p, int s, Seq &sq) {
-  return seq_from(p, __ldg(p.cu_q + s), __ldg(p.cu_q + s + 1), __ldg(p.cu_kv + s),
-                  __ldg(p.cu_kv + s + 1), sq);
+  return seq_from(p, ld(p.cu_q + s), ld(p.cu_q + s + 1), ld(p.cu_kv + s),
+                  ld(p.cu_kv + s + 1), sq);
 }
 
 // ---------------------------------------------------------------- tile scheduler (band math)
@@ -179,7 +179,7 @@ __device__ __forceinline__ void visible_rows(int j, int off, int q_len, int caus
 __device__ __forceinline__ float bias_at(const Params &p, int grow, int h, int j) {
   const int bh = p.bias_heads == 1 ? 0 : h;
   const size_t off = ((size_t)grow * (size_t)p.bias_heads + (size_t)bh) * (size_t)p.max_kv + (size_t)j;
-  return __ldg(p.bias + off);
+  return ld(p.bias + off);
 }
 
 }  // namespace vlf

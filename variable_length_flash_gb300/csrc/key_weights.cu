@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(kThreads) simt_key_weights_kernel(const KeyWei
   const int s = blockIdx.z, hk = blockIdx.y, j0 = blockIdx.x * kKeys;
   Seq sq;
   if (!load_seq(p, s, sq)) return;
-  if (s == 0 && (__ldg(p.cu_q) != 0 || __ldg(p.cu_kv) != 0)) set_error(p.err, VLF_ERR_BAD_SEQLENS);
+  if (s == 0 && (ld(p.cu_q) != 0 || ld(p.cu_kv) != 0)) set_error(p.err, VLF_ERR_BAD_SEQLENS);
   if (s == p.num_seqs - 1 && (sq.q0 + sq.q_len != p.total_q || sq.k0 + sq.kv_len != p.total_kv))
     set_error(p.err, VLF_ERR_BAD_SEQLENS);
   if (j0 >= sq.kv_len) return;
@@ -166,7 +166,7 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
   const int s = STREAM_K ? (int)blockIdx.z : (int)blockIdx.z / pl.splits, hk = blockIdx.y;
   Seq sq;
   if (!load_seq(p, s, sq)) return;
-  if (s == 0 && (__ldg(p.cu_q) != 0 || __ldg(p.cu_kv) != 0)) set_error(p.err, VLF_ERR_BAD_SEQLENS);
+  if (s == 0 && (ld(p.cu_q) != 0 || ld(p.cu_kv) != 0)) set_error(p.err, VLF_ERR_BAD_SEQLENS);
   if (s == p.num_seqs - 1 && (sq.q0 + sq.q_len != p.total_q || sq.k0 + sq.kv_len != p.total_kv))
     set_error(p.err, VLF_ERR_BAD_SEQLENS);
   // key tiles [t0, t1) of this CTA (one where the columns stream)
@@ -325,7 +325,7 @@ tc_key_weights_kernel(const __grid_constant__ KwMaps maps, const KeyWeightParams
       for (int e = 0; e < 4; ++e) {
         x[e] = -INFINITY;
         if (lane + 32 * e < valid && r0 + ri[e] < sq.q_len)
-          x[e] = __ldg(kp.lse + (size_t)(h0 + hi_[e]) * p.total_q + sq.q0 + r0 + ri[e]);
+          x[e] = ld(kp.lse + (size_t)(h0 + hi_[e]) * p.total_q + sq.q0 + r0 + ri[e]);
       }
     };
     float next[4];

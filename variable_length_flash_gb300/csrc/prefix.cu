@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) simt_prefix_kernel(const PrefixParam
   const int s = blockIdx.z, h = blockIdx.y, hk = h / p.group;
   Seq sq;
   if (!load_seq(p, s, sq)) return;
-  if (s == 0 && (__ldg(p.cu_q) != 0 || __ldg(p.cu_kv) != 0)) set_error(p.err, VLF_ERR_BAD_SEQLENS);
+  if (s == 0 && (ld(p.cu_q) != 0 || ld(p.cu_kv) != 0)) set_error(p.err, VLF_ERR_BAD_SEQLENS);
   if (s == p.num_seqs - 1 && (sq.q0 + sq.q_len != p.total_q || sq.k0 + sq.kv_len != p.total_kv))
     set_error(p.err, VLF_ERR_BAD_SEQLENS);
   const int r0 = blockIdx.x * kRows;
@@ -270,7 +270,7 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
     hd = x % pl.heads;
     const int s = x / pl.heads;
     if (!load_seq(p, s, sq)) return;
-    if (s == 0 && (__ldg(p.cu_q) != 0 || __ldg(p.cu_kv) != 0)) set_error(p.err, VLF_ERR_BAD_SEQLENS);
+    if (s == 0 && (ld(p.cu_q) != 0 || ld(p.cu_kv) != 0)) set_error(p.err, VLF_ERR_BAD_SEQLENS);
     if (s == p.num_seqs - 1 && (sq.q0 + sq.q_len != p.total_q || sq.k0 + sq.kv_len != p.total_kv))
       set_error(p.err, VLF_ERR_BAD_SEQLENS);
     if (p.causal) rb = pl.rb_own - 1 - rb;  // the rows that see most first
@@ -325,8 +325,8 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
     if (threadIdx.x < 128) seq_of[threadIdx.x] = 0xffff;
     __syncthreads();
     for (int s = threadIdx.x; s < p.num_seqs; s += 256) {
-      const int a = __ldg(p.cu_q + s), b = __ldg(p.cu_q + s + 1);
-      const int c = __ldg(p.cu_kv + s), d = __ldg(p.cu_kv + s + 1);
+      const int a = ld(p.cu_q + s), b = ld(p.cu_q + s + 1);
+      const int c = ld(p.cu_kv + s), d = ld(p.cu_kv + s + 1);
       if (a < 0 || a > b || b > p.total_q || b - a > p.max_q || c < 0 || c > d || d > p.total_kv || d - c > p.max_kv)
         continue;  // (recorded by that sequence's own CTAs)
       const int x = max(a, row0), y = min(b, row0 + nrows);
@@ -478,8 +478,8 @@ tc_prefix_kernel(const __grid_constant__ PfxMaps maps, const PrefixParams pp, co
       const int s = seq_of[row_ok ? tok : 0];
       row_ok = row_ok && s != 0xffff;
       if (row_ok) {
-        const int q0 = __ldg(p.cu_q + s), ql = __ldg(p.cu_q + s + 1) - q0;
-        const int ks = P + __ldg(p.cu_kv + s + 1) - __ldg(p.cu_kv + s);
+        const int q0 = ld(p.cu_q + s), ql = ld(p.cu_q + s + 1) - q0;
+        const int ks = P + ld(p.cu_kv + s + 1) - ld(p.cu_kv + s);
         visible_range(grow - q0, ks - ql, ks, p.causal, p.window, vlo, vhi);
       }
     } else if (row_ok) {
@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const Params p, int p
   const size_t pairs = (size_t)p.total_q * p.h_q;
   const size_t w = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (w >= pairs || w / p.h_q >= (size_t)max(0, __ldg(p.cu_q + p.num_seqs))) return;
+  if (w >= pairs || w / p.h_q >= (size_t)max(0, ld(p.cu_q + p.num_seqs))) return;
   constexpr int NL = D / 4;                // lanes per part
   constexpr int PER = NL <= 16 ? 2 : 1;    // parts at a time
   constexpr int FLY = 12;                  // their loads in flight, together with the log-sum-exps'

@@ -197,7 +197,7 @@ tc_fwd_kernel(const __grid_constant__ typename FwdMapsFor<DQK, PACK, BIAS>::type
   const int s = SPLIT ? (int)blockIdx.z / p.kv_splits : (int)blockIdx.z;
   Seq sq;
   if (!load_seq(p, s, sq)) return;
-  if (s == 0 && (__ldg(p.cu_q) != 0 || __ldg(p.cu_kv) != 0)) set_error(p.err, VLF_ERR_BAD_SEQLENS);
+  if (s == 0 && (ld(p.cu_q) != 0 || ld(p.cu_kv) != 0)) set_error(p.err, VLF_ERR_BAD_SEQLENS);
   if (s == p.num_seqs - 1 && (sq.q0 + sq.q_len != p.total_q || sq.k0 + sq.kv_len != p.total_kv))
     set_error(p.err, VLF_ERR_BAD_SEQLENS);
   // heavy (late, long-band) row blocks first under causal masking; heads_fast swaps the grid's
@@ -227,10 +227,10 @@ tc_fwd_kernel(const __grid_constant__ typename FwdMapsFor<DQK, PACK, BIAS>::type
     if (p.bias_blocks && ti.hi > ti.lo) {
       const int hb = p.bias_heads == 1 ? 0 : ti.head[0];
       const int4 *bb = p.bias_blocks + (size_t)hb * p.total_q + sq.q0 + ti.row0[0];
-      const int4 e0 = __ldg(bb);
+      const int4 e0 = ld(bb);
       int blo = e0.x, bhi = e0.y, pure = e0.z >= 0;
       if (ti.row0[0] + 64 < sq.q_len) {
-        const int4 e1 = __ldg(bb + 64);
+        const int4 e1 = ld(bb + 64);
         if (e1.y > e1.x) {
           blo = bhi > blo ? min(blo, e1.x) : e1.x;
           bhi = max(bhi, e1.y);
@@ -478,7 +478,7 @@ tc_fwd_kernel(const __grid_constant__ typename FwdMapsFor<DQK, PACK, BIAS>::type
     int rlo = 0, rhi = sq.kv_len;
     if (BIAS && cta_pure && row_ok) {
       const int bh = p.bias_heads == 1 ? 0 : head;
-      const int4 e = __ldg(p.bias_rows + (size_t)bh * p.total_q + sq.q0 + i);
+      const int4 e = ld(p.bias_rows + (size_t)bh * p.total_q + sq.q0 + i);
       rlo = e.x;
       rhi = e.y;
     }
@@ -604,7 +604,7 @@ tc_fwd_kernel(const __grid_constant__ typename FwdMapsFor<DQK, PACK, BIAS>::type
             const float4 *b4 = reinterpret_cast<const float4 *>(brow + kb);
 #pragma unroll
             for (int q = 0; q < kBN / 4; ++q) {
-              const float4 bq = __ldg(b4 + q);
+              const float4 bq = ld(b4 + q);
               v[4 * q + 0] = __float_as_uint(fmaf(bq.x, kLog2e, __uint_as_float(v[4 * q + 0]) * sl2));
               v[4 * q + 1] = __float_as_uint(fmaf(bq.y, kLog2e, __uint_as_float(v[4 * q + 1]) * sl2));
               v[4 * q + 2] = __float_as_uint(fmaf(bq.z, kLog2e, __uint_as_float(v[4 * q + 2]) * sl2));
@@ -614,7 +614,7 @@ tc_fwd_kernel(const __grid_constant__ typename FwdMapsFor<DQK, PACK, BIAS>::type
 #pragma unroll
             for (int e = 0; e < kBN; ++e) {
               float x = __uint_as_float(v[e]) * sl2;
-              if (BIAS && brow) x = fmaf(__ldg(brow + min(kb + e, sq.kv_len - 1)), kLog2e, x);
+              if (BIAS && brow) x = fmaf(ld(brow + min(kb + e, sq.kv_len - 1)), kLog2e, x);
               v[e] = __float_as_uint(x);
             }
           }
