@@ -581,8 +581,9 @@ int vlf_pages_write(const void *k, int64_t k_stride, const void *v, int64_t v_st
  * outside the pool.  What other bytes of a page hold never reaches a row, but a value of its own sequence
  * that is NaN may also reach rows that do not see its key.  A row that sees a NaN logit is NaN, and so is
  * its lse.  Tensor-core kernels for F16 / BF16 and d_qk = d_v in {64, 128}; fp32 FMA otherwise.  On the
- * tensor cores the value scales of a sequence's pages lie within a factor of 2^100 of one another (a key
- * whose page's scale is further below the others' may lose its weight).  max_seqlen_q decides which kernel
+ * tensor cores a weight times its page's value scale is held to 11 bits, and to 2^-24 of the largest such product of
+ * the keys that the row sees; a value scale more than 2^100 below that key's may cost the key its part of the lse.
+ * Scales of pages that a row does not see do not matter to it.  max_seqlen_q decides which kernel
  * runs: more than 32 rows of a kv head's group (max_seqlen_q * h_q / h_kv) take the one for many rows, so a
  * loose bound makes single rows slower (2.7 times, in large batches), never wrong.  No backward.
  */

@@ -1,14 +1,15 @@
 // Attention over pages in e4m3 for many query rows (prompts, extended chats), 16-bit queries, widths 64 and 128:
 // rows are the rows of the products, as in the forward (tc_fwd.cu), and a key tile serves 256 of them.
 //
-// The products are tcgen05 kind::f16 in fp16.  An e4m3 number is an fp16 number, so four warps turn the
+// The products are tcgen05 kind::f16 in fp16.  An e4m3 number is an fp16 number, so eight warps turn the
 // bytes of a tile into fp16 tiles in shared memory, exactly, once for two query tiles; a query is brought to
 // [128, 256) by a power of two for its row, where fp16 holds bf16's 8 bits down to 2^-24 of the row's largest
-// (fp16 queries are taken as they are).  Scales of pages: a tile has one for its keys and one for its values,
-// the largest of its pages' (of 64 and more tokens: the page's own); smaller ones of other pages are multiplied
-// into the fp16 numbers, powers of two.  The key scale goes into the softmax's scale, the value scale into the
-// exponent, as in pages_tc.cu, whose runs of key tiles, parts and join these are as well.  P is rounded to
-// fp16 with the row's largest between 2^7 and 2^15: half a step of 2^-11, nothing above 2^-31 of the largest lost.
+// (fp16 queries are taken as they are).  Scales of pages stay out of the fp16 numbers: a page's key scale multiplies the
+// logits of its keys, its value scale goes into their exponent, as in pages_tc.cu, whose runs of key tiles, parts
+// and join these are as well.  (Tiles that held their pages' values over the largest scale of a page lost those of pages
+// 2^16 below it, which a row that sees no other page needs.)  A tile of 64 keys has one page, or, SMALL, two or four.
+// P is rounded to fp16 with the row's largest between 2^7 and 2^15: half a step of 2^-11, nothing above 2^-31 of the
+// largest lost.
 //
 // Roles of a CTA (one per SM): warp 0 page loads, warp 1 S = Q K^T, warp 2 O += P V, warp 3 the items of the CTA's
 // run, which it lays out in shared memory for the others (their registers are full without it), warps 4-11 bytes
@@ -18,10 +19,11 @@
 //
 // Bound: the softmax warps' exponentials and roundings beside the conversions, and the fetching of the roles'
 // instructions, which do not all fit the instruction cache.  16 chats of 436 to 8192 keys with 64 to 436 new
-// rows, 32 heads over 8 of 128: 479 us (717 TFLOP/s, 38% of the rate of a large product); prompts of 4 x 4096 tokens
-// 782 us (703 TFLOP/s); width 64 386 us.  Steps: 2607 us on the decode kernel's columns; 598 as rows; 557 with a
-// warp that lays the items out; 506 with bodies short enough for the instruction cache; 479 with masks as bits,
-// output places found once and scales ahead of S.  Slower: exponentials before the vote (829, registers spilled),
+// rows, 32 heads over 8 of 128: 458 us (751 TFLOP/s, 40% of the rate of a large product), 476 in pages of 16 tokens;
+// prompts of 4 x 4096 tokens 753 us (730 TFLOP/s); width 64 346 us.  Steps: 2607 us on the decode kernel's columns; 598
+// as rows; 557 with a warp that lays the items out; 506 with bodies short enough for the instruction cache; 479 with masks
+// as bits, output places found once and scales ahead of S; 458 with numbers that hold no scales.  Slower:
+// exponentials before the vote (829, registers spilled),
 // rolled loops that read S again (525 to 566), masks kept in TMEM (534), queries brought in by the converting warps (494).
 #include "e4m3.cuh"
 #include "pages_tc.cuh"
@@ -76,10 +78,6 @@ __device__ __forceinline__ uint32_t fp16_of(uint32_t two_bytes) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two_bytes));
   return h;
 }
-__device__ __forceinline__ uint32_t scaled(uint32_t h, uint32_t by) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&by));
-  return *reinterpret_cast<const uint32_t *>(&r);
-}
 
 __device__ __forceinline__ float rcp(float x) {
   float y;
@@ -87,7 +85,8 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-template <int D, bool BF16>
+// SMALL: pages of 16 and 32 tokens.
+template <int D, bool BF16, bool SMALL>
 __global__ void __launch_bounds__(kThreads, 1)
     pages_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                       const __grid_constant__ TcParams p) {
@@ -346,7 +345,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ bytes to fp16
     const int tid = threadIdx.x - 128;
     constexpr int PER = D / 16, UNITS = kN * PER / kTurners;  // 16-byte pieces of a row; of a thread
-    const int log2_page = min(p.a.log2_page, 6), npt = kN >> log2_page;
     bool ok = true;
     int nt = 0;
     while (volatile Item *const x = ok ? next_item() : nullptr) {
@@ -354,12 +352,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       done_item();
       if (flags & kTiles) {
         for (int m = 0; m < n && ok; ++m, ++nt) {
-          const int j0 = (tile + m) * kN, sb = nt % C::NB, sc = nt % kScales;
+          const int j0 = (tile + m) * kN, sb = nt % C::NB;
           const bool inside = j0 >= lo && j0 + kN <= hi;
-          if (npt > 1) ok = wait(C::B_SC + sc, nt / kScales);
-          // keys, then values (one body: the loops of all roles share the SM's instruction cache, which holds no more)
-#pragma unroll 1
-          for (int v = 0; v < 2 && ok; ++v) {
+          // keys, then values (a body for each: extends of width 128 take 458 us, 475 with one body for both)
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            if (!ok) break;
             const int to_slot = nt % C::NK, full = C::B_BKF + 2 * C::NB * v + sb, turned = C::B_KF + 2 * C::NK * v + to_slot;
             ok = wait(full, nt / C::NB);
             if (ok && nt >= C::NK) ok = wait(turned + C::NK, nt / C::NK - 1);
@@ -374,14 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < UNITS; ++i)
               lds_v4(from + r * D + ((D == 128 ? piece(i) ^ (r & 7) : piece(i) ^ (r >> 1 & 3)) << 4), q[i][0], q[i][1], q[i][2], q[i][3]);
-            const bool in = inside || (j0 + r >= lo && j0 + r < hi);
-            uint32_t by = 0x3c003c00u;  // the page's scale against the tile's, the largest of its pages'
-            if (npt > 1) {
-              const float *x = reinterpret_cast<const float *>(scales + sc * 4) + v;
-              float top = 0.f;
-              for (int i = 0; i < npt; ++i) top = fmaxf(top, x[2 * i]);
-              const __half2 f = __float2half2_rn(x[2 * (r >> log2_page)] * rcp(top));
-              by = *reinterpret_cast<const uint32_t *>(&f);
+            // (slots that hold no key of the item; as bytes, in a branch that most tiles pass by: 491 us as numbers)
+            if (!inside && !(j0 + r >= lo && j0 + r < hi)) {
+#pragma unroll
+              for (int i = 0; i < UNITS; ++i) q[i][0] = q[i][1] = q[i][2] = q[i][3] = 0;
             }
 #pragma unroll
             for (int i = 0; i < UNITS; ++i) {
@@ -390,14 +384,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 4; ++e) {
                 h[2 * e] = fp16_of(q[i][e]);
                 h[2 * e + 1] = fp16_of(q[i][e] >> 16);
-              }
-              if (npt > 1) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) h[e] = scaled(h[e], by);
-              }
-              if (!in) {  // (slots that hold no key of the item)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) h[e] = 0;
               }
               const uint32_t at = to + (piece(i) >> 2) * C::BLK + r * 128;
               const int c = 2 * (piece(i) & 3);
@@ -418,7 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = (warp - 12) / 4, r = (threadIdx.x - 384) % 128;  // query tile and row of it
     const uint32_t t_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t o_addr = t_addr + t * D, s_addr = t_addr + C::S_COL + 2 * t * kN;
-    const int log2_page = min(p.a.log2_page, 6), npt = kN >> log2_page;
+    constexpr int G = SMALL ? kN / 16 : 1;  // groups of a tile's keys that have a page of their own (one of 32: two groups)
+    const int log2_page = p.a.log2_page;
     int nt = 0, ns = 0;  // tiles; the ones of this query tile
     bool ok = true;
     const int wr = 32 * (warp & 3);  // first row of the warp
@@ -506,13 +493,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           // query tile: S tells then that the barrier is in this tile's phase)
           ok = m > 0 || wait(C::B_S + 2 * t + sb, ns / 2);
           ok = ok && wait(C::B_SC + sc, nt / kScales);
-          float kref = 0.f, vref = 0.f;
-          for (int i = 0; i < npt; ++i) {
-            kref = fmaxf(kref, scales[sc * 4 + i].x);
-            vref = fmaxf(vref, scales[sc * 4 + i].y);
+          float c1[G], lv[G], over[G];
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const float2 s2 = scales[sc * 4 + (SMALL ? 16 * g >> log2_page : 0)];
+            const float vs = fminf(fmaxf(s2.y, 0x1p-100f), 0x1p120f);  // (a scale of zero or no number: of no weight)
+            c1[g] = fmaxf(s2.x * sl2, 1e-37f);
+            lv[g] = lg2(vs);
+            over[g] = rcp(vs);
           }
-          vref = fminf(fmaxf(vref, 0x1p-100f), 0x1p120f);  // (a scale of zero or no number: of no weight)
-          const float c1 = fmaxf(kref * sl2, 1e-37f), lv = lg2(vref), over = rcp(vref);
           ok = ok && wait(C::B_S + 2 * t + sb, ns / 2);
           if (!ok) break;
           fence_after();
@@ -540,7 +529,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto f = [&](int k) { return __uint_as_float(x[k]); };
             m8[i] = fmax3(fmax3(f(0), f(1), f(2)), fmax3(f(3), f(4), f(5)), fmaxf(f(6), f(7)));
           }
-          const float mx = fmaf(fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])), c1, lv);
+          float mx;
+          if constexpr (SMALL) {
+            float y[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) y[g] = fmaf(fmaxf(m8[2 * g], m8[2 * g + 1]), c1[g], lv[g]);
+            mx = fmaxf(fmax3(y[0], y[1], y[2]), y[3]);
+          } else {
+            mx = fmaf(fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])), c1[0], lv[0]);
+          }
           const bool move = mx > m_ref + kMove;  // (not by a NaN, nor where nothing is seen)
           if (__any_sync(0xffffffffu, move)) {
             const float m_new = move ? mx : m_ref, alpha = move ? ex2(m_ref - m_new) : 1.f;
@@ -565,26 +562,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             l *= alpha;
             m_ref = m_new;
           }
-          const float add = m_ref == -INFINITY ? 0.f : lv - m_ref + kLift;
-          const uint64_t c2 = f2pack(c1, c1), a2 = f2pack(add, add);
-          uint64_t s0 = f2pack(0.f, 0.f), s1 = s0;
+          uint64_t c2[G], a2[G], s0[G], s1[G];
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const float add = m_ref == -INFINITY ? 0.f : lv[g] - m_ref + kLift;
+            c2[g] = f2pack(c1[g], c1[g]);
+            a2[g] = f2pack(add, add);
+            s0[g] = s1[g] = f2pack(0.f, 0.f);
+          }
 #pragma unroll
           for (int ch = 0; ch < 2; ++ch) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int i = 32 * ch + 2 * e;
-              const float2 x = f2unpack(fma2(f2pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), c2, a2));
+              const int i = 32 * ch + 2 * e, g = SMALL ? i / 16 : 0;
+              const float2 x = f2unpack(fma2(f2pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), c2[g], a2[g]));
               const float pa = ex2(x.x), pb = ex2(x.y);
               pk[e] = pack2(pa, pb, 0);
-              if (e & 1) s1 = add2(s1, f2pack(pa, pb));
-              else s0 = add2(s0, f2pack(pa, pb));
+              if (e & 1) s1[g] = add2(s1[g], f2pack(pa, pb));
+              else s0[g] = add2(s0[g], f2pack(pa, pb));
             }
             __syncwarp();
             tmem_st16(s_at + ch * 16, pk);
           }
-          const float2 f0 = f2unpack(s0), f1 = f2unpack(s1);
-          l = fmaf((f0.x + f0.y) + (f1.x + f1.y), over, l);
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const float2 f0 = f2unpack(s0[g]), f1 = f2unpack(s1[g]);
+            l = fmaf((f0.x + f0.y) + (f1.x + f1.y), over[g], l);
+          }
           __syncwarp();
           tmem_st_wait();
           fence_before();
@@ -695,7 +700,9 @@ cudaError_t pages_rows_forward(const PagesAttnParams &a, void *workspace, int nu
     p.rec = static_cast<int4 *>(workspace);
     p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + (((size_t)num_sms * 2 * sizeof(int4) + 255) & ~(size_t)255));
     const bool bf = a.p.dtype == VLF_BF16;
-    const void *kern = bf ? (const void *)pages_rows_kernel<D, true> : (const void *)pages_rows_kernel<D, false>;
+    const bool small = a.page < kN;
+    const void *kern = bf ? (small ? (const void *)pages_rows_kernel<D, true, true> : (const void *)pages_rows_kernel<D, true, false>)
+                          : (small ? (const void *)pages_rows_kernel<D, false, true> : (const void *)pages_rows_kernel<D, false, false>);
     const void *join = bf ? (const void *)pages_join_kernel<D, C::NC, kN, true> : (const void *)pages_join_kernel<D, C::NC, kN, false>;
     cudaError_t e = set_smem_once(kern, C::SMEM);
     if (e != cudaSuccess) return e;
