@@ -510,8 +510,8 @@ int vlf_cache_evict(const void *k, const void *v, const float *weights,
  *                page_table[s][j / page]; entries behind a sequence's last page are not looked at
  *   seqlens_kv   int32 [num_seqs], at most max_pages * page
  * max_pages * page and the numbers of tokens are below 2^31 - 2^16; d_qk, d_v <= 256.  A page that is needed
- * and lies outside 0..num_pages - 1 records VLF_ERR_BAD_PAGES and is passed over, a sequence whose lengths
- * are out of range VLF_ERR_BAD_SEQLENS.
+ * and lies outside 0..num_pages - 1 records VLF_ERR_BAD_PAGES and is passed over (nothing is written for it, and
+ * rows do not see its keys), a sequence whose lengths are out of range VLF_ERR_BAD_SEQLENS.
  */
 
 /*

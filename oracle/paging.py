@@ -82,7 +82,7 @@ def pages_write(k, v, cache, table, cu, lens):
 
 
 def keys_of(pages, scale, row, length):
-    """[length, H, D]: what a sequence's bytes stand for."""
+    """[length, H, D]: what a sequence's bytes stand for (0 for a page outside the pool)."""
     page = pages.shape[2]
     out = np.zeros((length, pages.shape[1], pages.shape[3]))
     for j in range(length):
@@ -106,6 +106,8 @@ def pages_attention(q, cache, table, cu_q, lens, scale, causal, window):
             continue
         k, v = keys_of(kp, ks, table[s], lens[s]), keys_of(vp, vs, table[s], lens[s])
         ok = orc.visible(b - a, lens[s], causal, window)
+        page = np.asarray(table[s])[np.arange(lens[s]) // kp.shape[2]]
+        ok = ok & ((page >= 0) & (page < kp.shape[0]))  # (keys of a page outside the pool are passed over)
         for h in range(hq):
             g = h // (hq // hkv)
             x = np.where(ok, scale * (q[a:b, h] @ k[:, g].T), -np.inf)

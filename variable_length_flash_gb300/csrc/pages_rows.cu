@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto real = [&](int id) { return id >= 0 && id < p.a.num_pages; };
         auto scale_of = [&](int id) {
-          if (!real(id)) return make_float2(0.f, 0.f);
+          if (!real(id)) return make_float2(0.f, -1.f);  // (keys of no weight, below)
           const long long at = (long long)id * b.h_kv + kv_head;
           return make_float2(ld(p.a.k_scale + at), ld(p.a.v_scale + at));
         };
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 sc_next = scale_of(next);
           const bool have = id != -2;
           if (have && !real(id)) set_error(err, VLF_ERR_BAD_PAGES);
-          const int z = real(id) ? id * b.h_kv + kv_head : none;  // (outside: zeros)
+          const int z = real(id) ? id * b.h_kv + kv_head : none;  // (outside: zeros, so that nothing is a NaN)
           const int bytes = __popc(__ballot_sync(0xffffffffu, have)) * page * D;
           const int y = p.a.page > kN ? (tile + m) * kN & (p.a.page - 1) : 0;
           const int sb = nt % C::NB;
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 s2 = scales[sc * 4 + (SMALL ? 16 * g >> log2_page : 0)];
             const float vs = fminf(fmaxf(s2.y, 0x1p-100f), 0x1p120f);  // (a scale of zero or no number: of no weight)
             c1[g] = fmaxf(s2.x * sl2, 1e-37f);
-            lv[g] = lg2(vs);
+            lv[g] = s2.y < 0.f ? -INFINITY : lg2(vs);  // (a page outside the pool: passed over)
             over[g] = rcp(vs);
           }
           ok = ok && wait(C::B_S + 2 * t + sb, ns / 2);
@@ -563,9 +563,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             m_ref = m_new;
           }
           uint64_t c2[G], a2[G], s0[G], s1[G];
+          const float lift = m_ref == -INFINITY ? 0.f : kLift - m_ref;
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            const float add = m_ref == -INFINITY ? 0.f : lv[g] - m_ref + kLift;
+            const float add = lv[g] + lift;
             c2[g] = f2pack(c1[g], c1[g]);
             a2[g] = f2pack(add, add);
             s0[g] = s1[g] = f2pack(0.f, 0.f);

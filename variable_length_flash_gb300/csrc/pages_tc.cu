@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
         auto real = [&](int id) { return id >= 0 && id < p.a.num_pages; };
         int id = id_of(first + lane), id_next = id_of(first + 32 + lane);
         auto scale_of = [&](int i) {
-          if (!real(i)) return make_float2(0.f, 0.f);
+          if (!real(i)) return make_float2(0.f, -1.f);  // (keys of no weight, below)
           const long long at = (long long)i * b.h_kv + w.head;
           return make_float2(ld(p.a.k_scale + at), ld(p.a.v_scale + at));
         };
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
           const int mine_id = __shfl_sync(0xffffffffu, id, in + lane % npt);
           const bool have = lane < npt && mine_id != -2;
           if (have && !real(mine_id)) set_error(err, VLF_ERR_BAD_PAGES);
-          const int z = real(mine_id) ? mine_id * b.h_kv + w.head : none;  // (outside: zeros)
+          const int z = real(mine_id) ? mine_id * b.h_kv + w.head : none;  // (outside: zeros, so that nothing is a NaN)
           const int bytes = __popc(__ballot_sync(0xffffffffu, have)) * page * D;
           const int y = p.a.page > kKeys ? (j0 + m * kKeys) & (p.a.page - 1) : 0;
           const int ks = nk % C::KST, vs = nv % C::VST;
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(192, Cfg<D, NC>::CTAS)
           }
           const float2 s2 = scales[sc * 8 + (tid >> min(p.a.log2_page, 7))];
           const float vs = fminf(fmaxf(s2.y, 0x1p-100f), 0x1p120f);  // (a scale of zero or no number: of no weight)
-          const float lv = lg2(vs), over = 1.f / vs;
+          const float lv = s2.y < 0.f ? -INFINITY : lg2(vs), over = 1.f / vs;  // (a page outside the pool: passed over)
           const bool in = j >= w.lo && j < w.hi;
           const bool full = j0 >= all_lo && j0 + kKeys <= all_hi;
           if (j0 < w.lo || j0 + kKeys > w.hi) {
