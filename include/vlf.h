@@ -580,7 +580,8 @@ int vlf_pages_write(const void *k, int64_t k_stride, const void *v, int64_t v_st
  * Pages of which no row of a sequence sees a key (in front of the window) are not looked at and may be
  * outside the pool.  What other bytes of a page hold never reaches a row, but a value of its own sequence
  * that is NaN may also reach rows that do not see its key.  A row that sees a NaN logit is NaN, and so is
- * its lse.  Tensor-core kernels for F16 / BF16 and d_qk = d_v in {64, 128}; fp32 FMA otherwise.  On the
+ * its lse; a query that holds an infinity or a NaN has NaN logits alone (vlf_attn_varlen_fwd takes infinite ones as
+ * they are, and a row of minus infinities for one that sees no key).  Tensor-core kernels for F16 / BF16 and d_qk = d_v in {64, 128}; fp32 FMA otherwise.  On the
  * tensor cores a weight times its page's value scale is held to 11 bits, and to 2^-24 of the largest such product of
  * the keys that the row sees; a value scale more than 2^100 below that key's may cost the key its part of the lse.
  * Scales of pages that a row does not see do not matter to it.  max_seqlen_q decides which kernel

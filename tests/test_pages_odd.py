@@ -69,3 +69,72 @@ def test_rows_that_have_no_other_page(page, q_lens, flags):
     c["table"].copy_(good)
     holds(call(c, causal=True, flags=flags), c)
     assert vlf.vlf_check_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("q_lens,flags", KERNELS)
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_a_query_that_is_not_finite_makes_its_row_nan(page, q_lens, flags, dtype):
+    """Whatever the signs of its products are; a row that sees no key is 0 all the same, and no other row changes."""
+    c = problem(q_lens, [20, 700], page, 4, 2, 128, 128, dtype, seed=page)
+    for name in ("k_pages",):  # (keys of one sign: an infinite query's logits are all infinite, and of one sign)
+        c[name] = torch.where(c[name] & 127 == 127, c[name], c[name] & 127)
+    want = call(c, causal=True, flags=flags)
+    sees = [i >= q_lens[0] - 20 for i in range(q_lens[0])] + [True] * q_lens[1]
+    for x in (INF, -INF, NAN):
+        for i, h, col in ((0, 0, 0), (q_lens[0] - 1, 1, 77), (q_lens[0], 3, 127), (sum(q_lens) - 1, 2, 5)):
+            d = dict(c, q=c["q"].clone())
+            d["q"][i, h, col] = x
+            out, lse = call(d, causal=True, flags=flags)
+            if sees[i]:
+                assert out[i, h].isnan().all() and lse[h, i].isnan()
+            else:
+                assert not out[i, h].any() and lse[h, i] == -INF
+            out, lse = out.clone(), lse.clone()
+            out[i, h], lse[h, i] = want[0][i, h], want[1][h, i]
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert vlf.vlf_check_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("q_lens,flags", KERNELS)
+def test_a_nan_in_the_cache_reaches_the_rows_that_see_it(page, q_lens, flags):
+    """A key's: rows in front of it keep their bits, the others are NaN.  A value's: its column, and the lse is what it was.
+    Rows of other kv heads and of the other sequence never change."""
+    c = problem(q_lens, [300, 200], page, 4, 2, 128, 128, BF, seed=2)
+    a, b = q_lens
+    want = call(c, causal=True, flags=flags)
+    pool = c["k_pages"].clone(), c["v_pages"].clone()
+    j = 200 - b + b // 2  # seen from row b // 2 on
+    c["k_pages"][c["rows"][1][j // page], 0, j % page, 3] = 127
+    out, lse = call(c, causal=True, flags=flags)
+    at = a + b // 2
+    assert out[at:, :2].isnan().all() and lse[:2, at:].isnan().all()
+    assert torch.equal(out[:at], want[0][:at]) and torch.equal(lse[:, :at], want[1][:, :at])
+    assert torch.equal(out[:, 2:], want[0][:, 2:]) and torch.equal(lse[2:], want[1][2:])
+    c["k_pages"].copy_(pool[0])
+    c["v_pages"][c["rows"][1][j // page], 1, j % page, 3] = 255
+    out, lse = call(c, causal=True, flags=flags)
+    assert out[at:, 2:, 3].isnan().all() and torch.equal(lse, want[1])
+    rest = torch.tensor([x for x in range(128) if x != 3], device="cuda")
+    assert torch.equal(out[:, :, rest], want[0][:, :, rest]) and torch.equal(out[:a], want[0][:a])
+    assert torch.equal(out[:, :2], want[0][:, :2]) and vlf.vlf_check_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("change,status", [(dict(length=2000), -6), (dict(length=-1), -6), (dict(cu=[0, 90, 40]), -6), (dict(cu=[0, 40, 500]), -6)])
+def test_bad_lengths_with_many_rows_are_recorded(change, status, page):
+    c = problem([40, 70], [300, 200], page, 4, 2, 128, 128, BF, seed=2)
+    want = call(c, causal=True)
+    if "length" in change:
+        c["kv"][1] = change["length"]
+    else:
+        c["cu_q"] = torch.tensor(change["cu"], dtype=torch.int32, device="cuda")
+    out, _ = call(c, causal=True)
+    assert vlf.vlf_check_error() == status
+    if change != dict(cu=[0, 90, 40]):
+        assert torch.equal(out[:40], want[0][:40])
+    assert vlf.vlf_check_error() == 0

@@ -50,7 +50,8 @@ __global__ void __launch_bounds__(32 * kFmaWarps) pages_fma_kernel(const PagesAt
   const long long first = (long long)(q0 + i) * p.h_q + (long long)kv_head * p.group + h0;  // row of the first head
   for (int x = threadIdx.x; x < p.d_qk * H; x += NT) {
     const int c = x % p.d_qk, h = x / p.d_qk;
-    q[c][h] = h < heads ? to_f32<T>(static_cast<const T *>(p.q)[(first + h) * p.d_qk + c]) : 0.f;
+    const float y = h < heads ? to_f32<T>(static_cast<const T *>(p.q)[(first + h) * p.d_qk + c]) : 0.f;
+    q[c][h] = fmaf(y, 0.f, y);  // (an infinity becomes a NaN, and the row with it, as on the tensor cores)
   }
   __syncthreads();
   int lo, hi;

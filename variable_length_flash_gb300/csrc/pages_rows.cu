@@ -461,12 +461,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int o = PL / 2; o > 0; o /= 2) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
                 top = max(top & 0xffffu, top >> 16);
                 const int ex = min(max((int)(top >> 7) - 127, -100), 127);
-                const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
+                // (a query that is not finite: every logit of the row is NaN)
+                const float up = __uint_as_float(top >= 0x7f80u ? 0x7fffffffu : (uint32_t)(127 + 7 - ex) << 23);
                 if (piece == 0) downs[t * 128 + r2] = __uint_as_float((uint32_t)(127 - 7 + ex) << 23);
     #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const float2 f = unpack2(y[e], 1);
                   y[e] = pack2(f.x * up, f.y * up, 0);
+                }
+                y4[k] = make_uint4(y[0], y[1], y[2], y[3]);
+              } else {
+                uint32_t y[4] = {y4[k].x, y4[k].y, y4[k].z, y4[k].w};
+    #pragma unroll
+                for (int e = 0; e < 4; ++e) {  // (so here: x + 0 x is x, and NaN for an infinity)
+                  const __half2 h = *reinterpret_cast<const __half2 *>(&y[e]), r = __hfma2(h, __half2half2(__ushort_as_half(0)), h);
+                  y[e] = *reinterpret_cast<const uint32_t *>(&r);
                 }
                 y4[k] = make_uint4(y[0], y[1], y[2], y[3]);
               }
