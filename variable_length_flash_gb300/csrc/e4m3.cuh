@@ -31,7 +31,5 @@ __device__ __forceinline__ float page_scale(float amax) {
   const int e = (int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // biased
   return __uint_as_float((uint32_t)max(e, 127 - 64) << 23);
 }
-// 1 / s of a power of two between 2^-126 and 2^126.
-__device__ __forceinline__ float power_inverse(float s) { return __uint_as_float(0x7f000000u - __float_as_uint(s)); }
 
 }  // namespace vlf
