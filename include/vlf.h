@@ -535,7 +535,7 @@ int vlf_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stri
  *   dq_out, dk_out   gradients of the outputs, dtype, with strides of their own
  *   dq, dk       as q, k (written); may be dq_out / dk_out or q / k (same pointer and stride)
  *   dq_weight, dk_weight   [d] of type weight_dtype (written), or NULL: not wanted.  The sums over tokens
- *                and heads are fp32, in a fixed order, rounded once
+ *                and heads are fp32, in a fixed order, rounded once (0 where there are none)
  *   workspace    at least vlf_norm_rope_bwd_workspace_size(d) bytes where a weight's gradient is
  *                wanted; owned by the caller, clobbered (two calls that may overlap need two)
  */

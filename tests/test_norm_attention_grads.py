@@ -113,3 +113,17 @@ def test_every_element_of_the_gradients(hq, hkv, d, rot, lens, window):
             ends = [loss(*[a + s * h * e if n == i else a for n, a in enumerate(leaves)]) for s in (1, -1)]
             num, room = (ends[0] - ends[1]) / (2 * h), (size * e.abs()).sum()
             assert (num - (leaves[i].grad * e).sum()).abs() <= 2.0 ** -14 * room + 2.0 ** -30 * go.abs().sum()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t,hk", [(5, 0), (0, 2), (0, 0)])
+def test_the_weights_of_no_rows_have_no_gradient(t, hk):
+    """What the forward takes, the backward takes: keys without heads, calls without tokens."""
+    d = 64
+    q, k = (torch.randn(t, h, d, device="cuda", requires_grad=True) for h in (2, hk))
+    wq, wk = (torch.ones(d, device="cuda", requires_grad=True) for _ in range(2))
+    yq, yk = vlf.norm_rotary_embedding(q, k, wq, wk)
+    (yq * yq.detach()).sum().add((yk * yk.detach()).sum()).backward()
+    assert q.grad.shape == q.shape and k.grad.shape == k.shape
+    assert not wk.grad.any() and bool(wq.grad.any()) == (t > 0)
+    assert not wq.grad.isnan().any() and vlf.vlf_check_error() == 0

@@ -809,7 +809,7 @@ int vlf_norm_rope_bwd(const void *dq_out, int64_t dq_out_stride, const void *dk_
   const int st = norm_rope_args(p, q, q_stride, k, k_stride, q_weight, k_weight, weight_dtype, eps, positions, n_axes,
                                 sections, inv_freq, total, h_q, h_k, d, rot, dtype, interleaved);
   if (st != VLF_OK) return st;
-  if ((dq_weight && !q_weight) || (dk_weight && (!k_weight || h_k == 0))) return VLF_ERR_INVALID;
+  if ((dq_weight && !q_weight) || (dk_weight && !k_weight)) return VLF_ERR_INVALID;
   if (total > 0 && (!dq_out || !dq || (h_k > 0 && (!dk_out || !dk)))) return VLF_ERR_INVALID;
   if (dq_out_stride < 0 || dk_out_stride < 0 ||
       (total > 1 && (dq_stride < (int64_t)h_q * d || (h_k > 0 && dk_stride < (int64_t)h_k * d))))
