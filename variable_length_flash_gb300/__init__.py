@@ -1389,7 +1389,9 @@ def vlf_pages_fork(page_table, seqlens, refs, parents, grow, page_size, table_ou
     copies.  Returns (table [m, max_pages], seqlens [m] with the growth, refs [pages], src [m], dst [m],
     left [1]); src and dst are for vlf_pages_copy of every layer, before anything is written; left, the free
     pages that are left, is negative where there were too few: nothing has changed then, and the tables
-    returned are empty (include/vlf.h).  Nothing is read on the host."""
+    returned are empty (include/vlf.h).  Nothing is read on the host.  Outputs that the call makes may share one
+    allocation, its workspace (up to 256 KB) behind them: one that is kept, or saved to a file, keeps or saves all, so
+    clone what outlives the step."""
     if all(t is None for t in (table_out, seqlens_out, refs_out, src, dst, left, workspace, stream)):
         done = _calls.pages_fork(page_table, seqlens, refs, parents, grow, page_size)
         if done is not None:
@@ -1434,7 +1436,7 @@ def vlf_pages_compact(page_table, refs, table_out=None, refs_out=None, to=None, 
     """The pages in use (``refs`` [pages] above 0) moved to the front of the pool.  Returns (table, refs, to, src,
     dst, used): the tables and counts afterwards, where each page in use then is (-1: it was free), the
     copies to make (int32 [pages // 2], -1 behind them) with vlf_pages_copy of every layer, and int32 [1]
-    how many pages are in use.  Nothing is read on the host."""
+    how many pages are in use.  Nothing is read on the host.  Outputs share their memory as vlf_pages_fork's do."""
     if all(t is None for t in (table_out, refs_out, to, src, dst, used, workspace, stream)):
         done = _calls.pages_compact(page_table, refs)
         if done is not None:

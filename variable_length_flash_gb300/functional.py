@@ -193,7 +193,8 @@ def norm_rotary_embedding(q, k, q_weight, k_weight, positions=None, inv_freq=Non
                           interleaved=False, eps=1e-6):
     """Root-mean-square norm of each head of packed q [tokens, H_q, D] and k [tokens, H_k, D] with its weight
     [D] (or None), and rotary positions in the same pass (see ``vlf_norm_rope``), differentiable in q, k
-    and the weights.  q and k may be slices of a packed projection.  Before a backward pass is captured into a
+    and the weights, once (``rotary_embedding`` is twice).  Both q and k are given: for q alone, k may have no
+    heads ([tokens, 0, D]).  They may be slices of a packed projection.  Before a backward pass is captured into a
     CUDA graph, let go of eager results that depend on the same leaves (PyTorch accumulates their gradients on
     the eager pass's stream, which a capture cannot wait for)."""
     for t in (positions, inv_freq):
