@@ -521,7 +521,7 @@ int vlf_cache_evict(const void *k, const void *v, const float *weights,
  *   q_weight, k_weight   [d] of type weight_dtype (`dtype` or VLF_F32), for every head; NULL: ones
  *   eps          >= 0, finite
  *   others       as in vlf_rope (rot = 0, positions and inv_freq NULL: the norm alone)
- * The arithmetic is fp32, the result is rounded once.
+ * The arithmetic is fp32 (a row's sum of squares too: elements are below 2^59 in size), the result is rounded once.
  */
 int vlf_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                   const void *q_weight, const void *k_weight, int weight_dtype, float eps,
@@ -580,13 +580,16 @@ int vlf_pages_write(const void *k, int64_t k_stride, const void *v, int64_t v_st
  * Pages of which no row of a sequence sees a key (in front of the window) are not looked at and may be
  * outside the pool.  What other bytes of a page hold never reaches a row, but a value of its own sequence
  * that is NaN may also reach rows that do not see its key.  A row that sees a NaN logit is NaN, and so is
- * its lse; a query that holds an infinity or a NaN has NaN logits alone (vlf_attn_varlen_fwd takes infinite ones as
- * they are, and a row of minus infinities for one that sees no key).  Tensor-core kernels for F16 / BF16 and d_qk = d_v in {64, 128}; fp32 FMA otherwise.  On the
- * tensor cores a weight times its page's value scale is held to 11 bits, and to 2^-24 of the largest such product of
- * the keys that the row sees; a value scale more than 2^100 below that key's may cost the key its part of the lse.
- * Scales of pages that a row does not see do not matter to it.  max_seqlen_q decides which kernel
- * runs: more than 32 rows of a kv head's group (max_seqlen_q * h_q / h_kv) take the one for many rows, so a
- * loose bound makes single rows slower (2.7 times, in large batches), never wrong.  No backward.
+ * its lse; a query that holds an infinity or a NaN has NaN logits alone (vlf_attn_varlen_fwd takes infinite
+ * ones as they are, and a row of minus infinities for one that sees no key).  Tensor-core kernels for
+ * F16 / BF16 and d_qk = d_v in {64, 128}; fp32 FMA otherwise.  On the tensor cores a weight times its page's
+ * value scale is held to 11 bits, and to 2^-24 of the largest such product of the keys that the row sees; a
+ * value scale more than 2^100 below that key's may cost the key its part of the lse.  Scales of pages that a
+ * row does not see do not matter to it.  Logits are below 2^26 in size there (fp32 holds them to whole units
+ * from 2^24 on, and from 2^27 on weights pass what fp16 holds: the row may be NaN).
+ * max_seqlen_q decides which kernel runs: more than 32 rows of a kv head's group (max_seqlen_q * h_q / h_kv)
+ * take the one for many rows, so a loose bound makes single rows slower (2.6 times, in large batches), never
+ * wrong.  No backward.
  */
 int vlf_attn_varlen_fwd_pages(const void *q, const void *k_pages, const void *v_pages,
                               const float *k_scale, const float *v_scale, const int32_t *page_table,
