@@ -18,7 +18,7 @@
 // weights and turns that a lane keeps leave one block an SM its registers, eight warps.  So what the next heads need
 // is on its way to shared memory meanwhile, each thread's to places of its own (85 us with the loads in
 // registers, four heads at a time), and two numbers go through an instruction where there is one for two (74
-// without).  Two heads at a time 73, two such blocks an SM 116.  64 tokens 4.2 us, which is a launch.
+// without).  Two heads at a time 73, two such blocks an SM 116.  64 tokens 4.1 us, which is a launch.
 #include "kernels.h"
 #include "rope.cuh"
 #include "tc_common.cuh"
@@ -59,8 +59,14 @@ __global__ void __launch_bounds__(256, BWD || V == 1 ? 1 : 2) norm_rope_kernel(c
   const Rows &rows = is_k ? p.k : p.q;
   tc::pdl_trigger();
   tc::pdl_wait();
-  for (int c = threadIdx.x; c < half; c += 256) F[c] = turns_of(ld(p.inv_freq + c));
-  for (int c = threadIdx.x; c < 256 + 8; c += 256) w[c] = c < p.d ? weight_at(rows.w, p.w_dtype, c) : 0.f;
+  {
+    // (both loads before a store, which would hold the second one up; half <= 128, d <= 256)
+    const int c = threadIdx.x;
+    const float f = c < half ? ld(p.inv_freq + c) : 0.f, x = c < p.d ? weight_at(rows.w, p.w_dtype, c) : 0.f;
+    if (c < half) F[c] = turns_of(f);
+    w[c] = x;
+    if (c < 8) w[256 + c] = 0.f;
+  }
   __syncthreads();
   const int ntail = ((p.d - p.rot + V - 1) / V + 1) / 2, units = nrot + ntail;
   const int G = p.lanes, run = 256 / G, u = threadIdx.x % G, g = threadIdx.x / G;
