@@ -588,7 +588,7 @@ int vlf_pages_write(const void *k, int64_t k_stride, const void *v, int64_t v_st
  * row does not see do not matter to it.  Logits are below 2^26 in size there (fp32 holds them to whole units
  * from 2^24 on, and from 2^27 on weights pass what fp16 holds: the row may be NaN).
  * max_seqlen_q decides which kernel runs: more than 32 rows of a kv head's group (max_seqlen_q * h_q / h_kv)
- * take the one for many rows, so a loose bound makes single rows slower (2.6 times, in large batches), never
+ * take the one for many rows, so a loose bound makes single rows slower (2.4 times, in large batches), never
  * wrong.  No backward.
  */
 int vlf_attn_varlen_fwd_pages(const void *q, const void *k_pages, const void *v_pages,

@@ -11,9 +11,10 @@
 // columns are the same for every row, so dw is summed in registers over all its rows, then over
 // the block's tokens, and a second launch adds the blocks' parts: every sum in a fixed order.
 //
-// Measured: 20011 tokens of 40 heads of 128 in bf16, sliced from a fused projection, 78 us (78% of the copy
-// rate; the weights times sine and cosine are made once for a token, which took it from 92); the gradients of
-// 16384 tokens of 32 heads of 96 in fp16, 64 columns of which turn in pairs of neighbours, 70.5 us (63%): a
+// Measured: 20011 tokens of 40 heads of 128 in bf16, sliced from a fused projection, 77 us (79% of the copy
+// rate; the weights times sine and cosine are made once for a token, which took it from 92), in fp32 123 (98%); the
+// gradients of 16384 tokens of 32 heads of 96 in fp16, 64 columns of which turn in pairs of neighbours, 70.4 us (63%),
+// in fp32 104 (86%), of heads of 128 in bf16 69 (86%), in fp32 135 (88%).  At 96 a
 // quarter of what it issues is for lanes that have no columns (12 chunks of a row over 8 lanes), and the sums,
 // weights and turns that a lane keeps leave one block an SM its registers, eight warps.  So what the next heads need
 // is on its way to shared memory meanwhile, each thread's to places of its own (85 us with the loads in

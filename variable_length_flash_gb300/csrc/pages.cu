@@ -19,8 +19,8 @@ namespace {
 //
 // Bound: HBM, each token read once, a byte written for it.  A block has one page of one head, of K or of
 // V: it keeps the rows in registers between the maximum and the rounding.  Measured: 66k tokens of 8 heads of
-// 128 in bf16, 75 us (80% of the copy rate; 300 us with values kept in fp32 and places found by division);
-// 64 single tokens 3.5 us, which is a launch.
+// 128 in bf16, 74 us (81% of the copy rate; 300 us with values kept in fp32 and places found by division), in fp32
+// 110 (91%); 64 single tokens 3.6 us, which is a launch.
 constexpr int kKeep = 8;  // chunks a thread keeps; what is behind them is read again
 
 // V values as they are read.
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const PagesCopyParams p
 
 // ------------------------------------------------------------------------------ tables
 // Bound: latency; a call is three or four dependent steps, each a launch that starts while the one before ends
-// (its blocks are there already, and wait).  256 rows of up to 1041 pages on 256 others, with their copies: 16.0 us,
+// (its blocks are there already, and wait).  256 rows of up to 1041 pages on 256 others, with their copies: 15.5 us,
 // of which the entries and counts are 1 us at the memory's rate; 21.1 with a warp for each row in the last step
 // instead of a block (a row's entries are 33 loads one behind another then), 66 as one cluster of eight CTAs with its
 // barriers between the steps (eight SMs look at a quarter of a million entries).  Tables of few entries

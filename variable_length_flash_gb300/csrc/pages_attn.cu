@@ -17,10 +17,10 @@ namespace {
 // the end, over the cluster's blocks as well where the launch has few rows and gives a row's keys to several.
 //
 // Bound: latency of a warp's dependent steps (loads, sums, exponentials), then issue.  A decode step of 64 caches of
-// 1000 to 16384 keys, 32 heads over 8 of 128 in fp32: 810 us, 21% of the copy rate (3451 with a block for each head
-// and bytes of values read singly; 907 with four keys in flight); width 96 in bf16 700 us; one cache of 131071 keys
-// 491 us.  Four blocks an SM, by bounding the registers, were 10% faster on the 64 caches and 65% slower
-// on the one.  Rows of one sequence share nothing here: 16 chats with 64 to 436 new rows take 22 ms.
+// 1000 to 16384 keys, 32 heads over 8 of 128 in fp32: 814 us, 21% of the copy rate (3451 with a block for each head
+// and bytes of values read singly; 907 with four keys in flight); width 96 in bf16 703 us; one cache of 131071 keys
+// 497 us.  Four blocks an SM, by bounding the registers, were 10% faster on the 64 caches and 65% slower
+// on the one.  Rows of one sequence share nothing here: 16 chats with 64 to 436 new rows take 21 ms, 17 at width 96.
 constexpr int kFmaWarps = 8, kFmaSplit = 8;  // warps of a block; blocks of a row, if it is shared out
 
 template <typename T, int H>
@@ -248,8 +248,8 @@ template <typename T> cudaError_t fma_forward(const PagesAttnParams &a, int num_
 }
 
 // Whether a sequence's rows of a kv head's group are enough for the kernel that has them as rows of its products.  64
-// caches of 1000 to 16384 keys, groups of 4 heads of 128: 4 rows (16 with the heads) take 226 us as columns, 489 as
-// rows; 8 rows 355 and 504; 9 rows 614 and 503 (two tiles of columns then, each reading the cache); 16 rows 659 and 507.
+// caches of 1000 to 16384 keys, groups of 4 heads of 128: 4 rows (16 with the heads) take 227 us as columns, 446 as
+// rows; 8 rows 353 and 458; 9 rows 614 and 460 (two tiles of columns then, each reading the cache); 16 rows 659 and 467.
 bool many_rows(int max_q, int group) { return (long long)max_q * group > 32; }
 
 }  // namespace

@@ -17,14 +17,15 @@
 // the others give up (64 and 144 of the 96 that the launch has; a wait or a walk that is not inlined
 // takes more than 64).  TMEM: O of both tiles, two S of 64 keys each, over which P is written.
 //
-// Bound: the softmax warps' exponentials and roundings beside the conversions, and the fetching of the roles'
-// instructions, which do not all fit the instruction cache.  16 chats of 436 to 8192 keys with 64 to 436 new
-// rows, 32 heads over 8 of 128: 458 us (751 TFLOP/s, 40% of the rate of a large product), 476 in pages of 16 tokens;
-// prompts of 4 x 4096 tokens 753 us (730 TFLOP/s); width 64 346 us.  Steps: 2607 us on the decode kernel's columns; 598
-// as rows; 557 with a warp that lays the items out; 506 with bodies short enough for the instruction cache; 479 with masks
-// as bits, output places found once and scales ahead of S; 458 with numbers that hold no scales.  Slower:
-// exponentials before the vote (829, registers spilled),
-// rolled loops that read S again (525 to 566), masks kept in TMEM (534), queries brought in by the converting warps (494).
+// Bound: latency.  No unit is full (4 x 256 rows on 4096 keys: tensor pipe 33%, issue slots 43%, exponentials 17%, 94% of
+// instruction fetches hit); a tile of 64 keys goes from the conversion over S, a vote and P to O with a barrier at
+// each hand-over, and the order of a role's instructions moves the whole by several percent.  16 chats of 436 to 8192
+// keys with 64 to 436 new rows, 32 heads over 8 of 128: 454 us (757 TFLOP/s, 40% of the rate of a large product), 472
+// in pages of 16 tokens; prompts of 4 x 4096 tokens 747 us (736 TFLOP/s); width 64 345 us.  Steps: 2607 us on the
+// decode kernel's columns; 598 as rows; 557 with a warp that lays the items out; 506 with bodies short enough for the
+// instruction cache; 479 with masks as bits, output places found once and scales ahead of S; 458 with numbers that
+// hold no scales.  Slower: exponentials before the vote (829, registers spilled), rolled loops that read S again (525 to
+// 566), masks kept in TMEM (534), queries brought in by the converting warps (494).
 #include "e4m3.cuh"
 #include "pages_tc.cuh"
 

@@ -33,10 +33,10 @@
 // warp 5 both products.
 //
 // Bound: HBM, each byte of the cache read once.  64 single rows on caches of 1000 to 16384 keys, 32 heads over 8 of
-// 128: 178 us (94% of the copy rate), 182 with pages of 16 tokens, 191 with groups of 8 heads, 226 with 4 rows
-// a sequence; width 64 in fp16 124 us (68%: a tile's softmax steps take longer than its bytes then, and the CTAs'
+// 128: 180 us (93% of the copy rate), 181 with pages of 16 tokens, 192 with groups of 8 heads, 227 with 4 rows
+// a sequence; width 64 in fp16 107 us (79%: a tile's softmax steps take longer than its bytes then, and the CTAs'
 // roles fetch instructions past the cache); one cache of 131071 keys 56 us (71%: 40 us of bytes, the
-// ends of the runs and the join).  Three short caches 10.6 us, which is latency.
+// ends of the runs and the join).  Three short caches 10.7 us, which is latency.
 #include "e4m3.cuh"
 #include "pages_tc.cuh"
 
